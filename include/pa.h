@@ -375,6 +375,176 @@ PA_API int pa_decode_static_ws_status(int *status_out, void *stream);
  * pipeline's one-second bound.) */
 PA_API int pa_selftest_wait_timeout(long long limit_cycles, int *status_device, void *stream);
 
+/* ------------------------------------------------------- latent KV cache */
+
+/* A latent cache keeps, for each token and layer, one row shared by all
+ * heads instead of K and V rows per kv head: a latent vector of
+ * PA_LATENT_DIM elements, from which every head's key and value are linear
+ * maps, and a rotary key part of PA_LATENT_ROPE_DIM elements that all heads
+ * use as it is.  Blocks, slots and block tables are those of the K/V caches
+ * (the pages' block tables do not depend on what a slot holds).
+ *   PA_KV_F16, PA_KV_BF16  [num_blocks][block_size][576] 16-bit elements, a
+ *                  row = 512 latent elements, then 64 rotary ones
+ *   PA_KV_FP8_E4M3 [num_blocks][block_size][656] bytes, a row = 512 one-byte
+ *                  E4M3 codes, 64 bf16 rotary elements, 4 float scales: the
+ *                  latent element d is e4m3(code d) * scale[d / 128].  The
+ *                  scales are powers of two, so every value is a bf16 value.
+ *                  Rows that go in or come out of such a cache are bf16.
+ * block_size 8, 16, 32 or 64; caches 16-byte aligned. */
+#define PA_LATENT_DIM 512
+#define PA_LATENT_ROPE_DIM 64
+#define PA_LATENT_ROW 576
+#define PA_LATENT_ROW_FP8_BYTES 656
+
+/* Write the rows of new tokens into their slots of a latent cache.
+ *   latent  16-bit [num_tokens][512], rows latent_stride elements apart
+ *   rope    16-bit [num_tokens][64], rows rope_stride elements apart
+ *           (strides >= the row and multiples of 8, pointers 16-byte aligned:
+ *           both may be slices of one projection's rows)
+ *   slot_mapping  int64 [num_tokens], as in pa_kv_write
+ * fp16 and bf16 rows are copied.  For PA_KV_FP8_E4M3 bf16 rows are quantised
+ * as they are written: a group of 128 latent elements gets the scale 2^e with
+ * the smallest e in [-100, 119] for which its largest magnitude is at most
+ * 448 * 2^e (NaN aside; e = -100 for a group of zeros), and each element the
+ * E4M3 code nearest to x / 2^e, ties to the even code, saturated at +-448
+ * (NaN stays NaN); rotary elements are copied.
+ * num_tokens = 0 is valid and launches nothing. */
+PA_API int pa_latent_write(const uint16_t *latent, const uint16_t *rope, const int64_t *slot_mapping, void *cache,
+                           int num_tokens, int64_t latent_stride, int64_t rope_stride, int block_size,
+                           int64_t num_blocks, int kv_dtype, void *stream);
+
+/* pa_block_copy for a latent cache (same rules for the pairs). */
+PA_API int pa_latent_block_copy(void *cache, const int64_t *pairs, int num_pairs, int block_size,
+                                int64_t num_blocks, int kv_dtype, void *stream);
+
+/* Read rows of a latent cache back: row row_start[i] + j of out gets token
+ * first_token[i] + j of sequence i, for 0 <= j < row_start[i + 1] -
+ * row_start[i], as 16-bit elements (512 latent, 64 rotary; a quantised row as
+ * the bf16 values that it stands for).  This feeds the product that expands a
+ * cached prefix into per-head keys and values.
+ *   out          16-bit [num_rows][576], rows out_stride elements apart (a
+ *                multiple of 8, >= 576), 16-byte aligned
+ *   row_start    int32 [num_seqs + 1], device: 0 = row_start[0] <= ... <=
+ *                row_start[num_seqs] <= num_rows; rows from
+ *                row_start[num_seqs] on are left as they are
+ *   first_token  int32 [num_seqs], device, or NULL for 0
+ * A row whose token is negative or past the table, or whose block id is out of
+ * range, is NaN; so is every row when row_start breaks its order. */
+PA_API int pa_latent_read(uint16_t *out, const void *cache, const int32_t *block_tables, const int32_t *row_start,
+                          const int32_t *first_token, int num_seqs, int num_rows, int64_t out_stride,
+                          int block_size, int64_t num_blocks, int max_blocks_per_seq, int kv_dtype, void *stream);
+
+/* Workspace bytes pa_latent_attention needs on the current device (a
+ * host-side bound; 0 for invalid sizes). */
+PA_API size_t pa_latent_attention_workspace_size(int num_seqs, int num_query_tokens, int num_heads,
+                                                 int max_context_len);
+
+/* Attention over a latent cache in the absorbed form: the map from a latent
+ * to a head's key has been multiplied into the query, and the map to its
+ * value is applied to the output afterwards, so all heads attend to the same
+ * rows.  With query row q (576 elements) of a new token and row c_t of
+ * position t:
+ *   s_t = scale * <q, c_t>,  out = sum_t softmax(s)_t * c_t[0 .. 511].
+ * New tokens, query_start and causality as in pa_attention_causal: new token
+ * j of T sees positions t <= L - T + j.  query_start = NULL is the decode: one
+ * new token per sequence, num_query_tokens = num_seqs.
+ *   out          16-bit [num_query_tokens][num_heads][512]
+ *   query        16-bit [num_query_tokens][num_heads][576]
+ *   num_heads    1 .. 128
+ *   block_tables, context_lens, max_blocks_per_seq, max_context_len, scale as
+ *                in pa_decode; types fp16 for PA_KV_F16, bf16 otherwise
+ *   workspace    pa_latent_attention_workspace_size bytes, 256-byte aligned,
+ *                used only for the duration of the work on `stream`; it needs
+ *                no initialisation
+ * Scores, softmax and sums in fp32; the probabilities are rounded to the
+ * cache's 16-bit type for the product with the rows.  Device-side cases as in
+ * pa_attention_causal (L = 0 decodes to a zero row, an invalid L, T > L or a
+ * block id out of range to NaN rows).  Deterministic.  pa_workspace_status
+ * reads the error word. */
+PA_API int pa_latent_attention(void *out, const void *query, const void *cache, const int32_t *block_tables,
+                               const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                               int num_query_tokens, int num_heads, int block_size, int64_t num_blocks,
+                               int max_blocks_per_seq, int max_context_len, float scale, int kv_dtype,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes pa_latent_attention_expanded needs (a host-side bound; 0
+ * for invalid sizes). */
+PA_API size_t pa_latent_attention_expanded_workspace_size(int num_seqs, int num_query_tokens, int num_heads);
+
+/* Attention in the expanded form, for prompts: every head's keys and values
+ * have been computed from the latents (of the new tokens, and of the cached
+ * prefix through pa_latent_read), so that a score costs 192 products instead
+ * of the absorbed form's 576.  Tokens of sequence i are rows kv_start[i] ..
+ * kv_start[i + 1] - 1 of the keys and values, its new tokens (the last T of
+ * them) rows query_start[i] .. of query and out; new token j sees keys
+ * t <= Lk - T + j, Lk = kv_start[i + 1] - kv_start[i]:
+ *   s_t = scale * (<q[0 .. 127], k_nope_t[h]> + <q[128 .. 191], k_rope_t>),
+ *   out = sum_t softmax(s)_t * value_t[h].
+ *   out      16-bit [num_query_tokens][num_heads][128]
+ *   query    16-bit [num_query_tokens][num_heads][192]
+ *   k_nope   16-bit [num_kv_tokens][num_heads][128], value alike, token and
+ *            head strides in elements (multiples of 8, head stride >= 128:
+ *            both may be slices of one product's rows)
+ *   k_rope   16-bit [num_kv_tokens][64], rows rope_stride elements apart
+ *   query_start, kv_start  int32 [num_seqs + 1], device, each a non-decreasing
+ *            cover of its rows
+ *   dtype    PA_KV_F16 or PA_KV_BF16, all tensors; pointers 16-byte aligned
+ * A sequence with T > Lk gets NaN rows, and every row is NaN when query_start
+ * or kv_start breaks its order or does not end at its row count.  Scores,
+ * softmax and sums in fp32.  Deterministic.  pa_workspace_status reads the
+ * error word. */
+PA_API int pa_latent_attention_expanded(void *out, const void *query, const void *k_nope, const void *k_rope,
+                                        const void *value, const int32_t *query_start, const int32_t *kv_start,
+                                        int num_seqs, int num_query_tokens, int num_kv_tokens, int num_heads,
+                                        int64_t k_token_stride, int64_t k_head_stride, int64_t rope_stride,
+                                        int64_t v_token_stride, int64_t v_head_stride, float scale, int dtype,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------- verification of drafted tokens */
+
+/* Element type of probability rows. */
+enum {
+    PA_PROBS_F32 = 0,
+    PA_PROBS_F16 = 1,
+    PA_PROBS_BF16 = 2
+};
+
+/* Decide which drafted tokens of a speculative step stand, and the token that
+ * follows them (the step after pa_attention_causal or pa_latent_attention has
+ * run over T = n + 1 new tokens of a sequence: the last known one and its n
+ * drafts).  Sequence i has the drafts draft_start[i] .. draft_start[i + 1] - 1
+ * (n of them) and n + 1 rows of target probabilities p, from row
+ * draft_start[i] + i on.  Draft j (token d, draft probabilities q) stands when
+ * it and all drafts before it pass
+ *   uniform[j] * q[d] < p_j[d]            (products and comparison exact).
+ * With a drafts standing, the next token is drawn from the weights
+ *   w_v = max(p_a[v] - q_a[v], 0) if a < n,   w_v = p_n[v] if a = n,
+ * as the smallest v with w_0 + ... + w_v > sample_uniform[i] * sum(w).  So the
+ * tokens are distributed as if drawn from p one by one.
+ *   accepted      int32 [num_seqs]: a
+ *   tokens        int32 [num_seqs][max_drafts + 1]: the a drafts, the drawn
+ *                 token, then -1
+ *   target_probs  [num_drafts + num_seqs] rows of vocab_size, target_stride
+ *                 elements apart (>= vocab_size), of type probs_dtype; rows
+ *                 need not sum to one
+ *   draft_probs   [num_drafts] rows, draft_stride apart, or NULL: each draft
+ *                 had probability one (so w is p without the failed draft)
+ *   draft_tokens, uniform  int32 / float [num_drafts]
+ *   draft_start   int32 [num_seqs + 1], device, a non-decreasing cover of the
+ *                 drafts; n at most max_drafts
+ *   sample_uniform  float [num_seqs], in [0, 1)
+ * NaN and negative weights count as zero.  If the weights of a failed draft
+ * sum to zero (q covers p), the token is drawn from p_a; if that sums to zero
+ * as well, or a sum is not finite, it is -1.  A sequence with a draft token
+ * outside the vocabulary before its first failing draft, or with a bad
+ * draft_start, gets a = -1 and tokens -1.  Sums are carried in twice the
+ * precision of a float.  Needs no workspace. */
+PA_API int pa_verify_drafts(int32_t *accepted, int32_t *tokens, const void *target_probs, const void *draft_probs,
+                            const int32_t *draft_tokens, const int32_t *draft_start, const float *uniform,
+                            const float *sample_uniform, int num_seqs, int num_drafts, int max_drafts,
+                            int vocab_size, int64_t target_stride, int64_t draft_stride, int probs_dtype,
+                            void *stream);
+
 /* ------------------------------------------------------ block allocator */
 
 /* Host-side block allocator with reference counts (no GPU involved).

@@ -12,6 +12,10 @@ streams only):
   caches    fp16 [num_blocks, num_kv_heads, block_size, head_dim]
   query/out fp16 [num_seqs, num_heads, head_dim]
   key/value fp16 [num_tokens, num_kv_heads, head_dim]
+Latent caches (the pa_latent_* calls) hold one row per token for all heads:
+  16-bit    [num_blocks, block_size, 576] = 512 latent elements, 64 rotary ones
+  FP8       uint8 [num_blocks, block_size, 656] = 512 E4M3 codes, 64 bf16
+            rotary elements, 4 float scales
 """
 from __future__ import annotations
 
@@ -41,11 +45,19 @@ EXPORTS = (
     "pa_alloc_match_prefix", "pa_alloc_append_ids", "pa_alloc_block_hash", "pa_alloc_prefix_stats", "pa_sha256",
     "pa_decode_shared_prefix_workspace_size", "pa_decode_shared_prefix", "pa_selftest_wait_timeout",
     "pa_attention_causal_workspace_size", "pa_attention_causal", "pa_kv_write_fp8", "pa_block_copy_typed",
-    "pa_decode_typed", "pa_attention_causal_typed", "pa_decode_static_ws_status",
+    "pa_decode_typed", "pa_attention_causal_typed", "pa_decode_static_ws_status", "pa_latent_write",
+    "pa_latent_block_copy", "pa_latent_read", "pa_latent_attention_workspace_size", "pa_latent_attention",
+    "pa_latent_attention_expanded_workspace_size", "pa_latent_attention_expanded", "pa_verify_drafts",
 )
 
 # cache element types (PA_KV_* in pa.h)
 PA_KV_F16, PA_KV_BF16, PA_KV_FP8_E4M3 = 0, 1, 2
+
+# a latent cache's row (PA_LATENT_* in pa.h): latent and rotary elements, bytes when quantised
+PA_LATENT_DIM, PA_LATENT_ROPE_DIM, PA_LATENT_ROW, PA_LATENT_ROW_FP8_BYTES = 512, 64, 576, 656
+
+# element types of probability rows (PA_PROBS_* in pa.h)
+PA_PROBS_F32, PA_PROBS_F16, PA_PROBS_BF16 = 0, 1, 2
 
 # bytes of the library's built-in scratch array used by pa_decode_static_ws
 PA_DECODE_STATIC_WS_BYTES = 64 << 20
@@ -115,6 +127,16 @@ def lib():
                                            ctypes.c_float, i32, ctypes.c_float, ctypes.c_float, vp, sz, vp], i32),
             "pa_attention_causal": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64, i32, i32,
                                      ctypes.c_float, vp, sz, vp], i32),
+            "pa_latent_write": ([vp, vp, vp, vp, i32, i64, i64, i32, i64, i32, vp], i32),
+            "pa_latent_block_copy": ([vp, vp, i32, i32, i64, i32, vp], i32),
+            "pa_latent_read": ([vp, vp, vp, vp, vp, i32, i32, i64, i32, i64, i32, i32, vp], i32),
+            "pa_latent_attention_workspace_size": ([i32, i32, i32, i32], sz),
+            "pa_latent_attention": ([vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i32, i32, ctypes.c_float, i32,
+                                     vp, sz, vp], i32),
+            "pa_latent_attention_expanded_workspace_size": ([i32, i32, i32], sz),
+            "pa_latent_attention_expanded": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i64, i64, i64, i64,
+                                              ctypes.c_float, i32, vp, sz, vp], i32),
+            "pa_verify_drafts": ([vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i64, i32, vp], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -425,6 +447,203 @@ def pa_workspace_status(workspace, stream=None) -> int:
     st = ctypes.c_int(0)
     _check(lib().pa_workspace_status(workspace.data_ptr(), ctypes.byref(st), _stream(stream)), "pa_workspace_status")
     return st.value
+
+
+# ---------------------------------------------------------------- latent cache
+
+def _tensors(where, dev, *specs):
+    """Check (tensor, name, dtypes, dims, contiguous) entries: CUDA tensors on
+    one device; those not contiguous need unit stride in the last dimension."""
+    for t, name, dtypes, ndim, dense in specs:
+        if t.device != dev or not t.is_cuda:
+            raise ValueError(f"{where}: {name} must be a CUDA tensor on the device of the others ({dev})")
+        if t.dtype not in dtypes or t.dim() != ndim:
+            raise ValueError(f"{where}: {name}: expected a {ndim}-d tensor of {dtypes[0]}, got {t.dim()}-d {t.dtype}")
+        if dense and not t.is_contiguous() or not dense and t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{where}: {name} must be contiguous" + ("" if dense else " in its last dimension"))
+
+
+def _run(where, dev, stream, *args):
+    """Call the library on device `dev` and the given (or its current) stream."""
+    import torch
+    f = getattr(lib(), where)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(f(*args, h), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, h), where)
+
+
+def _latent_cache(where, cache):
+    """(PA_KV_*, torch dtype of the rows that go in and come out) of a latent cache tensor."""
+    import torch
+    if cache.dim() == 3:
+        if cache.dtype == torch.uint8 and cache.shape[2] == PA_LATENT_ROW_FP8_BYTES:
+            return PA_KV_FP8_E4M3, torch.bfloat16
+        if cache.dtype in (torch.float16, torch.bfloat16) and cache.shape[2] == PA_LATENT_ROW:
+            return (PA_KV_F16 if cache.dtype == torch.float16 else PA_KV_BF16), cache.dtype
+    raise ValueError(f"{where}: a latent cache is [num_blocks, block_size, {PA_LATENT_ROW}] float16 or bfloat16, or "
+                     f"[num_blocks, block_size, {PA_LATENT_ROW_FP8_BYTES}] uint8")
+
+
+def pa_latent_write(latent, rope, slot_mapping, cache, stream=None):
+    """Write latent[t] ([num_tokens, 512]) and rope[t] ([num_tokens, 64]) to
+    slot slot_mapping[t] of a latent cache (slot < 0: skipped); bf16 rows are
+    quantised as they go into an FP8 cache.  latent and rope may be slices of
+    wider rows (unit stride in the last dimension)."""
+    import torch
+    kv, dt = _latent_cache("pa_latent_write", cache)
+    n = latent.shape[0]
+    _tensors("pa_latent_write", cache.device, (cache, "cache", (cache.dtype,), 3, True),
+             (latent, "latent", (dt,), 2, False), (rope, "rope", (dt,), 2, False),
+             (slot_mapping, "slot_mapping", (torch.int64,), 1, True))
+    if latent.shape[1] != PA_LATENT_DIM or rope.shape != (n, PA_LATENT_ROPE_DIM) or slot_mapping.shape[0] != n:
+        raise ValueError("pa_latent_write: shape mismatch")
+    # one row (or none) has no stride of its own
+    sl, sr = (latent.stride(0), rope.stride(0)) if n > 1 else (PA_LATENT_DIM, PA_LATENT_ROPE_DIM)
+    _run("pa_latent_write", cache.device, stream, latent.data_ptr(), rope.data_ptr(), slot_mapping.data_ptr(),
+         cache.data_ptr(), n, sl, sr, cache.shape[1], cache.shape[0], kv)
+
+
+def pa_latent_block_copy(cache, pairs, stream=None):
+    """Copy every (src, dst) block pair of int64 ``pairs`` [n, 2] of a latent cache."""
+    import torch
+    kv, _ = _latent_cache("pa_latent_block_copy", cache)
+    _tensors("pa_latent_block_copy", cache.device, (cache, "cache", (cache.dtype,), 3, True),
+             (pairs, "pairs", (torch.int64,), 2, True))
+    if pairs.shape[1] != 2:
+        raise ValueError("pa_latent_block_copy: shape mismatch")
+    _run("pa_latent_block_copy", cache.device, stream, cache.data_ptr(), pairs.data_ptr(), pairs.shape[0],
+         cache.shape[1], cache.shape[0], kv)
+
+
+def pa_latent_read(out, cache, block_tables, row_start, first_token=None, stream=None):
+    """Read cached rows back: out[row_start[i] + j] ([num_rows, 576], rows may
+    be strided) = token first_token[i] + j (0 + j without first_token) of
+    sequence i; rows from row_start[-1] on are left as they are."""
+    import torch
+    kv, dt = _latent_cache("pa_latent_read", cache)
+    i32 = (torch.int32,)
+    _tensors("pa_latent_read", cache.device, (cache, "cache", (cache.dtype,), 3, True), (out, "out", (dt,), 2, False),
+             (block_tables, "block_tables", i32, 2, True), (row_start, "row_start", i32, 1, True),
+             *(((first_token, "first_token", i32, 1, True),) if first_token is not None else ()))
+    n, b = out.shape[0], block_tables.shape[0]
+    if out.shape[1] != PA_LATENT_ROW or row_start.shape[0] != b + 1 or \
+            (first_token is not None and first_token.shape[0] != b):
+        raise ValueError("pa_latent_read: shape mismatch")
+    _run("pa_latent_read", cache.device, stream, out.data_ptr(), cache.data_ptr(), block_tables.data_ptr(),
+         row_start.data_ptr(), None if first_token is None else first_token.data_ptr(), b, n,
+         out.stride(0) if n > 1 else PA_LATENT_ROW, cache.shape[1], cache.shape[0], block_tables.shape[1], kv)
+
+
+def pa_latent_attention_workspace_size(num_seqs, num_query_tokens, num_heads, max_context_len) -> int:
+    n = lib().pa_latent_attention_workspace_size(int(num_seqs), int(num_query_tokens), int(num_heads),
+                                                 int(max_context_len))
+    if n == 0:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_latent_attention_workspace_size")
+    return n
+
+
+def pa_latent_attention(out, query, cache, block_tables, context_lens, scale, max_context_len, workspace,
+                        query_start=None, stream=None):
+    """Attention over a latent cache, queries multiplied into the latent space:
+    out[row][h] ([n, heads, 512]) = softmax(scale q C^T) C[:, :512] over the
+    rows C of the sequence, q = query[row][h] ([n, heads, 576]).  Without
+    query_start one row per sequence (decode); with it rows query_start[i] ..
+    query_start[i + 1] - 1 are sequence i's last new tokens, causal."""
+    import torch
+    kv, dt = _latent_cache("pa_latent_attention", cache)
+    i32 = (torch.int32,)
+    _tensors("pa_latent_attention", cache.device, (cache, "cache", (cache.dtype,), 3, True),
+             (out, "out", (dt,), 3, True), (query, "query", (dt,), 3, True),
+             (block_tables, "block_tables", i32, 2, True), (context_lens, "context_lens", i32, 1, True),
+             (workspace, "workspace", (torch.uint8,), 1, True),
+             *(((query_start, "query_start", i32, 1, True),) if query_start is not None else ()))
+    nq, h, w = query.shape
+    b = context_lens.shape[0]
+    if w != PA_LATENT_ROW or out.shape != (nq, h, PA_LATENT_DIM) or block_tables.shape[0] != b or \
+            (nq != b if query_start is None else query_start.shape[0] != b + 1):
+        raise ValueError("pa_latent_attention: shape mismatch")
+    _run("pa_latent_attention", cache.device, stream, out.data_ptr(), query.data_ptr(), cache.data_ptr(),
+         block_tables.data_ptr(), context_lens.data_ptr(), None if query_start is None else query_start.data_ptr(), b,
+         nq, h, cache.shape[1], cache.shape[0], block_tables.shape[1], int(max_context_len), float(scale), kv,
+         workspace.data_ptr(), workspace.numel())
+
+
+def pa_latent_attention_expanded_workspace_size(num_seqs, num_query_tokens, num_heads) -> int:
+    n = lib().pa_latent_attention_expanded_workspace_size(int(num_seqs), int(num_query_tokens), int(num_heads))
+    if n == 0:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_latent_attention_expanded_workspace_size")
+    return n
+
+
+def pa_latent_attention_expanded(out, query, k_nope, k_rope, value, query_start, kv_start, scale, workspace,
+                                 stream=None):
+    """Causal attention over keys and values expanded per head from latents:
+    query [nq, heads, 192], k_nope and value [nk, heads, 128] (token and head
+    strides free: slices of one product), k_rope [nk, 64] shared by the heads,
+    out [nq, heads, 128]; sequence i has rows kv_start[i] .. kv_start[i + 1] - 1
+    of the keys, its last new tokens rows query_start[i] .. of the queries."""
+    import torch
+    where = "pa_latent_attention_expanded"
+    dt, i32 = (query.dtype,), (torch.int32,)
+    if query.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{where}: query must be float16 or bfloat16")
+    _tensors(where, query.device, (query, "query", dt, 3, True), (out, "out", dt, 3, True),
+             (k_nope, "k_nope", dt, 3, False), (value, "value", dt, 3, False), (k_rope, "k_rope", dt, 2, False),
+             (query_start, "query_start", i32, 1, True), (kv_start, "kv_start", i32, 1, True),
+             (workspace, "workspace", (torch.uint8,), 1, True))
+    nq, h, w = query.shape
+    nk = k_nope.shape[0]
+    if w != 192 or out.shape != (nq, h, 128) or k_nope.shape != (nk, h, 128) or value.shape != (nk, h, 128) or \
+            k_rope.shape != (nk, 64) or query_start.shape != kv_start.shape or query_start.shape[0] < 1:
+        raise ValueError(f"{where}: shape mismatch")
+
+    def strides(t):   # a dimension of size one has no stride of its own
+        head = t.stride(1) if h > 1 else 128
+        return (t.stride(0) if nk > 1 else h * head), head
+    kt, kh = strides(k_nope)
+    vt, vh = strides(value)
+    _run(where, query.device, stream, out.data_ptr(), query.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(),
+         value.data_ptr(), query_start.data_ptr(), kv_start.data_ptr(), query_start.shape[0] - 1, nq, nk, h, kt, kh,
+         k_rope.stride(0) if nk > 1 else 64, vt, vh, float(scale),
+         PA_KV_F16 if query.dtype == torch.float16 else PA_KV_BF16, workspace.data_ptr(), workspace.numel())
+
+
+# ---------------------------------------------------------------- speculative steps
+
+def pa_verify_drafts(accepted, tokens, target_probs, draft_probs, draft_tokens, draft_start, uniform, sample_uniform,
+                     stream=None):
+    """How many drafted tokens of each sequence stand (accepted [num_seqs]) and
+    the tokens that follow (tokens [num_seqs, max_drafts + 1]: those drafts, one
+    token drawn from max(p - q, 0) or p, then -1).  target_probs [num_drafts +
+    num_seqs, vocab] and draft_probs [num_drafts, vocab] (or None: drafts of
+    probability one) are float32, float16 or bfloat16 rows; sequence i's drafts
+    are draft_start[i] .. draft_start[i + 1] - 1."""
+    import torch
+    where = "pa_verify_drafts"
+    kinds = {torch.float32: PA_PROBS_F32, torch.float16: PA_PROBS_F16, torch.bfloat16: PA_PROBS_BF16}
+    if target_probs.dtype not in kinds:
+        raise ValueError(f"{where}: target_probs must be float32, float16 or bfloat16")
+    dt, i32, f32 = (target_probs.dtype,), (torch.int32,), (torch.float32,)
+    _tensors(where, target_probs.device, (target_probs, "target_probs", dt, 2, False),
+             (accepted, "accepted", i32, 1, True), (tokens, "tokens", i32, 2, True),
+             (draft_tokens, "draft_tokens", i32, 1, True), (draft_start, "draft_start", i32, 1, True),
+             (uniform, "uniform", f32, 1, True), (sample_uniform, "sample_uniform", f32, 1, True),
+             *(((draft_probs, "draft_probs", dt, 2, False),) if draft_probs is not None else ()))
+    b, nd, v = accepted.shape[0], draft_tokens.shape[0], target_probs.shape[1]
+    if target_probs.shape[0] != nd + b or tokens.shape[0] != b or tokens.shape[1] < 1 or uniform.shape[0] != nd or \
+            draft_start.shape[0] != b + 1 or sample_uniform.shape[0] != b or \
+            (draft_probs is not None and draft_probs.shape != (nd, v)):
+        raise ValueError(f"{where}: shape mismatch")
+    _run(where, target_probs.device, stream, accepted.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(),
+         None if draft_probs is None else draft_probs.data_ptr(), draft_tokens.data_ptr(), draft_start.data_ptr(),
+         uniform.data_ptr(), sample_uniform.data_ptr(), b, nd, tokens.shape[1] - 1, v,
+         target_probs.stride(0) if nd + b > 1 else v, draft_probs.stride(0) if draft_probs is not None and nd > 1 else v,
+         kinds[target_probs.dtype])
 
 
 # ---------------------------------------------------------------- allocator

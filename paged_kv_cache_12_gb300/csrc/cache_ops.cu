@@ -103,13 +103,18 @@ __global__ void block_copy_kernel(uint4 *__restrict__ k_cache, uint4 *__restrict
     }
 }
 
-// PA_DEBUG_VALIDATE: every slot below num_slots, no slot written twice.
-int validate_slots(const int64_t *slot_mapping, int num_tokens, long long num_slots, cudaStream_t st) {
-    std::vector<int64_t> h((size_t)num_tokens);
-    if (cudaMemcpyAsync(h.data(), slot_mapping, sizeof(int64_t) * num_tokens, cudaMemcpyDeviceToHost, st) !=
-            cudaSuccess ||
+}  // namespace
+
+int copy_to_host(void *dst, const void *src, size_t bytes, cudaStream_t st) {
+    if (cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
         return PA_ERR_CUDA;
+    return 0;
+}
+
+int validate_slots(const int64_t *slot_mapping, int num_tokens, long long num_slots, cudaStream_t st) try {
+    std::vector<int64_t> h((size_t)num_tokens);
+    if (const int e = copy_to_host(h.data(), slot_mapping, sizeof(int64_t) * h.size(), st)) return e;
     std::vector<int64_t> seen;
     seen.reserve(h.size());
     for (int64_t s : h) {
@@ -120,11 +125,31 @@ int validate_slots(const int64_t *slot_mapping, int num_tokens, long long num_sl
     for (size_t i = 1; i < seen.size(); ++i)
         if (seen[i] == seen[i - 1]) return PA_ERR_INVALID_ARG;
     return 0;
+} catch (...) {   // no host memory for the check
+    return PA_ERR_STATE;
 }
 
-// SM count of the current device, asked on every call (a cheap attribute
-// query), so that each device sizes its own grid.  The kernels stride over
-// their work, so the count only sets the grid cap.
+int validate_pairs(const int64_t *pairs, int num_pairs, long long num_blocks, cudaStream_t st) try {
+    std::vector<int64_t> h((size_t)num_pairs * 2);
+    if (const int e = copy_to_host(h.data(), pairs, sizeof(int64_t) * h.size(), st)) return e;
+    std::vector<int64_t> srcs, dsts;
+    for (int i = 0; i < num_pairs; ++i) {
+        int64_t s = h[2 * i], d = h[2 * i + 1];
+        if (s < 0 || s >= num_blocks || d < 0 || d >= num_blocks) return PA_ERR_INVALID_ARG;
+        srcs.push_back(s);
+        dsts.push_back(d);
+    }
+    std::sort(srcs.begin(), srcs.end());
+    std::sort(dsts.begin(), dsts.end());
+    for (size_t i = 1; i < dsts.size(); ++i)
+        if (dsts[i] == dsts[i - 1]) return PA_ERR_INVALID_ARG;
+    for (int64_t d : dsts)
+        if (std::binary_search(srcs.begin(), srcs.end(), d)) return PA_ERR_INVALID_ARG;
+    return 0;
+} catch (...) {
+    return PA_ERR_STATE;
+}
+
 int num_sms() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
@@ -133,7 +158,6 @@ int num_sms() {
     return n;
 }
 
-}  // namespace
 }  // namespace pa
 
 using namespace pa;
@@ -174,26 +198,8 @@ extern "C" int pa_block_copy(uint16_t *k_cache, uint16_t *v_cache, const int64_t
     if (!k_cache || !v_cache || !pairs || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
     if (num_pairs > 65535) return PA_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (debug_validate()) {
-        std::vector<int64_t> h((size_t)num_pairs * 2);
-        if (cudaMemcpyAsync(h.data(), pairs, sizeof(int64_t) * h.size(), cudaMemcpyDeviceToHost, st) !=
-                cudaSuccess ||
-            cudaStreamSynchronize(st) != cudaSuccess)
-            return PA_ERR_CUDA;
-        std::vector<int64_t> srcs, dsts;
-        for (int i = 0; i < num_pairs; ++i) {
-            int64_t s = h[2 * i], d = h[2 * i + 1];
-            if (s < 0 || s >= num_blocks || d < 0 || d >= num_blocks) return PA_ERR_INVALID_ARG;
-            srcs.push_back(s);
-            dsts.push_back(d);
-        }
-        std::sort(srcs.begin(), srcs.end());
-        std::sort(dsts.begin(), dsts.end());
-        for (size_t i = 1; i < dsts.size(); ++i)
-            if (dsts[i] == dsts[i - 1]) return PA_ERR_INVALID_ARG;
-        for (int64_t d : dsts)
-            if (std::binary_search(srcs.begin(), srcs.end(), d)) return PA_ERR_INVALID_ARG;
-    }
+    if (debug_validate())
+        if (const int e = validate_pairs(pairs, num_pairs, num_blocks, st)) return e;
     const long long vecs_per_block = (long long)num_kv_heads * block_size * head_dim / 8;
     const int threads = 256;
     long long gx = (vecs_per_block + threads - 1) / threads;

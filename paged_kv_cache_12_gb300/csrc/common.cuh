@@ -19,6 +19,20 @@ namespace pa {
 // to the host and check them before launching.
 bool debug_validate();
 
+// Copy device memory to the host through `st`, and wait for it; 0 or PA_ERR_CUDA.
+int copy_to_host(void *dst, const void *src, size_t bytes, cudaStream_t st);
+
+// PA_DEBUG_VALIDATE: every slot below num_slots, no slot written twice.
+int validate_slots(const int64_t *slot_mapping, int num_tokens, long long num_slots, cudaStream_t st);
+
+// PA_DEBUG_VALIDATE: every id of a block copy in range, destinations distinct
+// and none of them a source.
+int validate_pairs(const int64_t *pairs, int num_pairs, long long num_blocks, cudaStream_t st);
+
+// SM count of the current device, asked on every call (a cheap attribute
+// query), so that each device sizes its own grid.
+int num_sms();
+
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
