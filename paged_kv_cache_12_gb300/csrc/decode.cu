@@ -1207,3 +1207,11 @@ extern "C" int pa_decode_static_ws_status(int *status_out, void *stream) {
     if (!ws) return PA_ERR_CUDA;
     return pa_workspace_status(ws, status_out, stream);
 }
+
+namespace pa {
+
+PFN_cuTensorMapEncodeTiled_v12000 tma_encoder() { return tensor_map_encoder(); }
+
+long long pipeline_wait_limit() { return wait_limit_cycles(); }
+
+}  // namespace pa

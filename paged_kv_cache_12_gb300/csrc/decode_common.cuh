@@ -48,6 +48,10 @@
 
 namespace pa {
 
+// The driver's tensor-map encoder (null if it cannot be had) and the bound of
+// the pipelines' waits in clock cycles.
+PFN_cuTensorMapEncodeTiled_v12000 tma_encoder();
+long long pipeline_wait_limit();
 
 constexpr int MAX_PART_TOKENS = 1024;           // largest partition (one work item)
 #ifndef PA_DECODE_TARGET_ITEMS
