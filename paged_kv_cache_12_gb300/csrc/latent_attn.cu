@@ -5,9 +5,13 @@
 #include "decode_common.cuh"
 #include "latent.h"
 #include "umma.cuh"
+#include "work_axis.cuh"
 
 namespace pa {
 namespace {
+
+constexpr int LT_ROWS = 64;   // query rows of a row tile (new token x head, token-major)
+constexpr int LT_TOK = 64;    // tokens of a KV tile
 
 struct LatentArgs {
     uint16_t *out;
@@ -20,10 +24,49 @@ struct LatentArgs {
     float scale_log2;
     long long wait_limit;
     // workspace
-    int *status;            // [LT_MAX_CTAS] nonzero: the CTA gave up waiting
-    long long *unit_base;   // [num_seqs + 1] first work unit of each sequence
-    float2 *ml;             // [2 LT_MAX_CTAS][LT_ROWS] maximum (log2 units) and sum of a partial row
-    float *o;               // [2 LT_MAX_CTAS][LT_ROWS][LC] its unnormalised output
+    int *status;            // [AXIS_MAX_CTAS] nonzero: the CTA gave up waiting
+    long long *unit_base;   // [num_seqs + 1]
+    float2 *ml;             // [2 AXIS_MAX_CTAS][LT_ROWS] maximum (log2 units) and sum of a partial row
+    float *o;               // [2 AXIS_MAX_CTAS][LT_ROWS][LC] its unnormalised output
+
+    // ---- the work axis
+    static constexpr int COST = 1;
+    struct Seq {
+        int L, T, q0;   // context, new tokens, first query token
+        int tiles;      // KV tiles of the context (0: nothing to compute)
+        int rts;        // row tiles
+        bool valid;     // rows are computed (or zero, for an empty context)
+    };
+    __device__ __forceinline__ Seq seq_work(int i) const {
+        Seq w;
+        w.L = __ldg(context_lens + i);
+        w.q0 = query_start ? __ldg(query_start + i) : i;
+        w.T = query_start ? __ldg(query_start + i + 1) - w.q0 : 1;
+        w.valid = w.L >= 0 && w.L <= max_context_len && (long long)w.L <= (long long)mbps * bs &&
+                  !(query_start && w.T > w.L);
+        w.tiles = w.valid && w.T > 0 ? (w.L + LT_TOK - 1) / LT_TOK : 0;
+        w.rts = w.tiles ? (int)(((long long)w.T * H + LT_ROWS - 1) / LT_ROWS) : 0;
+        return w;
+    }
+    // Every row tile counts the whole context's KV tiles (a chunk's earlier
+    // rows see fewer, which matters only for long chunks; those belong to the
+    // expanded form).
+    __device__ __forceinline__ long long start(const Seq &w, int r) const { return (long long)r * (w.tiles + COST); }
+    // KV tiles that row tile r sees: up to its last row's own position.
+    __device__ __forceinline__ int row_tiles(const Seq &w, int r) const {
+        const long long last = min((long long)w.T * H, (long long)(r + 1) * LT_ROWS) - 1;
+        return (w.L - w.T + (int)(last / H) + 1 + LT_TOK - 1) / LT_TOK;
+    }
+    __device__ __forceinline__ bool starts_ok() const {
+        return !query_start || offsets_ok(query_start, num_seqs, num_query_tokens);
+    }
+    // rows of row tile r, and its first row in the query
+    __device__ __forceinline__ int rows(const Seq &w, int r) const {
+        return (int)min((long long)LT_ROWS, (long long)w.T * H - (long long)r * LT_ROWS);
+    }
+    __device__ __forceinline__ long long first_row(const Seq &w, int r) const {
+        return (long long)w.q0 * H + (long long)r * LT_ROWS;
+    }
 };
 
 template <int KV>
@@ -39,183 +82,6 @@ __device__ __forceinline__ uint16_t to_bits(float x) {
         return __half_as_ushort(__float2half_rn(x));
     else
         return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-
-// ------------------------------------------------------------------ the work
-//
-// A row tile is LT_ROWS consecutive query rows (new token x head, token-major)
-// of one sequence; its work is the KV tiles of LT_TOK tokens that its last row
-// sees.  All row tiles laid end to end, each with LT_COST more units for its
-// start and end, make one axis of work units, which is cut into equal ranges,
-// one per CTA: a CTA takes the pieces of row tiles inside its range.  A row tile
-// that lies in one range is finished there; the pieces of one that is cut leave
-// partial rows, at most two a CTA (one continued from the left, one to the
-// right), which a second kernel merges.  Every CTA derives the cut from the
-// lengths by itself, so nothing is planned on the host or in a launch of its own.
-
-constexpr int LT_ROWS = 64;
-constexpr int LT_TOK = 64;
-constexpr int LT_COST = 1;
-constexpr int LT_MAX_CTAS = 160;
-
-struct SeqWork {
-    int L, T, q0;     // context, new tokens, first query token
-    int tiles;        // KV tiles of the context (0: nothing to compute)
-    int rts;          // row tiles
-    bool valid;       // rows are computed (or zero, for an empty context)
-};
-
-__device__ __forceinline__ SeqWork seq_work(const LatentArgs &a, int i) {
-    SeqWork w;
-    w.L = __ldg(a.context_lens + i);
-    w.q0 = a.query_start ? __ldg(a.query_start + i) : i;
-    w.T = a.query_start ? __ldg(a.query_start + i + 1) - w.q0 : 1;
-    w.valid = w.L >= 0 && w.L <= a.max_context_len && (long long)w.L <= (long long)a.mbps * a.bs &&
-              !(a.query_start && w.T > w.L);
-    w.tiles = w.valid && w.T > 0 ? (w.L + LT_TOK - 1) / LT_TOK : 0;
-    w.rts = w.tiles ? (int)(((long long)w.T * a.H + LT_ROWS - 1) / LT_ROWS) : 0;
-    return w;
-}
-
-// KV tiles that row tile r sees: up to its last row's own position.
-__device__ __forceinline__ int row_tiles(const LatentArgs &a, const SeqWork &w, int r) {
-    const long long last = min((long long)w.T * a.H, (long long)(r + 1) * LT_ROWS) - 1;
-    const int vis = w.L - w.T + (int)(last / a.H) + 1;
-    return (vis + LT_TOK - 1) / LT_TOK;
-}
-
-// First unit of CTA k's range; `parts` = min(CTAs, total) CTAs have one, of at
-// least a unit each.
-__device__ __forceinline__ long long range_begin(long long total, int k, int parts) { return total * k / parts; }
-
-// The KV tiles [t0, t1) of the row tile at unit s that lie in [u0, u1).
-__device__ __forceinline__ void piece_tiles(long long s, int ntiles, long long u0, long long u1, int &t0, int &t1) {
-    t0 = (int)max(0LL, min((long long)ntiles, u0 - s - LT_COST));
-    t1 = (int)max(0LL, min((long long)ntiles, u1 - s - LT_COST));
-}
-
-struct Plan {
-    long long u0, u1, base;   // this CTA's range; first unit of sequence seq
-    int seq;                  // the sequence in which the range begins
-};
-
-// Walks the pieces of a CTA's range, in every role alike.
-struct Walk {
-    const LatentArgs &a;
-    long long u1, u0, s;      // s: first unit of row tile r of sequence seq
-    int seq, r;
-    SeqWork w;
-    int t0, t1, ntiles, local;   // the piece: KV tiles [t0, t1) of ntiles; its number in this CTA
-
-    __device__ Walk(const LatentArgs &args, const Plan &p) : a(args), u1(p.u1), u0(p.u0), s(p.base), seq(p.seq), r(0) {
-        local = -1;
-        if (u0 >= u1) return;
-        w = seq_work(a, seq);
-        if (w.tiles) {
-            r = (int)((u0 - s) / (w.tiles + LT_COST));
-            s += (long long)r * (w.tiles + LT_COST);
-        }
-        --r;
-        s -= w.tiles + LT_COST;
-    }
-    // The next piece; false at the end of the range.
-    __device__ bool next() {
-        if (u0 >= u1) return false;
-        for (;;) {
-            ++r;
-            s += w.tiles + LT_COST;
-            if (r >= w.rts) {
-                if (s >= u1) return false;
-                do {   // on to the next sequence that has work (s is its first unit)
-                    if (++seq >= a.num_seqs) return false;
-                    w = seq_work(a, seq);
-                } while (w.rts == 0);
-                r = 0;
-            }
-            if (s >= u1) return false;
-            ntiles = row_tiles(a, w, r);
-            piece_tiles(s, ntiles, u0, u1, t0, t1);
-            if (t1 > t0) {
-                ++local;
-                return true;
-            }
-        }
-    }
-    __device__ bool whole() const { return t0 == 0 && t1 == ntiles; }
-    // slot of this piece's partial rows: 0 if the row tile began before the range
-    __device__ int slot() const { return 2 * (int)blockIdx.x + (s < u0 ? 0 : 1); }
-    __device__ int rows() const { return (int)min((long long)LT_ROWS, (long long)w.T * a.H - (long long)r * LT_ROWS); }
-    __device__ long long first_row() const { return (long long)w.q0 * a.H + (long long)r * LT_ROWS; }
-};
-
-// Whether query_start is a non-decreasing cover of the query tokens (every
-// thread of the block calls it and gets the answer).
-__device__ __forceinline__ bool query_start_ok(const LatentArgs &a) {
-    if (!a.query_start) return true;
-    bool ok = a.query_start[0] == 0 && a.query_start[a.num_seqs] == a.num_query_tokens;
-    for (int i = threadIdx.x; i < a.num_seqs; i += blockDim.x)
-        if (a.query_start[i] > a.query_start[i + 1]) ok = false;
-    return __syncthreads_and(ok);
-}
-
-// The block's plan: units of all sequences summed in chunks, one per thread.
-// CTA 0 also writes every sequence's first unit for the merge.
-__device__ __forceinline__ void make_plan(const LatentArgs &a, Plan *plan, long long *warp_sums) {
-    const bool ok = query_start_ok(a);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    const int per = (a.num_seqs + blockDim.x - 1) / blockDim.x;
-    const int i0 = min(a.num_seqs, (int)threadIdx.x * per), i1 = min(a.num_seqs, i0 + per);
-    long long mine = 0;
-    for (int i = i0; ok && i < i1; ++i) {
-        const SeqWork w = seq_work(a, i);
-        mine += (long long)w.rts * (w.tiles + LT_COST);
-    }
-    long long upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += x;
-    }
-    if (lane == 31) warp_sums[warp] = upto;
-    if (threadIdx.x == 0) plan->seq = a.num_seqs;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int k = 0; k < nwarps; ++k) {
-        if (k < warp) before += warp_sums[k];
-        total += warp_sums[k];
-    }
-    const long long begin = before + upto - mine, end = before + upto;
-    const int parts = (int)min((long long)gridDim.x, total), cta = blockIdx.x;
-    const long long u0 = cta < parts ? range_begin(total, cta, parts) : 0;
-    const long long u1 = cta < parts ? range_begin(total, cta + 1, parts) : 0;
-    if (threadIdx.x == 0) {
-        plan->u0 = u0;
-        plan->u1 = u1;
-    }
-    if (u0 < u1 && begin <= u0 && u0 < end) {   // one thread
-        long long s = begin;
-        int i = i0;
-        for (;; ++i) {
-            const SeqWork w = seq_work(a, i);
-            const long long n = (long long)w.rts * (w.tiles + LT_COST);
-            if (u0 < s + n) break;
-            s += n;
-        }
-        plan->seq = i;
-        plan->base = s;
-    }
-    if (blockIdx.x == 0) {
-        long long s = begin;
-        for (int i = i0; i < i1; ++i) {
-            a.unit_base[i] = ok ? s : -1;
-            if (ok) {
-                const SeqWork w = seq_work(a, i);
-                s += (long long)w.rts * (w.tiles + LT_COST);
-            }
-        }
-        if (threadIdx.x == 0) a.unit_base[a.num_seqs] = ok ? total : -1;
-    }
-    __syncthreads();
 }
 
 // ------------------------------------------------------------------ 16-bit kernel
@@ -284,7 +150,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) latent_kernel(const __grid_cons
         __syncthreads();
         tc_fence_after_sync();
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
-        Walk p(a, plan);
+        Walk<LatentArgs> p(a, plan);
         if (warp == 0) {
             // ---- producer: lane j < 8 copies tokens 8 j .. 8 j + 7 of a tile, lanes 8 .. 15 the query rows
             const uint64_t first = policy_evict_first(), keep = policy_evict_normal();
@@ -302,7 +168,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) latent_kernel(const __grid_cons
                 if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.qfull), LT_ROWS / 8 * LT_GROUP);
                 __syncwarp();
                 if (lane >= 8 && lane < 16)
-                    tma_load_3d(base + LT_OFF_Q + (lane - 8) * LT_GROUP, &tmq, 0, (int)(p.first_row() + 8 * (lane - 8)),
+                    tma_load_3d(base + LT_OFF_Q + (lane - 8) * LT_GROUP, &tmq, 0, (int)(a.first_row(p.w, p.r) + 8 * (lane - 8)),
                                 0, smem_u32(&c.qfull), keep);
                 ++pieces;
                 for (int t = p.t0; t < p.t1; ++t) {
@@ -407,7 +273,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) latent_kernel(const __grid_cons
             };
             int n = 0;
             while (ok && p.next()) {
-                const int rows = p.rows();
+                const int rows = a.rows(p.w, p.r);
                 const bool live = 16 * q < rows;      // some row of this warp exists
                 const bool mine = m < rows;
                 const int vis = mine ? p.w.L - p.w.T + (int)(((long long)p.r * LT_ROWS + m) / a.H) + 1 : p.w.L;
@@ -502,7 +368,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) latent_kernel(const __grid_cons
                     if (bad) l = __int_as_float(0x7fc00000);
                     const bool whole = p.whole();
                     const float inv = 1.f / l;
-                    uint16_t *orow = a.out + (p.first_row() + m) * LC + 256 * half;
+                    uint16_t *orow = a.out + (a.first_row(p.w, p.r) + m) * LC + 256 * half;
                     float *part = a.o + ((long long)p.slot() * LT_ROWS + m) * LC + 256 * half;
                     if (!whole && mine && half == 0) a.ml[p.slot() * LT_ROWS + m] = make_float2(mrun, l);
 #pragma unroll 1
@@ -562,17 +428,9 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentArgs a, i
     if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
     const long long total = a.unit_base[a.num_seqs];
     uint16_t *orow = a.out + row * LC;
-    int seq = qt;
-    if (a.query_start && total >= 0) {   // the last sequence that starts at or before this token
-        int lo = 0, hi = a.num_seqs;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.query_start[mid] <= qt) lo = mid; else hi = mid;
-        }
-        seq = lo;
-    }
-    SeqWork w{};
-    if (total >= 0) w = seq_work(a, seq);
+    const int seq = a.query_start && total >= 0 ? sequence_of(a.query_start, a.num_seqs, qt) : qt;
+    LatentArgs::Seq w{};
+    if (total >= 0) w = a.seq_work(seq);
     if (failed || total < 0 || !w.valid || w.tiles == 0) {
         const uint16_t x = !failed && total >= 0 && w.valid ? 0 : out_bits<KV>(__int_as_float(0x7fc00000));
         for (int d = threadIdx.x; d < LC; d += blockDim.x) orow[d] = x;
@@ -580,32 +438,18 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentArgs a, i
     }
     const long long idx = row - (long long)w.q0 * a.H;
     const int r = (int)(idx / LT_ROWS), m = (int)(idx % LT_ROWS);
-    const int ntiles = row_tiles(a, w, r);
-    const long long s = a.unit_base[seq] + (long long)r * (w.tiles + LT_COST);
-    // the CTA whose range holds unit u is the smallest k with range_begin(k + 1) > u
-    const long long ufirst = s + LT_COST, ulast = s + LT_COST + ntiles - 1;
-    const int parts = (int)min((long long)ctas, total);
-    auto cta_of = [&](long long u) {
-        int k = (int)(u * parts / total);
-        while (range_begin(total, k + 1, parts) <= u) ++k;
-        while (range_begin(total, k, parts) > u) --k;
-        return k;
-    };
-    const int k0 = cta_of(ufirst), k1 = cta_of(ulast);
-    if (k0 == k1) return;   // finished by one CTA
+    const Pieces pc(a.unit_base[seq] + a.start(w, r), a.row_tiles(w, r), LatentArgs::COST, total, ctas);
+    if (pc.k0 == pc.k1) return;   // finished by one CTA
     const int g = threadIdx.x >> 7, d = threadIdx.x & 127;
     float M = -INFINITY;
 #pragma unroll 8
-    for (int k = k0; k <= k1; ++k) {
-        const int slot = 2 * k + (s < range_begin(total, k, parts) ? 0 : 1);
-        M = fmaxf(M, a.ml[slot * LT_ROWS + m].x);
-    }
+    for (int k = pc.k0; k <= pc.k1; ++k) M = fmaxf(M, a.ml[pc.slot(k) * LT_ROWS + m].x);
     const float mu = M == -INFINITY ? 0.f : M;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll 4
-    for (int k = k0 + g; k <= k1; k += 4) {
-        const int slot = 2 * k + (s < range_begin(total, k, parts) ? 0 : 1);
+    for (int k = pc.k0 + g; k <= pc.k1; k += 4) {
+        const int slot = pc.slot(k);
         const float2 ml = a.ml[slot * LT_ROWS + m];
         const float4 o = *reinterpret_cast<const float4 *>(a.o + ((long long)slot * LT_ROWS + m) * LC + 4 * d);
         const float wt = fast_exp2(ml.x - mu);
@@ -652,10 +496,10 @@ LtLayout lt_layout(int num_seqs) {
         at = (at + bytes + 255) / 256 * 256;
         return p;
     };
-    l.status = take(sizeof(int) * LT_MAX_CTAS);
+    l.status = take(sizeof(int) * AXIS_MAX_CTAS);
     l.unit_base = take(sizeof(long long) * ((size_t)num_seqs + 1));
-    l.ml = take(sizeof(float2) * 2 * LT_MAX_CTAS * LT_ROWS);
-    l.o = take(sizeof(float) * 2 * LT_MAX_CTAS * LT_ROWS * LC);
+    l.ml = take(sizeof(float2) * 2 * AXIS_MAX_CTAS * LT_ROWS);
+    l.o = take(sizeof(float) * 2 * AXIS_MAX_CTAS * LT_ROWS * LC);
     l.total = at;
     return l;
 }
@@ -710,7 +554,7 @@ int launch_latent(const LatentArgs &a, cudaStream_t st) {
     if (!row_map(&tmkv, a.cache, a.num_blocks * a.bs, KV) ||
         !row_map(&tmq, a.query, (long long)a.num_query_tokens * a.H, KV))
         return PA_ERR_CUDA;
-    const int ctas = std::min(num_sms(), LT_MAX_CTAS);
+    const int ctas = std::min(num_sms(), AXIS_MAX_CTAS);
     latent_kernel<KV><<<ctas, LT_THREADS, LT_SMEM, st>>>(tmkv, tmq, a);
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     return launch_merge<KV>(a, ctas, st);

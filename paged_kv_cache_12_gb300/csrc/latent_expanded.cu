@@ -1,94 +1,616 @@
-// Attention in the expanded form.
+// Attention in the expanded form: every head's keys and values have been
+// computed from the latents, contiguous and ragged (no block table), keys of
+// 128 + 64 elements whose last 64 all heads share.
+//
+// A row tile is 256 consecutive new tokens of one sequence and one head, in two
+// halves of 128 rows that share every key and value block the CTA loads.  Its
+// causal KV tiles are a stretch of the work axis (work_axis.cuh), cut into
+// equal ranges over the CTAs, so that a chunk of few heads or a ragged batch
+// leaves no CTA idle in a last round (2048 new tokens of 32 heads are 256 row
+// tiles for 152 CTAs: whole tiles would take two rounds where 1.7 do).
+//
+// Warps: 0 loads, 1 and 3 idle, 2 issues the MMAs, 4-7 and 8-11 run the softmax
+// of the two halves, one row per thread.  Tensor memory: S0, S1, O0, O1 (128
+// columns each); P is written over the first 64 columns of its S.  Shared
+// memory: both halves' queries (96 KB) and a ring of eight 16 KB blocks (128
+// tokens x 64 elements), which the three blocks of a key tile and the two of a
+// value tile pass through in the order in which the MMAs take them: 128 KB hold
+// 1.6 KV tiles, where whole tiles would leave room for one and a half stages.
+// MMA order: PV0(n), S0(n + 1), PV1(n), S1(n + 1): while one half's softmax works
+// on its S, the other half's products run.  The MMAs of one thread complete in
+// issue order, so when S_x(n) is complete so is PV_x(n - 1).
+
+#include <algorithm>
 #include <cmath>
 
 #include "decode_common.cuh"
 #include "latent.h"
+#include "umma.cuh"
+#include "work_axis.cuh"
 
 namespace pa {
 namespace {
 
 constexpr int EN = 128, ER = PA_LATENT_ROPE_DIM, EQ = EN + ER, EV = 128;
+constexpr int EX_HALF = 128;               // rows of a half
+constexpr int EX_ROWS = 2 * EX_HALF;       // rows of a row tile
+constexpr int EX_TOK = 128;                // tokens of a KV tile
 
 struct ExpandedArgs {
     uint16_t *out;
-    const uint16_t *query, *k_nope, *k_rope, *value;
     const int32_t *query_start, *kv_start;
     WsHeader *hdr;
     int num_seqs, num_query_tokens, num_kv_tokens, H;
-    long long kt, kh, rt, vt, vh;
     float scale_log2;
+    long long wait_limit;
+    // workspace
+    int *status;            // [AXIS_MAX_CTAS] nonzero: the CTA gave up waiting
+    long long *unit_base;   // [num_seqs + 1]
+    float2 *ml;             // [2 AXIS_MAX_CTAS][EX_ROWS] maximum (log2 units) and sum of a partial row
+    float *o;               // [2 AXIS_MAX_CTAS][EX_ROWS][EV] its unnormalised output
+
+    // ---- the work axis: row tile r of a sequence is tile r % tiles_per_head of head r / tiles_per_head
+    static constexpr int COST = 1;
+    struct Seq {
+        int L, T, q0, k0;
+        int per_head;   // row tiles of a head
+        int rts;
+        bool valid;
+    };
+    __device__ __forceinline__ Seq seq_work(int i) const {
+        Seq w;
+        w.q0 = __ldg(query_start + i);
+        w.T = __ldg(query_start + i + 1) - w.q0;
+        w.k0 = __ldg(kv_start + i);
+        w.L = __ldg(kv_start + i + 1) - w.k0;
+        w.valid = w.T <= w.L;
+        w.per_head = w.valid ? (w.T + EX_ROWS - 1) / EX_ROWS : 0;
+        w.rts = w.per_head * H;
+        return w;
+    }
+    // Tile j but a head's last sees ceil(past / 128) + 2 (j + 1) KV tiles.
+    __device__ __forceinline__ long long start(const Seq &w, int r) const {
+        if (w.per_head == 0) return 0;
+        const long long past = (w.L - w.T + EX_TOK - 1) / EX_TOK;
+        auto before = [&](long long j) { return j * (COST + past) + j * (j + 1); };
+        const int h = r / w.per_head, j = r - h * w.per_head;
+        return h * (before(w.per_head - 1) + COST + (w.L + EX_TOK - 1) / EX_TOK) + before(j);
+    }
+    // KV tiles of the first `rows` new tokens.
+    __device__ __forceinline__ int tiles_of(const Seq &w, int rows) const {
+        return (w.L - w.T + rows + EX_TOK - 1) / EX_TOK;
+    }
+    __device__ __forceinline__ int row_tiles(const Seq &w, int r) const {
+        return tiles_of(w, min(w.T, (r % w.per_head + 1) * EX_ROWS));
+    }
+    __device__ __forceinline__ bool starts_ok() const {
+        const bool q = offsets_ok(query_start, num_seqs, num_query_tokens);
+        return offsets_ok(kv_start, num_seqs, num_kv_tokens) && q;
+    }
 };
 
-template <int KV>
-__device__ __forceinline__ float to_float(uint16_t b) {
-    if constexpr (KV == PA_KV_F16)
-        return __half2float(__ushort_as_half(b));
-    else
-        return __uint_as_float((uint32_t)b << 16);
+// The halves of a piece: half 0 the later rows, which see the longer range,
+// half 1 the earlier ones (no tiles if the row tile has at most 128 rows, or if
+// the piece lies past what they see).
+struct Half {
+    int row0;     // first new token
+    int ntiles;   // KV tiles that its rows see
+    int n;        // KV tiles of the piece that it takes, from the piece's first on
+};
+
+__device__ __forceinline__ Half half_of(const ExpandedArgs &a, const Walk<ExpandedArgs> &p, int x) {
+    const int first = p.r % p.w.per_head * EX_ROWS;
+    const bool both = p.w.T - first > EX_HALF;
+    Half h;
+    h.row0 = first + (both && x == 0 ? EX_HALF : 0);
+    h.ntiles = x == 0 ? p.ntiles : both ? a.tiles_of(p.w, first + EX_HALF) : 0;
+    h.n = max(0, min(p.t1, h.ntiles) - p.t0);
+    return h;
 }
+
+constexpr int EX_THREADS = 12 * 32;
+constexpr int EX_BLOCK = EX_TOK * 128;               // 128 rows x 64 elements, 128-byte swizzle
+constexpr int EX_RING = 8;
+constexpr int EX_Q = 3 * EX_BLOCK;                   // one half's queries
+constexpr int EX_OFF_RING = 2 * EX_Q;
+constexpr int EX_OFF_CTRL = EX_OFF_RING + EX_RING * EX_BLOCK;
+constexpr int EX_CTRL = 1024;
+constexpr int EX_SMEM = EX_OFF_CTRL + EX_CTRL + 1024;   // + alignment slack
+static_assert(EX_SMEM <= 227 * 1024, "shared memory of one CTA");
+constexpr int EX_TMEM = 512, EX_O = 256;             // S0, S1 at columns 0 and 128; O0, O1 at 256 and 384
+constexpr int EX_REGS_LAUNCH = 168;                  // per thread at launch: 65536 / 384, rounded down to 8
+constexpr int EX_REGS_LOW = 104;                     // warpgroup 0
+constexpr int EX_REGS_HIGH = 200;                    // the softmax warpgroups
+static_assert(128 * EX_REGS_LOW + 256 * EX_REGS_HIGH <= EX_THREADS * EX_REGS_LAUNCH,
+              "register split within the launch's pool");
+
+struct ExCtrl {
+    uint64_t full[EX_RING], empty[EX_RING], qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2], done;
+    uint32_t tmem;
+    int abort;
+    Plan plan;
+    long long warp_sums[EX_THREADS / 32];
+};
+static_assert(sizeof(ExCtrl) <= EX_CTRL, "control block");
+
+// One lane: queries and ring blocks in the order the MMAs take them.
+__device__ void ex_load(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk<ExpandedArgs> &p, const CUtensorMap *tmq,
+                        const CUtensorMap *tmk, const CUtensorMap *tmr, const CUtensorMap *tmv) {
+    const uint32_t base = smem_u32(smem);
+    const uint64_t keep = policy_evict_normal();
+    volatile int *abort_flag = &c.abort;
+    int cnt = 0, qc[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        ok = ok && !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, a.wait_limit);
+        if (!ok) *abort_flag = 1;
+        return ok;
+    };
+    // a free ring slot's address and barrier
+    auto slot = [&](uint32_t &bar) {
+        const int s = cnt % EX_RING;
+        if (!wait(&c.empty[s], (uint32_t)(((cnt / EX_RING) & 1) ^ 1))) return 0u;
+        bar = smem_u32(&c.full[s]);
+        mbar_arrive_expect_tx(bar, EX_BLOCK);
+        ++cnt;
+        return base + EX_OFF_RING + s * EX_BLOCK;
+    };
+    while (ok && p.next()) {
+        const int head = p.r / p.w.per_head;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const Half h = half_of(a, p, x);
+            if (h.n == 0) continue;
+            if (!wait(&c.qempty[x], (uint32_t)((qc[x] & 1) ^ 1))) break;
+            const uint32_t bar = smem_u32(&c.qfull[x]);
+            mbar_arrive_expect_tx(bar, EX_Q);
+            for (int b = 0; b < 3; ++b)
+                tma_load_3d(base + x * EX_Q + b * EX_BLOCK, tmq, 64 * b, head, p.w.q0 + h.row0, bar, keep);
+            ++qc[x];
+        }
+        for (int t = p.t0; ok && t < p.t1; ++t) {
+            const int y = p.w.k0 + t * EX_TOK;
+            uint32_t bar, dst;
+            for (int b = 0; ok && b < 2; ++b)
+                if ((dst = slot(bar))) tma_load_3d(dst, tmk, 64 * b, head, y, bar, keep);
+            if (ok && (dst = slot(bar))) tma_load_2d(dst, tmr, 0, y, bar, keep);
+            for (int b = 0; ok && b < 2; ++b)
+                if ((dst = slot(bar))) tma_load_3d(dst, tmv, 64 * b, head, y, bar, keep);
+        }
+    }
+    // the last copies into every buffer have landed before the CTA leaves
+    for (int s = 0; s < EX_RING; ++s)
+        if (cnt > s)
+            mbar_wait_bounded(smem_u32(&c.full[s]), (uint32_t)(((cnt - 1 - s) / EX_RING) & 1), WAIT_LIMIT);
+    for (int x = 0; x < 2; ++x)
+        if (qc[x]) mbar_wait_bounded(smem_u32(&c.qfull[x]), (uint32_t)((qc[x] - 1) & 1), WAIT_LIMIT);
+}
+
+// One lane: the MMAs.
 template <int KV>
-__device__ __forceinline__ uint16_t to_bits(float x) {
-    if constexpr (KV == PA_KV_F16)
-        return __half_as_ushort(__float2half_rn(x));
-    else
-        return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+__device__ void ex_mma(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk<ExpandedArgs> &p, uint32_t tmem) {
+    const uint32_t base = smem_u32(smem);
+    constexpr uint32_t ID_S = idesc_f16(EX_HALF, EX_TOK, KV == PA_KV_BF16, false);
+    constexpr uint32_t ID_O = idesc_f16(EX_HALF, EV, KV == PA_KV_BF16, true);
+    constexpr uint32_t ID_O64 = idesc_f16(EX_HALF, EV / 2, KV == PA_KV_BF16, true);
+    const uint64_t dq0 = sw128_desc(base, 16, 1024);
+    const uint64_t dk0 = sw128_desc(base + EX_OFF_RING, 16, 1024);
+    const uint64_t dv0 = sw128_desc(base + EX_OFF_RING, EX_BLOCK, 1024);
+    volatile int *abort_flag = &c.abort;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        ok = ok && !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, a.wait_limit);
+        if (!ok) *abort_flag = 1;
+        return ok;
+    };
+    int cnt = 0, qc[2] = {0, 0}, pc[2] = {0, 0};   // ring blocks released; queries and P tiles taken
+    auto ring_wait = [&](int k) { return wait(&c.full[k % EX_RING], (uint32_t)((k / EX_RING) & 1)); };
+    // S_x = Q_x K^T, the key tile in ring blocks cnt .. cnt + 2 (waited for by half 0)
+    auto issue_s = [&](int x, int at, bool load) {
+        for (int b = 0; b < 3; ++b) {
+            if (load) {
+                if (!ring_wait(at + b)) return;
+                tc_fence_after_sync();
+            }
+            const uint64_t dk = dk0 + (uint64_t)((at + b) % EX_RING * (EX_BLOCK >> 4));
+            const uint64_t dq = dq0 + (uint64_t)((x * EX_Q + b * EX_BLOCK) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                umma_f16(tmem + x * EX_TOK, dq + 2 * k, dk + 2 * k, ID_S, b > 0 || k > 0 ? 1u : 0u);
+        }
+        umma_commit(smem_u32(&c.sfull[x]));
+    };
+    // O_x += P_x V, the value tile in ring blocks at and at + 1 (64 dims each), P_x
+    // over S_x: one product of N 128, or, where the ring wraps between the two
+    // (every eighth tile), two of N 64
+    auto issue_pv = [&](int x, int at, int n) {
+        const int b0 = at % EX_RING;
+        const uint64_t dv = dv0 + (uint64_t)(b0 * (EX_BLOCK >> 4));
+        const uint32_t o = tmem + EX_O + x * EV, pt = tmem + x * EX_TOK;
+        if (b0 + 1 < EX_RING) {
+#pragma unroll
+            for (int k = 0; k < EX_TOK / 16; ++k)   // 16 tokens: P columns 8 k .. 8 k + 7, V rows 16 k ..
+                umma_f16_ts(o, pt + 8 * k, dv + (uint64_t)((k * 16 * 128) >> 4), ID_O, n > 0 || k > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+            for (int k = 0; k < EX_TOK / 16; ++k) {
+                umma_f16_ts(o, pt + 8 * k, dv + (uint64_t)((k * 16 * 128) >> 4), ID_O64, n > 0 || k > 0 ? 1u : 0u);
+                umma_f16_ts(o + 64, pt + 8 * k, dv0 + (uint64_t)((k * 16 * 128) >> 4), ID_O64,
+                            n > 0 || k > 0 ? 1u : 0u);
+            }
+        }
+        umma_commit(smem_u32(&c.pvdone[x]));
+    };
+    while (ok && p.next()) {
+        const int n0 = half_of(a, p, 0).n, n1 = half_of(a, p, 1).n;
+        if (!wait(&c.qfull[0], (uint32_t)(qc[0]++ & 1))) break;
+        if (n1 > 0 && !wait(&c.qfull[1], (uint32_t)(qc[1]++ & 1))) break;
+        issue_s(0, cnt, true);
+        if (!ok) break;
+        if (n1 > 0) issue_s(1, cnt, false);
+        for (int b = 0; b < 3; ++b) umma_commit(smem_u32(&c.empty[(cnt + b) % EX_RING]));
+        cnt += 3;
+        for (int n = 0; n < n0; ++n) {   // ring: V(n), then K(n + 1)
+            if (n + 1 == n0) umma_commit(smem_u32(&c.qempty[0]));
+            if (n + 1 == n1) umma_commit(smem_u32(&c.qempty[1]));
+            const bool more0 = n + 1 < n0, more1 = n + 1 < n1;
+            if (!wait(&c.pfull[0], (uint32_t)(pc[0]++ & 1)) || !ring_wait(cnt) || !ring_wait(cnt + 1)) break;
+            tc_fence_after_sync();
+            issue_pv(0, cnt, n);
+            if (more0) issue_s(0, cnt + 2, true);
+            if (!ok) break;
+            if (n < n1) {
+                if (!wait(&c.pfull[1], (uint32_t)(pc[1]++ & 1))) break;
+                tc_fence_after_sync();
+                issue_pv(1, cnt, n);
+                if (more1) issue_s(1, cnt + 2, false);
+            }
+            const int used = more0 ? 5 : 2;
+            for (int b = 0; b < used; ++b) umma_commit(smem_u32(&c.empty[(cnt + b) % EX_RING]));
+            cnt += used;
+        }
+    }
+    // every product issued has completed before tensor memory is freed
+    umma_commit(smem_u32(&c.done));
+    mbar_wait_bounded(smem_u32(&c.done), 0, WAIT_LIMIT);
+}
+
+// One warpgroup: the softmax of half x, a row per thread.
+template <int KV>
+__device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk<ExpandedArgs> &p, uint32_t tmem, int x) {
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, m = quarter * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t scol = (uint32_t)(x * EX_TOK), ocol = (uint32_t)(EX_O + x * EV);
+    const float sl2 = a.scale_log2;
+    volatile int *abort_flag = &c.abort;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        const bool got = ok && !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, a.wait_limit);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) *abort_flag = 1;
+        return ok;
+    };
+    int sc = 0, cnt = 0;   // S_x and P_x so far; ring blocks before this piece
+    while (ok && p.next()) {
+        const Half h = half_of(a, p, x);
+        const int blocks = 5 * (p.t1 - p.t0);
+        if (h.n == 0) {
+            cnt += blocks;
+            continue;
+        }
+        const int tok = h.row0 + m;
+        const bool mine = tok < p.w.T;
+        const int vis = mine ? p.w.L - p.w.T + tok + 1 : p.w.L;   // positions this row sees
+        float mrun = -INFINITY, l = 0.f;
+        for (int n = 0; n < h.n && ok; ++n) {
+            if (!wait(&c.sfull[x], (uint32_t)(sc & 1))) break;
+            tc_fence_after_sync();
+            float s[EX_TOK];
+#pragma unroll
+            for (int q = 0; q < EX_TOK / 32; ++q) {
+                uint32_t r[32];
+                tmem_ld32(trow + scol + 32 * q, r);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) s[32 * q + k] = __uint_as_float(r[k]);
+            }
+            tmem_wait_ld();
+            const int t0 = (p.t0 + n) * EX_TOK;
+            if (t0 + EX_TOK > vis) {
+#pragma unroll
+                for (int k = 0; k < EX_TOK; ++k) s[k] = t0 + k < vis ? s[k] : -INFINITY;
+            }
+            float mp[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) mp[j] = s[j];
+#pragma unroll
+            for (int k = 8; k < EX_TOK; ++k) mp[k & 7] = fmaxf(mp[k & 7], s[k]);
+            const float mx = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                                   fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+            // decided per row, done warp-wide (tensor-memory accesses are the
+            // whole warp's); rows that do not grow scale by exactly 1
+            const bool grow = mx > mrun + RESCALE_THRESHOLD;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float nm = grow ? mx : mrun;
+                const float alpha = grow ? fast_exp2(mrun - nm) : 1.f;
+                if (n > 0) {   // PV_x(n - 1) is complete: S_x(n) was committed after it
+#pragma unroll 1
+                    for (int q = 0; q < EV / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(trow + ocol + 32 * q, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        tmem_st32(trow + ocol + 32 * q, o);
+                    }
+                    tmem_wait_st();
+                }
+                l *= alpha;
+                mrun = nm;
+            }
+            // value rows past the sequence are the next one's, or nothing: zeroed
+            // (P is 0 there); half 0 runs every KV tile, ahead of half 1
+            bool zeroed = false;
+            if (x == 0 && t0 + EX_TOK > p.w.L) {
+                const int at = cnt + 5 * n + 3;   // the value tile's ring blocks
+#pragma unroll 1
+                for (int b = 0; b < 2; ++b) {
+                    if (!wait(&c.full[(at + b) % EX_RING], (uint32_t)(((at + b) / EX_RING) & 1))) break;
+                    uint8_t *blk = smem + EX_OFF_RING + (at + b) % EX_RING * EX_BLOCK;
+                    for (int k = m + (p.w.L - t0) * 8; k < EX_TOK * 8; k += EX_HALF)
+                        *reinterpret_cast<uint4 *>(blk + 16 * k) = make_uint4(0, 0, 0, 0);
+                }
+                if (!ok) break;
+                zeroed = true;
+            }
+            const float mu = mrun == -INFINITY ? 0.f : mrun;   // a row that has seen nothing yet
+            float lp[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) lp[j] = 0.f;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t r[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float e0 = fast_exp2(fmaf(s[64 * q + 2 * k], sl2, -mu));
+                    const float e1 = fast_exp2(fmaf(s[64 * q + 2 * k + 1], sl2, -mu));
+                    lp[(2 * k) & 7] += e0;
+                    lp[(2 * k + 1) & 7] += e1;
+                    r[k] = pack_p<KV>(e0, e1);
+                }
+                tmem_st32(trow + scol + 32 * q, r);
+            }
+            l += ((lp[0] + lp[1]) + (lp[2] + lp[3])) + ((lp[4] + lp[5]) + (lp[6] + lp[7]));
+            tmem_wait_st();
+            if (zeroed) fence_proxy_async_smem();
+            tc_fence_before_sync();
+            mbar_arrive(smem_u32(&c.pfull[x]));
+            ++sc;
+        }
+        if (!ok || !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1))) break;
+        tc_fence_after_sync();
+        // ---- the piece's rows: finished, or a partial row
+        const bool whole = p.t0 == 0 && p.t1 >= h.ntiles;
+        const int slot_row = p.slot() * EX_ROWS + h.row0 % EX_ROWS + m;
+        if (!whole && mine) a.ml[slot_row] = make_float2(mrun, l);
+        const float inv = 1.f / l;
+        uint16_t *orow = a.out + ((long long)(p.w.q0 + tok) * a.H + p.r / p.w.per_head) * EV;
+        float *part = a.o + (long long)slot_row * EV;
+#pragma unroll 1
+        for (int q = 0; q < EV / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(trow + ocol + 32 * q, o);
+            tmem_wait_ld();
+            if (mine && whole) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = (uint32_t)out_bits<KV>(__uint_as_float(o[k + 2 * i]) * inv) |
+                               ((uint32_t)out_bits<KV>(__uint_as_float(o[k + 2 * i + 1]) * inv) << 16);
+                    *reinterpret_cast<uint4 *>(orow + 32 * q + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else if (mine) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<uint4 *>(part + 32 * q + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
+            __syncwarp();   // the next load is the whole warp's
+        }
+        tc_fence_before_sync();
+        cnt += blocks;
+    }
 }
 
 template <int KV>
-__global__ void __launch_bounds__(256) expanded_simple_kernel(const ExpandedArgs a) {
-    const int h = blockIdx.x % a.H, qt = blockIdx.x / a.H;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->error = 0;
-    __shared__ float sm[8], sl[8], so[8][EV];
-    bool order = a.query_start[0] == 0 && a.query_start[a.num_seqs] == a.num_query_tokens && a.kv_start[0] == 0 &&
-                 a.kv_start[a.num_seqs] == a.num_kv_tokens;
-    for (int i = threadIdx.x; i < a.num_seqs; i += blockDim.x)
-        if (a.query_start[i] > a.query_start[i + 1] || a.kv_start[i] > a.kv_start[i + 1]) order = false;
-    bool bad = !__syncthreads_and(order);
-    int lo = 0, hi = a.num_seqs;
-    while (!bad && hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.query_start[mid] <= qt) lo = mid; else hi = mid;
+__global__ void __launch_bounds__(EX_THREADS, 1)
+    expanded_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                    const __grid_constant__ CUtensorMap tmr, const __grid_constant__ CUtensorMap tmv,
+                    const ExpandedArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    ExCtrl &c = *reinterpret_cast<ExCtrl *>(smem + EX_OFF_CTRL);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < EX_RING; ++s) {
+            mbar_init(smem_u32(&c.full[s]), 1);
+            mbar_init(smem_u32(&c.empty[s]), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&c.qfull[x]), 1);
+            mbar_init(smem_u32(&c.qempty[x]), 1);
+            mbar_init(smem_u32(&c.sfull[x]), 1);
+            mbar_init(smem_u32(&c.pfull[x]), EX_HALF);
+            mbar_init(smem_u32(&c.pvdone[x]), 1);
+        }
+        mbar_init(smem_u32(&c.done), 1);
+        c.abort = 0;
+        fence_mbar_init();
     }
-    int vis = 0;
-    long long k0 = 0;
-    if (!bad) {
-        const int T = a.query_start[lo + 1] - a.query_start[lo];
-        const int L = a.kv_start[lo + 1] - a.kv_start[lo];
-        k0 = a.kv_start[lo];
-        bad = T > L;
-        vis = L - T + (qt - a.query_start[lo]) + 1;
+    make_plan(a, &c.plan, c.warp_sums);
+    const Plan plan = c.plan;
+    if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
+        if (warp == 2) {
+            tmem_alloc(smem_u32(&c.tmem), EX_TMEM);
+            tmem_relinquish();
+        }
+        tc_fence_before_sync();
+        __syncthreads();
+        tc_fence_after_sync();
+        const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
+        Walk<ExpandedArgs> p(a, plan);
+        if (warp >= 4) {
+            regs_increase<EX_REGS_HIGH>();
+            ex_softmax<KV>(smem, c, a, p, tmem, (warp - 4) >> 2);
+        } else {
+            regs_decrease<EX_REGS_LOW>();
+            if ((threadIdx.x & 31) == 0) {
+                if (warp == 0) ex_load(smem, c, a, p, &tmq, &tmk, &tmr, &tmv);
+                if (warp == 2) ex_mma<KV>(smem, c, a, p, tmem);
+            }
+            __syncwarp();
+        }
+        tc_fence_before_sync();
+        __syncthreads();
+        if (warp == 2) {
+            tc_fence_after_sync();
+            tmem_dealloc(tmem, EX_TMEM);
+        }
     }
-    const uint16_t *qr = a.query + (long long)blockIdx.x * EQ;
-    float q[6], o[4], m = -INFINITY, l = 0.f;
-    for (int k = 0; k < 6; ++k) q[k] = to_float<KV>(qr[32 * k + lane]);
-    for (int k = 0; k < 4; ++k) o[k] = 0.f;
-    for (int t = warp; !bad && t < vis; t += 8) {
-        const uint16_t *kn = a.k_nope + (k0 + t) * a.kt + h * a.kh, *kr = a.k_rope + (k0 + t) * a.rt;
-        const uint16_t *vr = a.value + (k0 + t) * a.vt + h * a.vh;
-        float s = 0.f;
-        for (int k = 0; k < 4; ++k) s = fmaf(q[k], to_float<KV>(kn[32 * k + lane]), s);
-        for (int k = 0; k < 2; ++k) s = fmaf(q[4 + k], to_float<KV>(kr[32 * k + lane]), s);
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= a.scale_log2;
-        const float nm = fmaxf(m, s), al = fast_exp2(m - nm), p = s != s ? s : fast_exp2(s - nm);
-        l = l * al + p;
-        for (int k = 0; k < 4; ++k) o[k] = o[k] * al + p * to_float<KV>(vr[32 * k + lane]);
-        m = nm;
+    if (threadIdx.x == 0) a.status[blockIdx.x] = c.abort;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// One warp per output row: rows of a cut row tile from their pieces' partial
+// rows, NaN for a sequence with more new tokens than keys (and for every row
+// when a CTA of the first kernel gave up).
+template <int KV>
+__global__ void __launch_bounds__(256) expanded_merge_kernel(const ExpandedArgs a, int ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int failed = 0;
+    for (int i = threadIdx.x; i < ctas; i += blockDim.x) failed |= a.status[i];
+    failed = __syncthreads_or(failed);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
+    const int lane = threadIdx.x & 31;
+    const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5);
+    if (row >= (long long)a.num_query_tokens * a.H) return;
+    const int qt = (int)(row / a.H), head = (int)(row - (long long)qt * a.H);
+    const long long total = a.unit_base[a.num_seqs];
+    uint2 *out = reinterpret_cast<uint2 *>(a.out + row * EV) + lane;
+    const int seq = total >= 0 ? sequence_of(a.query_start, a.num_seqs, qt) : 0;
+    ExpandedArgs::Seq w{};
+    if (total >= 0) w = a.seq_work(seq);
+    if (failed || total < 0 || !w.valid) {
+        const uint32_t x = (uint32_t)out_bits<KV>(__int_as_float(0x7fc00000)) * 0x10001u;
+        *out = make_uint2(x, x);
+        return;
     }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-    for (int k = 0; k < 4; ++k) so[warp][32 * k + lane] = o[k];
-    __syncthreads();
-    float M = -INFINITY, den = 0.f;
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w]);
-    for (int w = 0; w < 8; ++w)
-        if (sl[w] != 0.f) den += sl[w] * fast_exp2(sm[w] - M);
-    for (int d = threadIdx.x; d < EV; d += 256) {
-        float v = 0.f;
-        for (int w = 0; w < 8; ++w)
-            if (sl[w] != 0.f) v += so[w][d] * fast_exp2(sm[w] - M);
-        a.out[(long long)blockIdx.x * EV + d] = to_bits<KV>(bad ? __int_as_float(0x7fc00000) : v / den);
+    const int tok = qt - w.q0, j = tok / EX_ROWS, m = tok % EX_ROWS;
+    // what the row's half sees: the first half of a full row tile, or its last rows
+    const int rows = m < EX_HALF && w.T - j * EX_ROWS > EX_HALF ? j * EX_ROWS + EX_HALF : min(w.T, (j + 1) * EX_ROWS);
+    const Pieces pc(a.unit_base[seq] + a.start(w, head * w.per_head + j), a.tiles_of(w, rows), ExpandedArgs::COST, total,
+                    ctas);
+    if (pc.k0 == pc.k1) return;   // finished by one CTA
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int k = pc.k0; k <= pc.k1; ++k) M = fmaxf(M, a.ml[pc.slot(k) * EX_ROWS + m].x);
+    const float mu = M == -INFINITY ? 0.f : M;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 8
+    for (int k = pc.k0; k <= pc.k1; ++k) {
+        const int at = pc.slot(k) * EX_ROWS + m;
+        const float2 ml = a.ml[at];
+        const float4 o = *reinterpret_cast<const float4 *>(a.o + (long long)at * EV + 4 * lane);
+        const float wt = fast_exp2(ml.x - mu);
+        l = fmaf(ml.y, wt, l);
+        acc.x = fmaf(o.x, wt, acc.x);
+        acc.y = fmaf(o.y, wt, acc.y);
+        acc.z = fmaf(o.z, wt, acc.z);
+        acc.w = fmaf(o.w, wt, acc.w);
     }
+    const float inv = 1.f / l;
+    *out = make_uint2((uint32_t)out_bits<KV>(acc.x * inv) | ((uint32_t)out_bits<KV>(acc.y * inv) << 16),
+                      (uint32_t)out_bits<KV>(acc.z * inv) | ((uint32_t)out_bits<KV>(acc.w * inv) << 16));
+}
+
+// ------------------------------------------------------------------ launch
+
+struct ExLayout {
+    size_t status, unit_base, ml, o, total;
+};
+
+ExLayout ex_layout(int num_seqs) {
+    ExLayout l;
+    size_t at = 256;   // header
+    auto take = [&](size_t bytes) {
+        const size_t p = at;
+        at = (at + bytes + 255) / 256 * 256;
+        return p;
+    };
+    l.status = take(sizeof(int) * AXIS_MAX_CTAS);
+    l.unit_base = take(sizeof(long long) * ((size_t)num_seqs + 1));
+    l.ml = take(sizeof(float2) * 2 * AXIS_MAX_CTAS * EX_ROWS);
+    l.o = take(sizeof(float) * 2 * AXIS_MAX_CTAS * EX_ROWS * EV);
+    l.total = at;
+    return l;
+}
+
+// [rows][heads][width] 16-bit elements with the given strides, boxes of 64
+// elements of one head over 128 rows; heads = 0: [rows][width].
+bool heads_map(CUtensorMap *map, const void *base, int width, int heads, long long rows, long long head_stride,
+               long long row_stride, int dtype) {
+    auto enc = tma_encoder();
+    if (!enc) return false;
+    const int rank = heads ? 3 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)(heads ? heads : rows), (cuuint64_t)rows};
+    cuuint64_t strides[2] = {2 * (cuuint64_t)(heads ? head_stride : row_stride), 2 * (cuuint64_t)row_stride};
+    cuuint32_t box[3] = {64, heads ? 1u : (cuuint32_t)EX_TOK, EX_TOK};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, dtype == PA_KV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+               (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared-memory limits are set per device, on its first call; the kernel runs
+// only if it was built with the registers that its split assumes (with another
+// count the softmax warpgroups' increase could wait forever).
+template <int KV>
+int ex_setup() {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && done[dev]) return PA_OK;
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(expanded_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, EX_SMEM) !=
+            cudaSuccess ||
+        cudaFuncGetAttributes(&fa, expanded_kernel<KV>) != cudaSuccess)
+        return PA_ERR_CUDA;
+    if (fa.numRegs != EX_REGS_LAUNCH) return PA_ERR_UNSUPPORTED;
+    if (dev < 64) done[dev] = true;
+    return PA_OK;
+}
+
+template <int KV>
+int launch_expanded(const ExpandedArgs &a, const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmr,
+                    const CUtensorMap &tmv, cudaStream_t st) {
+    if (const int e = ex_setup<KV>()) return e;
+    const int ctas = std::min(num_sms(), AXIS_MAX_CTAS);
+    expanded_kernel<KV><<<ctas, EX_THREADS, EX_SMEM, st>>>(tmq, tmk, tmr, tmv, a);
+    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(((long long)a.num_query_tokens * a.H + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // launched while the first kernel drains
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, expanded_merge_kernel<KV>, a, ctas));
 }
 
 }  // namespace
@@ -98,7 +620,7 @@ using namespace pa;
 
 extern "C" size_t pa_latent_attention_expanded_workspace_size(int num_seqs, int num_query_tokens, int num_heads) {
     if (num_seqs < 0 || num_query_tokens < 0 || num_heads <= 0) return 0;
-    return 4096;
+    return ex_layout(num_seqs).total;
 }
 
 extern "C" int pa_latent_attention_expanded(void *out, const void *query, const void *k_nope, const void *k_rope,
@@ -112,6 +634,7 @@ extern "C" int pa_latent_attention_expanded(void *out, const void *query, const 
         k_head_stride < EN || v_head_stride < EV || rope_stride < ER || k_token_stride < EN || v_token_stride < EV ||
         (k_token_stride | k_head_stride | rope_stride | v_token_stride | v_head_stride) % 8 != 0)
         return PA_ERR_INVALID_ARG;
+    if ((long long)num_query_tokens * num_heads >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
     if (num_query_tokens == 0) return PA_OK;
     if (!out || !query || !query_start || !kv_start || !aligned16(out) || !aligned16(query) ||
         (num_kv_tokens > 0 && (!k_nope || !k_rope || !value)) || !aligned16(k_nope) || !aligned16(k_rope) ||
@@ -120,14 +643,33 @@ extern "C" int pa_latent_attention_expanded(void *out, const void *query, const 
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
         workspace_bytes < pa_latent_attention_expanded_workspace_size(num_seqs, num_query_tokens, num_heads))
         return PA_ERR_WORKSPACE;
-    ExpandedArgs a{static_cast<uint16_t *>(out), static_cast<const uint16_t *>(query),
-                   static_cast<const uint16_t *>(k_nope), static_cast<const uint16_t *>(k_rope),
-                   static_cast<const uint16_t *>(value), query_start, kv_start, static_cast<WsHeader *>(workspace),
-                   num_seqs, num_query_tokens, num_kv_tokens, num_heads, k_token_stride, k_head_stride, rope_stride,
-                   v_token_stride, v_head_stride, scale * 1.4426950408889634f};
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const ExLayout lay = ex_layout(num_seqs);
+    ExpandedArgs a{};
+    a.out = static_cast<uint16_t *>(out);
+    a.query_start = query_start;
+    a.kv_start = kv_start;
+    a.hdr = reinterpret_cast<WsHeader *>(ws);
+    a.num_seqs = num_seqs;
+    a.num_query_tokens = num_query_tokens;
+    a.num_kv_tokens = num_kv_tokens;
+    a.H = num_heads;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.wait_limit = pipeline_wait_limit();
+    a.status = reinterpret_cast<int *>(ws + lay.status);
+    a.unit_base = reinterpret_cast<long long *>(ws + lay.unit_base);
+    a.ml = reinterpret_cast<float2 *>(ws + lay.ml);
+    a.o = reinterpret_cast<float *>(ws + lay.o);
+    // without keys no row tile has work and no copy is made: any base will do
+    const bool none = num_kv_tokens == 0;
+    const long long nk = none ? 1 : num_kv_tokens;
+    CUtensorMap tmq, tmk, tmr, tmv;
+    if (!heads_map(&tmq, query, EQ, num_heads, num_query_tokens, EQ, (long long)EQ * num_heads, dtype) ||
+        !heads_map(&tmk, none ? query : k_nope, EN, num_heads, nk, k_head_stride, k_token_stride, dtype) ||
+        !heads_map(&tmr, none ? query : k_rope, ER, 0, nk, 0, rope_stride, dtype) ||
+        !heads_map(&tmv, none ? query : value, EV, num_heads, nk, v_head_stride, v_token_stride, dtype))
+        return PA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)num_query_tokens * num_heads;
-    if (dtype == PA_KV_F16) expanded_simple_kernel<PA_KV_F16><<<grid, 256, 0, st>>>(a);
-    else expanded_simple_kernel<PA_KV_BF16><<<grid, 256, 0, st>>>(a);
-    return cuda_status(cudaGetLastError());
+    return dtype == PA_KV_F16 ? launch_expanded<PA_KV_F16>(a, tmq, tmk, tmr, tmv, st)
+                              : launch_expanded<PA_KV_BF16>(a, tmq, tmk, tmr, tmv, st);
 }

@@ -1,0 +1,185 @@
+// Work shared out evenly over the CTAs of one launch, without a plan made on
+// the host or in a launch of its own.
+//
+// The work of an attention call is a list of row tiles (some query rows of one
+// sequence and the KV tiles that they see).  Laid end to end they make one axis
+// of work units, a unit being a KV tile; each row tile has COST units more for
+// its start and its end.  The axis is cut into equal ranges, one per CTA, and a
+// CTA takes the pieces of row tiles inside its range.  A row tile that lies in
+// one range is finished there; the pieces of a cut one leave partial rows (at
+// most two pieces a CTA: one continued from the left, one to the right), which
+// a second kernel merges.  Every CTA derives the cut by itself from the lengths,
+// by one sum over the sequences.
+//
+// A problem P gives
+//   P::COST                 units of a row tile besides its KV tiles
+//   P::Seq, seq_work(i)     what is needed of sequence i; Seq::rts row tiles
+//   start(w, r)             first unit of row tile r within its sequence;
+//                           start(w, w.rts) = the sequence's units
+//   row_tiles(w, r)         KV tiles of row tile r
+//   starts_ok()             whether the row offsets are in order (called by
+//                           every thread of the block)
+//   num_seqs, unit_base     sequences; [num_seqs + 1] their first units, written
+//                           by CTA 0 for the merge (-1: offsets out of order)
+#pragma once
+
+#include <stdint.h>
+
+namespace pa {
+namespace {
+
+constexpr int AXIS_MAX_CTAS = 160;   // CTAs of a launch: one per SM, at most this many
+
+struct Plan {
+    long long u0, u1, base;   // this CTA's range; first unit of sequence seq
+    int seq;                  // the sequence in which the range begins
+};
+
+// First unit of CTA k's range; `parts` = min(CTAs, total) CTAs have one, of at
+// least a unit each.
+__device__ __forceinline__ long long range_begin(long long total, int k, int parts) { return total * k / parts; }
+
+// Whether the n + 1 device offsets are a non-decreasing cover of [0, end):
+// every thread of the block calls it and gets the answer.
+__device__ __forceinline__ bool offsets_ok(const int32_t *start, int n, int end) {
+    bool ok = start[0] == 0 && start[n] == end;
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (start[i] > start[i + 1]) ok = false;
+    return __syncthreads_and(ok);
+}
+
+// The last of n sequences that starts at or before row `row`.
+__device__ __forceinline__ int sequence_of(const int32_t *start, int n, int row) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= row) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// This block's plan (warp_sums: one number per warp, in shared memory).
+template <class P>
+__device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *warp_sums) {
+    const bool ok = a.starts_ok();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    const int per = (a.num_seqs + blockDim.x - 1) / blockDim.x;
+    const int i0 = min(a.num_seqs, (int)threadIdx.x * per), i1 = min(a.num_seqs, i0 + per);
+    auto units = [&](int i) {
+        const typename P::Seq w = a.seq_work(i);
+        return a.start(w, w.rts);
+    };
+    long long mine = 0;
+    for (int i = i0; ok && i < i1; ++i) mine += units(i);
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += x;
+    }
+    if (lane == 31) warp_sums[warp] = upto;
+    if (threadIdx.x == 0) plan->seq = a.num_seqs;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int k = 0; k < nwarps; ++k) {
+        if (k < warp) before += warp_sums[k];
+        total += warp_sums[k];
+    }
+    const long long begin = before + upto - mine, end = before + upto;
+    const int parts = (int)min((long long)gridDim.x, total), cta = blockIdx.x;
+    const long long u0 = cta < parts ? range_begin(total, cta, parts) : 0;
+    const long long u1 = cta < parts ? range_begin(total, cta + 1, parts) : 0;
+    if (threadIdx.x == 0) {
+        plan->u0 = u0;
+        plan->u1 = u1;
+    }
+    if (u0 < u1 && begin <= u0 && u0 < end) {   // one thread
+        long long s = begin;
+        int i = i0;
+        for (;; ++i) {
+            const long long n = units(i);
+            if (u0 < s + n) break;
+            s += n;
+        }
+        plan->seq = i;
+        plan->base = s;
+    }
+    if (cta == 0) {
+        long long s = begin;
+        for (int i = i0; i < i1; ++i) {
+            a.unit_base[i] = ok ? s : -1;
+            if (ok) s += units(i);
+        }
+        if (threadIdx.x == 0) a.unit_base[a.num_seqs] = ok ? total : -1;
+    }
+    __syncthreads();
+}
+
+// Walks the pieces of a CTA's range, in every role alike.
+template <class P>
+struct Walk {
+    const P &a;
+    long long u0, u1, base, s;   // the range; first unit of the sequence, and of row tile r
+    int seq, r;
+    typename P::Seq w;
+    int t0, t1, ntiles, local;   // the piece: KV tiles [t0, t1) of ntiles; its number in this CTA
+
+    __device__ Walk(const P &args, const Plan &p) : a(args), u0(p.u0), u1(p.u1), base(p.base), seq(p.seq), r(0) {
+        local = -1;
+        if (u0 >= u1) return;
+        w = a.seq_work(seq);
+        int hi = w.rts;   // the last row tile that starts at or before u0
+        while (hi - r > 1) {
+            const int mid = (r + hi) >> 1;
+            if (base + a.start(w, mid) <= u0) r = mid; else hi = mid;
+        }
+        --r;
+    }
+    // The next piece; false at the end of the range.
+    __device__ bool next() {
+        if (u0 >= u1) return false;
+        for (;;) {
+            ++r;
+            while (r >= w.rts) {   // on to the next sequence
+                base += a.start(w, w.rts);
+                if (base >= u1 || ++seq >= a.num_seqs) return false;
+                w = a.seq_work(seq);
+                r = 0;
+            }
+            s = base + a.start(w, r);
+            if (s >= u1) return false;
+            ntiles = a.row_tiles(w, r);
+            t0 = (int)max(0LL, min((long long)ntiles, u0 - s - P::COST));
+            t1 = (int)max(0LL, min((long long)ntiles, u1 - s - P::COST));
+            if (t1 > t0) {
+                ++local;
+                return true;
+            }
+        }
+    }
+    __device__ bool whole() const { return t0 == 0 && t1 == ntiles; }
+    // slot of this piece's partial rows: 0 if the row tile began before the range
+    __device__ int slot() const { return 2 * (int)blockIdx.x + (s < u0 ? 0 : 1); }
+};
+
+// The CTAs k0 .. k1 that hold the pieces of the row tile of `ntiles` KV tiles
+// at unit s, and the slot of each one's partial rows.
+struct Pieces {
+    int k0, k1, parts;
+    long long s, total;
+    __device__ Pieces(long long s_, int ntiles, int cost, long long total_, int ctas) : s(s_), total(total_) {
+        parts = (int)min((long long)ctas, total);
+        k0 = cta_of(s + cost);
+        k1 = cta_of(s + cost + ntiles - 1);
+    }
+    __device__ int cta_of(long long u) const {
+        int k = (int)(u * parts / total);
+        while (range_begin(total, k + 1, parts) <= u) ++k;
+        while (range_begin(total, k, parts) > u) --k;
+        return k;
+    }
+    __device__ int slot(int k) const { return 2 * k + (s < range_begin(total, k, parts) ? 0 : 1); }
+};
+
+}  // namespace
+}  // namespace pa
