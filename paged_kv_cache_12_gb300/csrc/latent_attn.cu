@@ -11,8 +11,9 @@ namespace pa {
 namespace {
 
 constexpr int LT_ROWS = 64;   // query rows of a row tile (new token x head, token-major)
-constexpr int LT_TOK = 64;    // tokens of a KV tile
 
+// TOK: tokens of a KV tile.
+template <int TOK>
 struct LatentArgs {
     uint16_t *out;
     const uint16_t *query;
@@ -44,7 +45,7 @@ struct LatentArgs {
         w.T = query_start ? __ldg(query_start + i + 1) - w.q0 : 1;
         w.valid = w.L >= 0 && w.L <= max_context_len && (long long)w.L <= (long long)mbps * bs &&
                   !(query_start && w.T > w.L);
-        w.tiles = w.valid && w.T > 0 ? (w.L + LT_TOK - 1) / LT_TOK : 0;
+        w.tiles = w.valid && w.T > 0 ? (w.L + TOK - 1) / TOK : 0;
         w.rts = w.tiles ? (int)(((long long)w.T * H + LT_ROWS - 1) / LT_ROWS) : 0;
         return w;
     }
@@ -55,7 +56,7 @@ struct LatentArgs {
     // KV tiles that row tile r sees: up to its last row's own position.
     __device__ __forceinline__ int row_tiles(const Seq &w, int r) const {
         const long long last = min((long long)w.T * H, (long long)(r + 1) * LT_ROWS) - 1;
-        return (w.L - w.T + (int)(last / H) + 1 + LT_TOK - 1) / LT_TOK;
+        return (w.L - w.T + (int)(last / H) + 1 + TOK - 1) / TOK;
     }
     __device__ __forceinline__ bool starts_ok() const {
         return !query_start || offsets_ok(query_start, num_seqs, num_query_tokens);
@@ -70,13 +71,6 @@ struct LatentArgs {
 };
 
 template <int KV>
-__device__ __forceinline__ float to_float(uint16_t b) {
-    if constexpr (KV == PA_KV_F16)
-        return __half2float(__ushort_as_half(b));
-    else
-        return __uint_as_float((uint32_t)b << 16);
-}
-template <int KV>
 __device__ __forceinline__ uint16_t to_bits(float x) {
     if constexpr (KV == PA_KV_F16)
         return __half_as_ushort(__float2half_rn(x));
@@ -84,50 +78,408 @@ __device__ __forceinline__ uint16_t to_bits(float x) {
         return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// ------------------------------------------------------------------ 16-bit kernel
+// ------------------------------------------------------------------ the kernel
 
-constexpr int LT_THREADS = 256;
 constexpr int LT_GROUP = 9 * 1024;            // 8 rows of 576 elements: nine 128-byte-swizzled blocks of 64 columns
-constexpr int LT_STAGES = 2;
-constexpr int LT_STAGE = LT_TOK / 8 * LT_GROUP;
-constexpr int LT_OFF_Q = 0;
-constexpr int LT_OFF_KV = LT_ROWS / 8 * LT_GROUP;
-constexpr int LT_OFF_P = LT_OFF_KV + LT_STAGES * LT_STAGE;
-constexpr int LT_OFF_CTRL = LT_OFF_P + LT_ROWS * LT_TOK * 2;
+constexpr int LT_Q = LT_ROWS / 8 * LT_GROUP;
+constexpr int LT_P = LT_ROWS * 128;
 constexpr int LT_CTRL = 1024;
-constexpr int LT_SMEM = LT_OFF_CTRL + LT_CTRL + 1024;   // + alignment slack
-static_assert(LT_SMEM <= 227 * 1024, "shared memory of one CTA");
 constexpr int LT_TMEM = 512;                  // columns: O (256), S0, S1 (64 each)
 constexpr int LT_S = 256;
 constexpr uint32_t LT_HI = 16u << 16;         // lanes 16 .. 31 of each quarter: output dims 256 .. 511
 constexpr int LT_BAD_SLOTS = 16;
+constexpr int L8_STEP = 16;                   // tokens of a staging slot of codes
+constexpr int L8_SLOTS = 4;
+constexpr int L8_SLOT = L8_STEP * (LC + 16);  // their codes, then their scales
+constexpr int L8_WARPS = 8;                   // converting warps
+
+// What differs between a 16-bit and an E4M3 cache.
+template <int KV>
+struct Lt {
+    static constexpr bool F8 = KV == PA_KV_FP8_E4M3;
+    static constexpr int TOK = F8 ? 48 : 64;
+    static constexpr int THREADS = F8 ? 256 + 32 * L8_WARPS : 256;
+    static constexpr int STAGE = TOK / 8 * LT_GROUP;
+    static constexpr int OFF_KV = LT_Q;
+    static constexpr int OFF_P = OFF_KV + 2 * STAGE;
+    static constexpr int OFF_8 = OFF_P + LT_P;
+    static constexpr int OFF_CTRL = OFF_8 + (F8 ? L8_SLOTS * L8_SLOT : 0);
+    static constexpr int SMEM = OFF_CTRL + LT_CTRL + 1024;   // + alignment slack
+    static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+    static_assert(TOK % L8_STEP == 0 && OFF_8 % 1024 == 0, "layout");
+    using Args = LatentArgs<TOK>;
+};
 
 struct LtCtrl {
     uint64_t kvfull[2], kvempty[2], sfull[2], sfree[2], pfull, pvdone, qfull, qempty, done;
+    uint64_t full8[L8_SLOTS], empty8[L8_SLOTS];
     uint32_t tmem;
     int abort;
     int bad[LT_BAD_SLOTS];   // 1 + the number of a piece that met a block id out of range
     Plan plan;
-    long long warp_sums[LT_THREADS / 32];
+    long long warp_sums[16];
 };
 static_assert(sizeof(LtCtrl) <= LT_CTRL, "control block");
 
+// Tensor maps: the cache's rows (16-bit), or a quantised cache's codes, rotary
+// elements and scales; the query's rows.
+struct LtMaps {
+    CUtensorMap kv, rope, scale, q;
+};
+
+// A role's bounded wait, the outcome shared by the warp (or one lane's own).
+struct Waiter {
+    volatile int *abort_flag;
+    long long limit;
+    bool ok = true;
+    __device__ __forceinline__ bool warp(const uint64_t &bar, int parity) {
+        const bool got = ok && !*abort_flag && mbar_wait_bounded(smem_u32(&bar), (uint32_t)(parity & 1), limit);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) *abort_flag = 1;
+        return ok;
+    }
+    __device__ __forceinline__ bool lane(const uint64_t &bar, int parity) {
+        ok = ok && !*abort_flag && mbar_wait_bounded(smem_u32(&bar), (uint32_t)(parity & 1), limit);
+        if (!ok) *abort_flag = 1;
+        return ok;
+    }
+};
+
+// The producer warp: lane j copies tokens 8 j .. 8 j + 7 of a tile, lanes 8 ..
+// 15 the query rows.  A quantised tile goes in steps of 16 tokens: codes and
+// scales into the staging ring, rotary elements straight into the 16-bit stage
+// (which the step waits for as well; the converting warps need it free anyway).
 template <int KV>
-__global__ void __launch_bounds__(LT_THREADS, 1) latent_kernel(const __grid_constant__ CUtensorMap tmkv,
-                                                              const __grid_constant__ CUtensorMap tmq,
-                                                              const LatentArgs a) {
+__device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p,
+                        const LtMaps &maps) {
+    using L = Lt<KV>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_u32(smem);
+    const uint64_t first = policy_evict_first(), keep = policy_evict_normal();
+    Waiter w{&c.abort, a.wait_limit};
+    int cnt = 0, steps = 0, pieces = 0;
+    while (w.ok && p.next()) {
+        const int32_t *row = a.block_tables + (long long)p.seq * a.mbps;
+        if (!w.warp(c.qempty, pieces + 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.qfull), LT_Q);
+        __syncwarp();
+        if (lane >= 8 && lane < 16)
+            tma_load_3d(base + (lane - 8) * LT_GROUP, &maps.q, 0, (int)a.first_row(p.w, p.r) + 8 * (lane - 8), 0,
+                        smem_u32(&c.qfull), keep);
+        ++pieces;
+        for (int t = p.t0; t < p.t1 && w.ok; ++t, ++cnt) {
+            const int tok = t * L::TOK + 8 * lane, st = cnt & 1;
+            const bool mine = lane < L::TOK / 8 && tok < p.w.L;
+            const int32_t blk = mine ? __ldg(row + tok / a.bs) : 0;
+            const bool bad = __any_sync(0xffffffffu, mine && (blk < 0 || blk >= a.num_blocks));
+            const unsigned boxes = __ballot_sync(0xffffffffu, mine && !bad);
+            const int y = (int)((long long)blk * a.bs) + tok % a.bs;
+            const uint32_t dst = base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP;
+            if (bad && lane == 0) *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) = p.local + 1;
+            if constexpr (L::F8) {
+                for (int k = 0; k < L::TOK / L8_STEP; ++k, ++steps) {
+                    const int s = steps % L8_SLOTS, j = lane - 2 * k;   // groups 2 k and 2 k + 1 of the tile
+                    if (!w.warp(c.empty8[s], steps / L8_SLOTS + 1)) break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(smem_u32(&c.full8[s]), (uint32_t)(__popc(boxes >> (2 * k) & 3u) * 8 * (LC + 16)));
+                    __syncwarp();
+                    if ((j == 0 || j == 1) && (boxes >> lane & 1u)) {
+                        const uint32_t d8 = base + L::OFF_8 + s * L8_SLOT;
+                        tma_load_2d(d8 + j * 8 * LC, &maps.kv, 0, y, smem_u32(&c.full8[s]), first);
+                        tma_load_2d(d8 + j * 8 * LC + 8 * 256, &maps.kv, 256, y, smem_u32(&c.full8[s]), first);
+                        tma_load_2d(d8 + L8_STEP * LC + j * 128, &maps.scale, 0, y, smem_u32(&c.full8[s]), first);
+                    }
+                    __syncwarp();
+                }
+                if (!w.ok || !w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]), (uint32_t)(__popc(boxes) * 1024));
+                __syncwarp();
+                if (boxes >> lane & 1u) tma_load_2d(dst + 8192, &maps.rope, 0, y, smem_u32(&c.kvfull[st]), first);
+            } else {
+                if (!w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
+                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]), (uint32_t)(__popc(boxes) * LT_GROUP));
+                __syncwarp();
+                if (boxes >> lane & 1u) tma_load_3d(dst, &maps.kv, 0, y, 0, smem_u32(&c.kvfull[st]), first);
+            }
+            __syncwarp();
+        }
+    }
+    // the last copies into every buffer have landed before the CTA leaves (a
+    // stage of a quantised tile also waits for its converting warps, which may
+    // have given up: its copies are then waited for until the limit)
+    for (int s = 0; s < 2; ++s)
+        if (cnt > s) mbar_wait_bounded(smem_u32(&c.kvfull[s]), (uint32_t)(((cnt - 1 - s) / 2) & 1), WAIT_LIMIT);
+    if constexpr (L::F8)
+        for (int s = 0; s < L8_SLOTS; ++s)
+            if (steps > s)
+                mbar_wait_bounded(smem_u32(&c.full8[s]), (uint32_t)(((steps - 1 - s) / L8_SLOTS) & 1), WAIT_LIMIT);
+    if (pieces) mbar_wait_bounded(smem_u32(&c.qfull), (uint32_t)((pieces - 1) & 1), WAIT_LIMIT);
+}
+
+// A converting warp: rows w and w + 8 of every step of 16 tokens, codes times
+// their group's scale as bf16 in the layout a 16-bit copy would have written.
+// Lane l turns elements 8 l .. 8 l + 7 and 256 + 8 l .. into one 16-byte chunk
+// each, so eight lanes of a store cover all banks.  Rows past the context become
+// zeros (their probabilities are 0).
+template <int KV>
+__device__ void lt_convert(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p) {
+    using L = Lt<KV>;
+    const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - 8;
+    Waiter w{&c.abort, a.wait_limit};
+    int cnt = 0, steps = 0;
+    while (w.ok && p.next()) {
+        for (int t = p.t0; t < p.t1 && w.ok; ++t, ++cnt) {
+            const int st = cnt & 1, left = p.w.L - t * L::TOK;   // tokens from the tile's first on
+            if (!w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
+            for (int k = 0; k < L::TOK / L8_STEP; ++k, ++steps) {
+                const int s = steps % L8_SLOTS;
+                if (!w.warp(c.full8[s], steps / L8_SLOTS)) break;
+                const uint8_t *src = smem + L::OFF_8 + s * L8_SLOT;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // row cw of group i; its codes in two boxes of 256
+                    const int tok = k * L8_STEP + 8 * i + cw;
+                    const uint8_t *codes = src + i * 8 * LC + cw * 256 + 8 * lane;
+                    const float *scale = reinterpret_cast<const float *>(src + L8_STEP * LC + (8 * i + cw) * 16);
+                    uint8_t *row = smem + L::OFF_KV + st * L::STAGE + (tok >> 3) * LT_GROUP + (lane >> 3) * 1024 + cw * 128 +
+                                   (((lane & 7) ^ cw) << 4);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (tok < left) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(codes + h * 8 * 256);
+                            const float sc = scale[2 * h + (lane >> 4)];
+                            const uint2 lo = latent_codes_to_bf16(v.x, sc), hi = latent_codes_to_bf16(v.y, sc);
+                            x = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                        }
+                        *reinterpret_cast<uint4 *>(row + h * 4096) = x;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c.empty8[s]));
+            }
+            if (!w.ok) break;
+            fence_proxy_async_smem();   // the rows, for the tensor cores
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.kvfull[st]));
+        }
+    }
+}
+
+// MMA issuers, one lane each: warps 1 and 2 the S products of even and odd KV
+// tiles, warp 3 the products with the values.
+template <int KV>
+__device__ void lt_mma(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p,
+                       uint32_t tmem, int warp) {
+    using L = Lt<KV>;
+    constexpr bool BF16 = KV != PA_KV_F16;
+    const uint32_t base = smem_u32(smem);
+    Waiter w{&c.abort, a.wait_limit};
+    int n = 0, pieces = 0;   // KV tiles and pieces so far
+    if (warp < 3) {
+        const int e = warp - 1;
+        constexpr uint32_t ID = idesc_f16(LT_ROWS, L::TOK, BF16, false);
+        const uint64_t dq = sw128_desc(base, 16, LT_GROUP);
+        const uint64_t dk = sw128_desc(base + L::OFF_KV + e * L::STAGE, 16, LT_GROUP);
+        const uint32_t d = tmem + LT_S + 64 * e;
+        while (w.ok && p.next()) {
+            if (!w.lane(c.qfull, pieces)) break;
+            ++pieces;
+            for (int t = p.t0; t < p.t1; ++t, ++n) {
+                if ((n & 1) != e) continue;
+                if (!w.lane(c.sfree[e], (n >> 1) + 1) || !w.lane(c.kvfull[e], n >> 1)) break;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int k = 0; k < LROW / 16; ++k) {
+                    const uint64_t off = (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4);
+                    umma_f16(d, dq + off, dk + off, ID, k > 0 ? 1u : 0u);
+                }
+                umma_commit(smem_u32(&c.sfull[e]));
+            }
+            if (w.ok) umma_commit(smem_u32(&c.qempty));   // after this issuer's last product of the piece
+        }
+    } else {
+        constexpr uint32_t ID = idesc_f16(LT_ROWS, LC / 2, BF16, true);
+        const uint64_t dp = sw128_desc(base + L::OFF_P, 16, 1024);
+        const uint64_t dv0 = sw128_desc(base + L::OFF_KV, 1024, LT_GROUP);
+        while (w.ok && p.next()) {
+            for (int t = p.t0; t < p.t1; ++t, ++n) {
+                const int st = n & 1;
+                if (!w.lane(c.kvfull[st], n >> 1) || !w.lane(c.pfull, n)) break;
+                tc_fence_after_sync();
+                const uint64_t dv = dv0 + (uint64_t)(st * (L::STAGE >> 4));
+#pragma unroll
+                for (int k = 0; k < L::TOK / 16; ++k) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        umma_f16(tmem + (h ? LT_HI : 0u), dp + (uint64_t)((k * 32) >> 4),
+                                 dv + (uint64_t)((k * 2 * LT_GROUP + h * 4096) >> 4), ID, t > p.t0 || k > 0 ? 1u : 0u);
+                }
+                umma_commit(smem_u32(&c.pvdone));
+                umma_commit(smem_u32(&c.kvempty[st]));
+            }
+        }
+    }
+    // every product issued has completed before tensor memory is freed
+    umma_commit(smem_u32(&c.done));
+    mbar_wait_bounded(smem_u32(&c.done), 0, WAIT_LIMIT);
+}
+
+// The softmax warps (4 .. 7): row 16 (warp - 4) + (lane & 15); lanes 0 .. 15
+// take the first half of a tile's tokens and output dims 0 .. 255, lanes 16 ..
+// 31 the others.
+template <int KV>
+__device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p,
+                           uint32_t tmem) {
+    using L = Lt<KV>;
+    constexpr int HT = L::TOK / 2;   // tokens of a tile per thread
+    const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
+    const int half = lane >> 4, m = 16 * q + (lane & 15), tid = threadIdx.x & 127;
+    const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
+    uint8_t *prow = smem + L::OFF_P + m * 128;
+    Waiter w{&c.abort, a.wait_limit};
+    int n = 0;
+    while (w.ok && p.next()) {
+        const int rows = a.rows(p.w, p.r);
+        const bool live = 16 * q < rows;   // some row of this warp exists
+        const bool mine = m < rows;
+        const int vis = mine ? p.w.L - p.w.T + (int)(((long long)p.r * LT_ROWS + m) / a.H) + 1 : p.w.L;
+        float mrun = -INFINITY, l = 0.f;
+        for (int t = p.t0; t < p.t1; ++t, ++n) {
+            const int st = n & 1, t0 = t * L::TOK;
+            if (!w.warp(c.sfull[st], n >> 1)) break;
+            tc_fence_after_sync();
+            uint32_t pw[HT / 2];
+            float alpha = 1.f;
+            bool grew = false;
+            if (live) {
+                float s[HT];
+                tmem_ld_halves(trow + LT_S + 64 * st, s);
+                tmem_wait_ld();
+                tc_fence_before_sync();
+                const int first = t0 + HT * half;
+                if (first + HT > vis) {
+#pragma unroll
+                    for (int k = 0; k < HT; ++k) s[k] = first + k < vis ? s[k] : -INFINITY;
+                }
+                float mp[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int k = 4; k < HT; ++k) mp[k & 3] = fmaxf(mp[k & 3], s[k]);
+                float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * a.scale_log2;
+                const bool grow = mx > mrun + RESCALE_THRESHOLD;
+                grew = __any_sync(0xffffffffu, grow);
+                if (grew) {
+                    const float nm = grow ? mx : mrun;
+                    alpha = grow ? fast_exp2(mrun - nm) : 1.f;
+                    l *= alpha;
+                    mrun = nm;
+                }
+                const float mu = mrun == -INFINITY ? 0.f : mrun;   // a row that has seen nothing yet
+                float lp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < HT / 2; ++k) {
+                    const float x = fast_exp2(fmaf(s[2 * k], a.scale_log2, -mu));
+                    const float y = fast_exp2(fmaf(s[2 * k + 1], a.scale_log2, -mu));
+                    lp[k & 1] += x;
+                    lp[2 + (k & 1)] += y;
+                    pw[k] = pack_p<KV == PA_KV_F16 ? PA_KV_F16 : PA_KV_BF16>(x, y);
+                }
+                l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+            }
+            mbar_arrive(smem_u32(&c.sfree[st]));
+            // P is free, and O up to date, once the previous product is done
+            if (n > 0 && !w.warp(c.pvdone, n - 1)) break;
+            if (live) {
+                if (grew && t > p.t0) {
+                    tc_fence_after_sync();
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t o[32];
+                        tmem_ld32(trow + 32 * k, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                        tmem_st32(trow + 32 * k, o);
+                    }
+                    tmem_wait_st();
+                }
+#pragma unroll
+                for (int k = 0; k < HT / 8; ++k)
+                    *reinterpret_cast<uint4 *>(prow + (((HT / 8 * half + k) ^ (m & 7)) << 4)) =
+                        make_uint4(pw[4 * k], pw[4 * k + 1], pw[4 * k + 2], pw[4 * k + 3]);
+            }
+            if (!L::F8 && t0 + L::TOK > p.w.L) {
+                // the context's last tile: rows past it hold anything, and P is 0 there
+                uint8_t *kv = smem + L::OFF_KV + st * L::STAGE;
+                for (int k = tid + (p.w.L - t0) * 64; k < L::TOK * 64; k += 128) {
+                    const int r = k >> 6, cc = k & 63;
+                    *reinterpret_cast<uint4 *>(kv + (r >> 3) * LT_GROUP + (cc >> 3) * 1024 + (r & 7) * 128 +
+                                               (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            mbar_arrive(smem_u32(&c.pfull));
+        }
+        // ---- the piece's rows: finished, or a partial row
+        if (!w.ok || !w.warp(c.pvdone, n - 1)) break;
+        tc_fence_after_sync();
+        if (live) {
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const bool bad = *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) == p.local + 1;
+            if (bad) l = __int_as_float(0x7fc00000);
+            const bool whole = p.whole();
+            const float inv = 1.f / l;
+            uint16_t *orow = a.out + (a.first_row(p.w, p.r) + m) * LC + 256 * half;
+            float *part = a.o + ((long long)p.slot() * LT_ROWS + m) * LC + 256 * half;
+            if (!whole && mine && half == 0) a.ml[p.slot() * LT_ROWS + m] = make_float2(mrun, l);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                uint32_t o[32];
+                tmem_ld32(trow + 32 * k, o);
+                tmem_wait_ld();
+                if (mine && whole) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = (uint32_t)to_bits<KV>(__uint_as_float(o[j + 2 * i]) * inv) |
+                                   ((uint32_t)to_bits<KV>(__uint_as_float(o[j + 2 * i + 1]) * inv) << 16);
+                        *reinterpret_cast<uint4 *>(orow + 32 * k + j) = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                } else if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<uint4 *>(part + 32 * k + j) =
+                            make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                }
+                __syncwarp();   // the next load is the whole warp's
+            }
+        }
+        tc_fence_before_sync();
+    }
+}
+
+template <int KV>
+__global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
+    latent_kernel(const __grid_constant__ LtMaps maps, const typename Lt<KV>::Args a) {
+    using L = Lt<KV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    LtCtrl &c = *reinterpret_cast<LtCtrl *>(smem + LT_OFF_CTRL);
+    LtCtrl &c = *reinterpret_cast<LtCtrl *>(smem + L::OFF_CTRL);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t base = smem_u32(smem);
-    constexpr bool BF16 = KV != PA_KV_F16;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&c.kvfull[s]), 1);
+            mbar_init(smem_u32(&c.kvfull[s]), L::F8 ? 1 + L8_WARPS : 1);
             mbar_init(smem_u32(&c.kvempty[s]), 1);
             mbar_init(smem_u32(&c.sfull[s]), 1);
             mbar_init(smem_u32(&c.sfree[s]), 128);
+        }
+        for (int s = 0; s < L8_SLOTS; ++s) {
+            mbar_init(smem_u32(&c.full8[s]), 1);
+            mbar_init(smem_u32(&c.empty8[s]), L8_WARPS);
         }
         mbar_init(smem_u32(&c.pfull), 128);
         mbar_init(smem_u32(&c.pvdone), 1);
@@ -140,7 +492,6 @@ __global__ void __launch_bounds__(LT_THREADS, 1) latent_kernel(const __grid_cons
     }
     make_plan(a, &c.plan, c.warp_sums);
     const Plan plan = c.plan;
-    volatile int *abort_flag = &c.abort;
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
         if (warp == 0) {
             tmem_alloc(smem_u32(&c.tmem), LT_TMEM);
@@ -150,253 +501,16 @@ __global__ void __launch_bounds__(LT_THREADS, 1) latent_kernel(const __grid_cons
         __syncthreads();
         tc_fence_after_sync();
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
-        Walk<LatentArgs> p(a, plan);
+        Walk<typename L::Args> p(a, plan);
         if (warp == 0) {
-            // ---- producer: lane j < 8 copies tokens 8 j .. 8 j + 7 of a tile, lanes 8 .. 15 the query rows
-            const uint64_t first = policy_evict_first(), keep = policy_evict_normal();
-            int cnt = 0, pieces = 0;
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                const bool got = !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, a.wait_limit);
-                ok = __all_sync(0xffffffffu, got);
-                if (!ok) *abort_flag = 1;
-                return ok;
-            };
-            while (ok && p.next()) {
-                const int32_t *row = a.block_tables + (long long)p.seq * a.mbps;
-                if (!wait(&c.qempty, (uint32_t)((pieces & 1) ^ 1))) break;
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.qfull), LT_ROWS / 8 * LT_GROUP);
-                __syncwarp();
-                if (lane >= 8 && lane < 16)
-                    tma_load_3d(base + LT_OFF_Q + (lane - 8) * LT_GROUP, &tmq, 0, (int)(a.first_row(p.w, p.r) + 8 * (lane - 8)),
-                                0, smem_u32(&c.qfull), keep);
-                ++pieces;
-                for (int t = p.t0; t < p.t1; ++t) {
-                    const int tok = t * LT_TOK + 8 * lane;
-                    const bool mine = lane < LT_TOK / 8 && tok < p.w.L;
-                    const int32_t blk = mine ? __ldg(row + tok / a.bs) : 0;
-                    const int st = cnt & 1;
-                    if (!wait(&c.kvempty[st], (uint32_t)(((cnt >> 1) & 1) ^ 1))) break;
-                    const unsigned boxes = __ballot_sync(0xffffffffu, mine);
-                    const bool bad = __any_sync(0xffffffffu, mine && (blk < 0 || blk >= a.num_blocks));
-                    if (lane == 0) {
-                        if (bad) *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) = p.local + 1;
-                        mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]), bad ? 0u : (uint32_t)(__popc(boxes) * LT_GROUP));
-                    }
-                    __syncwarp();
-                    if (!bad && mine)
-                        tma_load_3d(base + LT_OFF_KV + st * LT_STAGE + lane * LT_GROUP, &tmkv, 0,
-                                    (int)((long long)blk * a.bs) + tok % a.bs, 0, smem_u32(&c.kvfull[st]), first);
-                    __syncwarp();
-                    ++cnt;
-                }
-            }
-            // the last copies into every buffer have landed before the CTA leaves
-            for (int s = 0; s < 2; ++s)
-                if (cnt > s)
-                    mbar_wait_bounded(smem_u32(&c.kvfull[s]), (uint32_t)(((cnt - 1 - s) / 2) & 1), WAIT_LIMIT);
-            if (pieces) mbar_wait_bounded(smem_u32(&c.qfull), (uint32_t)((pieces - 1) & 1), WAIT_LIMIT);
+            lt_load<KV>(smem, c, a, p, maps);
         } else if (warp < 4) {
-            // ---- MMA issuers, one thread each: warps 1 and 2 the S products of even and odd KV tiles, warp 3 P V
-            if (lane == 0) {
-                bool ok = true;
-                auto wait = [&](uint64_t *bar, uint32_t parity) {
-                    ok = !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, a.wait_limit);
-                    if (!ok) *abort_flag = 1;
-                    return ok;
-                };
-                int n = 0, pieces = 0;   // KV tiles and pieces so far
-                if (warp < 3) {
-                    const int e = warp - 1;
-                    constexpr uint32_t ID = idesc_f16(LT_ROWS, LT_TOK, BF16, false);
-                    const uint64_t dq = sw128_desc(base + LT_OFF_Q, 16, LT_GROUP);
-                    const uint64_t dk = sw128_desc(base + LT_OFF_KV + e * LT_STAGE, 16, LT_GROUP);
-                    const uint32_t d = tmem + LT_S + 64 * e;
-                    while (ok && p.next()) {
-                        if (!wait(&c.qfull, (uint32_t)(pieces & 1))) break;
-                        ++pieces;
-                        for (int t = p.t0; t < p.t1; ++t, ++n) {
-                            if ((n & 1) != e) continue;
-                            if (!wait(&c.sfree[e], (uint32_t)(((n >> 1) & 1) ^ 1))) break;
-                            if (!wait(&c.kvfull[e], (uint32_t)((n >> 1) & 1))) break;
-                            tc_fence_after_sync();
-#pragma unroll
-                            for (int k = 0; k < LROW / 16; ++k) {
-                                const uint64_t off = (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4);
-                                umma_f16(d, dq + off, dk + off, ID, k > 0 ? 1u : 0u);
-                            }
-                            umma_commit(smem_u32(&c.sfull[e]));
-                        }
-                        if (ok) umma_commit(smem_u32(&c.qempty));   // after this issuer's last product of the piece
-                    }
-                } else {
-                    constexpr uint32_t ID = idesc_f16(LT_ROWS, LC / 2, BF16, true);
-                    const uint64_t dp = sw128_desc(base + LT_OFF_P, 16, 1024);
-                    const uint64_t dv0 = sw128_desc(base + LT_OFF_KV, 1024, LT_GROUP);
-                    while (ok && p.next()) {
-                        for (int t = p.t0; t < p.t1; ++t, ++n) {
-                            const int st = n & 1;
-                            if (!wait(&c.kvfull[st], (uint32_t)((n >> 1) & 1))) break;
-                            if (!wait(&c.pfull, (uint32_t)(n & 1))) break;
-                            tc_fence_after_sync();
-                            const uint64_t dv = dv0 + (uint64_t)(st * (LT_STAGE >> 4));
-#pragma unroll
-                            for (int k = 0; k < LT_TOK / 16; ++k) {
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    umma_f16(tmem + (h ? LT_HI : 0u), dp + (uint64_t)((k * 32) >> 4),
-                                             dv + (uint64_t)((k * 2 * LT_GROUP + h * 4096) >> 4), ID,
-                                             t > p.t0 || k > 0 ? 1u : 0u);
-                            }
-                            umma_commit(smem_u32(&c.pvdone));
-                            umma_commit(smem_u32(&c.kvempty[st]));
-                        }
-                    }
-                }
-                // every product issued has completed before tensor memory is freed
-                umma_commit(smem_u32(&c.done));
-                mbar_wait_bounded(smem_u32(&c.done), 0, WAIT_LIMIT);
-            }
+            if (lane == 0) lt_mma<KV>(smem, c, a, p, tmem, warp);
             __syncwarp();
+        } else if (warp < 8) {
+            lt_softmax<KV>(smem, c, a, p, tmem);
         } else {
-            // ---- softmax: row 16 (warp - 4) + (lane & 15); lanes 0 .. 15 take tokens 0 .. 31 of a tile and
-            // output dims 0 .. 255, lanes 16 .. 31 the others
-            const int q = warp - 4, half = lane >> 4, m = 16 * q + (lane & 15), tid = threadIdx.x - 128;
-            const uint32_t trow = tmem + ((uint32_t)(32 * q) << 16);
-            uint8_t *prow = smem + LT_OFF_P + m * 128;
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                const bool got = !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, a.wait_limit);
-                ok = __all_sync(0xffffffffu, got);
-                if (!ok) *abort_flag = 1;
-                return ok;
-            };
-            int n = 0;
-            while (ok && p.next()) {
-                const int rows = a.rows(p.w, p.r);
-                const bool live = 16 * q < rows;      // some row of this warp exists
-                const bool mine = m < rows;
-                const int vis = mine ? p.w.L - p.w.T + (int)(((long long)p.r * LT_ROWS + m) / a.H) + 1 : p.w.L;
-                float mrun = -INFINITY, l = 0.f;
-                for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
-                    const int st = n & 1, t0 = t * LT_TOK;
-                    if (!wait(&c.sfull[st], (uint32_t)((n >> 1) & 1))) break;
-                    tc_fence_after_sync();
-                    uint32_t pw[16];
-                    float alpha = 1.f;
-                    bool grew = false;
-                    if (live) {
-                        uint32_t sr[32];
-                        tmem_ld_half32(trow + LT_S + 64 * st, sr);
-                        tmem_wait_ld();
-                        tc_fence_before_sync();
-                        float s[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(sr[k]);
-                        const int first = t0 + 32 * half;
-                        if (first + 32 > vis) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) s[k] = first + k < vis ? s[k] : -INFINITY;
-                        }
-                        float mp[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                        for (int k = 4; k < 32; ++k) mp[k & 3] = fmaxf(mp[k & 3], s[k]);
-                        float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) * a.scale_log2;
-                        const bool grow = mx > mrun + RESCALE_THRESHOLD;
-                        grew = __any_sync(0xffffffffu, grow);
-                        if (grew) {
-                            const float nm = grow ? mx : mrun;
-                            alpha = grow ? fast_exp2(mrun - nm) : 1.f;
-                            l *= alpha;
-                            mrun = nm;
-                        }
-                        const float mu = mrun == -INFINITY ? 0.f : mrun;   // a row that has seen nothing yet
-                        float lp[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float x = fast_exp2(fmaf(s[2 * k], a.scale_log2, -mu));
-                            const float y = fast_exp2(fmaf(s[2 * k + 1], a.scale_log2, -mu));
-                            lp[k & 1] += x;
-                            lp[2 + (k & 1)] += y;
-                            pw[k] = pack_p<KV>(x, y);
-                        }
-                        l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
-                    }
-                    mbar_arrive(smem_u32(&c.sfree[st]));
-                    // P is free, and O up to date, once the previous product is done
-                    if (n > 0 && !wait(&c.pvdone, (uint32_t)((n - 1) & 1))) break;
-                    if (live) {
-                        if (grew && t > p.t0) {
-                            tc_fence_after_sync();
-#pragma unroll 1
-                            for (int k = 0; k < 8; ++k) {
-                                uint32_t o[32];
-                                tmem_ld32(trow + 32 * k, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                                tmem_st32(trow + 32 * k, o);
-                            }
-                            tmem_wait_st();
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4 *>(prow + (((4 * half + k) ^ (m & 7)) << 4)) =
-                                make_uint4(pw[4 * k], pw[4 * k + 1], pw[4 * k + 2], pw[4 * k + 3]);
-                    }
-                    if (t0 + LT_TOK > p.w.L) {
-                        // the context's last tile: rows past it hold anything, and P is 0 there
-                        uint8_t *kv = smem + LT_OFF_KV + st * LT_STAGE;
-                        for (int k = tid + (p.w.L - t0) * 64; k < LT_TOK * 64; k += 128) {
-                            const int r = k >> 6, cc = k & 63;
-                            *reinterpret_cast<uint4 *>(kv + (r >> 3) * LT_GROUP + (cc >> 3) * 1024 + (r & 7) * 128 +
-                                                       (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    tc_fence_before_sync();
-                    mbar_arrive(smem_u32(&c.pfull));
-                }
-                if (!ok) break;
-                // ---- the piece's rows: finished, or a partial row
-                if (!wait(&c.pvdone, (uint32_t)((n - 1) & 1))) break;
-                tc_fence_after_sync();
-                if (live) {
-                    l += __shfl_xor_sync(0xffffffffu, l, 16);
-                    const bool bad = *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) == p.local + 1;
-                    if (bad) l = __int_as_float(0x7fc00000);
-                    const bool whole = p.whole();
-                    const float inv = 1.f / l;
-                    uint16_t *orow = a.out + (a.first_row(p.w, p.r) + m) * LC + 256 * half;
-                    float *part = a.o + ((long long)p.slot() * LT_ROWS + m) * LC + 256 * half;
-                    if (!whole && mine && half == 0) a.ml[p.slot() * LT_ROWS + m] = make_float2(mrun, l);
-#pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        uint32_t o[32];
-                        tmem_ld32(trow + 32 * k, o);
-                        tmem_wait_ld();
-                        if (mine && whole) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    w[i] = (uint32_t)out_bits<KV>(__uint_as_float(o[j + 2 * i]) * inv) |
-                                           ((uint32_t)out_bits<KV>(__uint_as_float(o[j + 2 * i + 1]) * inv) << 16);
-                                *reinterpret_cast<uint4 *>(orow + 32 * k + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else if (mine) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<uint4 *>(part + 32 * k + j) =
-                                    make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                        }
-                        __syncwarp();   // the next load is the whole warp's
-                    }
-                }
-                tc_fence_before_sync();
-            }
+            if constexpr (L::F8) lt_convert<KV>(smem, c, a, p);
         }
         tc_fence_before_sync();
         __syncthreads();
@@ -416,7 +530,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1) latent_kernel(const __grid_cons
 // CTA of the first kernel gave up).  Four groups of 128 threads take every
 // fourth piece, four output dims a thread.
 template <int KV>
-__global__ void __launch_bounds__(512) latent_merge_kernel(const LatentArgs a, int ctas) {
+__global__ void __launch_bounds__(512) latent_merge_kernel(const typename Lt<KV>::Args a, int ctas) {
+    using Args = typename Lt<KV>::Args;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float4 so[3][128];
     __shared__ float sl[3];
@@ -429,16 +544,16 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentArgs a, i
     const long long total = a.unit_base[a.num_seqs];
     uint16_t *orow = a.out + row * LC;
     const int seq = a.query_start && total >= 0 ? sequence_of(a.query_start, a.num_seqs, qt) : qt;
-    LatentArgs::Seq w{};
+    typename Args::Seq w{};
     if (total >= 0) w = a.seq_work(seq);
     if (failed || total < 0 || !w.valid || w.tiles == 0) {
-        const uint16_t x = !failed && total >= 0 && w.valid ? 0 : out_bits<KV>(__int_as_float(0x7fc00000));
+        const uint16_t x = !failed && total >= 0 && w.valid ? 0 : to_bits<KV>(__int_as_float(0x7fc00000));
         for (int d = threadIdx.x; d < LC; d += blockDim.x) orow[d] = x;
         return;
     }
     const long long idx = row - (long long)w.q0 * a.H;
     const int r = (int)(idx / LT_ROWS), m = (int)(idx % LT_ROWS);
-    const Pieces pc(a.unit_base[seq] + a.start(w, r), a.row_tiles(w, r), LatentArgs::COST, total, ctas);
+    const Pieces pc(a.unit_base[seq] + a.start(w, r), a.row_tiles(w, r), Args::COST, total, ctas);
     if (pc.k0 == pc.k1) return;   // finished by one CTA
     const int g = threadIdx.x >> 7, d = threadIdx.x & 127;
     float M = -INFINITY;
@@ -476,8 +591,8 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const LatentArgs a, i
         }
         const float inv = 1.f / l;
         uint2 v;
-        v.x = (uint32_t)out_bits<KV>(acc.x * inv) | ((uint32_t)out_bits<KV>(acc.y * inv) << 16);
-        v.y = (uint32_t)out_bits<KV>(acc.z * inv) | ((uint32_t)out_bits<KV>(acc.w * inv) << 16);
+        v.x = (uint32_t)to_bits<KV>(acc.x * inv) | ((uint32_t)to_bits<KV>(acc.y * inv) << 16);
+        v.y = (uint32_t)to_bits<KV>(acc.z * inv) | ((uint32_t)to_bits<KV>(acc.w * inv) << 16);
         *reinterpret_cast<uint2 *>(orow + 4 * d) = v;
     }
 }
@@ -519,6 +634,21 @@ bool row_map(CUtensorMap *map, const void *base, long long rows, int kv) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// `width` elements from byte `at` of a quantised cache's rows, boxes of
+// `box_width` x 8 rows.
+bool row8_map(CUtensorMap *map, const uint8_t *cache, int at, int width, int box_width, CUtensorMapDataType type,
+              CUtensorMapSwizzle swizzle, long long rows) {
+    auto enc = tma_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {LROW8};
+    cuuint32_t box[2] = {(cuuint32_t)box_width, 8};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, type, 2, const_cast<uint8_t *>(cache) + at, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Shared-memory limits are set per device, on its first call.
 template <int KV>
 cudaError_t lt_setup() {
@@ -528,13 +658,13 @@ cudaError_t lt_setup() {
     if (const cudaError_t e = cudaGetDevice(&dev)) return e;
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 64 && done[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(latent_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, LT_SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(latent_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lt<KV>::SMEM);
     if (e == cudaSuccess && dev < 64) done[dev] = true;
     return e;
 }
 
 template <int KV>
-int launch_merge(const LatentArgs &a, int ctas, cudaStream_t st) {
+int launch_merge(const typename Lt<KV>::Args &a, int ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.num_query_tokens * a.H));
     cfg.blockDim = dim3(512);
@@ -548,95 +678,55 @@ int launch_merge(const LatentArgs &a, int ctas, cudaStream_t st) {
 }
 
 template <int KV>
-int launch_latent(const LatentArgs &a, cudaStream_t st) {
+int launch_latent(const typename Lt<KV>::Args &a, cudaStream_t st) {
     if (lt_setup<KV>() != cudaSuccess) return PA_ERR_CUDA;
-    CUtensorMap tmkv, tmq;
-    if (!row_map(&tmkv, a.cache, a.num_blocks * a.bs, KV) ||
-        !row_map(&tmq, a.query, (long long)a.num_query_tokens * a.H, KV))
-        return PA_ERR_CUDA;
+    LtMaps maps{};
+    const long long rows = a.num_blocks * a.bs;
+    bool ok = row_map(&maps.q, a.query, (long long)a.num_query_tokens * a.H, KV);
+    if (KV == PA_KV_FP8_E4M3)
+        ok = ok && row8_map(&maps.kv, a.cache, 0, LC, 256, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, rows) &&
+             row8_map(&maps.rope, a.cache, L8_ROPE, LR, LR, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      CU_TENSOR_MAP_SWIZZLE_128B, rows) &&
+             row8_map(&maps.scale, a.cache, L8_SCALE, 4, 4, CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                      CU_TENSOR_MAP_SWIZZLE_NONE, rows);
+    else
+        ok = ok && row_map(&maps.kv, a.cache, rows, KV);
+    if (!ok) return PA_ERR_CUDA;
     const int ctas = std::min(num_sms(), AXIS_MAX_CTAS);
-    latent_kernel<KV><<<ctas, LT_THREADS, LT_SMEM, st>>>(tmkv, tmq, a);
+    latent_kernel<KV><<<ctas, Lt<KV>::THREADS, Lt<KV>::SMEM, st>>>(maps, a);
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     return launch_merge<KV>(a, ctas, st);
 }
 
-// One CTA per query row, a token per warp and step.
+// Arguments of the kernels for a call.
 template <int KV>
-__global__ void __launch_bounds__(256) latent_simple_kernel(const LatentArgs a) {
-    const int h = blockIdx.x % a.H, qt = blockIdx.x / a.H;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->error = 0;
-    __shared__ float sm[8], sl[8], so[8][LC];
-    int seq = qt, L = 0, vis = 0;
-    bool bad = false;
-    if (a.query_start) {
-        bool order = a.query_start[0] == 0 && a.query_start[a.num_seqs] == a.num_query_tokens;
-        for (int i = threadIdx.x; i < a.num_seqs; i += blockDim.x)
-            if (a.query_start[i] > a.query_start[i + 1]) order = false;
-        bad = !__syncthreads_and(order);
-        int lo = 0, hi = a.num_seqs;
-        while (!bad && hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.query_start[mid] <= qt) lo = mid; else hi = mid;
-        }
-        seq = lo;
-    }
-    if (!bad) {
-        L = a.context_lens[seq];
-        const int q0 = a.query_start ? a.query_start[seq] : qt, T = a.query_start ? a.query_start[seq + 1] - q0 : 1;
-        bad = L < 0 || L > a.max_context_len || (long long)L > (long long)a.mbps * a.bs ||
-              (a.query_start && T > L);
-        vis = L - T + (qt - q0) + 1;
-        if (!a.query_start) vis = L;
-    }
-    const uint16_t *qr = a.query + (long long)blockIdx.x * LROW;
-    float q[18], o[16], m = -INFINITY, l = 0.f;
-    for (int k = 0; k < 18; ++k) q[k] = to_float<KV>(qr[32 * k + lane]);
-    for (int k = 0; k < 16; ++k) o[k] = 0.f;
-    for (int t = warp; !bad && t < vis; t += 8) {
-        const long long blk = a.block_tables[(long long)seq * a.mbps + t / a.bs];
-        float x[18];
-        if (blk < 0 || blk >= a.num_blocks) {
-            for (int k = 0; k < 18; ++k) x[k] = __int_as_float(0x7fc00000);
-        } else {
-            const long long slot = blk * a.bs + t % a.bs;
-            if constexpr (KV == PA_KV_FP8_E4M3) {
-                const uint8_t *row = a.cache + slot * LROW8;
-                for (int k = 0; k < 16; ++k) {
-                    const uint32_t c = row[32 * k + lane];
-                    const float s = *reinterpret_cast<const float *>(row + L8_SCALE + 4 * (k / 4));
-                    x[k] = __uint_as_float(latent_codes_to_bf16(c, s).x << 16);
-                }
-                for (int k = 0; k < 2; ++k)
-                    x[16 + k] = to_float<KV>(*reinterpret_cast<const uint16_t *>(row + L8_ROPE + 2 * (32 * k + lane)));
-            } else {
-                const uint16_t *row = reinterpret_cast<const uint16_t *>(a.cache) + slot * LROW;
-                for (int k = 0; k < 18; ++k) x[k] = to_float<KV>(row[32 * k + lane]);
-            }
-        }
-        float s = 0.f;
-        for (int k = 0; k < 18; ++k) s = fmaf(q[k], x[k], s);
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= a.scale_log2;
-        const float nm = fmaxf(m, s), al = fast_exp2(m - nm), p = s != s ? s : fast_exp2(s - nm);
-        l = l * al + p;
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * al + p * x[k];
-        m = nm;
-    }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-    for (int k = 0; k < 16; ++k) so[warp][32 * k + lane] = o[k];
-    __syncthreads();
-    float M = -INFINITY, den = 0.f;
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w]);
-    for (int w = 0; w < 8; ++w)
-        if (sl[w] != 0.f) den += sl[w] * fast_exp2(sm[w] - M);
-    for (int d = threadIdx.x; d < LC; d += 256) {
-        float v = 0.f;
-        for (int w = 0; w < 8; ++w)
-            if (sl[w] != 0.f) v += so[w][d] * fast_exp2(sm[w] - M);
-        v = bad ? __int_as_float(0x7fc00000) : vis <= 0 ? 0.f : v / den;
-        a.out[(long long)blockIdx.x * LC + d] = to_bits<KV>(v);
-    }
+int run_latent(void *out, const void *query, const void *cache, const int32_t *block_tables,
+               const int32_t *context_lens, const int32_t *query_start, int num_seqs, int num_query_tokens,
+               int num_heads, int block_size, int64_t num_blocks, int max_blocks_per_seq, int max_context_len,
+               float scale, uint8_t *ws, cudaStream_t st) {
+    const LtLayout lay = lt_layout(num_seqs);
+    typename Lt<KV>::Args a{};
+    a.out = static_cast<uint16_t *>(out);
+    a.query = static_cast<const uint16_t *>(query);
+    a.cache = static_cast<const uint8_t *>(cache);
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.hdr = reinterpret_cast<WsHeader *>(ws);
+    a.num_seqs = num_seqs;
+    a.num_query_tokens = num_query_tokens;
+    a.H = num_heads;
+    a.bs = block_size;
+    a.mbps = max_blocks_per_seq;
+    a.max_context_len = max_context_len;
+    a.num_blocks = num_blocks;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.wait_limit = pipeline_wait_limit();
+    a.status = reinterpret_cast<int *>(ws + lay.status);
+    a.unit_base = reinterpret_cast<long long *>(ws + lay.unit_base);
+    a.ml = reinterpret_cast<float2 *>(ws + lay.ml);
+    a.o = reinterpret_cast<float *>(ws + lay.o);
+    return launch_latent<KV>(a, st);
 }
 
 }  // namespace
@@ -672,31 +762,9 @@ extern "C" int pa_latent_attention(void *out, const void *query, const void *cac
         return PA_ERR_WORKSPACE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const LtLayout lay = lt_layout(num_seqs);
-    LatentArgs a{};
-    a.out = static_cast<uint16_t *>(out);
-    a.query = static_cast<const uint16_t *>(query);
-    a.cache = static_cast<const uint8_t *>(cache);
-    a.block_tables = block_tables;
-    a.context_lens = context_lens;
-    a.query_start = query_start;
-    a.hdr = reinterpret_cast<WsHeader *>(ws);
-    a.num_seqs = num_seqs;
-    a.num_query_tokens = num_query_tokens;
-    a.H = num_heads;
-    a.bs = block_size;
-    a.mbps = max_blocks_per_seq;
-    a.max_context_len = max_context_len;
-    a.num_blocks = num_blocks;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.wait_limit = pipeline_wait_limit();
-    a.status = reinterpret_cast<int *>(ws + lay.status);
-    a.unit_base = reinterpret_cast<long long *>(ws + lay.unit_base);
-    a.ml = reinterpret_cast<float2 *>(ws + lay.ml);
-    a.o = reinterpret_cast<float *>(ws + lay.o);
-    if (kv_dtype == PA_KV_F16) return launch_latent<PA_KV_F16>(a, st);
-    if (kv_dtype == PA_KV_BF16) return launch_latent<PA_KV_BF16>(a, st);
-    const unsigned grid = (unsigned)num_query_tokens * num_heads;
-    latent_simple_kernel<PA_KV_FP8_E4M3><<<grid, 256, 0, st>>>(a);
-    return cuda_status(cudaGetLastError());
+    const auto run = kv_dtype == PA_KV_F16    ? run_latent<PA_KV_F16>
+                     : kv_dtype == PA_KV_BF16 ? run_latent<PA_KV_BF16>
+                                              : run_latent<PA_KV_FP8_E4M3>;
+    return run(out, query, cache, block_tables, context_lens, query_start, num_seqs, num_query_tokens, num_heads,
+               block_size, num_blocks, max_blocks_per_seq, max_context_len, scale, ws, st);
 }
