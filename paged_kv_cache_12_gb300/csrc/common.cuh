@@ -232,6 +232,20 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
     return d;
 }
 
+// True in one thread of the (whole) warp.  A branch on it, unlike one on the
+// lane number, tells the compiler that a single thread runs it: operands of
+// tcgen05.mma then stay in uniform registers (one thread issuing M 64, N 64
+// products from shared memory: 59 cycles each, 136 behind a lane test).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "elect.sync _|P, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // 2^x, hardware approximation (flushes subnormal results to zero).
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

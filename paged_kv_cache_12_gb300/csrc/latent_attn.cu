@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
         if (warp == 0) {
             lt_load<KV>(smem, c, a, p, maps);
         } else if (warp < 4) {
-            if (lane == 0) lt_mma<KV>(smem, c, a, p, tmem, warp);
+            if (elect_one()) lt_mma<KV>(smem, c, a, p, tmem, warp);
             __syncwarp();
         } else if (warp < 8) {
             lt_softmax<KV>(smem, c, a, p, tmem);

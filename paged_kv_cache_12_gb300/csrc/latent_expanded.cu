@@ -464,9 +464,10 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
             ex_softmax<KV>(smem, c, a, p, tmem, (warp - 4) >> 2);
         } else {
             regs_decrease<EX_REGS_LOW>();
-            if ((threadIdx.x & 31) == 0) {
-                if (warp == 0) ex_load(smem, c, a, p, &tmq, &tmk, &tmr, &tmv);
-                if (warp == 2) ex_mma<KV>(smem, c, a, p, tmem);
+            if (warp == 0) {
+                if (elect_one()) ex_load(smem, c, a, p, &tmq, &tmk, &tmr, &tmv);
+            } else if (warp == 2) {
+                if (elect_one()) ex_mma<KV>(smem, c, a, p, tmem);
             }
             __syncwarp();
         }
