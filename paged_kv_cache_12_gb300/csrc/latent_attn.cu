@@ -26,7 +26,7 @@ struct LatentArgs {
     long long wait_limit;
     // workspace
     int *status;            // [AXIS_MAX_CTAS] nonzero: the CTA gave up waiting
-    long long *unit_base;   // [num_seqs + 1]
+    Cut *cuts;              // [AXIS_MAX_CTAS]
     float2 *ml;             // [2 AXIS_MAX_CTAS][LT_ROWS] maximum (log2 units) and sum of a partial row
     float *o;               // [2 AXIS_MAX_CTAS][LT_ROWS][LC] its unnormalised output
 
@@ -62,6 +62,7 @@ struct LatentArgs {
         return !query_start || offsets_ok(query_start, num_seqs, num_query_tokens);
     }
     // rows of row tile r, and its first row in the query
+    __device__ __forceinline__ int cut_rows(const Seq &w, int r) const { return rows(w, r); }
     __device__ __forceinline__ int rows(const Seq &w, int r) const {
         return (int)min((long long)LT_ROWS, (long long)w.T * H - (long long)r * LT_ROWS);
     }
@@ -492,6 +493,8 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
     }
     make_plan(a, &c.plan, c.warp_sums);
     const Plan plan = c.plan;
+    fill_idle_rows<LC / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
+                           KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
         if (warp == 0) {
             tmem_alloc(smem_u32(&c.tmem), LT_TMEM);
@@ -525,85 +528,100 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
 
 // ------------------------------------------------------------------ merge
 
-// One CTA per query row: rows of a cut row tile from their pieces' partial rows,
-// zeros for an empty context, NaN for an invalid one (and for every row when a
-// CTA of the first kernel gave up).  Four groups of 128 threads take every
-// fourth piece, four output dims a thread.
+// Rows of the cut row tiles from their pieces' partial rows; blockIdx.x is the
+// CTA whose range begins in the row tile.  Few pieces (two as a rule): block y
+// = 0, 8, .. takes eight rows, a warp each.  Many (a few long sequences): block
+// y takes row y, its warps every eighth piece.  When a CTA of the first kernel
+// gave up, every row becomes NaN.
+constexpr int MG_FEW = 8;
+
+// Pieces first, first + step, .. of a row: adds their weighted outputs, 16 dims a lane.
+struct RowSum {
+    float4 o[4];
+    float l;
+};
+__device__ __forceinline__ RowSum add_pieces(const float2 *ml, const float *o, const Pieces &pc, int m, float mu, int first,
+                                             int step) {
+    const int lane = threadIdx.x & 31;
+    RowSum x{};
+#pragma unroll 4
+    for (int k = pc.k0 + first; k <= pc.k1; k += step) {
+        const long long at = (long long)pc.slot(k) * LT_ROWS + m;
+        const float2 v = ml[at];
+        const float wt = fast_exp2(v.x - mu);
+        const float4 *src = reinterpret_cast<const float4 *>(o + at * LC) + lane;
+        x.l = fmaf(v.y, wt, x.l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 y = src[32 * j];
+            x.o[j].x = fmaf(y.x, wt, x.o[j].x);
+            x.o[j].y = fmaf(y.y, wt, x.o[j].y);
+            x.o[j].z = fmaf(y.z, wt, x.o[j].z);
+            x.o[j].w = fmaf(y.w, wt, x.o[j].w);
+        }
+    }
+    return x;
+}
+
 template <int KV>
-__global__ void __launch_bounds__(512) latent_merge_kernel(const typename Lt<KV>::Args a, int ctas) {
-    using Args = typename Lt<KV>::Args;
+__global__ void __launch_bounds__(256) latent_merge_kernel(const typename Lt<KV>::Args a, int ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ float4 so[3][128];
-    __shared__ float sl[3];
-    const long long row = blockIdx.x;
-    const int qt = (int)(row / a.H);
-    int failed = 0;
-    for (int i = threadIdx.x; i < ctas; i += blockDim.x) failed |= a.status[i];
-    failed = __syncthreads_or(failed);
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
-    const long long total = a.unit_base[a.num_seqs];
-    uint16_t *orow = a.out + row * LC;
-    const int seq = a.query_start && total >= 0 ? sequence_of(a.query_start, a.num_seqs, qt) : qt;
-    typename Args::Seq w{};
-    if (total >= 0) w = a.seq_work(seq);
-    if (failed || total < 0 || !w.valid || w.tiles == 0) {
-        const uint16_t x = !failed && total >= 0 && w.valid ? 0 : to_bits<KV>(__int_as_float(0x7fc00000));
-        for (int d = threadIdx.x; d < LC; d += blockDim.x) orow[d] = x;
+    __shared__ RowSum part[8][32];
+    const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Cut cut = a.cuts[cta];
+    const bool failed = any_gave_up(a.status, ctas);
+    if (cta == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
+    if (failed) {
+        const long long n = (long long)a.num_query_tokens * a.H * (LC / 8);
+        if (blockIdx.y == 0)
+            fill_rows(a.out, range_begin(n, cta, ctas), range_begin(n, cta + 1, ctas),
+                      KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
         return;
     }
-    const long long idx = row - (long long)w.q0 * a.H;
-    const int r = (int)(idx / LT_ROWS), m = (int)(idx % LT_ROWS);
-    const Pieces pc(a.unit_base[seq] + a.start(w, r), a.row_tiles(w, r), Args::COST, total, ctas);
-    if (pc.k0 == pc.k1) return;   // finished by one CTA
-    const int g = threadIdx.x >> 7, d = threadIdx.x & 127;
+    if ((int)blockIdx.y >= cut.rows) return;
+    const Pieces pc(cut, cta, cut.ntiles, Lt<KV>::Args::COST, ctas);
+    const int pieces = pc.k1 - pc.k0 + 1;
+    const bool few = pieces <= MG_FEW;
+    const int m = few ? blockIdx.y + warp : blockIdx.y;
+    if (few && ((blockIdx.y & 7) != 0 || m >= cut.rows)) return;
     float M = -INFINITY;
-#pragma unroll 8
-    for (int k = pc.k0; k <= pc.k1; ++k) M = fmaxf(M, a.ml[pc.slot(k) * LT_ROWS + m].x);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int k = pc.k0 + g; k <= pc.k1; k += 4) {
-        const int slot = pc.slot(k);
-        const float2 ml = a.ml[slot * LT_ROWS + m];
-        const float4 o = *reinterpret_cast<const float4 *>(a.o + ((long long)slot * LT_ROWS + m) * LC + 4 * d);
-        const float wt = fast_exp2(ml.x - mu);
-        l = fmaf(ml.y, wt, l);
-        acc.x = fmaf(o.x, wt, acc.x);
-        acc.y = fmaf(o.y, wt, acc.y);
-        acc.z = fmaf(o.z, wt, acc.z);
-        acc.w = fmaf(o.w, wt, acc.w);
-    }
-    if (g) {
-        so[g - 1][d] = acc;
-        if (d == 0) sl[g - 1] = l;
-    }
-    __syncthreads();
-    if (g == 0) {
+    for (int k = pc.k0 + lane; k <= pc.k1; k += 32) M = fmaxf(M, a.ml[(long long)pc.slot(k) * LT_ROWS + m].x);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const float4 x = so[k][d];
-            acc.x += x.x;
-            acc.y += x.y;
-            acc.z += x.z;
-            acc.w += x.w;
-            l += sl[k];
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    const float mu = M == -INFINITY ? 0.f : M;
+    RowSum x = add_pieces(a.ml, a.o, pc, m, mu, few ? 0 : warp, few ? 1 : 8);
+    if (!few) {
+        part[warp][lane] = x;
+        __syncthreads();
+        if (warp) return;
+        for (int k = 1; k < 8; ++k) {
+            const RowSum y = part[k][lane];
+            x.l += y.l;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x.o[j].x += y.o[j].x;
+                x.o[j].y += y.o[j].y;
+                x.o[j].z += y.o[j].z;
+                x.o[j].w += y.o[j].w;
+            }
         }
-        const float inv = 1.f / l;
-        uint2 v;
-        v.x = (uint32_t)to_bits<KV>(acc.x * inv) | ((uint32_t)to_bits<KV>(acc.y * inv) << 16);
-        v.y = (uint32_t)to_bits<KV>(acc.z * inv) | ((uint32_t)to_bits<KV>(acc.w * inv) << 16);
-        *reinterpret_cast<uint2 *>(orow + 4 * d) = v;
     }
+    const float inv = 1.f / x.l;
+    const long long row = a.first_row(a.seq_work(cut.seq), cut.r) + m;
+    uint2 *out = reinterpret_cast<uint2 *>(a.out + row * LC) + lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        out[32 * j] = make_uint2((uint32_t)to_bits<KV>(x.o[j].x * inv) | ((uint32_t)to_bits<KV>(x.o[j].y * inv) << 16),
+                                 (uint32_t)to_bits<KV>(x.o[j].z * inv) | ((uint32_t)to_bits<KV>(x.o[j].w * inv) << 16));
 }
 
 // ------------------------------------------------------------------ launch
 
 struct LtLayout {
-    size_t status, unit_base, ml, o, total;
+    size_t status, cuts, ml, o, total;
 };
 
-LtLayout lt_layout(int num_seqs) {
+LtLayout lt_layout() {
     LtLayout l;
     size_t at = 256;   // header
     auto take = [&](size_t bytes) {
@@ -612,7 +630,7 @@ LtLayout lt_layout(int num_seqs) {
         return p;
     };
     l.status = take(sizeof(int) * AXIS_MAX_CTAS);
-    l.unit_base = take(sizeof(long long) * ((size_t)num_seqs + 1));
+    l.cuts = take(sizeof(Cut) * AXIS_MAX_CTAS);
     l.ml = take(sizeof(float2) * 2 * AXIS_MAX_CTAS * LT_ROWS);
     l.o = take(sizeof(float) * 2 * AXIS_MAX_CTAS * LT_ROWS * LC);
     l.total = at;
@@ -666,8 +684,8 @@ cudaError_t lt_setup() {
 template <int KV>
 int launch_merge(const typename Lt<KV>::Args &a, int ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.num_query_tokens * a.H));
-    cfg.blockDim = dim3(512);
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(a.query_start ? LT_ROWS : std::min(LT_ROWS, a.H)));
+    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // launched while the first kernel drains
@@ -704,7 +722,7 @@ int run_latent(void *out, const void *query, const void *cache, const int32_t *b
                const int32_t *context_lens, const int32_t *query_start, int num_seqs, int num_query_tokens,
                int num_heads, int block_size, int64_t num_blocks, int max_blocks_per_seq, int max_context_len,
                float scale, uint8_t *ws, cudaStream_t st) {
-    const LtLayout lay = lt_layout(num_seqs);
+    const LtLayout lay = lt_layout();
     typename Lt<KV>::Args a{};
     a.out = static_cast<uint16_t *>(out);
     a.query = static_cast<const uint16_t *>(query);
@@ -723,7 +741,7 @@ int run_latent(void *out, const void *query, const void *cache, const int32_t *b
     a.scale_log2 = scale * 1.4426950408889634f;
     a.wait_limit = pipeline_wait_limit();
     a.status = reinterpret_cast<int *>(ws + lay.status);
-    a.unit_base = reinterpret_cast<long long *>(ws + lay.unit_base);
+    a.cuts = reinterpret_cast<Cut *>(ws + lay.cuts);
     a.ml = reinterpret_cast<float2 *>(ws + lay.ml);
     a.o = reinterpret_cast<float *>(ws + lay.o);
     return launch_latent<KV>(a, st);
@@ -737,7 +755,7 @@ using namespace pa;
 extern "C" size_t pa_latent_attention_workspace_size(int num_seqs, int num_query_tokens, int num_heads,
                                                      int max_context_len) {
     if (num_seqs < 0 || num_query_tokens < 0 || num_heads <= 0 || num_heads > 128 || max_context_len < 0) return 0;
-    return lt_layout(num_seqs).total;
+    return lt_layout().total;
 }
 
 extern "C" int pa_latent_attention(void *out, const void *query, const void *cache, const int32_t *block_tables,

@@ -45,7 +45,7 @@ struct ExpandedArgs {
     long long wait_limit;
     // workspace
     int *status;            // [AXIS_MAX_CTAS] nonzero: the CTA gave up waiting
-    long long *unit_base;   // [num_seqs + 1]
+    Cut *cuts;              // [AXIS_MAX_CTAS]
     float2 *ml;             // [2 AXIS_MAX_CTAS][EX_ROWS] maximum (log2 units) and sum of a partial row
     float *o;               // [2 AXIS_MAX_CTAS][EX_ROWS][EV] its unnormalised output
 
@@ -82,6 +82,9 @@ struct ExpandedArgs {
     }
     __device__ __forceinline__ int row_tiles(const Seq &w, int r) const {
         return tiles_of(w, min(w.T, (r % w.per_head + 1) * EX_ROWS));
+    }
+    __device__ __forceinline__ int cut_rows(const Seq &w, int r) const {
+        return min(EX_ROWS, w.T - r % w.per_head * EX_ROWS);
     }
     __device__ __forceinline__ bool starts_ok() const {
         const bool q = offsets_ok(query_start, num_seqs, num_query_tokens);
@@ -449,6 +452,8 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     }
     make_plan(a, &c.plan, c.warp_sums);
     const Plan plan = c.plan;
+    fill_idle_rows<EV / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
+                           KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
         if (warp == 2) {
             tmem_alloc(smem_u32(&c.tmem), EX_TMEM);
@@ -482,39 +487,35 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// One warp per output row: rows of a cut row tile from their pieces' partial
-// rows, NaN for a sequence with more new tokens than keys (and for every row
-// when a CTA of the first kernel gave up).
+// Rows of the cut row tiles from their pieces' partial rows, a warp each:
+// blockIdx.x is the CTA whose range begins in the row tile.  When a CTA of the
+// first kernel gave up, every row becomes NaN.
 template <int KV>
 __global__ void __launch_bounds__(256) expanded_merge_kernel(const ExpandedArgs a, int ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int failed = 0;
-    for (int i = threadIdx.x; i < ctas; i += blockDim.x) failed |= a.status[i];
-    failed = __syncthreads_or(failed);
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
-    const int lane = threadIdx.x & 31;
-    const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5);
-    if (row >= (long long)a.num_query_tokens * a.H) return;
-    const int qt = (int)(row / a.H), head = (int)(row - (long long)qt * a.H);
-    const long long total = a.unit_base[a.num_seqs];
-    uint2 *out = reinterpret_cast<uint2 *>(a.out + row * EV) + lane;
-    const int seq = total >= 0 ? sequence_of(a.query_start, a.num_seqs, qt) : 0;
-    ExpandedArgs::Seq w{};
-    if (total >= 0) w = a.seq_work(seq);
-    if (failed || total < 0 || !w.valid) {
-        const uint32_t x = (uint32_t)out_bits<KV>(__int_as_float(0x7fc00000)) * 0x10001u;
-        *out = make_uint2(x, x);
+    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const Cut cut = a.cuts[cta];
+    const bool failed = any_gave_up(a.status, ctas);
+    if (cta == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
+    if (failed) {
+        const long long n = (long long)a.num_query_tokens * a.H * (EV / 8);
+        if (blockIdx.y == 0)
+            fill_rows(a.out, range_begin(n, cta, ctas), range_begin(n, cta + 1, ctas),
+                      KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
         return;
     }
-    const int tok = qt - w.q0, j = tok / EX_ROWS, m = tok % EX_ROWS;
-    // what the row's half sees: the first half of a full row tile, or its last rows
-    const int rows = m < EX_HALF && w.T - j * EX_ROWS > EX_HALF ? j * EX_ROWS + EX_HALF : min(w.T, (j + 1) * EX_ROWS);
-    const Pieces pc(a.unit_base[seq] + a.start(w, head * w.per_head + j), a.tiles_of(w, rows), ExpandedArgs::COST, total,
-                    ctas);
-    if (pc.k0 == pc.k1) return;   // finished by one CTA
+    const int m = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (m >= cut.rows) return;
+    const ExpandedArgs::Seq w = a.seq_work(cut.seq);
+    const int first = cut.r % w.per_head * EX_ROWS;
+    // what the row's half sees: the first half of a row tile of two, or its last rows
+    const int rows = m < EX_HALF && cut.rows > EX_HALF ? first + EX_HALF : first + cut.rows;
+    const Pieces pc(cut, cta, a.tiles_of(w, rows), ExpandedArgs::COST, ctas);
+    if (pc.k0 == pc.k1) return;   // this half was finished by one CTA
     float M = -INFINITY;
-#pragma unroll 8
-    for (int k = pc.k0; k <= pc.k1; ++k) M = fmaxf(M, a.ml[pc.slot(k) * EX_ROWS + m].x);
+    for (int k = pc.k0 + lane; k <= pc.k1; k += 32) M = fmaxf(M, a.ml[pc.slot(k) * EX_ROWS + m].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     const float mu = M == -INFINITY ? 0.f : M;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
@@ -531,17 +532,19 @@ __global__ void __launch_bounds__(256) expanded_merge_kernel(const ExpandedArgs 
         acc.w = fmaf(o.w, wt, acc.w);
     }
     const float inv = 1.f / l;
-    *out = make_uint2((uint32_t)out_bits<KV>(acc.x * inv) | ((uint32_t)out_bits<KV>(acc.y * inv) << 16),
-                      (uint32_t)out_bits<KV>(acc.z * inv) | ((uint32_t)out_bits<KV>(acc.w * inv) << 16));
+    const long long row = (long long)(w.q0 + first + m) * a.H + cut.r / w.per_head;
+    *(reinterpret_cast<uint2 *>(a.out + row * EV) + lane) =
+        make_uint2((uint32_t)out_bits<KV>(acc.x * inv) | ((uint32_t)out_bits<KV>(acc.y * inv) << 16),
+                   (uint32_t)out_bits<KV>(acc.z * inv) | ((uint32_t)out_bits<KV>(acc.w * inv) << 16));
 }
 
 // ------------------------------------------------------------------ launch
 
 struct ExLayout {
-    size_t status, unit_base, ml, o, total;
+    size_t status, cuts, ml, o, total;
 };
 
-ExLayout ex_layout(int num_seqs) {
+ExLayout ex_layout() {
     ExLayout l;
     size_t at = 256;   // header
     auto take = [&](size_t bytes) {
@@ -550,7 +553,7 @@ ExLayout ex_layout(int num_seqs) {
         return p;
     };
     l.status = take(sizeof(int) * AXIS_MAX_CTAS);
-    l.unit_base = take(sizeof(long long) * ((size_t)num_seqs + 1));
+    l.cuts = take(sizeof(Cut) * AXIS_MAX_CTAS);
     l.ml = take(sizeof(float2) * 2 * AXIS_MAX_CTAS * EX_ROWS);
     l.o = take(sizeof(float) * 2 * AXIS_MAX_CTAS * EX_ROWS * EV);
     l.total = at;
@@ -603,7 +606,7 @@ int launch_expanded(const ExpandedArgs &a, const CUtensorMap &tmq, const CUtenso
     expanded_kernel<KV><<<ctas, EX_THREADS, EX_SMEM, st>>>(tmq, tmk, tmr, tmv, a);
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(((long long)a.num_query_tokens * a.H + 7) / 8));
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((std::min(EX_ROWS, a.num_query_tokens) + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -621,7 +624,7 @@ using namespace pa;
 
 extern "C" size_t pa_latent_attention_expanded_workspace_size(int num_seqs, int num_query_tokens, int num_heads) {
     if (num_seqs < 0 || num_query_tokens < 0 || num_heads <= 0) return 0;
-    return ex_layout(num_seqs).total;
+    return ex_layout().total;
 }
 
 extern "C" int pa_latent_attention_expanded(void *out, const void *query, const void *k_nope, const void *k_rope,
@@ -645,7 +648,7 @@ extern "C" int pa_latent_attention_expanded(void *out, const void *query, const 
         workspace_bytes < pa_latent_attention_expanded_workspace_size(num_seqs, num_query_tokens, num_heads))
         return PA_ERR_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const ExLayout lay = ex_layout(num_seqs);
+    const ExLayout lay = ex_layout();
     ExpandedArgs a{};
     a.out = static_cast<uint16_t *>(out);
     a.query_start = query_start;
@@ -658,7 +661,7 @@ extern "C" int pa_latent_attention_expanded(void *out, const void *query, const 
     a.scale_log2 = scale * 1.4426950408889634f;
     a.wait_limit = pipeline_wait_limit();
     a.status = reinterpret_cast<int *>(ws + lay.status);
-    a.unit_base = reinterpret_cast<long long *>(ws + lay.unit_base);
+    a.cuts = reinterpret_cast<Cut *>(ws + lay.cuts);
     a.ml = reinterpret_cast<float2 *>(ws + lay.ml);
     a.o = reinterpret_cast<float *>(ws + lay.o);
     // without keys no row tile has work and no copy is made: any base will do

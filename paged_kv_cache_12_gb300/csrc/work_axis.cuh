@@ -19,8 +19,9 @@
 //   row_tiles(w, r)         KV tiles of row tile r
 //   starts_ok()             whether the row offsets are in order (called by
 //                           every thread of the block)
-//   num_seqs, unit_base     sequences; [num_seqs + 1] their first units, written
-//                           by CTA 0 for the merge (-1: offsets out of order)
+//   num_seqs, cuts          sequences; [AXIS_MAX_CTAS] what a cut row tile's merge
+//                           needs, written by the CTA whose range begins in it
+//   cut_row, cut_rows       (w, r): a row tile's first output row and its rows
 #pragma once
 
 #include <stdint.h>
@@ -32,7 +33,17 @@ constexpr int AXIS_MAX_CTAS = 160;   // CTAs of a launch: one per SM, at most th
 
 struct Plan {
     long long u0, u1, base;   // this CTA's range; first unit of sequence seq
+    long long total;          // units of the axis (0 too if the row offsets are out of order)
     int seq;                  // the sequence in which the range begins
+    int ok;                   // the row offsets are in order
+};
+
+// A row tile whose first two pieces are CTA k - 1's and CTA k's, in cuts[k];
+// rows = 0 where there is none (the range begins with a row tile, or in one
+// that an earlier range cuts as well).
+struct Cut {
+    long long s, total;   // its first unit; units of the axis
+    int seq, r, rows, ntiles;
 };
 
 // First unit of CTA k's range; `parts` = min(CTAs, total) CTAs have one, of at
@@ -58,6 +69,17 @@ __device__ __forceinline__ int sequence_of(const int32_t *start, int n, int row)
     return lo;
 }
 
+// The last row tile of a sequence that starts at or before unit u of it.
+template <class P>
+__device__ __forceinline__ int row_tile_at(const P &a, const typename P::Seq &w, long long u) {
+    int r = 0, hi = w.rts;
+    while (hi - r > 1) {
+        const int mid = (r + hi) >> 1;
+        if (a.start(w, mid) <= u) r = mid; else hi = mid;
+    }
+    return r;
+}
+
 // This block's plan (warp_sums: one number per warp, in shared memory).
 template <class P>
 __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *warp_sums) {
@@ -78,7 +100,6 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         if (lane >= d) upto += x;
     }
     if (lane == 31) warp_sums[warp] = upto;
-    if (threadIdx.x == 0) plan->seq = a.num_seqs;
     __syncthreads();
     long long before = 0, total = 0;
     for (int k = 0; k < nwarps; ++k) {
@@ -92,6 +113,12 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
     if (threadIdx.x == 0) {
         plan->u0 = u0;
         plan->u1 = u1;
+        plan->total = total;
+        plan->ok = ok;
+        if (u0 >= u1) {
+            a.cuts[cta].rows = 0;
+            plan->seq = a.num_seqs;
+        }
     }
     if (u0 < u1 && begin <= u0 && u0 < end) {   // one thread
         long long s = begin;
@@ -103,14 +130,19 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         }
         plan->seq = i;
         plan->base = s;
-    }
-    if (cta == 0) {
-        long long s = begin;
-        for (int i = i0; i < i1; ++i) {
-            a.unit_base[i] = ok ? s : -1;
-            if (ok) s += units(i);
-        }
-        if (threadIdx.x == 0) a.unit_base[a.num_seqs] = ok ? total : -1;
+        // the row tile in which the range begins: cut here if a KV tile of it lies on either side
+        const typename P::Seq w = a.seq_work(i);
+        const int r = row_tile_at(a, w, u0 - s);
+        Cut cut;
+        cut.s = s + a.start(w, r);
+        cut.total = total;
+        cut.seq = i;
+        cut.r = r;
+        cut.ntiles = a.row_tiles(w, r);
+        const long long first = cut.s + P::COST;
+        const bool here = cta > 0 && first < u0 && u0 < first + cut.ntiles && range_begin(total, cta - 1, parts) <= first;
+        cut.rows = here ? a.cut_rows(w, r) : 0;
+        a.cuts[cta] = cut;
     }
     __syncthreads();
 }
@@ -128,12 +160,7 @@ struct Walk {
         local = -1;
         if (u0 >= u1) return;
         w = a.seq_work(seq);
-        int hi = w.rts;   // the last row tile that starts at or before u0
-        while (hi - r > 1) {
-            const int mid = (r + hi) >> 1;
-            if (base + a.start(w, mid) <= u0) r = mid; else hi = mid;
-        }
-        --r;
+        r = row_tile_at(a, w, u0 - base) - 1;
     }
     // The next piece; false at the end of the range.
     __device__ bool next() {
@@ -162,24 +189,51 @@ struct Walk {
     __device__ int slot() const { return 2 * (int)blockIdx.x + (s < u0 ? 0 : 1); }
 };
 
-// The CTAs k0 .. k1 that hold the pieces of the row tile of `ntiles` KV tiles
-// at unit s, and the slot of each one's partial rows.
+// The pieces of a cut row tile that hold its first `ntiles` KV tiles: CTAs k0
+// (= the cut's - 1) .. k1, and the slot of each one's partial rows.
 struct Pieces {
     int k0, k1, parts;
     long long s, total;
-    __device__ Pieces(long long s_, int ntiles, int cost, long long total_, int ctas) : s(s_), total(total_) {
+    __device__ Pieces(const Cut &cut, int cta, int ntiles, int cost, int ctas) : k0(cta - 1), s(cut.s), total(cut.total) {
         parts = (int)min((long long)ctas, total);
-        k0 = cta_of(s + cost);
-        k1 = cta_of(s + cost + ntiles - 1);
-    }
-    __device__ int cta_of(long long u) const {
-        int k = (int)(u * parts / total);
-        while (range_begin(total, k + 1, parts) <= u) ++k;
-        while (range_begin(total, k, parts) > u) --k;
-        return k;
+        const long long last = s + cost + ntiles - 1;
+        k1 = (int)(last * parts / total);
+        while (range_begin(total, k1 + 1, parts) <= last) ++k1;
+        while (range_begin(total, k1, parts) > last) --k1;
     }
     __device__ int slot(int k) const { return 2 * k + (s < range_begin(total, k, parts) ? 0 : 1); }
 };
+
+// Whether a CTA of the first kernel gave up (called by the whole block).
+__device__ __forceinline__ bool any_gave_up(const int *status, int ctas) {
+    int failed = 0;
+    for (int i = threadIdx.x; i < ctas; i += blockDim.x) failed |= status[i];
+    return __syncthreads_or(failed);
+}
+
+// The block writes `bits` to 16-byte vectors [from, to) of out.
+__device__ __forceinline__ void fill_rows(uint16_t *out, long long from, long long to, uint32_t bits) {
+    uint4 *o = reinterpret_cast<uint4 *>(out);
+    for (long long i = from + threadIdx.x; i < to; i += blockDim.x) o[i] = make_uint4(bits, bits, bits, bits);
+}
+
+// Rows that no KV tile makes: zeros for an empty context, NaN for an invalid
+// sequence, and NaN for every row when the row offsets are out of order.  Each
+// CTA takes every gridDim-th sequence.  VEC: 16-byte vectors of an output row.
+template <int VEC, class P>
+__device__ __forceinline__ void fill_idle_rows(const P &a, const Plan &plan, uint16_t *out, long long all_rows,
+                                               uint32_t nan_pair) {
+    if (!plan.ok) {
+        const long long n = all_rows * VEC;
+        fill_rows(out, range_begin(n, blockIdx.x, gridDim.x), range_begin(n, blockIdx.x + 1, gridDim.x), nan_pair);
+        return;
+    }
+    for (int i = blockIdx.x; i < a.num_seqs; i += gridDim.x) {
+        const typename P::Seq w = a.seq_work(i);
+        if (w.rts == 0 && w.T > 0)
+            fill_rows(out, (long long)w.q0 * a.H * VEC, ((long long)w.q0 + w.T) * a.H * VEC, w.valid ? 0u : nan_pair);
+    }
+}
 
 }  // namespace
 }  // namespace pa
