@@ -451,42 +451,56 @@ def pa_workspace_status(workspace, stream=None) -> int:
 
 # ---------------------------------------------------------------- latent cache
 
-def _tensors(where, dev, *specs):
-    """Check (tensor, name, dtypes, dims, contiguous) entries: CUDA tensors on
-    one device; those not contiguous need unit stride in the last dimension."""
-    for t, name, dtypes, ndim, dense in specs:
-        if t.device != dev or not t.is_cuda:
-            raise ValueError(f"{where}: {name} must be a CUDA tensor on the device of the others ({dev})")
-        if t.dtype not in dtypes or t.dim() != ndim:
-            raise ValueError(f"{where}: {name}: expected a {ndim}-d tensor of {dtypes[0]}, got {t.dim()}-d {t.dtype}")
-        if dense and not t.is_contiguous() or not dense and t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{where}: {name} must be contiguous" + ("" if dense else " in its last dimension"))
+def _need_on(where, dev, t, name, dtype, ndim, dense=True):
+    """Check one tensor: on CUDA device `dev` (an index), of the type and number
+    of dimensions, contiguous (with dense=False: unit stride in the last
+    dimension).  Decode steps make these calls per layer, so the test is one
+    expression and the message is made only when it fails."""
+    if t.get_device() != dev or dev < 0 or t.dtype is not dtype or t.dim() != ndim or \
+            not (t.is_contiguous() if dense else t.stride(-1) == 1 or t.shape[-1] <= 1 or t.numel() == 0):
+        raise ValueError(f"{where}: {name}: expected a {ndim}-d {dtype} tensor on CUDA device {dev}, contiguous"
+                         f"{'' if dense else ' in its last dimension'}; got {t.dim()}-d {t.dtype} on {t.device}, strides "
+                         f"{t.stride()}")
+
+
+_raw_stream = None
 
 
 def _run(where, dev, stream, *args):
-    """Call the library on device `dev` and the given (or its current) stream."""
+    """Call the library on device `dev` (an index) and the given stream (default:
+    that device's current torch stream)."""
+    global _raw_stream
     import torch
-    f = getattr(lib(), where)
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(f(*args, h), where)
+        if _raw_stream is None:   # the handle alone, without a Stream object around it, where torch offers it
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+                (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        h = _raw_stream(dev)
+    else:
+        h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    f = getattr(_lib or lib(), where)
+    if dev == torch.cuda.current_device():
+        rc = f(*args, h)
     else:
         with torch.cuda.device(dev):
-            _check(f(*args, h), where)
+            rc = f(*args, h)
+    if rc != PA_OK:
+        raise PAError(rc, where)
 
 
 def _latent_cache(where, cache):
-    """(PA_KV_*, torch dtype of the rows that go in and come out) of a latent cache tensor."""
+    """(PA_KV_*, torch dtype of the rows that go in and come out, device index,
+    blocks, block size) of a latent cache tensor."""
     import torch
-    if cache.dim() == 3:
-        if cache.dtype == torch.uint8 and cache.shape[2] == PA_LATENT_ROW_FP8_BYTES:
-            return PA_KV_FP8_E4M3, torch.bfloat16
-        if cache.dtype in (torch.float16, torch.bfloat16) and cache.shape[2] == PA_LATENT_ROW:
-            return (PA_KV_F16 if cache.dtype == torch.float16 else PA_KV_BF16), cache.dtype
-    raise ValueError(f"{where}: a latent cache is [num_blocks, block_size, {PA_LATENT_ROW}] float16 or bfloat16, or "
-                     f"[num_blocks, block_size, {PA_LATENT_ROW_FP8_BYTES}] uint8")
+    dt = cache.dtype
+    if cache.dim() == 3 and cache.is_contiguous() and cache.is_cuda:
+        nb, bs, w = cache.shape
+        if dt is torch.uint8 and w == PA_LATENT_ROW_FP8_BYTES:
+            return PA_KV_FP8_E4M3, torch.bfloat16, cache.get_device(), nb, bs
+        if w == PA_LATENT_ROW and (dt is torch.bfloat16 or dt is torch.float16):
+            return (PA_KV_BF16 if dt is torch.bfloat16 else PA_KV_F16), dt, cache.get_device(), nb, bs
+    raise ValueError(f"{where}: a latent cache is a contiguous CUDA tensor [num_blocks, block_size, {PA_LATENT_ROW}] "
+                     f"float16 or bfloat16, or [num_blocks, block_size, {PA_LATENT_ROW_FP8_BYTES}] uint8")
 
 
 def pa_latent_write(latent, rope, slot_mapping, cache, stream=None):
@@ -495,29 +509,29 @@ def pa_latent_write(latent, rope, slot_mapping, cache, stream=None):
     quantised as they go into an FP8 cache.  latent and rope may be slices of
     wider rows (unit stride in the last dimension)."""
     import torch
-    kv, dt = _latent_cache("pa_latent_write", cache)
+    where = "pa_latent_write"
+    kv, dt, dev, nb, bs = _latent_cache(where, cache)
+    _need_on(where, dev, latent, "latent", dt, 2, False)
+    _need_on(where, dev, rope, "rope", dt, 2, False)
+    _need_on(where, dev, slot_mapping, "slot_mapping", torch.int64, 1)
     n = latent.shape[0]
-    _tensors("pa_latent_write", cache.device, (cache, "cache", (cache.dtype,), 3, True),
-             (latent, "latent", (dt,), 2, False), (rope, "rope", (dt,), 2, False),
-             (slot_mapping, "slot_mapping", (torch.int64,), 1, True))
     if latent.shape[1] != PA_LATENT_DIM or rope.shape != (n, PA_LATENT_ROPE_DIM) or slot_mapping.shape[0] != n:
         raise ValueError("pa_latent_write: shape mismatch")
     # one row (or none) has no stride of its own
     sl, sr = (latent.stride(0), rope.stride(0)) if n > 1 else (PA_LATENT_DIM, PA_LATENT_ROPE_DIM)
-    _run("pa_latent_write", cache.device, stream, latent.data_ptr(), rope.data_ptr(), slot_mapping.data_ptr(),
-         cache.data_ptr(), n, sl, sr, cache.shape[1], cache.shape[0], kv)
+    _run(where, dev, stream, latent.data_ptr(), rope.data_ptr(), slot_mapping.data_ptr(), cache.data_ptr(), n, sl, sr,
+         bs, nb, kv)
 
 
 def pa_latent_block_copy(cache, pairs, stream=None):
     """Copy every (src, dst) block pair of int64 ``pairs`` [n, 2] of a latent cache."""
     import torch
-    kv, _ = _latent_cache("pa_latent_block_copy", cache)
-    _tensors("pa_latent_block_copy", cache.device, (cache, "cache", (cache.dtype,), 3, True),
-             (pairs, "pairs", (torch.int64,), 2, True))
+    where = "pa_latent_block_copy"
+    kv, _, dev, nb, bs = _latent_cache(where, cache)
+    _need_on(where, dev, pairs, "pairs", torch.int64, 2)
     if pairs.shape[1] != 2:
         raise ValueError("pa_latent_block_copy: shape mismatch")
-    _run("pa_latent_block_copy", cache.device, stream, cache.data_ptr(), pairs.data_ptr(), pairs.shape[0],
-         cache.shape[1], cache.shape[0], kv)
+    _run(where, dev, stream, cache.data_ptr(), pairs.data_ptr(), pairs.shape[0], bs, nb, kv)
 
 
 def pa_latent_read(out, cache, block_tables, row_start, first_token=None, stream=None):
@@ -525,18 +539,20 @@ def pa_latent_read(out, cache, block_tables, row_start, first_token=None, stream
     be strided) = token first_token[i] + j (0 + j without first_token) of
     sequence i; rows from row_start[-1] on are left as they are."""
     import torch
-    kv, dt = _latent_cache("pa_latent_read", cache)
-    i32 = (torch.int32,)
-    _tensors("pa_latent_read", cache.device, (cache, "cache", (cache.dtype,), 3, True), (out, "out", (dt,), 2, False),
-             (block_tables, "block_tables", i32, 2, True), (row_start, "row_start", i32, 1, True),
-             *(((first_token, "first_token", i32, 1, True),) if first_token is not None else ()))
-    n, b = out.shape[0], block_tables.shape[0]
-    if out.shape[1] != PA_LATENT_ROW or row_start.shape[0] != b + 1 or \
-            (first_token is not None and first_token.shape[0] != b):
+    where, i32 = "pa_latent_read", torch.int32
+    kv, dt, dev, nb, bs = _latent_cache(where, cache)
+    _need_on(where, dev, out, "out", dt, 2, False)
+    _need_on(where, dev, block_tables, "block_tables", i32, 2)
+    _need_on(where, dev, row_start, "row_start", i32, 1)
+    if first_token is not None:
+        _need_on(where, dev, first_token, "first_token", i32, 1)
+    n, w = out.shape
+    b, mb = block_tables.shape
+    if w != PA_LATENT_ROW or row_start.shape[0] != b + 1 or (first_token is not None and first_token.shape[0] != b):
         raise ValueError("pa_latent_read: shape mismatch")
-    _run("pa_latent_read", cache.device, stream, out.data_ptr(), cache.data_ptr(), block_tables.data_ptr(),
-         row_start.data_ptr(), None if first_token is None else first_token.data_ptr(), b, n,
-         out.stride(0) if n > 1 else PA_LATENT_ROW, cache.shape[1], cache.shape[0], block_tables.shape[1], kv)
+    _run(where, dev, stream, out.data_ptr(), cache.data_ptr(), block_tables.data_ptr(), row_start.data_ptr(),
+         None if first_token is None else first_token.data_ptr(), b, n, out.stride(0) if n > 1 else PA_LATENT_ROW, bs,
+         nb, mb, kv)
 
 
 def pa_latent_attention_workspace_size(num_seqs, num_query_tokens, num_heads, max_context_len) -> int:
@@ -555,22 +571,23 @@ def pa_latent_attention(out, query, cache, block_tables, context_lens, scale, ma
     query_start one row per sequence (decode); with it rows query_start[i] ..
     query_start[i + 1] - 1 are sequence i's last new tokens, causal."""
     import torch
-    kv, dt = _latent_cache("pa_latent_attention", cache)
-    i32 = (torch.int32,)
-    _tensors("pa_latent_attention", cache.device, (cache, "cache", (cache.dtype,), 3, True),
-             (out, "out", (dt,), 3, True), (query, "query", (dt,), 3, True),
-             (block_tables, "block_tables", i32, 2, True), (context_lens, "context_lens", i32, 1, True),
-             (workspace, "workspace", (torch.uint8,), 1, True),
-             *(((query_start, "query_start", i32, 1, True),) if query_start is not None else ()))
+    where, i32 = "pa_latent_attention", torch.int32
+    kv, dt, dev, nb, bs = _latent_cache(where, cache)
+    _need_on(where, dev, out, "out", dt, 3)
+    _need_on(where, dev, query, "query", dt, 3)
+    _need_on(where, dev, block_tables, "block_tables", i32, 2)
+    _need_on(where, dev, context_lens, "context_lens", i32, 1)
+    _need_on(where, dev, workspace, "workspace", torch.uint8, 1)
+    if query_start is not None:
+        _need_on(where, dev, query_start, "query_start", i32, 1)
     nq, h, w = query.shape
-    b = context_lens.shape[0]
-    if w != PA_LATENT_ROW or out.shape != (nq, h, PA_LATENT_DIM) or block_tables.shape[0] != b or \
+    b, mb = block_tables.shape
+    if w != PA_LATENT_ROW or out.shape != (nq, h, PA_LATENT_DIM) or context_lens.shape[0] != b or \
             (nq != b if query_start is None else query_start.shape[0] != b + 1):
         raise ValueError("pa_latent_attention: shape mismatch")
-    _run("pa_latent_attention", cache.device, stream, out.data_ptr(), query.data_ptr(), cache.data_ptr(),
-         block_tables.data_ptr(), context_lens.data_ptr(), None if query_start is None else query_start.data_ptr(), b,
-         nq, h, cache.shape[1], cache.shape[0], block_tables.shape[1], int(max_context_len), float(scale), kv,
-         workspace.data_ptr(), workspace.numel())
+    _run(where, dev, stream, out.data_ptr(), query.data_ptr(), cache.data_ptr(), block_tables.data_ptr(),
+         context_lens.data_ptr(), None if query_start is None else query_start.data_ptr(), b, nq, h, bs, nb, mb,
+         int(max_context_len), float(scale), kv, workspace.data_ptr(), workspace.shape[0])
 
 
 def pa_latent_attention_expanded_workspace_size(num_seqs, num_query_tokens, num_heads) -> int:
@@ -588,14 +605,18 @@ def pa_latent_attention_expanded(out, query, k_nope, k_rope, value, query_start,
     out [nq, heads, 128]; sequence i has rows kv_start[i] .. kv_start[i + 1] - 1
     of the keys, its last new tokens rows query_start[i] .. of the queries."""
     import torch
-    where = "pa_latent_attention_expanded"
-    dt, i32 = (query.dtype,), (torch.int32,)
-    if query.dtype not in (torch.float16, torch.bfloat16):
+    where, i32 = "pa_latent_attention_expanded", torch.int32
+    dt, dev = query.dtype, query.get_device()
+    if dt is not torch.float16 and dt is not torch.bfloat16:
         raise ValueError(f"{where}: query must be float16 or bfloat16")
-    _tensors(where, query.device, (query, "query", dt, 3, True), (out, "out", dt, 3, True),
-             (k_nope, "k_nope", dt, 3, False), (value, "value", dt, 3, False), (k_rope, "k_rope", dt, 2, False),
-             (query_start, "query_start", i32, 1, True), (kv_start, "kv_start", i32, 1, True),
-             (workspace, "workspace", (torch.uint8,), 1, True))
+    _need_on(where, dev, query, "query", dt, 3)
+    _need_on(where, dev, out, "out", dt, 3)
+    _need_on(where, dev, k_nope, "k_nope", dt, 3, False)
+    _need_on(where, dev, value, "value", dt, 3, False)
+    _need_on(where, dev, k_rope, "k_rope", dt, 2, False)
+    _need_on(where, dev, query_start, "query_start", i32, 1)
+    _need_on(where, dev, kv_start, "kv_start", i32, 1)
+    _need_on(where, dev, workspace, "workspace", torch.uint8, 1)
     nq, h, w = query.shape
     nk = k_nope.shape[0]
     if w != 192 or out.shape != (nq, h, 128) or k_nope.shape != (nk, h, 128) or value.shape != (nk, h, 128) or \
@@ -607,10 +628,10 @@ def pa_latent_attention_expanded(out, query, k_nope, k_rope, value, query_start,
         return (t.stride(0) if nk > 1 else h * head), head
     kt, kh = strides(k_nope)
     vt, vh = strides(value)
-    _run(where, query.device, stream, out.data_ptr(), query.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(),
-         value.data_ptr(), query_start.data_ptr(), kv_start.data_ptr(), query_start.shape[0] - 1, nq, nk, h, kt, kh,
-         k_rope.stride(0) if nk > 1 else 64, vt, vh, float(scale),
-         PA_KV_F16 if query.dtype == torch.float16 else PA_KV_BF16, workspace.data_ptr(), workspace.numel())
+    _run(where, dev, stream, out.data_ptr(), query.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), value.data_ptr(),
+         query_start.data_ptr(), kv_start.data_ptr(), query_start.shape[0] - 1, nq, nk, h, kt, kh,
+         k_rope.stride(0) if nk > 1 else 64, vt, vh, float(scale), PA_KV_F16 if dt is torch.float16 else PA_KV_BF16,
+         workspace.data_ptr(), workspace.shape[0])
 
 
 # ---------------------------------------------------------------- speculative steps
@@ -624,26 +645,32 @@ def pa_verify_drafts(accepted, tokens, target_probs, draft_probs, draft_tokens, 
     probability one) are float32, float16 or bfloat16 rows; sequence i's drafts
     are draft_start[i] .. draft_start[i + 1] - 1."""
     import torch
-    where = "pa_verify_drafts"
-    kinds = {torch.float32: PA_PROBS_F32, torch.float16: PA_PROBS_F16, torch.bfloat16: PA_PROBS_BF16}
-    if target_probs.dtype not in kinds:
+    where, i32, f32 = "pa_verify_drafts", torch.int32, torch.float32
+    dt, dev = target_probs.dtype, target_probs.get_device()
+    kind = PA_PROBS_F32 if dt is f32 else PA_PROBS_F16 if dt is torch.float16 else \
+        PA_PROBS_BF16 if dt is torch.bfloat16 else -1
+    if kind < 0:
         raise ValueError(f"{where}: target_probs must be float32, float16 or bfloat16")
-    dt, i32, f32 = (target_probs.dtype,), (torch.int32,), (torch.float32,)
-    _tensors(where, target_probs.device, (target_probs, "target_probs", dt, 2, False),
-             (accepted, "accepted", i32, 1, True), (tokens, "tokens", i32, 2, True),
-             (draft_tokens, "draft_tokens", i32, 1, True), (draft_start, "draft_start", i32, 1, True),
-             (uniform, "uniform", f32, 1, True), (sample_uniform, "sample_uniform", f32, 1, True),
-             *(((draft_probs, "draft_probs", dt, 2, False),) if draft_probs is not None else ()))
-    b, nd, v = accepted.shape[0], draft_tokens.shape[0], target_probs.shape[1]
-    if target_probs.shape[0] != nd + b or tokens.shape[0] != b or tokens.shape[1] < 1 or uniform.shape[0] != nd or \
+    _need_on(where, dev, target_probs, "target_probs", dt, 2, False)
+    _need_on(where, dev, accepted, "accepted", i32, 1)
+    _need_on(where, dev, tokens, "tokens", i32, 2)
+    _need_on(where, dev, draft_tokens, "draft_tokens", i32, 1)
+    _need_on(where, dev, draft_start, "draft_start", i32, 1)
+    _need_on(where, dev, uniform, "uniform", f32, 1)
+    _need_on(where, dev, sample_uniform, "sample_uniform", f32, 1)
+    if draft_probs is not None:
+        _need_on(where, dev, draft_probs, "draft_probs", dt, 2, False)
+    b, nd = accepted.shape[0], draft_tokens.shape[0]
+    rows, v = target_probs.shape
+    most = tokens.shape[1] - 1
+    if rows != nd + b or tokens.shape[0] != b or most < 0 or uniform.shape[0] != nd or \
             draft_start.shape[0] != b + 1 or sample_uniform.shape[0] != b or \
             (draft_probs is not None and draft_probs.shape != (nd, v)):
         raise ValueError(f"{where}: shape mismatch")
-    _run(where, target_probs.device, stream, accepted.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(),
+    _run(where, dev, stream, accepted.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(),
          None if draft_probs is None else draft_probs.data_ptr(), draft_tokens.data_ptr(), draft_start.data_ptr(),
-         uniform.data_ptr(), sample_uniform.data_ptr(), b, nd, tokens.shape[1] - 1, v,
-         target_probs.stride(0) if nd + b > 1 else v, draft_probs.stride(0) if draft_probs is not None and nd > 1 else v,
-         kinds[target_probs.dtype])
+         uniform.data_ptr(), sample_uniform.data_ptr(), b, nd, most, v, target_probs.stride(0) if rows > 1 else v,
+         draft_probs.stride(0) if draft_probs is not None and nd > 1 else v, kind)
 
 
 # ---------------------------------------------------------------- allocator

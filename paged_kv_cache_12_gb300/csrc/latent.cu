@@ -105,10 +105,14 @@ __global__ void __launch_bounds__(256) latent_write_fp8_kernel(const uint4 *__re
     }
 }
 
-// Read back: a CTA takes READ_ROWS consecutive rows of out.  One thread per
-// row finds its sequence by binary search in row_start and its slot through the
-// block table (a slot below 0 marks a NaN row), then all threads move vectors.
+// Read back: a CTA takes READ_ROWS consecutive rows of out.  It checks the
+// order of row_start (and keeps it in shared memory when it fits), one thread
+// per row finds its sequence by binary search and its slot through the block
+// table (a slot below 0 marks a NaN row), then all threads move vectors, eight
+// loads each on their way at once.  100,000 quantised rows of a ragged batch:
+// 45 us searching in global memory and loading vector by vector.
 constexpr int READ_ROWS = 32, READ_THREADS = 288;   // 288 = 4 x 72 vectors, so a thread keeps its column
+constexpr int READ_STARTS = 1024;
 
 template <bool F8>
 __global__ void __launch_bounds__(READ_THREADS) latent_read_kernel(
@@ -116,26 +120,28 @@ __global__ void __launch_bounds__(READ_THREADS) latent_read_kernel(
     const int32_t *__restrict__ row_start, const int32_t *__restrict__ first_token, int num_seqs, int num_rows,
     long long out_vecs, int block_size, long long num_blocks, int mbps, uint32_t nan_pair) {
     __shared__ long long slots[READ_ROWS];
-    __shared__ int bad;
+    __shared__ int starts[READ_STARTS + 1];
     const int base = blockIdx.x * READ_ROWS;
-    if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < num_seqs; i += blockDim.x) {
-        const int a = row_start[i], b = row_start[i + 1];
-        if (a < 0 || b < a || b > num_rows || (i == 0 && a != 0)) bad = 1;
+    const bool kept = num_seqs <= READ_STARTS;
+    bool ok = true;
+    for (int i = threadIdx.x; i <= num_seqs; i += blockDim.x) {
+        const int b = row_start[i], a = i ? row_start[i - 1] : 0;
+        if (b < a || b > num_rows || (i == 0 && b != 0)) ok = false;
+        if (kept) starts[i] = b;
     }
-    __syncthreads();
-    const int end = bad ? num_rows : min(num_rows, row_start[num_seqs]);
+    ok = __syncthreads_and(ok);
+    const int end = ok ? min(num_rows, kept ? starts[num_seqs] : row_start[num_seqs]) : num_rows;
     if (threadIdx.x < READ_ROWS) {
         const int row = base + threadIdx.x;
+        const int *from = kept ? starts : row_start;
         long long slot = -1;
-        if (!bad && row < end) {
+        if (ok && row < end) {
             int lo = 0, hi = num_seqs;   // the last i with row_start[i] <= row
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (row_start[mid] <= row) lo = mid; else hi = mid;
+                if (from[mid] <= row) lo = mid; else hi = mid;
             }
-            const long long t = (long long)row - row_start[lo] + (first_token ? first_token[lo] : 0);
+            const long long t = (long long)row - from[lo] + (first_token ? first_token[lo] : 0);
             if (t >= 0 && t < (long long)mbps * block_size) {
                 const long long blk = block_tables[(long long)lo * mbps + t / block_size];
                 if (blk >= 0 && blk < num_blocks) slot = blk * block_size + t % block_size;
@@ -144,29 +150,46 @@ __global__ void __launch_bounds__(READ_THREADS) latent_read_kernel(
         slots[threadIdx.x] = slot;
     }
     __syncthreads();
-    const int v = threadIdx.x % VROW;
+    const int v = threadIdx.x % VROW, r0 = threadIdx.x / VROW;
+    constexpr int STEP = READ_THREADS / VROW, N = READ_ROWS / STEP;
+    const int left = end - base;   // rows of this CTA
+    if constexpr (F8) {
+        if (v < VLAT) {
+            uint2 c[N];
+            float s[N];
 #pragma unroll
-    for (int k = 0; k < READ_ROWS / (READ_THREADS / VROW); ++k) {
-        const int r = threadIdx.x / VROW + k * (READ_THREADS / VROW);
-        if (base + r >= end) break;
-        const long long slot = slots[r];
-        uint4 x = make_uint4(nan_pair, nan_pair, nan_pair, nan_pair);
-        if (slot >= 0) {
-            if constexpr (F8) {
-                const uint8_t *row = cache + slot * LROW8;
-                if (v < VLAT) {
-                    const uint2 c = *reinterpret_cast<const uint2 *>(row + 8 * v);
-                    const float s = *reinterpret_cast<const float *>(row + L8_SCALE + 4 * (v / (LGROUP / 8)));
-                    const uint2 a = latent_codes_to_bf16(c.x, s), b = latent_codes_to_bf16(c.y, s);
-                    x = make_uint4(a.x, a.y, b.x, b.y);
-                } else {
-                    x = *reinterpret_cast<const uint4 *>(row + L8_ROPE + 16 * (v - VLAT));
+            for (int k = 0; k < N; ++k) {
+                const long long slot = slots[r0 + STEP * k];
+                c[k] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN codes
+                s[k] = 1.f;
+                if (slot >= 0) {
+                    const uint8_t *row = cache + slot * LROW8;
+                    c[k] = *reinterpret_cast<const uint2 *>(row + 8 * v);
+                    s[k] = *reinterpret_cast<const float *>(row + L8_SCALE + 4 * (v / (LGROUP / 8)));
                 }
-            } else {
-                x = *reinterpret_cast<const uint4 *>(cache + slot * (2 * LROW) + 16 * v);
             }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int r = r0 + STEP * k;
+                const uint2 a = latent_codes_to_bf16(c[k].x, s[k]), b = latent_codes_to_bf16(c[k].y, s[k]);
+                if (r < left) out[(long long)(base + r) * out_vecs + v] = make_uint4(a.x, a.y, b.x, b.y);
+            }
+            return;
         }
-        out[(long long)(base + r) * out_vecs + v] = x;
+    }
+    uint4 x[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const long long slot = slots[r0 + STEP * k];
+        x[k] = make_uint4(nan_pair, nan_pair, nan_pair, nan_pair);
+        if (slot >= 0)
+            x[k] = F8 ? *reinterpret_cast<const uint4 *>(cache + slot * LROW8 + L8_ROPE + 16 * (v - VLAT))
+                      : *reinterpret_cast<const uint4 *>(cache + slot * (2 * LROW) + 16 * v);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int r = r0 + STEP * k;
+        if (r < left) out[(long long)(base + r) * out_vecs + v] = x[k];
     }
 }
 
@@ -241,7 +264,7 @@ extern "C" int pa_latent_read(uint16_t *out, const void *cache, const int32_t *b
     if (num_seqs < 0 || num_rows < 0 || (num_seqs == 0 && num_rows > 0) || out_stride < LROW || out_stride % 8 != 0 ||
         block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || latent_row_bytes(kv_dtype) == 0)
         return PA_ERR_INVALID_ARG;
-    if (!latent_block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+    if (!latent_block_size_ok(block_size) || num_rows > (1 << 30)) return PA_ERR_UNSUPPORTED;
     if (num_rows == 0) return PA_OK;
     if (!out || !cache || !block_tables || !row_start || !aligned16(out) || !aligned16(cache))
         return PA_ERR_INVALID_ARG;

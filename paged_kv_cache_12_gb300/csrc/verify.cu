@@ -13,16 +13,19 @@
 // read whole, with the draft's row beside it: the kernel is bound by HBM on a
 // batch and by latency on a few sequences.  A cluster of eight CTAs takes a
 // sequence.  Every CTA finds the number of standing drafts (a warp, one draft a
-// lane), then the row's elements are summed in 512 groups, dealt to the
-// cluster's 64 warps in turn; the totals are exchanged through distributed
-// shared memory, and one warp reads the group again in which the running sum
-// passes the drawn height.
+// lane); the row's elements are summed in 64 slices, one a warp of the cluster;
+// one warp collects the 64 totals through distributed shared memory and finds
+// the slice in which the running sum passes the drawn height; its CTA reads
+// that slice again in eight parts, and a warp the part that passes.
 //
 // Sums: a draw is decided where a running sum over up to a hundred thousand
 // terms passes u * total, so sums are carried as an unevaluated pair of floats
-// (Knuth's two-sum, exact error terms), and joined in 64 bits over groups.  In
-// 64 bits throughout the adds alone would take longer than the reads: this
-// GPU's 64-bit rate is two per clock and SM.
+// (Knuth's two-sum, exact error terms) and compared in 64 bits.  Summing in 64
+// bits throughout costs more than the reads: this GPU's 64-bit rate is two a
+// clock and SM (512 totals of a row scanned in 64 bits by one warp took 14,000
+// clocks, more than a 128 KB slice of two rows).
+
+#include <climits>
 
 #include <cooperative_groups.h>
 
@@ -36,9 +39,10 @@ namespace {
 constexpr int VCTAS = 8;                       // CTAs of a sequence's cluster
 constexpr int VTHREADS = 256;
 constexpr int VWARPS = VTHREADS / 32;
-constexpr int VPER = 8;                        // groups per warp
-constexpr int VGROUPS = VCTAS * VWARPS * VPER; // groups of a row
+constexpr int VSLICES = VCTAS * VWARPS;        // slices of a row, two a lane of the collecting warp
 constexpr int VCHUNK = 128;                    // elements a warp reads at once, four a lane
+constexpr int VBATCH = 4;                      // chunks on their way at once
+static_assert(VSLICES == 64, "two totals a lane");
 
 struct VerifyArgs {
     int32_t *accepted, *tokens;
@@ -69,8 +73,29 @@ struct Sum2 {
         hi = t;
         lo = __fadd_rn(lo, __fadd_rn(r, e));
     }
+    __device__ __forceinline__ void add(const Sum2 &x) { add(x.hi, x.lo); }
     __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    __device__ __forceinline__ bool any() const { return hi > 0.f; }   // sums of weights >= 0
 };
+
+// The sum over the warp's lanes, the same in every lane.
+__device__ __forceinline__ Sum2 warp_sum(Sum2 x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        x.add(__shfl_xor_sync(0xffffffffu, x.hi, d), __shfl_xor_sync(0xffffffffu, x.lo, d));
+    return Sum2{__shfl_sync(0xffffffffu, x.hi, 0), __shfl_sync(0xffffffffu, x.lo, 0)};
+}
+
+// The sum over this lane and the ones before it.
+__device__ __forceinline__ Sum2 warp_scan(Sum2 x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const float h = __shfl_up_sync(0xffffffffu, x.hi, d), l = __shfl_up_sync(0xffffffffu, x.lo, d);
+        if (lane >= d) x.add(h, l);
+    }
+    return x;
+}
 
 // The weight max(p - q, 0) as its rounded value and rounding error; NaN is 0.
 __device__ __forceinline__ void weight(float p, float q, float &s, float &e) {
@@ -86,95 +111,88 @@ template <typename T>
 struct Weights {
     const T *p, *q;
     int out;
+    bool quads;   // both rows may be read four elements at a time
+    __device__ __forceinline__ Weights(const T *p_, const T *q_, int out_) : p(p_), q(q_), out(out_) {
+        quads = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & (4 * sizeof(T) - 1)) == 0;
+    }
     __device__ __forceinline__ void at(int v, float pv, float qv, float &s, float &e) const {
         weight(pv, qv, s, e);
         if (v == out) s = e = 0.f;
     }
 };
 
-// Sum of the warp's group [lo, hi): four elements a lane and step.  Every
-// element belongs to one lane; the sum's order is fixed.
-template <typename T, bool QUADS>
-__device__ __forceinline__ Sum2 group_sum(const Weights<T> &w, int lo, int hi) {
-    const int lane = threadIdx.x & 31;
-    Sum2 acc;
-    for (int base = lo; base < hi; base += VCHUNK) {
-        float p[4], q[4];
-        int v[4];
-        if (QUADS && base + VCHUNK <= hi) {
-            const int at = base + 4 * lane;
-            const Quad<T> a = *reinterpret_cast<const Quad<T> *>(w.p + at);
-            Quad<T> b{};
-            if (w.q) b = *reinterpret_cast<const Quad<T> *>(w.q + at);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = at + k, p[k] = prob(a.v[k]), q[k] = w.q ? prob(b.v[k]) : 0.f;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[k] = base + 32 * k + lane;
-                p[k] = v[k] < hi ? prob(w.p[v[k]]) : 0.f;
-                q[k] = w.q && v[k] < hi ? prob(w.q[v[k]]) : 0.f;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float s, e;
-            w.at(v[k], p[k], q[k], s, e);
-            acc.add(s, e);
-        }
-    }
-    return acc;
-}
-
-// The smallest v in [lo, hi) whose running sum, from `before` on, passes
-// `height`; -1 if none does (rounding at the end of a group).  One warp, in
-// element order: four consecutive elements a lane.
+// Four elements a lane of the chunk at `base` (elements from `end` on are 0).
 template <typename T>
-__device__ int find_in_group(const Weights<T> &w, int lo, int hi, double before, double height) {
+__device__ __forceinline__ void load_chunk(const Weights<T> &w, int base, int end, float (&p)[4], float (&q)[4]) {
     const int lane = threadIdx.x & 31;
-    for (int base = lo; base < hi; base += VCHUNK) {
-        float s[4], e[4];
-        double mine = 0.0;
+    if (w.quads && base + VCHUNK <= end) {
+        const Quad<T> a = *reinterpret_cast<const Quad<T> *>(w.p + base + 4 * lane);
+        Quad<T> b{};
+        if (w.q) b = *reinterpret_cast<const Quad<T> *>(w.q + base + 4 * lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = prob(a.v[k]), q[k] = w.q ? prob(b.v[k]) : 0.f;
+    } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int v = base + 4 * lane + k;
-            s[k] = e[k] = 0.f;
-            if (v < hi) w.at(v, prob(w.p[v]), w.q ? prob(w.q[v]) : 0.f, s[k], e[k]);
-            mine += (double)s[k] + (double)e[k];
+            p[k] = v < end ? prob(w.p[v]) : 0.f;
+            q[k] = w.q && v < end ? prob(w.q[v]) : 0.f;
         }
-        double upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const double x = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += x;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, mine > 0.0 && before + upto > height);
-        if (hit) {
-            const int src = __ffs((int)hit) - 1;
-            double run = before + (upto - mine);
-            int v = -1, last = -1;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                run += (double)s[k] + (double)e[k];
-                if (s[k] > 0.f) last = base + 4 * lane + k;
-                if (v < 0 && s[k] > 0.f && run > height) v = base + 4 * lane + k;
-            }
-            if (v < 0) v = last;   // the lane's sum passed in another rounding
-            return __shfl_sync(0xffffffffu, v, src);
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return -1;
 }
 
-// The last v in [lo, hi) of positive weight, -1 if none.  One warp.
+// Sum of the weights [lo, hi), lo a multiple of four, by a warp: the same in every lane.
 template <typename T>
-__device__ int last_in_group(const Weights<T> &w, int lo, int hi) {
+__device__ __forceinline__ Sum2 range_sum(const Weights<T> &w, int lo, int hi) {
+    const int lane = threadIdx.x & 31;
+    Sum2 acc;
+    for (int base = lo; base < hi; base += VBATCH * VCHUNK) {
+        float p[VBATCH][4], q[VBATCH][4];
+#pragma unroll
+        for (int u = 0; u < VBATCH; ++u) load_chunk(w, min(hi, base + u * VCHUNK), hi, p[u], q[u]);
+#pragma unroll
+        for (int u = 0; u < VBATCH; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float s, e;
+                w.at(base + u * VCHUNK + 4 * lane + i, p[u][i], q[u][i], s, e);
+                acc.add(s, e);
+            }
+    }
+    return warp_sum(acc);
+}
+
+// The smallest v in [lo, hi) of positive weight whose running sum, from
+// `before` on, passes `height`; where rounding lets none pass, the last of
+// positive weight.  One warp, in element order: four consecutive elements a lane.
+template <typename T>
+__device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, double height) {
+    const int lane = threadIdx.x & 31;
     int last = -1;
-    for (int v = lo + (int)(threadIdx.x & 31); v < hi; v += 32) {
-        float s, e;
-        w.at(v, prob(w.p[v]), w.q ? prob(w.q[v]) : 0.f, s, e);
-        if (s > 0.f) last = v;
+    for (int base = lo; base < hi; base += VCHUNK) {
+        float p[4], q[4], s[4], e[4];
+        load_chunk(w, base, hi, p, q);
+        Sum2 mine;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w.at(base + 4 * lane + k, p[k], q[k], s[k], e[k]);
+            mine.add(s[k], e[k]);
+            if (s[k] > 0.f) last = base + 4 * lane + k;
+        }
+        const Sum2 upto = warp_scan(mine);
+        Sum2 run = upto;   // the running sum before this lane's elements
+        run.add(-mine.hi, -mine.lo);
+        run.add(before);
+        int v = INT_MAX;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            run.add(s[k], e[k]);
+            if (v == INT_MAX && s[k] > 0.f && run.value() > height) v = base + 4 * lane + k;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
+        if (v != INT_MAX) return v;
+        before.add(__shfl_sync(0xffffffffu, upto.hi, 31), __shfl_sync(0xffffffffu, upto.lo, 31));
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, d));
@@ -182,14 +200,16 @@ __device__ int last_in_group(const Weights<T> &w, int lo, int hi) {
 }
 
 template <typename T>
-__global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS) verify_kernel(const VerifyArgs a) {
+__global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, 4) verify_kernel(const VerifyArgs a) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank();
     const int seq = blockIdx.x / VCTAS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ double totals[VWARPS * VPER];   // this CTA's groups: [turn][warp]
-    __shared__ double part[VGROUPS], sums[VGROUPS];   // the row's groups in order: totals, running sums
-    __shared__ double warp_sum[VWARPS];
+    __shared__ Sum2 totals[VWARPS];   // this CTA's slices; then, in rank 0, the parts of one
+    __shared__ Sum2 s_before;         // rank 0: the sum before the slice that passes
+    __shared__ double s_height;
+    __shared__ int s_slice;           // rank 0: that slice; -1: no token; -2: draw from p itself
+    __shared__ int s_next;
     __shared__ int s_kept, s_n, s_d0;
 
     if (warp == 0) {
@@ -232,81 +252,83 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS) verify
     int next = -1;
     if (kept >= 0) {   // the same in every CTA of the cluster
         const bool failed = kept < n;
-        Weights<T> w;
-        w.p = static_cast<const T *>(a.target) + (long long)(d0 + seq + kept) * a.target_stride;
-        w.q = failed && a.draft ? static_cast<const T *>(a.draft) + (long long)(d0 + kept) * a.draft_stride : nullptr;
-        w.out = failed && !a.draft ? a.draft_tokens[d0 + kept] : -1;
-        const int len = ((a.vocab + VGROUPS - 1) / VGROUPS + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a group
-        const int used = (a.vocab + len - 1) / len;
+        const T *p = static_cast<const T *>(a.target) + (long long)(d0 + seq + kept) * a.target_stride;
+        const T *q = failed && a.draft ? static_cast<const T *>(a.draft) + (long long)(d0 + kept) * a.draft_stride : nullptr;
+        Weights<T> w(p, q, failed && !a.draft ? a.draft_tokens[d0 + kept] : -1);
+        const int len = ((a.vocab + VSLICES - 1) / VSLICES + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
         for (int attempt = 0; attempt < 2; ++attempt) {
-            const bool quads = ((reinterpret_cast<uintptr_t>(w.p) | (w.q ? reinterpret_cast<uintptr_t>(w.q) : 0)) &
-                                (4 * sizeof(T) - 1)) == 0;
-#pragma unroll 1
-            for (int k = 0; k < VPER; ++k) {
-                const int g = (k * VCTAS + rank) * VWARPS + warp;
-                const long long lo = (long long)g * len;
-                Sum2 acc;
-                if (g < used) {
-                    const int hi = (int)min((long long)a.vocab, lo + len);
-                    acc = quads ? group_sum<T, true>(w, (int)lo, hi) : group_sum<T, false>(w, (int)lo, hi);
-                }
-                double x = acc.value();
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                if (lane == 0) totals[k * VWARPS + warp] = x;
-            }
+            const long long lo = (long long)(rank * VWARPS + warp) * len;
+            const Sum2 mine = range_sum(w, (int)min((long long)a.vocab, lo), (int)min((long long)a.vocab, lo + len));
+            if (lane == 0) totals[warp] = mine;
             cluster.sync();
-            // running sums over all groups, the same in every CTA: two a thread
-            double x[2];
+            if (rank == 0 && warp == 0) {   // lane l: slices 2 l and 2 l + 1
+                const Sum2 *src = cluster.map_shared_rank(totals, 2 * lane / VWARPS) + 2 * lane % VWARPS;
+                const Sum2 x0 = src[0], x1 = src[1];
+                Sum2 both = x0;
+                both.add(x1);
+                const Sum2 upto = warp_scan(both);
+                const Sum2 all{__shfl_sync(0xffffffffu, upto.hi, 31), __shfl_sync(0xffffffffu, upto.lo, 31)};
+                const double total = all.value();   // the same in all lanes
+                int slice = attempt == 0 && failed && total == 0.0 ? -2 : -1;
+                if (total > 0.0 && isfinite(total)) {
+                    const double height = (double)a.sample[seq] * total;
+                    Sum2 run = upto;   // before the lane's slices
+                    run.add(-both.hi, -both.lo);
+                    Sum2 run1 = run;
+                    run1.add(x0);
+                    // the first slice whose running sum passes, else the last of any weight
+                    const int g = x0.any() && run1.value() > height  ? 2 * lane
+                                  : x1.any() && upto.value() > height ? 2 * lane + 1
+                                                                      : INT_MAX;
+                    int first = g, last = x1.any() ? 2 * lane + 1 : x0.any() ? 2 * lane : -1;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int g = 2 * threadIdx.x + k;
-                const double *src = cluster.map_shared_rank(totals, (g / VWARPS) % VCTAS);
-                part[g] = x[k] = src[g / (VWARPS * VCTAS) * VWARPS + g % VWARPS];
-            }
-            double upto = x[0] + x[1];
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += y;
-            }
-            if (lane == 31) warp_sum[warp] = upto;
-            __syncthreads();
-            double before = 0.0;
-            for (int k = 0; k < warp; ++k) before += warp_sum[k];
-            sums[2 * threadIdx.x] = before + (upto - x[1]);
-            sums[2 * threadIdx.x + 1] = before + upto;
-            __syncthreads();
-            const double total = sums[VGROUPS - 1];
-            const bool none = !(total > 0.0);
-            cluster.sync();   // no CTA leaves, or sums again, while another reads its totals
-            if (none && attempt == 0 && failed && total == 0.0) {   // nothing is left of p: draw from p itself
-                w.q = nullptr;
-                w.out = -1;
-                continue;
-            }
-            if (rank == 0 && warp == 0 && !none && isfinite(total)) {
-                const double height = (double)a.sample[seq] * total;
-                // the first group whose running sum passes, else the last with any weight
-                int first = VGROUPS, last = 0;
-                for (int g = lane; g < VGROUPS; g += 32) {
-                    if (part[g] > 0.0) {
-                        last = g;
-                        if (sums[g] > height && first == VGROUPS) first = g;
+                    for (int d = 16; d > 0; d >>= 1) {
+                        first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
+                        last = max(last, __shfl_xor_sync(0xffffffffu, last, d));
+                    }
+                    slice = first != INT_MAX ? first : last;
+                    if (slice >> 1 == lane) {
+                        s_before = slice & 1 ? run1 : run;
+                        s_height = height;
                     }
                 }
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) {
-                    first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
-                    last = max(last, __shfl_xor_sync(0xffffffffu, last, d));
-                }
-                const int g = first < VGROUPS ? first : last;
-                const int lo = g * len, hi = min(a.vocab, lo + len);
-                next = first < VGROUPS ? find_in_group<T>(w, lo, hi, g ? sums[g - 1] : 0.0, height) : -1;
-                if (next < 0) next = last_in_group<T>(w, lo, hi);
+                if (lane == 0) s_slice = slice;
             }
-            break;
+            cluster.sync();   // rank 0 has read every CTA's totals and decided
+            const bool again = *cluster.map_shared_rank(&s_slice, 0) == -2;
+            if (rank == 0 && s_slice >= 0) {   // the slice again, in parts
+                const int from = s_slice * len, part = (len / VCHUNK + VWARPS - 1) / VWARPS * VCHUNK;
+                const int lo = min(a.vocab, min(from + len, from + warp * part));
+                const int hi = min(a.vocab, min(from + len, lo + part));
+                const Sum2 mine = range_sum(w, lo, hi);
+                if (lane == 0) totals[warp] = mine;
+                __syncthreads();
+                Sum2 run = s_before, before = run;
+                int at = -1;       // the first part that passes, else the last of any weight
+                bool passed = false;
+                for (int k = 0; k < VWARPS; ++k) {
+                    const Sum2 x = totals[k];
+                    Sum2 after = run;
+                    after.add(x);
+                    if (!passed && x.any()) {
+                        at = k;
+                        before = run;
+                        passed = after.value() > s_height;
+                    }
+                    run = after;
+                }
+                if (warp == at) {
+                    const int v = find_in_range(w, lo, hi, before, s_height);
+                    if (lane == 0) s_next = v;
+                }
+                __syncthreads();
+                next = s_next;
+            }
+            if (!again) break;
+            w = Weights<T>(p, nullptr, -1);
+            cluster.sync();   // every CTA has read the decision
         }
+        cluster.sync();   // rank 0's shared memory outlives its readers
     }
     if (rank == 0 && warp == 0) {
         for (int j = lane; j <= a.max_drafts; j += 32)
