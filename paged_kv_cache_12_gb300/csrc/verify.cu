@@ -11,19 +11,20 @@
 //
 // Of the n + 1 rows of a sequence only the one after the last standing draft is
 // read whole, with the draft's row beside it: the kernel is bound by HBM on a
-// batch and by latency on a few sequences.  A cluster of eight CTAs takes a
-// sequence.  Every CTA finds the number of standing drafts (a warp, one draft a
-// lane); the row's elements are summed in 64 slices, one a warp of the cluster;
-// one warp collects the 64 totals through distributed shared memory and finds
-// the slice in which the running sum passes the drawn height; its CTA reads
-// that slice again in eight parts, and a warp the part that passes.
+// batch and by latency on a few sequences.  A cluster of eight CTAs, or of fewer
+// where the batch fills the GPU's CTA slots, takes a sequence.  Every CTA finds
+// the number of standing drafts (a warp, one draft a lane); the row's elements
+// are summed in slices, one a warp of the cluster; one warp collects the totals
+// through distributed shared memory and finds the slice in which the running sum
+// passes the drawn height; its CTA reads that slice again in eight parts, and a
+// warp the part that passes.
 //
 // Sums: a draw is decided where a running sum over up to a hundred thousand
 // terms passes u * total, so sums are carried as an unevaluated pair of floats
-// (Knuth's two-sum, exact error terms) and compared in 64 bits.  Summing in 64
-// bits throughout costs more than the reads: this GPU's 64-bit rate is two a
-// clock and SM (512 totals of a row scanned in 64 bits by one warp took 14,000
-// clocks, more than a 128 KB slice of two rows).
+// (Knuth's two-sum, exact error terms) and compared as such.  64-bit sums cost
+// more than the reads: this GPU's 64-bit rate is two a clock and SM (512 totals
+// of a row scanned in 64 bits by one warp took 14,000 clocks, eight partial sums
+// compared in 64 bits by eight warps 4,000).
 
 #include <climits>
 
@@ -36,13 +37,13 @@ namespace cg = cooperative_groups;
 namespace pa {
 namespace {
 
-constexpr int VCTAS = 8;                       // CTAs of a sequence's cluster
+constexpr int VMAX_CTAS = 8;                   // CTAs of a sequence's cluster, at most
 constexpr int VTHREADS = 256;
 constexpr int VWARPS = VTHREADS / 32;
-constexpr int VSLICES = VCTAS * VWARPS;        // slices of a row, two a lane of the collecting warp
+constexpr int VRESIDENT = 4;                   // CTAs an SM holds (64 registers a thread)
 constexpr int VCHUNK = 128;                    // elements a warp reads at once, four a lane
 constexpr int VBATCH = 4;                      // chunks on their way at once
-static_assert(VSLICES == 64, "two totals a lane");
+static_assert(VMAX_CTAS * VWARPS == 64, "at most two slices a lane of the collecting warp");
 
 struct VerifyArgs {
     int32_t *accepted, *tokens;
@@ -74,7 +75,15 @@ struct Sum2 {
         lo = __fadd_rn(lo, __fadd_rn(r, e));
     }
     __device__ __forceinline__ void add(const Sum2 &x) { add(x.hi, x.lo); }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+    // this > x: the high parts' difference is exact where they are near
+    __device__ __forceinline__ bool over(const Sum2 &x) const {
+        return __fadd_rn(__fsub_rn(hi, x.hi), __fsub_rn(lo, x.lo)) > 0.f;
+    }
+    __device__ __forceinline__ Sum2 times(float u) const {   // exact to twice a float's precision
+        const float h = __fmul_rn(u, hi);
+        return Sum2{h, __fmaf_rn(u, lo, __fmaf_rn(u, hi, -h))};
+    }
     __device__ __forceinline__ bool any() const { return hi > 0.f; }   // sums of weights >= 0
 };
 
@@ -166,7 +175,7 @@ __device__ __forceinline__ Sum2 range_sum(const Weights<T> &w, int lo, int hi) {
 // `before` on, passes `height`; where rounding lets none pass, the last of
 // positive weight.  One warp, in element order: four consecutive elements a lane.
 template <typename T>
-__device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, double height) {
+__device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, Sum2 height) {
     const int lane = threadIdx.x & 31;
     int last = -1;
     for (int base = lo; base < hi; base += VCHUNK) {
@@ -187,7 +196,7 @@ __device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, d
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             run.add(s[k], e[k]);
-            if (v == INT_MAX && s[k] > 0.f && run.value() > height) v = base + 4 * lane + k;
+            if (v == INT_MAX && s[k] > 0.f && run.over(height)) v = base + 4 * lane + k;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
@@ -199,15 +208,15 @@ __device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, d
     return last;
 }
 
-template <typename T>
-__global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, 4) verify_kernel(const VerifyArgs a) {
+template <typename T, int VCTAS>
+__global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESIDENT) verify_kernel(const VerifyArgs a) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank();
     const int seq = blockIdx.x / VCTAS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ Sum2 totals[VWARPS];   // this CTA's slices; then, in rank 0, the parts of one
     __shared__ Sum2 s_before;         // rank 0: the sum before the slice that passes
-    __shared__ double s_height;
+    __shared__ Sum2 s_height;
     __shared__ int s_slice;           // rank 0: that slice; -1: no token; -2: draw from p itself
     __shared__ int s_next;
     __shared__ int s_kept, s_n, s_d0;
@@ -255,6 +264,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, 4) ver
         const T *p = static_cast<const T *>(a.target) + (long long)(d0 + seq + kept) * a.target_stride;
         const T *q = failed && a.draft ? static_cast<const T *>(a.draft) + (long long)(d0 + kept) * a.draft_stride : nullptr;
         Weights<T> w(p, q, failed && !a.draft ? a.draft_tokens[d0 + kept] : -1);
+        constexpr int VSLICES = VCTAS * VWARPS;
         const int len = ((a.vocab + VSLICES - 1) / VSLICES + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
         for (int attempt = 0; attempt < 2; ++attempt) {
             const long long lo = (long long)(rank * VWARPS + warp) * len;
@@ -262,23 +272,27 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, 4) ver
             if (lane == 0) totals[warp] = mine;
             cluster.sync();
             if (rank == 0 && warp == 0) {   // lane l: slices 2 l and 2 l + 1
-                const Sum2 *src = cluster.map_shared_rank(totals, 2 * lane / VWARPS) + 2 * lane % VWARPS;
-                const Sum2 x0 = src[0], x1 = src[1];
+                Sum2 x0, x1;
+                if (2 * lane < VSLICES) {
+                    const Sum2 *src = cluster.map_shared_rank(totals, 2 * lane / VWARPS) + 2 * lane % VWARPS;
+                    x0 = src[0];
+                    x1 = src[1];
+                }
                 Sum2 both = x0;
                 both.add(x1);
                 const Sum2 upto = warp_scan(both);
                 const Sum2 all{__shfl_sync(0xffffffffu, upto.hi, 31), __shfl_sync(0xffffffffu, upto.lo, 31)};
-                const double total = all.value();   // the same in all lanes
-                int slice = attempt == 0 && failed && total == 0.0 ? -2 : -1;
-                if (total > 0.0 && isfinite(total)) {
-                    const double height = (double)a.sample[seq] * total;
+                const float total = all.value();   // the same in all lanes
+                int slice = attempt == 0 && failed && total == 0.f ? -2 : -1;
+                if (total > 0.f && isfinite(total)) {
+                    const Sum2 height = all.times(a.sample[seq]);
                     Sum2 run = upto;   // before the lane's slices
                     run.add(-both.hi, -both.lo);
                     Sum2 run1 = run;
                     run1.add(x0);
                     // the first slice whose running sum passes, else the last of any weight
-                    const int g = x0.any() && run1.value() > height  ? 2 * lane
-                                  : x1.any() && upto.value() > height ? 2 * lane + 1
+                    const int g = x0.any() && run1.over(height)  ? 2 * lane
+                                  : x1.any() && upto.over(height) ? 2 * lane + 1
                                                                       : INT_MAX;
                     int first = g, last = x1.any() ? 2 * lane + 1 : x0.any() ? 2 * lane : -1;
 #pragma unroll
@@ -313,7 +327,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, 4) ver
                     if (!passed && x.any()) {
                         at = k;
                         before = run;
-                        passed = after.value() > s_height;
+                        passed = after.over(s_height);
                     }
                     run = after;
                 }
@@ -337,9 +351,21 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, 4) ver
     }
 }
 
+// The largest cluster with which all sequences' CTAs are resident at once (100
+// sequences of 131072 tokens: clusters of 8, in two rounds, 34 us; 4 sequences of
+// 32003: 9 us with 8).
 template <typename T>
 int launch_verify(const VerifyArgs &a, cudaStream_t st) {
-    verify_kernel<T><<<(unsigned)a.num_seqs * VCTAS, VTHREADS, 0, st>>>(a);
+    const long long slots = (long long)num_sms() * VRESIDENT;
+    const unsigned b = (unsigned)a.num_seqs;
+    if (b * 8LL <= slots)
+        verify_kernel<T, 8><<<b * 8, VTHREADS, 0, st>>>(a);
+    else if (b * 4LL <= slots)
+        verify_kernel<T, 4><<<b * 4, VTHREADS, 0, st>>>(a);
+    else if (b * 2LL <= slots)
+        verify_kernel<T, 2><<<b * 2, VTHREADS, 0, st>>>(a);
+    else
+        verify_kernel<T, 1><<<b, VTHREADS, 0, st>>>(a);
     return cuda_status(cudaGetLastError());
 }
 
