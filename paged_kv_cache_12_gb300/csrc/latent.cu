@@ -171,7 +171,12 @@ __global__ void __launch_bounds__(READ_THREADS) latent_read_kernel(
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 const int r = r0 + STEP * k;
-                const uint2 a = latent_codes_to_bf16(c[k].x, s[k]), b = latent_codes_to_bf16(c[k].y, s[k]);
+                const uint32_t up = latent_scale_up(s[k]);
+                uint2 a = latent_codes_fast(c[k].x, up), b = latent_codes_fast(c[k].y, up);
+                if (latent_codes_nan(c[k]) || latent_scale_special(s[k])) {
+                    a = latent_codes_to_bf16(c[k].x, s[k]);
+                    b = latent_codes_to_bf16(c[k].y, s[k]);
+                }
                 if (r < left) out[(long long)(base + r) * out_vecs + v] = make_uint4(a.x, a.y, b.x, b.y);
             }
             return;

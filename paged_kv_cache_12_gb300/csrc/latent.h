@@ -22,31 +22,47 @@ inline int latent_row_bytes(int kv) {
     return kv == PA_KV_F16 || kv == PA_KV_BF16 ? 2 * LROW : kv == PA_KV_FP8_E4M3 ? LROW8 : 0;
 }
 
-// Four E4M3 codes times a power of two, as two pairs of bf16 (exact: a code
-// has four significant bits and the scale none).  By bits: a code's exponent and
-// mantissa, moved to the low end of a bf16's, are the value times 2^-120 (a
-// subnormal code becomes a subnormal bf16); two exact products undo that and
-// scale.  Conversion instructions (E4M3 to fp16 to float to bf16) would take
-// three times as long: 3100 cycles for a tile of 48 x 512 codes by eight warps.
+// E4M3 codes times a power of two as bf16 (exact: a code has four significant
+// bits and the scale none), by bits: a code's exponent and mantissa, moved to
+// the low end of a bf16's, are the value times 2^-120 (a subnormal code becomes a
+// subnormal bf16), and a product with 2^120 times the scale is exact.
+// Conversion instructions (E4M3 to fp16 to float to bf16) take three times as
+// long.  Two cases need the long way: NaN codes, and scales above 2^7, where
+// 2^120 times the scale is no bf16; latent_codes_special finds them.
 __device__ __forceinline__ uint32_t bf162_mul(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint2 latent_codes_to_bf16(uint32_t codes, float scale) {
-    const uint32_t s2 = (__float_as_uint(scale) >> 16) * 0x10001u;   // a power of two, or NaN, twice
+// Four codes (lowest byte first) at 2^-120 of their values.
+__device__ __forceinline__ uint2 latent_codes_low(uint32_t codes) {
     const uint32_t w0 = __byte_perm(codes, 0, 0x1404), w1 = __byte_perm(codes, 0, 0x3424);
-    constexpr uint32_t UP = 0x7b807b80u;   // 2^120, twice
-    uint2 r = make_uint2(((w0 >> 4) & 0x07f007f0u) | (w0 & 0x80008000u),
-                         ((w1 >> 4) & 0x07f007f0u) | (w1 & 0x80008000u));
-    r.x = bf162_mul(bf162_mul(r.x, UP), s2);
-    r.y = bf162_mul(bf162_mul(r.y, UP), s2);
-    if (((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {   // a NaN code (all exponent and mantissa bits)
-        if ((codes & 0x7fu) == 0x7fu) r.x = (r.x & 0xffff0000u) | 0x7fc0u;
-        if ((codes >> 8 & 0x7fu) == 0x7fu) r.x = (r.x & 0xffffu) | 0x7fc00000u;
-        if ((codes >> 16 & 0x7fu) == 0x7fu) r.y = (r.y & 0xffff0000u) | 0x7fc0u;
-        if ((codes >> 24 & 0x7fu) == 0x7fu) r.y = (r.y & 0xffffu) | 0x7fc00000u;
-    }
+    return make_uint2(((w0 >> 4) & 0x07f007f0u) | (w0 & 0x80008000u),
+                      ((w1 >> 4) & 0x07f007f0u) | (w1 & 0x80008000u));
+}
+// 2^120 times the scale, twice (scales up to 2^7).
+__device__ __forceinline__ uint32_t latent_scale_up(float scale) {
+    return __byte_perm(__float_as_uint(scale * 0x1p120f), 0, 0x3232);
+}
+__device__ __forceinline__ uint2 latent_codes_fast(uint32_t codes, uint32_t scale_up) {
+    const uint2 r = latent_codes_low(codes);
+    return make_uint2(bf162_mul(r.x, scale_up), bf162_mul(r.y, scale_up));
+}
+// Nonzero if one of eight codes is NaN (all exponent and mantissa bits set).
+__device__ __forceinline__ uint32_t latent_codes_nan(uint2 codes) {
+    return (((codes.x & 0x7f7f7f7fu) + 0x01010101u) | ((codes.y & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+}
+__device__ __forceinline__ bool latent_scale_special(float scale) { return !(scale <= 128.f); }
+// Any codes and scale.
+__device__ __forceinline__ uint2 latent_codes_to_bf16(uint32_t codes, float scale) {
+    uint2 r = latent_codes_low(codes);
+    const uint32_t s2 = __byte_perm(__float_as_uint(scale), 0, 0x3232);
+    r.x = bf162_mul(bf162_mul(r.x, 0x7b807b80u), s2);   // 2^120, then the scale
+    r.y = bf162_mul(bf162_mul(r.y, 0x7b807b80u), s2);
+    if ((codes & 0x7fu) == 0x7fu) r.x = (r.x & 0xffff0000u) | 0x7fc0u;
+    if ((codes >> 8 & 0x7fu) == 0x7fu) r.x = (r.x & 0xffffu) | 0x7fc00000u;
+    if ((codes >> 16 & 0x7fu) == 0x7fu) r.y = (r.y & 0xffff0000u) | 0x7fc0u;
+    if ((codes >> 24 & 0x7fu) == 0x7fu) r.y = (r.y & 0xffffu) | 0x7fc00000u;
     return r;
 }
 

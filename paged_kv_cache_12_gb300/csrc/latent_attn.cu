@@ -20,7 +20,7 @@ struct LatentArgs {
     const uint8_t *cache;
     const int32_t *block_tables, *context_lens, *query_start;
     WsHeader *hdr;
-    int num_seqs, num_query_tokens, H, bs, mbps, max_context_len;
+    int num_seqs, num_query_tokens, H, bs_log2, mbps, max_context_len;
     long long num_blocks;
     float scale_log2;
     long long wait_limit;
@@ -43,7 +43,7 @@ struct LatentArgs {
         w.L = __ldg(context_lens + i);
         w.q0 = query_start ? __ldg(query_start + i) : i;
         w.T = query_start ? __ldg(query_start + i + 1) - w.q0 : 1;
-        w.valid = w.L >= 0 && w.L <= max_context_len && (long long)w.L <= (long long)mbps * bs &&
+        w.valid = w.L >= 0 && w.L <= max_context_len && (long long)w.L <= (long long)mbps << bs_log2 &&
                   !(query_start && w.T > w.L);
         w.tiles = w.valid && w.T > 0 ? (w.L + TOK - 1) / TOK : 0;
         w.rts = w.tiles ? (int)(((long long)w.T * H + LT_ROWS - 1) / LT_ROWS) : 0;
@@ -61,8 +61,13 @@ struct LatentArgs {
     __device__ __forceinline__ bool starts_ok() const {
         return !query_start || offsets_ok(query_start, num_seqs, num_query_tokens);
     }
+    // A token's entry in its block table, and its offset in the block (a block
+    // size is a power of two).
+    __device__ __forceinline__ int entry_of(int tok) const { return tok >> bs_log2; }
+    __device__ __forceinline__ int offset_of(int tok) const { return tok & ((1 << bs_log2) - 1); }
     // rows of row tile r, and its first row in the query
     __device__ __forceinline__ int cut_rows(const Seq &w, int r) const { return rows(w, r); }
+    __device__ __forceinline__ int first_tiles(const Seq &w, int r) const { return row_tiles(w, r); }
     __device__ __forceinline__ int rows(const Seq &w, int r) const {
         return (int)min((long long)LT_ROWS, (long long)w.T * H - (long long)r * LT_ROWS);
     }
@@ -89,25 +94,24 @@ constexpr int LT_TMEM = 512;                  // columns: O (256), S0, S1 (64 ea
 constexpr int LT_S = 256;
 constexpr uint32_t LT_HI = 16u << 16;         // lanes 16 .. 31 of each quarter: output dims 256 .. 511
 constexpr int LT_BAD_SLOTS = 16;
-constexpr int L8_STEP = 16;                   // tokens of a staging slot of codes
-constexpr int L8_SLOTS = 4;
-constexpr int L8_SLOT = L8_STEP * (LC + 16);  // their codes, then their scales
 constexpr int L8_WARPS = 8;                   // converting warps
+constexpr int L8_STEP = 16;                   // tokens of a staging slot of quantised rows: two groups of eight
+constexpr int L8_GROUP = 8 * LROW8;           // bytes of a group, consecutive in its block
+constexpr int L8_SLOTS = 3;
 
 // What differs between a 16-bit and an E4M3 cache.
 template <int KV>
 struct Lt {
     static constexpr bool F8 = KV == PA_KV_FP8_E4M3;
-    static constexpr int TOK = F8 ? 48 : 64;
+    static constexpr int TOK = F8 ? 48 : 64;   // tokens of a KV tile
     static constexpr int THREADS = F8 ? 256 + 32 * L8_WARPS : 256;
     static constexpr int STAGE = TOK / 8 * LT_GROUP;
     static constexpr int OFF_KV = LT_Q;
     static constexpr int OFF_P = OFF_KV + 2 * STAGE;
     static constexpr int OFF_8 = OFF_P + LT_P;
-    static constexpr int OFF_CTRL = OFF_8 + (F8 ? L8_SLOTS * L8_SLOT : 0);
+    static constexpr int OFF_CTRL = OFF_8 + (F8 ? L8_SLOTS * 2 * L8_GROUP : 0);
     static constexpr int SMEM = OFF_CTRL + LT_CTRL + 1024;   // + alignment slack
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
-    static_assert(TOK % L8_STEP == 0 && OFF_8 % 1024 == 0, "layout");
     using Args = LatentArgs<TOK>;
 };
 
@@ -122,10 +126,10 @@ struct LtCtrl {
 };
 static_assert(sizeof(LtCtrl) <= LT_CTRL, "control block");
 
-// Tensor maps: the cache's rows (16-bit), or a quantised cache's codes, rotary
-// elements and scales; the query's rows.
+// Tensor maps: rows of a 16-bit cache (a quantised one is copied as it lies),
+// rows of the query.
 struct LtMaps {
-    CUtensorMap kv, rope, scale, q;
+    CUtensorMap kv, q;
 };
 
 // A role's bounded wait, the outcome shared by the warp (or one lane's own).
@@ -146,10 +150,13 @@ struct Waiter {
     }
 };
 
-// The producer warp: lane j copies tokens 8 j .. 8 j + 7 of a tile, lanes 8 ..
-// 15 the query rows.  A quantised tile goes in steps of 16 tokens: codes and
-// scales into the staging ring, rotary elements straight into the 16-bit stage
-// (which the step waits for as well; the converting warps need it free anyway).
+// The producer warp: lane j copies tokens 8 j .. 8 j + 7 of a tile, lanes 8 .. 15
+// the query rows.  A quantised tile goes in steps of 16 tokens into the staging
+// ring, a group of eight rows (5248 bytes, consecutive in its block) per copy:
+// with a tensor map per part of a row a step took eight copies, and issuing them
+// was what bound the kernel (3600 clocks a tile of 48 tokens).  The next tile's rows are fetched into L2 while both
+// stages are full: 100 x 8192 tokens 167 -> 164 us, 128 heads 237 -> 229 us; two,
+// three or four tiles ahead gain less and less.
 template <int KV>
 __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p,
                         const LtMaps &maps) {
@@ -171,102 +178,124 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
         for (int t = p.t0; t < p.t1 && w.ok; ++t, ++cnt) {
             const int tok = t * L::TOK + 8 * lane, st = cnt & 1;
             const bool mine = lane < L::TOK / 8 && tok < p.w.L;
-            const int32_t blk = mine ? __ldg(row + tok / a.bs) : 0;
+            const int32_t blk = mine ? __ldg(row + a.entry_of(tok)) : 0;
+            // lanes 8 ..: a group of the next tile, to be fetched into L2
+            const int ntok = tok + L::TOK - 64;
+            const bool ahead = lane >= 8 && lane < 8 + L::TOK / 8 && t + 1 < p.t1 && ntok < p.w.L;
+            const int32_t nblk = ahead ? __ldg(row + a.entry_of(ntok)) : -1;
             const bool bad = __any_sync(0xffffffffu, mine && (blk < 0 || blk >= a.num_blocks));
             const unsigned boxes = __ballot_sync(0xffffffffu, mine && !bad);
-            const int y = (int)((long long)blk * a.bs) + tok % a.bs;
-            const uint32_t dst = base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP;
+            const int y = (blk << a.bs_log2) + a.offset_of(tok);
             if (bad && lane == 0) *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) = p.local + 1;
             if constexpr (L::F8) {
                 for (int k = 0; k < L::TOK / L8_STEP; ++k, ++steps) {
                     const int s = steps % L8_SLOTS, j = lane - 2 * k;   // groups 2 k and 2 k + 1 of the tile
                     if (!w.warp(c.empty8[s], steps / L8_SLOTS + 1)) break;
                     if (lane == 0)
-                        mbar_arrive_expect_tx(smem_u32(&c.full8[s]), (uint32_t)(__popc(boxes >> (2 * k) & 3u) * 8 * (LC + 16)));
+                        mbar_arrive_expect_tx(smem_u32(&c.full8[s]), (uint32_t)(__popc(boxes >> (2 * k) & 3u) * L8_GROUP));
                     __syncwarp();
-                    if ((j == 0 || j == 1) && (boxes >> lane & 1u)) {
-                        const uint32_t d8 = base + L::OFF_8 + s * L8_SLOT;
-                        tma_load_2d(d8 + j * 8 * LC, &maps.kv, 0, y, smem_u32(&c.full8[s]), first);
-                        tma_load_2d(d8 + j * 8 * LC + 8 * 256, &maps.kv, 256, y, smem_u32(&c.full8[s]), first);
-                        tma_load_2d(d8 + L8_STEP * LC + j * 128, &maps.scale, 0, y, smem_u32(&c.full8[s]), first);
-                    }
+                    if ((j == 0 || j == 1) && (boxes >> lane & 1u))
+                        bulk_load(base + L::OFF_8 + (2 * s + j) * L8_GROUP, a.cache + (long long)y * LROW8, L8_GROUP,
+                                  smem_u32(&c.full8[s]));
                     __syncwarp();
                 }
-                if (!w.ok || !w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]), (uint32_t)(__popc(boxes) * 1024));
-                __syncwarp();
-                if (boxes >> lane & 1u) tma_load_2d(dst + 8192, &maps.rope, 0, y, smem_u32(&c.kvfull[st]), first);
             } else {
                 if (!w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
                 if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]), (uint32_t)(__popc(boxes) * LT_GROUP));
                 __syncwarp();
-                if (boxes >> lane & 1u) tma_load_3d(dst, &maps.kv, 0, y, 0, smem_u32(&c.kvfull[st]), first);
-                // the next tile's rows on their way into L2 while this kernel's two
-                // stages are full: 100 x 8192 tokens 167 -> 164 us, 128 heads 237 ->
-                // 229 us; two, three or four tiles ahead gain less and less
-                const int ntok = tok + L::TOK - 64;   // lanes 8 .. 15
-                if (lane >= 8 && lane < 16 && t + 1 < p.t1 && ntok < p.w.L) {
-                    const int32_t nb = __ldg(row + ntok / a.bs);
-                    if (nb >= 0 && nb < a.num_blocks)
-                        tma_prefetch_3d(&maps.kv, 0, (int)((long long)nb * a.bs) + ntok % a.bs, 0);
-                }
+                if (boxes >> lane & 1u)
+                    tma_load_3d(base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP, &maps.kv, 0, y, 0,
+                                smem_u32(&c.kvfull[st]), first);
+            }
+            if (nblk >= 0 && nblk < a.num_blocks) {
+                const int ny = (nblk << a.bs_log2) + a.offset_of(ntok);
+                if constexpr (L::F8)
+                    bulk_prefetch(a.cache + (long long)ny * LROW8, L8_GROUP);
+                else
+                    tma_prefetch_3d(&maps.kv, 0, ny, 0);
             }
             __syncwarp();
         }
     }
-    // the last copies into every buffer have landed before the CTA leaves (a
-    // stage of a quantised tile also waits for its converting warps, which may
-    // have given up: its copies are then waited for until the limit)
-    for (int s = 0; s < 2; ++s)
-        if (cnt > s) mbar_wait_bounded(smem_u32(&c.kvfull[s]), (uint32_t)(((cnt - 1 - s) / 2) & 1), WAIT_LIMIT);
-    if constexpr (L::F8)
+    // the last copies into every buffer have landed before the CTA leaves
+    if constexpr (L::F8) {
         for (int s = 0; s < L8_SLOTS; ++s)
             if (steps > s)
                 mbar_wait_bounded(smem_u32(&c.full8[s]), (uint32_t)(((steps - 1 - s) / L8_SLOTS) & 1), WAIT_LIMIT);
+    } else {
+        for (int s = 0; s < 2; ++s)
+            if (cnt > s) mbar_wait_bounded(smem_u32(&c.kvfull[s]), (uint32_t)(((cnt - 1 - s) / 2) & 1), WAIT_LIMIT);
+    }
     if (pieces) mbar_wait_bounded(smem_u32(&c.qfull), (uint32_t)((pieces - 1) & 1), WAIT_LIMIT);
 }
 
-// A converting warp: rows w and w + 8 of every step of 16 tokens, codes times
-// their group's scale as bf16 in the layout a 16-bit copy would have written.
-// Lane l turns elements 8 l .. 8 l + 7 and 256 + 8 l .. into one 16-byte chunk
-// each, so eight lanes of a store cover all banks.  Rows past the context become
-// zeros (their probabilities are 0).
+// A converting warp of a quantised cache: row cw of both groups of every step,
+// codes times their group's scale as bf16 and the rotary elements, in the layout
+// a 16-bit copy would have written.  Lane l turns the codes 16 l .. 16 l + 15 into
+// two 16-byte chunks; lanes of odd 64-element blocks store their second chunk
+// first, so that eight lanes of a store cover all banks.  Rows past the context
+// become zeros (their probabilities are 0).  (Loading the rows from global memory
+// into registers instead of staging them: the loads in flight held up the stores
+// behind them, 130 us for the step that takes __ here.)
 template <int KV>
 __device__ void lt_convert(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p) {
     using L = Lt<KV>;
     const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - 8;
+    const bool odd = (lane >> 2) & 1;
+    // chunks 2 (l % 4) and 2 (l % 4) + 1 of block l / 4, in the order of their stores; rotary elements 2 l, 2 l + 1
+    const int at0 = (lane >> 2) * 1024 + cw * 128 + (((2 * (lane & 3) + odd) ^ cw) << 4);
+    const int at1 = (lane >> 2) * 1024 + cw * 128 + (((2 * (lane & 3) + 1 - odd) ^ cw) << 4);
+    const int atr = 8192 + cw * 128 + (((lane >> 2) ^ cw) << 4) + (lane & 3) * 4;
     Waiter w{&c.abort, a.wait_limit};
     int cnt = 0, steps = 0;
     while (w.ok && p.next()) {
-        for (int t = p.t0; t < p.t1 && w.ok; ++t, ++cnt) {
+        for (int t = p.t0; t < p.t1; ++t, ++cnt) {
             const int st = cnt & 1, left = p.w.L - t * L::TOK;   // tokens from the tile's first on
             if (!w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
+            uint8_t *stage = smem + L::OFF_KV + st * L::STAGE;
             for (int k = 0; k < L::TOK / L8_STEP; ++k, ++steps) {
                 const int s = steps % L8_SLOTS;
                 if (!w.warp(c.full8[s], steps / L8_SLOTS)) break;
-                const uint8_t *src = smem + L::OFF_8 + s * L8_SLOT;
+                const uint8_t *src = smem + L::OFF_8 + 2 * s * L8_GROUP + cw * LROW8;
+                uint4 v[2];
+                float sc[2];
+                uint32_t rope[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    // row cw of group i; its codes in two boxes of 256
-                    const int tok = k * L8_STEP + 8 * i + cw;
-                    const uint8_t *codes = src + i * 8 * LC + cw * 256 + 8 * lane;
-                    const float *scale = reinterpret_cast<const float *>(src + L8_STEP * LC + (8 * i + cw) * 16);
-                    uint8_t *row = smem + L::OFF_KV + st * L::STAGE + (tok >> 3) * LT_GROUP + (lane >> 3) * 1024 + cw * 128 +
-                                   (((lane & 7) ^ cw) << 4);
+                    v[i] = *reinterpret_cast<const uint4 *>(src + i * L8_GROUP + 16 * lane);
+                    sc[i] = *reinterpret_cast<const float *>(src + i * L8_GROUP + L8_SCALE + 4 * (lane >> 3));
+                    rope[i] = *reinterpret_cast<const uint32_t *>(src + i * L8_GROUP + L8_ROPE + 4 * lane);
+                }
+                uint2 x[2][4];
+                uint32_t special = left < (k + 1) * L8_STEP;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (tok < left) {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(codes + h * 8 * 256);
-                            const float sc = scale[2 * h + (lane >> 4)];
-                            const uint2 lo = latent_codes_to_bf16(v.x, sc), hi = latent_codes_to_bf16(v.y, sc);
-                            x = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                        }
-                        *reinterpret_cast<uint4 *>(row + h * 4096) = x;
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t up = latent_scale_up(sc[i]);
+                    x[i][0] = latent_codes_fast(v[i].x, up), x[i][1] = latent_codes_fast(v[i].y, up);
+                    x[i][2] = latent_codes_fast(v[i].z, up), x[i][3] = latent_codes_fast(v[i].w, up);
+                    special |= latent_codes_nan(make_uint2(v[i].x, v[i].y)) | latent_codes_nan(make_uint2(v[i].z, v[i].w)) |
+                               (uint32_t)latent_scale_special(sc[i]);
+                }
+                if (__any_sync(0xffffffffu, special)) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        x[i][0] = latent_codes_to_bf16(v[i].x, sc[i]), x[i][1] = latent_codes_to_bf16(v[i].y, sc[i]);
+                        x[i][2] = latent_codes_to_bf16(v[i].z, sc[i]), x[i][3] = latent_codes_to_bf16(v[i].w, sc[i]);
+                        if (k * L8_STEP + 8 * i + cw >= left)
+                            x[i][0] = x[i][1] = x[i][2] = x[i][3] = make_uint2(0, 0);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&c.empty8[s]));
+                if (lane == 0) mbar_arrive(smem_u32(&c.empty8[s]));   // (after the vote: every lane has its codes)
+                uint8_t *dst = stage + 2 * k * LT_GROUP;
+#pragma unroll
+                for (int i = 0; i < 2; ++i, dst += LT_GROUP) {
+                    const int f = odd ? 2 : 0;
+                    const uint2 a0 = f ? x[i][2] : x[i][0], b0 = f ? x[i][3] : x[i][1];
+                    const uint2 a1 = f ? x[i][0] : x[i][2], b1 = f ? x[i][1] : x[i][3];
+                    *reinterpret_cast<uint4 *>(dst + at0) = make_uint4(a0.x, a0.y, b0.x, b0.y);
+                    *reinterpret_cast<uint4 *>(dst + at1) = make_uint4(a1.x, a1.y, b1.x, b1.y);
+                    *reinterpret_cast<uint32_t *>(dst + atr) = rope[i];
+                }
             }
             if (!w.ok) break;
             fence_proxy_async_smem();   // the rows, for the tensor cores
@@ -482,7 +511,7 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&c.kvfull[s]), L::F8 ? 1 + L8_WARPS : 1);
+            mbar_init(smem_u32(&c.kvfull[s]), L::F8 ? L8_WARPS : 1);
             mbar_init(smem_u32(&c.kvempty[s]), 1);
             mbar_init(smem_u32(&c.sfull[s]), 1);
             mbar_init(smem_u32(&c.sfree[s]), 128);
@@ -539,10 +568,10 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
 
 // Rows of the cut row tiles from their pieces' partial rows; blockIdx.x is the
 // CTA whose range begins in the row tile.  Few pieces (two as a rule): block y
-// = 0, 8, .. takes eight rows, a warp each.  Many (a few long sequences): block
-// y takes row y, its warps every eighth piece.  When a CTA of the first kernel
-// gave up, every row becomes NaN.
-constexpr int MG_FEW = 8;
+// takes rows 8 y .. 8 y + 7, a warp each.  Many (a few long sequences): it takes
+// rows y, y + 8, .., its warps every eighth piece.  When a CTA of the first
+// kernel gave up, every row becomes NaN.
+constexpr int MG_FEW = 16, MG_BLOCKS = 8;
 
 // Pieces first, first + step, .. of a row: adds their weighted outputs, 16 dims a lane.
 struct RowSum {
@@ -578,50 +607,48 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const typename Lt<KV>
     __shared__ RowSum part[8][32];
     const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Cut cut = a.cuts[cta];
+    if (cut.rows == 0 && (cta || blockIdx.y)) return;
     const bool failed = any_gave_up(a.status, ctas);
-    if (cta == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
-    if (failed) {
-        const long long n = (long long)a.num_query_tokens * a.H * (LC / 8);
-        if (blockIdx.y == 0)
-            fill_rows(a.out, range_begin(n, cta, ctas), range_begin(n, cta + 1, ctas),
-                      KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
-        return;
+    if (cta == 0 && blockIdx.y == 0) {
+        if (threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
+        if (failed) fill_rows(a.out, 0, (long long)a.num_query_tokens * a.H * (LC / 8), KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     }
-    if ((int)blockIdx.y >= cut.rows) return;
+    if (failed || cut.rows == 0) return;
     const Pieces pc(cut, cta, cut.ntiles, Lt<KV>::Args::COST, ctas);
-    const int pieces = pc.k1 - pc.k0 + 1;
-    const bool few = pieces <= MG_FEW;
-    const int m = few ? blockIdx.y + warp : blockIdx.y;
-    if (few && ((blockIdx.y & 7) != 0 || m >= cut.rows)) return;
-    float M = -INFINITY;
-    for (int k = pc.k0 + lane; k <= pc.k1; k += 32) M = fmaxf(M, a.ml[(long long)pc.slot(k) * LT_ROWS + m].x);
+    const bool few = pc.k1 - pc.k0 < MG_FEW;
+    const int step = few ? cut.rows : MG_BLOCKS;   // one row a warp, or rows y, y + 8, .. of the block
+    for (int m = few ? blockIdx.y * 8 + warp : blockIdx.y; m < cut.rows; m += step) {
+        float M = -INFINITY;
+        for (int k = pc.k0 + lane; k <= pc.k1; k += 32) M = fmaxf(M, a.ml[(long long)pc.slot(k) * LT_ROWS + m].x);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    const float mu = M == -INFINITY ? 0.f : M;
-    RowSum x = add_pieces(a.ml, a.o, pc, m, mu, few ? 0 : warp, few ? 1 : 8);
-    if (!few) {
-        part[warp][lane] = x;
-        __syncthreads();
-        if (warp) return;
-        for (int k = 1; k < 8; ++k) {
-            const RowSum y = part[k][lane];
-            x.l += y.l;
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        const float mu = M == -INFINITY ? 0.f : M;
+        RowSum x = add_pieces(a.ml, a.o, pc, m, mu, few ? 0 : warp, few ? 1 : 8);
+        if (!few) {
+            part[warp][lane] = x;
+            __syncthreads();
+            if (warp == 0)
+                for (int k = 1; k < 8; ++k) {
+                    const RowSum y = part[k][lane];
+                    x.l += y.l;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x.o[j].x += y.o[j].x;
-                x.o[j].y += y.o[j].y;
-                x.o[j].z += y.o[j].z;
-                x.o[j].w += y.o[j].w;
-            }
+                    for (int j = 0; j < 4; ++j) {
+                        x.o[j].x += y.o[j].x;
+                        x.o[j].y += y.o[j].y;
+                        x.o[j].z += y.o[j].z;
+                        x.o[j].w += y.o[j].w;
+                    }
+                }
+            __syncthreads();
+            if (warp) continue;
         }
-    }
-    const float inv = 1.f / x.l;
-    const long long row = a.first_row(a.seq_work(cut.seq), cut.r) + m;
-    uint2 *out = reinterpret_cast<uint2 *>(a.out + row * LC) + lane;
+        const float inv = 1.f / x.l;
+        uint2 *out = reinterpret_cast<uint2 *>(a.out + (cut.row0 + m) * LC) + lane;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        out[32 * j] = make_uint2((uint32_t)to_bits<KV>(x.o[j].x * inv) | ((uint32_t)to_bits<KV>(x.o[j].y * inv) << 16),
-                                 (uint32_t)to_bits<KV>(x.o[j].z * inv) | ((uint32_t)to_bits<KV>(x.o[j].w * inv) << 16));
+        for (int j = 0; j < 4; ++j)
+            out[32 * j] = make_uint2((uint32_t)to_bits<KV>(x.o[j].x * inv) | ((uint32_t)to_bits<KV>(x.o[j].y * inv) << 16),
+                                     (uint32_t)to_bits<KV>(x.o[j].z * inv) | ((uint32_t)to_bits<KV>(x.o[j].w * inv) << 16));
+    }
 }
 
 // ------------------------------------------------------------------ launch
@@ -661,21 +688,6 @@ bool row_map(CUtensorMap *map, const void *base, long long rows, int kv) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// `width` elements from byte `at` of a quantised cache's rows, boxes of
-// `box_width` x 8 rows.
-bool row8_map(CUtensorMap *map, const uint8_t *cache, int at, int width, int box_width, CUtensorMapDataType type,
-              CUtensorMapSwizzle swizzle, long long rows) {
-    auto enc = tma_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {LROW8};
-    cuuint32_t box[2] = {(cuuint32_t)box_width, 8};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(map, type, 2, const_cast<uint8_t *>(cache) + at, dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Shared-memory limits are set per device, on its first call.
 template <int KV>
 cudaError_t lt_setup() {
@@ -693,7 +705,7 @@ cudaError_t lt_setup() {
 template <int KV>
 int launch_merge(const typename Lt<KV>::Args &a, int ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(a.query_start ? LT_ROWS : std::min(LT_ROWS, a.H)));
+    cfg.gridDim = dim3((unsigned)ctas, MG_BLOCKS);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -708,16 +720,8 @@ template <int KV>
 int launch_latent(const typename Lt<KV>::Args &a, cudaStream_t st) {
     if (lt_setup<KV>() != cudaSuccess) return PA_ERR_CUDA;
     LtMaps maps{};
-    const long long rows = a.num_blocks * a.bs;
-    bool ok = row_map(&maps.q, a.query, (long long)a.num_query_tokens * a.H, KV);
-    if (KV == PA_KV_FP8_E4M3)
-        ok = ok && row8_map(&maps.kv, a.cache, 0, LC, 256, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, rows) &&
-             row8_map(&maps.rope, a.cache, L8_ROPE, LR, LR, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                      CU_TENSOR_MAP_SWIZZLE_128B, rows) &&
-             row8_map(&maps.scale, a.cache, L8_SCALE, 4, 4, CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                      CU_TENSOR_MAP_SWIZZLE_NONE, rows);
-    else
-        ok = ok && row_map(&maps.kv, a.cache, rows, KV);
+    const bool ok = row_map(&maps.q, a.query, (long long)a.num_query_tokens * a.H, KV) &&
+                    (Lt<KV>::F8 || row_map(&maps.kv, a.cache, a.num_blocks << a.bs_log2, KV));
     if (!ok) return PA_ERR_CUDA;
     const int ctas = std::min(num_sms(), AXIS_MAX_CTAS);
     latent_kernel<KV><<<ctas, Lt<KV>::THREADS, Lt<KV>::SMEM, st>>>(maps, a);
@@ -743,7 +747,7 @@ int run_latent(void *out, const void *query, const void *cache, const int32_t *b
     a.num_seqs = num_seqs;
     a.num_query_tokens = num_query_tokens;
     a.H = num_heads;
-    a.bs = block_size;
+    a.bs_log2 = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : 6;
     a.mbps = max_blocks_per_seq;
     a.max_context_len = max_context_len;
     a.num_blocks = num_blocks;

@@ -86,6 +86,12 @@ struct ExpandedArgs {
     __device__ __forceinline__ int cut_rows(const Seq &w, int r) const {
         return min(EX_ROWS, w.T - r % w.per_head * EX_ROWS);
     }
+    __device__ __forceinline__ long long first_row(const Seq &w, int r) const {   // later rows: H apart
+        return (long long)(w.q0 + r % w.per_head * EX_ROWS) * H + r / w.per_head;
+    }
+    __device__ __forceinline__ int first_tiles(const Seq &w, int r) const {   // the first half's, of two
+        return tiles_of(w, min(w.T, r % w.per_head * EX_ROWS + EX_HALF));
+    }
     __device__ __forceinline__ bool starts_ok() const {
         const bool q = offsets_ok(query_start, num_seqs, num_query_tokens);
         return offsets_ok(kv_start, num_seqs, num_kv_tokens) && q;
@@ -487,55 +493,51 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Rows of the cut row tiles from their pieces' partial rows, a warp each:
-// blockIdx.x is the CTA whose range begins in the row tile.  When a CTA of the
-// first kernel gave up, every row becomes NaN.
+// Rows of the cut row tiles from their pieces' partial rows, eight lanes a row:
+// blockIdx.x is the CTA whose range begins in the row tile, block y takes rows 32 y
+// .. 32 y + 31.  When a CTA of the first kernel gave up, every row becomes NaN.
 template <int KV>
 __global__ void __launch_bounds__(256) expanded_merge_kernel(const ExpandedArgs a, int ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x, lane = threadIdx.x & 7;
     const Cut cut = a.cuts[cta];
+    if (cut.rows == 0 && (cta || blockIdx.y)) return;
     const bool failed = any_gave_up(a.status, ctas);
-    if (cta == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
-    if (failed) {
-        const long long n = (long long)a.num_query_tokens * a.H * (EV / 8);
-        if (blockIdx.y == 0)
-            fill_rows(a.out, range_begin(n, cta, ctas), range_begin(n, cta + 1, ctas),
-                      KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
-        return;
+    if (cta == 0 && blockIdx.y == 0) {
+        if (threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
+        if (failed) fill_rows(a.out, 0, (long long)a.num_query_tokens * a.H * (EV / 8), KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     }
-    const int m = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (m >= cut.rows) return;
-    const ExpandedArgs::Seq w = a.seq_work(cut.seq);
-    const int first = cut.r % w.per_head * EX_ROWS;
-    // what the row's half sees: the first half of a row tile of two, or its last rows
-    const int rows = m < EX_HALF && cut.rows > EX_HALF ? first + EX_HALF : first + cut.rows;
-    const Pieces pc(cut, cta, a.tiles_of(w, rows), ExpandedArgs::COST, ctas);
+    const int m = blockIdx.y * 32 + (threadIdx.x >> 3);
+    if (failed || m >= cut.rows) return;
+    const Pieces pc(cut, cta, m < EX_HALF ? cut.ntiles1 : cut.ntiles, ExpandedArgs::COST, ctas);
     if (pc.k0 == pc.k1) return;   // this half was finished by one CTA
     float M = -INFINITY;
-    for (int k = pc.k0 + lane; k <= pc.k1; k += 32) M = fmaxf(M, a.ml[pc.slot(k) * EX_ROWS + m].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    for (int k = pc.k0; k <= pc.k1; ++k) M = fmaxf(M, a.ml[pc.slot(k) * EX_ROWS + m].x);
     const float mu = M == -INFINITY ? 0.f : M;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 acc[4] = {};
     float l = 0.f;
-#pragma unroll 8
+#pragma unroll 2
     for (int k = pc.k0; k <= pc.k1; ++k) {
         const int at = pc.slot(k) * EX_ROWS + m;
         const float2 ml = a.ml[at];
-        const float4 o = *reinterpret_cast<const float4 *>(a.o + (long long)at * EV + 4 * lane);
+        const float4 *src = reinterpret_cast<const float4 *>(a.o + (long long)at * EV) + lane;
         const float wt = fast_exp2(ml.x - mu);
         l = fmaf(ml.y, wt, l);
-        acc.x = fmaf(o.x, wt, acc.x);
-        acc.y = fmaf(o.y, wt, acc.y);
-        acc.z = fmaf(o.z, wt, acc.z);
-        acc.w = fmaf(o.w, wt, acc.w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 o = src[8 * j];
+            acc[j].x = fmaf(o.x, wt, acc[j].x);
+            acc[j].y = fmaf(o.y, wt, acc[j].y);
+            acc[j].z = fmaf(o.z, wt, acc[j].z);
+            acc[j].w = fmaf(o.w, wt, acc[j].w);
+        }
     }
     const float inv = 1.f / l;
-    const long long row = (long long)(w.q0 + first + m) * a.H + cut.r / w.per_head;
-    *(reinterpret_cast<uint2 *>(a.out + row * EV) + lane) =
-        make_uint2((uint32_t)out_bits<KV>(acc.x * inv) | ((uint32_t)out_bits<KV>(acc.y * inv) << 16),
-                   (uint32_t)out_bits<KV>(acc.z * inv) | ((uint32_t)out_bits<KV>(acc.w * inv) << 16));
+    uint2 *out = reinterpret_cast<uint2 *>(a.out + (cut.row0 + (long long)m * a.H) * EV) + lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        out[8 * j] = make_uint2((uint32_t)out_bits<KV>(acc[j].x * inv) | ((uint32_t)out_bits<KV>(acc[j].y * inv) << 16),
+                                (uint32_t)out_bits<KV>(acc[j].z * inv) | ((uint32_t)out_bits<KV>(acc[j].w * inv) << 16));
 }
 
 // ------------------------------------------------------------------ launch
@@ -606,7 +608,7 @@ int launch_expanded(const ExpandedArgs &a, const CUtensorMap &tmq, const CUtenso
     expanded_kernel<KV><<<ctas, EX_THREADS, EX_SMEM, st>>>(tmq, tmk, tmr, tmv, a);
     if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((std::min(EX_ROWS, a.num_query_tokens) + 7) / 8));
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((std::min(EX_ROWS, a.num_query_tokens) + 31) / 32));
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute at{};

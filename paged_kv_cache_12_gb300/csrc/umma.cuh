@@ -49,9 +49,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
-// Warp-collective, for an M = 64 accumulator (16 rows per warp) of 64 or 48
-// columns: thread i < 16 gets lane (lane base of `taddr`) + i, the first half
-// of the columns; thread i + 16 the same lane, the second half.
+// Warp-collective, for an M = 64 accumulator (16 rows per warp) of 64 columns:
+// thread i < 16 gets lane (lane base of `taddr`) + i, columns col .. col + 31;
+// thread i + 16 the same lane, columns col + 32 .. col + 63.
 __device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, float (&s)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
@@ -63,6 +63,8 @@ __device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, float (&s)[32]) {
           "=f"(s[24]), "=f"(s[25]), "=f"(s[26]), "=f"(s[27]), "=f"(s[28]), "=f"(s[29]), "=f"(s[30]), "=f"(s[31])
         : "r"(taddr));
 }
+
+// The same for 48 columns, 24 each.
 __device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, float (&s)[24]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "

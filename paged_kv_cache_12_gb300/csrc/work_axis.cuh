@@ -21,7 +21,10 @@
 //                           every thread of the block)
 //   num_seqs, cuts          sequences; [AXIS_MAX_CTAS] what a cut row tile's merge
 //                           needs, written by the CTA whose range begins in it
-//   cut_row, cut_rows       (w, r): a row tile's first output row and its rows
+//   cut_rows(w, r)          rows of a row tile
+//   first_row(w, r)         its first row in the output
+//   first_tiles(w, r)       KV tiles that its first rows see (where the merge
+//                           treats a row tile's rows alike: row_tiles)
 #pragma once
 
 #include <stdint.h>
@@ -40,10 +43,12 @@ struct Plan {
 
 // A row tile whose first two pieces are CTA k - 1's and CTA k's, in cuts[k];
 // rows = 0 where there is none (the range begins with a row tile, or in one
-// that an earlier range cuts as well).
+// that an earlier range cuts as well).  All that the merge needs of it.
 struct Cut {
-    long long s, total;   // its first unit; units of the axis
-    int seq, r, rows, ntiles;
+    long long s, total;        // its first unit; units of the axis
+    long long row0;            // its first row in the output
+    int rows, ntiles, ntiles1; // rows; KV tiles, and those its first rows see
+    int pad;
 };
 
 // First unit of CTA k's range; `parts` = min(CTAs, total) CTAs have one, of at
@@ -136,9 +141,10 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         Cut cut;
         cut.s = s + a.start(w, r);
         cut.total = total;
-        cut.seq = i;
-        cut.r = r;
+        cut.row0 = a.first_row(w, r);
         cut.ntiles = a.row_tiles(w, r);
+        cut.ntiles1 = a.first_tiles(w, r);
+        cut.pad = 0;
         const long long first = cut.s + P::COST;
         const bool here = cta > 0 && first < u0 && u0 < first + cut.ntiles && range_begin(total, cta - 1, parts) <= first;
         cut.rows = here ? a.cut_rows(w, r) : 0;
