@@ -28,7 +28,7 @@ struct LatentArgs {
     int *status;            // [AXIS_MAX_CTAS] nonzero: the CTA gave up waiting
     Cut *cuts;              // [AXIS_MAX_CTAS]
     float2 *ml;             // [2 AXIS_MAX_CTAS][LT_ROWS] maximum (log2 units) and sum of a partial row
-    float *o;               // [2 AXIS_MAX_CTAS][LT_ROWS][LC] its unnormalised output
+    float4 *o;              // [2 AXIS_MAX_CTAS][LT_ROWS * LC / 4] its unnormalised output (see partial_at)
 
     // ---- the work axis
     static constexpr int COST = 1;
@@ -84,6 +84,12 @@ __device__ __forceinline__ uint16_t to_bits(float x) {
         return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
+// Where a softmax thread keeps four dims (32 k + 4 j ..) of its row's half, in
+// float4: a store of the warp's lanes (16 rows x 2 halves) is one run of 512 bytes.
+__device__ __forceinline__ long long partial_at(int slot, int quarter, int k, int j, int lane) {
+    return (((long long)slot * 4 + quarter) * 8 + k) * 8 * 32 + j * 32 + lane;
+}
+
 // ------------------------------------------------------------------ the kernel
 
 constexpr int LT_GROUP = 9 * 1024;            // 8 rows of 576 elements: nine 128-byte-swizzled blocks of 64 columns
@@ -132,31 +138,39 @@ struct LtMaps {
     CUtensorMap kv, q;
 };
 
-// A role's bounded wait, the outcome shared by the warp (or one lane's own).
+// A role's bounded wait, the outcome shared by the warp (or one lane's own).  A
+// barrier that is ready costs one test; the flag of a role that gave up is looked
+// at only before waiting.
 struct Waiter {
     volatile int *abort_flag;
     long long limit;
     bool ok = true;
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+        return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait_bounded(bar, parity, limit));
+    }
     __device__ __forceinline__ bool warp(const uint64_t &bar, int parity) {
-        const bool got = ok && !*abort_flag && mbar_wait_bounded(smem_u32(&bar), (uint32_t)(parity & 1), limit);
-        ok = __all_sync(0xffffffffu, got);
+        ok = __all_sync(0xffffffffu, ok && wait(smem_u32(&bar), (uint32_t)(parity & 1)));
         if (!ok) *abort_flag = 1;
         return ok;
     }
     __device__ __forceinline__ bool lane(const uint64_t &bar, int parity) {
-        ok = ok && !*abort_flag && mbar_wait_bounded(smem_u32(&bar), (uint32_t)(parity & 1), limit);
+        ok = ok && wait(smem_u32(&bar), (uint32_t)(parity & 1));
         if (!ok) *abort_flag = 1;
         return ok;
     }
 };
 
-// The producer warp: lane j copies tokens 8 j .. 8 j + 7 of a tile, lanes 8 .. 15
-// the query rows.  A quantised tile goes in steps of 16 tokens into the staging
-// ring, a group of eight rows (5248 bytes, consecutive in its block) per copy:
-// with a tensor map per part of a row a step took eight copies, and issuing them
-// was what bound the kernel (3600 clocks a tile of 48 tokens).  The next tile's rows are fetched into L2 while both
-// stages are full: 100 x 8192 tokens 167 -> 164 us, 128 heads 237 -> 229 us; two,
-// three or four tiles ahead gain less and less.
+// One arrival for a warp, after all its lanes' accesses (an arrival per thread
+// is 32 atomics on one word, and they hold up the shared-memory pipe).
+__device__ __forceinline__ void arrive_warp(uint64_t &bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
+}
+
+// The producer warp of a 16-bit cache: lane j copies tokens 8 j .. 8 j + 7 of a
+// tile, lanes 8 .. 15 the query rows.  The next tile's rows are fetched into L2
+// while both stages are full: 100 x 8192 tokens 167 -> 164 us, 128 heads 237 -> 229
+// us; two, three or four tiles ahead gain less and less.
 template <int KV>
 __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p,
                         const LtMaps &maps) {
@@ -165,7 +179,7 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
     const uint32_t base = smem_u32(smem);
     const uint64_t first = policy_evict_first(), keep = policy_evict_normal();
     Waiter w{&c.abort, a.wait_limit};
-    int cnt = 0, steps = 0, pieces = 0;
+    int cnt = 0, pieces = 0;
     while (w.ok && p.next()) {
         const int32_t *row = a.block_tables + (long long)p.seq * a.mbps;
         if (!w.warp(c.qempty, pieces + 1)) break;
@@ -175,57 +189,92 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
             tma_load_3d(base + (lane - 8) * LT_GROUP, &maps.q, 0, (int)a.first_row(p.w, p.r) + 8 * (lane - 8), 0,
                         smem_u32(&c.qfull), keep);
         ++pieces;
-        for (int t = p.t0; t < p.t1 && w.ok; ++t, ++cnt) {
+        for (int t = p.t0; t < p.t1; ++t, ++cnt) {
             const int tok = t * L::TOK + 8 * lane, st = cnt & 1;
             const bool mine = lane < L::TOK / 8 && tok < p.w.L;
             const int32_t blk = mine ? __ldg(row + a.entry_of(tok)) : 0;
-            // lanes 8 ..: a group of the next tile, to be fetched into L2
+            // lanes 8 .. 15: a group of the next tile, to be fetched into L2
             const int ntok = tok + L::TOK - 64;
-            const bool ahead = lane >= 8 && lane < 8 + L::TOK / 8 && t + 1 < p.t1 && ntok < p.w.L;
+            const bool ahead = lane >= 8 && lane < 16 && t + 1 < p.t1 && ntok < p.w.L;
             const int32_t nblk = ahead ? __ldg(row + a.entry_of(ntok)) : -1;
             const bool bad = __any_sync(0xffffffffu, mine && (blk < 0 || blk >= a.num_blocks));
             const unsigned boxes = __ballot_sync(0xffffffffu, mine && !bad);
-            const int y = (blk << a.bs_log2) + a.offset_of(tok);
             if (bad && lane == 0) *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) = p.local + 1;
-            if constexpr (L::F8) {
-                for (int k = 0; k < L::TOK / L8_STEP; ++k, ++steps) {
-                    const int s = steps % L8_SLOTS, j = lane - 2 * k;   // groups 2 k and 2 k + 1 of the tile
-                    if (!w.warp(c.empty8[s], steps / L8_SLOTS + 1)) break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(smem_u32(&c.full8[s]), (uint32_t)(__popc(boxes >> (2 * k) & 3u) * L8_GROUP));
-                    __syncwarp();
-                    if ((j == 0 || j == 1) && (boxes >> lane & 1u))
-                        bulk_load(base + L::OFF_8 + (2 * s + j) * L8_GROUP, a.cache + (long long)y * LROW8, L8_GROUP,
-                                  smem_u32(&c.full8[s]));
-                    __syncwarp();
-                }
-            } else {
-                if (!w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
-                if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]), (uint32_t)(__popc(boxes) * LT_GROUP));
-                __syncwarp();
-                if (boxes >> lane & 1u)
-                    tma_load_3d(base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP, &maps.kv, 0, y, 0,
-                                smem_u32(&c.kvfull[st]), first);
-            }
-            if (nblk >= 0 && nblk < a.num_blocks) {
-                const int ny = (nblk << a.bs_log2) + a.offset_of(ntok);
-                if constexpr (L::F8)
-                    bulk_prefetch(a.cache + (long long)ny * LROW8, L8_GROUP);
-                else
-                    tma_prefetch_3d(&maps.kv, 0, ny, 0);
-            }
+            if (!w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
+            if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]), (uint32_t)(__popc(boxes) * LT_GROUP));
+            __syncwarp();
+            if (boxes >> lane & 1u)
+                tma_load_3d(base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP, &maps.kv, 0,
+                            (blk << a.bs_log2) + a.offset_of(tok), 0, smem_u32(&c.kvfull[st]), first);
+            if (nblk >= 0 && nblk < a.num_blocks)
+                tma_prefetch_3d(&maps.kv, 0, (nblk << a.bs_log2) + a.offset_of(ntok), 0);
             __syncwarp();
         }
     }
     // the last copies into every buffer have landed before the CTA leaves
-    if constexpr (L::F8) {
-        for (int s = 0; s < L8_SLOTS; ++s)
-            if (steps > s)
-                mbar_wait_bounded(smem_u32(&c.full8[s]), (uint32_t)(((steps - 1 - s) / L8_SLOTS) & 1), WAIT_LIMIT);
-    } else {
-        for (int s = 0; s < 2; ++s)
-            if (cnt > s) mbar_wait_bounded(smem_u32(&c.kvfull[s]), (uint32_t)(((cnt - 1 - s) / 2) & 1), WAIT_LIMIT);
+    for (int s = 0; s < 2; ++s)
+        if (cnt > s) mbar_wait_bounded(smem_u32(&c.kvfull[s]), (uint32_t)(((cnt - 1 - s) / 2) & 1), WAIT_LIMIT);
+    if (pieces) mbar_wait_bounded(smem_u32(&c.qfull), (uint32_t)((pieces - 1) & 1), WAIT_LIMIT);
+}
+
+// The producer warp of a quantised cache: steps of 16 tokens (two groups of
+// eight rows, 5248 bytes each, consecutive in their block) into the staging ring.
+// The ring holds only a tile, so the time from a freed slot to its next rows
+// counts: block ids are loaded 32 groups at a time, a batch early, and a batch's
+// rows are fetched into L2 when its ids are first used.  (Ids loaded per step
+// kept the warp waiting for 1500 clocks a step, whether by lane or queued in a
+// thread's registers, since moving a register waits for its load: 123 to 140 us
+// for four new tokens of 100 sequences.)
+template <int KV>
+__device__ void lt_load8(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p,
+                         const LtMaps &maps) {
+    using L = Lt<KV>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_u32(smem);
+    const uint64_t keep = policy_evict_normal();
+    Waiter w{&c.abort, a.wait_limit};
+    int steps = 0, pieces = 0;
+    while (w.ok && p.next()) {
+        const int32_t *row = a.block_tables + (long long)p.seq * a.mbps;
+        const int g0 = p.t0 * (L::TOK / 8), groups = (p.t1 - p.t0) * (L::TOK / 8);   // of the piece
+        const int with = min(groups, (p.w.L + 7) / 8 - g0);                            // those with tokens
+        auto ids = [&](int g) { return g + lane < with ? __ldg(row + a.entry_of(8 * (g0 + g + lane))) : 0; };
+        // lane j's group of a batch: its rows in the cache, null if its id is out of range or it has no tokens
+        auto rows_of = [&](int32_t id, int g) {
+            const bool in = g < with && id >= 0 && id < a.num_blocks;
+            return in ? a.cache + (((long long)id << a.bs_log2) + a.offset_of(8 * (g0 + g))) * LROW8 : nullptr;
+        };
+        int32_t next_ids = ids(0);
+        if (!w.warp(c.qempty, pieces + 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.qfull), LT_Q);
+        __syncwarp();
+        if (lane < 8)
+            tma_load_3d(base + lane * LT_GROUP, &maps.q, 0, (int)a.first_row(p.w, p.r) + 8 * lane, 0,
+                        smem_u32(&c.qfull), keep);
+        ++pieces;
+        const uint8_t *mine = nullptr;
+        for (int g = 0; g < groups; g += 2, ++steps) {
+            if ((g & 31) == 0) {   // the next batch
+                mine = rows_of(next_ids, g + lane);
+                if (__any_sync(0xffffffffu, !mine && g + lane < with) && lane == 0)
+                    *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) = p.local + 1;
+                next_ids = ids(g + 32);
+                if (mine) bulk_prefetch(mine, L8_GROUP);
+            }
+            const int s = steps % L8_SLOTS, j = lane - (g & 31);   // lanes of the step's groups: j = 0, 1
+            if (!w.warp(c.empty8[s], steps / L8_SLOTS + 1)) break;
+            const unsigned there = __ballot_sync(0xffffffffu, (j == 0 || j == 1) && mine);
+            if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.full8[s]), (uint32_t)(__popc(there) * L8_GROUP));
+            __syncwarp();
+            if (there >> lane & 1u)
+                bulk_load(base + L::OFF_8 + (2 * s + j) * L8_GROUP, mine, L8_GROUP, smem_u32(&c.full8[s]));
+            __syncwarp();
+        }
     }
+    // the last copies into every buffer have landed before the CTA leaves
+    for (int s = 0; s < L8_SLOTS; ++s)
+        if (steps > s)
+            mbar_wait_bounded(smem_u32(&c.full8[s]), (uint32_t)(((steps - 1 - s) / L8_SLOTS) & 1), WAIT_LIMIT);
     if (pieces) mbar_wait_bounded(smem_u32(&c.qfull), (uint32_t)((pieces - 1) & 1), WAIT_LIMIT);
 }
 
@@ -234,9 +283,11 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
 // a 16-bit copy would have written.  Lane l turns the codes 16 l .. 16 l + 15 into
 // two 16-byte chunks; lanes of odd 64-element blocks store their second chunk
 // first, so that eight lanes of a store cover all banks.  Rows past the context
-// become zeros (their probabilities are 0).  (Loading the rows from global memory
-// into registers instead of staging them: the loads in flight held up the stores
-// behind them, 130 us for the step that takes __ here.)
+// become zeros (their probabilities are 0).  Other shapes were slower (a step of
+// four new tokens of 100 sequences, 123 us here): sixteen warps of a row each, 141;
+// twelve of four rows of one step, 152; rows loaded from global memory into
+// registers instead of staged, 130 (the loads in flight held up the stores behind
+// them).
 template <int KV>
 __device__ void lt_convert(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p) {
     using L = Lt<KV>;
@@ -426,7 +477,7 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
                 }
                 l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
             }
-            mbar_arrive(smem_u32(&c.sfree[st]));
+            arrive_warp(c.sfree[st]);
             // P is free, and O up to date, once the previous product is done
             if (n > 0 && !w.warp(c.pvdone, n - 1)) break;
             if (live) {
@@ -459,7 +510,7 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
             }
             fence_proxy_async_smem();
             tc_fence_before_sync();
-            mbar_arrive(smem_u32(&c.pfull));
+            arrive_warp(c.pfull);
         }
         // ---- the piece's rows: finished, or a partial row
         if (!w.ok || !w.warp(c.pvdone, n - 1)) break;
@@ -471,7 +522,6 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
             const bool whole = p.whole();
             const float inv = 1.f / l;
             uint16_t *orow = a.out + (a.first_row(p.w, p.r) + m) * LC + 256 * half;
-            float *part = a.o + ((long long)p.slot() * LT_ROWS + m) * LC + 256 * half;
             if (!whole && mine && half == 0) a.ml[p.slot() * LT_ROWS + m] = make_float2(mrun, l);
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
@@ -491,7 +541,7 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
                 } else if (mine) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<uint4 *>(part + 32 * k + j) =
+                        *reinterpret_cast<uint4 *>(a.o + partial_at(p.slot(), q, k, j / 4, lane)) =
                             make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 }
                 __syncwarp();   // the next load is the whole warp's
@@ -514,13 +564,13 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
             mbar_init(smem_u32(&c.kvfull[s]), L::F8 ? L8_WARPS : 1);
             mbar_init(smem_u32(&c.kvempty[s]), 1);
             mbar_init(smem_u32(&c.sfull[s]), 1);
-            mbar_init(smem_u32(&c.sfree[s]), 128);
+            mbar_init(smem_u32(&c.sfree[s]), 4);
         }
         for (int s = 0; s < L8_SLOTS; ++s) {
             mbar_init(smem_u32(&c.full8[s]), 1);
             mbar_init(smem_u32(&c.empty8[s]), L8_WARPS);
         }
-        mbar_init(smem_u32(&c.pfull), 128);
+        mbar_init(smem_u32(&c.pfull), 4);
         mbar_init(smem_u32(&c.pvdone), 1);
         mbar_init(smem_u32(&c.qfull), 1);
         mbar_init(smem_u32(&c.qempty), 2);
@@ -544,7 +594,10 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
         Walk<typename L::Args> p(a, plan);
         if (warp == 0) {
-            lt_load<KV>(smem, c, a, p, maps);
+            if constexpr (L::F8)
+                lt_load8<KV>(smem, c, a, p, maps);
+            else
+                lt_load<KV>(smem, c, a, p, maps);
         } else if (warp < 4) {
             if (elect_one()) lt_mma<KV>(smem, c, a, p, tmem, warp);
             __syncwarp();
@@ -566,89 +619,56 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
 
 // ------------------------------------------------------------------ merge
 
-// Rows of the cut row tiles from their pieces' partial rows; blockIdx.x is the
-// CTA whose range begins in the row tile.  Few pieces (two as a rule): block y
-// takes rows 8 y .. 8 y + 7, a warp each.  Many (a few long sequences): it takes
-// rows y, y + 8, .., its warps every eighth piece.  When a CTA of the first
-// kernel gave up, every row becomes NaN.
-constexpr int MG_FEW = 16, MG_BLOCKS = 8;
-
-// Pieces first, first + step, .. of a row: adds their weighted outputs, 16 dims a lane.
-struct RowSum {
-    float4 o[4];
-    float l;
-};
-__device__ __forceinline__ RowSum add_pieces(const float2 *ml, const float *o, const Pieces &pc, int m, float mu, int first,
-                                             int step) {
-    const int lane = threadIdx.x & 31;
-    RowSum x{};
-#pragma unroll 4
-    for (int k = pc.k0 + first; k <= pc.k1; k += step) {
-        const long long at = (long long)pc.slot(k) * LT_ROWS + m;
-        const float2 v = ml[at];
-        const float wt = fast_exp2(v.x - mu);
-        const float4 *src = reinterpret_cast<const float4 *>(o + at * LC) + lane;
-        x.l = fmaf(v.y, wt, x.l);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 y = src[32 * j];
-            x.o[j].x = fmaf(y.x, wt, x.o[j].x);
-            x.o[j].y = fmaf(y.y, wt, x.o[j].y);
-            x.o[j].z = fmaf(y.z, wt, x.o[j].z);
-            x.o[j].w = fmaf(y.w, wt, x.o[j].w);
-        }
-    }
-    return x;
-}
+// Rows of the cut row tiles from their pieces' partial rows.  blockIdx.x is the
+// CTA whose range begins in the row tile; a warp takes a quarter of its rows (16,
+// two lanes each) and eight of a half's 256 dims, in the order in which the
+// softmax warps left them.  When a CTA of the first kernel gave up, every row
+// becomes NaN.
+constexpr int MG_WARPS = 8, MG_BLOCKS = 4 * 32 / MG_WARPS;
 
 template <int KV>
-__global__ void __launch_bounds__(256) latent_merge_kernel(const typename Lt<KV>::Args a, int ctas) {
+__global__ void __launch_bounds__(32 * MG_WARPS) latent_merge_kernel(const typename Lt<KV>::Args a, int ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ RowSum part[8][32];
-    const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x, lane = threadIdx.x & 31;
     const Cut cut = a.cuts[cta];
-    if (cut.rows == 0 && (cta || blockIdx.y)) return;
+    const int unit = blockIdx.y * MG_WARPS + (threadIdx.x >> 5), quarter = unit >> 5;
+    if (16 * (blockIdx.y * MG_WARPS >> 5) >= cut.rows && (cta || blockIdx.y)) return;   // the whole block
     const bool failed = any_gave_up(a.status, ctas);
     if (cta == 0 && blockIdx.y == 0) {
         if (threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
         if (failed) fill_rows(a.out, 0, (long long)a.num_query_tokens * a.H * (LC / 8), KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     }
-    if (failed || cut.rows == 0) return;
+    const int m = 16 * quarter + (lane & 15), k8 = (unit & 31) >> 2, j = 2 * (unit & 3);
+    if (failed || m >= cut.rows) return;
     const Pieces pc(cut, cta, cut.ntiles, Lt<KV>::Args::COST, ctas);
-    const bool few = pc.k1 - pc.k0 < MG_FEW;
-    const int step = few ? cut.rows : MG_BLOCKS;   // one row a warp, or rows y, y + 8, .. of the block
-    for (int m = few ? blockIdx.y * 8 + warp : blockIdx.y; m < cut.rows; m += step) {
-        float M = -INFINITY;
-        for (int k = pc.k0 + lane; k <= pc.k1; k += 32) M = fmaxf(M, a.ml[(long long)pc.slot(k) * LT_ROWS + m].x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        const float mu = M == -INFINITY ? 0.f : M;
-        RowSum x = add_pieces(a.ml, a.o, pc, m, mu, few ? 0 : warp, few ? 1 : 8);
-        if (!few) {
-            part[warp][lane] = x;
-            __syncthreads();
-            if (warp == 0)
-                for (int k = 1; k < 8; ++k) {
-                    const RowSum y = part[k][lane];
-                    x.l += y.l;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x.o[j].x += y.o[j].x;
-                        x.o[j].y += y.o[j].y;
-                        x.o[j].z += y.o[j].z;
-                        x.o[j].w += y.o[j].w;
-                    }
-                }
-            __syncthreads();
-            if (warp) continue;
-        }
-        const float inv = 1.f / x.l;
-        uint2 *out = reinterpret_cast<uint2 *>(a.out + (cut.row0 + m) * LC) + lane;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            out[32 * j] = make_uint2((uint32_t)to_bits<KV>(x.o[j].x * inv) | ((uint32_t)to_bits<KV>(x.o[j].y * inv) << 16),
-                                     (uint32_t)to_bits<KV>(x.o[j].z * inv) | ((uint32_t)to_bits<KV>(x.o[j].w * inv) << 16));
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int k = pc.k0; k <= pc.k1; ++k) M = fmaxf(M, a.ml[pc.slot(k) * LT_ROWS + m].x);
+    const float mu = M == -INFINITY ? 0.f : M;
+    float acc[8] = {}, l = 0.f;
+#pragma unroll 8
+    for (int k = pc.k0; k <= pc.k1; ++k) {
+        const int slot = pc.slot(k);
+        const float2 ml = a.ml[slot * LT_ROWS + m];
+        const float4 x = a.o[partial_at(slot, quarter, k8, j, lane)], y = a.o[partial_at(slot, quarter, k8, j + 1, lane)];
+        const float wt = fast_exp2(ml.x - mu);
+        l = fmaf(ml.y, wt, l);
+        acc[0] = fmaf(x.x, wt, acc[0]);
+        acc[1] = fmaf(x.y, wt, acc[1]);
+        acc[2] = fmaf(x.z, wt, acc[2]);
+        acc[3] = fmaf(x.w, wt, acc[3]);
+        acc[4] = fmaf(y.x, wt, acc[4]);
+        acc[5] = fmaf(y.y, wt, acc[5]);
+        acc[6] = fmaf(y.z, wt, acc[6]);
+        acc[7] = fmaf(y.w, wt, acc[7]);
     }
+    const float inv = 1.f / l;
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (uint32_t)to_bits<KV>(acc[2 * i] * inv) | ((uint32_t)to_bits<KV>(acc[2 * i + 1] * inv) << 16);
+    *reinterpret_cast<uint4 *>(a.out + (cut.row0 + m) * LC + 256 * (lane >> 4) + 32 * k8 + 4 * j) =
+        make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // ------------------------------------------------------------------ launch
@@ -706,7 +726,7 @@ template <int KV>
 int launch_merge(const typename Lt<KV>::Args &a, int ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas, MG_BLOCKS);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(32 * MG_WARPS);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // launched while the first kernel drains
@@ -756,7 +776,7 @@ int run_latent(void *out, const void *query, const void *cache, const int32_t *b
     a.status = reinterpret_cast<int *>(ws + lay.status);
     a.cuts = reinterpret_cast<Cut *>(ws + lay.cuts);
     a.ml = reinterpret_cast<float2 *>(ws + lay.ml);
-    a.o = reinterpret_cast<float *>(ws + lay.o);
+    a.o = reinterpret_cast<float4 *>(ws + lay.o);
     return launch_latent<KV>(a, st);
 }
 

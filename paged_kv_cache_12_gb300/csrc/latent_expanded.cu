@@ -392,7 +392,8 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
             tmem_wait_st();
             if (zeroed) fence_proxy_async_smem();
             tc_fence_before_sync();
-            mbar_arrive(smem_u32(&c.pfull[x]));
+            __syncwarp();   // one arrival a warp: 32 atomics on one word hold up the shared-memory pipe
+            if (lane == 0) mbar_arrive(smem_u32(&c.pfull[x]));
             ++sc;
         }
         if (!ok || !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1))) break;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
             mbar_init(smem_u32(&c.qfull[x]), 1);
             mbar_init(smem_u32(&c.qempty[x]), 1);
             mbar_init(smem_u32(&c.sfull[x]), 1);
-            mbar_init(smem_u32(&c.pfull[x]), EX_HALF);
+            mbar_init(smem_u32(&c.pfull[x]), EX_HALF / 32);
             mbar_init(smem_u32(&c.pvdone[x]), 1);
         }
         mbar_init(smem_u32(&c.done), 1);
