@@ -334,13 +334,14 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
 #pragma unroll
                 for (int k = 0; k < EX_TOK; ++k) s[k] = t0 + k < vis ? s[k] : -INFINITY;
             }
-            float mp[8];
+            float mp[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mp[j] = s[j];
+            for (int k = 4; k + 8 <= EX_TOK; k += 8)
 #pragma unroll
-            for (int k = 8; k < EX_TOK; ++k) mp[k & 7] = fmaxf(mp[k & 7], s[k]);
-            const float mx = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                                   fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+                for (int j = 0; j < 4; ++j) mp[j] = max3(mp[j], s[k + 2 * j], s[k + 2 * j + 1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mp[j] = fmaxf(mp[j], s[EX_TOK - 4 + j]);
+            const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
             // decided per row, done warp-wide (tensor-memory accesses are the
             // whole warp's); rows that do not grow scale by exactly 1
             const bool grow = mx > mrun + RESCALE_THRESHOLD;
@@ -378,23 +379,27 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
                 zeroed = true;
             }
             const float mu = mrun == -INFINITY ? 0.f : mrun;   // a row that has seen nothing yet
-            float lp[8];
+            const uint64_t sl2x2 = pair_of(sl2, sl2), negm = pair_of(-mu, -mu);
+            uint64_t lp[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) lp[j] = 0.f;
+            for (int j = 0; j < 4; ++j) lp[j] = 0;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 uint32_t r[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    const float e0 = fast_exp2(fmaf(s[64 * q + 2 * k], sl2, -mu));
-                    const float e1 = fast_exp2(fmaf(s[64 * q + 2 * k + 1], sl2, -mu));
-                    lp[(2 * k) & 7] += e0;
-                    lp[(2 * k + 1) & 7] += e1;
+                    float e0, e1;
+                    pair_parts(pair_fma(pair_of(s[64 * q + 2 * k], s[64 * q + 2 * k + 1]), sl2x2, negm), e0, e1);
+                    e0 = fast_exp2(e0);
+                    e1 = fast_exp2(e1);
+                    lp[k & 3] = pair_add(lp[k & 3], pair_of(e0, e1));
                     r[k] = pack_p<KV>(e0, e1);
                 }
                 tmem_st32(trow + scol + 32 * q, r);
             }
-            l += ((lp[0] + lp[1]) + (lp[2] + lp[3])) + ((lp[4] + lp[5]) + (lp[6] + lp[7]));
+            float l0, l1;
+            pair_parts(pair_add(pair_add(lp[0], lp[1]), pair_add(lp[2], lp[3])), l0, l1);
+            l += l0 + l1;
             tmem_wait_st();
             if (zeroed) fence_proxy_async_smem();
             tc_fence_before_sync();

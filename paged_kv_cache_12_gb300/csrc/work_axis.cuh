@@ -198,16 +198,17 @@ struct Walk {
 // The pieces of a cut row tile that hold its first `ntiles` KV tiles: CTAs k0
 // (= the cut's - 1) .. k1, and the slot of each one's partial rows.
 struct Pieces {
-    int k0, k1, parts;
-    long long s, total;
-    __device__ Pieces(const Cut &cut, int cta, int ntiles, int cost, int ctas) : k0(cta - 1), s(cut.s), total(cut.total) {
-        parts = (int)min((long long)ctas, total);
-        const long long last = s + cost + ntiles - 1;
-        k1 = (int)(last * parts / total);
-        while (range_begin(total, k1 + 1, parts) <= last) ++k1;
-        while (range_begin(total, k1, parts) > last) --k1;
+    int k0, k1, first;
+    __device__ Pieces(const Cut &cut, int cta, int ntiles, int cost, int ctas) : k0(cta - 1) {
+        const int parts = (int)min((long long)ctas, cut.total);
+        const long long last = cut.s + cost + ntiles - 1;
+        k1 = (int)(last * parts / cut.total);
+        while (range_begin(cut.total, k1 + 1, parts) <= last) ++k1;
+        while (range_begin(cut.total, k1, parts) > last) --k1;
+        first = 2 * k0 + (cut.s < range_begin(cut.total, k0, parts) ? 0 : 1);
     }
-    __device__ int slot(int k) const { return 2 * k + (s < range_begin(total, k, parts) ? 0 : 1); }
+    // (the row tile began before every later piece's range)
+    __device__ int slot(int k) const { return k == k0 ? first : 2 * k; }
 };
 
 // Whether a CTA of the first kernel gave up (called by the whole block).
