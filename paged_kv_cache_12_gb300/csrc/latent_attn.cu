@@ -110,6 +110,8 @@ template <int KV>
 struct Lt {
     static constexpr bool F8 = KV == PA_KV_FP8_E4M3;
     static constexpr int TOK = F8 ? 48 : 64;   // tokens of a KV tile
+    // a stage is freed in parts, as the products with the values pass them
+    static constexpr int PARTS = F8 ? 3 : 2, PART_TOK = TOK / PARTS;
     static constexpr int THREADS = F8 ? 256 + 32 * L8_WARPS : 256;
     static constexpr int STAGE = TOK / 8 * LT_GROUP;
     static constexpr int OFF_KV = LT_Q;
@@ -122,7 +124,7 @@ struct Lt {
 };
 
 struct LtCtrl {
-    uint64_t kvfull[2], kvempty[2], sfull[2], sfree[2], pfull, pvdone, qfull, qempty, done;
+    uint64_t kvfull[2], kvempty[2][3], sfull[2], sfree[2], pfull, pvdone, qfull, qempty, done;
     uint64_t full8[L8_SLOTS], empty8[L8_SLOTS];
     uint32_t tmem;
     int abort;
@@ -200,12 +202,22 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
             const bool bad = __any_sync(0xffffffffu, mine && (blk < 0 || blk >= a.num_blocks));
             const unsigned boxes = __ballot_sync(0xffffffffu, mine && !bad);
             if (bad && lane == 0) *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) = p.local + 1;
-            if (!w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
-            if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]), (uint32_t)(__popc(boxes) * LT_GROUP));
-            __syncwarp();
-            if (boxes >> lane & 1u)
-                tma_load_3d(base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP, &maps.kv, 0,
-                            (blk << a.bs_log2) + a.offset_of(tok), 0, smem_u32(&c.kvfull[st]), first);
+#pragma unroll
+            for (int part = 0; part < L::PARTS; ++part) {
+                constexpr int N = L::PART_TOK / 8;   // groups of a part
+                if (!w.warp(c.kvempty[st][part], (cnt >> 1) + 1)) break;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]),
+                                          (uint32_t)(__popc(boxes >> (part * N) & ((1u << N) - 1)) * LT_GROUP));
+                __syncwarp();
+                if (lane / N == part && (boxes >> lane & 1u))
+                    tma_load_3d(base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP, &maps.kv, 0,
+                                (blk << a.bs_log2) + a.offset_of(tok), 0, smem_u32(&c.kvfull[st]), first);
+            }
+            if (!w.ok) {   // a part may be on its way: the stage counts as sent below
+                ++cnt;
+                break;
+            }
             if (nblk >= 0 && nblk < a.num_blocks)
                 tma_prefetch_3d(&maps.kv, 0, (nblk << a.bs_log2) + a.offset_of(ntok), 0);
             __syncwarp();
@@ -302,7 +314,6 @@ __device__ void lt_convert(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
     while (w.ok && p.next()) {
         for (int t = p.t0; t < p.t1; ++t, ++cnt) {
             const int st = cnt & 1, left = p.w.L - t * L::TOK;   // tokens from the tile's first on
-            if (!w.warp(c.kvempty[st], (cnt >> 1) + 1)) break;
             uint8_t *stage = smem + L::OFF_KV + st * L::STAGE;
             for (int k = 0; k < L::TOK / L8_STEP; ++k, ++steps) {
                 const int s = steps % L8_SLOTS;
@@ -337,6 +348,7 @@ __device__ void lt_convert(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
                     }
                 }
                 if (lane == 0) mbar_arrive(smem_u32(&c.empty8[s]));   // (after the vote: every lane has its codes)
+                if (!w.warp(c.kvempty[st][k], (cnt >> 1) + 1)) break;
                 uint8_t *dst = stage + 2 * k * LT_GROUP;
 #pragma unroll
                 for (int i = 0; i < 2; ++i, dst += LT_GROUP) {
@@ -404,9 +416,10 @@ __device__ void lt_mma(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a,
                     for (int h = 0; h < 2; ++h)
                         umma_f16(tmem + (h ? LT_HI : 0u), dp + (uint64_t)((k * 32) >> 4),
                                  dv + (uint64_t)((k * 2 * LT_GROUP + h * 4096) >> 4), ID, t > p.t0 || k > 0 ? 1u : 0u);
+                    if ((k + 1) % (L::PART_TOK / 16) == 0)
+                        umma_commit(smem_u32(&c.kvempty[st][k / (L::PART_TOK / 16)]));
                 }
                 umma_commit(smem_u32(&c.pvdone));
-                umma_commit(smem_u32(&c.kvempty[st]));
             }
         }
     }
@@ -561,8 +574,8 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&c.kvfull[s]), L::F8 ? L8_WARPS : 1);
-            mbar_init(smem_u32(&c.kvempty[s]), 1);
+            mbar_init(smem_u32(&c.kvfull[s]), L::F8 ? L8_WARPS : L::PARTS);
+            for (int part = 0; part < 3; ++part) mbar_init(smem_u32(&c.kvempty[s][part]), 1);
             mbar_init(smem_u32(&c.sfull[s]), 1);
             mbar_init(smem_u32(&c.sfree[s]), 4);
         }
