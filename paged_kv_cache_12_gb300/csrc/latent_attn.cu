@@ -31,6 +31,7 @@ struct LatentArgs {
     float4 *o;              // [2 AXIS_MAX_CTAS][LT_ROWS * LC / 4] its unnormalised output (see partial_at)
 
     // ---- the work axis
+    static constexpr int TEAM = 2;   // (a chunk's row tiles see about the same tokens)
     static constexpr int COST = 2;   // 128 heads: 214 us with 1, 209 with 2, 212 with 3, 217 with 6
     struct Seq {
         int L, T, q0;   // context, new tokens, first query token

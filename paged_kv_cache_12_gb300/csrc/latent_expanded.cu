@@ -50,6 +50,7 @@ struct ExpandedArgs {
     float4 *o;              // [2 AXIS_MAX_CTAS][EX_ROWS * EV / 4] its unnormalised output (see partial_at)
 
     // ---- the work axis: row tile r of a sequence is tile r % tiles_per_head of head r / tiles_per_head
+    static constexpr int TEAM = 1;
     static constexpr int COST = 4;   // 600 tokens, 16 heads: 27.6 us with 1, 26.6 with 4, 27.9 with 6
     struct Seq {
         int L, T, q0, k0;

@@ -11,8 +11,15 @@
 // a second kernel merges.  Every CTA derives the cut by itself from the lengths,
 // by one sum over the sequences.
 //
+// Where every sequence has an even number of row tiles over the same KV tiles
+// (P::TEAM = 2), the CTAs work in teams of two: a team takes a range of the axis of
+// every second row tile, and its two CTAs a row tile each of the pairs in it, so
+// that they read the same KV tiles at the same time (the second read comes from
+// L2; one CTA after the other, both came from HBM).
+//
 // A problem P gives
 //   P::COST                 units of a row tile besides its KV tiles
+//   P::TEAM                 1, or 2: see above
 //   P::Seq, seq_work(i)     what is needed of sequence i; Seq::rts row tiles
 //   start(w, r)             first unit of row tile r within its sequence;
 //                           start(w, w.rts) = the sequence's units
@@ -38,20 +45,22 @@ struct Plan {
     long long u0, u1, base;   // this CTA's range; first unit of sequence seq
     long long total;          // units of the axis (0 too if the row offsets are out of order)
     int seq;                  // the sequence in which the range begins
+    int team;                 // CTAs of a team
     int ok;                   // the row offsets are in order
 };
 
-// A row tile whose first two pieces are CTA k - 1's and CTA k's, in cuts[k];
+// A row tile whose first two pieces are the CTA's own and that of the CTA before
+// it (a team before it), in cuts[CTA];
 // rows = 0 where there is none (the range begins with a row tile, or in one
 // that an earlier range cuts as well).  All that the merge needs of it.
 struct Cut {
     long long s, total;        // its first unit; units of the axis
     long long row0;            // its first row in the output
     int rows, ntiles, ntiles1; // rows; KV tiles, and those its first rows see
-    int pad;
+    int team;
 };
 
-// First unit of CTA k's range; `parts` = min(CTAs, total) CTAs have one, of at
+// First unit of team k's range; `parts` = min(teams, total) teams have one, of at
 // least a unit each.
 __device__ __forceinline__ long long range_begin(long long total, int k, int parts) { return total * k / parts; }
 
@@ -74,10 +83,11 @@ __device__ __forceinline__ int sequence_of(const int32_t *start, int n, int row)
     return lo;
 }
 
-// The last row tile of a sequence that starts at or before unit u of it.
+// The last of a team's row tiles (numbered as the axis has them) that starts at
+// or before unit u of the sequence.
 template <class P>
-__device__ __forceinline__ int row_tile_at(const P &a, const typename P::Seq &w, long long u) {
-    int r = 0, hi = w.rts;
+__device__ __forceinline__ int row_tile_at(const P &a, const typename P::Seq &w, int team, long long u) {
+    int r = 0, hi = w.rts / team;
     while (hi - r > 1) {
         const int mid = (r + hi) >> 1;
         if (a.start(w, mid) <= u) r = mid; else hi = mid;
@@ -92,9 +102,15 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     const int per = (a.num_seqs + blockDim.x - 1) / blockDim.x;
     const int i0 = min(a.num_seqs, (int)threadIdx.x * per), i1 = min(a.num_seqs, i0 + per);
+    int team = 1;
+    if constexpr (P::TEAM == 2) {
+        bool even = true;
+        for (int i = i0; ok && i < i1; ++i) even = even && a.seq_work(i).rts % 2 == 0;
+        if (__syncthreads_and(even)) team = 2;
+    }
     auto units = [&](int i) {
         const typename P::Seq w = a.seq_work(i);
-        return a.start(w, w.rts);
+        return a.start(w, w.rts / team);
     };
     long long mine = 0;
     for (int i = i0; ok && i < i1; ++i) mine += units(i);
@@ -107,18 +123,19 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
     if (lane == 31) warp_sums[warp] = upto;
     __syncthreads();
     long long before = 0, total = 0;
-    for (int k = 0; k < nwarps; ++k) {
-        if (k < warp) before += warp_sums[k];
-        total += warp_sums[k];
+    for (int j = 0; j < nwarps; ++j) {
+        if (j < warp) before += warp_sums[j];
+        total += warp_sums[j];
     }
     const long long begin = before + upto - mine, end = before + upto;
-    const int parts = (int)min((long long)gridDim.x, total), cta = blockIdx.x;
-    const long long u0 = cta < parts ? range_begin(total, cta, parts) : 0;
-    const long long u1 = cta < parts ? range_begin(total, cta + 1, parts) : 0;
+    const int parts = (int)min((long long)(gridDim.x / team), total), cta = blockIdx.x, k = cta / team;
+    const long long u0 = k < parts ? range_begin(total, k, parts) : 0;
+    const long long u1 = k < parts ? range_begin(total, k + 1, parts) : 0;
     if (threadIdx.x == 0) {
         plan->u0 = u0;
         plan->u1 = u1;
         plan->total = total;
+        plan->team = team;
         plan->ok = ok;
         if (u0 >= u1) {
             a.cuts[cta].rows = 0;
@@ -137,16 +154,16 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         plan->base = s;
         // the row tile in which the range begins: cut here if a KV tile of it lies on either side
         const typename P::Seq w = a.seq_work(i);
-        const int r = row_tile_at(a, w, u0 - s);
+        const int j = row_tile_at(a, w, team, u0 - s), r = j * team + cta % team;
         Cut cut;
-        cut.s = s + a.start(w, r);
+        cut.s = s + a.start(w, j);
         cut.total = total;
         cut.row0 = a.first_row(w, r);
         cut.ntiles = a.row_tiles(w, r);
         cut.ntiles1 = a.first_tiles(w, r);
-        cut.pad = 0;
+        cut.team = team;
         const long long first = cut.s + P::COST;
-        const bool here = cta > 0 && first < u0 && u0 < first + cut.ntiles && range_begin(total, cta - 1, parts) <= first;
+        const bool here = k > 0 && first < u0 && u0 < first + cut.ntiles && range_begin(total, k - 1, parts) <= first;
         cut.rows = here ? a.cut_rows(w, r) : 0;
         a.cuts[cta] = cut;
     }
@@ -158,29 +175,30 @@ template <class P>
 struct Walk {
     const P &a;
     long long u0, u1, base, s;   // the range; first unit of the sequence, and of row tile r
-    int seq, r;
+    int team, seq, j, r;         // row tile r is the j-th of the team's axis
     typename P::Seq w;
     int t0, t1, ntiles, local;   // the piece: KV tiles [t0, t1) of ntiles; its number in this CTA
 
-    __device__ Walk(const P &args, const Plan &p) : a(args), u0(p.u0), u1(p.u1), base(p.base), seq(p.seq), r(0) {
+    __device__ Walk(const P &args, const Plan &p) : a(args), u0(p.u0), u1(p.u1), base(p.base), team(p.team), seq(p.seq), j(0) {
         local = -1;
         if (u0 >= u1) return;
         w = a.seq_work(seq);
-        r = row_tile_at(a, w, u0 - base) - 1;
+        j = row_tile_at(a, w, team, u0 - base) - 1;
     }
     // The next piece; false at the end of the range.
     __device__ bool next() {
         if (u0 >= u1) return false;
         for (;;) {
-            ++r;
-            while (r >= w.rts) {   // on to the next sequence
-                base += a.start(w, w.rts);
+            ++j;
+            while (j >= w.rts / team) {   // on to the next sequence
+                base += a.start(w, w.rts / team);
                 if (base >= u1 || ++seq >= a.num_seqs) return false;
                 w = a.seq_work(seq);
-                r = 0;
+                j = 0;
             }
-            s = base + a.start(w, r);
+            s = base + a.start(w, j);
             if (s >= u1) return false;
+            r = j * team + (int)blockIdx.x % team;
             ntiles = a.row_tiles(w, r);
             t0 = (int)max(0LL, min((long long)ntiles, u0 - s - P::COST));
             t1 = (int)max(0LL, min((long long)ntiles, u1 - s - P::COST));
@@ -195,20 +213,21 @@ struct Walk {
     __device__ int slot() const { return 2 * (int)blockIdx.x + (s < u0 ? 0 : 1); }
 };
 
-// The pieces of a cut row tile that hold its first `ntiles` KV tiles: CTAs k0
-// (= the cut's - 1) .. k1, and the slot of each one's partial rows.
+// The pieces of a cut row tile that hold its first `ntiles` KV tiles: teams k0
+// (the one before the cut's) .. k1, and the slot of each one's partial rows.
 struct Pieces {
-    int k0, k1, first;
-    __device__ Pieces(const Cut &cut, int cta, int ntiles, int cost, int ctas) : k0(cta - 1) {
-        const int parts = (int)min((long long)ctas, cut.total);
+    int k0, k1, team, member, first;
+    __device__ Pieces(const Cut &cut, int cta, int ntiles, int cost, int ctas)
+        : k0(cta / cut.team - 1), team(cut.team), member(cta % cut.team) {
+        const int parts = (int)min((long long)(ctas / team), cut.total);
         const long long last = cut.s + cost + ntiles - 1;
         k1 = (int)(last * parts / cut.total);
         while (range_begin(cut.total, k1 + 1, parts) <= last) ++k1;
         while (range_begin(cut.total, k1, parts) > last) --k1;
-        first = 2 * k0 + (cut.s < range_begin(cut.total, k0, parts) ? 0 : 1);
+        first = 2 * (k0 * team + member) + (cut.s < range_begin(cut.total, k0, parts) ? 0 : 1);
     }
     // (the row tile began before every later piece's range)
-    __device__ int slot(int k) const { return k == k0 ? first : 2 * k; }
+    __device__ int slot(int k) const { return k == k0 ? first : 2 * (k * team + member); }
 };
 
 // Whether a CTA of the first kernel gave up (called by the whole block).
