@@ -459,8 +459,9 @@ PA_API size_t pa_latent_attention_workspace_size(int num_seqs, int num_query_tok
  * Scores, softmax and sums in fp32; the probabilities are rounded to the
  * cache's 16-bit type for the product with the rows.  Device-side cases as in
  * pa_attention_causal (L = 0 decodes to a zero row, an invalid L, T > L or a
- * block id out of range to NaN rows).  Deterministic.  pa_workspace_status
- * reads the error word. */
+ * block id out of range to NaN rows).  Rows of the cache that a new token does
+ * not see may hold anything, infinities and NaN included: they do not reach its
+ * output.  Deterministic.  pa_workspace_status reads the error word. */
 PA_API int pa_latent_attention(void *out, const void *query, const void *cache, const int32_t *block_tables,
                                const int32_t *context_lens, const int32_t *query_start, int num_seqs,
                                int num_query_tokens, int num_heads, int block_size, int64_t num_blocks,
@@ -490,9 +491,12 @@ PA_API size_t pa_latent_attention_expanded_workspace_size(int num_seqs, int num_
  *            cover of its rows
  *   dtype    PA_KV_F16 or PA_KV_BF16, all tensors; pointers 16-byte aligned
  * A sequence with T > Lk gets NaN rows, and every row is NaN when query_start
- * or kv_start breaks its order or does not end at its row count.  Scores,
- * softmax and sums in fp32.  Deterministic.  pa_workspace_status reads the
- * error word. */
+ * or kv_start breaks its order or does not end at its row count.  Keys and
+ * values that a new token does not see may be infinities or NaN: they do not
+ * reach its output (one that sees a value that is not finite gets a row that is
+ * not finite).  Scores, softmax and sums in fp32, the probabilities rounded to
+ * dtype for the product with the values.  Deterministic.  pa_workspace_status
+ * reads the error word. */
 PA_API int pa_latent_attention_expanded(void *out, const void *query, const void *k_nope, const void *k_rope,
                                         const void *value, const int32_t *query_start, const int32_t *kv_start,
                                         int num_seqs, int num_query_tokens, int num_kv_tokens, int num_heads,

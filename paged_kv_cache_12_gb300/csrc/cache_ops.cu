@@ -150,6 +150,33 @@ int validate_pairs(const int64_t *pairs, int num_pairs, long long num_blocks, cu
     return PA_ERR_STATE;
 }
 
+int validate_starts(const int32_t *start, int n, int end, bool exact, cudaStream_t st) try {
+    std::vector<int32_t> h((size_t)n + 1);
+    if (const int e = copy_to_host(h.data(), start, sizeof(int32_t) * h.size(), st)) return e;
+    if (h[0] != 0 || h[(size_t)n] > end || (exact && h[(size_t)n] != end)) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (h[(size_t)i] > h[(size_t)i + 1]) return PA_ERR_INVALID_ARG;
+    return 0;
+} catch (...) {
+    return PA_ERR_STATE;
+}
+
+int validate_tables(const int32_t *block_tables, const int64_t *last, int num_seqs, int mbps, int block_size,
+                    long long num_blocks, cudaStream_t st) try {
+    std::vector<int32_t> tab((size_t)num_seqs * mbps);
+    if (const int e = copy_to_host(tab.data(), block_tables, sizeof(int32_t) * tab.size(), st)) return e;
+    for (int i = 0; i < num_seqs; ++i) {
+        if (last[i] < 0 || last[i] > (int64_t)mbps * block_size) return PA_ERR_INVALID_ARG;
+        for (int64_t b = 0; b < (last[i] + block_size - 1) / block_size; ++b) {
+            const int32_t id = tab[(size_t)i * mbps + b];
+            if (id < 0 || id >= num_blocks) return PA_ERR_INVALID_ARG;
+        }
+    }
+    return 0;
+} catch (...) {
+    return PA_ERR_STATE;
+}
+
 int num_sms() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=

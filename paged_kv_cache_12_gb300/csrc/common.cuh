@@ -29,6 +29,15 @@ int validate_slots(const int64_t *slot_mapping, int num_tokens, long long num_sl
 // and none of them a source.
 int validate_pairs(const int64_t *pairs, int num_pairs, long long num_blocks, cudaStream_t st);
 
+// PA_DEBUG_VALIDATE: int32 start[n + 1] is a non-decreasing cover of [0, end)
+// (exact) or of a part of it from 0 on.
+int validate_starts(const int32_t *start, int n, int end, bool exact, cudaStream_t st);
+
+// PA_DEBUG_VALIDATE: the tables' blocks that hold tokens 0 .. last[i] - 1 of each
+// sequence are in range, and so are the lengths (host array).
+int validate_tables(const int32_t *block_tables, const int64_t *last, int num_seqs, int mbps, int block_size,
+                    long long num_blocks, cudaStream_t st);
+
 // SM count of the current device, asked on every call (a cheap attribute
 // query), so that each device sizes its own grid.
 int num_sms();

@@ -15,6 +15,7 @@
 // slot holds.
 
 #include <algorithm>
+#include <vector>
 
 #include "latent.h"
 
@@ -208,6 +209,26 @@ __global__ void latent_copy_kernel(uint4 *__restrict__ cache, const int64_t *__r
         cache[dst * vecs_per_block + i] = cache[src * vecs_per_block + i];
 }
 
+// PA_DEBUG_VALIDATE of a read: the rows' order, and a block in range for every
+// token read (the tables' entries before a sequence's last token count too).
+int validate_read(const int32_t *block_tables, const int32_t *row_start, const int32_t *first_token, int num_seqs,
+                  int num_rows, int block_size, long long num_blocks, int mbps, cudaStream_t st) try {
+    if (const int e = validate_starts(row_start, num_seqs, num_rows, false, st)) return e;
+    std::vector<int32_t> start((size_t)num_seqs + 1), first((size_t)num_seqs);
+    std::vector<int64_t> last((size_t)num_seqs);
+    if (const int e = copy_to_host(start.data(), row_start, sizeof(int32_t) * start.size(), st)) return e;
+    if (first_token)
+        if (const int e = copy_to_host(first.data(), first_token, sizeof(int32_t) * first.size(), st)) return e;
+    for (int i = 0; i < num_seqs; ++i) {
+        const int n = start[(size_t)i + 1] - start[(size_t)i];
+        if (n > 0 && first[(size_t)i] < 0) return PA_ERR_INVALID_ARG;
+        last[(size_t)i] = n > 0 ? (int64_t)first[(size_t)i] + n : 0;
+    }
+    return validate_tables(block_tables, last.data(), num_seqs, mbps, block_size, num_blocks, st);
+} catch (...) {   // no host memory for the check
+    return PA_ERR_STATE;
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -273,6 +294,10 @@ extern "C" int pa_latent_read(uint16_t *out, const void *cache, const int32_t *b
     if (!out || !cache || !block_tables || !row_start || !aligned16(out) || !aligned16(cache))
         return PA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug_validate())
+        if (const int e = validate_read(block_tables, row_start, first_token, num_seqs, num_rows, block_size, num_blocks,
+                                        max_blocks_per_seq, st))
+            return e;
     const unsigned grid = ((unsigned)num_rows + READ_ROWS - 1) / READ_ROWS;
     uint4 *o = reinterpret_cast<uint4 *>(out);
     const uint8_t *c = static_cast<const uint8_t *>(cache);

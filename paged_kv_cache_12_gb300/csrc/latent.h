@@ -66,4 +66,17 @@ __device__ __forceinline__ uint2 latent_codes_to_bf16(uint32_t codes, float scal
     return r;
 }
 
+// Whether one of eight 16-bit values is not finite (all exponent bits set), and a
+// pair with what is not finite made zero.
+template <int KV>
+__device__ __forceinline__ bool not_finite(uint4 v) {
+    constexpr uint32_t E = KV == PA_KV_F16 ? 0x7c007c00u : 0x7f807f80u, ONE = KV == PA_KV_F16 ? 0x04000400u : 0x00800080u;
+    return (((v.x & E) + ONE) | ((v.y & E) + ONE) | ((v.z & E) + ONE) | ((v.w & E) + ONE)) & 0x80008000u;
+}
+template <int KV>
+__device__ __forceinline__ uint32_t finite_part(uint32_t v) {
+    constexpr uint32_t E = KV == PA_KV_F16 ? 0x7c00u : 0x7f80u;
+    return ((v & E) == E ? 0u : v & 0xffffu) | ((v >> 16 & E) == E ? 0u : v & 0xffff0000u);
+}
+
 }  // namespace pa

@@ -31,7 +31,6 @@ struct LatentArgs {
     float4 *o;              // [2 AXIS_MAX_CTAS][LT_ROWS * LC / 4] its unnormalised output (see partial_at)
 
     // ---- the work axis
-    static constexpr int TEAM = 2;   // (a chunk's row tiles see about the same tokens)
     static constexpr int COST = 2;   // 128 heads: 214 us with 1, 209 with 2, 212 with 3, 217 with 6
     struct Seq {
         int L, T, q0;   // context, new tokens, first query token
@@ -53,7 +52,8 @@ struct LatentArgs {
     // Every row tile counts the whole context's KV tiles (a chunk's earlier
     // rows see fewer, which matters only for long chunks; those belong to the
     // expanded form).
-    __device__ __forceinline__ long long start(const Seq &w, int r) const { return (long long)r * (w.tiles + COST); }
+    __device__ __forceinline__ long long start(const Seq &w, int j, int) const { return (long long)j * (w.tiles + COST); }
+    __device__ __forceinline__ bool in_teams(const Seq &w) const { return w.rts % 2 == 0; }
     // KV tiles that row tile r sees: up to its last row's own position.
     __device__ __forceinline__ int row_tiles(const Seq &w, int r) const {
         const long long last = min((long long)w.T * H, (long long)(r + 1) * LT_ROWS) - 1;
@@ -448,6 +448,8 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
         const bool live = 16 * q < rows;   // some row of this warp exists
         const bool mine = m < rows;
         const int vis = mine ? p.w.L - p.w.T + (int)(((long long)p.r * LT_ROWS + m) / a.H) + 1 : p.w.L;
+        // what the row tile's first row sees
+        const int first_vis = p.w.L - p.w.T + (int)((long long)p.r * LT_ROWS / a.H) + 1;
         float mrun = -INFINITY, l = 0.f;
         for (int t = p.t0; t < p.t1; ++t, ++n) {
             const int st = n & 1, t0 = t * L::TOK;
@@ -513,13 +515,23 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
                     *reinterpret_cast<uint4 *>(prow + (((HT / 8 * half + k) ^ (m & 7)) << 4)) =
                         make_uint4(pw[4 * k], pw[4 * k + 1], pw[4 * k + 2], pw[4 * k + 3]);
             }
-            if (!L::F8 && t0 + L::TOK > p.w.L) {
-                // the context's last tile: rows past it hold anything, and P is 0 there
+            // Rows that some query row does not see, where P is 0 and a product with
+            // an infinity or a NaN would not be: those past the context are zeroed
+            // (a quantised tile's already are), and so is what is not finite among
+            // the new tokens' (a row that sees such a token has a score that is not
+            // finite, and is NaN for that).
+            if (t0 + L::TOK > first_vis) {
                 uint8_t *kv = smem + L::OFF_KV + st * L::STAGE;
-                for (int k = tid + (p.w.L - t0) * 64; k < L::TOK * 64; k += 128) {
+                for (int k = tid + max(0, first_vis - t0) * 64; k < L::TOK * 64; k += 128) {
                     const int r = k >> 6, cc = k & 63;
-                    *reinterpret_cast<uint4 *>(kv + (r >> 3) * LT_GROUP + (cc >> 3) * 1024 + (r & 7) * 128 +
-                                               (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    uint4 *at = reinterpret_cast<uint4 *>(kv + (r >> 3) * LT_GROUP + (cc >> 3) * 1024 + (r & 7) * 128 +
+                                                          (cc & 7) * 16);
+                    if (t0 + r >= p.w.L) {
+                        if (!L::F8) *at = make_uint4(0, 0, 0, 0);
+                    } else if (const uint4 v = *at; not_finite<KV>(v)) {
+                        *at = make_uint4(finite_part<KV>(v.x), finite_part<KV>(v.y), finite_part<KV>(v.z),
+                                         finite_part<KV>(v.w));
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -794,6 +806,28 @@ int run_latent(void *out, const void *query, const void *cache, const int32_t *b
     return launch_latent<KV>(a, st);
 }
 
+// PA_DEBUG_VALIDATE of a call: lengths, row offsets and the blocks of every token.
+int validate_latent(const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                    int num_query_tokens, int block_size, long long num_blocks, int mbps, int max_context_len,
+                    cudaStream_t st) try {
+    std::vector<int32_t> lens((size_t)num_seqs), start((size_t)num_seqs + 1);
+    if (const int e = copy_to_host(lens.data(), context_lens, sizeof(int32_t) * lens.size(), st)) return e;
+    if (query_start) {
+        if (const int e = validate_starts(query_start, num_seqs, num_query_tokens, true, st)) return e;
+        if (const int e = copy_to_host(start.data(), query_start, sizeof(int32_t) * start.size(), st)) return e;
+    }
+    std::vector<int64_t> last((size_t)num_seqs);
+    for (int i = 0; i < num_seqs; ++i) {
+        const int len = lens[(size_t)i];
+        if (len > max_context_len || (query_start && start[(size_t)i + 1] - start[(size_t)i] > len))
+            return PA_ERR_INVALID_ARG;
+        last[(size_t)i] = len;
+    }
+    return validate_tables(block_tables, last.data(), num_seqs, mbps, block_size, num_blocks, st);
+} catch (...) {   // no host memory for the check
+    return PA_ERR_STATE;
+}
+
 }  // namespace
 }  // namespace pa
 
@@ -826,6 +860,10 @@ extern "C" int pa_latent_attention(void *out, const void *query, const void *cac
         workspace_bytes < pa_latent_attention_workspace_size(num_seqs, num_query_tokens, num_heads, max_context_len))
         return PA_ERR_WORKSPACE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug_validate())
+        if (const int e = validate_latent(block_tables, context_lens, query_start, num_seqs, num_query_tokens, block_size,
+                                          num_blocks, max_blocks_per_seq, max_context_len, st))
+            return e;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const auto run = kv_dtype == PA_KV_F16    ? run_latent<PA_KV_F16>
                      : kv_dtype == PA_KV_BF16 ? run_latent<PA_KV_BF16>

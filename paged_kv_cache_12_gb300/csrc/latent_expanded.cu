@@ -21,6 +21,7 @@
 // issue order, so when S_x(n) is complete so is PV_x(n - 1).
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "decode_common.cuh"
@@ -35,6 +36,7 @@ constexpr int EN = 128, ER = PA_LATENT_ROPE_DIM, EQ = EN + ER, EV = 128;
 constexpr int EX_HALF = 128;               // rows of a half
 constexpr int EX_ROWS = 2 * EX_HALF;       // rows of a row tile
 constexpr int EX_TOK = 128;                // tokens of a KV tile
+constexpr int EX_PAST = 2;                 // teams of two from a past of this many times the new tokens on
 
 struct ExpandedArgs {
     uint16_t *out;
@@ -50,7 +52,6 @@ struct ExpandedArgs {
     float4 *o;              // [2 AXIS_MAX_CTAS][EX_ROWS * EV / 4] its unnormalised output (see partial_at)
 
     // ---- the work axis: row tile r of a sequence is tile r % tiles_per_head of head r / tiles_per_head
-    static constexpr int TEAM = 1;
     static constexpr int COST = 4;   // 600 tokens, 16 heads: 27.6 us with 1, 26.6 with 4, 27.9 with 6
     struct Seq {
         int L, T, q0, k0;
@@ -69,13 +70,21 @@ struct ExpandedArgs {
         w.rts = w.per_head * H;
         return w;
     }
-    // Tile j but a head's last sees ceil(past / 128) + 2 (j + 1) KV tiles.
-    __device__ __forceinline__ long long start(const Seq &w, int r) const {
-        if (w.per_head == 0) return 0;
+    // Row tile i of a head, but the last, sees ceil(past / 128) + 2 (i + 1) KV
+    // tiles; a team's two count as the later one.
+    __device__ __forceinline__ long long start(const Seq &w, int j, int team) const {
+        const int per = w.per_head / team;
+        if (per == 0) return 0;
         const long long past = (w.L - w.T + EX_TOK - 1) / EX_TOK;
-        auto before = [&](long long j) { return j * (COST + past) + j * (j + 1); };
-        const int h = r / w.per_head, j = r - h * w.per_head;
-        return h * (before(w.per_head - 1) + COST + (w.L + EX_TOK - 1) / EX_TOK) + before(j);
+        auto before = [&](long long i) { return i * (COST + past) + team * i * (i + 1); };
+        const int h = j / per, i = j - h * per;
+        return h * (before(per - 1) + COST + (w.L + EX_TOK - 1) / EX_TOK) + before(i);
+    }
+    // In teams where a sequence's past is long against its new tokens, so that
+    // the two row tiles' KV ranges are nearly the same (2048 of 12000 tokens, 32
+    // heads: 358 us in teams, 378 without).
+    __device__ __forceinline__ bool in_teams(const Seq &w) const {
+        return w.per_head % 2 == 0 && (w.per_head == 0 || w.L - w.T >= EX_PAST * w.T);
     }
     // KV tiles of the first `rows` new tokens.
     __device__ __forceinline__ int tiles_of(const Seq &w, int rows) const {
@@ -140,12 +149,18 @@ constexpr int EX_REGS_HIGH = 200;                    // the softmax warpgroups
 static_assert(128 * EX_REGS_LOW + 256 * EX_REGS_HIGH <= EX_THREADS * EX_REGS_LAUNCH,
               "register split within the launch's pool");
 
+constexpr int EX_POISON = 16;   // pieces that one half may be ahead of the other
+constexpr uint32_t EX_LAST = 0x7fffffffu;
+
 struct ExCtrl {
     uint64_t full[EX_RING], empty[EX_RING], qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2], done;
     uint32_t tmem;
     int abort;
     Plan plan;
     long long warp_sums[EX_THREADS / 32];
+    // by a piece's number: 1 + that number in the high word, and in the low one
+    // how far below the largest position its first non-finite value of a new token is
+    unsigned long long poison[EX_POISON];
 };
 static_assert(sizeof(ExCtrl) <= EX_CTRL, "control block");
 
@@ -317,6 +332,8 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
         const int tok = h.row0 + m;
         const bool mine = tok < p.w.T;
         const int vis = mine ? p.w.L - p.w.T + tok + 1 : p.w.L;   // positions this row sees
+        // what the row tile's first row sees
+        const int first_vis = p.w.L - p.w.T + p.r % p.w.per_head * EX_ROWS + 1;
         float mrun = -INFINITY, l = 0.f;
         for (int n = 0; n < h.n && ok; ++n) {
             if (!wait(&c.sfull[x], (uint32_t)(sc & 1))) break;
@@ -364,20 +381,35 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
                 l *= alpha;
                 mrun = nm;
             }
-            // value rows past the sequence are the next one's, or nothing: zeroed
-            // (P is 0 there); half 0 runs every KV tile, ahead of half 1
-            bool zeroed = false;
-            if (x == 0 && t0 + EX_TOK > p.w.L) {
+            // Value rows that some row of the row tile does not see, where P is 0 and
+            // a product with an infinity or a NaN would not be: those past the
+            // sequence (the next one's, or nothing) are zeroed, and so is what is not
+            // finite among the new tokens' (the rows that see it become NaN below).
+            // Half 0 does it for both: it runs every KV tile, and PV1(n) is issued
+            // after P0(n).
+            bool changed = false;
+            if (x == 0 && t0 + EX_TOK > first_vis) {
                 const int at = cnt + 5 * n + 3;   // the value tile's ring blocks
+                int bad = INT_MAX;
 #pragma unroll 1
                 for (int b = 0; b < 2; ++b) {
                     if (!wait(&c.full[(at + b) % EX_RING], (uint32_t)(((at + b) / EX_RING) & 1))) break;
-                    uint8_t *blk = smem + EX_OFF_RING + (at + b) % EX_RING * EX_BLOCK;
-                    for (int k = m + (p.w.L - t0) * 8; k < EX_TOK * 8; k += EX_HALF)
-                        *reinterpret_cast<uint4 *>(blk + 16 * k) = make_uint4(0, 0, 0, 0);
+                    uint4 *blk = reinterpret_cast<uint4 *>(smem + EX_OFF_RING + (at + b) % EX_RING * EX_BLOCK);
+                    for (int k = m + max(0, first_vis - t0) * 8; k < EX_TOK * 8; k += EX_HALF) {
+                        const int pos = t0 + k / 8;
+                        if (pos >= p.w.L) {
+                            blk[k] = make_uint4(0, 0, 0, 0);
+                        } else if (const uint4 v = blk[k]; not_finite<KV>(v)) {
+                            blk[k] = make_uint4(finite_part<KV>(v.x), finite_part<KV>(v.y), finite_part<KV>(v.z),
+                                                finite_part<KV>(v.w));
+                            bad = min(bad, pos);
+                        }
+                    }
                 }
                 if (!ok) break;
-                zeroed = true;
+                if (bad != INT_MAX)
+                    atomicMax(&c.poison[p.local % EX_POISON], (unsigned long long)(p.local + 1) << 32 | (EX_LAST - (uint32_t)bad));
+                changed = true;
             }
             const float mu = mrun == -INFINITY ? 0.f : mrun;   // a row that has seen nothing yet
             const uint64_t sl2x2 = pair_of(sl2, sl2), negm = pair_of(-mu, -mu);
@@ -402,7 +434,7 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
             pair_parts(pair_add(pair_add(lp[0], lp[1]), pair_add(lp[2], lp[3])), l0, l1);
             l += l0 + l1;
             tmem_wait_st();
-            if (zeroed) fence_proxy_async_smem();
+            if (changed) fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();   // one arrival a warp: 32 atomics on one word hold up the shared-memory pipe
             if (lane == 0) mbar_arrive(smem_u32(&c.pfull[x]));
@@ -411,6 +443,8 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
         if (!ok || !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1))) break;
         tc_fence_after_sync();
         // ---- the piece's rows: finished, or a partial row
+        const unsigned long long poison = *reinterpret_cast<volatile unsigned long long *>(&c.poison[p.local % EX_POISON]);
+        if ((int)(poison >> 32) == p.local + 1 && vis > (int)(EX_LAST - (uint32_t)poison)) l = __int_as_float(0x7fc00000);
         const bool whole = p.t0 == 0 && p.t1 >= h.ntiles;
         const int slot_row = p.slot() * EX_ROWS + h.row0 % EX_ROWS + m;
         if (!whole && mine) a.ml[slot_row] = make_float2(mrun, l);
@@ -468,6 +502,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
         mbar_init(smem_u32(&c.done), 1);
         c.abort = 0;
+        for (int k = 0; k < EX_POISON; ++k) c.poison[k] = 0;
         fence_mbar_init();
     }
     make_plan(a, &c.plan, c.warp_sums);
@@ -668,6 +703,11 @@ extern "C" int pa_latent_attention_expanded(void *out, const void *query, const 
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
         workspace_bytes < pa_latent_attention_expanded_workspace_size(num_seqs, num_query_tokens, num_heads))
         return PA_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug_validate()) {
+        if (const int e = validate_starts(query_start, num_seqs, num_query_tokens, true, st)) return e;
+        if (const int e = validate_starts(kv_start, num_seqs, num_kv_tokens, true, st)) return e;
+    }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const ExLayout lay = ex_layout();
     ExpandedArgs a{};
@@ -694,7 +734,6 @@ extern "C" int pa_latent_attention_expanded(void *out, const void *query, const 
         !heads_map(&tmr, none ? query : k_rope, ER, 0, nk, 0, rope_stride, dtype) ||
         !heads_map(&tmv, none ? query : value, EV, num_heads, nk, v_head_stride, v_token_stride, dtype))
         return PA_ERR_CUDA;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dtype == PA_KV_F16 ? launch_expanded<PA_KV_F16>(a, tmq, tmk, tmr, tmv, st)
                               : launch_expanded<PA_KV_BF16>(a, tmq, tmk, tmr, tmv, st);
 }

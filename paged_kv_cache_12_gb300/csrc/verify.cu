@@ -394,6 +394,8 @@ extern "C" int pa_verify_drafts(int32_t *accepted, int32_t *tokens, const void *
     VerifyArgs a{accepted, tokens, target_probs, draft_probs, draft_tokens, draft_start, uniform, sample_uniform,
                  num_seqs, num_drafts, max_drafts, vocab_size, target_stride, draft_stride};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug_validate())
+        if (const int e = validate_starts(draft_start, num_seqs, num_drafts, true, st)) return e;
     if (probs_dtype == PA_PROBS_F16) return launch_verify<__half>(a, st);
     if (probs_dtype == PA_PROBS_BF16) return launch_verify<__nv_bfloat16>(a, st);
     return launch_verify<float>(a, st);

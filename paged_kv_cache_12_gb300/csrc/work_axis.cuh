@@ -11,18 +11,19 @@
 // a second kernel merges.  Every CTA derives the cut by itself from the lengths,
 // by one sum over the sequences.
 //
-// Where every sequence has an even number of row tiles over the same KV tiles
-// (P::TEAM = 2), the CTAs work in teams of two: a team takes a range of the axis of
-// every second row tile, and its two CTAs a row tile each of the pairs in it, so
-// that they read the same KV tiles at the same time (the second read comes from
-// L2; one CTA after the other, both came from HBM).
+// Where every sequence has an even number of row tiles over (nearly) the same KV
+// tiles, the CTAs work in teams of two: a team takes a range of the axis of every
+// second row tile, and its two CTAs a row tile each of the pairs in it, so that
+// they read the same KV tiles at the same time (the second read comes from L2; one
+// CTA after the other, both came from HBM).
 //
 // A problem P gives
 //   P::COST                 units of a row tile besides its KV tiles
-//   P::TEAM                 1, or 2: see above
+//   in_teams(w)             whether teams of two suit the sequence
 //   P::Seq, seq_work(i)     what is needed of sequence i; Seq::rts row tiles
-//   start(w, r)             first unit of row tile r within its sequence;
-//                           start(w, w.rts) = the sequence's units
+//   start(w, j, team)       first unit, within its sequence, of the j-th row tile
+//                           of a team's axis (row tile j * team + member);
+//                           start(w, w.rts / team, team) = the sequence's units
 //   row_tiles(w, r)         KV tiles of row tile r
 //   starts_ok()             whether the row offsets are in order (called by
 //                           every thread of the block)
@@ -90,7 +91,7 @@ __device__ __forceinline__ int row_tile_at(const P &a, const typename P::Seq &w,
     int r = 0, hi = w.rts / team;
     while (hi - r > 1) {
         const int mid = (r + hi) >> 1;
-        if (a.start(w, mid) <= u) r = mid; else hi = mid;
+        if (a.start(w, mid, team) <= u) r = mid; else hi = mid;
     }
     return r;
 }
@@ -102,15 +103,12 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     const int per = (a.num_seqs + blockDim.x - 1) / blockDim.x;
     const int i0 = min(a.num_seqs, (int)threadIdx.x * per), i1 = min(a.num_seqs, i0 + per);
-    int team = 1;
-    if constexpr (P::TEAM == 2) {
-        bool even = true;
-        for (int i = i0; ok && i < i1; ++i) even = even && a.seq_work(i).rts % 2 == 0;
-        if (__syncthreads_and(even)) team = 2;
-    }
+    bool pairs = true;
+    for (int i = i0; ok && i < i1; ++i) pairs = pairs && a.in_teams(a.seq_work(i));
+    const int team = __syncthreads_and(pairs) ? 2 : 1;
     auto units = [&](int i) {
         const typename P::Seq w = a.seq_work(i);
-        return a.start(w, w.rts / team);
+        return a.start(w, w.rts / team, team);
     };
     long long mine = 0;
     for (int i = i0; ok && i < i1; ++i) mine += units(i);
@@ -156,7 +154,7 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         const typename P::Seq w = a.seq_work(i);
         const int j = row_tile_at(a, w, team, u0 - s), r = j * team + cta % team;
         Cut cut;
-        cut.s = s + a.start(w, j);
+        cut.s = s + a.start(w, j, team);
         cut.total = total;
         cut.row0 = a.first_row(w, r);
         cut.ntiles = a.row_tiles(w, r);
@@ -191,12 +189,12 @@ struct Walk {
         for (;;) {
             ++j;
             while (j >= w.rts / team) {   // on to the next sequence
-                base += a.start(w, w.rts / team);
+                base += a.start(w, w.rts / team, team);
                 if (base >= u1 || ++seq >= a.num_seqs) return false;
                 w = a.seq_work(seq);
                 j = 0;
             }
-            s = base + a.start(w, j);
+            s = base + a.start(w, j, team);
             if (s >= u1) return false;
             r = j * team + (int)blockIdx.x % team;
             ntiles = a.row_tiles(w, r);

@@ -246,6 +246,40 @@ def test_absorbed_bad_rows(kv):
     w.tables, w.lens_t = tables, lens_t
 
 
+@kvs
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf], ids=["nan", "inf", "ninf"])
+def test_absorbed_later_new_tokens_do_not_leak(kv, bad):
+    # a new token's row that is not finite: earlier new tokens do not see it, and
+    # their rows are as if it were not there; itself and later ones are not finite
+    heads, news, lens = 16, [6, 3, 9], [200, 64, 70]
+    w = R.Paged(lens, 16, kv, 61, DEV)
+    q, want = absorbed(w, heads, news, 8)
+    flat = w.cache.view(w.nb * w.bs, -1)
+    for i, j in ((0, 3), (1, 1), (2, 5)):
+        slot = int(w.seq_slots[i][lens[i] - news[i] + j])
+        if kv == pa.PA_KV_FP8_E4M3:
+            flat[slot, 40] = 0x7f if math.isnan(bad) else flat[slot, 40]
+            if not math.isnan(bad):
+                flat[slot, 512 + 128:512 + 132].view(torch.float32)[0] = bad
+        else:
+            flat[slot, 40] = bad
+    _, out = absorbed(w, heads, news, 8, query=q)
+    at = 0
+    for n, first in zip(news, (3, 1, 5)):
+        assert same_bits(out[at:at + first], want[at:at + first])
+        if not math.isinf(bad):
+            assert torch.isnan(out[at + first:at + n]).all()
+        else:
+            # a score of +inf makes the row NaN; one of -inf takes the token out of
+            # it, but for the infinite elements themselves, where the definition
+            # has 0 * inf
+            rows = out[at + first:at + n].float()
+            rows = torch.cat([rows[..., :40], rows[..., 41:128], rows[..., 256:]], -1)
+            assert (torch.isnan(rows).all(-1) | torch.isfinite(rows).all(-1)).all()
+            assert torch.isnan(rows).any()
+        at += n
+
+
 def test_absorbed_bad_query_start():
     w = R.Paged([50, 60], 16, pa.PA_KV_BF16, 41, DEV)
     q = torch.randn(6, 16, 576, device=DEV).bfloat16()
@@ -356,6 +390,40 @@ def test_expanded_neighbours_do_not_leak(dt):
     pa.pa_latent_attention_expanded(got, q, k, r, v, qs, ks, SCALE, ws)
     assert same_bits(got[:70], out[:70]) and same_bits(got[110:], out[110:])
     assert torch.isnan(got[70:110]).all()
+
+
+@types
+@pytest.mark.parametrize("bad", [math.nan, math.inf], ids=["nan", "inf"])
+def test_expanded_later_new_tokens_do_not_leak(dt, bad):
+    # values, keys and rotary keys of new tokens that are not finite: rows of
+    # earlier new tokens are as if they were finite, later ones are not finite
+    news, pasts = [300, 140, 20], [100, 0, 256]
+    q, k, r, v, out, (qs, ks, ws) = expanded(dt, news, pasts, 2, 29)
+    # (sequence, new token, tensor, head): the same token may be hit twice
+    hits = [(0, 290, v, 0), (0, 130, v, 1), (0, 131, v, 1), (1, 60, k, 0), (1, 139, v, 0), (2, 7, r, None)]
+    k0, q0 = [0, 400, 540], [0, 300, 440]
+    for i, j, t, h in hits:
+        row = k0[i] + pasts[i] + j
+        if h is None:
+            t[row, 5] = bad
+        else:
+            t[row, h, 77] = bad
+    got = torch.zeros_like(out)
+    pa.pa_latent_attention_expanded(got, q, k, r, v, qs, ks, SCALE, ws)
+    for i in range(3):
+        for h in range(2):
+            first = min([j for a, j, t, b in hits if a == i and (b is None or b == h)] + [news[i]])
+            a = q0[i]
+            assert same_bits(got[a:a + first, h], out[a:a + first, h]), (i, h)
+            last = got[a + first:a + news[i], h].float()
+            values = all(t is v for b, j, t, c in hits if b == i and (c is None or c == h))
+            if values:   # that element at least
+                assert not torch.isfinite(last[:, 77]).any(), (i, h)
+            elif math.isnan(bad):
+                assert torch.isnan(last).all(), (i, h)
+            else:
+                # an infinite key: +inf makes a row NaN, -inf takes the token out of it
+                assert (torch.isnan(last).all(-1) | torch.isfinite(last).all(-1)).all(), (i, h)
 
 
 def test_expanded_bad_starts():

@@ -148,6 +148,20 @@ def test_bad_sequences():
     assert run(t, q, d, [0, 3, 4, 6, 8], u, pick, 2)[0][0] == -1          # three drafts of at most two
 
 
+@pytest.mark.parametrize("n", [100, 200, 400, 900])
+def test_cluster_sizes(n):
+    # a sequence's cluster shrinks as the batch grows; rows of odd length, some
+    # sequences without drafts, one whose draft covers the target
+    counts = [i % 3 for i in range(n)]
+    args = list(case("f32", counts, 1501, n))
+    t, q, d, start, u, pick = args
+    i = next(i for i in range(n) if counts[i] == 2)
+    r = start[i]
+    q[r] = torch.clamp(t[r + i] * 1.5, min=1e-6)
+    u[r] = 0.999
+    compare((t, q, d, start, u, pick), 2)
+
+
 def test_many_sequences_captured():
     counts = [i % 4 for i in range(300)]
     t, q, d, start, u, pick = case("f32", counts, 4099, 10)
