@@ -395,14 +395,26 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
                 for (int b = 0; b < 2; ++b) {
                     if (!wait(&c.full[(at + b) % EX_RING], (uint32_t)(((at + b) / EX_RING) & 1))) break;
                     uint4 *blk = reinterpret_cast<uint4 *>(smem + EX_OFF_RING + (at + b) % EX_RING * EX_BLOCK);
-                    for (int k = m + max(0, first_vis - t0) * 8; k < EX_TOK * 8; k += EX_HALF) {
-                        const int pos = t0 + k / 8;
-                        if (pos >= p.w.L) {
-                            blk[k] = make_uint4(0, 0, 0, 0);
-                        } else if (const uint4 v = blk[k]; not_finite<KV>(v)) {
-                            blk[k] = make_uint4(finite_part<KV>(v.x), finite_part<KV>(v.y), finite_part<KV>(v.z),
-                                                finite_part<KV>(v.w));
-                            bad = min(bad, pos);
+                    // this thread's chunks m, m + 128, ..: row m / 8 + 16 i
+                    const int lo = max(0, first_vis - t0), hi = p.w.L - t0;
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = m / 8 + 16 * i;
+                        if (r >= lo && r < hi) any |= not_finite<KV>(blk[m + EX_HALF * i]);
+                    }
+                    if (any || hi < EX_TOK) {
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = m / 8 + 16 * i;
+                            uint4 &v = blk[m + EX_HALF * i];
+                            if (r >= hi) {
+                                v = make_uint4(0, 0, 0, 0);
+                            } else if (r >= lo && not_finite<KV>(v)) {
+                                v = make_uint4(finite_part<KV>(v.x), finite_part<KV>(v.y), finite_part<KV>(v.z),
+                                               finite_part<KV>(v.w));
+                                bad = min(bad, t0 + r);
+                            }
                         }
                     }
                 }
