@@ -607,6 +607,8 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
     }
     make_plan(a, &c.plan, c.warp_sums);
     const Plan plan = c.plan;
+    // the merge's CTAs may come as this kernel's leave (they wait for all of them)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     fill_idle_rows<LC / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
                            KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
@@ -640,7 +642,6 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
         }
     }
     if (threadIdx.x == 0) a.status[blockIdx.x] = c.abort;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ merge
@@ -666,15 +667,14 @@ __global__ void __launch_bounds__(32 * MG_WARPS) latent_merge_kernel(const typen
     }
     const int m = 16 * quarter + (lane & 15), k8 = (unit & 31) >> 2, j = 2 * (unit & 3);
     if (failed || m >= cut.rows) return;
-    const Pieces pc(cut, cta, cut.ntiles, Lt<KV>::Args::COST, ctas);
     float M = -INFINITY;
 #pragma unroll 8
-    for (int k = pc.k0; k <= pc.k1; ++k) M = fmaxf(M, a.ml[pc.slot(k) * LT_ROWS + m].x);
+    for (int k = 0; k < cut.pieces; ++k) M = fmaxf(M, a.ml[piece_slot(cut, cta, k) * LT_ROWS + m].x);
     const float mu = M == -INFINITY ? 0.f : M;
     float acc[8] = {}, l = 0.f;
 #pragma unroll 8
-    for (int k = pc.k0; k <= pc.k1; ++k) {
-        const int slot = pc.slot(k);
+    for (int k = 0; k < cut.pieces; ++k) {
+        const int slot = piece_slot(cut, cta, k);
         const float2 ml = a.ml[slot * LT_ROWS + m];
         const float4 x = a.o[partial_at(slot, quarter, k8, j, lane)], y = a.o[partial_at(slot, quarter, k8, j + 1, lane)];
         const float wt = fast_exp2(ml.x - mu);

@@ -519,6 +519,8 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     }
     make_plan(a, &c.plan, c.warp_sums);
     const Plan plan = c.plan;
+    // the merge's CTAs may come as this kernel's leave (they wait for all of them)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     fill_idle_rows<EV / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
                            KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
@@ -551,7 +553,6 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
     }
     if (threadIdx.x == 0) a.status[blockIdx.x] = c.abort;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Rows of the cut row tiles from their pieces' partial rows: blockIdx.x is the
@@ -574,16 +575,16 @@ __global__ void __launch_bounds__(32 * EM_WARPS) expanded_merge_kernel(const Exp
     }
     const int m = 32 * q + lane, k4 = unit % EM_UNITS >> 2, j = 2 * (unit & 3);
     if (failed || m >= cut.rows) return;
-    const Pieces pc(cut, cta, m < EX_HALF ? cut.ntiles1 : cut.ntiles, ExpandedArgs::COST, ctas);
-    if (pc.k0 == pc.k1) return;   // this half was finished by one CTA
+    const int pieces = m < EX_HALF ? cut.pieces1 : cut.pieces;
+    if (pieces == 1) return;   // this half was finished by one CTA
     float M = -INFINITY;
 #pragma unroll 8
-    for (int k = pc.k0; k <= pc.k1; ++k) M = fmaxf(M, a.ml[pc.slot(k) * EX_ROWS + m].x);
+    for (int k = 0; k < pieces; ++k) M = fmaxf(M, a.ml[piece_slot(cut, cta, k) * EX_ROWS + m].x);
     const float mu = M == -INFINITY ? 0.f : M;
     float acc[8] = {}, l = 0.f;
 #pragma unroll 8
-    for (int k = pc.k0; k <= pc.k1; ++k) {
-        const int slot = pc.slot(k);
+    for (int k = 0; k < pieces; ++k) {
+        const int slot = piece_slot(cut, cta, k);
         const float2 ml = a.ml[slot * EX_ROWS + m];
         const float4 x = a.o[partial_at(slot, q, k4, j, lane)], y = a.o[partial_at(slot, q, k4, j + 1, lane)];
         const float wt = fast_exp2(ml.x - mu);

@@ -51,14 +51,16 @@ struct Plan {
 };
 
 // A row tile whose first two pieces are the CTA's own and that of the CTA before
-// it (a team before it), in cuts[CTA];
-// rows = 0 where there is none (the range begins with a row tile, or in one
-// that an earlier range cuts as well).  All that the merge needs of it.
+// it (a team before it), in cuts[CTA]: all that the merge needs of it.  rows = 0
+// where there is none (the range begins with a row tile, or in one that an earlier
+// range cuts as well).
 struct Cut {
-    long long s, total;        // its first unit; units of the axis
-    long long row0;            // its first row in the output
-    int rows, ntiles, ntiles1; // rows; KV tiles, and those its first rows see
-    int team;
+    long long row0;     // its first row in the output
+    int rows;
+    int pieces;         // its pieces, in consecutive teams from the one before on
+    int pieces1;        // those that its first rows have tiles in (see first_tiles)
+    int first, step;    // slots of their partial rows: first, then 2 CTA, 2 CTA + step, ..
+    int pad;
 };
 
 // First unit of team k's range; `parts` = min(teams, total) teams have one, of at
@@ -153,16 +155,22 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         // the row tile in which the range begins: cut here if a KV tile of it lies on either side
         const typename P::Seq w = a.seq_work(i);
         const int j = row_tile_at(a, w, team, u0 - s), r = j * team + cta % team;
-        Cut cut;
-        cut.s = s + a.start(w, j, team);
-        cut.total = total;
-        cut.row0 = a.first_row(w, r);
-        cut.ntiles = a.row_tiles(w, r);
-        cut.ntiles1 = a.first_tiles(w, r);
-        cut.team = team;
-        const long long first = cut.s + P::COST;
-        const bool here = k > 0 && first < u0 && u0 < first + cut.ntiles && range_begin(total, k - 1, parts) <= first;
-        cut.rows = here ? a.cut_rows(w, r) : 0;
+        const long long at = s + a.start(w, j, team), first = at + P::COST;
+        const int ntiles = a.row_tiles(w, r);
+        Cut cut{};
+        if (k > 0 && first < u0 && u0 < first + ntiles && range_begin(total, k - 1, parts) <= first) {
+            auto pieces = [&](int tiles) {   // of the row tile's first `tiles` KV tiles
+                int n = 1;
+                while (range_begin(total, k - 1 + n, parts) < first + tiles) ++n;
+                return n;
+            };
+            cut.row0 = a.first_row(w, r);
+            cut.rows = a.cut_rows(w, r);
+            cut.pieces = pieces(ntiles);
+            cut.pieces1 = pieces(a.first_tiles(w, r));
+            cut.first = 2 * (cta - team) + (at < range_begin(total, k - 1, parts) ? 0 : 1);
+            cut.step = 2 * team;
+        }
         a.cuts[cta] = cut;
     }
     __syncthreads();
@@ -211,22 +219,10 @@ struct Walk {
     __device__ int slot() const { return 2 * (int)blockIdx.x + (s < u0 ? 0 : 1); }
 };
 
-// The pieces of a cut row tile that hold its first `ntiles` KV tiles: teams k0
-// (the one before the cut's) .. k1, and the slot of each one's partial rows.
-struct Pieces {
-    int k0, k1, team, member, first;
-    __device__ Pieces(const Cut &cut, int cta, int ntiles, int cost, int ctas)
-        : k0(cta / cut.team - 1), team(cut.team), member(cta % cut.team) {
-        const int parts = (int)min((long long)(ctas / team), cut.total);
-        const long long last = cut.s + cost + ntiles - 1;
-        k1 = (int)(last * parts / cut.total);
-        while (range_begin(cut.total, k1 + 1, parts) <= last) ++k1;
-        while (range_begin(cut.total, k1, parts) > last) --k1;
-        first = 2 * (k0 * team + member) + (cut.s < range_begin(cut.total, k0, parts) ? 0 : 1);
-    }
-    // (the row tile began before every later piece's range)
-    __device__ int slot(int k) const { return k == k0 ? first : 2 * (k * team + member); }
-};
+// The slot of a cut row tile's i-th piece (it began before every later piece's range).
+__device__ __forceinline__ int piece_slot(const Cut &cut, int cta, int i) {
+    return i ? 2 * cta + (i - 1) * cut.step : cut.first;
+}
 
 // Whether a CTA of the first kernel gave up (called by the whole block).
 __device__ __forceinline__ bool any_gave_up(const int *status, int ctas) {
