@@ -434,8 +434,8 @@ PA_API int pa_latent_read(uint16_t *out, const void *cache, const int32_t *block
                           const int32_t *first_token, int num_seqs, int num_rows, int64_t out_stride,
                           int block_size, int64_t num_blocks, int max_blocks_per_seq, int kv_dtype, void *stream);
 
-/* Workspace bytes pa_latent_attention needs on the current device (a
- * host-side bound; 0 for invalid sizes). */
+/* Workspace bytes pa_latent_attention needs (a host-side bound; 0 for invalid
+ * sizes). */
 PA_API size_t pa_latent_attention_workspace_size(int num_seqs, int num_query_tokens, int num_heads,
                                                  int max_context_len);
 
@@ -461,7 +461,8 @@ PA_API size_t pa_latent_attention_workspace_size(int num_seqs, int num_query_tok
  * pa_attention_causal (L = 0 decodes to a zero row, an invalid L, T > L or a
  * block id out of range to NaN rows).  Rows of the cache that a new token does
  * not see may hold anything, infinities and NaN included: they do not reach its
- * output.  Deterministic.  pa_workspace_status reads the error word. */
+ * output; one that sees a latent element that is not finite gets a row that is
+ * not finite.  Deterministic.  pa_workspace_status reads the error word. */
 PA_API int pa_latent_attention(void *out, const void *query, const void *cache, const int32_t *block_tables,
                                const int32_t *context_lens, const int32_t *query_start, int num_seqs,
                                int num_query_tokens, int num_heads, int block_size, int64_t num_blocks,

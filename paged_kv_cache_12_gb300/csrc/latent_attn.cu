@@ -1,4 +1,32 @@
-// Attention over the latent cache in the absorbed form.
+// Attention over the latent cache in the absorbed form: with the map from a
+// latent to a head's key multiplied into the query, all heads of a token attend
+// to the same rows c_t of 576 elements,
+//   s_t = scale <q, c_t>,  out = sum_t softmax(s)_t c_t[0 .. 511],
+// the running maximum m and sum l of 2^(s_t scale log2 e - m) carried in fp32 (m
+// follows the maximum only when that grows by more than 2^8, which keeps the
+// probabilities, rounded to the 16-bit type for the second product, below 2^8),
+// and pieces of a context joined by M = max m, sum of 2^(m - M) (l, o).
+//
+// A row tile is 64 query rows (new token x head) of a sequence.  Each KV tile of 64
+// tokens is read once into shared memory and serves both products: S = Q C^T
+// (M 64, N 64, K 576) and O += P C (M 64, N 2 x 256, K 64).  Why 64 rows: O of 512
+// dims in fp32 is 512 columns at M = 128, all of tensor memory; at M = 64 an
+// accumulator uses 16 of each quarter's 32 lanes, so dims 0 .. 255 and 256 .. 511
+// share 256 columns and S has room.  One CTA per SM; warps: 0 loads, 1 and 2 issue
+// S of even and odd KV tiles, 3 issues P C, 4-7 run the softmax (two threads a row),
+// 8-15 turn E4M3 rows into bf16.  Shared memory: the query rows (72 KB), two KV
+// stages (72 KB each; 54 KB of 48 tokens over a quantised cache, beside a staging
+// ring of 31 KB), P (8 KB).
+//
+// What bounds it (one GB300, 1.9 GHz): 16 heads, 100 x 8192 bf16 tokens: 160 us,
+// the kernel 153 at 6.2 TB/s of HBM reads, tensor pipe 62 % busy.  128 heads are
+// two row tiles a token, 96 contexts of 64 .. 32768 fp16 tokens: 193 us, a latency
+// chain: a stage goes through load, S (36 products of 38 clocks), softmax and P C
+// (8 of 155) in 5500 clocks, and two stages are all that fits beside the queries;
+// halving both products takes 158.  Products of M 64 run at half the tensor
+// cores' rate.  E4M3, 16 heads x 4 new tokens, 100 contexts of 1024 .. 8192: 117 us,
+// 3800 clocks a tile in the converting warps (110 dependent instructions, waits and
+// votes a step of 16 tokens; ALU pipe 44 %, HBM 30 %).
 #include <algorithm>
 #include <cmath>
 
@@ -45,7 +73,7 @@ struct LatentArgs {
         w.T = query_start ? __ldg(query_start + i + 1) - w.q0 : 1;
         w.valid = w.L >= 0 && w.L <= max_context_len && (long long)w.L <= (long long)mbps << bs_log2 &&
                   !(query_start && w.T > w.L);
-        w.tiles = w.valid && w.T > 0 ? (w.L + TOK - 1) / TOK : 0;
+        w.tiles = w.valid && w.T > 0 ? w.L / TOK + (w.L % TOK != 0) : 0;
         w.rts = w.tiles ? (int)(((long long)w.T * H + LT_ROWS - 1) / LT_ROWS) : 0;
         return w;
     }
@@ -57,7 +85,7 @@ struct LatentArgs {
     // KV tiles that row tile r sees: up to its last row's own position.
     __device__ __forceinline__ int row_tiles(const Seq &w, int r) const {
         const long long last = min((long long)w.T * H, (long long)(r + 1) * LT_ROWS) - 1;
-        return (w.L - w.T + (int)(last / H) + 1 + TOK - 1) / TOK;
+        return (w.L - w.T + (int)(last / H)) / TOK + 1;
     }
     __device__ __forceinline__ bool starts_ok() const {
         return !query_start || offsets_ok(query_start, num_seqs, num_query_tokens);
@@ -101,6 +129,7 @@ constexpr int LT_TMEM = 512;                  // columns: O (256), S0, S1 (64 ea
 constexpr int LT_S = 256;
 constexpr uint32_t LT_HI = 16u << 16;         // lanes 16 .. 31 of each quarter: output dims 256 .. 511
 constexpr int LT_BAD_SLOTS = 16;
+constexpr uint32_t LT_LAST = 0x7fffffffu;
 constexpr int L8_WARPS = 8;                   // converting warps
 constexpr int L8_STEP = 16;                   // tokens of a staging slot of quantised rows: two groups of eight
 constexpr int L8_GROUP = 8 * LROW8;           // bytes of a group, consecutive in its block
@@ -130,6 +159,9 @@ struct LtCtrl {
     uint32_t tmem;
     int abort;
     int bad[LT_BAD_SLOTS];   // 1 + the number of a piece that met a block id out of range
+    // by a piece's number: 1 + that number in the high word, and in the low one
+    // how far below the largest position its first non-finite new token is
+    unsigned long long poison[LT_BAD_SLOTS];
     Plan plan;
     long long warp_sums[16];
 };
@@ -250,7 +282,7 @@ __device__ void lt_load8(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &
     while (w.ok && p.next()) {
         const int32_t *row = a.block_tables + (long long)p.seq * a.mbps;
         const int g0 = p.t0 * (L::TOK / 8), groups = (p.t1 - p.t0) * (L::TOK / 8);   // of the piece
-        const int with = min(groups, (p.w.L + 7) / 8 - g0);                            // those with tokens
+        const int with = min(groups, p.w.L / 8 + (p.w.L % 8 != 0) - g0);               // those with tokens
         auto ids = [&](int g) { return g + lane < with ? __ldg(row + a.entry_of(8 * (g0 + g + lane))) : 0; };
         // lane j's group of a batch: its rows in the cache, null if its id is out of range or it has no tokens
         auto rows_of = [&](int32_t id, int g) {
@@ -463,10 +495,10 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
                 tmem_ld_halves(trow + LT_S + 64 * st, s);
                 tmem_wait_ld();
                 tc_fence_before_sync();
-                const int first = t0 + HT * half;
-                if (first + HT > vis) {
+                const int seen = vis - t0 - HT * half;   // of this thread's tokens (the tile may end past the last int)
+                if (seen < HT) {
 #pragma unroll
-                    for (int k = 0; k < HT; ++k) s[k] = first + k < vis ? s[k] : -INFINITY;
+                    for (int k = 0; k < HT; ++k) s[k] = k < seen ? s[k] : -INFINITY;
                 }
                 float mp[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -518,19 +550,20 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
             // Rows that some query row does not see, where P is 0 and a product with
             // an infinity or a NaN would not be: those past the context are zeroed
             // (a quantised tile's already are), and so is what is not finite among
-            // the new tokens' (a row that sees such a token has a score that is not
-            // finite, and is NaN for that).
-            if (t0 + L::TOK > first_vis) {
+            // the new tokens' (the rows that see it become NaN below).
+            if (first_vis - t0 < L::TOK) {
                 uint8_t *kv = smem + L::OFF_KV + st * L::STAGE;
                 for (int k = tid + max(0, first_vis - t0) * 64; k < L::TOK * 64; k += 128) {
                     const int r = k >> 6, cc = k & 63;
                     uint4 *at = reinterpret_cast<uint4 *>(kv + (r >> 3) * LT_GROUP + (cc >> 3) * 1024 + (r & 7) * 128 +
                                                           (cc & 7) * 16);
-                    if (t0 + r >= p.w.L) {
+                    if (r >= p.w.L - t0) {
                         if (!L::F8) *at = make_uint4(0, 0, 0, 0);
                     } else if (const uint4 v = *at; not_finite<KV>(v)) {
                         *at = make_uint4(finite_part<KV>(v.x), finite_part<KV>(v.y), finite_part<KV>(v.z),
                                          finite_part<KV>(v.w));
+                        atomicMax(&c.poison[p.local % LT_BAD_SLOTS],
+                                  (unsigned long long)(p.local + 1) << 32 | (LT_LAST - (uint32_t)(t0 + r)));
                     }
                 }
             }
@@ -544,7 +577,10 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
         if (live) {
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             const bool bad = *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) == p.local + 1;
-            if (bad) l = __int_as_float(0x7fc00000);
+            const unsigned long long poison =
+                *reinterpret_cast<volatile unsigned long long *>(&c.poison[p.local % LT_BAD_SLOTS]);
+            const bool poisoned = (int)(poison >> 32) == p.local + 1 && vis > (int)(LT_LAST - (uint32_t)poison);
+            if (bad || poisoned) l = __int_as_float(0x7fc00000);
             const bool whole = p.whole();
             const float inv = 1.f / l;
             uint16_t *orow = a.out + (a.first_row(p.w, p.r) + m) * LC + 256 * half;
@@ -602,7 +638,7 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
         mbar_init(smem_u32(&c.qempty), 2);
         mbar_init(smem_u32(&c.done), 3);
         c.abort = 0;
-        for (int k = 0; k < LT_BAD_SLOTS; ++k) c.bad[k] = 0;
+        for (int k = 0; k < LT_BAD_SLOTS; ++k) c.bad[k] = 0, c.poison[k] = 0;
         fence_mbar_init();
     }
     make_plan(a, &c.plan, c.warp_sums);

@@ -280,6 +280,62 @@ def test_absorbed_later_new_tokens_do_not_leak(kv, bad):
         at += n
 
 
+@kvs
+@pytest.mark.parametrize("heads", [16, 128])
+def test_absorbed_seen_infinities_reach_the_row(kv, heads):
+    # an infinite latent element that a row sees makes the row not finite whatever
+    # the sign of its score: 0 * inf in the definition where the score is -inf
+    news, lens = [5, 2, 1], [150, 130, 90]
+    w = R.Paged(lens, 32, kv, 67, DEV)
+    q, want = absorbed(w, heads, news, 12)
+    q = q.abs()
+    q, want = absorbed(w, heads, news, 12, query=q)
+    flat = w.cache.view(w.nb * w.bs, -1)
+    for i, j in ((0, 2), (1, 0), (2, 0)):
+        slot = int(w.seq_slots[i][lens[i] - news[i] + j])
+        if kv == pa.PA_KV_FP8_E4M3:
+            flat[slot, 40] = 0xb8                            # -1 times an infinite scale
+            flat[slot, 512 + 128:512 + 132].view(torch.float32)[0] = math.inf
+        else:
+            flat[slot, 40] = -math.inf
+    _, out = absorbed(w, heads, news, 12, query=q)
+    at = 0
+    for n, first in zip(news, (2, 0, 0)):
+        assert same_bits(out[at:at + first], want[at:at + first])
+        rows = out[at + first:at + n].float()
+        assert not torch.isfinite(rows[..., 40]).any()
+        at += n
+
+
+def test_absorbed_longest_contexts():
+    # 5,000,001 positions of which a table names 40 blocks again and again: the
+    # same as over those blocks' rows weighted by how often they are seen
+    bs, nb, n = 64, 40, 5_000_001
+    g = torch.Generator().manual_seed(3)
+    rows = torch.randn(nb * bs, 576, generator=g).bfloat16()
+    q = torch.randn(1, 16, 576, generator=g).bfloat16()
+    entries = torch.randint(nb, (-(-n // bs),), generator=g)
+    seen = torch.zeros(nb * bs, dtype=torch.float64)
+    for k in range(bs):   # the last block is seen up to its remainder
+        hit = entries if k < (n - 1) % bs + 1 else entries[:-1]
+        seen.view(nb, bs)[:, k] = torch.bincount(hit, minlength=nb).double()
+    s = (q[0].double() @ rows.double().T) * SCALE + torch.log(seen)
+    want = torch.softmax(s, -1) @ rows[:, :512].double()
+    ws = torch.empty(pa.pa_latent_attention_workspace_size(1, 1, 16, n), dtype=torch.uint8, device=DEV)
+    out = torch.zeros(1, 16, 512, dtype=torch.bfloat16, device=DEV)
+    pa.pa_latent_attention(out, q.to(DEV), rows.view(nb, bs, 576).to(DEV), entries.int()[None].to(DEV), i32([n]), SCALE,
+                           2 ** 31 - 1, ws)
+    # a probability is rounded by at most 2^-8 of itself and the output by 2^-8 of
+    # it; a score's 576 additions (in 32 bits, truncated at worst) lose at most
+    # 576 * 2^-23 of the sum of magnitudes, which the softmax doubles; a range of
+    # 33,000 positions is 516 tiles of 64 additions to O and to l, a range's piece
+    # one of 160
+    score = 576 * 2 ** -23 * SCALE * float((q[0].double().abs() @ rows.double().abs().T).max())
+    mass = torch.softmax(s, -1) @ rows[:, :512].double().abs()
+    bound = (2 ** -8 + 2 * score + 2 * (516 * 64 + 160) * 2 ** -23) * mass + 2 ** -8 * want.abs()
+    assert ((out[0].cpu().double() - want).abs() <= bound).all()
+
+
 def test_absorbed_bad_query_start():
     w = R.Paged([50, 60], 16, pa.PA_KV_BF16, 41, DEV)
     q = torch.randn(6, 16, 576, device=DEV).bfloat16()
