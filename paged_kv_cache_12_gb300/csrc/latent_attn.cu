@@ -87,8 +87,11 @@ struct LatentArgs {
         const long long last = min((long long)w.T * H, (long long)(r + 1) * LT_ROWS) - 1;
         return (w.L - w.T + (int)(last / H)) / TOK + 1;
     }
-    __device__ __forceinline__ bool starts_ok() const {
-        return !query_start || offsets_ok(query_start, num_seqs, num_query_tokens);
+    __device__ __forceinline__ bool seq_ok(int i) const {
+        return !query_start || __ldg(query_start + i) <= __ldg(query_start + i + 1);
+    }
+    __device__ __forceinline__ bool ends_ok() const {
+        return !query_start || (__ldg(query_start) == 0 && __ldg(query_start + num_seqs) == num_query_tokens);
     }
     // A token's entry in its block table, and its offset in the block (a block
     // size is a power of two).
@@ -233,7 +236,9 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
             const bool ahead = lane >= 8 && lane < 16 && t + 1 < p.t1 && ntok < p.w.L;
             const int32_t nblk = ahead ? __ldg(row + a.entry_of(ntok)) : -1;
             const bool bad = __any_sync(0xffffffffu, mine && (blk < 0 || blk >= a.num_blocks));
-            const unsigned boxes = __ballot_sync(0xffffffffu, mine && !bad);
+            // (a group past the context is a box outside the cache, which reads as zeros)
+            const unsigned boxes = __ballot_sync(0xffffffffu, lane < L::TOK / 8 && !bad);
+            const int from = mine ? (blk << a.bs_log2) + a.offset_of(tok) : -8;
             if (bad && lane == 0) *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) = p.local + 1;
 #pragma unroll
             for (int part = 0; part < L::PARTS; ++part) {
@@ -244,8 +249,8 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
                                           (uint32_t)(__popc(boxes >> (part * N) & ((1u << N) - 1)) * LT_GROUP));
                 __syncwarp();
                 if (lane / N == part && (boxes >> lane & 1u))
-                    tma_load_3d(base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP, &maps.kv, 0,
-                                (blk << a.bs_log2) + a.offset_of(tok), 0, smem_u32(&c.kvfull[st]), first);
+                    tma_load_3d(base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP, &maps.kv, 0, from, 0,
+                                smem_u32(&c.kvfull[st]), first);
             }
             if (!w.ok) {   // a part may be on its way: the stage counts as sent below
                 ++cnt;
@@ -548,17 +553,19 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
                         make_uint4(pw[4 * k], pw[4 * k + 1], pw[4 * k + 2], pw[4 * k + 3]);
             }
             // Rows that some query row does not see, where P is 0 and a product with
-            // an infinity or a NaN would not be: those past the context are zeroed
-            // (a quantised tile's already are), and so is what is not finite among
-            // the new tokens' (the rows that see it become NaN below).
+            // an infinity or a NaN would not be: those past the context in its last
+            // group of eight are zeroed (a quantised tile's and those of later groups
+            // already are), and so is what is not finite among the new tokens' (the
+            // rows that see it become NaN below).
             if (first_vis - t0 < L::TOK) {
                 uint8_t *kv = smem + L::OFF_KV + st * L::STAGE;
-                for (int k = tid + max(0, first_vis - t0) * 64; k < L::TOK * 64; k += 128) {
+                const int left = min(L::TOK, p.w.L - t0), end = L::F8 ? left : (left + 7) & ~7;
+                for (int k = tid + max(0, first_vis - t0) * 64; k < end * 64; k += 128) {
                     const int r = k >> 6, cc = k & 63;
                     uint4 *at = reinterpret_cast<uint4 *>(kv + (r >> 3) * LT_GROUP + (cc >> 3) * 1024 + (r & 7) * 128 +
                                                           (cc & 7) * 16);
-                    if (r >= p.w.L - t0) {
-                        if (!L::F8) *at = make_uint4(0, 0, 0, 0);
+                    if (r >= left) {
+                        *at = make_uint4(0, 0, 0, 0);
                     } else if (const uint4 v = *at; not_finite<KV>(v)) {
                         *at = make_uint4(finite_part<KV>(v.x), finite_part<KV>(v.y), finite_part<KV>(v.z),
                                          finite_part<KV>(v.w));
@@ -638,13 +645,17 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
         mbar_init(smem_u32(&c.qempty), 2);
         mbar_init(smem_u32(&c.done), 3);
         c.abort = 0;
-        for (int k = 0; k < LT_BAD_SLOTS; ++k) c.bad[k] = 0, c.poison[k] = 0;
         fence_mbar_init();
+        tma_prefetch_map(&maps.q);
+        if (!L::F8) tma_prefetch_map(&maps.kv);
+    } else if (threadIdx.x >= 32 && threadIdx.x < 32 + LT_BAD_SLOTS) {
+        c.bad[threadIdx.x - 32] = 0;
+        c.poison[threadIdx.x - 32] = 0;
     }
+    grid_wait();
     make_plan(a, &c.plan, c.warp_sums);
     const Plan plan = c.plan;
-    // the merge's CTAs may come as this kernel's leave (they wait for all of them)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_release();   // the merge's CTAs may come as this kernel's leave (they wait for all of them)
     fill_idle_rows<LC / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
                            KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
@@ -688,42 +699,29 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
 // softmax warps left them.  When a CTA of the first kernel gave up, every row
 // becomes NaN.
 constexpr int MG_WARPS = 8, MG_BLOCKS = 4 * 32 / MG_WARPS;
+static_assert(32 * MG_WARPS >= AXIS_MAX_CTAS, "a thread per CTA's status");
 
 template <int KV>
 __global__ void __launch_bounds__(32 * MG_WARPS) latent_merge_kernel(const typename Lt<KV>::Args a, int ctas) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_release();
+    grid_wait();
     const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const int gave_up = threadIdx.x < ctas ? a.status[threadIdx.x] : 0;
     const Cut cut = a.cuts[cta];
     const int unit = blockIdx.y * MG_WARPS + (threadIdx.x >> 5), quarter = unit >> 5;
     if (16 * (blockIdx.y * MG_WARPS >> 5) >= cut.rows && (cta || blockIdx.y)) return;   // the whole block
-    const bool failed = any_gave_up(a.status, ctas);
+    const bool failed = __syncthreads_or(gave_up);
     if (cta == 0 && blockIdx.y == 0) {
         if (threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
         if (failed) fill_rows(a.out, 0, (long long)a.num_query_tokens * a.H * (LC / 8), KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     }
     const int m = 16 * quarter + (lane & 15), k8 = (unit & 31) >> 2, j = 2 * (unit & 3);
     if (failed || m >= cut.rows) return;
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < cut.pieces; ++k) M = fmaxf(M, a.ml[piece_slot(cut, cta, k) * LT_ROWS + m].x);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float acc[8] = {}, l = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < cut.pieces; ++k) {
-        const int slot = piece_slot(cut, cta, k);
-        const float2 ml = a.ml[slot * LT_ROWS + m];
-        const float4 x = a.o[partial_at(slot, quarter, k8, j, lane)], y = a.o[partial_at(slot, quarter, k8, j + 1, lane)];
-        const float wt = fast_exp2(ml.x - mu);
-        l = fmaf(ml.y, wt, l);
-        acc[0] = fmaf(x.x, wt, acc[0]);
-        acc[1] = fmaf(x.y, wt, acc[1]);
-        acc[2] = fmaf(x.z, wt, acc[2]);
-        acc[3] = fmaf(x.w, wt, acc[3]);
-        acc[4] = fmaf(y.x, wt, acc[4]);
-        acc[5] = fmaf(y.y, wt, acc[5]);
-        acc[6] = fmaf(y.z, wt, acc[6]);
-        acc[7] = fmaf(y.w, wt, acc[7]);
-    }
+    float acc[8], l;
+    join_pieces(
+        cut.pieces, [&](int i) { return a.ml[piece_slot(cut, cta, i) * LT_ROWS + m]; },
+        [&](int i) { return a.o[partial_at(piece_slot(cut, cta, i), quarter, k8, j, lane)]; },
+        [&](int i) { return a.o[partial_at(piece_slot(cut, cta, i), quarter, k8, j + 1, lane)]; }, acc, l);
     const float inv = 1.f / l;
     uint32_t v[4];
 #pragma unroll
@@ -785,20 +783,6 @@ cudaError_t lt_setup() {
 }
 
 template <int KV>
-int launch_merge(const typename Lt<KV>::Args &a, int ctas, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas, MG_BLOCKS);
-    cfg.blockDim = dim3(32 * MG_WARPS);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // launched while the first kernel drains
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, latent_merge_kernel<KV>, a, ctas));
-}
-
-template <int KV>
 int launch_latent(const typename Lt<KV>::Args &a, cudaStream_t st) {
     if (lt_setup<KV>() != cudaSuccess) return PA_ERR_CUDA;
     LtMaps maps{};
@@ -806,9 +790,9 @@ int launch_latent(const typename Lt<KV>::Args &a, cudaStream_t st) {
                     (Lt<KV>::F8 || row_map(&maps.kv, a.cache, a.num_blocks << a.bs_log2, KV));
     if (!ok) return PA_ERR_CUDA;
     const int ctas = std::min(num_sms(), AXIS_MAX_CTAS);
-    latent_kernel<KV><<<ctas, Lt<KV>::THREADS, Lt<KV>::SMEM, st>>>(maps, a);
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-    return launch_merge<KV>(a, ctas, st);
+    if (const int e = launch_early(latent_kernel<KV>, dim3((unsigned)ctas), Lt<KV>::THREADS, Lt<KV>::SMEM, st, maps, a))
+        return e;
+    return launch_early(latent_merge_kernel<KV>, dim3((unsigned)ctas, MG_BLOCKS), 32 * MG_WARPS, 0, st, a, ctas);
 }
 
 // Arguments of the kernels for a call.

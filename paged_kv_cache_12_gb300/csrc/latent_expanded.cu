@@ -109,9 +109,12 @@ struct ExpandedArgs {
     __device__ __forceinline__ int first_tiles(const Seq &w, int r) const {   // the first half's, of two
         return tiles_of(w, min(w.T, r % w.per_head * EX_ROWS + EX_HALF));
     }
-    __device__ __forceinline__ bool starts_ok() const {
-        const bool q = offsets_ok(query_start, num_seqs, num_query_tokens);
-        return offsets_ok(kv_start, num_seqs, num_kv_tokens) && q;
+    __device__ __forceinline__ bool seq_ok(int i) const {
+        return __ldg(query_start + i) <= __ldg(query_start + i + 1) && __ldg(kv_start + i) <= __ldg(kv_start + i + 1);
+    }
+    __device__ __forceinline__ bool ends_ok() const {
+        return __ldg(query_start) == 0 && __ldg(query_start + num_seqs) == num_query_tokens && __ldg(kv_start) == 0 &&
+               __ldg(kv_start + num_seqs) == num_kv_tokens;
     }
 };
 
@@ -521,13 +524,18 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
         mbar_init(smem_u32(&c.done), 1);
         c.abort = 0;
-        for (int k = 0; k < EX_POISON; ++k) c.poison[k] = 0;
         fence_mbar_init();
+        tma_prefetch_map(&tmq);
+        tma_prefetch_map(&tmk);
+        tma_prefetch_map(&tmr);
+        tma_prefetch_map(&tmv);
+    } else if (threadIdx.x >= 32 && threadIdx.x < 32 + EX_POISON) {
+        c.poison[threadIdx.x - 32] = 0;
     }
+    grid_wait();
     make_plan(a, &c.plan, c.warp_sums);
     const Plan plan = c.plan;
-    // the merge's CTAs may come as this kernel's leave (they wait for all of them)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_release();   // the merge's CTAs may come as this kernel's leave (they wait for all of them)
     fill_idle_rows<EV / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
                            KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
@@ -567,15 +575,18 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 // dims, in the order in which the softmax left them.  When a CTA of the first
 // kernel gave up, every row becomes NaN.
 constexpr int EM_WARPS = 8, EM_UNITS = EV / 8;   // warps of 32 rows
+static_assert(32 * EM_WARPS >= AXIS_MAX_CTAS, "a thread per CTA's status");
 
 template <int KV>
 __global__ void __launch_bounds__(32 * EM_WARPS) expanded_merge_kernel(const ExpandedArgs a, int ctas) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_release();
+    grid_wait();
     const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const int gave_up = threadIdx.x < ctas ? a.status[threadIdx.x] : 0;
     const Cut cut = a.cuts[cta];
     const int unit = blockIdx.y * EM_WARPS + (threadIdx.x >> 5), q = unit / EM_UNITS;
     if (32 * (blockIdx.y * EM_WARPS / EM_UNITS) >= cut.rows && (cta || blockIdx.y)) return;   // the whole block
-    const bool failed = any_gave_up(a.status, ctas);
+    const bool failed = __syncthreads_or(gave_up);
     if (cta == 0 && blockIdx.y == 0) {
         if (threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
         if (failed) fill_rows(a.out, 0, (long long)a.num_query_tokens * a.H * (EV / 8), KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
@@ -584,27 +595,11 @@ __global__ void __launch_bounds__(32 * EM_WARPS) expanded_merge_kernel(const Exp
     if (failed || m >= cut.rows) return;
     const int pieces = m < EX_HALF ? cut.pieces1 : cut.pieces;
     if (pieces == 1) return;   // this half was finished by one CTA
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < pieces; ++k) M = fmaxf(M, a.ml[piece_slot(cut, cta, k) * EX_ROWS + m].x);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float acc[8] = {}, l = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < pieces; ++k) {
-        const int slot = piece_slot(cut, cta, k);
-        const float2 ml = a.ml[slot * EX_ROWS + m];
-        const float4 x = a.o[partial_at(slot, q, k4, j, lane)], y = a.o[partial_at(slot, q, k4, j + 1, lane)];
-        const float wt = fast_exp2(ml.x - mu);
-        l = fmaf(ml.y, wt, l);
-        acc[0] = fmaf(x.x, wt, acc[0]);
-        acc[1] = fmaf(x.y, wt, acc[1]);
-        acc[2] = fmaf(x.z, wt, acc[2]);
-        acc[3] = fmaf(x.w, wt, acc[3]);
-        acc[4] = fmaf(y.x, wt, acc[4]);
-        acc[5] = fmaf(y.y, wt, acc[5]);
-        acc[6] = fmaf(y.z, wt, acc[6]);
-        acc[7] = fmaf(y.w, wt, acc[7]);
-    }
+    float acc[8], l;
+    join_pieces(
+        pieces, [&](int i) { return a.ml[piece_slot(cut, cta, i) * EX_ROWS + m]; },
+        [&](int i) { return a.o[partial_at(piece_slot(cut, cta, i), q, k4, j, lane)]; },
+        [&](int i) { return a.o[partial_at(piece_slot(cut, cta, i), q, k4, j + 1, lane)]; }, acc, l);
     const float inv = 1.f / l;
     uint32_t v[4];
 #pragma unroll
@@ -679,18 +674,10 @@ int launch_expanded(const ExpandedArgs &a, const CUtensorMap &tmq, const CUtenso
                     const CUtensorMap &tmv, cudaStream_t st) {
     if (const int e = ex_setup<KV>()) return e;
     const int ctas = std::min(num_sms(), AXIS_MAX_CTAS);
-    expanded_kernel<KV><<<ctas, EX_THREADS, EX_SMEM, st>>>(tmq, tmk, tmr, tmv, a);
-    if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((std::min(EX_ROWS, a.num_query_tokens) + 31) / 32 * EM_UNITS / EM_WARPS));
-    cfg.blockDim = dim3(32 * EM_WARPS);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // launched while the first kernel drains
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, expanded_merge_kernel<KV>, a, ctas));
+    if (const int e = launch_early(expanded_kernel<KV>, dim3((unsigned)ctas), EX_THREADS, EX_SMEM, st, tmq, tmk, tmr, tmv, a))
+        return e;
+    const dim3 grid((unsigned)ctas, (unsigned)((std::min(EX_ROWS, a.num_query_tokens) + 31) / 32 * EM_UNITS / EM_WARPS));
+    return launch_early(expanded_merge_kernel<KV>, grid, 32 * EM_WARPS, 0, st, a, ctas);
 }
 
 }  // namespace

@@ -224,6 +224,8 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
     __shared__ int s_slice;           // rank 0: that slice; -1: no token; -2: draw from p itself
     __shared__ int s_next;
     __shared__ int s_kept, s_n, s_d0;
+    grid_release();
+    grid_wait();
 
     if (warp == 0) {
         const int d0 = a.draft_start[seq], d1 = a.draft_start[seq + 1];
@@ -363,14 +365,10 @@ int launch_verify(const VerifyArgs &a, cudaStream_t st) {
     const long long slots = (long long)num_sms() * VRESIDENT;
     const unsigned b = (unsigned)a.num_seqs;
     if (b * 8LL <= slots)
-        verify_kernel<T, 8><<<b * 8, VTHREADS, 0, st>>>(a);
-    else if (b * 4LL <= slots)
-        verify_kernel<T, 4><<<b * 4, VTHREADS, 0, st>>>(a);
-    else if (b * 2LL <= slots)
-        verify_kernel<T, 2><<<b * 2, VTHREADS, 0, st>>>(a);
-    else
-        verify_kernel<T, 1><<<b, VTHREADS, 0, st>>>(a);
-    return cuda_status(cudaGetLastError());
+        return launch_early(verify_kernel<T, 8>, dim3(b * 8), VTHREADS, 0, st, a);
+    if (b * 4LL <= slots) return launch_early(verify_kernel<T, 4>, dim3(b * 4), VTHREADS, 0, st, a);
+    if (b * 2LL <= slots) return launch_early(verify_kernel<T, 2>, dim3(b * 2), VTHREADS, 0, st, a);
+    return launch_early(verify_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a);
 }
 
 }  // namespace

@@ -25,8 +25,8 @@
 //                           of a team's axis (row tile j * team + member);
 //                           start(w, w.rts / team, team) = the sequence's units
 //   row_tiles(w, r)         KV tiles of row tile r
-//   starts_ok()             whether the row offsets are in order (called by
-//                           every thread of the block)
+//   seq_ok(i), ends_ok()    whether sequence i's row offsets are in order, and
+//                           all of them a cover of the rows
 //   num_seqs, cuts          sequences; [AXIS_MAX_CTAS] what a cut row tile's merge
 //                           needs, written by the CTA whose range begins in it
 //   cut_rows(w, r)          rows of a row tile
@@ -45,7 +45,7 @@ constexpr int AXIS_MAX_CTAS = 160;   // CTAs of a launch: one per SM, at most th
 struct Plan {
     long long u0, u1, base;   // this CTA's range; first unit of sequence seq
     long long total;          // units of the axis (0 too if the row offsets are out of order)
-    int seq;                  // the sequence in which the range begins
+    int seq, j;               // the sequence in which the range begins, and its row tile (numbered as the axis has them)
     int team;                 // CTAs of a team
     int ok;                   // the row offsets are in order
 };
@@ -64,26 +64,18 @@ struct Cut {
 };
 
 // First unit of team k's range; `parts` = min(teams, total) teams have one, of at
-// least a unit each.
-__device__ __forceinline__ long long range_begin(long long total, int k, int parts) { return total * k / parts; }
-
-// Whether the n + 1 device offsets are a non-decreasing cover of [0, end):
-// every thread of the block calls it and gets the answer.
-__device__ __forceinline__ bool offsets_ok(const int32_t *start, int n, int end) {
-    bool ok = start[0] == 0 && start[n] == end;
-    for (int i = threadIdx.x; i < n; i += blockDim.x)
-        if (start[i] > start[i + 1]) ok = false;
-    return __syncthreads_and(ok);
+// least a unit each.  (A 64-bit division takes several times a 32-bit one's time,
+// and the plan is most of a short call's start.)
+__device__ __forceinline__ long long range_begin(long long total, int k, int parts) {
+    static_assert(AXIS_MAX_CTAS <= 255, "total * k in 32 bits");
+    if (total < 1 << 24) return (uint32_t)total * (uint32_t)k / (uint32_t)parts;
+    return total * k / parts;
 }
 
-// The last of n sequences that starts at or before row `row`.
-__device__ __forceinline__ int sequence_of(const int32_t *start, int n, int row) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= row) lo = mid; else hi = mid;
-    }
-    return lo;
+// The first team whose range begins at unit u > 0 or later (`parts` if there is none).
+__device__ __forceinline__ int team_from(long long total, long long u, int parts) {
+    if (total < 1 << 24) return (int)(((uint32_t)u * (uint32_t)parts + (uint32_t)total - 1) / (uint32_t)total);
+    return (int)((u * parts + total - 1) / total);
 }
 
 // The last of a team's row tiles (numbered as the axis has them) that starts at
@@ -101,19 +93,25 @@ __device__ __forceinline__ int row_tile_at(const P &a, const typename P::Seq &w,
 // This block's plan (warp_sums: one number per warp, in shared memory).
 template <class P>
 __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *warp_sums) {
-    const bool ok = a.starts_ok();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     const int per = (a.num_seqs + blockDim.x - 1) / blockDim.x;
     const int i0 = min(a.num_seqs, (int)threadIdx.x * per), i1 = min(a.num_seqs, i0 + per);
-    bool pairs = true;
-    for (int i = i0; ok && i < i1; ++i) pairs = pairs && a.in_teams(a.seq_work(i));
+    bool in_order = a.ends_ok(), pairs = true;
+    long long one = 0, two = 0;   // units without teams and in teams
+    for (int i = i0; i < i1; ++i) {
+        const typename P::Seq w = a.seq_work(i);
+        in_order = in_order && a.seq_ok(i);
+        pairs = pairs && a.in_teams(w);
+        one += a.start(w, w.rts, 1);
+        if (pairs) two += a.start(w, w.rts / 2, 2);
+    }
+    const bool ok = __syncthreads_and(in_order);
     const int team = __syncthreads_and(pairs) ? 2 : 1;
     auto units = [&](int i) {
         const typename P::Seq w = a.seq_work(i);
         return a.start(w, w.rts / team, team);
     };
-    long long mine = 0;
-    for (int i = i0; ok && i < i1; ++i) mine += units(i);
+    const long long mine = !ok ? 0 : team == 2 ? two : one;
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -140,12 +138,13 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         if (u0 >= u1) {
             a.cuts[cta].rows = 0;
             plan->seq = a.num_seqs;
+            plan->j = 0;
         }
     }
     if (u0 < u1 && begin <= u0 && u0 < end) {   // one thread
         long long s = begin;
         int i = i0;
-        for (;; ++i) {
+        for (; i + 1 < i1; ++i) {
             const long long n = units(i);
             if (u0 < s + n) break;
             s += n;
@@ -155,15 +154,13 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         // the row tile in which the range begins: cut here if a KV tile of it lies on either side
         const typename P::Seq w = a.seq_work(i);
         const int j = row_tile_at(a, w, team, u0 - s), r = j * team + cta % team;
+        plan->j = j;
         const long long at = s + a.start(w, j, team), first = at + P::COST;
         const int ntiles = a.row_tiles(w, r);
         Cut cut{};
         if (k > 0 && first < u0 && u0 < first + ntiles && range_begin(total, k - 1, parts) <= first) {
-            auto pieces = [&](int tiles) {   // of the row tile's first `tiles` KV tiles
-                int n = 1;
-                while (range_begin(total, k - 1 + n, parts) < first + tiles) ++n;
-                return n;
-            };
+            // of the row tile's first `tiles` KV tiles: the teams from k - 1 on whose ranges begin before their end
+            auto pieces = [&](int tiles) { return max(1, team_from(total, first + tiles, parts) - (k - 1)); };
             cut.row0 = a.first_row(w, r);
             cut.rows = a.cut_rows(w, r);
             cut.pieces = pieces(ntiles);
@@ -185,11 +182,9 @@ struct Walk {
     typename P::Seq w;
     int t0, t1, ntiles, local;   // the piece: KV tiles [t0, t1) of ntiles; its number in this CTA
 
-    __device__ Walk(const P &args, const Plan &p) : a(args), u0(p.u0), u1(p.u1), base(p.base), team(p.team), seq(p.seq), j(0) {
+    __device__ Walk(const P &args, const Plan &p) : a(args), u0(p.u0), u1(p.u1), base(p.base), team(p.team), seq(p.seq), j(p.j - 1) {
         local = -1;
-        if (u0 >= u1) return;
-        w = a.seq_work(seq);
-        j = row_tile_at(a, w, team, u0 - base) - 1;
+        if (u0 < u1) w = a.seq_work(seq);
     }
     // The next piece; false at the end of the range.
     __device__ bool next() {
@@ -224,11 +219,45 @@ __device__ __forceinline__ int piece_slot(const Cut &cut, int cta, int i) {
     return i ? 2 * cta + (i - 1) * cut.step : cut.first;
 }
 
-// Whether a CTA of the first kernel gave up (called by the whole block).
-__device__ __forceinline__ bool any_gave_up(const int *status, int ctas) {
-    int failed = 0;
-    for (int i = threadIdx.x; i < ctas; i += blockDim.x) failed |= status[i];
-    return __syncthreads_or(failed);
+// Joins a cut row tile's pieces for one row and eight of its dims: piece i has the
+// maximum (log2 units) and sum ml(i) and the unnormalised x(i), y(i).  Four pieces
+// at a time, so that their loads are on their way together.
+template <class ML, class X, class Y>
+__device__ __forceinline__ void join_pieces(int pieces, ML ml, X x, Y y, float (&acc)[8], float &l) {
+    constexpr int N = 4;
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+    l = 0.f;
+    for (int i0 = 0; i0 < pieces; i0 += N) {
+        float2 s[N];
+        float4 v[N], w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i0 + i < pieces) {
+                s[i] = ml(i0 + i), v[i] = x(i0 + i), w[i] = y(i0 + i);
+            } else {
+                s[i] = make_float2(-INFINITY, 0.f), v[i] = w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        float m = M;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, s[i].x);
+        const float mu = m == -INFINITY ? 0.f : m;   // nothing seen yet
+        const float old = fast_exp2(M - mu);
+        l *= old;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] *= old;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float wt = fast_exp2(s[i].x - mu);
+            const float o[8] = {v[i].x, v[i].y, v[i].z, v[i].w, w[i].x, w[i].y, w[i].z, w[i].w};
+            l = fmaf(s[i].y, wt, l);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = fmaf(o[k], wt, acc[k]);
+        }
+        M = m;
+    }
 }
 
 // The block writes `bits` to 16-byte vectors [from, to) of out.

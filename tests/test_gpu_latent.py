@@ -584,3 +584,71 @@ def test_a_serving_run(kv):
     a, b = R.verify(target.double().cpu().numpy(), draft.double().cpu().numpy(), drafts.tolist(), [0, 3, 5],
                     u.double().tolist(), pick.double().tolist(), 3)
     assert acc.tolist() == a.tolist() and tok.tolist() == b.tolist()
+
+
+# ------------------------------------------------------------------ calls behind one another
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_one_another(captured):
+    # calls of three kinds queued without a pause, sharing a workspace, each on
+    # inputs that the operation before it has just written: as when run alone
+    dt = torch.bfloat16
+    heads, news = 16, [3, 1, 2]
+    w = R.Paged([700, 90, 333], 16, pa.PA_KV_BF16, 71, DEV)
+    g = torch.Generator().manual_seed(4)
+    nq = sum(news)
+    queries = [torch.randn(nq, heads, 576, generator=g).to(dt).to(DEV) for _ in range(4)]
+    starts = i32([0, 3, 4, 6])
+    alone = [absorbed(w, heads, news, 0, query=q)[1] for q in queries]
+    eq, ek, er, ev, ewant, (eqs, eks, _) = expanded(dt, [200, 40], [60, 300], 2, 13)
+    ws = torch.full((max(pa.pa_latent_attention_workspace_size(3, nq, heads, 700),
+                         pa.pa_latent_attention_expanded_workspace_size(2, 240, 2)),), 255, dtype=torch.uint8, device=DEV)
+    query, outs = torch.empty_like(queries[0]), [torch.empty_like(alone[0]) for _ in queries]
+    eouts = [torch.empty_like(ewant) for _ in queries]
+    probs = torch.rand(7, 1000, generator=g).to(DEV)
+    tokens = [torch.empty(2, 4, dtype=torch.int32, device=DEV) for _ in queries]
+    kept = [torch.empty(2, dtype=torch.int32, device=DEV) for _ in queries]
+    drafts, dstart = torch.randint(1000, (5,), generator=g).int().to(DEV), i32([0, 3, 5])
+    u, su = torch.rand(5, generator=g).to(DEV), torch.rand(2, generator=g).to(DEV)
+
+    def run():
+        for i, q in enumerate(queries):
+            outs[i].zero_()
+            query.copy_(q)
+            pa.pa_latent_attention(outs[i], query, w.cache, w.tables, w.lens_t, SCALE, 700, ws, query_start=starts)
+            eouts[i].zero_()
+            pa.pa_latent_attention_expanded(eouts[i], eq, ek, er, ev, eqs, eks, SCALE, ws)
+            pa.pa_verify_drafts(kept[i], tokens[i], probs, None, drafts, dstart, u, su)
+            pa.pa_verify_drafts(kept[i], tokens[i], probs, None, drafts, dstart, u, su)
+
+    def check():
+        torch.cuda.synchronize()
+        for i in range(len(queries)):
+            assert same_bits(outs[i], alone[i]) and same_bits(eouts[i], ewant)
+            assert torch.equal(tokens[i], tokens[0]) and torch.equal(kept[i], kept[0])
+            assert (kept[i] >= 0).all()
+
+    if not captured:
+        for _ in range(20):
+            run()
+        check()
+        return
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    side.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        other = torch.cuda.Stream()
+        other.wait_stream(side)
+        with torch.cuda.stream(other):   # a branch that joins right before a call
+            junk = torch.ones(1 << 20, device=DEV) * 2
+        side.wait_stream(other)
+        pa.pa_latent_attention(outs[0], queries[0], w.cache, w.tables, w.lens_t, SCALE, 700, ws, query_start=starts)
+        run()
+    for _ in range(3):
+        for t in outs + eouts:
+            t.fill_(math.nan)
+        graph.replay()
+        check()
+    del junk
