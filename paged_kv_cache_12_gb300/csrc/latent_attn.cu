@@ -81,11 +81,14 @@ struct LatentArgs {
     // rows see fewer, which matters only for long chunks; those belong to the
     // expanded form).
     __device__ __forceinline__ long long start(const Seq &w, int j, int) const { return (long long)j * (w.tiles + COST); }
+    __device__ __forceinline__ int row_tile_at(const Seq &w, long long u, int) const {
+        return (int)quick_div(u, w.tiles + COST);
+    }
     __device__ __forceinline__ bool in_teams(const Seq &w) const { return w.rts % 2 == 0; }
     // KV tiles that row tile r sees: up to its last row's own position.
     __device__ __forceinline__ int row_tiles(const Seq &w, int r) const {
-        const long long last = min((long long)w.T * H, (long long)(r + 1) * LT_ROWS) - 1;
-        return (w.L - w.T + (int)(last / H)) / TOK + 1;
+        const uint32_t last = min((uint32_t)w.T * H, ((uint32_t)r + 1) * LT_ROWS) - 1;
+        return (w.L - w.T + (int)(last / (uint32_t)H)) / TOK + 1;
     }
     __device__ __forceinline__ bool seq_ok(int i) const {
         return !query_start || __ldg(query_start + i) <= __ldg(query_start + i + 1);
@@ -220,6 +223,8 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
     int cnt = 0, pieces = 0;
     while (w.ok && p.next()) {
         const int32_t *row = a.block_tables + (long long)p.seq * a.mbps;
+        auto id_of = [&](int tok) { return lane < L::TOK / 8 && tok < p.w.L ? __ldg(row + a.entry_of(tok)) : 0; };
+        const int32_t first_id = id_of(p.t0 * L::TOK + 8 * lane);   // on its way with the queries
         if (!w.warp(c.qempty, pieces + 1)) break;
         if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.qfull), LT_Q);
         __syncwarp();
@@ -230,7 +235,7 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
         for (int t = p.t0; t < p.t1; ++t, ++cnt) {
             const int tok = t * L::TOK + 8 * lane, st = cnt & 1;
             const bool mine = lane < L::TOK / 8 && tok < p.w.L;
-            const int32_t blk = mine ? __ldg(row + a.entry_of(tok)) : 0;
+            const int32_t blk = t == p.t0 ? first_id : id_of(tok);
             // lanes 8 .. 15: a group of the next tile, to be fetched into L2
             const int ntok = tok + L::TOK - 64;
             const bool ahead = lane >= 8 && lane < 16 && t + 1 < p.t1 && ntok < p.w.L;
@@ -484,9 +489,9 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
         const int rows = a.rows(p.w, p.r);
         const bool live = 16 * q < rows;   // some row of this warp exists
         const bool mine = m < rows;
-        const int vis = mine ? p.w.L - p.w.T + (int)(((long long)p.r * LT_ROWS + m) / a.H) + 1 : p.w.L;
+        const int vis = mine ? p.w.L - p.w.T + (int)(((uint32_t)p.r * LT_ROWS + m) / (uint32_t)a.H) + 1 : p.w.L;
         // what the row tile's first row sees
-        const int first_vis = p.w.L - p.w.T + (int)((long long)p.r * LT_ROWS / a.H) + 1;
+        const int first_vis = p.w.L - p.w.T + (int)((uint32_t)p.r * LT_ROWS / (uint32_t)a.H) + 1;
         float mrun = -INFINITY, l = 0.f;
         for (int t = p.t0; t < p.t1; ++t, ++n) {
             const int st = n & 1, t0 = t * L::TOK;
@@ -653,20 +658,19 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
         c.poison[threadIdx.x - 32] = 0;
     }
     grid_wait();
+    if (warp == 3) {   // (not before: an earlier kernel may still need its own)
+        tmem_alloc(smem_u32(&c.tmem), LT_TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
     make_plan(a, &c.plan, c.warp_sums);
+    tc_fence_after_sync();
     const Plan plan = c.plan;
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
     grid_release();   // the merge's CTAs may come as this kernel's leave (they wait for all of them)
     fill_idle_rows<LC / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
                            KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
-        if (warp == 0) {
-            tmem_alloc(smem_u32(&c.tmem), LT_TMEM);
-            tmem_relinquish();
-        }
-        tc_fence_before_sync();
-        __syncthreads();
-        tc_fence_after_sync();
-        const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
         Walk<typename L::Args> p(a, plan);
         if (warp == 0) {
             if constexpr (L::F8)
@@ -683,11 +687,9 @@ __global__ void __launch_bounds__(Lt<KV>::THREADS, 1)
         }
         tc_fence_before_sync();
         __syncthreads();
-        if (warp == 0) {
-            tc_fence_after_sync();
-            tmem_dealloc(tmem, LT_TMEM);
-        }
+        tc_fence_after_sync();
     }
+    if (warp == 3) tmem_dealloc(tmem, LT_TMEM);
     if (threadIdx.x == 0) a.status[blockIdx.x] = c.abort;
 }
 

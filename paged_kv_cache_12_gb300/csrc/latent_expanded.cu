@@ -87,6 +87,16 @@ struct ExpandedArgs {
         const int h = j / per, i = j - h * per;
         return h * (before(per - 1) + COST + (w.L + EX_TOK - 1) / EX_TOK) + before(i);
     }
+    __device__ __forceinline__ int row_tile_at(const Seq &w, long long u, int team) const {
+        const int per = w.per_head / team;   // (of a sequence with work)
+        const int h = (int)quick_div(u, start(w, per, team));
+        int r = h * per, hi = r + per;
+        while (hi - r > 1) {
+            const int mid = (r + hi) >> 1;
+            if (start(w, mid, team) <= u) r = mid; else hi = mid;
+        }
+        return r;
+    }
     // In teams where a sequence's past is long against its new tokens, so that
     // the two row tiles' KV ranges are nearly the same (2048 of 12000 tokens, 32
     // heads: 358 us in teams, 378 without).
@@ -411,16 +421,17 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = m / 8 + 16 * i;
-                        if (r >= lo && r < hi) any |= not_finite<KV>(blk[m + EX_HALF * i]);
+                        if (r >= hi)
+                            blk[m + EX_HALF * i] = make_uint4(0, 0, 0, 0);
+                        else if (r >= lo)
+                            any |= not_finite<KV>(blk[m + EX_HALF * i]);
                     }
-                    if (any || hi < EX_TOK) {
+                    if (any) {
 #pragma unroll 1
                         for (int i = 0; i < 8; ++i) {
                             const int r = m / 8 + 16 * i;
                             uint4 &v = blk[m + EX_HALF * i];
-                            if (r >= hi) {
-                                v = make_uint4(0, 0, 0, 0);
-                            } else if (r >= lo && not_finite<KV>(v)) {
+                            if (r >= lo && r < hi && not_finite<KV>(v)) {
                                 v = make_uint4(finite_part<KV>(v.x), finite_part<KV>(v.y), finite_part<KV>(v.z),
                                                finite_part<KV>(v.w));
                                 bad = min(bad, t0 + r);
@@ -533,20 +544,19 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         c.poison[threadIdx.x - 32] = 0;
     }
     grid_wait();
+    if (warp == 2) {   // (not before: an earlier kernel may still need its own)
+        tmem_alloc(smem_u32(&c.tmem), EX_TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
     make_plan(a, &c.plan, c.warp_sums);
+    tc_fence_after_sync();
     const Plan plan = c.plan;
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
     grid_release();   // the merge's CTAs may come as this kernel's leave (they wait for all of them)
     fill_idle_rows<EV / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
                            KV == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
-        if (warp == 2) {
-            tmem_alloc(smem_u32(&c.tmem), EX_TMEM);
-            tmem_relinquish();
-        }
-        tc_fence_before_sync();
-        __syncthreads();
-        tc_fence_after_sync();
-        const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
         Walk<ExpandedArgs> p(a, plan);
         if (warp >= 4) {
             regs_increase<EX_REGS_HIGH>();
@@ -562,11 +572,9 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
         tc_fence_before_sync();
         __syncthreads();
-        if (warp == 2) {
-            tc_fence_after_sync();
-            tmem_dealloc(tmem, EX_TMEM);
-        }
+        tc_fence_after_sync();
     }
+    if (warp == 2) tmem_dealloc(tmem, EX_TMEM);
     if (threadIdx.x == 0) a.status[blockIdx.x] = c.abort;
 }
 

@@ -24,6 +24,7 @@
 //   start(w, j, team)       first unit, within its sequence, of the j-th row tile
 //                           of a team's axis (row tile j * team + member);
 //                           start(w, w.rts / team, team) = the sequence's units
+//   row_tile_at(w, u, team) the last of those that start at or before unit u
 //   row_tiles(w, r)         KV tiles of row tile r
 //   seq_ok(i), ends_ok()    whether sequence i's row offsets are in order, and
 //                           all of them a cover of the rows
@@ -41,6 +42,8 @@ namespace pa {
 namespace {
 
 constexpr int AXIS_MAX_CTAS = 160;   // CTAs of a launch: one per SM, at most this many
+constexpr int AXIS_MIN_UNITS = 2;    // units of a range, at least (600 tokens, 16 heads, absorbed: 13.0 us with 1, 12.4
+                                     // with 2, 14.1 with 3; expanded 24.3, 24.3 and 25.6)
 
 struct Plan {
     long long u0, u1, base;   // this CTA's range; first unit of sequence seq
@@ -63,31 +66,19 @@ struct Cut {
     int pad;
 };
 
-// First unit of team k's range; `parts` = min(teams, total) teams have one, of at
-// least a unit each.  (A 64-bit division takes several times a 32-bit one's time,
-// and the plan is most of a short call's start.)
-__device__ __forceinline__ long long range_begin(long long total, int k, int parts) {
-    static_assert(AXIS_MAX_CTAS <= 255, "total * k in 32 bits");
-    if (total < 1 << 24) return (uint32_t)total * (uint32_t)k / (uint32_t)parts;
-    return total * k / parts;
+// a / b for a, b >= 0: a 64-bit division takes several times a 32-bit one's time,
+// and the plan is most of a short call's start.
+__device__ __forceinline__ long long quick_div(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b;
 }
+
+// First unit of team k's range; `parts` teams have one, of AXIS_MIN_UNITS units each
+// at least.
+__device__ __forceinline__ long long range_begin(long long total, int k, int parts) { return quick_div(total * k, parts); }
 
 // The first team whose range begins at unit u > 0 or later (`parts` if there is none).
 __device__ __forceinline__ int team_from(long long total, long long u, int parts) {
-    if (total < 1 << 24) return (int)(((uint32_t)u * (uint32_t)parts + (uint32_t)total - 1) / (uint32_t)total);
-    return (int)((u * parts + total - 1) / total);
-}
-
-// The last of a team's row tiles (numbered as the axis has them) that starts at
-// or before unit u of the sequence.
-template <class P>
-__device__ __forceinline__ int row_tile_at(const P &a, const typename P::Seq &w, int team, long long u) {
-    int r = 0, hi = w.rts / team;
-    while (hi - r > 1) {
-        const int mid = (r + hi) >> 1;
-        if (a.start(w, mid, team) <= u) r = mid; else hi = mid;
-    }
-    return r;
+    return (int)quick_div(u * parts + total - 1, total);
 }
 
 // This block's plan (warp_sums: one number per warp, in shared memory).
@@ -126,7 +117,7 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         total += warp_sums[j];
     }
     const long long begin = before + upto - mine, end = before + upto;
-    const int parts = (int)min((long long)(gridDim.x / team), total), cta = blockIdx.x, k = cta / team;
+    const int parts = (int)min((long long)(gridDim.x / team), total > 0 ? max(1LL, quick_div(total, AXIS_MIN_UNITS)) : 0), cta = blockIdx.x, k = cta / team;
     const long long u0 = k < parts ? range_begin(total, k, parts) : 0;
     const long long u1 = k < parts ? range_begin(total, k + 1, parts) : 0;
     if (threadIdx.x == 0) {
@@ -153,7 +144,7 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         plan->base = s;
         // the row tile in which the range begins: cut here if a KV tile of it lies on either side
         const typename P::Seq w = a.seq_work(i);
-        const int j = row_tile_at(a, w, team, u0 - s), r = j * team + cta % team;
+        const int j = a.row_tile_at(w, u0 - s, team), r = j * team + cta % team;
         plan->j = j;
         const long long at = s + a.start(w, j, team), first = at + P::COST;
         const int ntiles = a.row_tiles(w, r);
