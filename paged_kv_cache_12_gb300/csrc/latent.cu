@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(256) latent_write_kernel(const uint4 *__restri
                                                            long long latent_vecs, long long rope_vecs,
                                                            long long num_slots) {
     const long long total = (long long)num_tokens * VROW;
+    grid_release();
+    grid_wait();
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
          i += (long long)gridDim.x * blockDim.x) {
         const long long t = i / VROW;
@@ -81,6 +83,8 @@ __global__ void __launch_bounds__(256) latent_write_fp8_kernel(const uint4 *__re
                                                                long long num_slots) {
     const int lane = threadIdx.x & 31;
     const int step = (int)(gridDim.x * (blockDim.x >> 5));
+    grid_release();
+    grid_wait();
     for (long long t = blockIdx.x * (long long)(blockDim.x >> 5) + (threadIdx.x >> 5); t < num_tokens; t += step) {
         const uint4 x = latent[t * latent_vecs + lane], y = latent[t * latent_vecs + 32 + lane];
         uint4 r = make_uint4(0, 0, 0, 0);
@@ -129,6 +133,8 @@ __global__ void __launch_bounds__(READ_THREADS) latent_read_kernel(
     const int base = blockIdx.x * READ_ROWS;
     const bool kept = num_seqs <= READ_STARTS;
     bool ok = true;
+    grid_release();
+    grid_wait();
     for (int i = threadIdx.x; i <= num_seqs; i += blockDim.x) {
         const int b = row_start[i], a = i ? row_start[i - 1] : 0;
         if (b < a || b > num_rows || (i == 0 && b != 0)) ok = false;
@@ -255,16 +261,14 @@ extern "C" int pa_latent_write(const uint16_t *latent, const uint16_t *rope, con
     const long long cap = (long long)num_sms() * 16;
     if (kv_dtype == PA_KV_FP8_E4M3) {
         const long long blocks = std::min(((long long)num_tokens + 7) / 8, cap);
-        latent_write_fp8_kernel<<<(unsigned)blocks, 256, 0, st>>>(c, r, slot_mapping, static_cast<uint8_t *>(cache),
-                                                                  num_tokens, latent_stride / 8, rope_stride / 8,
-                                                                  num_slots);
-    } else {
-        const long long blocks = std::min(((long long)num_tokens * VROW + 255) / 256, cap);
-        latent_write_kernel<<<(unsigned)blocks, 256, 0, st>>>(c, r, slot_mapping, static_cast<uint4 *>(cache),
-                                                              num_tokens, latent_stride / 8, rope_stride / 8,
-                                                              num_slots);
+        return launch_early(latent_write_fp8_kernel, dim3((unsigned)blocks), 256, 0, st, c, r, slot_mapping,
+                            static_cast<uint8_t *>(cache), num_tokens, (long long)latent_stride / 8,
+                            (long long)rope_stride / 8, num_slots);
     }
-    return cuda_status(cudaGetLastError());
+    const long long blocks = std::min(((long long)num_tokens * VROW + 255) / 256, cap);
+    return launch_early(latent_write_kernel, dim3((unsigned)blocks), 256, 0, st, c, r, slot_mapping,
+                        static_cast<uint4 *>(cache), num_tokens, (long long)latent_stride / 8,
+                        (long long)rope_stride / 8, num_slots);
 }
 
 extern "C" int pa_latent_block_copy(void *cache, const int64_t *pairs, int num_pairs, int block_size,
@@ -303,14 +307,8 @@ extern "C" int pa_latent_read(uint16_t *out, const void *cache, const int32_t *b
     const unsigned grid = ((unsigned)num_rows + READ_ROWS - 1) / READ_ROWS;
     uint4 *o = reinterpret_cast<uint4 *>(out);
     const uint8_t *c = static_cast<const uint8_t *>(cache);
-    if (kv_dtype == PA_KV_FP8_E4M3)
-        latent_read_kernel<true><<<grid, READ_THREADS, 0, st>>>(o, c, block_tables, row_start, first_token, num_seqs,
-                                                                num_rows, out_stride / 8, block_size, num_blocks,
-                                                                max_blocks_per_seq, 0x7fc07fc0u);
-    else
-        latent_read_kernel<false><<<grid, READ_THREADS, 0, st>>>(o, c, block_tables, row_start, first_token, num_seqs,
-                                                                 num_rows, out_stride / 8, block_size, num_blocks,
-                                                                 max_blocks_per_seq,
-                                                                 kv_dtype == PA_KV_BF16 ? 0x7fc07fc0u : 0x7e007e00u);
-    return cuda_status(cudaGetLastError());
+    const uint32_t nan_pair = kv_dtype == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u;
+    return launch_early(kv_dtype == PA_KV_FP8_E4M3 ? latent_read_kernel<true> : latent_read_kernel<false>, dim3(grid),
+                        READ_THREADS, 0, st, o, c, block_tables, row_start, first_token, num_seqs, num_rows,
+                        (long long)out_stride / 8, block_size, (long long)num_blocks, max_blocks_per_seq, nan_pair);
 }
