@@ -162,7 +162,9 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
 // Programmatic dependent launch: wait until the kernels before this one in the
 // stream have completed and their writes are visible (at once, if it was not
 // launched early), and let the next kernel, if it is launched that way, come as
-// this one's CTAs leave.
+// this one's CTAs leave.  What an earlier kernel may have written is read after the
+// wait and by ordinary loads (no __ldg, no const __restrict__: non-coherent loads may
+// come before it, or find an older line in L1).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -28,10 +28,8 @@ constexpr int VROW = LROW / 8;   // 16-byte vectors of a 16-bit row
 constexpr int VLAT = LC / 8;     // of them latent
 
 // Rows of 16-bit elements, one thread per 16-byte vector.
-__global__ void __launch_bounds__(256) latent_write_kernel(const uint4 *__restrict__ latent,
-                                                           const uint4 *__restrict__ rope,
-                                                           const int64_t *__restrict__ slot_mapping,
-                                                           uint4 *__restrict__ cache, int num_tokens,
+__global__ void __launch_bounds__(256) latent_write_kernel(const uint4 *latent, const uint4 *rope,
+                                                           const int64_t *slot_mapping, uint4 *cache, int num_tokens,
                                                            long long latent_vecs, long long rope_vecs,
                                                            long long num_slots) {
     const long long total = (long long)num_tokens * VROW;
@@ -75,10 +73,9 @@ __device__ __forceinline__ uint2 quantise_bf16x8(uint4 x, float inv) {
 
 // Quantised rows, one warp per token: lane l holds elements 8 l .. 8 l + 7
 // (groups 0 and 1, sixteen lanes each) and 256 + 8 l .. (groups 2 and 3).
-__global__ void __launch_bounds__(256) latent_write_fp8_kernel(const uint4 *__restrict__ latent,
-                                                               const uint4 *__restrict__ rope,
-                                                               const int64_t *__restrict__ slot_mapping,
-                                                               uint8_t *__restrict__ cache, int num_tokens,
+__global__ void __launch_bounds__(256) latent_write_fp8_kernel(const uint4 *latent, const uint4 *rope,
+                                                               const int64_t *slot_mapping, uint8_t *cache,
+                                                               int num_tokens,
                                                                long long latent_vecs, long long rope_vecs,
                                                                long long num_slots) {
     const int lane = threadIdx.x & 31;
@@ -125,8 +122,8 @@ constexpr int READ_STARTS = 1024;
 
 template <bool F8>
 __global__ void __launch_bounds__(READ_THREADS) latent_read_kernel(
-    uint4 *__restrict__ out, const uint8_t *__restrict__ cache, const int32_t *__restrict__ block_tables,
-    const int32_t *__restrict__ row_start, const int32_t *__restrict__ first_token, int num_seqs, int num_rows,
+    uint4 *out, const uint8_t *cache, const int32_t *block_tables, const int32_t *row_start,
+    const int32_t *first_token, int num_seqs, int num_rows,
     long long out_vecs, int block_size, long long num_blocks, int mbps, uint32_t nan_pair) {
     __shared__ long long slots[READ_ROWS];
     __shared__ int starts[READ_STARTS + 1];

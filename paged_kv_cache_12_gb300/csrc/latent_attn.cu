@@ -68,9 +68,9 @@ struct LatentArgs {
     };
     __device__ __forceinline__ Seq seq_work(int i) const {
         Seq w;
-        w.L = __ldg(context_lens + i);
-        w.q0 = query_start ? __ldg(query_start + i) : i;
-        w.T = query_start ? __ldg(query_start + i + 1) - w.q0 : 1;
+        w.L = context_lens[i];
+        w.q0 = query_start ? query_start[i] : i;
+        w.T = query_start ? query_start[i + 1] - w.q0 : 1;
         w.valid = w.L >= 0 && w.L <= max_context_len && (long long)w.L <= (long long)mbps << bs_log2 &&
                   !(query_start && w.T > w.L);
         w.tiles = w.valid && w.T > 0 ? w.L / TOK + (w.L % TOK != 0) : 0;
@@ -91,10 +91,10 @@ struct LatentArgs {
         return (w.L - w.T + (int)(last / (uint32_t)H)) / TOK + 1;
     }
     __device__ __forceinline__ bool seq_ok(int i) const {
-        return !query_start || __ldg(query_start + i) <= __ldg(query_start + i + 1);
+        return !query_start || query_start[i] <= query_start[i + 1];
     }
     __device__ __forceinline__ bool ends_ok() const {
-        return !query_start || (__ldg(query_start) == 0 && __ldg(query_start + num_seqs) == num_query_tokens);
+        return !query_start || (*query_start == 0 && query_start[num_seqs] == num_query_tokens);
     }
     // A token's entry in its block table, and its offset in the block (a block
     // size is a power of two).
@@ -223,7 +223,7 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
     int cnt = 0, pieces = 0;
     while (w.ok && p.next()) {
         const int32_t *row = a.block_tables + (long long)p.seq * a.mbps;
-        auto id_of = [&](int tok) { return lane < L::TOK / 8 && tok < p.w.L ? __ldg(row + a.entry_of(tok)) : 0; };
+        auto id_of = [&](int tok) { return lane < L::TOK / 8 && tok < p.w.L ? row[a.entry_of(tok)] : 0; };
         const int32_t first_id = id_of(p.t0 * L::TOK + 8 * lane);   // on its way with the queries
         if (!w.warp(c.qempty, pieces + 1)) break;
         if (lane == 0) mbar_arrive_expect_tx(smem_u32(&c.qfull), LT_Q);
@@ -239,7 +239,7 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
             // lanes 8 .. 15: a group of the next tile, to be fetched into L2
             const int ntok = tok + L::TOK - 64;
             const bool ahead = lane >= 8 && lane < 16 && t + 1 < p.t1 && ntok < p.w.L;
-            const int32_t nblk = ahead ? __ldg(row + a.entry_of(ntok)) : -1;
+            const int32_t nblk = ahead ? row[a.entry_of(ntok)] : -1;
             const bool bad = __any_sync(0xffffffffu, mine && (blk < 0 || blk >= a.num_blocks));
             // (a group past the context is a box outside the cache, which reads as zeros)
             const unsigned boxes = __ballot_sync(0xffffffffu, lane < L::TOK / 8 && !bad);
@@ -293,7 +293,7 @@ __device__ void lt_load8(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &
         const int32_t *row = a.block_tables + (long long)p.seq * a.mbps;
         const int g0 = p.t0 * (L::TOK / 8), groups = (p.t1 - p.t0) * (L::TOK / 8);   // of the piece
         const int with = min(groups, p.w.L / 8 + (p.w.L % 8 != 0) - g0);               // those with tokens
-        auto ids = [&](int g) { return g + lane < with ? __ldg(row + a.entry_of(8 * (g0 + g + lane))) : 0; };
+        auto ids = [&](int g) { return g + lane < with ? row[a.entry_of(8 * (g0 + g + lane))] : 0; };
         // lane j's group of a batch: its rows in the cache, null if its id is out of range or it has no tokens
         auto rows_of = [&](int32_t id, int g) {
             const bool in = g < with && id >= 0 && id < a.num_blocks;

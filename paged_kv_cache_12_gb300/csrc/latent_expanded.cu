@@ -68,10 +68,10 @@ struct ExpandedArgs {
     };
     __device__ __forceinline__ Seq seq_work(int i) const {
         Seq w;
-        w.q0 = __ldg(query_start + i);
-        w.T = __ldg(query_start + i + 1) - w.q0;
-        w.k0 = __ldg(kv_start + i);
-        w.L = __ldg(kv_start + i + 1) - w.k0;
+        w.q0 = query_start[i];
+        w.T = query_start[i + 1] - w.q0;
+        w.k0 = kv_start[i];
+        w.L = kv_start[i + 1] - w.k0;
         w.valid = w.T <= w.L;
         w.per_head = w.valid ? (w.T + EX_ROWS - 1) / EX_ROWS : 0;
         w.rts = w.per_head * H;
@@ -120,11 +120,11 @@ struct ExpandedArgs {
         return tiles_of(w, min(w.T, r % w.per_head * EX_ROWS + EX_HALF));
     }
     __device__ __forceinline__ bool seq_ok(int i) const {
-        return __ldg(query_start + i) <= __ldg(query_start + i + 1) && __ldg(kv_start + i) <= __ldg(kv_start + i + 1);
+        return query_start[i] <= query_start[i + 1] && kv_start[i] <= kv_start[i + 1];
     }
     __device__ __forceinline__ bool ends_ok() const {
-        return __ldg(query_start) == 0 && __ldg(query_start + num_seqs) == num_query_tokens && __ldg(kv_start) == 0 &&
-               __ldg(kv_start + num_seqs) == num_kv_tokens;
+        return *query_start == 0 && query_start[num_seqs] == num_query_tokens && *kv_start == 0 &&
+               kv_start[num_seqs] == num_kv_tokens;
     }
 };
 
