@@ -5,8 +5,8 @@
 // Every row is moved in 16-byte vectors and every index read from the device
 // is range-checked before it is used as an address.  All three are bound by
 // HBM on large calls and by the launch on a decode step's few rows (one GB300:
-// 65,536 rows to E4M3 in 20.9 us with the call, 17.6 us and 5.35 TB/s of reads and
-// writes in the kernel; 100 rows in 7.4 us, nearly all of it the call).
+// 65,536 rows to E4M3 in 19.1 us, 5.85 TB/s of reads and writes; 100 rows in 7.4 us,
+// nearly all of it the call).
 //
 // Sources: the new token goes into the free slot of the sequence's current
 // block ("PagedAttention : comment optimiser la memoire GPU lors de
@@ -115,8 +115,9 @@ __global__ void __launch_bounds__(256) latent_write_fp8_kernel(const uint4 *late
 // and its slot through the block table (a slot below 0 marks a NaN row), then all
 // threads move vectors, a load per row on its way at once.  Small CTAs, because
 // each spends two thirds of its time on those dependent steps: 115,000 quantised
-// rows of a ragged batch take 37 us with 8 rows by 72 threads, 38 with 16 by 288,
-// 42 with 32 by 288 and 48 with 64 by 288; the bytes alone take 28.5.
+// rows of a ragged batch took 37 us with 8 rows by 72 threads, 38 with 16 by 288,
+// 42 with 32 by 288 and 48 with 64 by 288 (34 launched early); the bytes alone take
+// 28.5.
 constexpr int READ_ROWS = 8, READ_THREADS = VROW;
 constexpr int READ_STARTS = 1024;
 

@@ -18,15 +18,15 @@
 // stages (72 KB each; 54 KB of 48 tokens over a quantised cache, beside a staging
 // ring of 31 KB), P (8 KB).
 //
-// What bounds it (one GB300, 1.9 GHz): 16 heads, 100 x 8192 bf16 tokens: 160 us,
+// What bounds it (one GB300, 1.9 GHz): 16 heads, 100 x 8192 bf16 tokens: 156 us,
 // the kernel 153 at 6.2 TB/s of HBM reads, tensor pipe 62 % busy.  128 heads are
-// two row tiles a token, 96 contexts of 64 .. 32768 fp16 tokens: 193 us, a latency
+// two row tiles a token, 96 contexts of 64 .. 32768 fp16 tokens: 192 us, a latency
 // chain: a stage goes through load, S (36 products of 38 clocks), softmax and P C
 // (8 of 155) in 5500 clocks, and two stages are all that fits beside the queries;
 // halving both products takes 158.  Products of M 64 run at half the tensor
-// cores' rate.  E4M3, 16 heads x 4 new tokens, 100 contexts of 1024 .. 8192: 117 us,
-// 3800 clocks a tile in the converting warps (110 dependent instructions, waits and
-// votes a step of 16 tokens; ALU pipe 44 %, HBM 30 %).
+// cores' rate.  E4M3, 16 heads x 4 new tokens, 100 contexts of 1024 .. 8192: 110 us,
+// 3600 clocks a tile in the converting warps (110 dependent instructions, waits and
+// votes a step of 16 tokens; ALU pipe 44 %, HBM 30 %; halving both products: 109.8).
 #include <algorithm>
 #include <cmath>
 

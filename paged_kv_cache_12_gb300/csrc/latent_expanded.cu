@@ -20,12 +20,12 @@
 // on its S, the other half's products run.  The MMAs of one thread complete in
 // issue order, so when S_x(n) is complete so is PV_x(n - 1).
 //
-// What bounds it (one GB300): 2048 new of 12,000 tokens, 32 heads, bf16: 363 us,
-// 1268 TFLOP/s, tensor pipe 57 % busy.  The S products read their queries from
+// What bounds it (one GB300): 2048 new of 12,000 tokens, 32 heads, bf16: 358 us,
+// 1285 TFLOP/s, tensor pipe 58 % busy.  The S products read their queries from
 // shared memory (107 clocks for M 128, N 128, K 16; 64 from tensor memory, which S,
 // P and O of two halves fill), and the keys and values, read by eight row tiles a
-// head, come 3.8 times from HBM.  A 600-token prompt of 16 heads takes 28.7 us, a
-// chain of the loads, one to three KV tiles and the merge.
+// head, come 3.8 times from HBM.  A 600-token prompt of 16 heads takes 24 us, a
+// chain of the plan, the loads, one to three KV tiles, partial rows and the merge.
 
 #include <algorithm>
 #include <climits>

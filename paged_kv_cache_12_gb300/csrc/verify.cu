@@ -26,9 +26,9 @@
 // of a row scanned in 64 bits by one warp took 14,000 clocks, eight partial sums
 // compared in 64 bits by eight warps 4,000).
 //
-// One GB300: 100 sequences of 131,072 tokens in fp32, 27 us (3.5 TB/s of reads
+// One GB300: 100 sequences of 131,072 tokens in fp32, 27.5 us (3.5 TB/s of reads
 // between the dependent steps: drafts, slices, collection, the slice again, the
-// part); 4 sequences of 32,003 tokens, 9.3 us.
+// part); 4 sequences of 32,003 tokens, 9 us.
 
 #include <climits>
 

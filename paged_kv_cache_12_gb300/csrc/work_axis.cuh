@@ -117,7 +117,9 @@ __device__ __forceinline__ void make_plan(const P &a, Plan *plan, long long *war
         total += warp_sums[j];
     }
     const long long begin = before + upto - mine, end = before + upto;
-    const int parts = (int)min((long long)(gridDim.x / team), total > 0 ? max(1LL, quick_div(total, AXIS_MIN_UNITS)) : 0), cta = blockIdx.x, k = cta / team;
+    const int cta = blockIdx.x, k = cta / team;
+    const long long most = min(total, max(1LL, quick_div(total, AXIS_MIN_UNITS)));   // teams with work
+    const int parts = (int)min((long long)(gridDim.x / team), most);
     const long long u0 = k < parts ? range_begin(total, k, parts) : 0;
     const long long u1 = k < parts ? range_begin(total, k + 1, parts) : 0;
     if (threadIdx.x == 0) {
