@@ -16,8 +16,9 @@
 // the number of standing drafts (a warp, one draft a lane); the row's elements
 // are summed in slices, one a warp of the cluster; one warp collects the totals
 // through distributed shared memory and finds the slice in which the running sum
-// passes the drawn height; its CTA reads that slice again in eight parts, and a
-// warp the part that passes.
+// passes the drawn height.  A short slice is searched by the warp that summed it;
+// a long one is read again by the first CTA in eight parts, and the part that
+// passes by a warp.
 //
 // Sums: a draw is decided where a running sum over up to a hundred thousand
 // terms passes u * total, so sums are carried as an unevaluated pair of floats
@@ -264,7 +265,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
     __syncthreads();
     const int kept = s_kept, n = s_n, d0 = s_d0;
     int32_t *out = a.tokens + (long long)seq * (a.max_drafts + 1);
-    int next = -1;
+    if (rank == 0 && threadIdx.x == 0) s_next = -1;   // (others write it after the cluster's first meeting)
     if (kept >= 0) {   // the same in every CTA of the cluster
         const bool failed = kept < n;
         const T *p = static_cast<const T *>(a.target) + (long long)(d0 + seq + kept) * a.target_stride;
@@ -273,8 +274,9 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         constexpr int VSLICES = VCTAS * VWARPS;
         const int len = ((a.vocab + VSLICES - 1) / VSLICES + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
         for (int attempt = 0; attempt < 2; ++attempt) {
-            const long long lo = (long long)(rank * VWARPS + warp) * len;
-            const Sum2 mine = range_sum(w, (int)min((long long)a.vocab, lo), (int)min((long long)a.vocab, lo + len));
+            const long long from = (long long)(rank * VWARPS + warp) * len;
+            const int lo = (int)min((long long)a.vocab, from), hi = (int)min((long long)a.vocab, from + len);
+            const Sum2 mine = range_sum(w, lo, hi);
             if (lane == 0) totals[warp] = mine;
             cluster.sync();
             if (rank == 0 && warp == 0) {   // lane l: slices 2 l and 2 l + 1
@@ -315,12 +317,18 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
                 if (lane == 0) s_slice = slice;
             }
             cluster.sync();   // rank 0 has read every CTA's totals and decided
-            const bool again = *cluster.map_shared_rank(&s_slice, 0) == -2;
-            if (rank == 0 && s_slice >= 0) {   // the slice again, in parts
-                const int from = s_slice * len, part = (len / VCHUNK + VWARPS - 1) / VWARPS * VCHUNK;
-                const int lo = min(a.vocab, min(from + len, from + warp * part));
-                const int hi = min(a.vocab, min(from + len, lo + part));
-                const Sum2 mine = range_sum(w, lo, hi);
+            const int slice = *cluster.map_shared_rank(&s_slice, 0);
+            if (len <= VBATCH * VCHUNK) {   // short slices: the warp that summed it finds the element
+                if (slice == rank * VWARPS + warp) {
+                    const int v = find_in_range(w, lo, hi, *cluster.map_shared_rank(&s_before, 0),
+                                                *cluster.map_shared_rank(&s_height, 0));
+                    if (lane == 0) *cluster.map_shared_rank(&s_next, 0) = v;
+                }
+            } else if (rank == 0 && slice >= 0) {   // the slice again, in parts
+                const int first = slice * len, part = (len / VCHUNK + VWARPS - 1) / VWARPS * VCHUNK;
+                const int plo = min(a.vocab, min(first + len, first + warp * part));
+                const int phi = min(a.vocab, min(first + len, plo + part));
+                const Sum2 mine = range_sum(w, plo, phi);
                 if (lane == 0) totals[warp] = mine;
                 __syncthreads();
                 Sum2 run = s_before, before = run;
@@ -338,21 +346,19 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
                     run = after;
                 }
                 if (warp == at) {
-                    const int v = find_in_range(w, lo, hi, before, s_height);
+                    const int v = find_in_range(w, plo, phi, before, s_height);
                     if (lane == 0) s_next = v;
                 }
-                __syncthreads();
-                next = s_next;
             }
-            if (!again) break;
+            if (slice != -2) break;
             w = Weights<T>(p, nullptr, -1);
             cluster.sync();   // every CTA has read the decision
         }
-        cluster.sync();   // rank 0's shared memory outlives its readers
+        cluster.sync();   // the token is there, and rank 0's shared memory outlives its readers
     }
     if (rank == 0 && warp == 0) {
         for (int j = lane; j <= a.max_drafts; j += 32)
-            out[j] = kept < 0 ? -1 : j < kept ? a.draft_tokens[d0 + j] : j == kept ? next : -1;
+            out[j] = kept < 0 ? -1 : j < kept ? a.draft_tokens[d0 + j] : j == kept ? s_next : -1;
         if (lane == 0) a.accepted[seq] = kept;
     }
 }
