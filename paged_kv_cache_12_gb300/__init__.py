@@ -451,47 +451,61 @@ def pa_workspace_status(workspace, stream=None) -> int:
 
 # ---------------------------------------------------------------- latent cache
 
-def _need_on(where, dev, t, name, dtype, ndim, dense=True):
+def _refuse(where, dev, t, name, dtype, ndim, how):
+    raise ValueError(f"{where}: {name}: expected a {ndim}-d {dtype} tensor on CUDA device {dev}, {how}; got {t.dim()}-d "
+                     f"{t.dtype} on {t.device}, strides {t.stride()}")
+
+
+def _need_on(where, dev, t, name, dtype, ndim):
     """Check one tensor: on CUDA device `dev` (an index), of the type and number
-    of dimensions, contiguous (with dense=False: unit stride in the last
-    dimension).  Decode steps make these calls per layer, so the test is one
-    expression and the message is made only when it fails."""
+    of dimensions, contiguous.  Decode steps make these calls per layer and each
+    question to a tensor takes 50 to 200 ns, so they are asked once and the message
+    is made only when it fails."""
+    if t.get_device() != dev or dev < 0 or t.dtype is not dtype or t.dim() != ndim or not t.is_contiguous():
+        _refuse(where, dev, t, name, dtype, ndim, "contiguous")
+
+
+def _need_rows(where, dev, t, name, dtype, ndim):
+    """The same for a tensor that needs unit stride in its last dimension only;
+    gives its strides."""
+    st = t.stride()
     if t.get_device() != dev or dev < 0 or t.dtype is not dtype or t.dim() != ndim or \
-            not (t.is_contiguous() if dense else t.stride(-1) == 1 or t.shape[-1] <= 1 or t.numel() == 0):
-        raise ValueError(f"{where}: {name}: expected a {ndim}-d {dtype} tensor on CUDA device {dev}, contiguous"
-                         f"{'' if dense else ' in its last dimension'}; got {t.dim()}-d {t.dtype} on {t.device}, strides "
-                         f"{t.stride()}")
+            (st[-1] != 1 and t.shape[-1] > 1 and t.numel() > 0):
+        _refuse(where, dev, t, name, dtype, ndim, "contiguous in its last dimension")
+    return st
 
 
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _run(where, dev, stream, *args):
     """Call the library on device `dev` (an index) and the given stream (default:
     that device's current torch stream)."""
-    global _raw_stream
-    import torch
+    global _raw_stream, _current_device
+    if _raw_stream is None:
+        import torch
+        # the handle alone, without a Stream object around it, where torch offers it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     if stream is None:
-        if _raw_stream is None:   # the handle alone, without a Stream object around it, where torch offers it
-            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-                (lambda d: torch.cuda.current_stream(d).cuda_stream)
         h = _raw_stream(dev)
     else:
         h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     f = getattr(_lib or lib(), where)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         rc = f(*args, h)
     else:
+        import torch
         with torch.cuda.device(dev):
             rc = f(*args, h)
     if rc != PA_OK:
         raise PAError(rc, where)
 
 
-def _latent_cache(where, cache):
+def _latent_cache(torch, where, cache):
     """(PA_KV_*, torch dtype of the rows that go in and come out, device index,
     blocks, block size) of a latent cache tensor."""
-    import torch
     dt = cache.dtype
     if cache.dim() == 3 and cache.is_contiguous() and cache.is_cuda:
         nb, bs, w = cache.shape
@@ -510,15 +524,15 @@ def pa_latent_write(latent, rope, slot_mapping, cache, stream=None):
     wider rows (unit stride in the last dimension)."""
     import torch
     where = "pa_latent_write"
-    kv, dt, dev, nb, bs = _latent_cache(where, cache)
-    _need_on(where, dev, latent, "latent", dt, 2, False)
-    _need_on(where, dev, rope, "rope", dt, 2, False)
+    kv, dt, dev, nb, bs = _latent_cache(torch, where, cache)
+    sl = _need_rows(where, dev, latent, "latent", dt, 2)[0]
+    sr = _need_rows(where, dev, rope, "rope", dt, 2)[0]
     _need_on(where, dev, slot_mapping, "slot_mapping", torch.int64, 1)
-    n = latent.shape[0]
-    if latent.shape[1] != PA_LATENT_DIM or rope.shape != (n, PA_LATENT_ROPE_DIM) or slot_mapping.shape[0] != n:
+    n, w = latent.shape
+    if w != PA_LATENT_DIM or rope.shape != (n, PA_LATENT_ROPE_DIM) or slot_mapping.shape[0] != n:
         raise ValueError("pa_latent_write: shape mismatch")
-    # one row (or none) has no stride of its own
-    sl, sr = (latent.stride(0), rope.stride(0)) if n > 1 else (PA_LATENT_DIM, PA_LATENT_ROPE_DIM)
+    if n <= 1:   # one row (or none) has no stride of its own
+        sl, sr = PA_LATENT_DIM, PA_LATENT_ROPE_DIM
     _run(where, dev, stream, latent.data_ptr(), rope.data_ptr(), slot_mapping.data_ptr(), cache.data_ptr(), n, sl, sr,
          bs, nb, kv)
 
@@ -527,7 +541,7 @@ def pa_latent_block_copy(cache, pairs, stream=None):
     """Copy every (src, dst) block pair of int64 ``pairs`` [n, 2] of a latent cache."""
     import torch
     where = "pa_latent_block_copy"
-    kv, _, dev, nb, bs = _latent_cache(where, cache)
+    kv, _, dev, nb, bs = _latent_cache(torch, where, cache)
     _need_on(where, dev, pairs, "pairs", torch.int64, 2)
     if pairs.shape[1] != 2:
         raise ValueError("pa_latent_block_copy: shape mismatch")
@@ -540,8 +554,8 @@ def pa_latent_read(out, cache, block_tables, row_start, first_token=None, stream
     sequence i; rows from row_start[-1] on are left as they are."""
     import torch
     where, i32 = "pa_latent_read", torch.int32
-    kv, dt, dev, nb, bs = _latent_cache(where, cache)
-    _need_on(where, dev, out, "out", dt, 2, False)
+    kv, dt, dev, nb, bs = _latent_cache(torch, where, cache)
+    so = _need_rows(where, dev, out, "out", dt, 2)[0]
     _need_on(where, dev, block_tables, "block_tables", i32, 2)
     _need_on(where, dev, row_start, "row_start", i32, 1)
     if first_token is not None:
@@ -551,7 +565,7 @@ def pa_latent_read(out, cache, block_tables, row_start, first_token=None, stream
     if w != PA_LATENT_ROW or row_start.shape[0] != b + 1 or (first_token is not None and first_token.shape[0] != b):
         raise ValueError("pa_latent_read: shape mismatch")
     _run(where, dev, stream, out.data_ptr(), cache.data_ptr(), block_tables.data_ptr(), row_start.data_ptr(),
-         None if first_token is None else first_token.data_ptr(), b, n, out.stride(0) if n > 1 else PA_LATENT_ROW, bs,
+         None if first_token is None else first_token.data_ptr(), b, n, so if n > 1 else PA_LATENT_ROW, bs,
          nb, mb, kv)
 
 
@@ -572,7 +586,7 @@ def pa_latent_attention(out, query, cache, block_tables, context_lens, scale, ma
     query_start[i + 1] - 1 are sequence i's last new tokens, causal."""
     import torch
     where, i32 = "pa_latent_attention", torch.int32
-    kv, dt, dev, nb, bs = _latent_cache(where, cache)
+    kv, dt, dev, nb, bs = _latent_cache(torch, where, cache)
     _need_on(where, dev, out, "out", dt, 3)
     _need_on(where, dev, query, "query", dt, 3)
     _need_on(where, dev, block_tables, "block_tables", i32, 2)
@@ -611,9 +625,9 @@ def pa_latent_attention_expanded(out, query, k_nope, k_rope, value, query_start,
         raise ValueError(f"{where}: query must be float16 or bfloat16")
     _need_on(where, dev, query, "query", dt, 3)
     _need_on(where, dev, out, "out", dt, 3)
-    _need_on(where, dev, k_nope, "k_nope", dt, 3, False)
-    _need_on(where, dev, value, "value", dt, 3, False)
-    _need_on(where, dev, k_rope, "k_rope", dt, 2, False)
+    ks = _need_rows(where, dev, k_nope, "k_nope", dt, 3)
+    vs = _need_rows(where, dev, value, "value", dt, 3)
+    rs = _need_rows(where, dev, k_rope, "k_rope", dt, 2)
     _need_on(where, dev, query_start, "query_start", i32, 1)
     _need_on(where, dev, kv_start, "kv_start", i32, 1)
     _need_on(where, dev, workspace, "workspace", torch.uint8, 1)
@@ -623,14 +637,12 @@ def pa_latent_attention_expanded(out, query, k_nope, k_rope, value, query_start,
             k_rope.shape != (nk, 64) or query_start.shape != kv_start.shape or query_start.shape[0] < 1:
         raise ValueError(f"{where}: shape mismatch")
 
-    def strides(t):   # a dimension of size one has no stride of its own
-        head = t.stride(1) if h > 1 else 128
-        return (t.stride(0) if nk > 1 else h * head), head
-    kt, kh = strides(k_nope)
-    vt, vh = strides(value)
+    # a dimension of size one has no stride of its own
+    kh, vh = (ks[1], vs[1]) if h > 1 else (128, 128)
+    kt, vt = (ks[0], vs[0]) if nk > 1 else (h * kh, h * vh)
     _run(where, dev, stream, out.data_ptr(), query.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), value.data_ptr(),
          query_start.data_ptr(), kv_start.data_ptr(), query_start.shape[0] - 1, nq, nk, h, kt, kh,
-         k_rope.stride(0) if nk > 1 else 64, vt, vh, float(scale), PA_KV_F16 if dt is torch.float16 else PA_KV_BF16,
+         rs[0] if nk > 1 else 64, vt, vh, float(scale), PA_KV_F16 if dt is torch.float16 else PA_KV_BF16,
          workspace.data_ptr(), workspace.shape[0])
 
 
@@ -651,26 +663,26 @@ def pa_verify_drafts(accepted, tokens, target_probs, draft_probs, draft_tokens, 
         PA_PROBS_BF16 if dt is torch.bfloat16 else -1
     if kind < 0:
         raise ValueError(f"{where}: target_probs must be float32, float16 or bfloat16")
-    _need_on(where, dev, target_probs, "target_probs", dt, 2, False)
+    st = _need_rows(where, dev, target_probs, "target_probs", dt, 2)[0]
     _need_on(where, dev, accepted, "accepted", i32, 1)
     _need_on(where, dev, tokens, "tokens", i32, 2)
     _need_on(where, dev, draft_tokens, "draft_tokens", i32, 1)
     _need_on(where, dev, draft_start, "draft_start", i32, 1)
     _need_on(where, dev, uniform, "uniform", f32, 1)
     _need_on(where, dev, sample_uniform, "sample_uniform", f32, 1)
-    if draft_probs is not None:
-        _need_on(where, dev, draft_probs, "draft_probs", dt, 2, False)
+    sd = 0 if draft_probs is None else _need_rows(where, dev, draft_probs, "draft_probs", dt, 2)[0]
     b, nd = accepted.shape[0], draft_tokens.shape[0]
     rows, v = target_probs.shape
-    most = tokens.shape[1] - 1
-    if rows != nd + b or tokens.shape[0] != b or most < 0 or uniform.shape[0] != nd or \
+    bt, most = tokens.shape
+    most -= 1
+    if rows != nd + b or bt != b or most < 0 or uniform.shape[0] != nd or \
             draft_start.shape[0] != b + 1 or sample_uniform.shape[0] != b or \
             (draft_probs is not None and draft_probs.shape != (nd, v)):
         raise ValueError(f"{where}: shape mismatch")
     _run(where, dev, stream, accepted.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(),
          None if draft_probs is None else draft_probs.data_ptr(), draft_tokens.data_ptr(), draft_start.data_ptr(),
-         uniform.data_ptr(), sample_uniform.data_ptr(), b, nd, most, v, target_probs.stride(0) if rows > 1 else v,
-         draft_probs.stride(0) if draft_probs is not None and nd > 1 else v, kind)
+         uniform.data_ptr(), sample_uniform.data_ptr(), b, nd, most, v, st if rows > 1 else v,
+         sd if draft_probs is not None and nd > 1 else v, kind)
 
 
 # ---------------------------------------------------------------- allocator
