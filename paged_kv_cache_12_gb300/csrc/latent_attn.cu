@@ -342,7 +342,8 @@ __device__ void lt_load8(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &
 // four new tokens of 100 sequences, 123 us here): sixteen warps of a row each, 141;
 // twelve of four rows of one step, 152; rows loaded from global memory into
 // registers instead of staged, 130 (the loads in flight held up the stores behind
-// them).
+// them); and, against 110 later, two sets of eight warps that take turns, 115, the
+// next step's loads before a step's stores, 114.
 template <int KV>
 __device__ void lt_convert(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a, Walk<typename Lt<KV>::Args> &p) {
     using L = Lt<KV>;
