@@ -20,8 +20,8 @@
 // on its S, the other half's products run.  The MMAs of one thread complete in
 // issue order, so when S_x(n) is complete so is PV_x(n - 1).
 //
-// What bounds it (one GB300): 2048 new of 12,000 tokens, 32 heads, bf16: 358 us,
-// 1285 TFLOP/s, tensor pipe 58 % busy.  The S products read their queries from
+// What bounds it (one GB300): 2048 new of 12,000 tokens, 32 heads, bf16: 360 us,
+// 1278 TFLOP/s, tensor pipe 58 % busy.  The S products read their queries from
 // shared memory (107 clocks for M 128, N 128, K 16; 64 from tensor memory, which S,
 // P and O of two halves fill), and the keys and values, read by eight row tiles a
 // head, come 3.8 times from HBM.  A 600-token prompt of 16 heads takes 24 us, a
@@ -357,6 +357,8 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
         float mrun = -INFINITY, l = 0.f;
         for (int n = 0; n < h.n && ok; ++n) {
             if (!wait(&c.sfull[x], (uint32_t)(sc & 1))) break;
+            // (done when S is; every phase is seen, so that the one waited for last is not taken for another)
+            if (n > 0 && !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1))) break;
             tc_fence_after_sync();
             float s[EX_TOK];
 #pragma unroll
