@@ -391,7 +391,7 @@ __device__ void lt_convert(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
                             x[i][0] = x[i][1] = x[i][2] = x[i][3] = make_uint2(0, 0);
                     }
                 }
-                if (lane == 0) mbar_arrive(smem_u32(&c.empty8[s]));   // (after the vote: every lane has its codes)
+                arrive_warp(c.empty8[s]);   // after every lane's loads (the vote orders no memory)
                 if (!w.warp(c.kvempty[st][k], (cnt >> 1) + 1)) break;
                 uint8_t *dst = stage + 2 * k * LT_GROUP;
 #pragma unroll
