@@ -245,10 +245,12 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
             const unsigned boxes = __ballot_sync(0xffffffffu, lane < L::TOK / 8 && !bad);
             const int from = mine ? (blk << a.bs_log2) + a.offset_of(tok) : -8;
             if (bad && lane == 0) *reinterpret_cast<volatile int *>(&c.bad[p.local % LT_BAD_SLOTS]) = p.local + 1;
+            int sent = 0;   // parts
 #pragma unroll
             for (int part = 0; part < L::PARTS; ++part) {
                 constexpr int N = L::PART_TOK / 8;   // groups of a part
                 if (!w.warp(c.kvempty[st][part], (cnt >> 1) + 1)) break;
+                ++sent;
                 if (lane == 0)
                     mbar_arrive_expect_tx(smem_u32(&c.kvfull[st]),
                                           (uint32_t)(__popc(boxes >> (part * N) & ((1u << N) - 1)) * LT_GROUP));
@@ -257,8 +259,14 @@ __device__ void lt_load(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args &a
                     tma_load_3d(base + L::OFF_KV + st * L::STAGE + lane * LT_GROUP, &maps.kv, 0, from, 0,
                                 smem_u32(&c.kvfull[st]), first);
             }
-            if (!w.ok) {   // a part may be on its way: the stage counts as sent below
-                ++cnt;
+            if (!w.ok) {
+                // parts on their way count as a use of the stage below: the others arrive
+                // without copies, so that its phase ends when these have landed
+                if (sent) {
+                    if (lane == 0)
+                        for (int part = sent; part < L::PARTS; ++part) mbar_arrive(smem_u32(&c.kvfull[st]));
+                    ++cnt;
+                }
                 break;
             }
             if (nblk >= 0 && nblk < a.num_blocks)
