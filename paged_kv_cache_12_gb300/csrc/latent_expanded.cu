@@ -169,7 +169,6 @@ constexpr int EX_REGS_HIGH = 200;                    // the softmax warpgroups
 static_assert(128 * EX_REGS_LOW + 256 * EX_REGS_HIGH <= EX_THREADS * EX_REGS_LAUNCH,
               "register split within the launch's pool");
 
-constexpr int EX_POISON = 16;   // pieces that one half may be ahead of the other
 constexpr uint32_t EX_LAST = 0x7fffffffu;
 
 struct ExCtrl {
@@ -178,9 +177,13 @@ struct ExCtrl {
     int abort;
     Plan plan;
     long long warp_sums[EX_THREADS / 32];
-    // by a piece's number: 1 + that number in the high word, and in the low one
-    // how far below the largest position its first non-finite value of a new token is
-    unsigned long long poison[EX_POISON];
+    // For each half, by the number of a piece among those that it takes: 1 + that
+    // number in the high word, and in the low one how far below the largest position
+    // the piece's first non-finite value of a new token is.  Half 0 writes both
+    // halves' records before it hands over a P.  Two of each are enough: half 0 has
+    // the first S of the half's piece k + 2 only after the MMA thread has had every P
+    // of that half's piece k + 1, and so after all its warps have read piece k's.
+    unsigned long long poison[2][2];
 };
 static_assert(sizeof(ExCtrl) <= EX_CTRL, "control block");
 
@@ -342,6 +345,7 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
         return ok;
     };
     int sc = 0, cnt = 0;   // S_x and P_x so far; ring blocks before this piece
+    int both = -1;         // number of the last piece that both halves take
     while (ok && p.next()) {
         const Half h = half_of(a, p, x);
         const int blocks = 5 * (p.t1 - p.t0);
@@ -349,6 +353,8 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
             cnt += blocks;
             continue;
         }
+        const bool shared = x == 1 || half_of(a, p, 1).n > 0;
+        if (shared) ++both;
         const int tok = h.row0 + m;
         const bool mine = tok < p.w.T;
         const int vis = mine ? p.w.L - p.w.T + tok + 1 : p.w.L;   // positions this row sees
@@ -442,8 +448,11 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
                     }
                 }
                 if (!ok) break;
-                if (bad != INT_MAX)
-                    atomicMax(&c.poison[p.local % EX_POISON], (unsigned long long)(p.local + 1) << 32 | (EX_LAST - (uint32_t)bad));
+                if (bad != INT_MAX) {
+                    const uint32_t below = EX_LAST - (uint32_t)bad;
+                    atomicMax(&c.poison[0][p.local & 1], (unsigned long long)(p.local + 1) << 32 | below);
+                    if (shared) atomicMax(&c.poison[1][both & 1], (unsigned long long)(both + 1) << 32 | below);
+                }
                 changed = true;
             }
             const float mu = mrun == -INFINITY ? 0.f : mrun;   // a row that has seen nothing yet
@@ -478,8 +487,9 @@ __device__ void ex_softmax(uint8_t *smem, ExCtrl &c, const ExpandedArgs &a, Walk
         if (!ok || !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1))) break;
         tc_fence_after_sync();
         // ---- the piece's rows: finished, or a partial row
-        const unsigned long long poison = *reinterpret_cast<volatile unsigned long long *>(&c.poison[p.local % EX_POISON]);
-        if ((int)(poison >> 32) == p.local + 1 && vis > (int)(EX_LAST - (uint32_t)poison)) l = __int_as_float(0x7fc00000);
+        const int piece = x == 0 ? p.local : both;   // (half 0 takes every piece)
+        const unsigned long long poison = *reinterpret_cast<volatile unsigned long long *>(&c.poison[x][piece & 1]);
+        if ((int)(poison >> 32) == piece + 1 && vis > (int)(EX_LAST - (uint32_t)poison)) l = __int_as_float(0x7fc00000);
         const bool whole = p.t0 == 0 && p.t1 >= h.ntiles;
         const int slot_row = p.slot() * EX_ROWS + h.row0 % EX_ROWS + m;
         if (!whole && mine) a.ml[slot_row] = make_float2(mrun, l);
@@ -542,8 +552,8 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         tma_prefetch_map(&tmk);
         tma_prefetch_map(&tmr);
         tma_prefetch_map(&tmv);
-    } else if (threadIdx.x >= 32 && threadIdx.x < 32 + EX_POISON) {
-        c.poison[threadIdx.x - 32] = 0;
+    } else if (threadIdx.x >= 32 && threadIdx.x < 36) {
+        c.poison[(threadIdx.x >> 1) & 1][threadIdx.x & 1] = 0;
     }
     grid_wait();
     if (warp == 2) {   // (not before: an earlier kernel may still need its own)

@@ -12,7 +12,7 @@ import torch
 
 import latent_ref as R
 import paged_kv_cache_12_gb300 as pa
-from test_gpu_latent import absorbed, compare_absorbed, same_bits
+from test_gpu_latent import absorbed, compare_absorbed, i32, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -40,6 +40,66 @@ def test_rotary_elements_of_quantised_rows():
     compare_absorbed(w, q, want, None)
     for _ in range(20):
         assert same_bits(absorbed(w, 16, None, 0, query=q)[1], want)
+
+
+# ------------------------------------------------------------------ expanded attention
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16], ids=["f16", "bf16"])
+def test_expanded_many_short_sequences(dt):
+    # some forty short pieces a CTA, of one or both halves of a row tile, with
+    # values of new tokens that are not finite in a third of the sequences: each
+    # row that sees one is not finite in that element, and every other row is as
+    # the definition says.  (A record of them is kept for two pieces of a half.)
+    # More sequences than the CTA has threads, some of them empty
+    heads, b = 2, 3001
+    g = torch.Generator().manual_seed(31)
+    kinds = torch.randint(5, (b,), generator=g).tolist()
+    news = [(0, 1, 5 + i % 120, 129 + i % 60, 3 + i % 20)[k] for i, k in enumerate(kinds)]
+    pasts = [(0, 2 + i % 9, 0, i % 140, 40 + i % 130)[k] for i, k in enumerate(kinds)]
+    lens = [a + p for a, p in zip(news, pasts)]
+    qs, ks = [0], [0]
+    for a, n in zip(news, lens):
+        qs.append(qs[-1] + a)
+        ks.append(ks[-1] + n)
+    q = torch.randn(qs[-1], heads, 192, generator=g).to(dt)
+    up = torch.randn(ks[-1], heads, 256, generator=g).to(dt)
+    r = torch.randn(ks[-1], 64, generator=g).to(dt)
+    hit = {}
+    for i in range(0, b, 3):
+        if news[i]:
+            j, h = int(torch.randint(news[i], (1,), generator=g)), i // 3 % heads
+            hit[i] = (j, h)
+            up[ks[i] + pasts[i] + j, h, 128 + 9] = (math.nan, math.inf)[i // 6 % 2]
+    q, up, r = q.to(DEV), up.to(DEV), r.to(DEV)
+    k, v = up[..., :128], up[..., 128:]
+    ws = torch.full((pa.pa_latent_attention_expanded_workspace_size(b, qs[-1], heads),), 255, dtype=torch.uint8, device=DEV)
+    out = torch.zeros(qs[-1], heads, 128, dtype=dt, device=DEV)
+    pa.pa_latent_attention_expanded(out, q, k, r, v, i32(qs), i32(ks), SCALE, ws)
+    assert pa.pa_workspace_status(ws) == pa.PA_OK
+    for i in range(b):
+        n, L = news[i], lens[i]
+        for h in range(heads if n else 0):
+            bad = hit[i][0] if i in hit and hit[i][1] == h else n
+            got = out[qs[i]:qs[i + 1], h]
+            assert not torch.isfinite(got[bad:, 9]).any(), (i, h)
+            s, e = ks[i], ks[i] + pasts[i] + bad
+            key = torch.cat([k[s:e, h], r[s:e]], 1).double()
+            o, tol = attend_causal(q[qs[i]:qs[i] + bad, h].double(), key, v[s:e, h].double(), SCALE, dt)
+            R.check(got[:bad], o, tol, f"sequence {i}, head {h}") if bad else None
+
+
+def attend_causal(q, k, v, scale, dt):
+    """R.attend for rows q of which row j sees len(k) - len(q) + j + 1 positions
+    (its tolerance with the largest of their score errors and counts)."""
+    n, past = k.shape[0], k.shape[0] - q.shape[0]
+    hide = torch.ones(q.shape[0], n, dtype=torch.bool, device=k.device).triu(past + 1)
+    p = torch.softmax((q @ k.T * scale).masked_fill(hide, -math.inf), 1)
+    o, u = p @ v, R.half_step(dt)
+    d = (q.abs() @ k.abs().T).amax(1, keepdim=True) * scale * q.shape[1] * 2.0 ** -24 if n else 0.0
+    tol = (u + 2 * d + n * 2.0 ** -24 + 2.0 ** -20) * (p @ v.abs()) + u * o.abs()
+    if dt == torch.float16 and n:
+        tol = tol + n * 2.0 ** -25 * v.abs().amax(0) + 2.0 ** -25
+    return o, tol
 
 
 # ------------------------------------------------------------------ waits that run out
