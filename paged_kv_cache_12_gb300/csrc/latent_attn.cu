@@ -572,6 +572,7 @@ __device__ void lt_softmax(uint8_t *smem, LtCtrl &c, const typename Lt<KV>::Args
             // already are), and so is what is not finite among the new tokens' (the
             // rows that see it become NaN below).
             if (first_vis - t0 < L::TOK) {
+                if (!w.warp(c.kvfull[st], n >> 1)) break;   // (long past: it makes the rows this warp's to read)
                 uint8_t *kv = smem + L::OFF_KV + st * L::STAGE;
                 const int left = min(L::TOK, p.w.L - t0), end = L::F8 ? left : (left + 7) & ~7;
                 for (int k = tid + max(0, first_vis - t0) * 64; k < end * 64; k += 128) {
