@@ -90,6 +90,7 @@ struct Sum2 {
         const float h = __fmul_rn(u, hi);
         return Sum2{h, __fmaf_rn(u, lo, __fmaf_rn(u, hi, -h))};
     }
+    __device__ __forceinline__ Sum2 scaled(float f) const { return Sum2{hi * f, lo * f}; }   // f a power of two
     __device__ __forceinline__ bool any() const { return hi > 0.f; }   // sums of weights >= 0
 };
 
@@ -177,11 +178,25 @@ __device__ __forceinline__ Sum2 range_sum(const Weights<T> &w, int lo, int hi) {
     return warp_sum(acc);
 }
 
+// The height u * total that a running sum has to pass.  Sums are compared with it
+// at `up` times their value: a small total's are raised, because a float's steps end
+// at 2^-149 and the low part of u * total would be lost there.
+struct Height {
+    Sum2 at;
+    float up = 1.f;
+    Height() = default;
+    __device__ __forceinline__ Height(const Sum2 &total, float u) {
+        up = total.hi < 0x1p-60f ? 0x1p60f : 1.f;
+        at = total.scaled(up).times(u);
+    }
+    __device__ __forceinline__ bool passed_by(const Sum2 &run) const { return run.scaled(up).over(at); }
+};
+
 // The smallest v in [lo, hi) of positive weight whose running sum, from
 // `before` on, passes `height`; where rounding lets none pass, the last of
 // positive weight.  One warp, in element order: four consecutive elements a lane.
 template <typename T>
-__device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, Sum2 height) {
+__device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, const Height height) {
     const int lane = threadIdx.x & 31;
     int last = -1;
     for (int base = lo; base < hi; base += VCHUNK) {
@@ -202,7 +217,7 @@ __device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, S
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             run.add(s[k], e[k]);
-            if (v == INT_MAX && s[k] > 0.f && run.over(height)) v = base + 4 * lane + k;
+            if (v == INT_MAX && s[k] > 0.f && height.passed_by(run)) v = base + 4 * lane + k;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
@@ -222,7 +237,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ Sum2 totals[VWARPS];   // this CTA's slices; then, in rank 0, the parts of one
     __shared__ Sum2 s_before;         // rank 0: the sum before the slice that passes
-    __shared__ Sum2 s_height;
+    __shared__ Height s_height;
     __shared__ int s_slice;           // rank 0: that slice; -1: no token; -2: draw from p itself
     __shared__ int s_next;
     __shared__ int s_kept, s_n, s_d0;
@@ -294,14 +309,14 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
                 const float total = all.value();   // the same in all lanes
                 int slice = attempt == 0 && failed && total == 0.f ? -2 : -1;
                 if (total > 0.f && isfinite(total)) {
-                    const Sum2 height = all.times(a.sample[seq]);
+                    const Height height(all, a.sample[seq]);
                     Sum2 run = upto;   // before the lane's slices
                     run.add(-both.hi, -both.lo);
                     Sum2 run1 = run;
                     run1.add(x0);
                     // the first slice whose running sum passes, else the last of any weight
-                    const int g = x0.any() && run1.over(height)  ? 2 * lane
-                                  : x1.any() && upto.over(height) ? 2 * lane + 1
+                    const int g = x0.any() && height.passed_by(run1)  ? 2 * lane
+                                  : x1.any() && height.passed_by(upto) ? 2 * lane + 1
                                                                       : INT_MAX;
                     int first = g, last = x1.any() ? 2 * lane + 1 : x0.any() ? 2 * lane : -1;
 #pragma unroll
@@ -342,7 +357,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
                     if (!passed && x.any()) {
                         at = k;
                         before = run;
-                        passed = after.over(s_height);
+                        passed = s_height.passed_by(after);
                     }
                     run = after;
                 }

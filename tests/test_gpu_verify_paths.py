@@ -29,3 +29,15 @@ def test_long_slices_in_small_clusters(kind, n, vocab):
         u[r] = 0.999
     pick[covered[0]], pick[covered[1]] = 0.0, below
     compare((t, q, d, start, u, pick), max(counts))
+
+
+@pytest.mark.parametrize("n,vocab", [(200, 37), (4, 32003), (100, 32003), (400, 9001)])
+def test_weights_next_to_the_smallest_float(n, vocab):
+    # rows need not sum to one: weights of a few times 2^-149 each, where a height
+    # u * total rounded to a float's steps passes other sums than it should
+    g = np.random.default_rng(n + vocab)
+    rows = g.integers(0, 4, size=(n, vocab)).astype(np.float64) * 2.0 ** -149
+    target = torch.tensor(rows.astype(np.float32), device="cuda")
+    assert (target.double().cpu().numpy() == rows).all()
+    pick = g.random(n).astype(np.float32)
+    compare((target, target[:0], [], [0] * (n + 1), np.zeros(0, dtype=np.float32), pick), 0)
