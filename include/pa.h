@@ -434,8 +434,8 @@ PA_API int pa_latent_read(uint16_t *out, const void *cache, const int32_t *block
                           const int32_t *first_token, int num_seqs, int num_rows, int64_t out_stride,
                           int block_size, int64_t num_blocks, int max_blocks_per_seq, int kv_dtype, void *stream);
 
-/* Workspace bytes pa_latent_attention needs (a host-side bound; 0 for invalid
- * sizes). */
+/* Workspace bytes pa_latent_attention needs (0 for invalid sizes): 42 MB,
+ * whatever the call's sizes. */
 PA_API size_t pa_latent_attention_workspace_size(int num_seqs, int num_query_tokens, int num_heads,
                                                  int max_context_len);
 
@@ -469,8 +469,8 @@ PA_API int pa_latent_attention(void *out, const void *query, const void *cache, 
                                int max_blocks_per_seq, int max_context_len, float scale, int kv_dtype,
                                void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace bytes pa_latent_attention_expanded needs (a host-side bound; 0
- * for invalid sizes). */
+/* Workspace bytes pa_latent_attention_expanded needs (0 for invalid sizes):
+ * 42 MB, whatever the call's sizes. */
 PA_API size_t pa_latent_attention_expanded_workspace_size(int num_seqs, int num_query_tokens, int num_heads);
 
 /* Attention in the expanded form, for prompts: every head's keys and values

@@ -27,8 +27,8 @@ inline int latent_row_bytes(int kv) {
 // the low end of a bf16's, are the value times 2^-120 (a subnormal code becomes a
 // subnormal bf16), and a product with 2^120 times the scale is exact.
 // Conversion instructions (E4M3 to fp16 to float to bf16) take three times as
-// long.  Two cases need the long way: NaN codes, and scales above 2^7, where
-// 2^120 times the scale is no bf16; latent_codes_special finds them.
+// long.  Two cases need the long way: NaN codes (latent_codes_nan finds them), and
+// scales above 2^7, where 2^120 times the scale is no bf16 (latent_scale_special).
 __device__ __forceinline__ uint32_t bf162_mul(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

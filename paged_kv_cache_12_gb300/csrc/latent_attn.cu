@@ -7,6 +7,13 @@
 // probabilities, rounded to the 16-bit type for the second product, below 2^8),
 // and pieces of a context joined by M = max m, sum of 2^(m - M) (l, o).
 //
+// Why the probabilities are rounded: the tensor cores take both operands of P C in
+// one type, and C lies in shared memory in the cache's.  The sum l takes them
+// unrounded.  Half a step of each probability, at random, comes to about what
+// rounding the output does: against 64 bits the whole is off by 0.0019 to 0.0021
+// normwise in bf16 and 0.00026 in fp16, where 32-bit arithmetic rounded once at the
+// end is off by 0.0016 to 0.0017 and 0.00021.
+//
 // A row tile is 64 query rows (new token x head) of a sequence.  Each KV tile of 64
 // tokens is read once into shared memory and serves both products: S = Q C^T
 // (M 64, N 64, K 576) and O += P C (M 64, N 2 x 256, K 64).  Why 64 rows: O of 512
@@ -18,15 +25,21 @@
 // stages (72 KB each; 54 KB of 48 tokens over a quantised cache, beside a staging
 // ring of 31 KB), P (8 KB).
 //
-// What bounds it (one GB300, 1.9 GHz): 16 heads, 100 x 8192 bf16 tokens: 156 us,
+// What bounds it (one GB300, 1.9 GHz): 16 heads, 100 x 8192 bf16 tokens: 157 us,
 // the kernel 153 at 6.2 TB/s of HBM reads, tensor pipe 62 % busy.  128 heads are
-// two row tiles a token, 96 contexts of 64 .. 32768 fp16 tokens: 192 us, a latency
+// two row tiles a token, 96 contexts of 64 .. 32768 fp16 tokens: 195 us, a latency
 // chain: a stage goes through load, S (36 products of 38 clocks), softmax and P C
 // (8 of 155) in 5500 clocks, and two stages are all that fits beside the queries;
 // halving both products takes 158.  Products of M 64 run at half the tensor
-// cores' rate.  E4M3, 16 heads x 4 new tokens, 100 contexts of 1024 .. 8192: 110 us,
-// 3600 clocks a tile in the converting warps (110 dependent instructions, waits and
-// votes a step of 16 tokens; ALU pipe 44 %, HBM 30 %; halving both products: 109.8).
+// cores' rate.  E4M3, 16 heads x 4 new tokens, 100 contexts of 1024 .. 8192: 111 us,
+// 3600 clocks a tile, in which no unit is busy half of the time (ALU 44 %, HBM 30 %).
+// Halving both products leaves it as it is, and without conversion and stores 96
+// us remain.  By elimination most of it is the way of the rows to the converting
+// warps (ids, copy, hand-over and hand-back of a slot) through a staging ring that
+// holds just one tile, with rows fetched into L2 only as their batch begins; its
+// steps are not measured one by one.  The E4M3 cache saves memory here, not time:
+// the same contexts in bf16 take 88 us; one new token 103 and 78, at 128 heads 197
+// and 140, where each of a token's row tiles converts the rows again.
 #include <algorithm>
 #include <cmath>
 
@@ -134,6 +147,9 @@ constexpr int LT_CTRL = 1024;
 constexpr int LT_TMEM = 512;                  // columns: O (256), S0, S1 (64 each)
 constexpr int LT_S = 256;
 constexpr uint32_t LT_HI = 16u << 16;         // lanes 16 .. 31 of each quarter: output dims 256 .. 511
+// Pieces whose flags are kept.  The producer has a piece's queries copied only after
+// all S of the piece before, and an S waits until the softmax has read the one two
+// tiles earlier: it is at most three pieces ahead of the softmax.
 constexpr int LT_BAD_SLOTS = 16;
 constexpr uint32_t LT_LAST = 0x7fffffffu;
 constexpr int L8_WARPS = 8;                   // converting warps
