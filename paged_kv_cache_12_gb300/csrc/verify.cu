@@ -315,9 +315,9 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
                     Sum2 run1 = run;
                     run1.add(x0);
                     // the first slice whose running sum passes, else the last of any weight
-                    const int g = x0.any() && height.passed_by(run1)  ? 2 * lane
+                    const int g = x0.any() && height.passed_by(run1)   ? 2 * lane
                                   : x1.any() && height.passed_by(upto) ? 2 * lane + 1
-                                                                      : INT_MAX;
+                                                                       : INT_MAX;
                     int first = g, last = x1.any() ? 2 * lane + 1 : x0.any() ? 2 * lane : -1;
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) {

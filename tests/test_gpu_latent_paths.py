@@ -303,7 +303,8 @@ def test_expanded_many_short_sequences(dt):
             s, e = ks[i], ks[i] + pasts[i] + bad
             key = torch.cat([k[s:e, h], r[s:e]], 1).double()
             o, tol = attend_causal(q[qs[i]:qs[i] + bad, h].double(), key, v[s:e, h].double(), SCALE, dt)
-            R.check(got[:bad], o, tol, f"sequence {i}, head {h}") if bad else None
+            if bad:
+                R.check(got[:bad], o, tol, f"sequence {i}, head {h}")
 
 
 def attend_causal(q, k, v, scale, dt):
