@@ -550,6 +550,154 @@ PA_API int pa_verify_drafts(int32_t *accepted, int32_t *tokens, const void *targ
                             int vocab_size, int64_t target_stride, int64_t draft_stride, int probs_dtype,
                             void *stream);
 
+/* ------------------------------------- KV write with the rotary positions */
+
+/* Axes of a token's position, at most (time, height and width take three). */
+#define PA_ROPE_MAX_AXES 4
+
+/* Turn the step's queries and keys to their positions and write the keys and
+ * values into their slots: pa_kv_write (pa_kv_write_fp8 for an FP8 cache) with
+ * the position rotation applied on the way, and the queries beside it.  Pair i
+ * of a head's first rope_dim elements, (x_i, x_{i + rope_dim / 2}), or with
+ * interleaved (x_2i, x_{2i + 1}), becomes
+ *   (x cos a - y sin a, y cos a + x sin a),
+ *   a = positions[pair_axis[i]][t] * inv_freq[i];
+ * the other elements stay.  A position is a number of its own, not the slot's:
+ * drafted siblings share one, and a token of an image or a video has one for
+ * each axis.
+ *   query          16-bit [num_tokens][num_heads][head_dim], tokens query_stride
+ *                  elements apart, or NULL with num_heads 0 (no queries)
+ *   query_out      the same shape, query_out_stride apart; it may be `query`
+ *                  itself (with the same stride) but must not overlap it otherwise
+ *   key, value     16-bit [num_tokens][num_kv_heads][head_dim], key_stride and
+ *                  value_stride elements apart (all strides multiples of 8 and
+ *                  at least a token's elements: the three may be slices of one
+ *                  projection's rows)
+ *   positions      int32 [num_axes][num_tokens], any value
+ *   inv_freq       float [rope_dim / 2]
+ *   pair_axis      int32 [rope_dim / 2], or NULL: axis 0 for every pair
+ *   slot_mapping   int64 [num_tokens], as in pa_kv_write.  A token whose slot is
+ *                  negative is padding: nothing of it is written, its row of
+ *                  query_out included.  (So is one whose slot is past the cache.)
+ *   k_cache, v_cache  caches of element type kv_dtype, the layout above; inputs
+ *                  and query_out bf16 for PA_KV_BF16, fp16 otherwise
+ *   head_dim       a multiple of 8; rope_dim a multiple of 16, at most head_dim
+ *                  and at most 512
+ *   num_axes       1 .. PA_ROPE_MAX_AXES
+ *   k_scale, v_scale  of an FP8 cache, as in pa_kv_write_fp8 (ignored otherwise)
+ * Angles in 64 bits up to the turn's fraction, cosines and the rotation in fp32;
+ * a turned key is rounded once, to the cache's type (for FP8 straight to the
+ * code of fl32(x' * fl32(1 / k_scale))).  An axis outside [0, num_axes) makes its
+ * pair NaN.  num_tokens = 0 is valid and launches nothing. */
+PA_API int pa_kv_write_rope(void *query_out, const void *query, const void *key, const void *value,
+                            const int32_t *positions, const float *inv_freq, const int32_t *pair_axis,
+                            const int64_t *slot_mapping, void *k_cache, void *v_cache, int num_tokens, int num_heads,
+                            int num_kv_heads, int head_dim, int rope_dim, int num_axes, int interleaved,
+                            int64_t query_stride, int64_t query_out_stride, int64_t key_stride, int64_t value_stride,
+                            int block_size, int64_t num_blocks, int kv_dtype, float k_scale, float v_scale,
+                            void *stream);
+
+/* ------------------------------------ a step over a tree of drafted tokens */
+
+/* A speculative step may draft a tree instead of a chain: several candidates
+ * for a position, each with drafts of its own after it.  The T nodes of a
+ * sequence's tree are its new tokens, parents before their children; node 0 is
+ * the last known token and parents[j] the node that node j follows (a number
+ * within the sequence, -1: none, the node follows the context).  Their K and V
+ * are written to the sequence's last T positions in the order of their numbers
+ * (pa_kv_write_rope with positions by depth, not by slot), pa_attention_tree
+ * computes their attention, pa_verify_tree finds the path that stands and
+ * pa_kv_move_path moves its K and V to the positions that follow the context. */
+
+/* Nodes of one sequence's tree, at most. */
+#define PA_TREE_MAX_NODES 256
+
+/* Workspace bytes pa_attention_tree needs (0 for invalid sizes), whatever the
+ * lengths. */
+PA_API size_t pa_attention_tree_workspace_size(int num_seqs, int num_query_tokens, int num_heads, int num_kv_heads,
+                                               int head_dim, int max_context_len);
+
+/* Attention of the nodes of trees over the paged cache: sequence i has L =
+ * context_lens[i] positions, the last T = query_start[i + 1] - query_start[i] of
+ * them its tree's nodes.  Node j (query row query_start[i] + j) sees the L - T
+ * positions before the tree, itself and its ancestors (position L - T + a for
+ * node a):
+ *   out[row][h] = sum over what it sees of softmax(scale <query[row][h], K_t[g]>)_t V_t[g].
+ * With parents[j] = j - 1 it is pa_attention_causal.
+ *   out, query     as in pa_attention_causal_typed, for kv_dtype
+ *   parents        int32 [num_query_tokens], each -1 or a smaller node of its
+ *                  sequence
+ *   other arguments as in pa_attention_causal_typed
+ *   workspace      pa_attention_tree_workspace_size bytes, 256-byte aligned, used
+ *                  only for the duration of the work on `stream`; it needs no
+ *                  initialisation
+ * Scores, softmax and sums in fp32; the probabilities are rounded to the
+ * operands' 16-bit type for the product with the values.  Device-side cases: a
+ * sequence with T > L, T > PA_TREE_MAX_NODES, an invalid L (as in pa_decode) or
+ * a block id out of range gets NaN rows; a node whose chain of parents meets a
+ * number that is neither -1 nor a smaller node gets a NaN row; a query_start
+ * that is not a non-decreasing cover of the rows makes every row NaN.  Positions
+ * that a node does not see (drafts that are not its ancestors, slots behind the
+ * context) may hold anything, infinities and NaN included: they do not reach its
+ * output; one that sees a key or value that is not finite gets a row that is not
+ * finite.  Deterministic.  pa_workspace_status reads the error word. */
+PA_API int pa_attention_tree(void *out, const void *query, const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                             const int32_t *parents, int num_seqs, int num_query_tokens, int num_heads,
+                             int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                             int max_blocks_per_seq, int max_context_len, float scale, int kv_dtype, float k_scale,
+                             float v_scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Find the path of a tree that stands, by drawing from the target itself: from
+ * node 0 on, the token that follows the present node c is drawn from its row of
+ * target probabilities p_c as the smallest v with
+ *   p_c[0] + ... + p_c[v] > uniform[c] * sum(p_c);
+ * if a child of c has that token (the first one of several), it stands and is
+ * the next present node, otherwise the path ends.  Tokens are drawn from the
+ * target one by one whatever the drafts are and however they were made, so no
+ * draft probabilities are asked for; a draft stands as often as the target would
+ * have drawn it.
+ *   accepted      int32 [num_seqs]: a, the drafts that stand
+ *   tokens        int32 [num_seqs][max_depth + 1]: the a drafts, the drawn token
+ *                 that is no child (or the one at depth max_depth), then -1
+ *   path          int32 [num_seqs][max_depth + 1]: node 0 and the a nodes that
+ *                 stand, then -1
+ *   target_probs  [num_nodes] rows of vocab_size, target_stride elements apart,
+ *                 of type probs_dtype (PA_PROBS_*); rows need not sum to one
+ *   node_tokens   int32 [num_nodes] (a sequence's first is not looked at)
+ *   parents       int32 [num_nodes], as in pa_attention_tree (only a larger
+ *                 node's entry can name its parent)
+ *   tree_start    int32 [num_seqs + 1], device, a non-decreasing cover of the nodes
+ *   uniform       float [num_nodes], in [0, 1)
+ * At most max_depth drafts are accepted.  NaN and negative weights count as
+ * zero; where a row sums to zero or its sum is not finite the token is -1 and the
+ * path ends.  A sequence without nodes or with a bad tree_start gets a = -1 and
+ * tokens and path -1.  Sums are carried in twice the precision of a float.
+ * Needs no workspace. */
+PA_API int pa_verify_tree(int32_t *accepted, int32_t *tokens, int32_t *path, const void *target_probs,
+                          const int32_t *node_tokens, const int32_t *parents, const int32_t *tree_start,
+                          const float *uniform, int num_seqs, int num_nodes, int max_depth, int vocab_size,
+                          int64_t target_stride, int probs_dtype, void *stream);
+
+/* Move the K and V of a verified path to the positions that follow the context:
+ * the row of node path[i][j], at position L - T + path[i][j], goes to position
+ * L - T + j for 0 <= j <= accepted[i] (L and T as in pa_attention_tree: the
+ * tree's nodes included), in every kv head and layer.  The sequence then has
+ * L - T + accepted[i] + 1 positions that count.
+ *   k_cache, v_cache  caches of element type kv_dtype of num_layers layers, one
+ *                  after another: [num_layers][num_blocks][num_kv_heads][block_size][head_dim]
+ *   block_tables, context_lens, query_start  as in pa_attention_tree
+ *   path, accepted  as pa_verify_tree wrote them
+ *   head_dim       a multiple of 8, for FP8 of 16; block_size >= 1
+ * A sequence stays as it is when accepted[i] is negative or above max_depth, its
+ * path does not begin with node 0, does not rise or leaves the tree, L, T or
+ * query_start is invalid, or a block id on the way is out of range.  Sequences
+ * must not share the blocks that hold their trees. */
+PA_API int pa_kv_move_path(void *k_cache, void *v_cache, const int32_t *block_tables, const int32_t *context_lens,
+                           const int32_t *query_start, const int32_t *path, const int32_t *accepted, int num_seqs,
+                           int max_depth, int num_layers, int num_kv_heads, int head_dim, int block_size,
+                           int64_t num_blocks, int max_blocks_per_seq, int kv_dtype, void *stream);
+
 /* ------------------------------------------------------ block allocator */
 
 /* Host-side block allocator with reference counts (no GPU involved).

@@ -48,6 +48,7 @@ EXPORTS = (
     "pa_decode_typed", "pa_attention_causal_typed", "pa_decode_static_ws_status", "pa_latent_write",
     "pa_latent_block_copy", "pa_latent_read", "pa_latent_attention_workspace_size", "pa_latent_attention",
     "pa_latent_attention_expanded_workspace_size", "pa_latent_attention_expanded", "pa_verify_drafts",
+    "pa_kv_write_rope", "pa_attention_tree_workspace_size", "pa_attention_tree", "pa_verify_tree", "pa_kv_move_path",
 )
 
 # cache element types (PA_KV_* in pa.h)
@@ -58,6 +59,9 @@ PA_LATENT_DIM, PA_LATENT_ROPE_DIM, PA_LATENT_ROW, PA_LATENT_ROW_FP8_BYTES = 512,
 
 # element types of probability rows (PA_PROBS_* in pa.h)
 PA_PROBS_F32, PA_PROBS_F16, PA_PROBS_BF16 = 0, 1, 2
+
+# axes of a token's position and nodes of a tree, at most (PA_ROPE_MAX_AXES, PA_TREE_MAX_NODES in pa.h)
+PA_ROPE_MAX_AXES, PA_TREE_MAX_NODES = 4, 256
 
 # bytes of the library's built-in scratch array used by pa_decode_static_ws
 PA_DECODE_STATIC_WS_BYTES = 64 << 20
@@ -137,6 +141,13 @@ def lib():
             "pa_latent_attention_expanded": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i64, i64, i64, i64,
                                               ctypes.c_float, i32, vp, sz, vp], i32),
             "pa_verify_drafts": ([vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i64, i32, vp], i32),
+            "pa_kv_write_rope": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i64, i64,
+                                  i64, i64, i32, i64, i32, ctypes.c_float, ctypes.c_float, vp], i32),
+            "pa_attention_tree_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
+            "pa_attention_tree": ([vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64, i32, i32,
+                                   ctypes.c_float, i32, ctypes.c_float, ctypes.c_float, vp, sz, vp], i32),
+            "pa_verify_tree": ([vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i32, vp], i32),
+            "pa_kv_move_path": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64, i32, i32, vp], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -683,6 +694,175 @@ def pa_verify_drafts(accepted, tokens, target_probs, draft_probs, draft_tokens, 
          None if draft_probs is None else draft_probs.data_ptr(), draft_tokens.data_ptr(), draft_start.data_ptr(),
          uniform.data_ptr(), sample_uniform.data_ptr(), b, nd, most, v, st if rows > 1 else v,
          sd if draft_probs is not None and nd > 1 else v, kind)
+
+
+# ---------------------------------------------------------------- rotary positions, trees of drafted tokens
+
+def _kv_caches(torch, where, k_cache, v_cache, ndim):
+    """(PA_KV_*, torch dtype of queries, keys and values, device index) of a pair of caches of `ndim` dimensions."""
+    dt = k_cache.dtype
+    if dt is torch.float16 or dt is torch.bfloat16:
+        kv, row = (PA_KV_F16 if dt is torch.float16 else PA_KV_BF16), dt
+    elif dt is torch.uint8 or dt is getattr(torch, "float8_e4m3fn", None):
+        kv, row = PA_KV_FP8_E4M3, torch.float16
+    else:
+        raise ValueError(f"{where}: unsupported cache dtype {dt}")
+    dev = k_cache.get_device()
+    _need_on(where, dev, k_cache, "k_cache", dt, ndim)
+    _need_on(where, dev, v_cache, "v_cache", dt, ndim)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"{where}: shape mismatch")
+    return kv, row, dev
+
+
+def _token_stride(where, dev, t, name, dtype, shape):
+    """The token stride of [tokens, heads, head_dim] rows whose heads lie side by side (slices of one projection's
+    rows, for instance); the tensor must have the shape."""
+    st = t.stride()
+    if t.get_device() != dev or dev < 0 or t.dtype is not dtype or t.dim() != 3 or \
+            (t.numel() > 0 and ((st[2] != 1 and shape[2] > 1) or (st[1] != shape[2] and shape[1] > 1))):
+        _refuse(where, dev, t, name, dtype, 3, "each token's heads contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{where}: shape mismatch")
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def pa_kv_write_rope(key, value, positions, inv_freq, slot_mapping, k_cache, v_cache, query=None, query_out=None,
+                     pair_axis=None, interleaved=False, k_scale=1.0, v_scale=1.0, stream=None):
+    """Turn keys and queries to their positions and write keys and values to
+    their slots (slot < 0: nothing of the token is written).  key, value
+    [tokens, kv_heads, head_dim], query [tokens, heads, head_dim] (token strides
+    free), positions int32 [tokens] or [axes, tokens], inv_freq float32
+    [rope_dim / 2], pair_axis int32 [rope_dim / 2] (the axis of each pair).  Turned
+    queries go to query_out, or to query itself without one."""
+    import torch
+    where, i32 = "pa_kv_write_rope", torch.int32
+    kv, dt, dev = _kv_caches(torch, where, k_cache, v_cache, 4)
+    nb, hk, bs, d = k_cache.shape
+    n = key.shape[0]
+    sk = _token_stride(where, dev, key, "key", dt, (n, hk, d))
+    sv = _token_stride(where, dev, value, "value", dt, (n, hk, d))
+    hq = sq = so = 0
+    qi = qo = None
+    if query is not None:
+        hq = query.shape[1]
+        sq = _token_stride(where, dev, query, "query", dt, (n, hq, d))
+        if query_out is None:
+            query_out, so = query, sq
+        else:
+            so = _token_stride(where, dev, query_out, "query_out", dt, (n, hq, d))
+        qi, qo = query.data_ptr(), query_out.data_ptr()
+    elif query_out is not None:
+        raise ValueError(f"{where}: query_out without query")
+    _need_on(where, dev, positions, "positions", i32, 1 if positions.dim() == 1 else 2)
+    _need_on(where, dev, inv_freq, "inv_freq", torch.float32, 1)
+    _need_on(where, dev, slot_mapping, "slot_mapping", torch.int64, 1)
+    pairs = inv_freq.shape[0]
+    if pair_axis is not None:
+        _need_on(where, dev, pair_axis, "pair_axis", i32, 1)
+        if pair_axis.shape[0] != pairs:
+            raise ValueError(f"{where}: shape mismatch")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.shape[-1] != n or slot_mapping.shape[0] != n:
+        raise ValueError(f"{where}: shape mismatch")
+    _run(where, dev, stream, qo, qi, key.data_ptr(), value.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+         None if pair_axis is None else pair_axis.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(),
+         v_cache.data_ptr(), n, hq, hk, d, 2 * pairs, axes, 1 if interleaved else 0, sq, so, sk, sv, bs, nb, kv,
+         float(k_scale), float(v_scale))
+
+
+def pa_attention_tree_workspace_size(num_seqs, num_query_tokens, num_heads, num_kv_heads, head_dim,
+                                     max_context_len) -> int:
+    n = lib().pa_attention_tree_workspace_size(int(num_seqs), int(num_query_tokens), int(num_heads),
+                                               int(num_kv_heads), int(head_dim), int(max_context_len))
+    if n == 0:
+        raise PAError(PA_ERR_INVALID_ARG, "pa_attention_tree_workspace_size")
+    return n
+
+
+def pa_attention_tree(out, query, k_cache, v_cache, block_tables, context_lens, query_start, parents, scale,
+                      max_context_len, workspace, k_scale=1.0, v_scale=1.0, stream=None):
+    """Attention of trees of drafted tokens: query rows query_start[i] ..
+    query_start[i + 1] - 1 are the nodes of sequence i's tree, its last
+    positions; each sees the context before the tree, itself and its ancestors
+    (parents [num_query_tokens] int32: a smaller node of the sequence, or -1).
+    Caches of fp16, bf16 or fp8 E4M3 codes as in pa_attention_causal_typed."""
+    import torch
+    where, i32 = "pa_attention_tree", torch.int32
+    kv, dt, dev = _kv_caches(torch, where, k_cache, v_cache, 4)
+    _need_on(where, dev, out, "out", dt, 3)
+    _need_on(where, dev, query, "query", dt, 3)
+    _need_on(where, dev, block_tables, "block_tables", i32, 2)
+    _need_on(where, dev, context_lens, "context_lens", i32, 1)
+    _need_on(where, dev, query_start, "query_start", i32, 1)
+    _need_on(where, dev, parents, "parents", i32, 1)
+    _need_on(where, dev, workspace, "workspace", torch.uint8, 1)
+    nb, hk, bs, d = k_cache.shape
+    nq, hq, w = query.shape
+    b, mb = block_tables.shape
+    if out.shape != query.shape or w != d or context_lens.shape[0] != b or query_start.shape[0] != b + 1 or \
+            parents.shape[0] != nq:
+        raise ValueError(f"{where}: shape mismatch")
+    _run(where, dev, stream, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+         block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), parents.data_ptr(), b, nq, hq, hk, d,
+         bs, nb, mb, int(max_context_len), float(scale), kv, float(k_scale), float(v_scale), workspace.data_ptr(),
+         workspace.shape[0])
+
+
+def pa_verify_tree(accepted, tokens, path, target_probs, node_tokens, parents, tree_start, uniform, stream=None):
+    """The path of each sequence's tree that stands: from node 0 on a token is
+    drawn from the node's row of target_probs ([num_nodes, vocab] float32, float16
+    or bfloat16) with its `uniform`, and the child with that token follows.
+    accepted [num_seqs], tokens and path [num_seqs, max_depth + 1] int32: the
+    drafts that stand and the token after them; node 0 and the nodes that stand;
+    then -1.  Sequence i's nodes are tree_start[i] .. tree_start[i + 1] - 1."""
+    import torch
+    where, i32, f32 = "pa_verify_tree", torch.int32, torch.float32
+    dt, dev = target_probs.dtype, target_probs.get_device()
+    kind = PA_PROBS_F32 if dt is f32 else PA_PROBS_F16 if dt is torch.float16 else \
+        PA_PROBS_BF16 if dt is torch.bfloat16 else -1
+    if kind < 0:
+        raise ValueError(f"{where}: target_probs must be float32, float16 or bfloat16")
+    st = _need_rows(where, dev, target_probs, "target_probs", dt, 2)[0]
+    _need_on(where, dev, accepted, "accepted", i32, 1)
+    _need_on(where, dev, tokens, "tokens", i32, 2)
+    _need_on(where, dev, path, "path", i32, 2)
+    _need_on(where, dev, node_tokens, "node_tokens", i32, 1)
+    _need_on(where, dev, parents, "parents", i32, 1)
+    _need_on(where, dev, tree_start, "tree_start", i32, 1)
+    _need_on(where, dev, uniform, "uniform", f32, 1)
+    n, v = target_probs.shape
+    b, width = tokens.shape
+    if accepted.shape[0] != b or path.shape != tokens.shape or width < 1 or node_tokens.shape[0] != n or \
+            parents.shape[0] != n or uniform.shape[0] != n or tree_start.shape[0] != b + 1:
+        raise ValueError(f"{where}: shape mismatch")
+    _run(where, dev, stream, accepted.data_ptr(), tokens.data_ptr(), path.data_ptr(), target_probs.data_ptr(),
+         node_tokens.data_ptr(), parents.data_ptr(), tree_start.data_ptr(), uniform.data_ptr(), b, n, width - 1, v,
+         st if n > 1 else v, kind)
+
+
+def pa_kv_move_path(k_cache, v_cache, block_tables, context_lens, query_start, path, accepted, stream=None):
+    """Move K and V of the nodes path[i][0 .. accepted[i]] of each sequence's tree
+    (its last query_start[i + 1] - query_start[i] positions) to the positions that
+    follow the context before the tree.  Caches of one layer [num_blocks,
+    kv_heads, block_size, head_dim] or of several [num_layers, ...]; path
+    [num_seqs, max_depth + 1] and accepted as pa_verify_tree wrote them."""
+    import torch
+    where, i32 = "pa_kv_move_path", torch.int32
+    kv, _, dev = _kv_caches(torch, where, k_cache, v_cache, 5 if k_cache.dim() == 5 else 4)
+    nb, hk, bs, d = k_cache.shape[-4:]
+    _need_on(where, dev, block_tables, "block_tables", i32, 2)
+    _need_on(where, dev, context_lens, "context_lens", i32, 1)
+    _need_on(where, dev, query_start, "query_start", i32, 1)
+    _need_on(where, dev, path, "path", i32, 2)
+    _need_on(where, dev, accepted, "accepted", i32, 1)
+    b, mb = block_tables.shape
+    if context_lens.shape[0] != b or query_start.shape[0] != b + 1 or path.shape[0] != b or path.shape[1] < 1 or \
+            accepted.shape[0] != b:
+        raise ValueError(f"{where}: shape mismatch")
+    _run(where, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+         query_start.data_ptr(), path.data_ptr(), accepted.data_ptr(), b, path.shape[1] - 1,
+         k_cache.shape[0] if k_cache.dim() == 5 else 1, hk, d, bs, nb, mb, kv)
 
 
 # ---------------------------------------------------------------- allocator

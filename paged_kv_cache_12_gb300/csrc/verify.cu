@@ -229,16 +229,110 @@ __device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, c
     return last;
 }
 
+// What a cluster's CTAs share while they draw a token.
+struct Draw {
+    Sum2 totals[VWARPS];   // this CTA's slices; then, in rank 0, the parts of one
+    Sum2 before;           // rank 0: the sum before the slice that passes
+    Height height;
+    int slice;             // rank 0: that slice; -1: no token; -2: no weight at all
+};
+
+// Draws a token by the weights w: the smallest whose running sum passes u times
+// the total.  The whole cluster; the token is in *next (in rank 0's shared memory,
+// -1 before) after the cluster's next meeting.  Returns the slice in which it lies,
+// -1 where there is none, or `empty` where the weights sum to zero.
+template <typename T, int VCTAS>
+__device__ __forceinline__ int draw_token(cg::cluster_group &cluster, Draw &sh, int *next, const Weights<T> &w,
+                                          int vocab, const float *u, int empty) {
+    const int rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int VSLICES = VCTAS * VWARPS;
+    const int len = ((vocab + VSLICES - 1) / VSLICES + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
+    const long long from = (long long)(rank * VWARPS + warp) * len;
+    const int lo = (int)min((long long)vocab, from), hi = (int)min((long long)vocab, from + len);
+    const Sum2 mine = range_sum(w, lo, hi);
+    if (lane == 0) sh.totals[warp] = mine;
+    cluster.sync();
+    if (rank == 0 && warp == 0) {   // lane l: slices 2 l and 2 l + 1
+        Sum2 x0, x1;
+        if (2 * lane < VSLICES) {
+            const Sum2 *src = cluster.map_shared_rank(sh.totals, 2 * lane / VWARPS) + 2 * lane % VWARPS;
+            x0 = src[0];
+            x1 = src[1];
+        }
+        Sum2 both = x0;
+        both.add(x1);
+        const Sum2 upto = warp_scan(both);
+        const Sum2 all{__shfl_sync(0xffffffffu, upto.hi, 31), __shfl_sync(0xffffffffu, upto.lo, 31)};
+        const float total = all.value();   // the same in all lanes
+        int slice = total == 0.f ? empty : -1;
+        if (total > 0.f && isfinite(total)) {
+            const Height height(all, *u);
+            Sum2 run = upto;   // before the lane's slices
+            run.add(-both.hi, -both.lo);
+            Sum2 run1 = run;
+            run1.add(x0);
+            // the first slice whose running sum passes, else the last of any weight
+            const int g = x0.any() && height.passed_by(run1)   ? 2 * lane
+                          : x1.any() && height.passed_by(upto) ? 2 * lane + 1
+                                                               : INT_MAX;
+            int first = g, last = x1.any() ? 2 * lane + 1 : x0.any() ? 2 * lane : -1;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
+                last = max(last, __shfl_xor_sync(0xffffffffu, last, d));
+            }
+            slice = first != INT_MAX ? first : last;
+            if (slice >> 1 == lane) {
+                sh.before = slice & 1 ? run1 : run;
+                sh.height = height;
+            }
+        }
+        if (lane == 0) sh.slice = slice;
+    }
+    cluster.sync();   // rank 0 has read every CTA's totals and decided
+    const int slice = *cluster.map_shared_rank(&sh.slice, 0);
+    if (len <= VBATCH * VCHUNK) {   // short slices: the warp that summed it finds the element
+        if (slice == rank * VWARPS + warp) {
+            const int v = find_in_range(w, lo, hi, *cluster.map_shared_rank(&sh.before, 0),
+                                        *cluster.map_shared_rank(&sh.height, 0));
+            if (lane == 0) *cluster.map_shared_rank(next, 0) = v;
+        }
+    } else if (rank == 0 && slice >= 0) {   // the slice again, in parts
+        const int first = slice * len, part = (len / VCHUNK + VWARPS - 1) / VWARPS * VCHUNK;
+        const int plo = min(vocab, min(first + len, first + warp * part));
+        const int phi = min(vocab, min(first + len, plo + part));
+        const Sum2 mine = range_sum(w, plo, phi);
+        if (lane == 0) sh.totals[warp] = mine;
+        __syncthreads();
+        Sum2 run = sh.before, before = run;
+        int at = -1;       // the first part that passes, else the last of any weight
+        bool passed = false;
+        for (int k = 0; k < VWARPS; ++k) {
+            const Sum2 x = sh.totals[k];
+            Sum2 after = run;
+            after.add(x);
+            if (!passed && x.any()) {
+                at = k;
+                before = run;
+                passed = sh.height.passed_by(after);
+            }
+            run = after;
+        }
+        if (warp == at) {
+            const int v = find_in_range(w, plo, phi, before, sh.height);
+            if (lane == 0) *next = v;
+        }
+    }
+    return slice;
+}
+
 template <typename T, int VCTAS>
 __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESIDENT) verify_kernel(const VerifyArgs a) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank();
     const int seq = blockIdx.x / VCTAS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ Sum2 totals[VWARPS];   // this CTA's slices; then, in rank 0, the parts of one
-    __shared__ Sum2 s_before;         // rank 0: the sum before the slice that passes
-    __shared__ Height s_height;
-    __shared__ int s_slice;           // rank 0: that slice; -1: no token; -2: draw from p itself
+    __shared__ Draw draw;
     __shared__ int s_next;
     __shared__ int s_kept, s_n, s_d0;
     grid_release();
@@ -287,87 +381,11 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         const T *p = static_cast<const T *>(a.target) + (long long)(d0 + seq + kept) * a.target_stride;
         const T *q = failed && a.draft ? static_cast<const T *>(a.draft) + (long long)(d0 + kept) * a.draft_stride : nullptr;
         Weights<T> w(p, q, failed && !a.draft ? a.draft_tokens[d0 + kept] : -1);
-        constexpr int VSLICES = VCTAS * VWARPS;
-        const int len = ((a.vocab + VSLICES - 1) / VSLICES + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
         for (int attempt = 0; attempt < 2; ++attempt) {
-            const long long from = (long long)(rank * VWARPS + warp) * len;
-            const int lo = (int)min((long long)a.vocab, from), hi = (int)min((long long)a.vocab, from + len);
-            const Sum2 mine = range_sum(w, lo, hi);
-            if (lane == 0) totals[warp] = mine;
-            cluster.sync();
-            if (rank == 0 && warp == 0) {   // lane l: slices 2 l and 2 l + 1
-                Sum2 x0, x1;
-                if (2 * lane < VSLICES) {
-                    const Sum2 *src = cluster.map_shared_rank(totals, 2 * lane / VWARPS) + 2 * lane % VWARPS;
-                    x0 = src[0];
-                    x1 = src[1];
-                }
-                Sum2 both = x0;
-                both.add(x1);
-                const Sum2 upto = warp_scan(both);
-                const Sum2 all{__shfl_sync(0xffffffffu, upto.hi, 31), __shfl_sync(0xffffffffu, upto.lo, 31)};
-                const float total = all.value();   // the same in all lanes
-                int slice = attempt == 0 && failed && total == 0.f ? -2 : -1;
-                if (total > 0.f && isfinite(total)) {
-                    const Height height(all, a.sample[seq]);
-                    Sum2 run = upto;   // before the lane's slices
-                    run.add(-both.hi, -both.lo);
-                    Sum2 run1 = run;
-                    run1.add(x0);
-                    // the first slice whose running sum passes, else the last of any weight
-                    const int g = x0.any() && height.passed_by(run1)   ? 2 * lane
-                                  : x1.any() && height.passed_by(upto) ? 2 * lane + 1
-                                                                       : INT_MAX;
-                    int first = g, last = x1.any() ? 2 * lane + 1 : x0.any() ? 2 * lane : -1;
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) {
-                        first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
-                        last = max(last, __shfl_xor_sync(0xffffffffu, last, d));
-                    }
-                    slice = first != INT_MAX ? first : last;
-                    if (slice >> 1 == lane) {
-                        s_before = slice & 1 ? run1 : run;
-                        s_height = height;
-                    }
-                }
-                if (lane == 0) s_slice = slice;
-            }
-            cluster.sync();   // rank 0 has read every CTA's totals and decided
-            const int slice = *cluster.map_shared_rank(&s_slice, 0);
-            if (len <= VBATCH * VCHUNK) {   // short slices: the warp that summed it finds the element
-                if (slice == rank * VWARPS + warp) {
-                    const int v = find_in_range(w, lo, hi, *cluster.map_shared_rank(&s_before, 0),
-                                                *cluster.map_shared_rank(&s_height, 0));
-                    if (lane == 0) *cluster.map_shared_rank(&s_next, 0) = v;
-                }
-            } else if (rank == 0 && slice >= 0) {   // the slice again, in parts
-                const int first = slice * len, part = (len / VCHUNK + VWARPS - 1) / VWARPS * VCHUNK;
-                const int plo = min(a.vocab, min(first + len, first + warp * part));
-                const int phi = min(a.vocab, min(first + len, plo + part));
-                const Sum2 mine = range_sum(w, plo, phi);
-                if (lane == 0) totals[warp] = mine;
-                __syncthreads();
-                Sum2 run = s_before, before = run;
-                int at = -1;       // the first part that passes, else the last of any weight
-                bool passed = false;
-                for (int k = 0; k < VWARPS; ++k) {
-                    const Sum2 x = totals[k];
-                    Sum2 after = run;
-                    after.add(x);
-                    if (!passed && x.any()) {
-                        at = k;
-                        before = run;
-                        passed = s_height.passed_by(after);
-                    }
-                    run = after;
-                }
-                if (warp == at) {
-                    const int v = find_in_range(w, plo, phi, before, s_height);
-                    if (lane == 0) s_next = v;
-                }
-            }
+            const int slice = draw_token<T, VCTAS>(cluster, draw, &s_next, w, a.vocab, a.sample + seq,
+                                                   attempt == 0 && failed ? -2 : -1);
             if (slice != -2) break;
-            w = Weights<T>(p, nullptr, -1);
+            w = Weights<T>(p, nullptr, -1);   // q covers p: draw from p itself
             cluster.sync();   // every CTA has read the decision
         }
         cluster.sync();   // the token is there, and rank 0's shared memory outlives its readers
@@ -377,6 +395,73 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
             out[j] = kept < 0 ? -1 : j < kept ? a.draft_tokens[d0 + j] : j == kept ? s_next : -1;
         if (lane == 0) a.accepted[seq] = kept;
     }
+}
+
+// ------------------------------------------------------------------ trees
+
+struct TreeVerifyArgs {
+    int32_t *accepted, *tokens, *path;
+    const void *target;
+    const int32_t *node_tokens, *parents, *tree_start;
+    const float *uniform;
+    int num_seqs, num_nodes, max_depth, vocab;
+    long long target_stride;
+};
+
+// A path through a sequence's tree: a cluster draws a token from the present
+// node's row and goes on to the child that has it.
+template <typename T, int VCTAS>
+__global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESIDENT)
+    verify_tree_kernel(const TreeVerifyArgs a) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank();
+    const int seq = blockIdx.x / VCTAS;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ Draw draw;
+    __shared__ int s_next[2];   // by the level's parity: a CTA may still read one level's token while the next is drawn
+    __shared__ int s_node;
+    grid_release();
+    grid_wait();
+    const int n0 = a.tree_start[seq], n1 = a.tree_start[seq + 1];
+    const bool ok = n0 >= 0 && n1 > n0 && n1 <= a.num_nodes && (seq > 0 || n0 == 0) &&
+                    (seq < a.num_seqs - 1 || n1 == a.num_nodes);
+    const int n = n1 - n0;
+    int32_t *tokens = a.tokens + (long long)seq * (a.max_depth + 1);
+    int32_t *path = a.path + (long long)seq * (a.max_depth + 1);
+    int level = -1, node = ok ? 0 : -1;   // the same in every CTA of the cluster
+    while (node >= 0) {
+        ++level;
+        int *next = &s_next[level & 1];
+        if (rank == 0 && threadIdx.x == 0) *next = -1;
+        const Weights<T> w(static_cast<const T *>(a.target) + (long long)(n0 + node) * a.target_stride, nullptr, -1);
+        draw_token<T, VCTAS>(cluster, draw, next, w, a.vocab, a.uniform + n0 + node, -1);
+        cluster.sync();   // the token is there
+        if (warp == 0) {
+            const int v = *cluster.map_shared_rank(next, 0);
+            if (rank == 0 && lane == 0) {
+                tokens[level] = v;
+                path[level] = node;
+            }
+            int child = -1;
+            for (int base = node + 1; v >= 0 && level < a.max_depth && base < n; base += 32) {
+                const int j = base + lane;
+                const unsigned has = __ballot_sync(0xffffffffu, j < n && a.parents[n0 + j] == node &&
+                                                                    a.node_tokens[n0 + j] == v);
+                if (has) {
+                    child = base + __ffs((int)has) - 1;
+                    break;
+                }
+            }
+            if (lane == 0) s_node = child;
+        }
+        __syncthreads();
+        node = s_node;
+    }
+    if (rank == 0) {
+        for (int j = level + 1 + (int)threadIdx.x; j <= a.max_depth; j += VTHREADS) tokens[j] = path[j] = -1;
+        if (threadIdx.x == 0) a.accepted[seq] = level;
+    }
+    cluster.sync();   // rank 0's shared memory outlives its readers
 }
 
 // The largest cluster with which all sequences' CTAs are resident at once (100
@@ -391,6 +476,17 @@ int launch_verify(const VerifyArgs &a, cudaStream_t st) {
     if (b * 4LL <= slots) return launch_early(verify_kernel<T, 4>, dim3(b * 4), VTHREADS, 0, st, a);
     if (b * 2LL <= slots) return launch_early(verify_kernel<T, 2>, dim3(b * 2), VTHREADS, 0, st, a);
     return launch_early(verify_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a);
+}
+
+// The same rule.
+template <typename T>
+int launch_verify_tree(const TreeVerifyArgs &a, cudaStream_t st) {
+    const long long slots = (long long)num_sms() * VRESIDENT;
+    const unsigned b = (unsigned)a.num_seqs;
+    if (b * 8LL <= slots) return launch_early(verify_tree_kernel<T, 8>, dim3(b * 8), VTHREADS, 0, st, a);
+    if (b * 4LL <= slots) return launch_early(verify_tree_kernel<T, 4>, dim3(b * 4), VTHREADS, 0, st, a);
+    if (b * 2LL <= slots) return launch_early(verify_tree_kernel<T, 2>, dim3(b * 2), VTHREADS, 0, st, a);
+    return launch_early(verify_tree_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a);
 }
 
 }  // namespace
@@ -423,4 +519,29 @@ extern "C" int pa_verify_drafts(int32_t *accepted, int32_t *tokens, const void *
     if (probs_dtype == PA_PROBS_F16) return launch_verify<__half>(a, st);
     if (probs_dtype == PA_PROBS_BF16) return launch_verify<__nv_bfloat16>(a, st);
     return launch_verify<float>(a, st);
+}
+
+extern "C" int pa_verify_tree(int32_t *accepted, int32_t *tokens, int32_t *path, const void *target_probs,
+                              const int32_t *node_tokens, const int32_t *parents, const int32_t *tree_start,
+                              const float *uniform, int num_seqs, int num_nodes, int max_depth, int vocab_size,
+                              int64_t target_stride, int probs_dtype, void *stream) {
+    if (num_seqs < 0 || num_nodes < 0 || max_depth < 0 || vocab_size <= 0 || target_stride < vocab_size ||
+        (num_seqs == 0 && num_nodes > 0))
+        return PA_ERR_INVALID_ARG;
+    if (probs_dtype != PA_PROBS_F32 && probs_dtype != PA_PROBS_F16 && probs_dtype != PA_PROBS_BF16)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > (1 << 24) || vocab_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!accepted || !tokens || !path || !tree_start ||
+        (num_nodes > 0 && (!target_probs || !node_tokens || !parents || !uniform)))
+        return PA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(target_probs) & (probs_dtype == PA_PROBS_F32 ? 3u : 1u)) return PA_ERR_INVALID_ARG;
+    const TreeVerifyArgs a{accepted, tokens, path, target_probs, node_tokens, parents, tree_start, uniform, num_seqs,
+                           num_nodes, max_depth, vocab_size, target_stride};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (debug_validate())
+        if (const int e = validate_starts(tree_start, num_seqs, num_nodes, true, st)) return e;
+    if (probs_dtype == PA_PROBS_F16) return launch_verify_tree<__half>(a, st);
+    if (probs_dtype == PA_PROBS_BF16) return launch_verify_tree<__nv_bfloat16>(a, st);
+    return launch_verify_tree<float>(a, st);
 }
