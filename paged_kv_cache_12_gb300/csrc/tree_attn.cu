@@ -1,8 +1,29 @@
 // Attention of trees of drafted tokens over the paged cache: a node sees the
 // context before the tree, itself and its ancestors.
 //
-// A warp takes one query row (a node's head) and walks the positions that it
-// sees, with a running maximum and sum.
+// The query rows of a sequence and kv head are its T nodes times the G heads of
+// the group, node by node.  A row tile is up to 256 of them (128 over an FP8
+// cache) and sees every KV tile of 128 tokens up to the context's end: only the
+// tiles that the tree's own positions reach are masked.  So a KV tile crosses HBM
+// once for all nodes of a usual tree.  The row tiles make the work axis
+// (work_axis.cuh), cut into equal ranges over the CTAs: one sequence with a long
+// context occupies the GPU as well as a batch.
+//
+// Warps: 0 loads keys and values (TMA boxes of a block's rows, the gather being
+// the row coordinate), 1 the queries, 2 issues the MMAs, 4-7 and 8-11 run the
+// softmax, a row per thread.  Over an FP8 cache 8-15 turn the staged codes into
+// 16-bit tiles instead.  Tensor memory: S0, S1 (128 columns each), O0, O1; P is
+// written over the first 64 columns of its S.
+//
+// A row tile of more than 128 rows is two halves, each with its own S, O and
+// softmax warps, that share every tile the CTA loads (PV0(n), S0(n + 1), PV1(n),
+// S1(n + 1): one half's products run while the other's softmax works).  With 128
+// rows or fewer S0 and S1 are the two buffers of one half: S(n + 1) is computed
+// while the softmax works on S(n).
+//
+// What a node sees of a masked tile is found by walking its chain of parents: a
+// set of 128 bits.  Values that some row does not see are made finite before the
+// product (0 times an infinity is none), and rows that do see one become NaN.
 
 #include <algorithm>
 #include <climits>
@@ -11,107 +32,822 @@
 #include <vector>
 
 #include "decode_common.cuh"
+#include "latent.h"
+#include "umma.cuh"
+#include "work_axis.cuh"
 
 namespace pa {
 namespace {
 
+constexpr int TR_HALF = 128;      // rows of a half
+constexpr int TR_TOK = 128;       // tokens of a KV tile
+constexpr int TR_MAX_ROWS = 256;
+
 struct TreeArgs {
     uint16_t *out;
     const uint16_t *query;
-    const void *k_cache, *v_cache;
     const int32_t *block_tables, *context_lens, *query_start, *parents;
     WsHeader *hdr;
-    int num_seqs, num_query_tokens, Hq, Hkv, G, bs, mbps, max_ctx;
+    int num_seqs, num_query_tokens, H, Hkv, G, bs, mbps, max_ctx;
+    int tile_toks;          // nodes of a row tile
+    int ginv;               // 65536 / G + 1: m / G = m * ginv >> 16 for a row m of a tile
     long long num_blocks;
     float scale_log2, v_scale;
+    long long wait_limit;
+    // workspace
+    int *status;            // [AXIS_MAX_CTAS] nonzero: the CTA gave up waiting
+    Cut *cuts;              // [AXIS_MAX_CTAS]
+    float2 *ml;             // [2 AXIS_MAX_CTAS][rows] maximum (log2 units) and sum of a partial row
+    float4 *o;              // [2 AXIS_MAX_CTAS][rows * D / 4] its unnormalised output (see partial_at)
+
+    // ---- the work axis: row tile r of a sequence is tile r % per_head of kv head r / per_head
+    static constexpr int COST = 4;
+    struct Seq {
+        int L, T, q0;
+        int per_head;   // row tiles of a kv head
+        int rts, ntiles;
+        bool valid;
+    };
+    __device__ __forceinline__ Seq seq_work(int i) const {
+        Seq w;
+        w.L = context_lens[i];
+        w.q0 = query_start[i];
+        w.T = query_start[i + 1] - w.q0;
+        w.valid = w.L >= 0 && w.L <= max_ctx && w.L <= (long long)mbps * bs && w.T <= w.L && w.T <= PA_TREE_MAX_NODES;
+        w.per_head = w.valid ? (w.T + tile_toks - 1) / tile_toks : 0;
+        w.rts = w.per_head * Hkv;
+        w.ntiles = w.valid ? w.L / TR_TOK + (w.L % TR_TOK != 0) : 0;
+        return w;
+    }
+    __device__ __forceinline__ long long start(const Seq &w, int j, int team) const {
+        return (long long)j * (COST + w.ntiles);
+    }
+    __device__ __forceinline__ int row_tile_at(const Seq &w, long long u, int team) const {
+        return min(w.rts / team - 1, (int)quick_div(u, COST + w.ntiles));
+    }
+    __device__ __forceinline__ bool in_teams(const Seq &w) const { return w.per_head % 2 == 0; }
+    __device__ __forceinline__ int row_tiles(const Seq &w, int r) const { return w.ntiles; }
+    __device__ __forceinline__ int first_tiles(const Seq &w, int r) const { return w.ntiles; }
+    __device__ __forceinline__ int first_node(const Seq &w, int r) const { return r % w.per_head * tile_toks; }
+    __device__ __forceinline__ int cut_rows(const Seq &w, int r) const {
+        return min(tile_toks, w.T - first_node(w, r)) * G;
+    }
+    __device__ __forceinline__ long long first_row(const Seq &w, int r) const {
+        return (long long)(w.q0 + first_node(w, r)) * H + r / w.per_head * G;
+    }
+    __device__ __forceinline__ bool seq_ok(int i) const { return query_start[i] <= query_start[i + 1]; }
+    __device__ __forceinline__ bool ends_ok() const {
+        return *query_start == 0 && query_start[num_seqs] == num_query_tokens;
+    }
+    // row m of a row tile, counted from the tile's first row in the output
+    __device__ __forceinline__ long long row_at(int m) const {
+        const int j = m * ginv >> 16;
+        return (long long)j * H + (m - j * G);
+    }
 };
 
-template <int KV>
-__device__ __forceinline__ float element(const void *cache, long long at) {
-    if constexpr (KV == PA_KV_F16) return __half2float(static_cast<const __half *>(cache)[at]);
-    if constexpr (KV == PA_KV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(cache)[at]);
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t *>(cache)[at], __NV_E4M3);
-    return __half2float(__half(h));
+// Shared memory, tiles and threads of the kernel for a cache type and head_dim.
+template <int KV, int D>
+struct Tree {
+    static constexpr bool F8 = KV == PA_KV_FP8_E4M3;
+    static constexpr int MK = F8 ? PA_KV_F16 : KV;         // type of the MMAs' operands
+    static constexpr int ROWS = F8 ? TR_HALF : TR_MAX_ROWS;
+    static constexpr int BLOCK = TR_TOK * 128;             // 128 rows x 64 elements, 128-byte swizzle
+    static constexpr int TILE = BLOCK * (D / 64);          // a key or value tile of 16-bit elements, a half's queries
+    static constexpr int RING = F8 ? 3 : 10 / (D / 64);    // tiles on their way
+    static constexpr int CODES = F8 ? TR_TOK * D : 0;      // a staged tile of codes
+    static constexpr int STAGES = F8 ? 4 : 0;
+    static constexpr int OFF_RING = 2 * TILE;
+    static constexpr int OFF_STAGE = OFF_RING + RING * TILE;
+    static constexpr int OFF_CTRL = OFF_STAGE + STAGES * CODES;
+    static constexpr int CTRL = 2048;
+    static constexpr int SMEM = OFF_CTRL + CTRL + 1024;    // + alignment slack
+    static constexpr int THREADS = F8 ? 512 : 384;
+    static constexpr int REGS_LAUNCH = F8 ? 128 : 168;     // per thread: 65536 / threads, rounded down to 8
+    static constexpr int REGS_LOW = F8 ? 80 : 104;         // warps 0 - 3
+    static constexpr int REGS_HIGH = F8 ? 208 : 200;       // the softmax warps
+    static constexpr int REGS_CONV = 112;                  // the converting warps
+    static constexpr int CONV_WARPS = 8;
+    static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
+    static_assert(128 * (REGS_LOW + (F8 ? REGS_HIGH + 2 * REGS_CONV : 2 * REGS_HIGH)) <= THREADS * REGS_LAUNCH,
+                  "register split within the launch's pool");
+};
+constexpr int TR_TMEM = 512, TR_O = 256;   // S0, S1 at columns 0 and 128; O0, O1 at 256 and 384
+constexpr int TR_MAX_RING = 10, TR_MAX_STAGES = 4;
+constexpr int TR_MARKS = 16;               // pieces whose tiles can be on their way, and more
+constexpr int TR_SEEN = PA_TREE_MAX_NODES / 32;
+
+struct TrCtrl {
+    uint64_t full[TR_MAX_RING], empty[TR_MAX_RING], stfull[TR_MAX_STAGES], stempty[TR_MAX_STAGES];
+    uint64_t qfull[2], qempty[2];
+    // one half: by S buffer; two halves: by half.  Two sets, so that the second
+    // half's warps, which one-half pieces do not concern, see every phase of theirs.
+    uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];
+    uint64_t done;
+    uint32_t tmem;
+    int abort;
+    Plan plan;
+    long long warp_sums[16];
+    int bad[TR_MARKS];      // 1 + the number of a piece that met a block id out of range
+    // Nodes whose values are not finite, as the first half's warps find them (a set
+    // each), for the piece's own rows and, of the pieces of two halves, for the
+    // second half's.  By the piece's parity: a warp begins the piece after next only
+    // when all warps are through with this one.
+    uint32_t poison[2][2][4][TR_SEEN];
+};
+
+// Where the softmax keeps four dims (32 k + 4 j ..) of a row, in float4: a store
+// of a warp's 32 rows (rows 32 q .. of the row tile) is one run of 512 bytes.
+template <int KV, int D>
+__device__ __forceinline__ long long partial_at(int slot, int q, int k, int j, int lane) {
+    return (((long long)slot * (Tree<KV, D>::ROWS / 32) + q) * (D / 32) + k) * 8 * 32 + j * 32 + lane;
 }
 
-constexpr int TS_WARPS = 8;
+// A piece of a row tile, in every role alike.
+struct TrPiece {
+    int g, node0, rows, n;   // kv head, first node, rows, KV tiles
+    bool two;                // two halves
+};
+__device__ __forceinline__ TrPiece piece_of(const TreeArgs &a, const Walk<TreeArgs> &p) {
+    TrPiece x;
+    x.g = p.r / p.w.per_head;
+    x.node0 = a.first_node(p.w, p.r);
+    x.rows = a.cut_rows(p.w, p.r);
+    x.n = p.t1 - p.t0;
+    x.two = x.rows > TR_HALF;
+    return x;
+}
+// The ring's order is K(0), then K(n + 1), V(n), the last V at the end: the place of a piece's tile.
+__device__ __forceinline__ int k_at(int n) { return n ? 2 * n - 1 : 0; }
+__device__ __forceinline__ int v_at(int n, int all) { return n + 1 < all ? 2 * n + 2 : 2 * all - 1; }
 
+// A whole warp's bounded wait.
+struct WarpWait {
+    TrCtrl &c;
+    long long limit;
+    bool ok = true;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) {
+        volatile int *abort_flag = &c.abort;
+        const bool got = ok && !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, limit);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) *abort_flag = 1;
+        return ok;
+    }
+};
+
+// One warp: keys and values in the order the MMAs take them, a lane per block.
 template <int KV, int D>
-__global__ void __launch_bounds__(32 * TS_WARPS) tree_simple_kernel(const TreeArgs a) {
-    constexpr int E = D / 32;
-    __shared__ uint32_t sees[TS_WARPS][PA_TREE_MAX_NODES / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_release();
-    grid_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->error = PA_OK;
-    bool ok = a.query_start[0] == 0 && a.query_start[a.num_seqs] == a.num_query_tokens;
-    for (int i = threadIdx.x; i < a.num_seqs; i += blockDim.x) ok = ok && a.query_start[i] <= a.query_start[i + 1];
-    ok = __syncthreads_and(ok);
-    const long long row = blockIdx.x * (long long)TS_WARPS + warp;
-    if (row >= (long long)a.num_query_tokens * a.Hq) return;
-    const int tok = (int)(row / a.Hq), h = (int)(row - (long long)tok * a.Hq), g = h / a.G;
-    float o[E], q[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f, q[e] = 0.f;
-    bool bad = !ok;
-    if (ok) {
-        int lo = 0, hi = a.num_seqs;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.query_start[mid] <= tok) lo = mid; else hi = mid;
-        }
-        const int q0 = a.query_start[lo], T = a.query_start[lo + 1] - q0, L = a.context_lens[lo];
-        bad = L < 0 || L > a.max_ctx || L > (long long)a.mbps * a.bs || T > L || T > PA_TREE_MAX_NODES;
-        if (!bad) {
-            if (lane < PA_TREE_MAX_NODES / 32) sees[warp][lane] = 0;
-            __syncwarp();
-            if (lane == 0)
-                for (int n = tok - q0; n >= 0;) {
-                    sees[warp][n >> 5] |= 1u << (n & 31);
-                    const int p = a.parents[q0 + n];
-                    if (p < -1 || p >= n) {
-                        bad = true;
-                        break;
-                    }
-                    n = p;
-                }
-            __syncwarp();
-            bad = __any_sync(0xffffffffu, bad);
-#pragma unroll
-            for (int e = 0; e < E; ++e) q[e] = element<KV == PA_KV_BF16 ? PA_KV_BF16 : PA_KV_F16>(a.query, row * D + lane * E + e);
-            for (int t = 0; !bad && t < L; ++t) {
-                const long long blk = a.block_tables[(long long)lo * a.mbps + t / a.bs];
-                if (blk < 0 || blk >= a.num_blocks) {
-                    bad = true;
-                    break;
-                }
-                const int n = t - (L - T);
-                if (n >= 0 && !(sees[warp][n >> 5] >> (n & 31) & 1u)) continue;
-                const long long at = ((blk * a.Hkv + g) * a.bs + t % a.bs) * D + lane * E;
-                float s = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) s = fmaf(q[e], element<KV>(a.k_cache, at + e), s);
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                s *= a.scale_log2;
-                const float nm = fmaxf(m, s), mu = nm == -INFINITY ? 0.f : nm, old = exp2f(m - mu), p = exp2f(s - mu);
-                m = nm;
-                l = l * old + p;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = o[e] * old + p * element<KV>(a.v_cache, at + e);
+__device__ void tr_load(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, const CUtensorMap *tmk,
+                        const CUtensorMap *tmv) {
+    using X = Tree<KV, D>;
+    constexpr int SLOTS = X::F8 ? X::STAGES : X::RING, BYTES = X::F8 ? X::CODES : X::TILE;
+    constexpr int ROW = X::F8 ? D : 2 * D;   // bytes of a row
+    const int lane = threadIdx.x & 31;
+    uint64_t *full = X::F8 ? c.stfull : c.full, *empty = X::F8 ? c.stempty : c.empty;
+    const uint32_t base = smem_u32(smem) + (X::F8 ? X::OFF_STAGE : X::OFF_RING);
+    const int boxes = TR_TOK / a.bs;
+    const uint64_t once = policy_evict_first(), again = policy_evict_normal();
+    WarpWait wait{c, a.wait_limit};
+    int cnt = 0;
+    while (wait.ok && p.next()) {
+        const TrPiece x = piece_of(a, p);
+        const uint64_t policy = p.w.per_head > 1 ? again : once;
+        const int32_t *table = a.block_tables + (long long)p.seq * a.mbps;
+        // this lane's row coordinate in tile t (-1: the context ends before its block)
+        auto row_of = [&](int t) {
+            const int pos = t * TR_TOK + lane * a.bs;
+            if (lane >= boxes || pos >= p.w.L) return -1;
+            long long id = table[pos / a.bs];
+            if (id < 0 || id >= a.num_blocks) {
+                c.bad[p.local % TR_MARKS] = p.local + 1;
+                id = 0;
             }
+            return (int)((id * a.Hkv + x.g) * a.bs);
+        };
+        auto load = [&](const CUtensorMap *tm, int row) {
+            const int s = cnt % SLOTS;
+            if (!wait(&empty[s], (uint32_t)(((cnt / SLOTS) & 1) ^ 1))) return;
+            const uint32_t bar = smem_u32(&full[s]);
+            const int some = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(some * a.bs * ROW));
+            __syncwarp();
+            if (row >= 0) {
+                const uint32_t dst = base + s * BYTES + lane * a.bs * 128;
+                tma_load_2d(dst, tm, 0, row, bar, policy);
+                if (!X::F8 && D == 128) tma_load_2d(dst + X::BLOCK, tm, 64, row, bar, policy);
+            }
+            ++cnt;
+        };
+        int row = row_of(p.t0);
+        load(tmk, row);
+        for (int t = p.t0; wait.ok && t < p.t1; ++t) {
+            int next = -1;
+            if (t + 1 < p.t1) {
+                next = row_of(t + 1);
+                load(tmk, next);
+            }
+            if (wait.ok) load(tmv, row);
+            row = next;
         }
     }
-    const float inv = bad ? __int_as_float(0x7fc00000) : a.v_scale / l;
+    // the last copies into every buffer have landed before the CTA leaves
+    for (int s = 0; s < SLOTS; ++s)
+        if (cnt > s)
+            mbar_wait_bounded(smem_u32(&full[s]), (uint32_t)(((cnt - 1 - s) / SLOTS) & 1), WAIT_LIMIT);
+}
+
+// One warp: the queries of a piece's rows, as the products read them.
+template <int KV, int D>
+__device__ void tr_query(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p) {
+    using X = Tree<KV, D>;
+    constexpr int CH = D / 8;   // 16-byte chunks of a row
+    const int lane = threadIdx.x & 31;
+    WarpWait wait{c, a.wait_limit};
+    int qc[2] = {0, 0}, sel = 0;
+    while (wait.ok && p.next()) {
+        const TrPiece x = piece_of(a, p);
+        const uint16_t *first = a.query + a.first_row(p.w, p.r) * D;
+        for (int h = 0; wait.ok && h < (x.two ? 2 : 1); ++h) {
+            const int b = x.two ? h : sel;
+            if (!wait(&c.qempty[b], (uint32_t)((qc[b] & 1) ^ 1))) break;
+            const uint32_t dst = smem_u32(smem) + b * X::TILE;
+            const int rows = min(TR_HALF, x.rows - h * TR_HALF);
+            for (int i = lane; i < rows * CH; i += 32) {
+                const int m = i / CH, ch = i % CH;
+                const uint16_t *src = first + a.row_at(h * TR_HALF + m) * D + 8 * ch;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 dst + (ch / 8) * X::BLOCK + m * 128 + (((ch & 7) ^ (m & 7)) << 4)),
+                             "l"(src)
+                             : "memory");
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.qfull[b]));
+            ++qc[b];
+        }
+        if (!x.two) sel ^= 1;
+    }
+}
+
+// The converting warps (w of CONV_WARPS): staged codes to fp16 tiles of the same
+// swizzled layout (every E4M3 value is an fp16 value).  A warp's eight lanes of a
+// row store their 16-byte pieces so that all banks are covered: those of the
+// second 64 dims their odd one first.
+template <int KV, int D>
+__device__ void tr_convert(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, int w) {
+    using X = Tree<KV, D>;
+    constexpr int N = X::CODES / 16 / (32 * X::CONV_WARPS);   // 16-byte chunks a thread
+    const int lane = threadIdx.x & 31;
+    WarpWait wait{c, a.wait_limit};
+    int cnt = 0;
+    while (wait.ok && p.next()) {
+        for (int k = 0; wait.ok && k < 2 * (p.t1 - p.t0); ++k, ++cnt) {
+            const int st = cnt % X::STAGES, s = cnt % X::RING;
+            if (!wait(&c.stfull[st], (uint32_t)((cnt / X::STAGES) & 1))) break;
+            const uint8_t *from = smem + X::OFF_STAGE + st * X::CODES;
+            uint4 v[N];
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.out[row * D + lane * E + e] = out_bits<KV>(o[e] * inv);
+            for (int i = 0; i < N; ++i) {
+                const int at = (w * N + i) * 32 + lane, m = at / 8, cc = at & 7;
+                v[i] = *reinterpret_cast<const uint4 *>(from + m * 128 + ((cc ^ (m & 7)) << 4));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.stempty[st]));
+            if (!wait(&c.empty[s], (uint32_t)(((cnt / X::RING) & 1) ^ 1))) break;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = (w * N + i) * 32 + lane, m = at / 8, cc = at & 7;
+                uint8_t *to = smem + X::OFF_RING + s * X::TILE + (cc >> 2) * X::BLOCK + m * 128;
+                const uint4 lo = make_uint4(e4m3x2_lo_to_f16x2(v[i].x), e4m3x2_hi_to_f16x2(v[i].x),
+                                            e4m3x2_lo_to_f16x2(v[i].y), e4m3x2_hi_to_f16x2(v[i].y));
+                const uint4 hi = make_uint4(e4m3x2_lo_to_f16x2(v[i].z), e4m3x2_hi_to_f16x2(v[i].z),
+                                            e4m3x2_lo_to_f16x2(v[i].w), e4m3x2_hi_to_f16x2(v[i].w));
+                const int odd = cc >> 2, ch = (cc & 3) * 2;
+                *reinterpret_cast<uint4 *>(to + (((ch + odd) ^ (m & 7)) << 4)) = odd ? hi : lo;
+                *reinterpret_cast<uint4 *>(to + (((ch + 1 - odd) ^ (m & 7)) << 4)) = odd ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c.full[s]));
+        }
+    }
+}
+
+// One lane: the MMAs.
+template <int KV, int D>
+__device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_t tmem) {
+    using X = Tree<KV, D>;
+    const uint32_t base = smem_u32(smem);
+    constexpr uint32_t ID_S = idesc_f16(TR_HALF, TR_TOK, X::MK == PA_KV_BF16, false);
+    constexpr uint32_t ID_O = idesc_f16(TR_HALF, D, X::MK == PA_KV_BF16, true);
+    const uint64_t dq0 = sw128_desc(base, 16, 1024);
+    const uint64_t dk0 = sw128_desc(base + X::OFF_RING, 16, 1024);
+    const uint64_t dv0 = sw128_desc(base + X::OFF_RING, X::BLOCK, 1024);
+    volatile int *abort_flag = &c.abort;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        ok = ok && !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, a.wait_limit);
+        if (!ok) *abort_flag = 1;
+        return ok;
+    };
+    int cnt = 0, qc[2] = {0, 0}, sel = 0;          // ring tiles before this piece; queries taken; the next buffer of one half
+    int pc[2] = {0, 0}, pc2 = 0;                   // P tiles taken: of each buffer; of each half
+    auto ring_wait = [&](int k) { return wait(&c.full[k % X::RING], (uint32_t)((k / X::RING) & 1)); };
+    auto release = [&](int k) { umma_commit(smem_u32(&c.empty[k % X::RING])); };
+    // S in buffer b = the queries of buffer q times the key tile at k
+    auto issue_s = [&](int b, int q, int k) {
+        const uint64_t dk = dk0 + (uint64_t)(k % X::RING * (X::TILE >> 4)), dq = dq0 + (uint64_t)(q * (X::TILE >> 4));
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                umma_f16(tmem + b * TR_TOK, dq + h * (X::BLOCK >> 4) + 2 * j, dk + h * (X::BLOCK >> 4) + 2 * j, ID_S,
+                         h > 0 || j > 0 ? 1u : 0u);
+    };
+    // O_o += P in buffer b times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
+    auto issue_pv = [&](int b, int o, int k, int n) {
+        const uint64_t dv = dv0 + (uint64_t)(k % X::RING * (X::TILE >> 4));
+#pragma unroll
+        for (int j = 0; j < TR_TOK / 16; ++j)
+            umma_f16_ts(tmem + TR_O + o * 128, tmem + b * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4), ID_O,
+                        n > 0 || j > 0 ? 1u : 0u);
+    };
+    while (ok && p.next()) {
+        const TrPiece x = piece_of(a, p);
+        const int N = x.n;
+        if (!x.two) {
+            if (!wait(&c.qfull[sel], (uint32_t)(qc[sel]++ & 1)) || !ring_wait(cnt)) break;
+            tc_fence_after_sync();
+            issue_s(0, sel, cnt);
+            umma_commit(smem_u32(&c.sfull[0][0]));
+            release(cnt);
+            if (N == 1) umma_commit(smem_u32(&c.qempty[sel]));
+            for (int n = 0; n < N; ++n) {
+                const int b = n & 1, v = cnt + v_at(n, N);
+                if (n + 1 < N) {   // buffer b ^ 1: its P has been taken by PV(n - 1)
+                    const int k = cnt + k_at(n + 1);
+                    if (!ring_wait(k)) break;
+                    tc_fence_after_sync();
+                    issue_s(b ^ 1, sel, k);
+                    umma_commit(smem_u32(&c.sfull[0][b ^ 1]));
+                    release(k);
+                    if (n + 2 == N) umma_commit(smem_u32(&c.qempty[sel]));
+                }
+                if (!wait(&c.pfull[0][b], (uint32_t)(pc[b]++ & 1)) || !ring_wait(v)) break;
+                tc_fence_after_sync();
+                issue_pv(b, 0, v, n);
+                umma_commit(smem_u32(&c.pvdone[0][b]));
+                release(v);
+            }
+            sel ^= 1;
+        } else {
+            if (!wait(&c.qfull[0], (uint32_t)(qc[0]++ & 1)) || !wait(&c.qfull[1], (uint32_t)(qc[1]++ & 1)) ||
+                !ring_wait(cnt))
+                break;
+            tc_fence_after_sync();
+            for (int h = 0; h < 2; ++h) {
+                issue_s(h, h, cnt);
+                umma_commit(smem_u32(&c.sfull[1][h]));
+                if (N == 1) umma_commit(smem_u32(&c.qempty[h]));
+            }
+            release(cnt);
+            for (int n = 0; ok && n < N; ++n) {
+                const bool more = n + 1 < N;
+                const int v = cnt + v_at(n, N), k = cnt + k_at(n + 1);
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait(&c.pfull[1][h], (uint32_t)(pc2 & 1)) || (h == 0 && !ring_wait(v))) break;
+                    tc_fence_after_sync();
+                    issue_pv(h, h, v, n);
+                    umma_commit(smem_u32(&c.pvdone[1][h]));
+                    if (h == 1) release(v);
+                    if (more) {
+                        if (h == 0 && !ring_wait(k)) break;
+                        tc_fence_after_sync();
+                        issue_s(h, h, k);
+                        umma_commit(smem_u32(&c.sfull[1][h]));
+                        if (n + 2 == N) umma_commit(smem_u32(&c.qempty[h]));
+                        if (h == 1) release(k);
+                    }
+                }
+                ++pc2;
+            }
+        }
+        cnt += 2 * N;
+    }
+    // every product issued has completed before tensor memory is freed
+    umma_commit(smem_u32(&c.done));
+    mbar_wait_bounded(smem_u32(&c.done), 0, WAIT_LIMIT);
+}
+
+// One warpgroup: the softmax of half x, a row per thread.
+template <int KV, int D>
+__device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_t tmem, int x) {
+    using X = Tree<KV, D>;
+    constexpr int MK = X::MK;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, m = quarter * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t ocol = (uint32_t)(TR_O + x * 128);
+    const float sl2 = a.scale_log2;
+    WarpWait wait{c, a.wait_limit};
+    int sc[2] = {0, 0}, sc2 = 0, cnt = 0;   // S and P so far, of each buffer and of each half; ring tiles before this piece
+    int both = -1;                          // number of the last piece of two halves
+    while (wait.ok && p.next()) {
+        const TrPiece pc = piece_of(a, p);
+        const int N = pc.n;
+        if (pc.two) ++both;
+        if (!pc.two && x == 1) {
+            cnt += 2 * N;
+            continue;
+        }
+        const int mm = pc.two ? x * TR_HALF + m : m;   // row of the row tile
+        const bool mine = mm < pc.rows;
+        const bool idle = !__any_sync(0xffffffffu, mine);
+        const int node = pc.node0 + (mm * a.ginv >> 16);
+        const int ctx = p.w.L - p.w.T;                 // positions before the tree
+        const int32_t *parents = a.parents + p.w.q0;
+        float mrun = -INFINITY, l = 0.f;
+        bool lost = false;                             // the chain of parents is broken
+        for (int n = 0; n < N; ++n) {
+            const int b = pc.two ? x : n & 1, set = pc.two ? 1 : 0, times = pc.two ? sc2 : sc[b];
+            if (!wait(&c.sfull[set][b], (uint32_t)(times & 1))) break;
+            // (every phase is seen, so that one waited for later is not taken for another)
+            if (n > (pc.two ? 0 : 1) && !wait(&c.pvdone[set][b], (uint32_t)((times - 1) & 1))) break;
+            if (n == 0 && x == 0 && lane < TR_SEEN) {
+                c.poison[0][p.local & 1][quarter][lane] = 0;
+                if (pc.two) c.poison[1][both & 1][quarter][lane] = 0;
+            }
+            __syncwarp();
+            tc_fence_after_sync();
+            const int t0 = (p.t0 + n) * TR_TOK;
+            const bool tail = ctx - t0 < TR_TOK;         // the tree's positions begin before the tile ends
+            bool changed = false;
+            if (tail && x == 0) {
+                // Value rows that some row of the row tile does not see, where P is 0
+                // and a product with an infinity or a NaN would not be: those behind the
+                // context are zeroed, and so is what is not finite among the nodes' (the
+                // rows that see it become NaN below).  The first half's warps do it for
+                // both: PV1(n) is issued after P0(n).
+                const int at = cnt + v_at(n, N);
+                if (!wait(&c.full[at % X::RING], (uint32_t)((at / X::RING) & 1))) break;
+                const int lo = max(0, ctx - t0), hi = p.w.L - t0;
+#pragma unroll 1
+                for (int h = 0; h < D / 64; ++h) {
+                    uint4 *blk = reinterpret_cast<uint4 *>(smem + X::OFF_RING + at % X::RING * X::TILE + h * X::BLOCK);
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {      // this thread's chunks m, m + 128, ..: row m / 8 + 16 i
+                        const int r = m / 8 + 16 * i;
+                        uint4 &v = blk[m + TR_HALF * i];
+                        if (r >= hi) {
+                            v = make_uint4(0, 0, 0, 0);
+                        } else if (r >= lo && not_finite<MK>(v)) {
+                            v = make_uint4(finite_part<MK>(v.x), finite_part<MK>(v.y), finite_part<MK>(v.z),
+                                           finite_part<MK>(v.w));
+                            const int bad = t0 + r - ctx;
+                            atomicOr(&c.poison[0][p.local & 1][quarter][bad >> 5], 1u << (bad & 31));
+                            if (pc.two) atomicOr(&c.poison[1][both & 1][quarter][bad >> 5], 1u << (bad & 31));
+                        }
+                    }
+                }
+                changed = true;
+            }
+            if (!idle) {
+                float s[TR_TOK];
+#pragma unroll
+                for (int q = 0; q < TR_TOK / 32; ++q) {
+                    uint32_t r[32];
+                    tmem_ld32(trow + b * TR_TOK + 32 * q, r);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[32 * q + k] = __uint_as_float(r[k]);
+                }
+                tmem_wait_ld();
+                if (tail) {
+                    // what the row sees of the tile, a bit per column: the context, then its chain
+                    uint32_t see[TR_TOK / 32];
+#pragma unroll
+                    for (int k = 0; k < TR_TOK / 32; ++k) {
+                        const int before = min(32, ctx - t0 - 32 * k);
+                        see[k] = !mine || before <= 0 ? 0u : before == 32 ? ~0u : (1u << before) - 1u;
+                    }
+                    for (int j = mine ? node : -1; j >= 0;) {
+                        const int at = ctx + j - t0;
+#pragma unroll
+                        for (int k = 0; k < TR_TOK / 32; ++k)
+                            if (at >> 5 == k) see[k] |= 1u << (at & 31);
+                        const int up = parents[j];
+                        lost = lost || up < -1 || up >= j;
+                        j = lost ? -1 : up;
+                    }
+#pragma unroll
+                    for (int k = 0; k < TR_TOK; ++k) s[k] = see[k / 32] >> (k & 31) & 1u ? s[k] : -INFINITY;
+                }
+                float mp[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int k = 4; k + 8 <= TR_TOK; k += 8)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mp[j] = max3(mp[j], s[k + 2 * j], s[k + 2 * j + 1]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mp[j] = fmaxf(mp[j], s[TR_TOK - 4 + j]);
+                const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
+                // decided per row, done warp-wide (tensor-memory accesses are the
+                // whole warp's); rows that do not grow scale by exactly 1
+                const bool grow = mx > mrun + RESCALE_THRESHOLD;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float nm = grow ? mx : mrun;
+                    const float alpha = grow ? fast_exp2(mrun - nm) : 1.f;
+                    if (n > 0) {
+                        // two halves: PV(n - 1) is complete, S(n) was issued after it
+                        if (!pc.two && !wait(&c.pvdone[0][b ^ 1], (uint32_t)((sc[b ^ 1] - 1) & 1))) break;
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t o[32];
+                            tmem_ld32(trow + ocol + 32 * q, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st32(trow + ocol + 32 * q, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    l *= alpha;
+                    mrun = nm;
+                }
+                const float mu = mrun == -INFINITY ? 0.f : mrun;   // a row that has seen nothing yet
+                const uint64_t sl2x2 = pair_of(sl2, sl2), negm = pair_of(-mu, -mu);
+                uint64_t lp[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) lp[j] = 0;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        float e0, e1;
+                        pair_parts(pair_fma(pair_of(s[64 * q + 2 * k], s[64 * q + 2 * k + 1]), sl2x2, negm), e0, e1);
+                        e0 = fast_exp2(e0);
+                        e1 = fast_exp2(e1);
+                        lp[k & 3] = pair_add(lp[k & 3], pair_of(e0, e1));
+                        r[k] = pack_p<MK>(e0, e1);
+                    }
+                    tmem_st32(trow + b * TR_TOK + 32 * q, r);
+                }
+                float l0, l1;
+                pair_parts(pair_add(pair_add(lp[0], lp[1]), pair_add(lp[2], lp[3])), l0, l1);
+                l += l0 + l1;
+                tmem_wait_st();
+            }
+            if (changed) fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();   // one arrival a warp: 32 atomics on one word hold up the shared-memory pipe
+            if (lane == 0) mbar_arrive(smem_u32(&c.pfull[set][b]));
+            if (pc.two) ++sc2; else ++sc[b];
+        }
+        if (!wait.ok) break;
+        // the last products (and, with one half, those before them)
+        if (pc.two) {
+            if (!wait(&c.pvdone[1][x], (uint32_t)((sc2 - 1) & 1))) break;
+        } else {
+            const int b = (N - 1) & 1;
+            if (N > 1 && !wait(&c.pvdone[0][b ^ 1], (uint32_t)((sc[b ^ 1] - 1) & 1))) break;
+            if (!wait(&c.pvdone[0][b], (uint32_t)((sc[b] - 1) & 1))) break;
+        }
+        cnt += 2 * N;
+        if (idle) continue;
+        tc_fence_after_sync();
+        // ---- the piece's rows: finished, or a partial row
+        const volatile uint32_t(*poison)[TR_SEEN] = x == 0 ? c.poison[0][p.local & 1] : c.poison[1][both & 1];
+        uint32_t any = 0;
+        if (lane < TR_SEEN) any = poison[0][lane] | poison[1][lane] | poison[2][lane] | poison[3][lane];
+        if (__any_sync(0xffffffffu, any != 0))
+            for (int j = mine && !lost ? node : -1; j >= 0;) {
+                const int w = j >> 5;
+                if ((poison[0][w] | poison[1][w] | poison[2][w] | poison[3][w]) >> (j & 31) & 1u) lost = true;
+                const int up = parents[j];   // (in order: a piece with such nodes has walked the chain)
+                j = lost || up >= j ? -1 : up;
+            }
+        if (*reinterpret_cast<volatile int *>(&c.bad[p.local % TR_MARKS]) == p.local + 1) lost = true;
+        if (lost) l = __int_as_float(0x7fc00000);
+        const bool whole = p.whole();
+        if (!whole && mine) a.ml[(long long)p.slot() * X::ROWS + mm] = make_float2(mrun, l);
+        const float inv = a.v_scale / l;
+        uint16_t *orow = a.out + (a.first_row(p.w, p.r) + a.row_at(mm)) * D;
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(trow + ocol + 32 * q, o);
+            tmem_wait_ld();
+            if (mine && whole) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = (uint32_t)out_bits<MK>(__uint_as_float(o[k + 2 * i]) * inv) |
+                               ((uint32_t)out_bits<MK>(__uint_as_float(o[k + 2 * i + 1]) * inv) << 16);
+                    *reinterpret_cast<uint4 *>(orow + 32 * q + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else if (mine) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<uint4 *>(a.o + partial_at<KV, D>(p.slot(), mm / 32, q, k / 4, lane)) =
+                        make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
+            __syncwarp();   // the next load is the whole warp's
+        }
+        tc_fence_before_sync();
+    }
 }
 
 template <int KV, int D>
-int launch_tree(const TreeArgs &a, cudaStream_t st) {
-    const long long rows = (long long)a.num_query_tokens * a.Hq;
-    return launch_early(tree_simple_kernel<KV, D>, dim3((unsigned)((rows + TS_WARPS - 1) / TS_WARPS)), 32 * TS_WARPS, 0, st,
-                        a);
+__global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const TreeArgs a) {
+    using X = Tree<KV, D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    TrCtrl &c = *reinterpret_cast<TrCtrl *>(smem + X::OFF_CTRL);
+    static_assert(sizeof(TrCtrl) <= X::CTRL, "control block");
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < X::RING; ++s) {
+            mbar_init(smem_u32(&c.full[s]), X::F8 ? X::CONV_WARPS : 1);
+            mbar_init(smem_u32(&c.empty[s]), 1);
+        }
+        for (int s = 0; s < X::STAGES; ++s) {
+            mbar_init(smem_u32(&c.stfull[s]), 1);
+            mbar_init(smem_u32(&c.stempty[s]), X::CONV_WARPS);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&c.qfull[b]), 1);
+            mbar_init(smem_u32(&c.qempty[b]), 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(smem_u32(&c.sfull[b][h]), 1);
+                mbar_init(smem_u32(&c.pfull[b][h]), TR_HALF / 32);
+                mbar_init(smem_u32(&c.pvdone[b][h]), 1);
+            }
+        }
+        mbar_init(smem_u32(&c.done), 1);
+        c.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&tmk);
+        tma_prefetch_map(&tmv);
+    } else if (threadIdx.x >= 32 && threadIdx.x < 32 + TR_MARKS) {
+        c.bad[threadIdx.x - 32] = 0;
+    }
+    grid_wait();
+    if (warp == 2) {   // (not before: an earlier kernel may still need its own)
+        tmem_alloc(smem_u32(&c.tmem), TR_TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    make_plan(a, &c.plan, c.warp_sums);
+    tc_fence_after_sync();
+    const Plan plan = c.plan;
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&c.tmem);
+    grid_release();   // the merge's CTAs may come as this kernel's leave (they wait for all of them)
+    fill_idle_rows<D / 8>(a, plan, a.out, (long long)a.num_query_tokens * a.H,
+                          X::MK == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
+    if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
+        Walk<TreeArgs> p(a, plan);
+        if (warp >= 4 && (!X::F8 || warp < 8)) {
+            regs_increase<X::REGS_HIGH>();
+            tr_softmax<KV, D>(smem, c, a, p, tmem, (warp - 4) >> 2);
+        } else if (warp >= 8) {
+            if constexpr (X::F8) {
+                regs_decrease<X::REGS_CONV>();
+                tr_convert<KV, D>(smem, c, a, p, warp - 8);
+            }
+        } else {
+            regs_decrease<X::REGS_LOW>();
+            if (warp == 0) {
+                tr_load<KV, D>(smem, c, a, p, &tmk, &tmv);
+            } else if (warp == 1) {
+                tr_query<KV, D>(smem, c, a, p);
+            } else if (warp == 2) {
+                if (elect_one()) tr_mma<KV, D>(smem, c, a, p, tmem);
+            }
+            __syncwarp();
+        }
+        tc_fence_before_sync();
+        __syncthreads();
+        tc_fence_after_sync();
+    }
+    if (warp == 2) tmem_dealloc(tmem, TR_TMEM);
+    if (threadIdx.x == 0) a.status[blockIdx.x] = c.abort;
+}
+
+// Rows of the cut row tiles from their pieces' partial rows: blockIdx.x is the
+// CTA whose range begins in the row tile; a warp takes 32 rows and eight of their
+// dims, in the order in which the softmax left them.  When a CTA of the first
+// kernel gave up, every row becomes NaN.
+constexpr int TM_WARPS = 8;
+static_assert(32 * TM_WARPS >= AXIS_MAX_CTAS, "a thread per CTA's status");
+
+template <int KV, int D>
+__global__ void __launch_bounds__(32 * TM_WARPS) tree_merge_kernel(const TreeArgs a, int ctas) {
+    using X = Tree<KV, D>;
+    constexpr int UNITS = D / 8;   // warps of 32 rows
+    grid_release();
+    grid_wait();
+    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const int gave_up = threadIdx.x < ctas ? a.status[threadIdx.x] : 0;
+    const Cut cut = a.cuts[cta];
+    const int unit = blockIdx.y * TM_WARPS + (threadIdx.x >> 5), q = unit / UNITS;
+    if (32 * (blockIdx.y * TM_WARPS / UNITS) >= cut.rows && (cta || blockIdx.y)) return;   // the whole block
+    const bool failed = __syncthreads_or(gave_up);
+    const uint32_t nan_pair = X::MK == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u;
+    if (cta == 0 && blockIdx.y == 0) {
+        if (threadIdx.x == 0) a.hdr->error = failed ? PA_ERR_TIMEOUT : PA_OK;
+        if (failed) fill_rows(a.out, 0, (long long)a.num_query_tokens * a.H * (D / 8), nan_pair);
+    }
+    const int m = 32 * q + lane, k4 = unit % UNITS >> 2, j = 2 * (unit & 3);
+    if (failed || m >= cut.rows || cut.pieces <= 1) return;
+    float acc[8], l;
+    join_pieces(
+        cut.pieces, [&](int i) { return a.ml[(long long)piece_slot(cut, cta, i) * X::ROWS + m]; },
+        [&](int i) { return a.o[partial_at<KV, D>(piece_slot(cut, cta, i), q, k4, j, lane)]; },
+        [&](int i) { return a.o[partial_at<KV, D>(piece_slot(cut, cta, i), q, k4, j + 1, lane)]; }, acc, l);
+    const float inv = a.v_scale / l;
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (uint32_t)out_bits<X::MK>(acc[2 * i] * inv) | ((uint32_t)out_bits<X::MK>(acc[2 * i + 1] * inv) << 16);
+    *reinterpret_cast<uint4 *>(a.out + (cut.row0 + a.row_at(m)) * D + 32 * k4 + 4 * j) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// ------------------------------------------------------------------ launch
+
+struct TrLayout {
+    size_t status, cuts, ml, o, total;
+};
+
+TrLayout tr_layout(int D) {
+    TrLayout l;
+    size_t at = 256;   // header
+    auto take = [&](size_t bytes) {
+        const size_t p = at;
+        at = (at + bytes + 255) / 256 * 256;
+        return p;
+    };
+    l.status = take(sizeof(int) * AXIS_MAX_CTAS);
+    l.cuts = take(sizeof(Cut) * AXIS_MAX_CTAS);
+    l.ml = take(sizeof(float2) * 2 * AXIS_MAX_CTAS * TR_MAX_ROWS);
+    l.o = take(sizeof(float) * 2 * AXIS_MAX_CTAS * TR_MAX_ROWS * (size_t)D);
+    l.total = at;
+    return l;
+}
+
+// A cache as [rows = num_blocks * Hkv * bs][D], boxes of 128 bytes by a block's rows.
+bool block_map(CUtensorMap *map, const void *base, long long rows, int D, int bs, int kv) {
+    auto enc = tma_encoder();
+    if (!enc) return false;
+    const bool fp8 = kv == PA_KV_FP8_E4M3;
+    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)D * (fp8 ? 1 : 2)};
+    cuuint32_t box[2] = {fp8 ? 128u : 64u, (cuuint32_t)bs};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                        : kv == PA_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+               2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared-memory limits are set per device, on its first call; the kernel runs
+// only if it was built with the registers that its split assumes (with another
+// count the softmax warps' increase could wait forever).
+template <int KV, int D>
+int tr_setup() {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && done[dev]) return PA_OK;
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(tree_kernel<KV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tree<KV, D>::SMEM) !=
+            cudaSuccess ||
+        cudaFuncGetAttributes(&fa, tree_kernel<KV, D>) != cudaSuccess)
+        return PA_ERR_CUDA;
+    if (fa.numRegs != Tree<KV, D>::REGS_LAUNCH) return PA_ERR_UNSUPPORTED;
+    if (dev < 64) done[dev] = true;
+    return PA_OK;
+}
+
+template <int KV, int D>
+int launch_tree(TreeArgs a, const void *k_cache, const void *v_cache, cudaStream_t st) {
+    using X = Tree<KV, D>;
+    if (const int e = tr_setup<KV, D>()) return e;
+    const long long rows = a.num_blocks * a.Hkv * a.bs;
+    CUtensorMap tmk, tmv;
+    if (!block_map(&tmk, k_cache, rows, D, a.bs, KV) || !block_map(&tmv, v_cache, rows, D, a.bs, KV)) return PA_ERR_CUDA;
+    a.tile_toks = X::ROWS / a.G;
+    const int ctas = std::min(num_sms(), AXIS_MAX_CTAS);
+    if (const int e = launch_early(tree_kernel<KV, D>, dim3((unsigned)ctas), X::THREADS, X::SMEM, st, tmk, tmv, a))
+        return e;
+    const long long most = std::min<long long>(X::ROWS, (long long)a.num_query_tokens * a.G);
+    const dim3 grid((unsigned)ctas, (unsigned)((most + 31) / 32 * (D / 8) / TM_WARPS));
+    return launch_early(tree_merge_kernel<KV, D>, grid, 32 * TM_WARPS, 0, st, a, ctas);
 }
 
 // PA_DEBUG_VALIDATE: lengths, row offsets, block ids and parents.
@@ -145,7 +881,7 @@ extern "C" size_t pa_attention_tree_workspace_size(int num_seqs, int num_query_t
     if (num_seqs < 0 || num_query_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
         num_heads % num_kv_heads != 0 || head_dim <= 0 || max_context_len < 0)
         return 0;
-    return 256;
+    return tr_layout(head_dim).total;
 }
 
 extern "C" int pa_attention_tree(void *out, const void *query, const void *k_cache, const void *v_cache,
@@ -184,18 +920,24 @@ extern "C" int pa_attention_tree(void *out, const void *query, const void *k_cac
     TreeArgs a{};
     a.out = static_cast<uint16_t *>(out);
     a.query = static_cast<const uint16_t *>(query);
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
     a.block_tables = block_tables;
     a.context_lens = context_lens;
     a.query_start = query_start;
     a.parents = parents;
-    a.hdr = static_cast<WsHeader *>(workspace);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const TrLayout lay = tr_layout(head_dim);
+    a.hdr = reinterpret_cast<WsHeader *>(ws);
+    a.status = reinterpret_cast<int *>(ws + lay.status);
+    a.cuts = reinterpret_cast<Cut *>(ws + lay.cuts);
+    a.ml = reinterpret_cast<float2 *>(ws + lay.ml);
+    a.o = reinterpret_cast<float4 *>(ws + lay.o);
     a.num_seqs = num_seqs;
     a.num_query_tokens = num_query_tokens;
-    a.Hq = num_heads;
+    a.H = num_heads;
     a.Hkv = num_kv_heads;
     a.G = G;
+    a.ginv = 65536 / G + 1;
+    a.wait_limit = pipeline_wait_limit();
     a.bs = block_size;
     a.mbps = max_blocks_per_seq;
     a.max_ctx = max_context_len;
@@ -205,8 +947,8 @@ extern "C" int pa_attention_tree(void *out, const void *query, const void *k_cac
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (debug_validate())
         if (const int e = validate_tree(a, st)) return e;
-    if (fp8) return launch_tree<PA_KV_FP8_E4M3, 128>(a, st);
+    if (fp8) return launch_tree<PA_KV_FP8_E4M3, 128>(a, k_cache, v_cache, st);
     if (kv_dtype == PA_KV_BF16)
-        return head_dim == 128 ? launch_tree<PA_KV_BF16, 128>(a, st) : launch_tree<PA_KV_BF16, 64>(a, st);
-    return head_dim == 128 ? launch_tree<PA_KV_F16, 128>(a, st) : launch_tree<PA_KV_F16, 64>(a, st);
+        return head_dim == 128 ? launch_tree<PA_KV_BF16, 128>(a, k_cache, v_cache, st) : launch_tree<PA_KV_BF16, 64>(a, k_cache, v_cache, st);
+    return head_dim == 128 ? launch_tree<PA_KV_F16, 128>(a, k_cache, v_cache, st) : launch_tree<PA_KV_F16, 64>(a, k_cache, v_cache, st);
 }
