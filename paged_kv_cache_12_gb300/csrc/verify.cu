@@ -231,31 +231,33 @@ __device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, c
 
 // What a cluster's CTAs share while they draw a token.
 struct Draw {
-    Sum2 totals[VWARPS];   // this CTA's slices; then, in rank 0, the parts of one
-    Sum2 before;           // rank 0: the sum before the slice that passes
+    Sum2 totals[VWARPS];   // this CTA's slices; then, in the leader, the parts of one
+    Sum2 before;           // the leader's: the sum before the slice that passes
     Height height;
-    int slice;             // rank 0: that slice; -1: no token; -2: no weight at all
+    int slice;             // the leader's: that slice; -1: no token; -2: no weight at all
 };
 
 // Draws a token by the weights w: the smallest whose running sum passes u times
-// the total.  The whole cluster; the token is in *next (in rank 0's shared memory,
-// -1 before) after the cluster's next meeting.  Returns the slice in which it lies,
-// -1 where there is none, or `empty` where the weights sum to zero.
-template <typename T, int VCTAS>
-__device__ __forceinline__ int draw_token(cg::cluster_group &cluster, Draw &sh, int *next, const Weights<T> &w,
-                                          int vocab, const float *u, int empty) {
+// the total.  `ctas` CTAs of the cluster from rank `leader` on do it, all CTAs of the
+// cluster take part in its meetings; the token is in *next (in the leader's shared
+// memory, -1 before) after the cluster's next meeting.  Returns the slice in which it
+// lies, -1 where there is none, or `empty` where the weights sum to zero.
+template <typename T, class Range>
+__device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader, int ctas, Draw &sh, int *next,
+                                          const Weights<T> &w, int vocab, const float *u, int empty, Range range) {
     const int rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int VSLICES = VCTAS * VWARPS;
-    const int len = ((vocab + VSLICES - 1) / VSLICES + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
-    const long long from = (long long)(rank * VWARPS + warp) * len;
+    const int slices = ctas * VWARPS;
+    const int len = ((vocab + slices - 1) / slices + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
+    const int own = (rank - leader) * VWARPS + warp;
+    const long long from = (long long)own * len;
     const int lo = (int)min((long long)vocab, from), hi = (int)min((long long)vocab, from + len);
-    const Sum2 mine = range_sum(w, lo, hi);
+    const Sum2 mine = range(w, lo, hi);
     if (lane == 0) sh.totals[warp] = mine;
     cluster.sync();
-    if (rank == 0 && warp == 0) {   // lane l: slices 2 l and 2 l + 1
+    if (rank == leader && warp == 0) {   // lane l: slices 2 l and 2 l + 1
         Sum2 x0, x1;
-        if (2 * lane < VSLICES) {
-            const Sum2 *src = cluster.map_shared_rank(sh.totals, 2 * lane / VWARPS) + 2 * lane % VWARPS;
+        if (2 * lane < slices) {
+            const Sum2 *src = cluster.map_shared_rank(sh.totals, leader + 2 * lane / VWARPS) + 2 * lane % VWARPS;
             x0 = src[0];
             x1 = src[1];
         }
@@ -289,19 +291,19 @@ __device__ __forceinline__ int draw_token(cg::cluster_group &cluster, Draw &sh, 
         }
         if (lane == 0) sh.slice = slice;
     }
-    cluster.sync();   // rank 0 has read every CTA's totals and decided
-    const int slice = *cluster.map_shared_rank(&sh.slice, 0);
+    cluster.sync();   // the leader has read every CTA's totals and decided
+    const int slice = *cluster.map_shared_rank(&sh.slice, leader);
     if (len <= VBATCH * VCHUNK) {   // short slices: the warp that summed it finds the element
-        if (slice == rank * VWARPS + warp) {
-            const int v = find_in_range(w, lo, hi, *cluster.map_shared_rank(&sh.before, 0),
-                                        *cluster.map_shared_rank(&sh.height, 0));
-            if (lane == 0) *cluster.map_shared_rank(next, 0) = v;
+        if (slice == own) {
+            const int v = find_in_range(w, lo, hi, *cluster.map_shared_rank(&sh.before, leader),
+                                        *cluster.map_shared_rank(&sh.height, leader));
+            if (lane == 0) *cluster.map_shared_rank(next, leader) = v;
         }
-    } else if (rank == 0 && slice >= 0) {   // the slice again, in parts
+    } else if (rank == leader && slice >= 0) {   // the slice again, in parts
         const int first = slice * len, part = (len / VCHUNK + VWARPS - 1) / VWARPS * VCHUNK;
         const int plo = min(vocab, min(first + len, first + warp * part));
         const int phi = min(vocab, min(first + len, plo + part));
-        const Sum2 mine = range_sum(w, plo, phi);
+        const Sum2 mine = range(w, plo, phi);
         if (lane == 0) sh.totals[warp] = mine;
         __syncthreads();
         Sum2 run = sh.before, before = run;
@@ -382,8 +384,9 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         const T *q = failed && a.draft ? static_cast<const T *>(a.draft) + (long long)(d0 + kept) * a.draft_stride : nullptr;
         Weights<T> w(p, q, failed && !a.draft ? a.draft_tokens[d0 + kept] : -1);
         for (int attempt = 0; attempt < 2; ++attempt) {
-            const int slice = draw_token<T, VCTAS>(cluster, draw, &s_next, w, a.vocab, a.sample + seq,
-                                                   attempt == 0 && failed ? -2 : -1);
+            const int slice =
+                draw_token<T>(cluster, 0, VCTAS, draw, &s_next, w, a.vocab, a.sample + seq, attempt == 0 && failed ? -2 : -1,
+                              [](const Weights<T> &x, int lo, int hi) { return range_sum(x, lo, hi); });
             if (slice != -2) break;
             w = Weights<T>(p, nullptr, -1);   // q covers p: draw from p itself
             cluster.sync();   // every CTA has read the decision
@@ -408,58 +411,173 @@ struct TreeVerifyArgs {
     long long target_stride;
 };
 
-// A path through a sequence's tree: a cluster draws a token from the present
-// node's row and goes on to the child that has it.
+// Two sums side by side, each hi + lo in two floats (Sum2 on pairs: seven
+// instructions for two terms).
+struct Sum2Pair {
+    uint64_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(uint64_t s) {
+        const uint64_t minus = pair_of(-1.f, -1.f);
+        const uint64_t t = pair_add(hi, s), b = pair_fma(hi, minus, t);
+        const uint64_t r = pair_add(pair_fma(pair_fma(b, minus, t), minus, hi), pair_fma(b, minus, s));
+        hi = t;
+        lo = pair_add(lo, r);
+    }
+    __device__ __forceinline__ Sum2 sum() const {
+        float h0, h1, l0, l1;
+        pair_parts(hi, h0, h1);
+        pair_parts(lo, l0, l1);
+        Sum2 x{h0, l0};
+        x.add(h1, l1);
+        return x;
+    }
+};
+
+// 16 bytes of a row added as weights (what is negative or NaN counts as zero).
+__device__ __forceinline__ void add16(Sum2Pair &acc, uint4 v, float) {
+    acc.add(pair_of(fmaxf(__uint_as_float(v.x), 0.f), fmaxf(__uint_as_float(v.y), 0.f)));
+    acc.add(pair_of(fmaxf(__uint_as_float(v.z), 0.f), fmaxf(__uint_as_float(v.w), 0.f)));
+}
+__device__ __forceinline__ void add16(Sum2Pair &acc, uint4 v, __nv_bfloat16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        acc.add(pair_of(fmaxf(__uint_as_float(w[k] << 16), 0.f), fmaxf(__uint_as_float(w[k] & 0xffff0000u), 0.f)));
+}
+__device__ __forceinline__ void add16(Sum2Pair &acc, uint4 v, __half) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+        acc.add(pair_of(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f)));
+    }
+}
+
+// range_sum of a row's own weights, with more bytes on their way: 16 at a time
+// from the first 16-byte boundary on, whatever the row's alignment.
+constexpr int VLOADS = 8;
+template <typename T>
+__device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
+    constexpr int E = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+    const int skip = (int)((16 - (reinterpret_cast<uintptr_t>(p + lo) & 15u)) & 15u) / (int)sizeof(T);
+    const int head = min(hi, lo + skip), nvec = (hi - head) / E, tail = head + nvec * E;
+    const uint4 *v = reinterpret_cast<const uint4 *>(p + head);
+    Sum2Pair acc;
+    if (lane < head - lo) acc.add(pair_of(fmaxf(prob(p[lo + lane]), 0.f), 0.f));
+    if (lane < hi - tail) acc.add(pair_of(fmaxf(prob(p[tail + lane]), 0.f), 0.f));
+    for (int i0 = 0; i0 < nvec; i0 += 32 * VLOADS) {
+        uint4 x[VLOADS];
+#pragma unroll
+        for (int k = 0; k < VLOADS; ++k) {
+            const int i = i0 + 32 * k + lane;
+            x[k] = i < nvec ? v[i] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < VLOADS; ++k) add16(acc, x[k], T());
+    }
+    return warp_sum(acc.sum());
+}
+
+// A path through a sequence's tree, by a cluster.  One level after another would
+// cost a row's read and the meetings for each; so the cluster's CTAs draw the
+// tokens of several nodes at a time, the present one's and those of descendants
+// that it may lead to, in groups of as many CTAs each, and then walk as far as
+// those tokens go.  `rows`: nodes of the first such wave (later ones, which few
+// sequences reach, take one a CTA).
 template <typename T, int VCTAS>
 __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESIDENT)
-    verify_tree_kernel(const TreeVerifyArgs a) {
+    verify_tree_kernel(const TreeVerifyArgs a, int rows) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank();
     const int seq = blockIdx.x / VCTAS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ Draw draw;
-    __shared__ int s_next[2];   // by the level's parity: a CTA may still read one level's token while the next is drawn
-    __shared__ int s_node;
+    __shared__ int s_next[2];   // by the wave's parity: a CTA may still read one wave's tokens while the next is drawn
+    __shared__ int s_nodes[VMAX_CTAS], s_count;
+    __shared__ int s_node, s_level;
     grid_release();
     grid_wait();
     const int n0 = a.tree_start[seq], n1 = a.tree_start[seq + 1];
     const bool ok = n0 >= 0 && n1 > n0 && n1 <= a.num_nodes && (seq > 0 || n0 == 0) &&
                     (seq < a.num_seqs - 1 || n1 == a.num_nodes);
     const int n = n1 - n0;
+    const int32_t *parents = a.parents + n0, *drafted = a.node_tokens + n0;
     int32_t *tokens = a.tokens + (long long)seq * (a.max_depth + 1);
     int32_t *path = a.path + (long long)seq * (a.max_depth + 1);
-    int level = -1, node = ok ? 0 : -1;   // the same in every CTA of the cluster
-    while (node >= 0) {
-        ++level;
-        int *next = &s_next[level & 1];
-        if (rank == 0 && threadIdx.x == 0) *next = -1;
-        const Weights<T> w(static_cast<const T *>(a.target) + (long long)(n0 + node) * a.target_stride, nullptr, -1);
-        draw_token<T, VCTAS>(cluster, draw, next, w, a.vocab, a.uniform + n0 + node, -1);
-        cluster.sync();   // the token is there
-        if (warp == 0) {
-            const int v = *cluster.map_shared_rank(next, 0);
-            if (rank == 0 && lane == 0) {
-                tokens[level] = v;
-                path[level] = node;
-            }
-            int child = -1;
-            for (int base = node + 1; v >= 0 && level < a.max_depth && base < n; base += 32) {
-                const int j = base + lane;
-                const unsigned has = __ballot_sync(0xffffffffu, j < n && a.parents[n0 + j] == node &&
-                                                                    a.node_tokens[n0 + j] == v);
-                if (has) {
-                    child = base + __ffs((int)has) - 1;
-                    break;
+    // everything here is the same in every CTA of the cluster
+    int level = 0, node = ok ? 0 : -1;
+    for (int wave = 0; node >= 0; ++wave) {
+        const int most = wave ? VCTAS : rows;
+        if (warp == 0) {   // the present node and the first of its descendants, in the order of their numbers
+            int mine = lane == 0 ? node : -1, count = 1;   // lane i: the i-th of them
+            for (int base = node + 1; count < most && base < n; base += 32) {
+                const int p = base + lane < n ? parents[base + lane] : -1;
+                bool taken = false;
+                for (int i = 0; i < count && count < most; ++i) {   // (a parent comes before its children)
+                    const int node_i = __shfl_sync(0xffffffffu, mine, i);   // (by every lane)
+                    unsigned kids = __ballot_sync(0xffffffffu, !taken && p >= 0 && p == node_i);
+                    if (kids >> lane & 1u) taken = true;
+                    for (; kids && count < most; kids &= kids - 1, ++count)
+                        if (lane == count) mine = base + __ffs((int)kids) - 1;
                 }
             }
-            if (lane == 0) s_node = child;
+            if (lane < count) s_nodes[lane] = mine;
+            if (lane == 0) s_count = count;
+        }
+        int *next = &s_next[wave & 1];
+        if (threadIdx.x == 0) *next = -1;
+        __syncthreads();
+        int groups = 1;
+        while (groups < s_count) groups *= 2;
+        const int ctas = VCTAS / groups, group = rank / ctas, leader = group * ctas;
+        const bool has = group < s_count;   // a group without a node has no row either
+        const int who = has ? s_nodes[group] : node;
+        const T *p = static_cast<const T *>(a.target) + (long long)(n0 + who) * a.target_stride;
+        draw_token<T>(cluster, leader, ctas, draw, next, Weights<T>(p, nullptr, -1), has ? a.vocab : 0, a.uniform + n0 + who,
+                      -1, [](const Weights<T> &x, int lo, int hi) { return row_sum(x.p, lo, hi); });
+        cluster.sync();   // the tokens are there
+        if (warp == 0) {
+            const int count = s_count;
+            const int token = lane < count ? *cluster.map_shared_rank(next, lane * ctas) : -1;
+            const int number = lane < count ? s_nodes[lane] : -1;
+            int at = 0, cur = node, lv = level, go = -1;
+            for (;;) {   // node cur, the at-th of the wave
+                const int v = __shfl_sync(0xffffffffu, token, at);
+                if (rank == 0 && lane == 0) {
+                    tokens[lv] = v;
+                    path[lv] = cur;
+                }
+                int child = -1;
+                for (int base = cur + 1; v >= 0 && lv < a.max_depth && base < n; base += 32) {
+                    const int j = base + lane;
+                    const unsigned has = __ballot_sync(0xffffffffu, j < n && parents[j] == cur && drafted[j] == v);
+                    if (has) {
+                        child = base + __ffs((int)has) - 1;
+                        break;
+                    }
+                }
+                if (child < 0) break;
+                cur = child;
+                ++lv;
+                const unsigned here = __ballot_sync(0xffffffffu, number == child);
+                if (!here) {
+                    go = child;   // drawn in the next wave
+                    break;
+                }
+                at = __ffs((int)here) - 1;
+            }
+            if (lane == 0) {
+                s_node = go;
+                s_level = lv;
+            }
         }
         __syncthreads();
         node = s_node;
+        level = s_level;
     }
     if (rank == 0) {
-        for (int j = level + 1 + (int)threadIdx.x; j <= a.max_depth; j += VTHREADS) tokens[j] = path[j] = -1;
-        if (threadIdx.x == 0) a.accepted[seq] = level;
+        for (int j = (ok ? level + 1 : 0) + (int)threadIdx.x; j <= a.max_depth; j += VTHREADS) tokens[j] = path[j] = -1;
+        if (threadIdx.x == 0) a.accepted[seq] = ok ? level : -1;
     }
     cluster.sync();   // rank 0's shared memory outlives its readers
 }
@@ -478,15 +596,22 @@ int launch_verify(const VerifyArgs &a, cudaStream_t st) {
     return launch_early(verify_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a);
 }
 
-// The same rule.
+// The same rule for the cluster.  The first wave takes as many nodes a sequence (a
+// power of two, at most a CTA each) as keep its reads within VWAVE_BYTES, and no more
+// than a tree has on average.
+constexpr long long VWAVE_BYTES = 64LL << 20;
 template <typename T>
 int launch_verify_tree(const TreeVerifyArgs &a, cudaStream_t st) {
     const long long slots = (long long)num_sms() * VRESIDENT;
     const unsigned b = (unsigned)a.num_seqs;
-    if (b * 8LL <= slots) return launch_early(verify_tree_kernel<T, 8>, dim3(b * 8), VTHREADS, 0, st, a);
-    if (b * 4LL <= slots) return launch_early(verify_tree_kernel<T, 4>, dim3(b * 4), VTHREADS, 0, st, a);
-    if (b * 2LL <= slots) return launch_early(verify_tree_kernel<T, 2>, dim3(b * 2), VTHREADS, 0, st, a);
-    return launch_early(verify_tree_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a);
+    const int ctas = b * 8LL <= slots ? 8 : b * 4LL <= slots ? 4 : b * 2LL <= slots ? 2 : 1;
+    const long long row = (long long)a.num_seqs * a.vocab * (long long)sizeof(T);
+    int rows = 1;
+    while (rows < ctas && 2 * rows * row <= VWAVE_BYTES && (long long)rows * a.num_seqs < a.num_nodes) rows *= 2;
+    if (ctas == 8) return launch_early(verify_tree_kernel<T, 8>, dim3(b * 8), VTHREADS, 0, st, a, rows);
+    if (ctas == 4) return launch_early(verify_tree_kernel<T, 4>, dim3(b * 4), VTHREADS, 0, st, a, rows);
+    if (ctas == 2) return launch_early(verify_tree_kernel<T, 2>, dim3(b * 2), VTHREADS, 0, st, a, rows);
+    return launch_early(verify_tree_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a, rows);
 }
 
 }  // namespace
