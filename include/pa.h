@@ -581,8 +581,8 @@ PA_API int pa_verify_drafts(int32_t *accepted, int32_t *tokens, const void *targ
  *                  query_out included.  (So is one whose slot is past the cache.)
  *   k_cache, v_cache  caches of element type kv_dtype, the layout above; inputs
  *                  and query_out bf16 for PA_KV_BF16, fp16 otherwise
- *   head_dim       a multiple of 8; rope_dim a multiple of 16, at most head_dim
- *                  and at most 512
+ *   head_dim       a multiple of 8, at most 1024; rope_dim a multiple of 16, at
+ *                  most head_dim and at most 512
  *   num_axes       1 .. PA_ROPE_MAX_AXES
  *   k_scale, v_scale  of an FP8 cache, as in pa_kv_write_fp8 (ignored otherwise)
  * Angles in 64 bits up to the turn's fraction, cosines and the rotation in fp32;

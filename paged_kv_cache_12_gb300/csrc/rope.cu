@@ -4,10 +4,9 @@
 // A rotation by angle a takes the pair (x, y) to (x cos a - y sin a,
 // y cos a + x sin a).  The angle of a pair is a position (an integer, one for each
 // axis) times a frequency.  A position of a million times a frequency of one has
-// lost the turn's fraction in 32 bits, so the angle is taken in turns in 64 bits
-// (position * inv_freq / 2 pi), reduced to its fraction exactly, and its sine and
-// cosine computed in 32.  All heads of a token share its angles: a CTA computes
-// them once a token, in shared memory.
+// lost most of the turn's fraction in 32 bits, so the fraction is found with whole
+// numbers of 64 bits, and its sine and cosine in 32.  All heads of a token share its
+// angles: they are computed once a token, in shared memory.
 //
 // Sources: the new token goes into the free slot of the sequence's current block
 // ("PagedAttention : comment optimiser la memoire GPU lors de l'inference des
@@ -22,9 +21,11 @@
 namespace pa {
 namespace {
 
-constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_MAX_DIM = 512;   // rotary elements of a head: a thread per pair
-static_assert(ROPE_MAX_DIM / 2 <= ROPE_THREADS, "a thread per pair");
+constexpr int ROPE_THREADS = 128;
+constexpr int ROPE_DEPTH = 4;       // steps of a thread on their way
+constexpr int ROPE_RESIDENT = 8;    // CTAs of an SM
+constexpr int ROPE_MAX_DIM = 512;   // rotary elements of a head
+constexpr int ROPE_MAX_HEAD = 8 * ROPE_THREADS;   // elements of a head: a thread a piece
 
 struct RopeArgs {
     uint16_t *query_out;
@@ -88,45 +89,161 @@ __device__ __forceinline__ void store_cache(void *cache, long long at, const flo
         *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(cache) + at) = pack8<KV>(x);
 }
 
-// A CTA takes every gridDim-th token.  A thread's piece of work is eight
-// elements of a head, or, where a pair's halves lie rope_dim / 2 apart, eight
-// and their eight partners.
-template <int KV>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_write_kernel(const RopeArgs a) {
-    __shared__ float2 turn[ROPE_MAX_DIM / 2];   // cosine and sine of every pair
+// Where a token's key and value go: its block's first row and its offset in the
+// block as an element offset of kv head 0, or -1 for padding.
+__device__ __forceinline__ long long cache_row(const RopeArgs &a, long long slot) {
+    if (slot < 0 || slot >= a.num_slots) return -1;
+    long long blk, off;
+    if (slot >> 32) {
+        blk = slot / a.block_size;
+        off = slot - blk * a.block_size;
+    } else {
+        const uint32_t q = (uint32_t)slot / (uint32_t)a.block_size;
+        blk = q;
+        off = (uint32_t)slot - q * (uint32_t)a.block_size;
+    }
+    return (blk * a.hk * a.block_size + off) * a.d;
+}
+
+__device__ __forceinline__ void cell_load(uint4 *cell, const uint16_t *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(cell)), "l"(src) : "memory");
+}
+
+// A pair's frequency: the fraction of a turn that a step of its axis makes, in
+// units of 2^-64 turns, so that the fraction after any number of steps is the low
+// 64 bits of a product (off by the roundings of the frequency in turns, 2^-53 of it,
+// times the steps).  axis: -1 where it is out of range or the frequency is not
+// finite.
+struct Frequency {
+    unsigned long long step;
+    int axis;
+    bool back;   // a negative frequency
+};
+__device__ __forceinline__ Frequency frequency(const RopeArgs &a, int pair) {
+    Frequency f;
+    const double turns = (double)a.inv_freq[pair] * 0.15915494309189535;   // 1 / (2 pi)
+    const double size = fabs(turns);
+    f.axis = a.pair_axis ? a.pair_axis[pair] : 0;
+    if (f.axis >= a.num_axes || !(size < 1e300)) f.axis = -1;
+    f.back = turns < 0.0;
+    f.step = f.axis < 0 ? 0ull : (unsigned long long)((size - floor(size)) * 18446744073709551616.0);
+    return f;
+}
+__device__ __forceinline__ float2 cosine_sine(const Frequency &f, int position) {
+    if (f.axis < 0) return make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
+    const unsigned long long turns = f.step * (unsigned long long)(long long)position;
+    float2 cs;
+    sincospif((float)(int)(turns >> 32) * 0x1p-31f, &cs.y, &cs.x);   // in half turns, from -1 to 1
+    if (f.back) cs.y = -cs.y;
+    return cs;
+}
+
+// A CTA takes every gridDim-th token, and a thread a piece of a head of its own --
+// eight elements, and their eight partners where a pair's halves lie rope_dim / 2
+// apart -- in every head that is its turn: so it reads its pairs' cosines and sines
+// once a token.  A thread's pieces of one token after another are one sequence of
+// steps (query heads, key heads, values), whose loads it has on their way ROPE_DEPTH
+// steps ahead, in shared memory cells that no other thread touches: the only thing
+// that the threads wait for one another for is the next token's angles.
+template <int KV, bool INTERLEAVED>
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_RESIDENT) rope_write_kernel(const RopeArgs a) {
+    constexpr int PER = INTERLEAVED ? 4 : 8;            // pairs of a piece that turns
+    constexpr int CELLS = INTERLEAVED ? 1 : 2;          // 16-byte cells of a step
+    __shared__ uint4 cells[ROPE_DEPTH * CELLS][ROPE_THREADS];
+    __shared__ float2 turn[2][ROPE_MAX_DIM / 2];        // cosine and sine of a token's pairs, by the token's parity
     const int pairs = a.rope_dim / 2, tid = threadIdx.x;
-    const int turned = a.interleaved ? a.rope_dim / 8 : a.rope_dim / 16;   // pieces of a head that turn
-    const int pieces = turned + (a.d - a.rope_dim) / 8;                    // of a query or key head
-    const int vecs = a.d / 8;                                              // of a value head
-    const int n_turn = (a.hq + a.hk) * pieces, n_all = n_turn + a.hk * vecs;
+    const int turned = pairs / PER;                     // pieces of a head that turn
+    const int pieces = turned + (a.d - a.rope_dim) / 8; // of a query or key head
+    const int vecs = a.d / 8;                           // of a value head
+    // heads at a time, and this thread's head and piece among them
+    const int heads = ROPE_THREADS / pieces, h0 = tid / pieces, p = tid - h0 * pieces;
+    const int vheads = ROPE_THREADS / vecs, vh0 = tid / vecs, v = tid - vh0 * vecs;
+    const bool some = h0 < heads, vsome = vh0 < vheads;
+    const bool turns = p < turned, two = turns && !INTERLEAVED;
+    const int e = turns ? 8 * p : a.rope_dim + 8 * (p - turned);   // the piece's first element
+    const int nq = (a.hq + heads - 1) / heads, nk = (a.hk + heads - 1) / heads, nv = (a.hk + vheads - 1) / vheads;
+    const int steps = nq + nk + nv;                     // of a token
+    const long long head_rows = (long long)a.block_size * a.d;
+    const int stride = gridDim.x;
     grid_release();
     grid_wait();
-    double per_turn = 0.0;   // this thread's pair: turns for each step of its axis
-    int axis = 0;
-    if (tid < pairs) {
-        per_turn = (double)a.inv_freq[tid] * 0.15915494309189535;   // 1 / (2 pi)
-        if (a.pair_axis) axis = a.pair_axis[tid];
-    }
-    for (int t = blockIdx.x; t < a.num_tokens; t += gridDim.x) {
-        const long long slot = a.slot_mapping[t];
-        if (slot < 0 || slot >= a.num_slots) continue;   // padding (the whole CTA)
-        __syncthreads();   // the last token's angles have been used
-        if (tid < pairs) {
-            float2 cs = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
-            if (axis >= 0 && axis < a.num_axes) {
-                const double x = per_turn * (double)a.positions[(long long)axis * a.num_tokens + t];
-                sincospif(2.f * (float)(x - rint(x)), &cs.y, &cs.x);
-            }
-            turn[tid] = cs;
+    Frequency f0{};
+    if (tid < pairs) f0 = frequency(a, tid);
+    auto position = [&](const Frequency &f, int t) {
+        return f.axis < 0 ? 0 : a.positions[(long long)f.axis * a.num_tokens + t];
+    };
+    auto angles = [&](int t, int place, int pos0) {     // of token t; pos0: this thread's first pair's position
+        if (tid < pairs) turn[place][tid] = cosine_sine(f0, pos0);
+        for (int i = tid + ROPE_THREADS; i < pairs; i += ROPE_THREADS) {   // (rotary parts above 2 ROPE_THREADS)
+            const Frequency f = frequency(a, i);
+            turn[place][i] = cosine_sine(f, position(f, t));
         }
-        __syncthreads();
-        const long long blk = slot / a.block_size, off = slot - blk * a.block_size;
-        for (int i = tid; i < n_all; i += ROPE_THREADS) {
-            if (i >= n_turn) {   // a value's piece
-                const int h = (i - n_turn) / vecs, v = (i - n_turn) - h * vecs;
-                const uint4 raw = *reinterpret_cast<const uint4 *>(a.value + (long long)t * a.value_stride +
-                                                                   (long long)h * a.d + 8 * v);
-                const long long at = ((blk * a.hk + h) * a.block_size + off) * a.d + 8 * v;
+    };
+    // the loads: a cursor ROPE_DEPTH - 1 steps ahead of the work
+    int lt = blockIdx.x, lu = 0, lc = 0;                // its token, step and cell
+    int64_t lslot = a.slot_mapping[lt], lnext = lt + stride < a.num_tokens ? a.slot_mapping[lt + stride] : -1;
+    auto load = [&]() {
+        if (lt < a.num_tokens) {
+            if (lslot >= 0 && lslot < a.num_slots) {    // (padding is not read)
+                const uint16_t *src;
+                bool mine, pair = two;
+                if (lu < nq) {
+                    const int h = h0 + lu * heads;
+                    mine = some && h < a.hq;
+                    src = a.query + (long long)lt * a.query_stride + h * a.d + e;
+                } else if (lu < nq + nk) {
+                    const int h = h0 + (lu - nq) * heads;
+                    mine = some && h < a.hk;
+                    src = a.key + (long long)lt * a.key_stride + h * a.d + e;
+                } else {
+                    const int h = vh0 + (lu - nq - nk) * vheads;
+                    mine = vsome && h < a.hk;
+                    src = a.value + (long long)lt * a.value_stride + h * a.d + 8 * v;
+                    pair = false;
+                }
+                if (mine) {
+                    cell_load(&cells[lc * CELLS][tid], src);
+                    if (CELLS == 2 && pair) cell_load(&cells[lc * CELLS + CELLS - 1][tid], src + pairs);
+                }
+            }
+            if (++lu == steps) {
+                lu = 0;
+                lt += stride;
+                lslot = lnext;
+                lnext = lt + stride < a.num_tokens ? a.slot_mapping[lt + stride] : -1;
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        lc = (lc + 1) % ROPE_DEPTH;
+    };
+#pragma unroll 1
+    for (int i = 0; i < ROPE_DEPTH - 1; ++i) load();
+    const int t00 = blockIdx.x;
+    angles(t00, 0, tid < pairs ? position(f0, t00) : 0);
+    int pos = tid < pairs && t00 + stride < a.num_tokens ? position(f0, t00 + stride) : 0;   // of the next token
+    int64_t slot = a.slot_mapping[t00];
+    int c = 0, place = 0;
+    __syncthreads();
+    for (int t = t00; t < a.num_tokens; t += stride, place ^= 1) {
+        const long long row = cache_row(a, slot);
+        if (t + stride < a.num_tokens) {
+            angles(t + stride, place ^ 1, pos);
+            slot = a.slot_mapping[t + stride];
+            if (tid < pairs && t + 2LL * stride < a.num_tokens) pos = position(f0, t + 2 * stride);
+        }
+        float2 cs[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) cs[k] = turns ? turn[place][PER * p + k] : make_float2(1.f, 0.f);
+#pragma unroll 1
+        for (int u = 0; u < steps; ++u, c = (c + 1) % ROPE_DEPTH) {
+            load();
+            asm volatile("cp.async.wait_group %0;" ::"n"(ROPE_DEPTH - 1) : "memory");
+            if (row < 0) continue;
+            if (u >= nq + nk) {   // a value's piece
+                const int h = vh0 + (u - nq - nk) * vheads;
+                if (!vsome || h >= a.hk) continue;
+                const uint4 raw = cells[c * CELLS][tid];
+                const long long at = row + h * head_rows + 8 * v;
                 if constexpr (KV == PA_KV_FP8_E4M3) {
                     float x[8];
                     unpack8<KV>(raw, x);
@@ -136,51 +253,48 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_write_kernel(const RopeArgs
                 }
                 continue;
             }
-            const int head = i / pieces, p = i - head * pieces;
-            const bool is_key = head >= a.hq;
-            const int h = is_key ? head - a.hq : head;
-            const uint16_t *src = is_key ? a.key + (long long)t * a.key_stride + (long long)h * a.d
-                                         : a.query + (long long)t * a.query_stride + (long long)h * a.d;
-            // first element of the piece, and of its partner's
-            const int e = p < turned ? 8 * p : a.rope_dim + 8 * (p - turned);
-            const bool two = p < turned && !a.interleaved;
+            const int h = h0 + (u < nq ? u : u - nq) * heads;
+            if (!some || h >= (u < nq ? a.hq : a.hk)) continue;
             float x[8], y[8];
-            unpack8<KV>(*reinterpret_cast<const uint4 *>(src + e), x);
-            if (two) {
-                unpack8<KV>(*reinterpret_cast<const uint4 *>(src + e + pairs), y);
+            unpack8<KV>(cells[c * CELLS][tid], x);
+            if (INTERLEAVED) {
+                if (turns)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 r = cs[k];
+                        const float m = x[2 * k], w = x[2 * k + 1];
+                        x[2 * k] = fmaf(m, r.x, -(w * r.y));
+                        x[2 * k + 1] = fmaf(w, r.x, m * r.y);
+                    }
+            } else if (two) {
+                unpack8<KV>(cells[c * CELLS + CELLS - 1][tid], y);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float2 cs = turn[e + k];
-                    const float u = x[k], w = y[k];
-                    x[k] = fmaf(u, cs.x, -(w * cs.y));
-                    y[k] = fmaf(w, cs.x, u * cs.y);
-                }
-            } else if (p < turned) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 cs = turn[e / 2 + k];
-                    const float u = x[2 * k], w = x[2 * k + 1];
-                    x[2 * k] = fmaf(u, cs.x, -(w * cs.y));
-                    x[2 * k + 1] = fmaf(w, cs.x, u * cs.y);
+                    const float2 r = cs[k % PER];
+                    const float m = x[k], w = y[k];
+                    x[k] = fmaf(m, r.x, -(w * r.y));
+                    y[k] = fmaf(w, r.x, m * r.y);
                 }
             }
-            if (is_key) {
-                const long long at = ((blk * a.hk + h) * a.block_size + off) * a.d + e;
+            if (u < nq) {
+                uint16_t *to = a.query_out + (long long)t * a.query_out_stride + h * a.d + e;
+                *reinterpret_cast<uint4 *>(to) = pack8<KV>(x);
+                if (two) *reinterpret_cast<uint4 *>(to + pairs) = pack8<KV>(y);
+            } else {
+                const long long at = row + h * head_rows + e;
                 store_cache<KV>(a.k_cache, at, x, a.kinv);
                 if (two) store_cache<KV>(a.k_cache, at + pairs, y, a.kinv);
-            } else {
-                uint16_t *dst = a.query_out + (long long)t * a.query_out_stride + (long long)h * a.d + e;
-                *reinterpret_cast<uint4 *>(dst) = pack8<KV>(x);
-                if (two) *reinterpret_cast<uint4 *>(dst + pairs) = pack8<KV>(y);
             }
         }
+        __syncthreads();   // the next token's angles are there, and this one's have been read
     }
 }
 
 template <int KV>
 int launch_rope(const RopeArgs &a, cudaStream_t st) {
-    const int ctas = std::min(a.num_tokens, 8 * num_sms());
-    return launch_early(rope_write_kernel<KV>, dim3((unsigned)ctas), ROPE_THREADS, 0, st, a);
+    const dim3 ctas((unsigned)std::min(a.num_tokens, ROPE_RESIDENT * num_sms()));
+    return a.interleaved ? launch_early(rope_write_kernel<KV, true>, ctas, ROPE_THREADS, 0, st, a)
+                         : launch_early(rope_write_kernel<KV, false>, ctas, ROPE_THREADS, 0, st, a);
 }
 
 }  // namespace
@@ -203,7 +317,7 @@ extern "C" int pa_kv_write_rope(void *query_out, const void *query, const void *
         (!std::isfinite(k_scale) || !(k_scale > 0.f) || !std::isfinite(v_scale) || !(v_scale > 0.f)))
         return PA_ERR_INVALID_ARG;
     // a token's pieces of work are counted in 32 bits
-    if (rope_dim > ROPE_MAX_DIM || (long long)(num_heads + 2LL * num_kv_heads) * head_dim >= (1LL << 30))
+    if (rope_dim > ROPE_MAX_DIM || head_dim > ROPE_MAX_HEAD || (long long)(num_heads + 2LL * num_kv_heads) * head_dim >= (1LL << 30))
         return PA_ERR_UNSUPPORTED;
     const long long q_row = (long long)num_heads * head_dim, k_row = (long long)num_kv_heads * head_dim;
     if (query_stride < q_row || query_out_stride < q_row || key_stride < k_row || value_stride < k_row ||
