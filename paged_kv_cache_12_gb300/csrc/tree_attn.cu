@@ -213,11 +213,12 @@ __device__ void tr_load(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeAr
         const TrPiece x = piece_of(a, p);
         const uint64_t policy = p.w.per_head > 1 ? again : once;
         const int32_t *table = a.block_tables + (long long)p.seq * a.mbps;
-        // this lane's row coordinate in tile t (-1: the context ends before its block)
-        auto row_of = [&](int t) {
-            const int pos = t * TR_TOK + lane * a.bs;
-            if (lane >= boxes || pos >= p.w.L) return -1;
-            long long id = table[pos / a.bs];
+        const int per_tile = TR_TOK / a.bs, blocks = (p.w.L - 1) / a.bs + 1;
+        // the id of this lane's block in tile t (read a tile ahead of its use), and its
+        // row coordinate (-1: the context ends before the block)
+        auto id_of = [&](int t) { return lane < boxes && t * per_tile + lane < blocks ? table[t * per_tile + lane] : 0; };
+        auto row_of = [&](int t, long long id) {
+            if (lane >= boxes || t * per_tile + lane >= blocks) return -1;
             if (id < 0 || id >= a.num_blocks) {
                 c.bad[p.local % TR_MARKS] = p.local + 1;
                 id = 0;
@@ -238,12 +239,13 @@ __device__ void tr_load(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeAr
             }
             ++cnt;
         };
-        int row = row_of(p.t0);
+        int row = row_of(p.t0, id_of(p.t0)), id = p.t0 + 1 < p.t1 ? id_of(p.t0 + 1) : 0;
         load(tmk, row);
         for (int t = p.t0; wait.ok && t < p.t1; ++t) {
             int next = -1;
             if (t + 1 < p.t1) {
-                next = row_of(t + 1);
+                next = row_of(t + 1, id);
+                if (t + 2 < p.t1) id = id_of(t + 2);
                 load(tmk, next);
             }
             if (wait.ok) load(tmv, row);
