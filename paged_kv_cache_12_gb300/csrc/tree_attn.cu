@@ -120,40 +120,39 @@ struct Tree {
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_STAGE = OFF_RING + RING * TILE;
     static constexpr int OFF_CTRL = OFF_STAGE + STAGES * CODES;
-    static constexpr int CTRL = 2048;
-    static constexpr int SMEM = OFF_CTRL + CTRL + 1024;    // + alignment slack
+    static constexpr int CTRL = 3072;
+    static constexpr int SMEM = OFF_CTRL + CTRL;
     static constexpr int THREADS = F8 ? 512 : 384;
     static constexpr int REGS_LAUNCH = F8 ? 128 : 168;     // per thread: 65536 / threads, rounded down to 8
-    static constexpr int REGS_LOW = F8 ? 80 : 104;         // warps 0 - 3
-    static constexpr int REGS_HIGH = F8 ? 208 : 200;       // the softmax warps
-    static constexpr int REGS_CONV = 112;                  // the converting warps
-    static constexpr int CONV_WARPS = 8;
+    static constexpr int REGS_LOW = F8 ? 56 : 104;         // warps 0 - 3
+    static constexpr int REGS_HIGH = F8 ? 176 : 200;       // the softmax warps
+    static constexpr int REGS_CONV = 104;                  // the converting warps
+    static constexpr int CONV_WARPS = 4;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
-    static_assert(128 * (REGS_LOW + (F8 ? REGS_HIGH + 2 * REGS_CONV : 2 * REGS_HIGH)) <= THREADS * REGS_LAUNCH,
+    static_assert(128 * (REGS_LOW + 2 * REGS_HIGH + (F8 ? REGS_CONV : 0)) <= THREADS * REGS_LAUNCH,
                   "register split within the launch's pool");
 };
 constexpr int TR_TMEM = 512, TR_O = 256;   // S0, S1 at columns 0 and 128; O0, O1 at 256 and 384
 constexpr int TR_MAX_RING = 10, TR_MAX_STAGES = 4;
 constexpr int TR_MARKS = 16;               // pieces whose tiles can be on their way, and more
 constexpr int TR_SEEN = PA_TREE_MAX_NODES / 32;
+static_assert(2 * TR_SEEN == TR_MARKS, "set up by the same threads");
 
 struct TrCtrl {
     uint64_t full[TR_MAX_RING], empty[TR_MAX_RING], stfull[TR_MAX_STAGES], stempty[TR_MAX_STAGES];
     uint64_t qfull[2], qempty[2];
-    // one half: by S buffer; two halves: by half.  Two sets, so that the second
-    // half's warps, which one-half pieces do not concern, see every phase of theirs.
-    uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];
+    uint64_t sfull[2], pfull[2], pvdone[2];   // of either S buffer
+    uint64_t meet[2];       // of all softmax warps, at a piece's end and after it
     uint64_t done;
     uint32_t tmem;
     int abort;
     Plan plan;
     long long warp_sums[16];
     int bad[TR_MARKS];      // 1 + the number of a piece that met a block id out of range
-    // Nodes whose values are not finite, as the first half's warps find them (a set
-    // each), for the piece's own rows and, of the pieces of two halves, for the
-    // second half's.  By the piece's parity: a warp begins the piece after next only
-    // when all warps are through with this one.
-    uint32_t poison[2][2][4][TR_SEEN];
+    // Nodes whose values are not finite, as the softmax warps find them, by the
+    // piece's parity (the next piece's set is emptied between the two meetings).
+    uint32_t poison[2][TR_SEEN];
+    float2 ml[2][TR_HALF];  // a row's maximum and sum over either parity's tiles
 };
 
 // Where the softmax keeps four dims (32 k + 4 j ..) of a row, in float4: a store
@@ -353,9 +352,18 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
         if (!ok) *abort_flag = 1;
         return ok;
     };
-    int cnt = 0, qc[2] = {0, 0}, sel = 0;          // ring tiles before this piece; queries taken; the next buffer of one half
-    int pc[2] = {0, 0}, pc2 = 0;                   // P tiles taken: of each buffer; of each half
-    auto ring_wait = [&](int k) { return wait(&c.full[k % X::RING], (uint32_t)((k / X::RING) & 1)); };
+    int cnt = 0, qc[2] = {0, 0}, sel = 0;   // ring tiles before this piece; queries taken; the next buffer of one half
+    int pc[2] = {0, 0};                     // P tiles taken, of either buffer
+    auto ring_wait = [&](int k) {
+        const bool got = wait(&c.full[k % X::RING], (uint32_t)((k / X::RING) & 1));
+        tc_fence_after_sync();
+        return got;
+    };
+    auto p_wait = [&](int b) {
+        const bool got = wait(&c.pfull[b], (uint32_t)(pc[b]++ & 1));
+        tc_fence_after_sync();
+        return got;
+    };
     auto release = [&](int k) { umma_commit(smem_u32(&c.empty[k % X::RING])); };
     // S in buffer b = the queries of buffer q times the key tile at k
     auto issue_s = [&](int b, int q, int k) {
@@ -366,51 +374,48 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
             for (int j = 0; j < 4; ++j)
                 umma_f16(tmem + b * TR_TOK, dq + h * (X::BLOCK >> 4) + 2 * j, dk + h * (X::BLOCK >> 4) + 2 * j, ID_S,
                          h > 0 || j > 0 ? 1u : 0u);
+        umma_commit(smem_u32(&c.sfull[b]));
     };
-    // O_o += P in buffer b times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
-    auto issue_pv = [&](int b, int o, int k, int n) {
+    // O_b += P_b times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
+    auto issue_pv = [&](int b, int k, bool first) {
         const uint64_t dv = dv0 + (uint64_t)(k % X::RING * (X::TILE >> 4));
 #pragma unroll
         for (int j = 0; j < TR_TOK / 16; ++j)
-            umma_f16_ts(tmem + TR_O + o * 128, tmem + b * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4), ID_O,
-                        n > 0 || j > 0 ? 1u : 0u);
+            umma_f16_ts(tmem + TR_O + b * 128, tmem + b * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4), ID_O,
+                        !first || j > 0 ? 1u : 0u);
+        umma_commit(smem_u32(&c.pvdone[b]));
     };
     while (ok && p.next()) {
         const TrPiece x = piece_of(a, p);
         const int N = x.n;
-        if (!x.two) {
-            if (!wait(&c.qfull[sel], (uint32_t)(qc[sel]++ & 1)) || !ring_wait(cnt)) break;
-            tc_fence_after_sync();
-            issue_s(0, sel, cnt);
-            umma_commit(smem_u32(&c.sfull[0][0]));
-            release(cnt);
-            if (N == 1) umma_commit(smem_u32(&c.qempty[sel]));
-            for (int n = 0; n < N; ++n) {
-                const int b = n & 1, v = cnt + v_at(n, N);
-                if (n + 1 < N) {   // buffer b ^ 1: its P has been taken by PV(n - 1)
-                    const int k = cnt + k_at(n + 1);
-                    if (!ring_wait(k)) break;
-                    tc_fence_after_sync();
-                    issue_s(b ^ 1, sel, k);
-                    umma_commit(smem_u32(&c.sfull[0][b ^ 1]));
-                    release(k);
-                    if (n + 2 == N) umma_commit(smem_u32(&c.qempty[sel]));
-                }
-                if (!wait(&c.pfull[0][b], (uint32_t)(pc[b]++ & 1)) || !ring_wait(v)) break;
-                tc_fence_after_sync();
-                issue_pv(b, 0, v, n);
-                umma_commit(smem_u32(&c.pvdone[0][b]));
+        if (!x.two) {   // tile n in buffer n & 1
+            if (!wait(&c.qfull[sel], (uint32_t)(qc[sel]++ & 1))) break;
+            for (int n = 0; n < min(N, 2); ++n) {
+                const int k = cnt + k_at(n);
+                if (!ring_wait(k)) break;
+                issue_s(n, sel, k);
+                release(k);
+                if (n + 1 == N) umma_commit(smem_u32(&c.qempty[sel]));
+            }
+            for (int n = 0; ok && n < N; ++n) {
+                const int b = n & 1, v = cnt + v_at(n, N), k = cnt + k_at(n + 2);
+                if (!p_wait(b) || !ring_wait(v)) break;
+                issue_pv(b, v, n < 2);
                 release(v);
+                if (n + 2 < N) {
+                    if (!ring_wait(k)) break;
+                    issue_s(b, sel, k);
+                    release(k);
+                    if (n + 3 == N) umma_commit(smem_u32(&c.qempty[sel]));
+                }
             }
             sel ^= 1;
-        } else {
+        } else {        // half h in buffer h
             if (!wait(&c.qfull[0], (uint32_t)(qc[0]++ & 1)) || !wait(&c.qfull[1], (uint32_t)(qc[1]++ & 1)) ||
                 !ring_wait(cnt))
                 break;
-            tc_fence_after_sync();
             for (int h = 0; h < 2; ++h) {
                 issue_s(h, h, cnt);
-                umma_commit(smem_u32(&c.sfull[1][h]));
                 if (N == 1) umma_commit(smem_u32(&c.qempty[h]));
             }
             release(cnt);
@@ -418,21 +423,16 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                 const bool more = n + 1 < N;
                 const int v = cnt + v_at(n, N), k = cnt + k_at(n + 1);
                 for (int h = 0; h < 2; ++h) {
-                    if (!wait(&c.pfull[1][h], (uint32_t)(pc2 & 1)) || (h == 0 && !ring_wait(v))) break;
-                    tc_fence_after_sync();
-                    issue_pv(h, h, v, n);
-                    umma_commit(smem_u32(&c.pvdone[1][h]));
+                    if (!p_wait(h) || (h == 0 && !ring_wait(v))) break;
+                    issue_pv(h, v, n == 0);
                     if (h == 1) release(v);
                     if (more) {
                         if (h == 0 && !ring_wait(k)) break;
-                        tc_fence_after_sync();
                         issue_s(h, h, k);
-                        umma_commit(smem_u32(&c.sfull[1][h]));
                         if (n + 2 == N) umma_commit(smem_u32(&c.qempty[h]));
                         if (h == 1) release(k);
                     }
                 }
-                ++pc2;
             }
         }
         cnt += 2 * N;
@@ -442,54 +442,51 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
     mbar_wait_bounded(smem_u32(&c.done), 0, WAIT_LIMIT);
 }
 
-// One warpgroup: the softmax of half x, a row per thread.
+// One warpgroup: the softmax of S buffer x, a row per thread.
 template <int KV, int D>
 __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_t tmem, int x) {
     using X = Tree<KV, D>;
     constexpr int MK = X::MK;
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, m = quarter * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t ocol = (uint32_t)(TR_O + x * 128);
+    const uint32_t scol = (uint32_t)(x * TR_TOK), ocol = (uint32_t)(TR_O + x * 128);
     const float sl2 = a.scale_log2;
     WarpWait wait{c, a.wait_limit};
-    int sc[2] = {0, 0}, sc2 = 0, cnt = 0;   // S and P so far, of each buffer and of each half; ring tiles before this piece
-    int both = -1;                          // number of the last piece of two halves
+    int sc = 0, cnt = 0, met = 0;   // S and P so far; ring tiles and pieces before this piece
+    auto meet = [&](int k) {        // all softmax warps
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.meet[k]));
+        const bool got = wait(&c.meet[k], (uint32_t)(met & 1));
+        tc_fence_after_sync();
+        return got;
+    };
     while (wait.ok && p.next()) {
         const TrPiece pc = piece_of(a, p);
-        const int N = pc.n;
-        if (pc.two) ++both;
-        if (!pc.two && x == 1) {
-            cnt += 2 * N;
-            continue;
-        }
+        const int N = pc.n, first = pc.two ? 0 : x, by = pc.two ? 1 : 2;   // this warpgroup's tiles
         const int mm = pc.two ? x * TR_HALF + m : m;   // row of the row tile
         const bool mine = mm < pc.rows;
         const bool idle = !__any_sync(0xffffffffu, mine);
         const int node = pc.node0 + (mm * a.ginv >> 16);
         const int ctx = p.w.L - p.w.T;                 // positions before the tree
         const int32_t *parents = a.parents + p.w.q0;
+        uint32_t *poison = c.poison[p.local & 1];
         float mrun = -INFINITY, l = 0.f;
         bool lost = false;                             // the chain of parents is broken
-        for (int n = 0; n < N; ++n) {
-            const int b = pc.two ? x : n & 1, set = pc.two ? 1 : 0, times = pc.two ? sc2 : sc[b];
-            if (!wait(&c.sfull[set][b], (uint32_t)(times & 1))) break;
-            // (every phase is seen, so that one waited for later is not taken for another)
-            if (n > (pc.two ? 0 : 1) && !wait(&c.pvdone[set][b], (uint32_t)((times - 1) & 1))) break;
-            if (n == 0 && x == 0 && lane < TR_SEEN) {
-                c.poison[0][p.local & 1][quarter][lane] = 0;
-                if (pc.two) c.poison[1][both & 1][quarter][lane] = 0;
-            }
-            __syncwarp();
+        for (int n = first; n < N; n += by) {
+            if (!wait(&c.sfull[x], (uint32_t)(sc & 1))) break;
+            // (done when S is; every phase is seen, so that the one waited for last is not taken for another)
+            if (n > first && !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1))) break;
             tc_fence_after_sync();
             const int t0 = (p.t0 + n) * TR_TOK;
-            const bool tail = ctx - t0 < TR_TOK;         // the tree's positions begin before the tile ends
+            const bool tail = ctx - t0 < TR_TOK;       // the tree's positions begin before the tile ends
             bool changed = false;
-            if (tail && x == 0) {
+            if (tail && (x == 0 || !pc.two)) {
                 // Value rows that some row of the row tile does not see, where P is 0
                 // and a product with an infinity or a NaN would not be: those behind the
                 // context are zeroed, and so is what is not finite among the nodes' (the
-                // rows that see it become NaN below).  The first half's warps do it for
-                // both: PV1(n) is issued after P0(n).
+                // rows that see it become NaN below).  Of two halves the first one's
+                // warps do it for both: PV1(n) is issued after P0(n).
                 const int at = cnt + v_at(n, N);
                 if (!wait(&c.full[at % X::RING], (uint32_t)((at / X::RING) & 1))) break;
                 const int lo = max(0, ctx - t0), hi = p.w.L - t0;
@@ -506,8 +503,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                             v = make_uint4(finite_part<MK>(v.x), finite_part<MK>(v.y), finite_part<MK>(v.z),
                                            finite_part<MK>(v.w));
                             const int bad = t0 + r - ctx;
-                            atomicOr(&c.poison[0][p.local & 1][quarter][bad >> 5], 1u << (bad & 31));
-                            if (pc.two) atomicOr(&c.poison[1][both & 1][quarter][bad >> 5], 1u << (bad & 31));
+                            atomicOr(&poison[bad >> 5], 1u << (bad & 31));
                         }
                     }
                 }
@@ -518,7 +514,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
 #pragma unroll
                 for (int q = 0; q < TR_TOK / 32; ++q) {
                     uint32_t r[32];
-                    tmem_ld32(trow + b * TR_TOK + 32 * q, r);
+                    tmem_ld32(trow + scol + 32 * q, r);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) s[32 * q + k] = __uint_as_float(r[k]);
                 }
@@ -557,10 +553,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                 if (__any_sync(0xffffffffu, grow)) {
                     const float nm = grow ? mx : mrun;
                     const float alpha = grow ? fast_exp2(mrun - nm) : 1.f;
-                    if (n > 0) {
-                        // two halves: PV(n - 1) is complete, S(n) was issued after it
-                        if (!pc.two && !wait(&c.pvdone[0][b ^ 1], (uint32_t)((sc[b ^ 1] - 1) & 1))) break;
-                        tc_fence_after_sync();
+                    if (n > first) {   // the last PV into O is complete: S(n) was issued after it
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
                             uint32_t o[32];
@@ -592,7 +585,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                         lp[k & 3] = pair_add(lp[k & 3], pair_of(e0, e1));
                         r[k] = pack_p<MK>(e0, e1);
                     }
-                    tmem_st32(trow + b * TR_TOK + 32 * q, r);
+                    tmem_st32(trow + scol + 32 * q, r);
                 }
                 float l0, l1;
                 pair_parts(pair_add(pair_add(lp[0], lp[1]), pair_add(lp[2], lp[3])), l0, l1);
@@ -602,62 +595,82 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
             if (changed) fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();   // one arrival a warp: 32 atomics on one word hold up the shared-memory pipe
-            if (lane == 0) mbar_arrive(smem_u32(&c.pfull[set][b]));
-            if (pc.two) ++sc2; else ++sc[b];
+            if (lane == 0) mbar_arrive(smem_u32(&c.pfull[x]));
+            ++sc;
         }
-        if (!wait.ok) break;
-        // the last products (and, with one half, those before them)
-        if (pc.two) {
-            if (!wait(&c.pvdone[1][x], (uint32_t)((sc2 - 1) & 1))) break;
-        } else {
-            const int b = (N - 1) & 1;
-            if (N > 1 && !wait(&c.pvdone[0][b ^ 1], (uint32_t)((sc[b ^ 1] - 1) & 1))) break;
-            if (!wait(&c.pvdone[0][b], (uint32_t)((sc[b] - 1) & 1))) break;
-        }
+        if (!wait.ok || (first < N && !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1)))) break;
         cnt += 2 * N;
-        if (idle) continue;
-        tc_fence_after_sync();
         // ---- the piece's rows: finished, or a partial row
-        const volatile uint32_t(*poison)[TR_SEEN] = x == 0 ? c.poison[0][p.local & 1] : c.poison[1][both & 1];
-        uint32_t any = 0;
-        if (lane < TR_SEEN) any = poison[0][lane] | poison[1][lane] | poison[2][lane] | poison[3][lane];
-        if (__any_sync(0xffffffffu, any != 0))
-            for (int j = mine && !lost ? node : -1; j >= 0;) {
-                const int w = j >> 5;
-                if ((poison[0][w] | poison[1][w] | poison[2][w] | poison[3][w]) >> (j & 31) & 1u) lost = true;
-                const int up = parents[j];   // (in order: a piece with such nodes has walked the chain)
-                j = lost || up >= j ? -1 : up;
-            }
-        if (*reinterpret_cast<volatile int *>(&c.bad[p.local % TR_MARKS]) == p.local + 1) lost = true;
         if (lost) l = __int_as_float(0x7fc00000);
-        const bool whole = p.whole();
-        if (!whole && mine) a.ml[(long long)p.slot() * X::ROWS + mm] = make_float2(mrun, l);
-        const float inv = a.v_scale / l;
-        uint16_t *orow = a.out + (a.first_row(p.w, p.r) + a.row_at(mm)) * D;
-#pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(trow + ocol + 32 * q, o);
-            tmem_wait_ld();
-            if (mine && whole) {
-#pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = (uint32_t)out_bits<MK>(__uint_as_float(o[k + 2 * i]) * inv) |
-                               ((uint32_t)out_bits<MK>(__uint_as_float(o[k + 2 * i + 1]) * inv) << 16);
-                    *reinterpret_cast<uint4 *>(orow + 32 * q + k) = make_uint4(w[0], w[1], w[2], w[3]);
+        c.ml[x][m] = make_float2(mrun, l);
+        if (!meet(0)) break;
+        if (x == 0 && threadIdx.x % 128 < TR_SEEN) c.poison[(p.local & 1) ^ 1][threadIdx.x % 128] = 0;
+        if (!idle) {
+            const float2 other = c.ml[x ^ 1][m];
+            const uint32_t any = lane < TR_SEEN ? *reinterpret_cast<volatile uint32_t *>(&poison[lane]) : 0u;
+            bool nan = *reinterpret_cast<volatile int *>(&c.bad[p.local % TR_MARKS]) == p.local + 1;
+            if (__any_sync(0xffffffffu, any != 0))
+                for (int j = mine ? node : -1; j >= 0;) {
+                    if (*reinterpret_cast<volatile uint32_t *>(&poison[j >> 5]) >> (j & 31) & 1u) nan = true;
+                    const int up = parents[j];
+                    j = up >= j ? -1 : up;   // (a broken chain has made its row NaN)
                 }
-            } else if (mine) {
-#pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                    *reinterpret_cast<uint4 *>(a.o + partial_at<KV, D>(p.slot(), mm / 32, q, k / 4, lane)) =
-                        make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            // one half: the tiles of both parities joined, each warpgroup half of the dims
+            const bool join = !pc.two && N > 1;
+            float wa = 1.f, wb = 0.f;
+            if (!pc.two) {
+                const float2 ma = x == 0 ? make_float2(mrun, l) : other, mb = x == 0 ? other : make_float2(mrun, l);
+                mrun = fmaxf(ma.x, mb.x);
+                const float mu = mrun == -INFINITY ? 0.f : mrun;
+                wa = fast_exp2(ma.x - mu);
+                wb = fast_exp2(mb.x - mu);
+                l = ma.y * wa + mb.y * wb;
             }
-            __syncwarp();   // the next load is the whole warp's
+            if (nan) l = __int_as_float(0x7fc00000);
+            const bool whole = p.whole();
+            if (!whole && mine && (pc.two || x == 0)) a.ml[(long long)p.slot() * X::ROWS + mm] = make_float2(mrun, l);
+            const float out = whole ? a.v_scale / l : 1.f;
+            wa *= out;
+            wb *= out;
+            uint16_t *orow = a.out + (a.first_row(p.w, p.r) + a.row_at(mm)) * D;
+            const int q0 = pc.two ? 0 : x * (D / 64), q1 = pc.two ? D / 32 : q0 + D / 64;
+#pragma unroll 1
+            for (int q = q0; q < q1; ++q) {
+                uint32_t o[32];
+                tmem_ld32(trow + (pc.two ? ocol : (uint32_t)TR_O) + 32 * q, o);
+                if (join) {
+                    uint32_t o2[32];
+                    tmem_ld32(trow + TR_O + 128 + 32 * q, o2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = __float_as_uint(fmaf(__uint_as_float(o2[k]), wb, __uint_as_float(o[k]) * wa));
+                } else {
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * wa);
+                }
+                if (mine && whole) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = (uint32_t)out_bits<MK>(__uint_as_float(o[k + 2 * i])) |
+                                   ((uint32_t)out_bits<MK>(__uint_as_float(o[k + 2 * i + 1])) << 16);
+                        *reinterpret_cast<uint4 *>(orow + 32 * q + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else if (mine) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<uint4 *>(a.o + partial_at<KV, D>(p.slot(), mm / 32, q, k / 4, lane)) =
+                            make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                }
+                __syncwarp();   // the next load is the whole warp's
+            }
         }
-        tc_fence_before_sync();
+        if (!meet(1)) break;   // (both O's have been read, the marks and sums too)
+        ++met;
     }
 }
 
@@ -665,11 +678,15 @@ template <int KV, int D>
 __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const TreeArgs a) {
     using X = Tree<KV, D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     TrCtrl &c = *reinterpret_cast<TrCtrl *>(smem + X::OFF_CTRL);
     static_assert(sizeof(TrCtrl) <= X::CTRL, "control block");
     const int warp = threadIdx.x >> 5;
+    if ((smem_u32(smem) & 1023u) != 0) {   // tiles lie on 1024-byte boundaries (they do: nothing else is in shared memory)
+        grid_wait();
+        if (threadIdx.x == 0) a.status[blockIdx.x] = 1;
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < X::RING; ++s) {
             mbar_init(smem_u32(&c.full[s]), X::F8 ? X::CONV_WARPS : 1);
@@ -682,11 +699,10 @@ __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c.qfull[b]), 1);
             mbar_init(smem_u32(&c.qempty[b]), 1);
-            for (int h = 0; h < 2; ++h) {
-                mbar_init(smem_u32(&c.sfull[b][h]), 1);
-                mbar_init(smem_u32(&c.pfull[b][h]), TR_HALF / 32);
-                mbar_init(smem_u32(&c.pvdone[b][h]), 1);
-            }
+            mbar_init(smem_u32(&c.sfull[b]), 1);
+            mbar_init(smem_u32(&c.pfull[b]), TR_HALF / 32);
+            mbar_init(smem_u32(&c.pvdone[b]), 1);
+            mbar_init(smem_u32(&c.meet[b]), 2 * TR_HALF / 32);
         }
         mbar_init(smem_u32(&c.done), 1);
         c.abort = 0;
@@ -695,6 +711,7 @@ __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
         tma_prefetch_map(&tmv);
     } else if (threadIdx.x >= 32 && threadIdx.x < 32 + TR_MARKS) {
         c.bad[threadIdx.x - 32] = 0;
+        c.poison[(threadIdx.x - 32) / TR_SEEN][(threadIdx.x - 32) % TR_SEEN] = 0;
     }
     grid_wait();
     if (warp == 2) {   // (not before: an earlier kernel may still need its own)
@@ -711,13 +728,13 @@ __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
                           X::MK == PA_KV_F16 ? 0x7e007e00u : 0x7fc07fc0u);
     if (plan.u0 < plan.u1) {   // the whole CTA has work, or none of it
         Walk<TreeArgs> p(a, plan);
-        if (warp >= 4 && (!X::F8 || warp < 8)) {
+        if (warp >= 4 && warp < 12) {
             regs_increase<X::REGS_HIGH>();
             tr_softmax<KV, D>(smem, c, a, p, tmem, (warp - 4) >> 2);
-        } else if (warp >= 8) {
+        } else if (warp >= 12) {
             if constexpr (X::F8) {
                 regs_decrease<X::REGS_CONV>();
-                tr_convert<KV, D>(smem, c, a, p, warp - 8);
+                tr_convert<KV, D>(smem, c, a, p, warp - 12);
             }
         } else {
             regs_decrease<X::REGS_LOW>();
