@@ -124,8 +124,8 @@ struct Tree {
     static constexpr int SMEM = OFF_CTRL + CTRL;
     static constexpr int THREADS = F8 ? 512 : 384;
     static constexpr int REGS_LAUNCH = F8 ? 128 : 168;     // per thread: 65536 / threads, rounded down to 8
-    static constexpr int REGS_LOW = F8 ? 56 : 104;         // warps 0 - 3
-    static constexpr int REGS_HIGH = F8 ? 176 : 200;       // the softmax warps
+    static constexpr int REGS_LOW = F8 ? 104 : 104;        // warps 0 - 3
+    static constexpr int REGS_HIGH = F8 ? 152 : 200;       // the softmax warps
     static constexpr int REGS_CONV = 104;                  // the converting warps
     static constexpr int CONV_WARPS = 4;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
@@ -141,7 +141,9 @@ static_assert(2 * TR_SEEN == TR_MARKS, "set up by the same threads");
 struct TrCtrl {
     uint64_t full[TR_MAX_RING], empty[TR_MAX_RING], stfull[TR_MAX_STAGES], stempty[TR_MAX_STAGES];
     uint64_t qfull[2], qempty[2];
-    uint64_t sfull[2], pfull[2], pvdone[2];   // of either S buffer
+    // by S buffer; one set for pieces of one half, one for those of two (whose P
+    // comes from one warpgroup, not from both)
+    uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];
     uint64_t meet[2];       // of all softmax warps, at a piece's end and after it
     uint64_t done;
     uint32_t tmem;
@@ -152,7 +154,7 @@ struct TrCtrl {
     // Nodes whose values are not finite, as the softmax warps find them, by the
     // piece's parity (the next piece's set is emptied between the two meetings).
     uint32_t poison[2][TR_SEEN];
-    float2 ml[2][TR_HALF];  // a row's maximum and sum over either parity's tiles
+    float2 ml[2][TR_HALF];  // a row's maximum and sum as either warpgroup has them
 };
 
 // Where the softmax keeps four dims (32 k + 4 j ..) of a row, in float4: a store
@@ -264,13 +266,14 @@ __device__ void tr_query(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeA
     constexpr int CH = D / 8;   // 16-byte chunks of a row
     const int lane = threadIdx.x & 31;
     WarpWait wait{c, a.wait_limit};
-    int qc[2] = {0, 0}, sel = 0;
+    uint32_t phase = 3;   // of the buffers' release (a bit each)
+    int sel = 0;
     while (wait.ok && p.next()) {
         const TrPiece x = piece_of(a, p);
         const uint16_t *first = a.query + a.first_row(p.w, p.r) * D;
         for (int h = 0; wait.ok && h < (x.two ? 2 : 1); ++h) {
             const int b = x.two ? h : sel;
-            if (!wait(&c.qempty[b], (uint32_t)((qc[b] & 1) ^ 1))) break;
+            if (!wait(&c.qempty[b], phase >> b & 1u)) break;
             const uint32_t dst = smem_u32(smem) + b * X::TILE;
             const int rows = min(TR_HALF, x.rows - h * TR_HALF);
             for (int i = lane; i < rows * CH; i += 32) {
@@ -285,7 +288,7 @@ __device__ void tr_query(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeA
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c.qfull[b]));
-            ++qc[b];
+            phase ^= 1u << b;
         }
         if (!x.two) sel ^= 1;
     }
@@ -352,15 +355,20 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
         if (!ok) *abort_flag = 1;
         return ok;
     };
-    int cnt = 0, qc[2] = {0, 0}, sel = 0;   // ring tiles before this piece; queries taken; the next buffer of one half
-    int pc[2] = {0, 0};                     // P tiles taken, of either buffer
+    int cnt = 0, sel = 0;           // ring tiles before this piece; the next query buffer of one half
+    uint32_t qphase = 0, phase = 0; // of the query barriers; of the P barriers: bits 0 and 1 of either buffer, bit 2 of the halves
+    auto q_wait = [&](int q) {
+        const uint32_t now = qphase >> q & 1u;
+        qphase ^= 1u << q;
+        return wait(&c.qfull[q], now);
+    };
     auto ring_wait = [&](int k) {
         const bool got = wait(&c.full[k % X::RING], (uint32_t)((k / X::RING) & 1));
         tc_fence_after_sync();
         return got;
     };
-    auto p_wait = [&](int b) {
-        const bool got = wait(&c.pfull[b], (uint32_t)(pc[b]++ & 1));
+    auto p_wait = [&](int two, int b) {
+        const bool got = wait(&c.pfull[two][b], phase >> (two ? 2 : b) & 1u);
         tc_fence_after_sync();
         return got;
     };
@@ -374,48 +382,51 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
             for (int j = 0; j < 4; ++j)
                 umma_f16(tmem + b * TR_TOK, dq + h * (X::BLOCK >> 4) + 2 * j, dk + h * (X::BLOCK >> 4) + 2 * j, ID_S,
                          h > 0 || j > 0 ? 1u : 0u);
-        umma_commit(smem_u32(&c.sfull[b]));
-    };
-    // O_b += P_b times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
-    auto issue_pv = [&](int b, int k, bool first) {
-        const uint64_t dv = dv0 + (uint64_t)(k % X::RING * (X::TILE >> 4));
-#pragma unroll
-        for (int j = 0; j < TR_TOK / 16; ++j)
-            umma_f16_ts(tmem + TR_O + b * 128, tmem + b * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4), ID_O,
-                        !first || j > 0 ? 1u : 0u);
-        umma_commit(smem_u32(&c.pvdone[b]));
     };
     while (ok && p.next()) {
         const TrPiece x = piece_of(a, p);
         const int N = x.n;
-        if (!x.two) {   // tile n in buffer n & 1
-            if (!wait(&c.qfull[sel], (uint32_t)(qc[sel]++ & 1))) break;
-            for (int n = 0; n < min(N, 2); ++n) {
-                const int k = cnt + k_at(n);
-                if (!ring_wait(k)) break;
-                issue_s(n, sel, k);
-                release(k);
-                if (n + 1 == N) umma_commit(smem_u32(&c.qempty[sel]));
-            }
-            for (int n = 0; ok && n < N; ++n) {
-                const int b = n & 1, v = cnt + v_at(n, N), k = cnt + k_at(n + 2);
-                if (!p_wait(b) || !ring_wait(v)) break;
-                issue_pv(b, v, n < 2);
-                release(v);
-                if (n + 2 < N) {
+        if (!x.two) {   // S(n) in buffer n & 1, its columns 64 w .. the warpgroup w's, whose products go to O_w
+            if (!q_wait(sel) || !ring_wait(cnt)) break;
+            issue_s(0, sel, cnt);
+            umma_commit(smem_u32(&c.sfull[0][0]));
+            release(cnt);
+            if (N == 1) umma_commit(smem_u32(&c.qempty[sel]));
+            for (int n = 0; n < N; ++n) {
+                const int b = n & 1, v = cnt + v_at(n, N);
+                if (n + 1 < N) {   // buffer b ^ 1: its P has been taken by PV(n - 1)
+                    const int k = cnt + k_at(n + 1);
                     if (!ring_wait(k)) break;
-                    issue_s(b, sel, k);
+                    issue_s(b ^ 1, sel, k);
+                    umma_commit(smem_u32(&c.sfull[0][b ^ 1]));
                     release(k);
-                    if (n + 3 == N) umma_commit(smem_u32(&c.qempty[sel]));
+                    if (n + 2 == N) umma_commit(smem_u32(&c.qempty[sel]));
                 }
+                if (!p_wait(0, b) || !ring_wait(v)) break;
+                phase ^= 1u << b;
+                const uint64_t dv = dv0 + (uint64_t)(v % X::RING * (X::TILE >> 4));
+#pragma unroll
+                for (int j = 0; j < TR_TOK / 16; ++j)   // 16 tokens: P columns 64 w + 8 (j % 4) .., V rows 16 j ..
+                    umma_f16_ts(tmem + TR_O + j / 4 * 128, tmem + b * TR_TOK + j / 4 * 64 + 8 * (j % 4),
+                                dv + (uint64_t)((j * 16 * 128) >> 4), ID_O, n > 0 || j % 4 > 0 ? 1u : 0u);
+                umma_commit(smem_u32(&c.pvdone[0][b]));
+                release(v);
             }
             sel ^= 1;
         } else {        // half h in buffer h
-            if (!wait(&c.qfull[0], (uint32_t)(qc[0]++ & 1)) || !wait(&c.qfull[1], (uint32_t)(qc[1]++ & 1)) ||
-                !ring_wait(cnt))
-                break;
+            // O_h += P_h times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
+            auto issue_pv = [&](int h, int k, int n) {
+                const uint64_t dv = dv0 + (uint64_t)(k % X::RING * (X::TILE >> 4));
+#pragma unroll
+                for (int j = 0; j < TR_TOK / 16; ++j)
+                    umma_f16_ts(tmem + TR_O + h * 128, tmem + h * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4),
+                                ID_O, n > 0 || j > 0 ? 1u : 0u);
+                umma_commit(smem_u32(&c.pvdone[1][h]));
+            };
+            if (!q_wait(0) || !q_wait(1) || !ring_wait(cnt)) break;
             for (int h = 0; h < 2; ++h) {
                 issue_s(h, h, cnt);
+                umma_commit(smem_u32(&c.sfull[1][h]));
                 if (N == 1) umma_commit(smem_u32(&c.qempty[h]));
             }
             release(cnt);
@@ -423,16 +434,18 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                 const bool more = n + 1 < N;
                 const int v = cnt + v_at(n, N), k = cnt + k_at(n + 1);
                 for (int h = 0; h < 2; ++h) {
-                    if (!p_wait(h) || (h == 0 && !ring_wait(v))) break;
-                    issue_pv(h, v, n == 0);
+                    if (!p_wait(1, h) || (h == 0 && !ring_wait(v))) break;
+                    issue_pv(h, v, n);
                     if (h == 1) release(v);
                     if (more) {
                         if (h == 0 && !ring_wait(k)) break;
                         issue_s(h, h, k);
+                        umma_commit(smem_u32(&c.sfull[1][h]));
                         if (n + 2 == N) umma_commit(smem_u32(&c.qempty[h]));
                         if (h == 1) release(k);
                     }
                 }
+                phase ^= 4u;
             }
         }
         cnt += 2 * N;
@@ -442,60 +455,62 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
     mbar_wait_bounded(smem_u32(&c.done), 0, WAIT_LIMIT);
 }
 
-// One warpgroup: the softmax of S buffer x, a row per thread.
+// A softmax warpgroup's state and its way through a piece's tiles, a row per
+// thread: COLS = 64, columns 64 x .. of every tile of a piece of one half (S in turn
+// in either buffer), or 128, all columns of half x.
 template <int KV, int D>
-__device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_t tmem, int x) {
+struct TrRows {
     using X = Tree<KV, D>;
-    constexpr int MK = X::MK;
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, m = quarter * 32 + lane;
-    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t scol = (uint32_t)(x * TR_TOK), ocol = (uint32_t)(TR_O + x * 128);
-    const float sl2 = a.scale_log2;
-    WarpWait wait{c, a.wait_limit};
-    int sc = 0, cnt = 0, met = 0;   // S and P so far; ring tiles and pieces before this piece
-    auto meet = [&](int k) {        // all softmax warps
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c.meet[k]));
-        const bool got = wait(&c.meet[k], (uint32_t)(met & 1));
-        tc_fence_after_sync();
-        return got;
-    };
-    while (wait.ok && p.next()) {
-        const TrPiece pc = piece_of(a, p);
-        const int N = pc.n, first = pc.two ? 0 : x, by = pc.two ? 1 : 2;   // this warpgroup's tiles
-        const int mm = pc.two ? x * TR_HALF + m : m;   // row of the row tile
-        const bool mine = mm < pc.rows;
-        const bool idle = !__any_sync(0xffffffffu, mine);
-        const int node = pc.node0 + (mm * a.ginv >> 16);
+    static constexpr int MK = X::MK;
+    TrCtrl &c;
+    const TreeArgs &a;
+    WarpWait wait;
+    uint8_t *smem;
+    uint32_t trow, ocol;
+    int x, m, lane;
+    uint32_t phase;        // of the S barriers: bits 0 and 1 of either buffer, bit 2 of the half
+    int cnt;               // ring tiles before this piece
+    float mrun, l;
+    bool lost;             // the chain of parents is broken
+
+    template <int COLS>
+    __device__ __forceinline__ void tiles(const Walk<TreeArgs> &p, const TrPiece &pc, bool mine, bool idle, int node,
+                                          uint32_t *poison) {
+        constexpr bool TWO = COLS == TR_TOK;
+        const float sl2 = a.scale_log2;
         const int ctx = p.w.L - p.w.T;                 // positions before the tree
         const int32_t *parents = a.parents + p.w.q0;
-        uint32_t *poison = c.poison[p.local & 1];
-        float mrun = -INFINITY, l = 0.f;
-        bool lost = false;                             // the chain of parents is broken
-        for (int n = first; n < N; n += by) {
-            if (!wait(&c.sfull[x], (uint32_t)(sc & 1))) break;
-            // (done when S is; every phase is seen, so that the one waited for last is not taken for another)
-            if (n > first && !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1))) break;
+        mrun = -INFINITY;
+        l = 0.f;
+        lost = false;
+        for (int n = 0; n < pc.n; ++n) {
+            const int b = TWO ? x : n & 1, bit = TWO ? 2 : b;
+            const uint32_t now = phase >> bit & 1u;
+            const uint32_t scol = (uint32_t)(b * TR_TOK + (TWO ? 0 : x * COLS));
+            if (!wait(&c.sfull[TWO][b], now)) return;
+            // the products with this buffer's last P (done when S is; every phase is
+            // seen, so that one waited for later is not taken for another)
+            if (n > (TWO ? 0 : 1) && !wait(&c.pvdone[TWO][b], now ^ 1u)) return;
             tc_fence_after_sync();
             const int t0 = (p.t0 + n) * TR_TOK;
             const bool tail = ctx - t0 < TR_TOK;       // the tree's positions begin before the tile ends
             bool changed = false;
-            if (tail && (x == 0 || !pc.two)) {
+            if (tail && (x == 0 || !TWO)) {
                 // Value rows that some row of the row tile does not see, where P is 0
                 // and a product with an infinity or a NaN would not be: those behind the
                 // context are zeroed, and so is what is not finite among the nodes' (the
                 // rows that see it become NaN below).  Of two halves the first one's
                 // warps do it for both: PV1(n) is issued after P0(n).
-                const int at = cnt + v_at(n, N);
-                if (!wait(&c.full[at % X::RING], (uint32_t)((at / X::RING) & 1))) break;
+                const int at = cnt + v_at(n, pc.n);
+                if (!wait(&c.full[at % X::RING], (uint32_t)((at / X::RING) & 1))) return;
                 const int lo = max(0, ctx - t0), hi = p.w.L - t0;
 #pragma unroll 1
                 for (int h = 0; h < D / 64; ++h) {
-                    uint4 *blk = reinterpret_cast<uint4 *>(smem + X::OFF_RING + at % X::RING * X::TILE + h * X::BLOCK);
+                    uint4 *blk = reinterpret_cast<uint4 *>(smem + X::OFF_RING + at % X::RING * X::TILE + h * X::BLOCK) +
+                                 (TWO ? 0 : x * COLS * 8);
 #pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {      // this thread's chunks m, m + 128, ..: row m / 8 + 16 i
-                        const int r = m / 8 + 16 * i;
+                    for (int i = 0; i < COLS / 16; ++i) {   // this thread's chunks m, m + 128, ..: row m / 8 + 16 i
+                        const int r = (TWO ? 0 : x * COLS) + m / 8 + 16 * i;
                         uint4 &v = blk[m + TR_HALF * i];
                         if (r >= hi) {
                             v = make_uint4(0, 0, 0, 0);
@@ -510,9 +525,9 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                 changed = true;
             }
             if (!idle) {
-                float s[TR_TOK];
+                float s[COLS];
 #pragma unroll
-                for (int q = 0; q < TR_TOK / 32; ++q) {
+                for (int q = 0; q < COLS / 32; ++q) {
                     uint32_t r[32];
                     tmem_ld32(trow + scol + 32 * q, r);
 #pragma unroll
@@ -520,32 +535,33 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                 }
                 tmem_wait_ld();
                 if (tail) {
-                    // what the row sees of the tile, a bit per column: the context, then its chain
-                    uint32_t see[TR_TOK / 32];
+                    // what the row sees of its columns, a bit each: the context, then its chain
+                    const int c0 = t0 + (TWO ? 0 : x * COLS);
+                    uint32_t see[COLS / 32];
 #pragma unroll
-                    for (int k = 0; k < TR_TOK / 32; ++k) {
-                        const int before = min(32, ctx - t0 - 32 * k);
+                    for (int k = 0; k < COLS / 32; ++k) {
+                        const int before = min(32, ctx - c0 - 32 * k);
                         see[k] = !mine || before <= 0 ? 0u : before == 32 ? ~0u : (1u << before) - 1u;
                     }
                     for (int j = mine ? node : -1; j >= 0;) {
-                        const int at = ctx + j - t0;
+                        const int at = ctx + j - c0;
 #pragma unroll
-                        for (int k = 0; k < TR_TOK / 32; ++k)
+                        for (int k = 0; k < COLS / 32; ++k)
                             if (at >> 5 == k) see[k] |= 1u << (at & 31);
                         const int up = parents[j];
                         lost = lost || up < -1 || up >= j;
                         j = lost ? -1 : up;
                     }
 #pragma unroll
-                    for (int k = 0; k < TR_TOK; ++k) s[k] = see[k / 32] >> (k & 31) & 1u ? s[k] : -INFINITY;
+                    for (int k = 0; k < COLS; ++k) s[k] = see[k / 32] >> (k & 31) & 1u ? s[k] : -INFINITY;
                 }
                 float mp[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int k = 4; k + 8 <= TR_TOK; k += 8)
+                for (int k = 4; k + 8 <= COLS; k += 8)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) mp[j] = max3(mp[j], s[k + 2 * j], s[k + 2 * j + 1]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mp[j] = fmaxf(mp[j], s[TR_TOK - 4 + j]);
+                for (int j = 0; j < 4; ++j) mp[j] = fmaxf(mp[j], s[COLS - 4 + j]);
                 const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
                 // decided per row, done warp-wide (tensor-memory accesses are the
                 // whole warp's); rows that do not grow scale by exactly 1
@@ -553,7 +569,10 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                 if (__any_sync(0xffffffffu, grow)) {
                     const float nm = grow ? mx : mrun;
                     const float alpha = grow ? fast_exp2(mrun - nm) : 1.f;
-                    if (n > first) {   // the last PV into O is complete: S(n) was issued after it
+                    if (n > 0) {
+                        // two halves: PV(n - 1) is complete, S(n) was issued after it
+                        if (!TWO && !wait(&c.pvdone[0][b ^ 1], (phase >> (b ^ 1) & 1u) ^ 1u)) return;
+                        tc_fence_after_sync();
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
                             uint32_t o[32];
@@ -574,7 +593,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
 #pragma unroll
                 for (int j = 0; j < 4; ++j) lp[j] = 0;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < COLS / 64; ++q) {
                     uint32_t r[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
@@ -595,13 +614,56 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
             if (changed) fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();   // one arrival a warp: 32 atomics on one word hold up the shared-memory pipe
-            if (lane == 0) mbar_arrive(smem_u32(&c.pfull[x]));
-            ++sc;
+            if (lane == 0) mbar_arrive(smem_u32(&c.pfull[TWO][b]));
+            phase ^= 1u << bit;
         }
-        if (!wait.ok || (first < N && !wait(&c.pvdone[x], (uint32_t)((sc - 1) & 1)))) break;
-        cnt += 2 * N;
+        // the last products (and, with one half, those before them)
+        if (TWO) {
+            wait(&c.pvdone[1][x], (phase >> 2 & 1u) ^ 1u);
+        } else {
+            const int b = (pc.n - 1) & 1;
+            if (pc.n > 1) wait(&c.pvdone[0][b ^ 1], (phase >> (b ^ 1) & 1u) ^ 1u);
+            wait(&c.pvdone[0][b], (phase >> b & 1u) ^ 1u);
+        }
+    }
+};
+
+// One warpgroup: the softmax and the output rows of half x, or of columns 64 x ..
+template <int KV, int D>
+__device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_t tmem, int x) {
+    using X = Tree<KV, D>;
+    constexpr int MK = X::MK;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, m = quarter * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t ocol = (uint32_t)(TR_O + x * 128);
+    TrRows<KV, D> rows{c, a, WarpWait{c, a.wait_limit}, smem, trow, ocol, x, m, lane, 0u, 0, 0.f, 0.f, false};
+    WarpWait &wait = rows.wait;
+    int met = 0;                    // pieces before this one
+    auto meet = [&](int k) {        // all softmax warps
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.meet[k]));
+        const bool got = wait(&c.meet[k], (uint32_t)(met & 1));
+        tc_fence_after_sync();
+        return got;
+    };
+    while (wait.ok && p.next()) {
+        const TrPiece pc = piece_of(a, p);
+        const int mm = pc.two ? x * TR_HALF + m : m;   // row of the row tile
+        const bool mine = mm < pc.rows;
+        const bool idle = !__any_sync(0xffffffffu, mine);
+        const int node = pc.node0 + (mm * a.ginv >> 16);
+        const int32_t *parents = a.parents + p.w.q0;
+        uint32_t *poison = c.poison[p.local & 1];
+        if constexpr (X::ROWS > TR_HALF) {
+            if (pc.two) rows.template tiles<TR_TOK>(p, pc, mine, idle, node, poison);
+        }
+        if (X::ROWS == TR_HALF || !pc.two) rows.template tiles<TR_TOK / 2>(p, pc, mine, idle, node, poison);
+        if (!wait.ok) break;
+        rows.cnt += 2 * pc.n;
+        float mrun = rows.mrun, l = rows.l;
         // ---- the piece's rows: finished, or a partial row
-        if (lost) l = __int_as_float(0x7fc00000);
+        if (rows.lost) l = __int_as_float(0x7fc00000);
         c.ml[x][m] = make_float2(mrun, l);
         if (!meet(0)) break;
         if (x == 0 && threadIdx.x % 128 < TR_SEEN) c.poison[(p.local & 1) ^ 1][threadIdx.x % 128] = 0;
@@ -615,8 +677,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                     const int up = parents[j];
                     j = up >= j ? -1 : up;   // (a broken chain has made its row NaN)
                 }
-            // one half: the tiles of both parities joined, each warpgroup half of the dims
-            const bool join = !pc.two && N > 1;
+            // one half: both warpgroups' columns joined, each of them makes half of the dims
             float wa = 1.f, wb = 0.f;
             if (!pc.two) {
                 const float2 ma = x == 0 ? make_float2(mrun, l) : other, mb = x == 0 ? other : make_float2(mrun, l);
@@ -638,7 +699,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
             for (int q = q0; q < q1; ++q) {
                 uint32_t o[32];
                 tmem_ld32(trow + (pc.two ? ocol : (uint32_t)TR_O) + 32 * q, o);
-                if (join) {
+                if (!pc.two) {
                     uint32_t o2[32];
                     tmem_ld32(trow + TR_O + 128 + 32 * q, o2);
                     tmem_wait_ld();
@@ -699,9 +760,11 @@ __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c.qfull[b]), 1);
             mbar_init(smem_u32(&c.qempty[b]), 1);
-            mbar_init(smem_u32(&c.sfull[b]), 1);
-            mbar_init(smem_u32(&c.pfull[b]), TR_HALF / 32);
-            mbar_init(smem_u32(&c.pvdone[b]), 1);
+            for (int two = 0; two < 2; ++two) {
+                mbar_init(smem_u32(&c.sfull[two][b]), 1);
+                mbar_init(smem_u32(&c.pfull[two][b]), (two ? 1 : 2) * TR_HALF / 32);
+                mbar_init(smem_u32(&c.pvdone[two][b]), 1);
+            }
             mbar_init(smem_u32(&c.meet[b]), 2 * TR_HALF / 32);
         }
         mbar_init(smem_u32(&c.done), 1);
