@@ -9,17 +9,18 @@
 // (work_axis.cuh), cut into equal ranges over the CTAs: one sequence with a long
 // context occupies the GPU as well as a batch.
 //
-// Warps: 0 loads keys and values (TMA boxes of a block's rows, the gather being
+// Warps: 0 loads keys and 3 values (TMA boxes of a block's rows, the gather being
 // the row coordinate), 1 the queries, 2 issues the MMAs, 4-7 and 8-11 run the
-// softmax, a row per thread.  Over an FP8 cache 8-15 turn the staged codes into
-// 16-bit tiles instead.  Tensor memory: S0, S1 (128 columns each), O0, O1; P is
-// written over the first 64 columns of its S.
+// softmax, a row per thread; over an FP8 cache 12-15 turn the staged codes into
+// 16-bit tiles.  Tensor memory: S0, S1 (128 columns each), O0, O1; P is written over
+// its S.
 //
 // A row tile of more than 128 rows is two halves, each with its own S, O and
 // softmax warps, that share every tile the CTA loads (PV0(n), S0(n + 1), PV1(n),
 // S1(n + 1): one half's products run while the other's softmax works).  With 128
-// rows or fewer S0 and S1 are the two buffers of one half: S(n + 1) is computed
-// while the softmax works on S(n).
+// rows or fewer S0 and S1 are two buffers: S(n + 1) is computed while the softmax
+// works on S(n), each of the two warpgroups on 64 of its columns with a maximum, a
+// sum and an O of its own, joined at the end.
 //
 // What a node sees of a masked tile is found by walking its chain of parents: a
 // set of 128 bits.  Values that some row does not see are made finite before the
@@ -114,9 +115,12 @@ struct Tree {
     static constexpr int ROWS = F8 ? TR_HALF : TR_MAX_ROWS;
     static constexpr int BLOCK = TR_TOK * 128;             // 128 rows x 64 elements, 128-byte swizzle
     static constexpr int TILE = BLOCK * (D / 64);          // a key or value tile of 16-bit elements, a half's queries
-    static constexpr int RING = F8 ? 3 : 10 / (D / 64);    // tiles on their way
+    // Tiles on their way: of 16-bit caches key tiles in the first K_RING slots, value
+    // tiles in the others; of FP8 caches staged codes likewise, and the converted tiles
+    // in the order in which they are used.
+    static constexpr int RING = F8 ? 3 : 10 / (D / 64), K_RING = (RING + 1) / 2;
     static constexpr int CODES = F8 ? TR_TOK * D : 0;      // a staged tile of codes
-    static constexpr int STAGES = F8 ? 4 : 0;
+    static constexpr int STAGES = F8 ? 4 : 0, K_STAGES = 2;
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_STAGE = OFF_RING + RING * TILE;
     static constexpr int OFF_CTRL = OFF_STAGE + STAGES * CODES;
@@ -178,9 +182,29 @@ __device__ __forceinline__ TrPiece piece_of(const TreeArgs &a, const Walk<TreeAr
     x.two = x.rows > TR_HALF;
     return x;
 }
-// The ring's order is K(0), then K(n + 1), V(n), the last V at the end: the place of a piece's tile.
-__device__ __forceinline__ int k_at(int n) { return n ? 2 * n - 1 : 0; }
-__device__ __forceinline__ int v_at(int n, int all) { return n + 1 < all ? 2 * n + 2 : 2 * all - 1; }
+// A slot of a ring and the parity of its use.
+struct TrSlot {
+    int at;
+    uint32_t parity;
+};
+__device__ __forceinline__ TrSlot slot_of(int first, int slots, int use) {
+    return {first + use % slots, (uint32_t)(use / slots & 1)};
+}
+// Where the n-th key or value tile of a piece lies, `done` tiles after the CTA's
+// first.  Converted tiles follow one another as K(0), then K(n + 1), V(n), the last V
+// at the end.
+template <int KV, int D>
+__device__ __forceinline__ TrSlot k_slot(int done, int n) {
+    using X = Tree<KV, D>;
+    if (X::F8) return slot_of(0, X::RING, 2 * done + (n ? 2 * n - 1 : 0));
+    return slot_of(0, X::K_RING, done + n);
+}
+template <int KV, int D>
+__device__ __forceinline__ TrSlot v_slot(int done, int n, int all) {
+    using X = Tree<KV, D>;
+    if (X::F8) return slot_of(0, X::RING, 2 * done + (n + 1 < all ? 2 * n + 2 : 2 * all - 1));
+    return slot_of(X::K_RING, X::RING - X::K_RING, done + n);
+}
 
 // A whole warp's bounded wait.
 struct WarpWait {
@@ -196,67 +220,71 @@ struct WarpWait {
     }
 };
 
-// One warp: keys and values in the order the MMAs take them, a lane per block.
+// One lane: the key tiles, or another one: the value tiles.  A box is a block's
+// rows (of 64 elements); block ids are read a tile ahead of their use.  (Lanes with
+// a box each took 42 clocks a box and 580 a tile, one after another, and bound the
+// kernel over FP8 caches.)
 template <int KV, int D>
-__device__ void tr_load(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, const CUtensorMap *tmk,
-                        const CUtensorMap *tmv) {
+__device__ void tr_load(TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_t smem, const CUtensorMap *tm, bool values) {
     using X = Tree<KV, D>;
-    constexpr int SLOTS = X::F8 ? X::STAGES : X::RING, BYTES = X::F8 ? X::CODES : X::TILE;
-    constexpr int ROW = X::F8 ? D : 2 * D;   // bytes of a row
-    const int lane = threadIdx.x & 31;
+    constexpr int ROW = X::F8 ? D : 2 * D;        // bytes of a row
+    constexpr int BOXES = TR_TOK / 8;             // of a tile, at most
+    constexpr int SLOTS = X::F8 ? X::STAGES : X::RING, KS = X::F8 ? X::K_STAGES : X::K_RING;
+    constexpr int BYTES = X::F8 ? X::CODES : X::TILE;
     uint64_t *full = X::F8 ? c.stfull : c.full, *empty = X::F8 ? c.stempty : c.empty;
-    const uint32_t base = smem_u32(smem) + (X::F8 ? X::OFF_STAGE : X::OFF_RING);
+    const int first = values ? KS : 0, slots = values ? SLOTS - KS : KS;
+    const uint32_t base = smem + (X::F8 ? X::OFF_STAGE : X::OFF_RING);
     const int boxes = TR_TOK / a.bs;
     const uint64_t once = policy_evict_first(), again = policy_evict_normal();
-    WarpWait wait{c, a.wait_limit};
-    int cnt = 0;
-    while (wait.ok && p.next()) {
-        const TrPiece x = piece_of(a, p);
+    volatile int *abort_flag = &c.abort;
+    bool ok = true;
+    int use = 0, at = 0;                          // tiles so far; the slot of the next (of this lane's)
+    uint32_t parity = 1;
+    while (ok && p.next()) {
+        const int g = p.r / p.w.per_head;
         const uint64_t policy = p.w.per_head > 1 ? again : once;
         const int32_t *table = a.block_tables + (long long)p.seq * a.mbps;
-        const int per_tile = TR_TOK / a.bs, blocks = (p.w.L - 1) / a.bs + 1;
-        // the id of this lane's block in tile t (read a tile ahead of its use), and its
-        // row coordinate (-1: the context ends before the block)
-        auto id_of = [&](int t) { return lane < boxes && t * per_tile + lane < blocks ? table[t * per_tile + lane] : 0; };
-        auto row_of = [&](int t, long long id) {
-            if (lane >= boxes || t * per_tile + lane >= blocks) return -1;
-            if (id < 0 || id >= a.num_blocks) {
-                c.bad[p.local % TR_MARKS] = p.local + 1;
-                id = 0;
-            }
-            return (int)((id * a.Hkv + x.g) * a.bs);
+        const int blocks = (p.w.L - 1) / a.bs + 1;
+        int id[BOXES];
+        auto read = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < BOXES; ++i) id[i] = i < boxes && t * boxes + i < blocks ? table[t * boxes + i] : 0;
         };
-        auto load = [&](const CUtensorMap *tm, int row) {
-            const int s = cnt % SLOTS;
-            if (!wait(&empty[s], (uint32_t)(((cnt / SLOTS) & 1) ^ 1))) return;
-            const uint32_t bar = smem_u32(&full[s]);
-            const int some = __popc(__ballot_sync(0xffffffffu, row >= 0));
-            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(some * a.bs * ROW));
-            __syncwarp();
-            if (row >= 0) {
-                const uint32_t dst = base + s * BYTES + lane * a.bs * 128;
-                tma_load_2d(dst, tm, 0, row, bar, policy);
-                if (!X::F8 && D == 128) tma_load_2d(dst + X::BLOCK, tm, 64, row, bar, policy);
+        read(p.t0);
+        for (int t = p.t0; t < p.t1; ++t) {
+            const int some = min(boxes, blocks - t * boxes);   // the context ends in the last of them
+            int row[BOXES];
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < BOXES; ++i) {
+                const bool out = id[i] < 0 || id[i] >= a.num_blocks;
+                bad = bad || out;
+                row[i] = ((out ? 0 : id[i]) * a.Hkv + g) * a.bs;
             }
-            ++cnt;
-        };
-        int row = row_of(p.t0, id_of(p.t0)), id = p.t0 + 1 < p.t1 ? id_of(p.t0 + 1) : 0;
-        load(tmk, row);
-        for (int t = p.t0; wait.ok && t < p.t1; ++t) {
-            int next = -1;
-            if (t + 1 < p.t1) {
-                next = row_of(t + 1, id);
-                if (t + 2 < p.t1) id = id_of(t + 2);
-                load(tmk, next);
+            if (bad) c.bad[p.local % TR_MARKS] = p.local + 1;
+            if (t + 1 < p.t1) read(t + 1);
+            ok = ok && !*abort_flag && mbar_wait_bounded(smem_u32(&empty[first + at]), parity, a.wait_limit);
+            if (!ok) {
+                *abort_flag = 1;
+                break;
             }
-            if (wait.ok) load(tmv, row);
-            row = next;
+            const uint32_t bar = smem_u32(&full[first + at]), dst = base + (first + at) * BYTES;
+            mbar_arrive_expect_tx(bar, (uint32_t)(some * a.bs * ROW));
+#pragma unroll
+            for (int i = 0; i < BOXES; ++i)
+                if (i < some) {
+                    tma_load_2d(dst + i * a.bs * 128, tm, 0, row[i], bar, policy);
+                    if (!X::F8 && D == 128) tma_load_2d(dst + i * a.bs * 128 + X::BLOCK, tm, 64, row[i], bar, policy);
+                }
+            ++use;
+            if (++at == slots) at = 0, parity ^= 1;
         }
     }
-    // the last copies into every buffer have landed before the CTA leaves
-    for (int s = 0; s < SLOTS; ++s)
-        if (cnt > s)
-            mbar_wait_bounded(smem_u32(&full[s]), (uint32_t)(((cnt - 1 - s) / SLOTS) & 1), WAIT_LIMIT);
+    // the last copies into every slot have landed before the CTA leaves
+    for (int s = 0; s < slots; ++s)
+        if (use > s)
+            mbar_wait_bounded(smem_u32(&full[first + (use - 1 - s) % slots]), (uint32_t)(((use - 1 - s) / slots) & 1),
+                              WAIT_LIMIT);
 }
 
 // One warp: the queries of a piece's rows, as the products read them.
@@ -304,11 +332,16 @@ __device__ void tr_convert(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
     constexpr int N = X::CODES / 16 / (32 * X::CONV_WARPS);   // 16-byte chunks a thread
     const int lane = threadIdx.x & 31;
     WarpWait wait{c, a.wait_limit};
-    int cnt = 0;
+    int cnt = 0, kuse = 0, vuse = 0;
     while (wait.ok && p.next()) {
         for (int k = 0; wait.ok && k < 2 * (p.t1 - p.t0); ++k, ++cnt) {
-            const int st = cnt % X::STAGES, s = cnt % X::RING;
-            if (!wait(&c.stfull[st], (uint32_t)((cnt / X::STAGES) & 1))) break;
+            // in the order of their use: K(0), then K(n + 1), V(n), the last V
+            const int s = cnt % X::RING, all = p.t1 - p.t0;
+            const bool value = k > 0 && (k % 2 == 0 || k == 2 * all - 1);
+            const TrSlot from_slot = value ? slot_of(X::K_STAGES, X::STAGES - X::K_STAGES, vuse++)
+                                           : slot_of(0, X::K_STAGES, kuse++);
+            const int st = from_slot.at;
+            if (!wait(&c.stfull[st], from_slot.parity)) break;
             const uint8_t *from = smem + X::OFF_STAGE + st * X::CODES;
             uint4 v[N];
 #pragma unroll
@@ -355,15 +388,15 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
         if (!ok) *abort_flag = 1;
         return ok;
     };
-    int cnt = 0, sel = 0;           // ring tiles before this piece; the next query buffer of one half
+    int done = 0, sel = 0;          // KV tiles before this piece; the next query buffer of one half
     uint32_t qphase = 0, phase = 0; // of the query barriers; of the P barriers: bits 0 and 1 of either buffer, bit 2 of the halves
     auto q_wait = [&](int q) {
         const uint32_t now = qphase >> q & 1u;
         qphase ^= 1u << q;
         return wait(&c.qfull[q], now);
     };
-    auto ring_wait = [&](int k) {
-        const bool got = wait(&c.full[k % X::RING], (uint32_t)((k / X::RING) & 1));
+    auto ring_wait = [&](const TrSlot &k) {
+        const bool got = wait(&c.full[k.at], k.parity);
         tc_fence_after_sync();
         return got;
     };
@@ -372,10 +405,10 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
         tc_fence_after_sync();
         return got;
     };
-    auto release = [&](int k) { umma_commit(smem_u32(&c.empty[k % X::RING])); };
+    auto release = [&](const TrSlot &k) { umma_commit(smem_u32(&c.empty[k.at])); };
     // S in buffer b = the queries of buffer q times the key tile at k
-    auto issue_s = [&](int b, int q, int k) {
-        const uint64_t dk = dk0 + (uint64_t)(k % X::RING * (X::TILE >> 4)), dq = dq0 + (uint64_t)(q * (X::TILE >> 4));
+    auto issue_s = [&](int b, int q, const TrSlot &k) {
+        const uint64_t dk = dk0 + (uint64_t)(k.at * (X::TILE >> 4)), dq = dq0 + (uint64_t)(q * (X::TILE >> 4));
 #pragma unroll
         for (int h = 0; h < D / 64; ++h)
 #pragma unroll
@@ -387,15 +420,17 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
         const TrPiece x = piece_of(a, p);
         const int N = x.n;
         if (!x.two) {   // S(n) in buffer n & 1, its columns 64 w .. the warpgroup w's, whose products go to O_w
-            if (!q_wait(sel) || !ring_wait(cnt)) break;
-            issue_s(0, sel, cnt);
+            const TrSlot k0 = k_slot<KV, D>(done, 0);
+            if (!q_wait(sel) || !ring_wait(k0)) break;
+            issue_s(0, sel, k0);
             umma_commit(smem_u32(&c.sfull[0][0]));
-            release(cnt);
+            release(k0);
             if (N == 1) umma_commit(smem_u32(&c.qempty[sel]));
             for (int n = 0; n < N; ++n) {
-                const int b = n & 1, v = cnt + v_at(n, N);
+                const int b = n & 1;
+                const TrSlot v = v_slot<KV, D>(done, n, N);
                 if (n + 1 < N) {   // buffer b ^ 1: its P has been taken by PV(n - 1)
-                    const int k = cnt + k_at(n + 1);
+                    const TrSlot k = k_slot<KV, D>(done, n + 1);
                     if (!ring_wait(k)) break;
                     issue_s(b ^ 1, sel, k);
                     umma_commit(smem_u32(&c.sfull[0][b ^ 1]));
@@ -404,7 +439,7 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                 }
                 if (!p_wait(0, b) || !ring_wait(v)) break;
                 phase ^= 1u << b;
-                const uint64_t dv = dv0 + (uint64_t)(v % X::RING * (X::TILE >> 4));
+                const uint64_t dv = dv0 + (uint64_t)(v.at * (X::TILE >> 4));
 #pragma unroll
                 for (int j = 0; j < TR_TOK / 16; ++j)   // 16 tokens: P columns 64 w + 8 (j % 4) .., V rows 16 j ..
                     umma_f16_ts(tmem + TR_O + j / 4 * 128, tmem + b * TR_TOK + j / 4 * 64 + 8 * (j % 4),
@@ -415,24 +450,25 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
             sel ^= 1;
         } else {        // half h in buffer h
             // O_h += P_h times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
-            auto issue_pv = [&](int h, int k, int n) {
-                const uint64_t dv = dv0 + (uint64_t)(k % X::RING * (X::TILE >> 4));
+            auto issue_pv = [&](int h, const TrSlot &k, int n) {
+                const uint64_t dv = dv0 + (uint64_t)(k.at * (X::TILE >> 4));
 #pragma unroll
                 for (int j = 0; j < TR_TOK / 16; ++j)
                     umma_f16_ts(tmem + TR_O + h * 128, tmem + h * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4),
                                 ID_O, n > 0 || j > 0 ? 1u : 0u);
                 umma_commit(smem_u32(&c.pvdone[1][h]));
             };
-            if (!q_wait(0) || !q_wait(1) || !ring_wait(cnt)) break;
+            const TrSlot k0 = k_slot<KV, D>(done, 0);
+            if (!q_wait(0) || !q_wait(1) || !ring_wait(k0)) break;
             for (int h = 0; h < 2; ++h) {
-                issue_s(h, h, cnt);
+                issue_s(h, h, k0);
                 umma_commit(smem_u32(&c.sfull[1][h]));
                 if (N == 1) umma_commit(smem_u32(&c.qempty[h]));
             }
-            release(cnt);
+            release(k0);
             for (int n = 0; ok && n < N; ++n) {
                 const bool more = n + 1 < N;
-                const int v = cnt + v_at(n, N), k = cnt + k_at(n + 1);
+                const TrSlot v = v_slot<KV, D>(done, n, N), k = k_slot<KV, D>(done, n + 1);
                 for (int h = 0; h < 2; ++h) {
                     if (!p_wait(1, h) || (h == 0 && !ring_wait(v))) break;
                     issue_pv(h, v, n);
@@ -448,7 +484,7 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                 phase ^= 4u;
             }
         }
-        cnt += 2 * N;
+        done += N;
     }
     // every product issued has completed before tensor memory is freed
     umma_commit(smem_u32(&c.done));
@@ -469,7 +505,7 @@ struct TrRows {
     uint32_t trow, ocol;
     int x, m, lane;
     uint32_t phase;        // of the S barriers: bits 0 and 1 of either buffer, bit 2 of the half
-    int cnt;               // ring tiles before this piece
+    int done;              // KV tiles before this piece
     float mrun, l;
     bool lost;             // the chain of parents is broken
 
@@ -501,12 +537,12 @@ struct TrRows {
                 // context are zeroed, and so is what is not finite among the nodes' (the
                 // rows that see it become NaN below).  Of two halves the first one's
                 // warps do it for both: PV1(n) is issued after P0(n).
-                const int at = cnt + v_at(n, pc.n);
-                if (!wait(&c.full[at % X::RING], (uint32_t)((at / X::RING) & 1))) return;
+                const TrSlot at = v_slot<KV, D>(done, n, pc.n);
+                if (!wait(&c.full[at.at], at.parity)) return;
                 const int lo = max(0, ctx - t0), hi = p.w.L - t0;
 #pragma unroll 1
                 for (int h = 0; h < D / 64; ++h) {
-                    uint4 *blk = reinterpret_cast<uint4 *>(smem + X::OFF_RING + at % X::RING * X::TILE + h * X::BLOCK) +
+                    uint4 *blk = reinterpret_cast<uint4 *>(smem + X::OFF_RING + at.at * X::TILE + h * X::BLOCK) +
                                  (TWO ? 0 : x * COLS * 8);
 #pragma unroll 1
                     for (int i = 0; i < COLS / 16; ++i) {   // this thread's chunks m, m + 128, ..: row m / 8 + 16 i
@@ -660,7 +696,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
         }
         if (X::ROWS == TR_HALF || !pc.two) rows.template tiles<TR_TOK / 2>(p, pc, mine, idle, node, poison);
         if (!wait.ok) break;
-        rows.cnt += 2 * pc.n;
+        rows.done += pc.n;
         float mrun = rows.mrun, l = rows.l;
         // ---- the piece's rows: finished, or a partial row
         if (rows.lost) l = __int_as_float(0x7fc00000);
@@ -801,8 +837,8 @@ __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
             }
         } else {
             regs_decrease<X::REGS_LOW>();
-            if (warp == 0) {
-                tr_load<KV, D>(smem, c, a, p, &tmk, &tmv);
+            if (warp == 0 || warp == 3) {
+                if (elect_one()) tr_load<KV, D>(c, a, p, smem_u32(smem), warp == 0 ? &tmk : &tmv, warp == 3);
             } else if (warp == 1) {
                 tr_query<KV, D>(smem, c, a, p);
             } else if (warp == 2) {
