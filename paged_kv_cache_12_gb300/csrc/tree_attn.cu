@@ -220,62 +220,47 @@ struct WarpWait {
     }
 };
 
-// One lane: the key tiles, or another one: the value tiles.  A box is a block's
-// rows (of 64 elements); block ids are read a tile ahead of their use.  (Lanes with
-// a box each took 42 clocks a box and 580 a tile, one after another, and bound the
-// kernel over FP8 caches.)
+// One warp: the key tiles, or another one: the value tiles.  A lane finds a block's
+// rows (its id is read a tile ahead of its use), and copies them as a box (two, of 64
+// elements each).  (One warp for both worked 1830 clocks a tile over FP8 caches and
+// bound the kernel, a single lane for each 1560.)
 template <int KV, int D>
 __device__ void tr_load(TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_t smem, const CUtensorMap *tm, bool values) {
     using X = Tree<KV, D>;
     constexpr int ROW = X::F8 ? D : 2 * D;        // bytes of a row
-    constexpr int BOXES = TR_TOK / 8;             // of a tile, at most
     constexpr int SLOTS = X::F8 ? X::STAGES : X::RING, KS = X::F8 ? X::K_STAGES : X::K_RING;
     constexpr int BYTES = X::F8 ? X::CODES : X::TILE;
+    const int lane = threadIdx.x & 31;
     uint64_t *full = X::F8 ? c.stfull : c.full, *empty = X::F8 ? c.stempty : c.empty;
     const int first = values ? KS : 0, slots = values ? SLOTS - KS : KS;
-    const uint32_t base = smem + (X::F8 ? X::OFF_STAGE : X::OFF_RING);
+    const uint32_t base = smem + (X::F8 ? X::OFF_STAGE : X::OFF_RING) + lane * a.bs * 128;
     const int boxes = TR_TOK / a.bs;
+    const uint32_t num_blocks = (uint32_t)a.num_blocks;   // (rows of the caches are counted in 31 bits)
     const uint64_t once = policy_evict_first(), again = policy_evict_normal();
-    volatile int *abort_flag = &c.abort;
-    bool ok = true;
-    int use = 0, at = 0;                          // tiles so far; the slot of the next (of this lane's)
+    WarpWait wait{c, a.wait_limit};
+    int use = 0, at = 0;                          // tiles so far; the slot of the next (of this warp's)
     uint32_t parity = 1;
-    while (ok && p.next()) {
+    while (wait.ok && p.next()) {
         const int g = p.r / p.w.per_head;
         const uint64_t policy = p.w.per_head > 1 ? again : once;
         const int32_t *table = a.block_tables + (long long)p.seq * a.mbps;
         const int blocks = (p.w.L - 1) / a.bs + 1;
-        int id[BOXES];
-        auto read = [&](int t) {
-#pragma unroll
-            for (int i = 0; i < BOXES; ++i) id[i] = i < boxes && t * boxes + i < blocks ? table[t * boxes + i] : 0;
-        };
-        read(p.t0);
+        auto read = [&](int t) { return lane < boxes && t * boxes + lane < blocks ? table[t * boxes + lane] : 0; };
+        int id = read(p.t0);
         for (int t = p.t0; t < p.t1; ++t) {
             const int some = min(boxes, blocks - t * boxes);   // the context ends in the last of them
-            int row[BOXES];
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < BOXES; ++i) {
-                const bool out = id[i] < 0 || id[i] >= a.num_blocks;
-                bad = bad || out;
-                row[i] = ((out ? 0 : id[i]) * a.Hkv + g) * a.bs;
-            }
-            if (bad) c.bad[p.local % TR_MARKS] = p.local + 1;
-            if (t + 1 < p.t1) read(t + 1);
-            ok = ok && !*abort_flag && mbar_wait_bounded(smem_u32(&empty[first + at]), parity, a.wait_limit);
-            if (!ok) {
-                *abort_flag = 1;
-                break;
-            }
+            const bool out = (uint32_t)id >= num_blocks;
+            if (out) c.bad[p.local % TR_MARKS] = p.local + 1;
+            const int row = ((out ? 0 : id) * a.Hkv + g) * a.bs;
+            if (t + 1 < p.t1) id = read(t + 1);
+            if (!wait(&empty[first + at], parity)) break;
             const uint32_t bar = smem_u32(&full[first + at]), dst = base + (first + at) * BYTES;
-            mbar_arrive_expect_tx(bar, (uint32_t)(some * a.bs * ROW));
-#pragma unroll
-            for (int i = 0; i < BOXES; ++i)
-                if (i < some) {
-                    tma_load_2d(dst + i * a.bs * 128, tm, 0, row[i], bar, policy);
-                    if (!X::F8 && D == 128) tma_load_2d(dst + i * a.bs * 128 + X::BLOCK, tm, 64, row[i], bar, policy);
-                }
+            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(some * a.bs * ROW));
+            __syncwarp();
+            if (lane < some) {
+                tma_load_2d(dst, tm, 0, row, bar, policy);
+                if (!X::F8 && D == 128) tma_load_2d(dst + X::BLOCK, tm, 64, row, bar, policy);
+            }
             ++use;
             if (++at == slots) at = 0, parity ^= 1;
         }
@@ -838,7 +823,7 @@ __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
         } else {
             regs_decrease<X::REGS_LOW>();
             if (warp == 0 || warp == 3) {
-                if (elect_one()) tr_load<KV, D>(c, a, p, smem_u32(smem), warp == 0 ? &tmk : &tmv, warp == 3);
+                tr_load<KV, D>(c, a, p, smem_u32(smem), warp == 0 ? &tmk : &tmv, warp == 3);
             } else if (warp == 1) {
                 tr_query<KV, D>(smem, c, a, p);
             } else if (warp == 2) {
