@@ -18,9 +18,10 @@
 // A row tile of more than 128 rows is two halves, each with its own S, O and
 // softmax warps, that share every tile the CTA loads (PV0(n), S0(n + 1), PV1(n),
 // S1(n + 1): one half's products run while the other's softmax works).  With 128
-// rows or fewer S0 and S1 are two buffers: S(n + 1) is computed while the softmax
-// works on S(n), each of the two warpgroups on 64 of its columns with a maximum, a
-// sum and an O of its own, joined at the end.
+// rows or fewer S0 and S1 are two buffers, and each softmax warpgroup has a maximum,
+// a sum and an O of its own, joined at the end: over 16-bit caches they share every
+// tile, 64 columns each, and S(n + 1) is computed meanwhile; over FP8 caches they take
+// every second tile, so that one's exponentials run beside the other's loads and waits.
 //
 // What a node sees of a masked tile is found by walking its chain of parents: a
 // set of 128 bits.  Values that some row does not see are made finite before the
@@ -128,9 +129,9 @@ struct Tree {
     static constexpr int SMEM = OFF_CTRL + CTRL;
     static constexpr int THREADS = F8 ? 512 : 384;
     static constexpr int REGS_LAUNCH = F8 ? 128 : 168;     // per thread: 65536 / threads, rounded down to 8
-    static constexpr int REGS_LOW = F8 ? 104 : 104;        // warps 0 - 3
-    static constexpr int REGS_HIGH = F8 ? 152 : 200;       // the softmax warps
-    static constexpr int REGS_CONV = 104;                  // the converting warps
+    static constexpr int REGS_LOW = F8 ? 72 : 104;         // warps 0 - 3
+    static constexpr int REGS_HIGH = F8 ? 176 : 200;       // the softmax warps
+    static constexpr int REGS_CONV = 88;                   // the converting warps
     static constexpr int CONV_WARPS = 4;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
     static_assert(128 * (REGS_LOW + 2 * REGS_HIGH + (F8 ? REGS_CONV : 0)) <= THREADS * REGS_LAUNCH,
@@ -145,8 +146,8 @@ static_assert(2 * TR_SEEN == TR_MARKS, "set up by the same threads");
 struct TrCtrl {
     uint64_t full[TR_MAX_RING], empty[TR_MAX_RING], stfull[TR_MAX_STAGES], stempty[TR_MAX_STAGES];
     uint64_t qfull[2], qempty[2];
-    // by S buffer; one set for pieces of one half, one for those of two (whose P
-    // comes from one warpgroup, not from both)
+    // by S buffer; one set for tiles whose columns both warpgroups share, one for
+    // buffers of one warpgroup each
     uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];
     uint64_t meet[2];       // of all softmax warps, at a piece's end and after it
     uint64_t done;
@@ -206,17 +207,25 @@ __device__ __forceinline__ TrSlot v_slot(int done, int n, int all) {
     return slot_of(X::K_RING, X::RING - X::K_RING, done + n);
 }
 
-// A whole warp's bounded wait.
+// A whole warp's bounded wait (for two barriers at once: a wait costs its latency
+// even when it is over).
 struct WarpWait {
     TrCtrl &c;
     long long limit;
     bool ok = true;
-    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) {
+    __device__ __forceinline__ bool slow(uint64_t *bar, uint32_t parity) {
         volatile int *abort_flag = &c.abort;
         const bool got = ok && !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, limit);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) *abort_flag = 1;
         return ok;
+    }
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity)) || slow(bar, parity);
+    }
+    __device__ __forceinline__ bool both(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb) {
+        const bool got_b = mbar_try_wait(smem_u32(b), pb), got_a = mbar_try_wait(smem_u32(a), pa);
+        return __all_sync(0xffffffffu, got_a && got_b) || (slow(a, pa) && slow(b, pb));
     }
 };
 
@@ -369,12 +378,13 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
     volatile int *abort_flag = &c.abort;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(smem_u32(bar), parity)) return true;
         ok = ok && !*abort_flag && mbar_wait_bounded(smem_u32(bar), parity, a.wait_limit);
         if (!ok) *abort_flag = 1;
         return ok;
     };
     int done = 0, sel = 0;          // KV tiles before this piece; the next query buffer of one half
-    uint32_t qphase = 0, phase = 0; // of the query barriers; of the P barriers: bits 0 and 1 of either buffer, bit 2 of the halves
+    uint32_t qphase = 0, phase = 0; // of the query barriers; of the P barriers: bits 0 and 1 of shared, 2 and 3 of own buffers
     auto q_wait = [&](int q) {
         const uint32_t now = qphase >> q & 1u;
         qphase ^= 1u << q;
@@ -385,8 +395,10 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
         tc_fence_after_sync();
         return got;
     };
-    auto p_wait = [&](int two, int b) {
-        const bool got = wait(&c.pfull[two][b], phase >> (two ? 2 : b) & 1u);
+    auto p_wait = [&](int own, int b) {
+        const uint32_t now = phase >> (2 * own + b) & 1u;
+        phase ^= 1u << (2 * own + b);
+        const bool got = wait(&c.pfull[own][b], now);
         tc_fence_after_sync();
         return got;
     };
@@ -401,10 +413,44 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                 umma_f16(tmem + b * TR_TOK, dq + h * (X::BLOCK >> 4) + 2 * j, dk + h * (X::BLOCK >> 4) + 2 * j, ID_S,
                          h > 0 || j > 0 ? 1u : 0u);
     };
+                // O_h += the P in buffer h times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
+                auto issue_pv = [&](int h, const TrSlot &k, bool first) {
+                    const uint64_t dv = dv0 + (uint64_t)(k.at * (X::TILE >> 4));
+    #pragma unroll
+                    for (int j = 0; j < TR_TOK / 16; ++j)
+                        umma_f16_ts(tmem + TR_O + h * 128, tmem + h * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4),
+                                    ID_O, !first || j > 0 ? 1u : 0u);
+                    umma_commit(smem_u32(&c.pvdone[1][h]));
+                };
     while (ok && p.next()) {
         const TrPiece x = piece_of(a, p);
         const int N = x.n;
-        if (!x.two) {   // S(n) in buffer n & 1, its columns 64 w .. the warpgroup w's, whose products go to O_w
+        if constexpr (X::F8) {   // tile n in buffer n & 1, the warpgroup's of that number
+            if (!q_wait(sel)) break;
+            for (int n = 0; n < min(N, 2); ++n) {
+                const TrSlot k = k_slot<KV, D>(done, n);
+                if (!ring_wait(k)) break;
+                issue_s(n, sel, k);
+                umma_commit(smem_u32(&c.sfull[1][n]));
+                release(k);
+                if (n + 1 == N) umma_commit(smem_u32(&c.qempty[sel]));
+            }
+            for (int n = 0; ok && n < N; ++n) {
+                const int b = n & 1;
+                const TrSlot v = v_slot<KV, D>(done, n, N), k = k_slot<KV, D>(done, n + 2);
+                if (!p_wait(1, b) || !ring_wait(v)) break;
+                issue_pv(b, v, n < 2);
+                release(v);
+                if (n + 2 < N) {
+                    if (!ring_wait(k)) break;
+                    issue_s(b, sel, k);
+                    umma_commit(smem_u32(&c.sfull[1][b]));
+                    release(k);
+                    if (n + 3 == N) umma_commit(smem_u32(&c.qempty[sel]));
+                }
+            }
+            sel ^= 1;
+        } else if (!x.two) {   // S(n) in buffer n & 1, its columns 64 w .. the warpgroup w's, whose products go to O_w
             const TrSlot k0 = k_slot<KV, D>(done, 0);
             if (!q_wait(sel) || !ring_wait(k0)) break;
             issue_s(0, sel, k0);
@@ -423,7 +469,6 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                     if (n + 2 == N) umma_commit(smem_u32(&c.qempty[sel]));
                 }
                 if (!p_wait(0, b) || !ring_wait(v)) break;
-                phase ^= 1u << b;
                 const uint64_t dv = dv0 + (uint64_t)(v.at * (X::TILE >> 4));
 #pragma unroll
                 for (int j = 0; j < TR_TOK / 16; ++j)   // 16 tokens: P columns 64 w + 8 (j % 4) .., V rows 16 j ..
@@ -434,15 +479,6 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
             }
             sel ^= 1;
         } else {        // half h in buffer h
-            // O_h += P_h times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
-            auto issue_pv = [&](int h, const TrSlot &k, int n) {
-                const uint64_t dv = dv0 + (uint64_t)(k.at * (X::TILE >> 4));
-#pragma unroll
-                for (int j = 0; j < TR_TOK / 16; ++j)
-                    umma_f16_ts(tmem + TR_O + h * 128, tmem + h * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4),
-                                ID_O, n > 0 || j > 0 ? 1u : 0u);
-                umma_commit(smem_u32(&c.pvdone[1][h]));
-            };
             const TrSlot k0 = k_slot<KV, D>(done, 0);
             if (!q_wait(0) || !q_wait(1) || !ring_wait(k0)) break;
             for (int h = 0; h < 2; ++h) {
@@ -456,7 +492,7 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                 const TrSlot v = v_slot<KV, D>(done, n, N), k = k_slot<KV, D>(done, n + 1);
                 for (int h = 0; h < 2; ++h) {
                     if (!p_wait(1, h) || (h == 0 && !ring_wait(v))) break;
-                    issue_pv(h, v, n);
+                    issue_pv(h, v, n == 0);
                     if (h == 1) release(v);
                     if (more) {
                         if (h == 0 && !ring_wait(k)) break;
@@ -466,7 +502,6 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                         if (h == 1) release(k);
                     }
                 }
-                phase ^= 4u;
             }
         }
         done += N;
@@ -476,9 +511,12 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
     mbar_wait_bounded(smem_u32(&c.done), 0, WAIT_LIMIT);
 }
 
-// A softmax warpgroup's state and its way through a piece's tiles, a row per
-// thread: COLS = 64, columns 64 x .. of every tile of a piece of one half (S in turn
-// in either buffer), or 128, all columns of half x.
+// How the two softmax warpgroups share a piece: COLUMNS, each takes 64 columns of
+// every tile (one half; S in turn in either buffer); HALVES, each takes its half's
+// rows; TILES, each takes every second tile (one half).
+enum { COLUMNS, HALVES, TILES };
+
+// A softmax warpgroup's state and its way through a piece's tiles, a row per thread.
 template <int KV, int D>
 struct TrRows {
     using X = Tree<KV, D>;
@@ -489,34 +527,37 @@ struct TrRows {
     uint8_t *smem;
     uint32_t trow, ocol;
     int x, m, lane;
-    uint32_t phase;        // of the S barriers: bits 0 and 1 of either buffer, bit 2 of the half
+    uint32_t phase;        // of the S barriers: bits 0 and 1 of shared buffers, bit 2 of its own
     int done;              // KV tiles before this piece
     float mrun, l;
     bool lost;             // the chain of parents is broken
 
-    template <int COLS>
+    template <int MODE>
     __device__ __forceinline__ void tiles(const Walk<TreeArgs> &p, const TrPiece &pc, bool mine, bool idle, int node,
                                           uint32_t *poison) {
-        constexpr bool TWO = COLS == TR_TOK;
+        constexpr bool SHARED = MODE == COLUMNS;
+        constexpr int COLS = SHARED ? TR_TOK / 2 : TR_TOK;
         const float sl2 = a.scale_log2;
         const int ctx = p.w.L - p.w.T;                 // positions before the tree
         const int32_t *parents = a.parents + p.w.q0;
+        const int first = MODE == TILES ? x : 0, by = MODE == TILES ? 2 : 1;
         mrun = -INFINITY;
         l = 0.f;
         lost = false;
-        for (int n = 0; n < pc.n; ++n) {
-            const int b = TWO ? x : n & 1, bit = TWO ? 2 : b;
+        for (int n = first; n < pc.n; n += by) {
+            const int b = SHARED ? n & 1 : x, bit = SHARED ? b : 2;
             const uint32_t now = phase >> bit & 1u;
-            const uint32_t scol = (uint32_t)(b * TR_TOK + (TWO ? 0 : x * COLS));
-            if (!wait(&c.sfull[TWO][b], now)) return;
-            // the products with this buffer's last P (done when S is; every phase is
-            // seen, so that one waited for later is not taken for another)
-            if (n > (TWO ? 0 : 1) && !wait(&c.pvdone[TWO][b], now ^ 1u)) return;
+            const uint32_t scol = (uint32_t)(b * TR_TOK + (SHARED ? x * COLS : 0));
+            // S, and the products with this buffer's last P (done when S is; every phase
+            // is seen, so that one waited for later is not taken for another)
+            if (n > (SHARED ? 1 : first) ? !wait.both(&c.sfull[!SHARED][b], now, &c.pvdone[!SHARED][b], now ^ 1u)
+                                         : !wait(&c.sfull[!SHARED][b], now))
+                return;
             tc_fence_after_sync();
             const int t0 = (p.t0 + n) * TR_TOK;
             const bool tail = ctx - t0 < TR_TOK;       // the tree's positions begin before the tile ends
             bool changed = false;
-            if (tail && (x == 0 || !TWO)) {
+            if (tail && (x == 0 || MODE != HALVES)) {
                 // Value rows that some row of the row tile does not see, where P is 0
                 // and a product with an infinity or a NaN would not be: those behind the
                 // context are zeroed, and so is what is not finite among the nodes' (the
@@ -528,10 +569,10 @@ struct TrRows {
 #pragma unroll 1
                 for (int h = 0; h < D / 64; ++h) {
                     uint4 *blk = reinterpret_cast<uint4 *>(smem + X::OFF_RING + at.at * X::TILE + h * X::BLOCK) +
-                                 (TWO ? 0 : x * COLS * 8);
+                                 (SHARED ? x * COLS * 8 : 0);
 #pragma unroll 1
                     for (int i = 0; i < COLS / 16; ++i) {   // this thread's chunks m, m + 128, ..: row m / 8 + 16 i
-                        const int r = (TWO ? 0 : x * COLS) + m / 8 + 16 * i;
+                        const int r = (SHARED ? x * COLS : 0) + m / 8 + 16 * i;
                         uint4 &v = blk[m + TR_HALF * i];
                         if (r >= hi) {
                             v = make_uint4(0, 0, 0, 0);
@@ -557,7 +598,7 @@ struct TrRows {
                 tmem_wait_ld();
                 if (tail) {
                     // what the row sees of its columns, a bit each: the context, then its chain
-                    const int c0 = t0 + (TWO ? 0 : x * COLS);
+                    const int c0 = t0 + (SHARED ? x * COLS : 0);
                     uint32_t see[COLS / 32];
 #pragma unroll
                     for (int k = 0; k < COLS / 32; ++k) {
@@ -590,9 +631,9 @@ struct TrRows {
                 if (__any_sync(0xffffffffu, grow)) {
                     const float nm = grow ? mx : mrun;
                     const float alpha = grow ? fast_exp2(mrun - nm) : 1.f;
-                    if (n > 0) {
-                        // two halves: PV(n - 1) is complete, S(n) was issued after it
-                        if (!TWO && !wait(&c.pvdone[0][b ^ 1], (phase >> (b ^ 1) & 1u) ^ 1u)) return;
+                    if (n > first) {
+                        // (a buffer of its own: the last products into O are complete, S(n) was issued after them)
+                        if (SHARED && !wait(&c.pvdone[0][b ^ 1], (phase >> (b ^ 1) & 1u) ^ 1u)) return;
                         tc_fence_after_sync();
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
@@ -635,12 +676,12 @@ struct TrRows {
             if (changed) fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();   // one arrival a warp: 32 atomics on one word hold up the shared-memory pipe
-            if (lane == 0) mbar_arrive(smem_u32(&c.pfull[TWO][b]));
+            if (lane == 0) mbar_arrive(smem_u32(&c.pfull[!SHARED][b]));
             phase ^= 1u << bit;
         }
-        // the last products (and, with one half, those before them)
-        if (TWO) {
-            wait(&c.pvdone[1][x], (phase >> 2 & 1u) ^ 1u);
+        // the last products (and, of shared buffers, those before them)
+        if (!SHARED) {
+            if (first < pc.n) wait(&c.pvdone[1][x], (phase >> 2 & 1u) ^ 1u);
         } else {
             const int b = (pc.n - 1) & 1;
             if (pc.n > 1) wait(&c.pvdone[0][b ^ 1], (phase >> (b ^ 1) & 1u) ^ 1u);
@@ -676,10 +717,12 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
         const int node = pc.node0 + (mm * a.ginv >> 16);
         const int32_t *parents = a.parents + p.w.q0;
         uint32_t *poison = c.poison[p.local & 1];
-        if constexpr (X::ROWS > TR_HALF) {
-            if (pc.two) rows.template tiles<TR_TOK>(p, pc, mine, idle, node, poison);
-        }
-        if (X::ROWS == TR_HALF || !pc.two) rows.template tiles<TR_TOK / 2>(p, pc, mine, idle, node, poison);
+        if constexpr (X::F8)
+            rows.template tiles<TILES>(p, pc, mine, idle, node, poison);
+        else if (pc.two)
+            rows.template tiles<HALVES>(p, pc, mine, idle, node, poison);
+        else
+            rows.template tiles<COLUMNS>(p, pc, mine, idle, node, poison);
         if (!wait.ok) break;
         rows.done += pc.n;
         float mrun = rows.mrun, l = rows.l;
@@ -698,7 +741,8 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                     const int up = parents[j];
                     j = up >= j ? -1 : up;   // (a broken chain has made its row NaN)
                 }
-            // one half: both warpgroups' columns joined, each of them makes half of the dims
+            // one half: what both warpgroups saw joined, each of them makes half of the dims
+            const bool join = !pc.two && (!X::F8 || pc.n > 1);
             float wa = 1.f, wb = 0.f;
             if (!pc.two) {
                 const float2 ma = x == 0 ? make_float2(mrun, l) : other, mb = x == 0 ? other : make_float2(mrun, l);
@@ -720,7 +764,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
             for (int q = q0; q < q1; ++q) {
                 uint32_t o[32];
                 tmem_ld32(trow + (pc.two ? ocol : (uint32_t)TR_O) + 32 * q, o);
-                if (!pc.two) {
+                if (join) {
                     uint32_t o2[32];
                     tmem_ld32(trow + TR_O + 128 + 32 * q, o2);
                     tmem_wait_ld();
@@ -781,10 +825,10 @@ __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&c.qfull[b]), 1);
             mbar_init(smem_u32(&c.qempty[b]), 1);
-            for (int two = 0; two < 2; ++two) {
-                mbar_init(smem_u32(&c.sfull[two][b]), 1);
-                mbar_init(smem_u32(&c.pfull[two][b]), (two ? 1 : 2) * TR_HALF / 32);
-                mbar_init(smem_u32(&c.pvdone[two][b]), 1);
+            for (int own = 0; own < 2; ++own) {
+                mbar_init(smem_u32(&c.sfull[own][b]), 1);
+                mbar_init(smem_u32(&c.pfull[own][b]), (own ? 1 : 2) * TR_HALF / 32);
+                mbar_init(smem_u32(&c.pvdone[own][b]), 1);
             }
             mbar_init(smem_u32(&c.meet[b]), 2 * TR_HALF / 32);
         }
