@@ -18,10 +18,10 @@
 // A row tile of more than 128 rows is two halves, each with its own S, O and
 // softmax warps, that share every tile the CTA loads (PV0(n), S0(n + 1), PV1(n),
 // S1(n + 1): one half's products run while the other's softmax works).  With 128
-// rows or fewer S0 and S1 are two buffers, and each softmax warpgroup has a maximum,
-// a sum and an O of its own, joined at the end: over 16-bit caches they share every
-// tile, 64 columns each, and S(n + 1) is computed meanwhile; over FP8 caches they take
-// every second tile, so that one's exponentials run beside the other's loads and waits.
+// rows or fewer S0 and S1 are two buffers: S(n + 1) is computed while the softmax
+// works on S(n), each of the two warpgroups on 64 of its columns with a maximum, a
+// sum and an O of its own, joined at the end.  (A warpgroup each second tile instead:
+// the same rate over 16-bit caches, 214 us against 193 on the mix over an FP8 cache.)
 //
 // What a node sees of a masked tile is found by walking its chain of parents: a
 // set of 128 bits.  Values that some row does not see are made finite before the
@@ -63,7 +63,7 @@ struct TreeArgs {
     float4 *o;              // [2 AXIS_MAX_CTAS][rows * D / 4] its unnormalised output (see partial_at)
 
     // ---- the work axis: row tile r of a sequence is tile r % per_head of kv head r / per_head
-    static constexpr int COST = 4;
+    static constexpr int COST = 8;   // 64 x 512 .. 16384 tokens, FP8: 194 us with 4, 187 with 8, 188 with 12, 197 with 16
     struct Seq {
         int L, T, q0;
         int per_head;   // row tiles of a kv head
@@ -129,9 +129,9 @@ struct Tree {
     static constexpr int SMEM = OFF_CTRL + CTRL;
     static constexpr int THREADS = F8 ? 512 : 384;
     static constexpr int REGS_LAUNCH = F8 ? 128 : 168;     // per thread: 65536 / threads, rounded down to 8
-    static constexpr int REGS_LOW = F8 ? 72 : 104;         // warps 0 - 3
-    static constexpr int REGS_HIGH = F8 ? 176 : 200;       // the softmax warps
-    static constexpr int REGS_CONV = 88;                   // the converting warps
+    static constexpr int REGS_LOW = 104;                   // warps 0 - 3
+    static constexpr int REGS_HIGH = F8 ? 152 : 200;       // the softmax warps
+    static constexpr int REGS_CONV = 104;                  // the converting warps
     static constexpr int CONV_WARPS = 4;
     static_assert(SMEM <= 227 * 1024, "shared memory of one CTA");
     static_assert(128 * (REGS_LOW + 2 * REGS_HIGH + (F8 ? REGS_CONV : 0)) <= THREADS * REGS_LAUNCH,
@@ -425,32 +425,7 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
     while (ok && p.next()) {
         const TrPiece x = piece_of(a, p);
         const int N = x.n;
-        if constexpr (X::F8) {   // tile n in buffer n & 1, the warpgroup's of that number
-            if (!q_wait(sel)) break;
-            for (int n = 0; n < min(N, 2); ++n) {
-                const TrSlot k = k_slot<KV, D>(done, n);
-                if (!ring_wait(k)) break;
-                issue_s(n, sel, k);
-                umma_commit(smem_u32(&c.sfull[1][n]));
-                release(k);
-                if (n + 1 == N) umma_commit(smem_u32(&c.qempty[sel]));
-            }
-            for (int n = 0; ok && n < N; ++n) {
-                const int b = n & 1;
-                const TrSlot v = v_slot<KV, D>(done, n, N), k = k_slot<KV, D>(done, n + 2);
-                if (!p_wait(1, b) || !ring_wait(v)) break;
-                issue_pv(b, v, n < 2);
-                release(v);
-                if (n + 2 < N) {
-                    if (!ring_wait(k)) break;
-                    issue_s(b, sel, k);
-                    umma_commit(smem_u32(&c.sfull[1][b]));
-                    release(k);
-                    if (n + 3 == N) umma_commit(smem_u32(&c.qempty[sel]));
-                }
-            }
-            sel ^= 1;
-        } else if (!x.two) {   // S(n) in buffer n & 1, its columns 64 w .. the warpgroup w's, whose products go to O_w
+        if (!x.two) {   // S(n) in buffer n & 1, its columns 64 w .. the warpgroup w's, whose products go to O_w
             const TrSlot k0 = k_slot<KV, D>(done, 0);
             if (!q_wait(sel) || !ring_wait(k0)) break;
             issue_s(0, sel, k0);
@@ -513,8 +488,8 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
 
 // How the two softmax warpgroups share a piece: COLUMNS, each takes 64 columns of
 // every tile (one half; S in turn in either buffer); HALVES, each takes its half's
-// rows; TILES, each takes every second tile (one half).
-enum { COLUMNS, HALVES, TILES };
+// rows.
+enum { COLUMNS, HALVES };
 
 // A softmax warpgroup's state and its way through a piece's tiles, a row per thread.
 template <int KV, int D>
@@ -540,24 +515,23 @@ struct TrRows {
         const float sl2 = a.scale_log2;
         const int ctx = p.w.L - p.w.T;                 // positions before the tree
         const int32_t *parents = a.parents + p.w.q0;
-        const int first = MODE == TILES ? x : 0, by = MODE == TILES ? 2 : 1;
         mrun = -INFINITY;
         l = 0.f;
         lost = false;
-        for (int n = first; n < pc.n; n += by) {
+        for (int n = 0; n < pc.n; ++n) {
             const int b = SHARED ? n & 1 : x, bit = SHARED ? b : 2;
             const uint32_t now = phase >> bit & 1u;
             const uint32_t scol = (uint32_t)(b * TR_TOK + (SHARED ? x * COLS : 0));
             // S, and the products with this buffer's last P (done when S is; every phase
             // is seen, so that one waited for later is not taken for another)
-            if (n > (SHARED ? 1 : first) ? !wait.both(&c.sfull[!SHARED][b], now, &c.pvdone[!SHARED][b], now ^ 1u)
+            if (n > (SHARED ? 1 : 0) ? !wait.both(&c.sfull[!SHARED][b], now, &c.pvdone[!SHARED][b], now ^ 1u)
                                          : !wait(&c.sfull[!SHARED][b], now))
                 return;
             tc_fence_after_sync();
             const int t0 = (p.t0 + n) * TR_TOK;
             const bool tail = ctx - t0 < TR_TOK;       // the tree's positions begin before the tile ends
             bool changed = false;
-            if (tail && (x == 0 || MODE != HALVES)) {
+            if (tail && (x == 0 || SHARED)) {
                 // Value rows that some row of the row tile does not see, where P is 0
                 // and a product with an infinity or a NaN would not be: those behind the
                 // context are zeroed, and so is what is not finite among the nodes' (the
@@ -631,7 +605,7 @@ struct TrRows {
                 if (__any_sync(0xffffffffu, grow)) {
                     const float nm = grow ? mx : mrun;
                     const float alpha = grow ? fast_exp2(mrun - nm) : 1.f;
-                    if (n > first) {
+                    if (n > 0) {
                         // (a buffer of its own: the last products into O are complete, S(n) was issued after them)
                         if (SHARED && !wait(&c.pvdone[0][b ^ 1], (phase >> (b ^ 1) & 1u) ^ 1u)) return;
                         tc_fence_after_sync();
@@ -681,7 +655,7 @@ struct TrRows {
         }
         // the last products (and, of shared buffers, those before them)
         if (!SHARED) {
-            if (first < pc.n) wait(&c.pvdone[1][x], (phase >> 2 & 1u) ^ 1u);
+            wait(&c.pvdone[1][x], (phase >> 2 & 1u) ^ 1u);
         } else {
             const int b = (pc.n - 1) & 1;
             if (pc.n > 1) wait(&c.pvdone[0][b ^ 1], (phase >> (b ^ 1) & 1u) ^ 1u);
@@ -717,12 +691,10 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
         const int node = pc.node0 + (mm * a.ginv >> 16);
         const int32_t *parents = a.parents + p.w.q0;
         uint32_t *poison = c.poison[p.local & 1];
-        if constexpr (X::F8)
-            rows.template tiles<TILES>(p, pc, mine, idle, node, poison);
-        else if (pc.two)
-            rows.template tiles<HALVES>(p, pc, mine, idle, node, poison);
-        else
-            rows.template tiles<COLUMNS>(p, pc, mine, idle, node, poison);
+        if constexpr (!X::F8) {
+            if (pc.two) rows.template tiles<HALVES>(p, pc, mine, idle, node, poison);
+        }
+        if (X::F8 || !pc.two) rows.template tiles<COLUMNS>(p, pc, mine, idle, node, poison);
         if (!wait.ok) break;
         rows.done += pc.n;
         float mrun = rows.mrun, l = rows.l;
@@ -742,7 +714,6 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
                     j = up >= j ? -1 : up;   // (a broken chain has made its row NaN)
                 }
             // one half: what both warpgroups saw joined, each of them makes half of the dims
-            const bool join = !pc.two && (!X::F8 || pc.n > 1);
             float wa = 1.f, wb = 0.f;
             if (!pc.two) {
                 const float2 ma = x == 0 ? make_float2(mrun, l) : other, mb = x == 0 ? other : make_float2(mrun, l);
@@ -764,7 +735,7 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
             for (int q = q0; q < q1; ++q) {
                 uint32_t o[32];
                 tmem_ld32(trow + (pc.two ? ocol : (uint32_t)TR_O) + 32 * q, o);
-                if (join) {
+                if (!pc.two) {
                     uint32_t o2[32];
                     tmem_ld32(trow + TR_O + 128 + 32 * q, o2);
                     tmem_wait_ld();
