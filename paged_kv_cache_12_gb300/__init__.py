@@ -698,33 +698,41 @@ def pa_verify_drafts(accepted, tokens, target_probs, draft_probs, draft_tokens, 
 
 # ---------------------------------------------------------------- rotary positions, trees of drafted tokens
 
-def _kv_caches(torch, where, k_cache, v_cache, ndim):
-    """(PA_KV_*, torch dtype of queries, keys and values, device index) of a pair of caches of `ndim` dimensions."""
-    dt = k_cache.dtype
-    if dt is torch.float16 or dt is torch.bfloat16:
-        kv, row = (PA_KV_F16 if dt is torch.float16 else PA_KV_BF16), dt
-    elif dt is torch.uint8 or dt is getattr(torch, "float8_e4m3fn", None):
-        kv, row = PA_KV_FP8_E4M3, torch.float16
-    else:
-        raise ValueError(f"{where}: unsupported cache dtype {dt}")
-    dev = k_cache.get_device()
-    _need_on(where, dev, k_cache, "k_cache", dt, ndim)
-    _need_on(where, dev, v_cache, "v_cache", dt, ndim)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError(f"{where}: shape mismatch")
-    return kv, row, dev
+# These calls run once a layer and step, and each question to a tensor takes 50 to
+# 120 ns: a call asks them in one expression, and only when that fails asks again, one
+# by one, for the message.
+
+def _kv_cache_type(torch, where, cache):
+    """(PA_KV_*, torch dtype of queries, keys and values) of a K or V cache tensor."""
+    dt = cache.dtype
+    if dt is torch.bfloat16:
+        return PA_KV_BF16, dt
+    if dt is torch.float16:
+        return PA_KV_F16, dt
+    if dt is torch.uint8 or dt is getattr(torch, "float8_e4m3fn", None):
+        return PA_KV_FP8_E4M3, torch.float16
+    raise ValueError(f"{where}: unsupported cache dtype {dt}")
+
+
+def _mismatch(where, dev, *tensors):
+    """Raise for the first of (tensor, name, dtype, dimensions) that is not a
+    contiguous tensor of that kind on the device, else for their shapes."""
+    for t, name, dtype, ndim in tensors:
+        _need_on(where, dev, t, name, dtype, ndim)
+    raise ValueError(f"{where}: shape mismatch")
 
 
 def _token_stride(where, dev, t, name, dtype, shape):
     """The token stride of [tokens, heads, head_dim] rows whose heads lie side by side (slices of one projection's
     rows, for instance); the tensor must have the shape."""
+    n, heads, d = shape
     st = t.stride()
-    if t.get_device() != dev or dev < 0 or t.dtype is not dtype or t.dim() != 3 or \
-            (t.numel() > 0 and ((st[2] != 1 and shape[2] > 1) or (st[1] != shape[2] and shape[1] > 1))):
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0 or len(st) != 3 or \
+            ((st[2] != 1 or st[1] != d) and t.numel() > 0 and ((st[2] != 1 and d > 1) or (st[1] != d and heads > 1))):
         _refuse(where, dev, t, name, dtype, 3, "each token's heads contiguous")
     if t.shape != shape:
         raise ValueError(f"{where}: shape mismatch")
-    return st[0] if shape[0] > 1 else shape[1] * shape[2]
+    return st[0] if n > 1 else heads * d
 
 
 def pa_kv_write_rope(key, value, positions, inv_freq, slot_mapping, k_cache, v_cache, query=None, query_out=None,
@@ -737,37 +745,44 @@ def pa_kv_write_rope(key, value, positions, inv_freq, slot_mapping, k_cache, v_c
     queries go to query_out, or to query itself without one."""
     import torch
     where, i32 = "pa_kv_write_rope", torch.int32
-    kv, dt, dev = _kv_caches(torch, where, k_cache, v_cache, 4)
-    nb, hk, bs, d = k_cache.shape
-    n = key.shape[0]
-    sk = _token_stride(where, dev, key, "key", dt, (n, hk, d))
-    sv = _token_stride(where, dev, value, "value", dt, (n, hk, d))
+    kv, dt = _kv_cache_type(torch, where, k_cache)
+    dev, held = k_cache.get_device(), k_cache.shape
+    pos, n, pairs = positions.shape, key.shape[0], inv_freq.shape[0]
+    if len(held) != 4 or v_cache.shape != held or v_cache.dtype is not k_cache.dtype or v_cache.get_device() != dev or \
+            dev < 0 or not k_cache.is_contiguous() or not v_cache.is_contiguous() or \
+            positions.dtype is not i32 or positions.get_device() != dev or not positions.is_contiguous() or \
+            len(pos) not in (1, 2) or pos[-1] != n or \
+            inv_freq.dtype is not torch.float32 or inv_freq.get_device() != dev or inv_freq.stride() != (1,) or \
+            slot_mapping.dtype is not torch.int64 or slot_mapping.get_device() != dev or \
+            not slot_mapping.is_contiguous() or slot_mapping.shape != (n,):
+        _mismatch(where, dev, (k_cache, "k_cache", k_cache.dtype, 4), (v_cache, "v_cache", k_cache.dtype, 4),
+                  (positions, "positions", i32, 1 if len(pos) == 1 else 2), (inv_freq, "inv_freq", torch.float32, 1),
+                  (slot_mapping, "slot_mapping", torch.int64, 1))
+    ax = None
+    if pair_axis is not None:
+        if pair_axis.dtype is not i32 or pair_axis.get_device() != dev or not pair_axis.is_contiguous() or \
+                pair_axis.shape != (pairs,):
+            _mismatch(where, dev, (pair_axis, "pair_axis", i32, 1))
+        ax = pair_axis.data_ptr()
+    nb, hk, bs, d = held
+    rows = (n, hk, d)
+    sk = _token_stride(where, dev, key, "key", dt, rows)
+    sv = _token_stride(where, dev, value, "value", dt, rows)
     hq = sq = so = 0
     qi = qo = None
     if query is not None:
         hq = query.shape[1]
-        sq = _token_stride(where, dev, query, "query", dt, (n, hq, d))
-        if query_out is None:
-            query_out, so = query, sq
-        else:
-            so = _token_stride(where, dev, query_out, "query_out", dt, (n, hq, d))
-        qi, qo = query.data_ptr(), query_out.data_ptr()
+        rows = (n, hq, d)
+        sq = so = _token_stride(where, dev, query, "query", dt, rows)
+        qi = qo = query.data_ptr()
+        if query_out is not None:
+            so = _token_stride(where, dev, query_out, "query_out", dt, rows)
+            qo = query_out.data_ptr()
     elif query_out is not None:
         raise ValueError(f"{where}: query_out without query")
-    _need_on(where, dev, positions, "positions", i32, 1 if positions.dim() == 1 else 2)
-    _need_on(where, dev, inv_freq, "inv_freq", torch.float32, 1)
-    _need_on(where, dev, slot_mapping, "slot_mapping", torch.int64, 1)
-    pairs = inv_freq.shape[0]
-    if pair_axis is not None:
-        _need_on(where, dev, pair_axis, "pair_axis", i32, 1)
-        if pair_axis.shape[0] != pairs:
-            raise ValueError(f"{where}: shape mismatch")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.shape[-1] != n or slot_mapping.shape[0] != n:
-        raise ValueError(f"{where}: shape mismatch")
-    _run(where, dev, stream, qo, qi, key.data_ptr(), value.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
-         None if pair_axis is None else pair_axis.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(),
-         v_cache.data_ptr(), n, hq, hk, d, 2 * pairs, axes, 1 if interleaved else 0, sq, so, sk, sv, bs, nb, kv,
+    _run(where, dev, stream, qo, qi, key.data_ptr(), value.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), ax,
+         slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), n, hq, hk, d, 2 * pairs,
+         1 if len(pos) == 1 else pos[0], 1 if interleaved else 0, sq, so, sk, sv, bs, nb, kv,
          float(k_scale), float(v_scale))
 
 
@@ -789,24 +804,32 @@ def pa_attention_tree(out, query, k_cache, v_cache, block_tables, context_lens, 
     Caches of fp16, bf16 or fp8 E4M3 codes as in pa_attention_causal_typed."""
     import torch
     where, i32 = "pa_attention_tree", torch.int32
-    kv, dt, dev = _kv_caches(torch, where, k_cache, v_cache, 4)
-    _need_on(where, dev, out, "out", dt, 3)
-    _need_on(where, dev, query, "query", dt, 3)
-    _need_on(where, dev, block_tables, "block_tables", i32, 2)
-    _need_on(where, dev, context_lens, "context_lens", i32, 1)
-    _need_on(where, dev, query_start, "query_start", i32, 1)
-    _need_on(where, dev, parents, "parents", i32, 1)
-    _need_on(where, dev, workspace, "workspace", torch.uint8, 1)
-    nb, hk, bs, d = k_cache.shape
-    nq, hq, w = query.shape
-    b, mb = block_tables.shape
-    if out.shape != query.shape or w != d or context_lens.shape[0] != b or query_start.shape[0] != b + 1 or \
-            parents.shape[0] != nq:
-        raise ValueError(f"{where}: shape mismatch")
+    kv, dt = _kv_cache_type(torch, where, k_cache)
+    dev, held, rows, tab = k_cache.get_device(), k_cache.shape, query.shape, block_tables.shape
+    if len(held) != 4 or v_cache.shape != held or v_cache.dtype is not k_cache.dtype or v_cache.get_device() != dev or \
+            dev < 0 or not k_cache.is_contiguous() or not v_cache.is_contiguous() or \
+            len(rows) != 3 or rows[2] != held[3] or query.dtype is not dt or query.get_device() != dev or \
+            not query.is_contiguous() or \
+            out.shape != rows or out.dtype is not dt or out.get_device() != dev or not out.is_contiguous() or \
+            len(tab) != 2 or block_tables.dtype is not i32 or block_tables.get_device() != dev or \
+            not block_tables.is_contiguous() or \
+            context_lens.shape != (tab[0],) or context_lens.dtype is not i32 or context_lens.get_device() != dev or \
+            not context_lens.is_contiguous() or \
+            query_start.shape != (tab[0] + 1,) or query_start.dtype is not i32 or query_start.get_device() != dev or \
+            not query_start.is_contiguous() or \
+            parents.shape != (rows[0],) or parents.dtype is not i32 or parents.get_device() != dev or \
+            not parents.is_contiguous() or \
+            workspace.dtype is not torch.uint8 or workspace.get_device() != dev or workspace.dim() != 1 or \
+            not workspace.is_contiguous():
+        _mismatch(where, dev, (k_cache, "k_cache", k_cache.dtype, 4), (v_cache, "v_cache", k_cache.dtype, 4),
+                  (query, "query", dt, 3), (out, "out", dt, 3), (block_tables, "block_tables", i32, 2),
+                  (context_lens, "context_lens", i32, 1), (query_start, "query_start", i32, 1),
+                  (parents, "parents", i32, 1), (workspace, "workspace", torch.uint8, 1))
+    nb, hk, bs, d = held
     _run(where, dev, stream, out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-         block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), parents.data_ptr(), b, nq, hq, hk, d,
-         bs, nb, mb, int(max_context_len), float(scale), kv, float(k_scale), float(v_scale), workspace.data_ptr(),
-         workspace.shape[0])
+         block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), parents.data_ptr(), tab[0], rows[0],
+         rows[1], hk, d, bs, nb, tab[1], int(max_context_len), float(scale), kv, float(k_scale), float(v_scale),
+         workspace.data_ptr(), workspace.shape[0])
 
 
 def pa_verify_tree(accepted, tokens, path, target_probs, node_tokens, parents, tree_start, uniform, stream=None):
@@ -824,20 +847,26 @@ def pa_verify_tree(accepted, tokens, path, target_probs, node_tokens, parents, t
     if kind < 0:
         raise ValueError(f"{where}: target_probs must be float32, float16 or bfloat16")
     st = _need_rows(where, dev, target_probs, "target_probs", dt, 2)[0]
-    _need_on(where, dev, accepted, "accepted", i32, 1)
-    _need_on(where, dev, tokens, "tokens", i32, 2)
-    _need_on(where, dev, path, "path", i32, 2)
-    _need_on(where, dev, node_tokens, "node_tokens", i32, 1)
-    _need_on(where, dev, parents, "parents", i32, 1)
-    _need_on(where, dev, tree_start, "tree_start", i32, 1)
-    _need_on(where, dev, uniform, "uniform", f32, 1)
     n, v = target_probs.shape
-    b, width = tokens.shape
-    if accepted.shape[0] != b or path.shape != tokens.shape or width < 1 or node_tokens.shape[0] != n or \
-            parents.shape[0] != n or uniform.shape[0] != n or tree_start.shape[0] != b + 1:
-        raise ValueError(f"{where}: shape mismatch")
+    out = tokens.shape
+    if len(out) != 2 or out[1] < 1 or tokens.dtype is not i32 or tokens.get_device() != dev or \
+            not tokens.is_contiguous() or \
+            path.shape != out or path.dtype is not i32 or path.get_device() != dev or not path.is_contiguous() or \
+            accepted.shape != (out[0],) or accepted.dtype is not i32 or accepted.get_device() != dev or \
+            not accepted.is_contiguous() or \
+            node_tokens.shape != (n,) or node_tokens.dtype is not i32 or node_tokens.get_device() != dev or \
+            not node_tokens.is_contiguous() or \
+            parents.shape != (n,) or parents.dtype is not i32 or parents.get_device() != dev or \
+            not parents.is_contiguous() or \
+            tree_start.shape != (out[0] + 1,) or tree_start.dtype is not i32 or tree_start.get_device() != dev or \
+            not tree_start.is_contiguous() or \
+            uniform.shape != (n,) or uniform.dtype is not f32 or uniform.get_device() != dev or \
+            not uniform.is_contiguous():
+        _mismatch(where, dev, (accepted, "accepted", i32, 1), (tokens, "tokens", i32, 2), (path, "path", i32, 2),
+                  (node_tokens, "node_tokens", i32, 1), (parents, "parents", i32, 1), (tree_start, "tree_start", i32, 1),
+                  (uniform, "uniform", f32, 1))
     _run(where, dev, stream, accepted.data_ptr(), tokens.data_ptr(), path.data_ptr(), target_probs.data_ptr(),
-         node_tokens.data_ptr(), parents.data_ptr(), tree_start.data_ptr(), uniform.data_ptr(), b, n, width - 1, v,
+         node_tokens.data_ptr(), parents.data_ptr(), tree_start.data_ptr(), uniform.data_ptr(), out[0], n, out[1] - 1, v,
          st if n > 1 else v, kind)
 
 
@@ -849,20 +878,28 @@ def pa_kv_move_path(k_cache, v_cache, block_tables, context_lens, query_start, p
     [num_seqs, max_depth + 1] and accepted as pa_verify_tree wrote them."""
     import torch
     where, i32 = "pa_kv_move_path", torch.int32
-    kv, _, dev = _kv_caches(torch, where, k_cache, v_cache, 5 if k_cache.dim() == 5 else 4)
-    nb, hk, bs, d = k_cache.shape[-4:]
-    _need_on(where, dev, block_tables, "block_tables", i32, 2)
-    _need_on(where, dev, context_lens, "context_lens", i32, 1)
-    _need_on(where, dev, query_start, "query_start", i32, 1)
-    _need_on(where, dev, path, "path", i32, 2)
-    _need_on(where, dev, accepted, "accepted", i32, 1)
-    b, mb = block_tables.shape
-    if context_lens.shape[0] != b or query_start.shape[0] != b + 1 or path.shape[0] != b or path.shape[1] < 1 or \
-            accepted.shape[0] != b:
-        raise ValueError(f"{where}: shape mismatch")
+    kv, _ = _kv_cache_type(torch, where, k_cache)
+    dev, held, tab, ways = k_cache.get_device(), k_cache.shape, block_tables.shape, path.shape
+    if len(held) not in (4, 5) or v_cache.shape != held or v_cache.dtype is not k_cache.dtype or \
+            v_cache.get_device() != dev or dev < 0 or not k_cache.is_contiguous() or not v_cache.is_contiguous() or \
+            len(tab) != 2 or block_tables.dtype is not i32 or block_tables.get_device() != dev or \
+            not block_tables.is_contiguous() or \
+            context_lens.shape != (tab[0],) or context_lens.dtype is not i32 or context_lens.get_device() != dev or \
+            not context_lens.is_contiguous() or \
+            query_start.shape != (tab[0] + 1,) or query_start.dtype is not i32 or query_start.get_device() != dev or \
+            not query_start.is_contiguous() or \
+            len(ways) != 2 or ways[0] != tab[0] or ways[1] < 1 or path.dtype is not i32 or path.get_device() != dev or \
+            not path.is_contiguous() or \
+            accepted.shape != (tab[0],) or accepted.dtype is not i32 or accepted.get_device() != dev or \
+            not accepted.is_contiguous():
+        _mismatch(where, dev, (k_cache, "k_cache", k_cache.dtype, 5 if len(held) == 5 else 4),
+                  (v_cache, "v_cache", k_cache.dtype, 5 if len(held) == 5 else 4),
+                  (block_tables, "block_tables", i32, 2), (context_lens, "context_lens", i32, 1),
+                  (query_start, "query_start", i32, 1), (path, "path", i32, 2), (accepted, "accepted", i32, 1))
+    nb, hk, bs, d = held[-4:]
     _run(where, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-         query_start.data_ptr(), path.data_ptr(), accepted.data_ptr(), b, path.shape[1] - 1,
-         k_cache.shape[0] if k_cache.dim() == 5 else 1, hk, d, bs, nb, mb, kv)
+         query_start.data_ptr(), path.data_ptr(), accepted.data_ptr(), tab[0], ways[1] - 1,
+         held[0] if len(held) == 5 else 1, hk, d, bs, nb, tab[1], kv)
 
 
 # ---------------------------------------------------------------- allocator
