@@ -290,6 +290,16 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_RESIDENT) rope_write_kernel
     }
 }
 
+// PA_DEBUG_VALIDATE: every pair's axis is one of the positions'.
+int validate_axes(const int32_t *pair_axis, int pairs, int num_axes, cudaStream_t st) {
+    int32_t axis[ROPE_MAX_DIM / 2];
+    if (!pair_axis) return 0;
+    if (const int e = copy_to_host(axis, pair_axis, sizeof(int32_t) * (size_t)pairs, st)) return e;
+    for (int i = 0; i < pairs; ++i)
+        if (axis[i] < 0 || axis[i] >= num_axes) return PA_ERR_INVALID_ARG;
+    return 0;
+}
+
 template <int KV>
 int launch_rope(const RopeArgs &a, cudaStream_t st) {
     const dim3 ctas((unsigned)std::min(a.num_tokens, ROPE_RESIDENT * num_sms()));
@@ -316,8 +326,8 @@ extern "C" int pa_kv_write_rope(void *query_out, const void *query, const void *
     if (kv_dtype == PA_KV_FP8_E4M3 &&
         (!std::isfinite(k_scale) || !(k_scale > 0.f) || !std::isfinite(v_scale) || !(v_scale > 0.f)))
         return PA_ERR_INVALID_ARG;
-    // a token's pieces of work are counted in 32 bits
-    if (rope_dim > ROPE_MAX_DIM || head_dim > ROPE_MAX_HEAD || (long long)(num_heads + 2LL * num_kv_heads) * head_dim >= (1LL << 30))
+    // tokens, and a token's elements, are counted in 32 bits
+    if (num_tokens > (1 << 30) || rope_dim > ROPE_MAX_DIM || head_dim > ROPE_MAX_HEAD || (long long)(num_heads + 2LL * num_kv_heads) * head_dim >= (1LL << 30))
         return PA_ERR_UNSUPPORTED;
     const long long q_row = (long long)num_heads * head_dim, k_row = (long long)num_kv_heads * head_dim;
     if (query_stride < q_row || query_out_stride < q_row || key_stride < k_row || value_stride < k_row ||
@@ -359,8 +369,10 @@ extern "C" int pa_kv_write_rope(void *query_out, const void *query, const void *
         a.kinv = 1.0f / k_scale;
         a.vinv = 1.0f / v_scale;
     }
-    if (debug_validate())
+    if (debug_validate()) {
         if (const int e = validate_slots(slot_mapping, num_tokens, a.num_slots, st)) return e;
+        if (const int e = validate_axes(pair_axis, rope_dim / 2, num_axes, st)) return e;
+    }
     if (kv_dtype == PA_KV_F16) return launch_rope<PA_KV_F16>(a, st);
     if (kv_dtype == PA_KV_BF16) return launch_rope<PA_KV_BF16>(a, st);
     return launch_rope<PA_KV_FP8_E4M3>(a, st);

@@ -241,8 +241,9 @@ struct Draw {
 // the total.  `ctas` CTAs of the cluster from rank `leader` on do it, all CTAs of the
 // cluster take part in its meetings; the token is in *next (in the leader's shared
 // memory, -1 before) after the cluster's next meeting.  Returns the slice in which it
-// lies, -1 where there is none, or `empty` where the weights sum to zero.
-template <typename T, class Range>
+// lies, -1 where there is none, or `empty` where the weights sum to zero.  DEEP: parts of
+// the slice are cut again while they are long (a row's slices are, where few CTAs have it).
+template <typename T, bool DEEP, class Range>
 __device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader, int ctas, Draw &sh, int *next,
                                           const Weights<T> &w, int vocab, const float *u, int empty, Range range) {
     const int rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -299,30 +300,40 @@ __device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader
                                         *cluster.map_shared_rank(&sh.height, leader));
             if (lane == 0) *cluster.map_shared_rank(next, leader) = v;
         }
-    } else if (rank == leader && slice >= 0) {   // the slice again, in parts
-        const int first = slice * len, part = (len / VCHUNK + VWARPS - 1) / VWARPS * VCHUNK;
-        const int plo = min(vocab, min(first + len, first + warp * part));
-        const int phi = min(vocab, min(first + len, plo + part));
-        const Sum2 mine = range(w, plo, phi);
-        if (lane == 0) sh.totals[warp] = mine;
-        __syncthreads();
-        Sum2 run = sh.before, before = run;
-        int at = -1;       // the first part that passes, else the last of any weight
-        bool passed = false;
-        for (int k = 0; k < VWARPS; ++k) {
-            const Sum2 x = sh.totals[k];
-            Sum2 after = run;
-            after.add(x);
-            if (!passed && x.any()) {
-                at = k;
-                before = run;
-                passed = sh.height.passed_by(after);
+    } else if (rank == leader && slice >= 0) {   // the slice again, in parts, until a part is short
+        int first = slice * len, n = len;
+        Sum2 before = sh.before;
+        for (;;) {
+            const int part = ((n + VWARPS - 1) / VWARPS + VCHUNK - 1) / VCHUNK * VCHUNK;
+            const int plo = min(vocab, min(first + n, first + warp * part));
+            const int phi = min(vocab, min(first + n, plo + part));
+            const Sum2 mine = range(w, plo, phi);
+            if (lane == 0) sh.totals[warp] = mine;
+            __syncthreads();
+            Sum2 run = before;
+            int at = -1;       // the first part that passes, else the last of any weight
+            bool passed = false;
+            for (int k = 0; k < VWARPS; ++k) {
+                const Sum2 x = sh.totals[k];
+                Sum2 after = run;
+                after.add(x);
+                if (!passed && x.any()) {
+                    at = k;
+                    before = run;
+                    passed = sh.height.passed_by(after);
+                }
+                run = after;
             }
-            run = after;
-        }
-        if (warp == at) {
-            const int v = find_in_range(w, plo, phi, before, sh.height);
-            if (lane == 0) *next = v;
+            if (!DEEP || at < 0 || part <= 2 * VCHUNK) {
+                if (warp == at) {
+                    const int v = find_in_range(w, plo, phi, before, sh.height);
+                    if (lane == 0) *next = v;
+                }
+                break;
+            }
+            n = min(part, n - at * part);
+            first += at * part;
+            __syncthreads();   // the totals have been read
         }
     }
     return slice;
@@ -385,7 +396,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         Weights<T> w(p, q, failed && !a.draft ? a.draft_tokens[d0 + kept] : -1);
         for (int attempt = 0; attempt < 2; ++attempt) {
             const int slice =
-                draw_token<T>(cluster, 0, VCTAS, draw, &s_next, w, a.vocab, a.sample + seq, attempt == 0 && failed ? -2 : -1,
+                draw_token<T, false>(cluster, 0, VCTAS, draw, &s_next, w, a.vocab, a.sample + seq, attempt == 0 && failed ? -2 : -1,
                               [](const Weights<T> &x, int lo, int hi) { return range_sum(x, lo, hi); });
             if (slice != -2) break;
             w = Weights<T>(p, nullptr, -1);   // q covers p: draw from p itself
@@ -453,7 +464,10 @@ __device__ __forceinline__ void add16(Sum2Pair &acc, uint4 v, __half) {
 }
 
 // range_sum of a row's own weights, with more bytes on their way: 16 at a time
-// from the first 16-byte boundary on, whatever the row's alignment.
+// from the first 16-byte boundary on, whatever the row's alignment.  Eight loads and
+// one sum are what 64 registers hold (64 sequences of 131072 tokens in bf16, mean of
+// eight draws: 54.5 us; with two and four sums 56 and 65, four loads 77; through
+// shared memory cells with two sums 57).
 constexpr int VLOADS = 8;
 template <typename T>
 __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
@@ -495,13 +509,20 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
     __shared__ int s_next[2];   // by the wave's parity: a CTA may still read one wave's tokens while the next is drawn
     __shared__ int s_nodes[VMAX_CTAS], s_count;
     __shared__ int s_node, s_level;
+    __shared__ int32_t s_parents[PA_TREE_MAX_NODES], s_tokens[PA_TREE_MAX_NODES];   // of the tree's first nodes
     grid_release();
     grid_wait();
     const int n0 = a.tree_start[seq], n1 = a.tree_start[seq + 1];
     const bool ok = n0 >= 0 && n1 > n0 && n1 <= a.num_nodes && (seq > 0 || n0 == 0) &&
                     (seq < a.num_seqs - 1 || n1 == a.num_nodes);
     const int n = n1 - n0;
-    const int32_t *parents = a.parents + n0, *drafted = a.node_tokens + n0;
+    auto parent = [&](int j) { return j < PA_TREE_MAX_NODES ? s_parents[j] : a.parents[n0 + j]; };
+    auto drafted = [&](int j) { return j < PA_TREE_MAX_NODES ? s_tokens[j] : a.node_tokens[n0 + j]; };
+    for (int j = threadIdx.x; ok && j < min(n, PA_TREE_MAX_NODES); j += VTHREADS) {
+        s_parents[j] = a.parents[n0 + j];
+        s_tokens[j] = a.node_tokens[n0 + j];
+    }
+    __syncthreads();
     int32_t *tokens = a.tokens + (long long)seq * (a.max_depth + 1);
     int32_t *path = a.path + (long long)seq * (a.max_depth + 1);
     // everything here is the same in every CTA of the cluster
@@ -511,7 +532,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         if (warp == 0) {   // the present node and the first of its descendants, in the order of their numbers
             int mine = lane == 0 ? node : -1, count = 1;   // lane i: the i-th of them
             for (int base = node + 1; count < most && base < n; base += 32) {
-                const int p = base + lane < n ? parents[base + lane] : -1;
+                const int p = base + lane < n ? parent(base + lane) : -1;
                 bool taken = false;
                 for (int i = 0; i < count && count < most; ++i) {   // (a parent comes before its children)
                     const int node_i = __shfl_sync(0xffffffffu, mine, i);   // (by every lane)
@@ -533,7 +554,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         const bool has = group < s_count;   // a group without a node has no row either
         const int who = has ? s_nodes[group] : node;
         const T *p = static_cast<const T *>(a.target) + (long long)(n0 + who) * a.target_stride;
-        draw_token<T>(cluster, leader, ctas, draw, next, Weights<T>(p, nullptr, -1), has ? a.vocab : 0, a.uniform + n0 + who,
+        draw_token<T, true>(cluster, leader, ctas, draw, next, Weights<T>(p, nullptr, -1), has ? a.vocab : 0, a.uniform + n0 + who,
                       -1, [](const Weights<T> &x, int lo, int hi) { return row_sum(x.p, lo, hi); });
         cluster.sync();   // the tokens are there
         if (warp == 0) {
@@ -550,7 +571,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
                 int child = -1;
                 for (int base = cur + 1; v >= 0 && lv < a.max_depth && base < n; base += 32) {
                     const int j = base + lane;
-                    const unsigned has = __ballot_sync(0xffffffffu, j < n && parents[j] == cur && drafted[j] == v);
+                    const unsigned has = __ballot_sync(0xffffffffu, j < n && parent(j) == cur && drafted(j) == v);
                     if (has) {
                         child = base + __ffs((int)has) - 1;
                         break;

@@ -1,4 +1,9 @@
 """pa_attention_tree against attention in 64 bits (bounds derived in tree_ref.tree_attention)."""
+import os
+import subprocess
+import sys
+import textwrap
+
 import numpy as np
 import pytest
 import torch
@@ -341,3 +346,60 @@ def test_refusals():
     refused(workspace=base["workspace"][:100])
     refused(workspace=base["workspace"].cpu())
     refused(k_cache=s["k"].view(torch.uint8)[..., :64].contiguous(), v_cache=s["v"].view(torch.uint8)[..., :64].contiguous())
+
+
+def test_pieces_of_one_and_two_halves_in_one_range():
+    # row tiles of more than 128 rows between shorter ones, several of them a CTA, cut
+    # or not, in an order that gives every CTA both kinds; with infinities and NaN in
+    # the values of nodes that are no ancestors
+    rng = np.random.default_rng(12)
+    counts = [int(x) for x in rng.choice([1, 3, 16, 17, 20, 33, 48, 64], 90)]
+    past = [int(x) for x in rng.integers(0, 700, 90)]
+    s = case(pa.PA_KV_BF16, [c + p for c, p in zip(counts, past)], trees(counts, 5), 64, 8, 128, 16, seed=31)
+    out = run(s)
+    check(s, out)
+    for i in range(0, 90, 7):   # a leaf of every seventh tree
+        leaf, pos = counts[i] - 1, past[i] + counts[i] - 1
+        s["v"][int(s["tables"][i, pos // 16]), :, pos % 16, 9] = float("nan" if i % 2 else "inf")
+        row = s["start"][i] + leaf
+        out[row] = float("nan")
+    again = run(s)
+    nan = torch.isnan(out).all(dim=-1)
+    assert torch.equal(again[~nan], out[~nan])
+    assert (~torch.isfinite(again[nan])).any(dim=-1).all()
+
+
+def test_waits_that_run_out():
+    # PA_WAIT_LIMIT_CYCLES (read once, so in a process of its own) at one clock: a
+    # wait that is not over when it first returns gives up.  A call either comes out
+    # as usual, or reports PA_ERR_TIMEOUT with NaN in every row; the context is
+    # usable after each
+    code = textwrap.dedent("""
+        import sys, numpy as np, torch
+        sys.path[:0] = [%r, %r]
+        import latent_ref as R
+        import paged_kv_cache_12_gb300 as pa
+        import test_gpu_tree as TT
+        seen = []
+        for kv in R.KVS:
+            for hq, hk in ((8, 2), (64, 8)):
+                counts = [5, 40, 1, 17, 64]
+                s = TT.case(kv, [c + p for c, p in zip(counts, [3000, 100, 0, 900, 5000])], TT.trees(counts), hq, hk, 128, 16)
+                ws = TT.workspace(s)
+                for _ in range(3):
+                    out = torch.zeros_like(s["q"])
+                    scales = dict(k_scale=TT.KS, v_scale=TT.VS) if kv == pa.PA_KV_FP8_E4M3 else {}
+                    pa.pa_attention_tree(out, s["q"], s["k"], s["v"], s["tables"], TT.i32(s["lens"]), TT.i32(s["start"]),
+                                         TT.i32([p for t in s["trees"] for p in t]), s["scale"], s["max_len"], ws, **scales)
+                    st = pa.pa_workspace_status(ws)
+                    seen.append(st)
+                    if st == pa.PA_OK:
+                        TT.check(s, out)
+                    else:
+                        assert st == pa.PA_ERR_TIMEOUT and torch.isnan(out).all(), st
+        print(" ".join(map(str, seen)))
+    """ % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__))))
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                         env=dict(os.environ, PA_WAIT_LIMIT_CYCLES="1"))
+    assert res.returncode == 0, res.stderr
+    assert pa.PA_ERR_TIMEOUT in {int(x) for x in res.stdout.split()}

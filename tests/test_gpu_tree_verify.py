@@ -3,6 +3,10 @@ to be equal: decisions lie far from their borders compared with the kernel's
 rounding, twice a float's precision), pa_kv_move_path against a copy of rows, and a
 whole step over trees."""
 import math
+import os
+import subprocess
+import sys
+import textwrap
 
 import numpy as np
 import pytest
@@ -96,6 +100,12 @@ def test_depths():
     args = tree_case("f32", [12] * 12, 50, 3, likely=0.97)
     deep = [compare(args, depth)[0].max() for depth in (0, 1, 2, 5, 11, 40)]
     assert deep[0] == 0 and deep[1] == 1 and deep[4] > 3 and deep[5] == deep[4]
+
+
+def test_trees_of_many_nodes():
+    # more nodes than are kept in shared memory, paths deeper than a wave
+    acc, _, _ = compare(tree_case("f32", [700, 300, 257, 5], 60, 21, likely=0.95), 40)
+    assert acc.max() > 8
 
 
 def test_siblings_of_one_token_and_foreign_nodes():
@@ -355,3 +365,54 @@ def test_a_step_over_trees_equals_tokens_one_by_one(kv):
         want, bound = TR.tree_attention(turned[rows], kk, vv, sees, d ** -0.5, dt)
         for x in (out[rows], got):
             assert ((x.double() - want).abs() <= bound).all()
+
+
+# ------------------------------------------------------------------ PA_DEBUG_VALIDATE
+
+def test_debug_validation_of_the_tree_calls():
+    code = textwrap.dedent("""
+        import sys, torch
+        sys.path.insert(0, %r)
+        import paged_kv_cache_12_gb300 as pa
+        t = lambda v, d=torch.int32: torch.tensor(v, dtype=d, device="cuda")
+        zeros = lambda *s, d=torch.float16: torch.zeros(s, dtype=d, device="cuda")
+        codes = []
+
+        def rc(f):
+            try:
+                f()
+                codes.append(0)
+            except pa.PAError as e:
+                codes.append(e.code)
+        k, v = zeros(8, 2, 16, 64), zeros(8, 2, 16, 64)
+        inv, pos = torch.ones(32, device="cuda"), t([[0, 1, 2]])
+        for slots, axis in (([5, 9, 5], 0), ([5, 9, 128], 0), ([5, -1, 9], 1), ([5, -1, 9], -1), ([5, -1, 9], 0)):
+            rc(lambda: pa.pa_kv_write_rope(zeros(3, 2, 64), zeros(3, 2, 64), pos, inv, t(slots, torch.int64), k, v,
+                                           pair_axis=t([axis] * 32)))
+        ws = torch.empty(pa.pa_attention_tree_workspace_size(2, 5, 4, 2, 64, 50), dtype=torch.uint8, device="cuda")
+        q, out, tab = zeros(5, 4, 64), zeros(5, 4, 64), [[0, 1, 2, 3], [4, 5, 6, 7]]
+        good = dict(tab=tab, lens=[40, 33], start=[0, 3, 5], parents=[-1, 0, 0, -1, 0])
+        for change in (dict(tab=[[0, 1, 9, 3], tab[1]]), dict(tab=[tab[0], [-1, 5, 6, 7]]), dict(lens=[51, 33]),
+                       dict(lens=[2, 33]), dict(lens=[-1, 33]), dict(start=[0, 3, 4]), dict(start=[0, 6, 5]),
+                       dict(parents=[-1, 0, 2, -1, 0]), dict(parents=[-1, 0, 0, -1, -2]), dict(), dict(tab=[[0, 1, 2, 99], tab[1]])):
+            c = {**good, **change}
+            rc(lambda: pa.pa_attention_tree(out, q, k, v, t(c["tab"]), t(c["lens"]), t(c["start"]), t(c["parents"]), 0.1, 50, ws))
+        p, u = torch.ones(5, 9, device="cuda"), torch.zeros(5, device="cuda")
+        acc, tok, path = zeros(2, d=torch.int32), zeros(2, 3, d=torch.int32), zeros(2, 3, d=torch.int32)
+        for start in ([0, 3, 4], [0, 6, 5], [0, 3, 5]):
+            rc(lambda: pa.pa_verify_tree(acc, tok, path, p, t([0, 1, 2, 0, 1]), t(good["parents"]), t(start), u))
+        good = dict(tab=tab, lens=[40, 33], start=[0, 3, 5], path=[[0, 2], [0, -1]], acc=[1, 0])
+        for change in (dict(acc=[2, 0]), dict(path=[[0, 0], [0, -1]]), dict(path=[[1, 2], [0, -1]]), dict(path=[[0, 3], [0, -1]]),
+                       dict(lens=[2, 33]), dict(tab=[[0, 1, -1, 3], tab[1]]), dict(start=[1, 3, 5]), dict(), dict(acc=[0, 0])):
+            c = {**good, **change}
+            rc(lambda: pa.pa_kv_move_path(k, v, t(c["tab"]), t(c["lens"]), t(c["start"]), t(c["path"]), t(c["acc"])))
+        print(" ".join(map(str, codes)))
+    """ % os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    env = dict(os.environ, PA_DEBUG_VALIDATE="1")
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, env=env, timeout=300)
+    assert res.returncode == 0, res.stderr
+    codes, E = [int(x) for x in res.stdout.split()], pa.PA_ERR_INVALID_ARG
+    assert codes[:5] == [E, E, E, E, 0]
+    assert codes[5:16] == [E] * 9 + [0, 0]
+    assert codes[16:19] == [E, E, 0]
+    assert codes[19:] == [E] * 7 + [0, 0]
