@@ -765,18 +765,31 @@ def pa_kv_write_rope(key, value, positions, inv_freq, slot_mapping, k_cache, v_c
             _mismatch(where, dev, (pair_axis, "pair_axis", i32, 1))
         ax = pair_axis.data_ptr()
     nb, hk, bs, d = held
-    rows = (n, hk, d)
-    sk = _token_stride(where, dev, key, "key", dt, rows)
-    sv = _token_stride(where, dev, value, "value", dt, rows)
+    rows, kst, vst = (n, hk, d), key.stride(), value.stride()
+    if key.shape == rows and value.shape == rows and key.dtype is dt and value.dtype is dt and \
+            key.get_device() == dev and value.get_device() == dev and kst[2] == 1 and kst[1] == d and vst[2] == 1 and \
+            vst[1] == d and n > 1:
+        sk, sv = kst[0], vst[0]
+    else:
+        sk = _token_stride(where, dev, key, "key", dt, rows)
+        sv = _token_stride(where, dev, value, "value", dt, rows)
     hq = sq = so = 0
     qi = qo = None
     if query is not None:
         hq = query.shape[1]
-        rows = (n, hq, d)
-        sq = so = _token_stride(where, dev, query, "query", dt, rows)
+        rows, kst = (n, hq, d), query.stride()
+        if query.shape == rows and query.dtype is dt and query.get_device() == dev and kst[2] == 1 and kst[1] == d and n > 1:
+            sq = so = kst[0]
+        else:
+            sq = so = _token_stride(where, dev, query, "query", dt, rows)
         qi = qo = query.data_ptr()
         if query_out is not None:
-            so = _token_stride(where, dev, query_out, "query_out", dt, rows)
+            kst = query_out.stride()
+            if query_out.shape == rows and query_out.dtype is dt and query_out.get_device() == dev and kst[2] == 1 and \
+                    kst[1] == d and n > 1:
+                so = kst[0]
+            else:
+                so = _token_stride(where, dev, query_out, "query_out", dt, rows)
             qo = query_out.data_ptr()
     elif query_out is not None:
         raise ValueError(f"{where}: query_out without query")

@@ -33,6 +33,7 @@
 // the call included.
 
 #include <climits>
+#include <mutex>
 
 #include <cooperative_groups.h>
 
@@ -507,7 +508,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ Draw draw;
     __shared__ int s_next[2];   // by the wave's parity: a CTA may still read one wave's tokens while the next is drawn
-    __shared__ int s_nodes[VMAX_CTAS], s_count;
+    __shared__ int s_nodes[VCTAS], s_count;
     __shared__ int s_node, s_level;
     __shared__ int32_t s_parents[PA_TREE_MAX_NODES], s_tokens[PA_TREE_MAX_NODES];   // of the tree's first nodes
     grid_release();
@@ -550,7 +551,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         __syncthreads();
         int groups = 1;
         while (groups < s_count) groups *= 2;
-        const int ctas = VCTAS / groups, group = rank / ctas, leader = group * ctas;
+        const int ctas = min(VMAX_CTAS, VCTAS / groups), group = rank / ctas, leader = group * ctas;
         const bool has = group < s_count;   // a group without a node has no row either
         const int who = has ? s_nodes[group] : node;
         const T *p = static_cast<const T *>(a.target) + (long long)(n0 + who) * a.target_stride;
@@ -617,18 +618,48 @@ int launch_verify(const VerifyArgs &a, cudaStream_t st) {
     return launch_early(verify_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a);
 }
 
-// The same rule for the cluster.  The first wave takes as many nodes a sequence (a
-// power of two, at most a CTA each) as keep its reads within VWAVE_BYTES, and no more
-// than a tree has on average.
+// Whether clusters of sixteen CTAs, above the portable size, can run on this device.
+template <typename T>
+bool wide_clusters() {
+    static std::mutex mu;
+    static int known[64] = {};   // 1: yes, 2: no
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known[dev]) {
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 16, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(VTHREADS);
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const bool ok = cudaFuncSetAttribute(verify_tree_kernel<T, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                             1) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&n, verify_tree_kernel<T, 16>, &cfg) == cudaSuccess && n >= 1;
+        if (!ok) cudaGetLastError();
+        known[dev] = ok ? 1 : 2;
+    }
+    return known[dev] == 1;
+}
+
+// The same rule for the cluster, up to sixteen CTAs where a tree has more than eight
+// nodes on average (4 x 16 nodes, mean of eight draws: 11.9 us against 15.2 with eight).
+// The first wave takes as many nodes a sequence (a power of two, at most a CTA each) as
+// keep its reads within VWAVE_BYTES, and no more than a tree has on average.
 constexpr long long VWAVE_BYTES = 64LL << 20;
 template <typename T>
 int launch_verify_tree(const TreeVerifyArgs &a, cudaStream_t st) {
     const long long slots = (long long)num_sms() * VRESIDENT;
     const unsigned b = (unsigned)a.num_seqs;
-    const int ctas = b * 8LL <= slots ? 8 : b * 4LL <= slots ? 4 : b * 2LL <= slots ? 2 : 1;
+    int ctas = b * 8LL <= slots ? 8 : b * 4LL <= slots ? 4 : b * 2LL <= slots ? 2 : 1;
+    if (b * 16LL <= slots && a.num_nodes > 8LL * a.num_seqs && wide_clusters<T>()) ctas = 16;
     const long long row = (long long)a.num_seqs * a.vocab * (long long)sizeof(T);
     int rows = 1;
     while (rows < ctas && 2 * rows * row <= VWAVE_BYTES && (long long)rows * a.num_seqs < a.num_nodes) rows *= 2;
+    if (ctas == 16) return launch_early(verify_tree_kernel<T, 16>, dim3(b * 16), VTHREADS, 0, st, a, rows);
     if (ctas == 8) return launch_early(verify_tree_kernel<T, 8>, dim3(b * 8), VTHREADS, 0, st, a, rows);
     if (ctas == 4) return launch_early(verify_tree_kernel<T, 4>, dim3(b * 4), VTHREADS, 0, st, a, rows);
     if (ctas == 2) return launch_early(verify_tree_kernel<T, 2>, dim3(b * 2), VTHREADS, 0, st, a, rows);
