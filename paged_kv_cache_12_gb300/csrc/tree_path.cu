@@ -46,15 +46,17 @@ __global__ void __launch_bounds__(MOVE_THREADS) move_path_kernel(const MoveArgs 
     const int seq = blockIdx.x;
     grid_release();
     grid_wait();
+    const int32_t *path = a.path + (long long)seq * (a.max_depth + 1);
+    const int first = threadIdx.x, here = first <= a.max_depth ? path[first] : 0;   // (read beside what it depends on)
+    const int before = first > 0 && first <= a.max_depth ? path[first - 1] : -1;
     const int n = a.accepted[seq];
     const int q0 = a.query_start[seq], T = a.query_start[seq + 1] - q0, L = a.context_lens[seq];
     bool ok = n >= 0 && n <= a.max_depth && T > 0 && T <= PA_TREE_MAX_NODES && n < T && T <= L &&
               L <= (long long)a.mbps * a.block_size && q0 >= 0;
     if (ok) {
-        const int32_t *path = a.path + (long long)seq * (a.max_depth + 1);
-        for (int j = threadIdx.x; j <= n; j += MOVE_THREADS) {
-            const int p = path[j];
-            if (j == 0 ? p != 0 : p <= path[j - 1]) ok = false;
+        for (int j = first; j <= n; j += MOVE_THREADS) {
+            const int p = j == first ? here : path[j];
+            if (j == 0 ? p != 0 : p <= (j == first ? before : path[j - 1])) ok = false;
             if (p < 0 || p >= T) {
                 ok = false;
                 continue;
