@@ -425,15 +425,15 @@ __device__ void tr_mma(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArg
                 umma_f16(tmem + b * TR_TOK, dq + h * (X::BLOCK >> 4) + 2 * j, dk + h * (X::BLOCK >> 4) + 2 * j, ID_S,
                          h > 0 || j > 0 ? 1u : 0u);
     };
-                // O_h += the P in buffer h times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
-                auto issue_pv = [&](int h, const TrSlot &k, bool first) {
-                    const uint64_t dv = dv0 + (uint64_t)(k.at * (X::TILE >> 4));
-    #pragma unroll
-                    for (int j = 0; j < TR_TOK / 16; ++j)
-                        umma_f16_ts(tmem + TR_O + h * 128, tmem + h * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4),
-                                    ID_O, !first || j > 0 ? 1u : 0u);
-                    umma_commit(smem_u32(&c.pvdone[1][h]));
-                };
+    // O_h += the P in buffer h times the value tile at k (16 tokens: P columns 8 j .., V rows 16 j ..)
+    auto issue_pv = [&](int h, const TrSlot &k, bool first) {
+        const uint64_t dv = dv0 + (uint64_t)(k.at * (X::TILE >> 4));
+#pragma unroll
+        for (int j = 0; j < TR_TOK / 16; ++j)
+            umma_f16_ts(tmem + TR_O + h * 128, tmem + h * TR_TOK + 8 * j, dv + (uint64_t)((j * 16 * 128) >> 4), ID_O,
+                        !first || j > 0 ? 1u : 0u);
+        umma_commit(smem_u32(&c.pvdone[1][h]));
+    };
     while (ok && p.next()) {
         const TrPiece x = piece_of(a, p);
         const int N = x.n;
@@ -536,9 +536,10 @@ struct TrRows {
             const uint32_t scol = (uint32_t)(b * TR_TOK + (SHARED ? x * COLS : 0));
             // S, and the products with this buffer's last P (done when S is; every phase
             // is seen, so that one waited for later is not taken for another)
-            if (n > (SHARED ? 1 : 0) ? !wait.both(&c.sfull[!SHARED][b], now, &c.pvdone[!SHARED][b], now ^ 1u)
-                                         : !wait(&c.sfull[!SHARED][b], now))
-                return;
+            const bool there = n > (SHARED ? 1 : 0)
+                                   ? wait.both(&c.sfull[!SHARED][b], now, &c.pvdone[!SHARED][b], now ^ 1u)
+                                   : wait(&c.sfull[!SHARED][b], now);
+            if (!there) return;
             tc_fence_after_sync();
             const int t0 = (p.t0 + n) * TR_TOK;
             const bool tail = ctx - t0 < TR_TOK;       // the tree's positions begin before the tile ends
