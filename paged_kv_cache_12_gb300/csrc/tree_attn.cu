@@ -137,7 +137,7 @@ struct Tree {
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_STAGE = OFF_RING + RING * TILE;
     static constexpr int OFF_CTRL = OFF_STAGE + STAGES * CODES;
-    static constexpr int CTRL = 3072;
+    static constexpr int CTRL = 3 * 1024;
     static constexpr int SMEM = OFF_CTRL + CTRL;
     static constexpr int THREADS = F8 ? 512 : 384;
     static constexpr int REGS_LAUNCH = F8 ? 128 : 168;     // per thread: 65536 / threads, rounded down to 8

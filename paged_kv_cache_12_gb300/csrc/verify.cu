@@ -47,10 +47,12 @@ namespace {
 constexpr int VMAX_CTAS = 8;                   // CTAs of a sequence's cluster, at most
 constexpr int VTHREADS = 256;
 constexpr int VWARPS = VTHREADS / 32;
+constexpr int VWIDE = 16;                      // warps of a CTA where few trees have the GPU
 constexpr int VRESIDENT = 4;                   // CTAs an SM holds (64 registers a thread)
 constexpr int VCHUNK = 128;                    // elements a warp reads at once, four a lane
 constexpr int VBATCH = 4;                      // chunks on their way at once
-static_assert(VMAX_CTAS * VWARPS == 64, "at most two slices a lane of the collecting warp");
+constexpr int VSLICES = 64;                    // of a row, at most: two a lane of the collecting warp
+static_assert(VMAX_CTAS * VWARPS == VSLICES, "two slices a lane");
 
 struct VerifyArgs {
     int32_t *accepted, *tokens;
@@ -93,6 +95,27 @@ struct Sum2 {
     }
     __device__ __forceinline__ Sum2 scaled(float f) const { return Sum2{hi * f, lo * f}; }   // f a power of two
     __device__ __forceinline__ bool any() const { return hi > 0.f; }   // sums of weights >= 0
+};
+
+// Two sums side by side, each hi + lo in two floats (Sum2 on pairs: seven
+// instructions for two terms).
+struct Sum2Pair {
+    uint64_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(uint64_t s) {
+        const uint64_t minus = pair_of(-1.f, -1.f);
+        const uint64_t t = pair_add(hi, s), b = pair_fma(hi, minus, t);
+        const uint64_t r = pair_add(pair_fma(pair_fma(b, minus, t), minus, hi), pair_fma(b, minus, s));
+        hi = t;
+        lo = pair_add(lo, r);
+    }
+    __device__ __forceinline__ Sum2 sum() const {
+        float h0, h1, l0, l1;
+        pair_parts(hi, h0, h1);
+        pair_parts(lo, l0, l1);
+        Sum2 x{h0, l0};
+        x.add(h1, l1);
+        return x;
+    }
 };
 
 // The sum over the warp's lanes, the same in every lane.
@@ -230,36 +253,109 @@ __device__ int find_in_range(const Weights<T> &w, int lo, int hi, Sum2 before, c
     return last;
 }
 
-// What a cluster's CTAs share while they draw a token.
+// What a cluster's CTAs, of W warps each, share while they draw a token.
+template <int W>
 struct Draw {
-    Sum2 totals[VWARPS];   // this CTA's slices; then, in the leader, the parts of one
+    Sum2 totals[W];   // this CTA's slices; then, in the leader, the parts of one
     Sum2 before;           // the leader's: the sum before the slice that passes
     Height height;
     int slice;             // the leader's: that slice; -1: no token; -2: no weight at all
 };
 
+// The first of the leader's parts (in sh.totals) at whose end the running sum, from `run`
+// on, passes the height, else the last of any weight; `before`: the sum before it.
+template <int W>
+__device__ __forceinline__ int passing_part(const Draw<W> &sh, Sum2 run, Sum2 &before) {
+    int at = -1;
+    bool passed = false;
+    for (int k = 0; k < W; ++k) {
+        const Sum2 x = sh.totals[k];
+        Sum2 after = run;
+        after.add(x);
+        if (!passed && x.any()) {
+            at = k;
+            before = run;
+            passed = sh.height.passed_by(after);
+        }
+        run = after;
+    }
+    return at;
+}
+
+// The sum of a row's own weights [lo, hi), lo a multiple of eight, by a thread.
+template <typename T>
+__device__ __forceinline__ Sum2 piece_sum(const Weights<T> &w, int lo, int hi) {
+    Sum2Pair acc;
+#pragma unroll 4
+    for (int base = lo; base < hi; base += 8) {
+        float p[8];
+        if (w.quads && base + 8 <= hi) {
+            const Quad<T> a = *reinterpret_cast<const Quad<T> *>(w.p + base);
+            const Quad<T> b = *reinterpret_cast<const Quad<T> *>(w.p + base + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = prob(a.v[k]), p[4 + k] = prob(b.v[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) p[k] = base + k < hi ? prob(w.p[base + k]) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) acc.add(pair_of(fmaxf(p[k], 0.f), fmaxf(p[k + 1], 0.f)));
+    }
+    return acc.sum();
+}
+
+// The element of a slice [lo, hi) of a row's own weights at which the running sum, `run`
+// before the slice, passes sh.height; by a CTA, a consecutive piece a thread.  (In parts
+// until one was as short as a warp's chunk: three reads one after another, and 64
+// sequences of 131072 tokens in bf16 took 54.8 us where this takes 45.8.)
+constexpr int VPIECE = 128;   // elements of a thread's piece, at most
+template <typename T, int W>
+__device__ __forceinline__ void find_in_slice(Draw<W> &sh, int *next, const Weights<T> &w, int lo, int hi, Sum2 run) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int piece = ((hi - lo + 32 * W - 1) / (32 * W) + 7) / 8 * 8;
+    const int plo = min(hi, lo + (int)threadIdx.x * piece), phi = min(hi, plo + piece);
+    const Sum2 mine = piece_sum(w, plo, phi);
+    const Sum2 upto = warp_scan(mine);
+    if (lane == 31) sh.totals[warp] = upto;
+    __syncthreads();
+    Sum2 before;
+    const int at = passing_part(sh, run, before);
+    if (warp != at) return;
+    Sum2 after = before;
+    after.add(upto);
+    const unsigned any = __ballot_sync(0xffffffffu, mine.any());
+    const unsigned over = __ballot_sync(0xffffffffu, mine.any() && sh.height.passed_by(after));
+    const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);   // (a part that was chosen has some weight)
+    after.add(-mine.hi, -mine.lo);   // before this lane's piece
+    const Sum2 from{__shfl_sync(0xffffffffu, after.hi, l), __shfl_sync(0xffffffffu, after.lo, l)};
+    const int v = find_in_range(w, __shfl_sync(0xffffffffu, plo, l), __shfl_sync(0xffffffffu, phi, l), from, sh.height);
+    if (lane == 0) *next = v;
+}
+
 // Draws a token by the weights w: the smallest whose running sum passes u times
-// the total.  `ctas` CTAs of the cluster from rank `leader` on do it, all CTAs of the
-// cluster take part in its meetings; the token is in *next (in the leader's shared
-// memory, -1 before) after the cluster's next meeting.  Returns the slice in which it
-// lies, -1 where there is none, or `empty` where the weights sum to zero.  DEEP: parts of
-// the slice are cut again while they are long (a row's slices are, where few CTAs have it).
-template <typename T, bool DEEP, class Range>
-__device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader, int ctas, Draw &sh, int *next,
-                                          const Weights<T> &w, int vocab, const float *u, int empty, Range range) {
+// the total.  `ctas` CTAs of the cluster from rank `leader` on do it (`has`: for a row;
+// the same CTAs may have none), all CTAs of the cluster take part in its meetings; the
+// token is in *next (in the leader's shared memory, -1 before) after the cluster's next
+// meeting.  Returns the slice in which it lies, -1 where there is none, or `empty` where
+// the weights sum to zero.  OWN: the weights are a row's own, nobody needs that answer, and
+// a slice may be long (where few CTAs have a row).
+template <typename T, bool OWN, int W, class Range>
+__device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader, int ctas, Draw<W> &sh, int *next,
+                                          const Weights<T> &w, int vocab, bool has, const float *u, int empty,
+                                          Range range) {
     const int rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slices = ctas * VWARPS;
+    const int slices = ctas * W;   // at most VSLICES
     const int len = ((vocab + slices - 1) / slices + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
-    const int own = (rank - leader) * VWARPS + warp;
+    const int own = (rank - leader) * W + warp;
     const long long from = (long long)own * len;
-    const int lo = (int)min((long long)vocab, from), hi = (int)min((long long)vocab, from + len);
+    const int lo = (int)min((long long)vocab, from), hi = has ? (int)min((long long)vocab, from + len) : lo;
     const Sum2 mine = range(w, lo, hi);
     if (lane == 0) sh.totals[warp] = mine;
     cluster.sync();
     if (rank == leader && warp == 0) {   // lane l: slices 2 l and 2 l + 1
         Sum2 x0, x1;
         if (2 * lane < slices) {
-            const Sum2 *src = cluster.map_shared_rank(sh.totals, leader + 2 * lane / VWARPS) + 2 * lane % VWARPS;
+            const Sum2 *src = cluster.map_shared_rank(sh.totals, leader + 2 * lane / W) + 2 * lane % W;
             x0 = src[0];
             x1 = src[1];
         }
@@ -293,39 +389,37 @@ __device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader
         }
         if (lane == 0) sh.slice = slice;
     }
-    cluster.sync();   // the leader has read every CTA's totals and decided
+    const bool is_short = !OWN && len <= VBATCH * VCHUNK;
+    if (OWN) {   // the leader goes on alone
+        if (rank != leader) return -1;
+        __syncthreads();
+    } else {
+        cluster.sync();   // the leader has read every CTA's totals and decided
+    }
     const int slice = *cluster.map_shared_rank(&sh.slice, leader);
-    if (len <= VBATCH * VCHUNK) {   // short slices: the warp that summed it finds the element
+    if (is_short) {   // short slices: the warp that summed it finds the element
         if (slice == own) {
             const int v = find_in_range(w, lo, hi, *cluster.map_shared_rank(&sh.before, leader),
                                         *cluster.map_shared_rank(&sh.height, leader));
             if (lane == 0) *cluster.map_shared_rank(next, leader) = v;
         }
-    } else if (rank == leader && slice >= 0) {   // the slice again, in parts, until a part is short
+    } else if (rank == leader && slice >= 0) {   // the slice again, in parts (OWN: while it is long)
         int first = slice * len, n = len;
         Sum2 before = sh.before;
         for (;;) {
-            const int part = ((n + VWARPS - 1) / VWARPS + VCHUNK - 1) / VCHUNK * VCHUNK;
+            if (OWN && n <= 32 * W * VPIECE) {
+                find_in_slice(sh, next, w, first, min(vocab, first + n), before);
+                break;
+            }
+            const int part = ((n + W - 1) / W + VCHUNK - 1) / VCHUNK * VCHUNK;
             const int plo = min(vocab, min(first + n, first + warp * part));
             const int phi = min(vocab, min(first + n, plo + part));
             const Sum2 mine = range(w, plo, phi);
             if (lane == 0) sh.totals[warp] = mine;
             __syncthreads();
-            Sum2 run = before;
-            int at = -1;       // the first part that passes, else the last of any weight
-            bool passed = false;
-            for (int k = 0; k < VWARPS; ++k) {
-                const Sum2 x = sh.totals[k];
-                Sum2 after = run;
-                after.add(x);
-                if (!passed && x.any()) {
-                    at = k;
-                    before = run;
-                    passed = sh.height.passed_by(after);
-                }
-                run = after;
-            }
-            if (!DEEP || at < 0 || part <= 2 * VCHUNK) {
+            const Sum2 run = before;
+            const int at = passing_part(sh, run, before);
+            if (!OWN || at < 0) {
                 if (warp == at) {
                     const int v = find_in_range(w, plo, phi, before, sh.height);
                     if (lane == 0) *next = v;
@@ -346,7 +440,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
     const int rank = (int)cluster.block_rank();
     const int seq = blockIdx.x / VCTAS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ Draw draw;
+    __shared__ Draw<VWARPS> draw;
     __shared__ int s_next;
     __shared__ int s_kept, s_n, s_d0;
     grid_release();
@@ -397,8 +491,9 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         Weights<T> w(p, q, failed && !a.draft ? a.draft_tokens[d0 + kept] : -1);
         for (int attempt = 0; attempt < 2; ++attempt) {
             const int slice =
-                draw_token<T, false>(cluster, 0, VCTAS, draw, &s_next, w, a.vocab, a.sample + seq, attempt == 0 && failed ? -2 : -1,
-                              [](const Weights<T> &x, int lo, int hi) { return range_sum(x, lo, hi); });
+                draw_token<T, false>(cluster, 0, VCTAS, draw, &s_next, w, a.vocab, true, a.sample + seq,
+                                     attempt == 0 && failed ? -2 : -1,
+                                     [](const Weights<T> &x, int lo, int hi) { return range_sum(x, lo, hi); });
             if (slice != -2) break;
             w = Weights<T>(p, nullptr, -1);   // q covers p: draw from p itself
             cluster.sync();   // every CTA has read the decision
@@ -421,27 +516,6 @@ struct TreeVerifyArgs {
     const float *uniform;
     int num_seqs, num_nodes, max_depth, vocab;
     long long target_stride;
-};
-
-// Two sums side by side, each hi + lo in two floats (Sum2 on pairs: seven
-// instructions for two terms).
-struct Sum2Pair {
-    uint64_t hi = 0, lo = 0;
-    __device__ __forceinline__ void add(uint64_t s) {
-        const uint64_t minus = pair_of(-1.f, -1.f);
-        const uint64_t t = pair_add(hi, s), b = pair_fma(hi, minus, t);
-        const uint64_t r = pair_add(pair_fma(pair_fma(b, minus, t), minus, hi), pair_fma(b, minus, s));
-        hi = t;
-        lo = pair_add(lo, r);
-    }
-    __device__ __forceinline__ Sum2 sum() const {
-        float h0, h1, l0, l1;
-        pair_parts(hi, h0, h1);
-        pair_parts(lo, l0, l1);
-        Sum2 x{h0, l0};
-        x.add(h1, l1);
-        return x;
-    }
 };
 
 // 16 bytes of a row added as weights (what is negative or NaN counts as zero).
@@ -504,14 +578,14 @@ __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
 // draws; one level after another 139), of which the first wave 26: sums 12 to 16 (67 MB), the
 // passing slice 5, meetings 4, collection and walk 2; 4 sequences of 16 nodes and 32,003
 // tokens in fp32 11.9 us.
-template <typename T, int VCTAS>
-__global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESIDENT)
+template <typename T, int VCTAS, int W>
+__global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(32 * W, VRESIDENT * VWARPS / W)
     verify_tree_kernel(const TreeVerifyArgs a, int rows) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank();
     const int seq = blockIdx.x / VCTAS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ Draw draw;
+    __shared__ Draw<W> draw;
     __shared__ int s_next[2];   // by the wave's parity: a CTA may still read one wave's tokens while the next is drawn
     __shared__ int s_nodes[VCTAS], s_count;
     __shared__ int s_node, s_level;
@@ -524,7 +598,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
     const int n = n1 - n0;
     auto parent = [&](int j) { return j < PA_TREE_MAX_NODES ? s_parents[j] : a.parents[n0 + j]; };
     auto drafted = [&](int j) { return j < PA_TREE_MAX_NODES ? s_tokens[j] : a.node_tokens[n0 + j]; };
-    for (int j = threadIdx.x; ok && j < min(n, PA_TREE_MAX_NODES); j += VTHREADS) {
+    for (int j = threadIdx.x; ok && j < min(n, PA_TREE_MAX_NODES); j += 32 * W) {
         s_parents[j] = a.parents[n0 + j];
         s_tokens[j] = a.node_tokens[n0 + j];
     }
@@ -556,12 +630,12 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         __syncthreads();
         int groups = 1;
         while (groups < s_count) groups *= 2;
-        const int ctas = min(VMAX_CTAS, VCTAS / groups), group = rank / ctas, leader = group * ctas;
+        const int ctas = min(VSLICES / W, VCTAS / groups), group = rank / ctas, leader = group * ctas;
         const bool has = group < s_count;   // a group without a node has no row either
         const int who = has ? s_nodes[group] : node;
         const T *p = static_cast<const T *>(a.target) + (long long)(n0 + who) * a.target_stride;
-        draw_token<T, true>(cluster, leader, ctas, draw, next, Weights<T>(p, nullptr, -1), has ? a.vocab : 0, a.uniform + n0 + who,
-                      -1, [](const Weights<T> &x, int lo, int hi) { return row_sum(x.p, lo, hi); });
+        draw_token<T, true>(cluster, leader, ctas, draw, next, Weights<T>(p, nullptr, -1), a.vocab, has,
+                            a.uniform + n0 + who, -1, [](const Weights<T> &x, int lo, int hi) { return row_sum(x.p, lo, hi); });
         cluster.sync();   // the tokens are there
         if (warp == 0) {
             const int count = s_count;
@@ -603,7 +677,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         level = s_level;
     }
     if (rank == 0) {
-        for (int j = (ok ? level + 1 : 0) + (int)threadIdx.x; j <= a.max_depth; j += VTHREADS) tokens[j] = path[j] = -1;
+        for (int j = (ok ? level + 1 : 0) + (int)threadIdx.x; j <= a.max_depth; j += 32 * W) tokens[j] = path[j] = -1;
         if (threadIdx.x == 0) a.accepted[seq] = ok ? level : -1;
     }
     cluster.sync();   // rank 0's shared memory outlives its readers
@@ -623,7 +697,26 @@ int launch_verify(const VerifyArgs &a, cudaStream_t st) {
     return launch_early(verify_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a);
 }
 
-// Whether clusters of sixteen CTAs, above the portable size, can run on this device.
+// Whether the kernel can run in clusters of sixteen CTAs, above the portable size.
+template <typename T, int W>
+bool wide_cluster() {
+    const auto kernel = verify_tree_kernel<T, 16, W>;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 16, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(32 * W);
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n >= 1;
+    if (!ok) cudaGetLastError();
+    return ok;
+}
+
+// The same for both forms of the current device, asked once.
 template <typename T>
 bool wide_clusters() {
     static std::mutex mu;
@@ -631,44 +724,38 @@ bool wide_clusters() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return false;
     std::lock_guard<std::mutex> lock(mu);
-    if (!known[dev]) {
-        cudaLaunchAttribute at{};
-        at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = 16, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(16);
-        cfg.blockDim = dim3(VTHREADS);
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
-        int n = 0;
-        const bool ok = cudaFuncSetAttribute(verify_tree_kernel<T, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                             1) == cudaSuccess &&
-                        cudaOccupancyMaxActiveClusters(&n, verify_tree_kernel<T, 16>, &cfg) == cudaSuccess && n >= 1;
-        if (!ok) cudaGetLastError();
-        known[dev] = ok ? 1 : 2;
-    }
+    if (!known[dev]) known[dev] = wide_cluster<T, VWARPS>() && wide_cluster<T, VWIDE>() ? 1 : 2;
     return known[dev] == 1;
 }
 
 // The same rule for the cluster, up to sixteen CTAs where a tree has more than eight
-// nodes on average (4 x 16 nodes, mean of eight draws: 11.9 us against 15.2 with eight).
+// nodes on average, and of twice the warps where such clusters leave half of the SMs
+// idle: rows in L2, mean of eight draws, with eight CTAs / sixteen / of sixteen warps:
+// 4 x 16 nodes of 32,003 tokens in fp32 - / 11.0 / 10.5 us, 2 x 64 of 131,072 in fp32
+// - / 19.8 / 17.9, but 8 x 12 of 32,003 in fp32 - / 12.4 / 12.9.
 // The first wave takes as many nodes a sequence (a power of two, at most a CTA each) as
-// keep its reads within VWAVE_BYTES, and no more than a tree has on average.
+// keep its reads within VWAVE_BYTES, and no more than a tree has on average (64 x 32
+// nodes of 131,072 tokens in bf16: 32, 64 and 128 MB 48, 46 and 50 us).
 constexpr long long VWAVE_BYTES = 64LL << 20;
 template <typename T>
 int launch_verify_tree(const TreeVerifyArgs &a, cudaStream_t st) {
     const long long slots = (long long)num_sms() * VRESIDENT;
     const unsigned b = (unsigned)a.num_seqs;
     int ctas = b * 8LL <= slots ? 8 : b * 4LL <= slots ? 4 : b * 2LL <= slots ? 2 : 1;
-    if (b * 16LL <= slots && a.num_nodes > 8LL * a.num_seqs && wide_clusters<T>()) ctas = 16;
+    int warps = VWARPS;
+    if (b * 16LL <= slots && a.num_nodes > 8LL * a.num_seqs && wide_clusters<T>()) {
+        ctas = 16;
+        if (b * 16LL <= num_sms() / 2) warps = VWIDE;
+    }
     const long long row = (long long)a.num_seqs * a.vocab * (long long)sizeof(T);
     int rows = 1;
     while (rows < ctas && 2 * rows * row <= VWAVE_BYTES && (long long)rows * a.num_seqs < a.num_nodes) rows *= 2;
-    if (ctas == 16) return launch_early(verify_tree_kernel<T, 16>, dim3(b * 16), VTHREADS, 0, st, a, rows);
-    if (ctas == 8) return launch_early(verify_tree_kernel<T, 8>, dim3(b * 8), VTHREADS, 0, st, a, rows);
-    if (ctas == 4) return launch_early(verify_tree_kernel<T, 4>, dim3(b * 4), VTHREADS, 0, st, a, rows);
-    if (ctas == 2) return launch_early(verify_tree_kernel<T, 2>, dim3(b * 2), VTHREADS, 0, st, a, rows);
-    return launch_early(verify_tree_kernel<T, 1>, dim3(b), VTHREADS, 0, st, a, rows);
+    if (warps == VWIDE) return launch_early(verify_tree_kernel<T, 16, VWIDE>, dim3(b * 16), 32 * VWIDE, 0, st, a, rows);
+    if (ctas == 16) return launch_early(verify_tree_kernel<T, 16, VWARPS>, dim3(b * 16), VTHREADS, 0, st, a, rows);
+    if (ctas == 8) return launch_early(verify_tree_kernel<T, 8, VWARPS>, dim3(b * 8), VTHREADS, 0, st, a, rows);
+    if (ctas == 4) return launch_early(verify_tree_kernel<T, 4, VWARPS>, dim3(b * 4), VTHREADS, 0, st, a, rows);
+    if (ctas == 2) return launch_early(verify_tree_kernel<T, 2, VWARPS>, dim3(b * 2), VTHREADS, 0, st, a, rows);
+    return launch_early(verify_tree_kernel<T, 1, VWARPS>, dim3(b), VTHREADS, 0, st, a, rows);
 }
 
 }  // namespace
