@@ -670,8 +670,9 @@ PA_API int pa_attention_tree(void *out, const void *query, const void *k_cache, 
  *   tree_start    int32 [num_seqs + 1], device, a non-decreasing cover of the nodes
  *   uniform       float [num_nodes], in [0, 1)
  * At most max_depth drafts are accepted.  NaN and negative weights count as
- * zero; where a row sums to zero or its sum is not finite the token is -1 and the
- * path ends.  A sequence without nodes or with a bad tree_start gets a = -1 and
+ * zero; where a row sums to zero or its sum is not finite (one of 2^126 or more may
+ * count so) the token is -1 and the path ends.  A sequence without nodes or with a
+ * bad tree_start gets a = -1 and
  * tokens and path -1.  Sums are carried in twice the precision of a float.
  * Needs no workspace. */
 PA_API int pa_verify_tree(int32_t *accepted, int32_t *tokens, int32_t *path, const void *target_probs,

@@ -34,6 +34,7 @@
 
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -107,6 +108,17 @@ struct Sum2Pair {
         const uint64_t r = pair_add(pair_fma(pair_fma(b, minus, t), minus, hi), pair_fma(b, minus, s));
         hi = t;
         lo = pair_add(lo, r);
+    }
+    // the same for 0 <= s <= hi in four (Dekker's form: there t - hi is exact)
+    __device__ __forceinline__ void add_below(uint64_t s) {
+        const uint64_t minus = pair_of(-1.f, -1.f), t = pair_add(hi, s);
+        lo = pair_add(lo, pair_fma(pair_fma(hi, minus, t), minus, s));
+        hi = t;
+    }
+    __device__ __forceinline__ float least() const {
+        float h0, h1;
+        pair_parts(hi, h0, h1);
+        return fminf(h0, h1);
     }
     __device__ __forceinline__ Sum2 sum() const {
         float h0, h1, l0, l1;
@@ -518,31 +530,59 @@ struct TreeVerifyArgs {
     long long target_stride;
 };
 
-// 16 bytes of a row added as weights (what is negative or NaN counts as zero).
-__device__ __forceinline__ void add16(Sum2Pair &acc, uint4 v, float) {
-    acc.add(pair_of(fmaxf(__uint_as_float(v.x), 0.f), fmaxf(__uint_as_float(v.y), 0.f)));
-    acc.add(pair_of(fmaxf(__uint_as_float(v.z), 0.f), fmaxf(__uint_as_float(v.w), 0.f)));
-}
-__device__ __forceinline__ void add16(Sum2Pair &acc, uint4 v, __nv_bfloat16) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        acc.add(pair_of(fmaxf(__uint_as_float(w[k] << 16), 0.f), fmaxf(__uint_as_float(w[k] & 0xffff0000u), 0.f)));
-}
-__device__ __forceinline__ void add16(Sum2Pair &acc, uint4 v, __half) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
-        acc.add(pair_of(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f)));
+// Eight 16-bit elements of a row as weights (what is negative or NaN becomes zero),
+// their largest, and their sum added to one that is no less than any of them.
+template <typename T>
+struct Weights8 {
+    static __device__ __forceinline__ void clamp(uint4 &v) {
+        v.x = not_below_zero(v.x), v.y = not_below_zero(v.y), v.z = not_below_zero(v.z), v.w = not_below_zero(v.w);
     }
-}
+    static __device__ __forceinline__ uint32_t largest(uint32_t m, uint4 v) {
+        return __vmaxu2(__vmaxu2(__vmaxu2(m, v.x), __vmaxu2(v.y, v.z)), v.w);
+    }
+    static __device__ __forceinline__ float value(uint32_t m) {
+        float a, b;
+        pair_parts(two(m), a, b);
+        return fmaxf(a, b);
+    }
+    static __device__ __forceinline__ void add(Sum2Pair &acc, uint4 v) {
+        acc.add_below(two(v.x));
+        acc.add_below(two(v.y));
+        acc.add_below(two(v.z));
+        acc.add_below(two(v.w));
+    }
+
+private:
+    static __device__ __forceinline__ uint32_t not_below_zero(uint32_t w) {
+        uint32_t r;
+        if constexpr (std::is_same<T, __half>::value)
+            asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0));
+        else
+            asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0));
+        return r;
+    }
+    static __device__ __forceinline__ uint64_t two(uint32_t w) {
+        if constexpr (std::is_same<T, __half>::value) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+            return pair_of(f.x, f.y);
+        } else {
+            return pair_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        }
+    }
+};
 
 // range_sum of a row's own weights, with more bytes on their way: 16 at a time
 // from the first 16-byte boundary on, whatever the row's alignment.  Eight loads and
 // one sum are what 64 registers hold (64 sequences of 131072 tokens in bf16, mean of
-// eight draws: 54.5 us; with two and four sums 56 and 65, four loads 77; through
+// eight draws, 54.5 us at first: with two and four sums 56 and 65, four loads 77; through
 // shared memory cells with two sums 57).
+//
+// The additions are a quarter of the time (plain fp32 sums: 46 us -> 35).  Of 16-bit
+// elements the largest of a lane's 64 costs half an instruction each, and a sum that is no
+// less than it needs four instructions for two terms instead of seven: so a sum that is
+// less is first lifted by that largest, which the end takes off again (46 -> 41; the lifts
+// at most double the sum, so the error stays a few steps of its second float).  Of fp32
+// elements the maxima cost what they save.
 constexpr int VLOADS = 8;
 template <typename T>
 __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
@@ -552,6 +592,7 @@ __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
     const int head = min(hi, lo + skip), nvec = (hi - head) / E, tail = head + nvec * E;
     const uint4 *v = reinterpret_cast<const uint4 *>(p + head);
     Sum2Pair acc;
+    Sum2 lift;   // what both sums of acc hold beside the weights
     if (lane < head - lo) acc.add(pair_of(fmaxf(prob(p[lo + lane]), 0.f), 0.f));
     if (lane < hi - tail) acc.add(pair_of(fmaxf(prob(p[tail + lane]), 0.f), 0.f));
     for (int i0 = 0; i0 < nvec; i0 += 32 * VLOADS) {
@@ -561,10 +602,32 @@ __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
             const int i = i0 + 32 * k + lane;
             x[k] = i < nvec ? v[i] : make_uint4(0, 0, 0, 0);
         }
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int k = 0; k < VLOADS; ++k) add16(acc, x[k], T());
+            for (int k = 0; k < VLOADS; ++k) {
+                acc.add(pair_of(fmaxf(__uint_as_float(x[k].x), 0.f), fmaxf(__uint_as_float(x[k].y), 0.f)));
+                acc.add(pair_of(fmaxf(__uint_as_float(x[k].z), 0.f), fmaxf(__uint_as_float(x[k].w), 0.f)));
+            }
+        } else {
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < VLOADS; ++k) {
+                Weights8<T>::clamp(x[k]);
+                m = Weights8<T>::largest(m, x[k]);
+            }
+            const float top = Weights8<T>::value(m);
+            if (top > acc.least()) {
+                acc.add(pair_of(top, top));
+                lift.add(top, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < VLOADS; ++k) Weights8<T>::add(acc, x[k]);
+        }
     }
-    return warp_sum(acc.sum());
+    Sum2 sum = acc.sum();
+    sum.add(-lift.hi, -lift.lo);
+    sum.add(-lift.hi, -lift.lo);
+    return warp_sum(sum);
 }
 
 // A path through a sequence's tree, by a cluster.  One level after another would

@@ -129,6 +129,30 @@ def test_rows_without_weight():
     assert got[1][:, 0].tolist()[0] == -1 and got[1][3, 0] == -1 and got[1][4, 0] == -1
 
 
+@pytest.mark.parametrize("kind,low", [("f32", -120), ("f16", -24), ("bf16", -120)])
+@pytest.mark.parametrize("seqs,vocab", [(700, 40003), (2, 300007), (20, 20004)])
+def test_weights_of_many_sizes(kind, low, seqs, vocab):
+    # rising rows (each step's largest passes the sum before it), falling and mixed ones,
+    # with negative elements, NaN and one infinity among them.  Powers of two: the 64-bit
+    # sums here are exact to 2^-53 of the total, the kernel's to about 2^-44, and a
+    # number of 24 bits falls within 2^-40 of one of the few sums above 2^-24 of the total
+    # with a probability below 1e-5.
+    rng = np.random.default_rng(seqs)
+    x = np.sort(np.exp2(rng.integers(low, 1, (seqs, vocab)).astype(np.float64)), axis=1)
+    x[1::3] = x[1::3, ::-1]
+    for i in range(2, seqs, 3):
+        rng.shuffle(x[i])
+    for i in range(0, seqs, 4):
+        at = rng.integers(0, vocab, 9)
+        x[i, at[:4]], x[i, at[4:8]] = math.nan, -0.5
+        if i % 8:
+            x[i, at[8]] = math.inf
+    target = torch.from_numpy(x).to(TYPES[kind]).to(DEV)
+    u = rng.random(seqs).astype(np.float32)
+    got = compare((target, [0] * seqs, [-1] * seqs, list(range(seqs + 1)), u), 0)
+    assert all((got[1][i, 0] == -1) == (i % 8 == 4) for i in range(seqs))
+
+
 def test_bad_tree_start():
     target, tokens, parents, _, u = tree_case("f32", [4, 4, 4], 30, 2)
     for start in ([0, 5, 4, 12], [1, 4, 8, 12], [0, 4, 8, 11], [0, 4, 8, 13], [0, -4, 8, 12]):
