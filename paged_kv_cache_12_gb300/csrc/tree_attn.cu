@@ -37,7 +37,7 @@
 // 1024, the products' operands 768, barriers and the rest 400).  64 nodes x 64 heads over
 // 4 x 32768 tokens, fp16: 225 us, 1220 TFLOP/s; the chain of a half, S with its queries
 // from shared memory 856 clocks, softmax 1900, PV 550 and the hand-overs between them.
-// One sequence of 600 tokens and 8 nodes: 13 us, latency.
+// One sequence of 600 tokens and 8 nodes: 12.5 us, latency (of 100 tokens 10.8).
 
 #include <algorithm>
 #include <climits>
@@ -56,6 +56,7 @@ namespace {
 constexpr int TR_HALF = 128;      // rows of a half
 constexpr int TR_TOK = 128;       // tokens of a KV tile
 constexpr int TR_MAX_ROWS = 256;
+constexpr int TR_SOFTMAX_WARPS = 8;
 
 struct TreeArgs {
     uint16_t *out;
@@ -65,6 +66,7 @@ struct TreeArgs {
     int num_seqs, num_query_tokens, H, Hkv, G, bs, mbps, max_ctx;
     int tile_toks;          // nodes of a row tile
     int ginv;               // 65536 / G + 1: m / G = m * ginv >> 16 for a row m of a tile
+    int tinv;               // 2^20 / tile_toks + 1: n / tile_toks = n * tinv >> 20 for n < 2 PA_TREE_MAX_NODES
     long long num_blocks;
     float scale_log2, v_scale;
     long long wait_limit;
@@ -88,7 +90,7 @@ struct TreeArgs {
         w.q0 = query_start[i];
         w.T = query_start[i + 1] - w.q0;
         w.valid = w.L >= 0 && w.L <= max_ctx && w.L <= (long long)mbps * bs && w.T <= w.L && w.T <= PA_TREE_MAX_NODES;
-        w.per_head = w.valid ? (w.T + tile_toks - 1) / tile_toks : 0;
+        w.per_head = w.valid ? (w.T + tile_toks - 1) * tinv >> 20 : 0;
         w.rts = w.per_head * Hkv;
         w.ntiles = w.valid ? w.L / TR_TOK + (w.L % TR_TOK != 0) : 0;
         return w;
@@ -102,12 +104,16 @@ struct TreeArgs {
     __device__ __forceinline__ bool in_teams(const Seq &w) const { return w.per_head % 2 == 0; }
     __device__ __forceinline__ int row_tiles(const Seq &w, int r) const { return w.ntiles; }
     __device__ __forceinline__ int first_tiles(const Seq &w, int r) const { return w.ntiles; }
-    __device__ __forceinline__ int first_node(const Seq &w, int r) const { return r % w.per_head * tile_toks; }
+    // kv head of a row tile, its first node (a tree is one row tile a head as a rule)
+    __device__ __forceinline__ int head(const Seq &w, int r) const { return w.per_head == 1 ? r : r / w.per_head; }
+    __device__ __forceinline__ int first_node(const Seq &w, int r) const {
+        return w.per_head == 1 ? 0 : r % w.per_head * tile_toks;
+    }
     __device__ __forceinline__ int cut_rows(const Seq &w, int r) const {
         return min(tile_toks, w.T - first_node(w, r)) * G;
     }
     __device__ __forceinline__ long long first_row(const Seq &w, int r) const {
-        return (long long)(w.q0 + first_node(w, r)) * H + r / w.per_head * G;
+        return (long long)(w.q0 + first_node(w, r)) * H + head(w, r) * G;
     }
     __device__ __forceinline__ bool seq_ok(int i) const { return query_start[i] <= query_start[i + 1]; }
     __device__ __forceinline__ bool ends_ok() const {
@@ -188,7 +194,7 @@ struct TrPiece {
 };
 __device__ __forceinline__ TrPiece piece_of(const TreeArgs &a, const Walk<TreeArgs> &p) {
     TrPiece x;
-    x.g = p.r / p.w.per_head;
+    x.g = a.head(p.w, p.r);
     x.node0 = a.first_node(p.w, p.r);
     x.rows = a.cut_rows(p.w, p.r);
     x.n = p.t1 - p.t0;
@@ -262,7 +268,7 @@ __device__ void tr_load(TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_
     int use = 0, at = 0;                          // tiles so far; the slot of the next (of this warp's)
     uint32_t parity = 1;
     while (wait.ok && p.next()) {
-        const int g = p.r / p.w.per_head;
+        const int g = a.head(p.w, p.r);
         const uint64_t policy = p.w.per_head > 1 ? again : once;
         const int32_t *table = a.block_tables + (long long)p.seq * a.mbps;
         const int blocks = (p.w.L - 1) / a.bs + 1;
@@ -293,11 +299,31 @@ __device__ void tr_load(TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_
                               WAIT_LIMIT);
 }
 
-// One warp: the queries of a piece's rows, as the products read them.
+// One warp: rows [from, to) of a half's queries, as the products read them, into the
+// tile at dst (query row m0 of the row tile is the half's first); they are there on return.
+template <int D>
+__device__ __forceinline__ void load_queries(const TreeArgs &a, const uint16_t *first, int m0, int from, int to, uint32_t dst) {
+    constexpr int CH = D / 8, BLOCK = TR_TOK * 128;   // 16-byte chunks of a row
+    const int lane = threadIdx.x & 31, ch = lane % CH;
+#pragma unroll 2
+    for (int m = from + lane / CH; m < to; m += 32 / CH) {
+        const uint16_t *src = first + a.row_at(m0 + m) * D + 8 * ch;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         dst + (ch / 8) * BLOCK + m * 128 + (((ch & 7) ^ (m & 7)) << 4)),
+                     "l"(src)
+                     : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// One warp: the queries of all pieces but a CTA's first.  (That one's the softmax warps
+// load, which have nothing else to do yet: a warp takes 60 clocks for 512 bytes, 256 rows
+// 7700.)
 template <int KV, int D>
 __device__ void tr_query(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p) {
     using X = Tree<KV, D>;
-    constexpr int CH = D / 8;   // 16-byte chunks of a row
     const int lane = threadIdx.x & 31;
     WarpWait wait{c, a.wait_limit};
     uint32_t phase = 3;   // of the buffers' release (a bit each)
@@ -307,22 +333,11 @@ __device__ void tr_query(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<TreeA
         const uint16_t *first = a.query + a.first_row(p.w, p.r) * D;
         for (int h = 0; wait.ok && h < (x.two ? 2 : 1); ++h) {
             const int b = x.two ? h : sel;
-            if (!wait(&c.qempty[b], phase >> b & 1u)) break;
-            const uint32_t dst = smem_u32(smem) + b * X::TILE;
-            const int rows = min(TR_HALF, x.rows - h * TR_HALF);
-            for (int i = lane; i < rows * CH; i += 32) {
-                const int m = i / CH, ch = i % CH;
-                const uint16_t *src = first + a.row_at(h * TR_HALF + m) * D + 8 * ch;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 dst + (ch / 8) * X::BLOCK + m * 128 + (((ch & 7) ^ (m & 7)) << 4)),
-                             "l"(src)
-                             : "memory");
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c.qfull[b]));
             phase ^= 1u << b;
+            if (p.local == 0) continue;
+            if (!wait(&c.qempty[b], phase >> b & 1u ^ 1u)) break;
+            load_queries<D>(a, first, h * TR_HALF, 0, min(TR_HALF, x.rows - h * TR_HALF), smem_u32(smem) + b * X::TILE);
+            if (lane == 0) mbar_arrive_many(smem_u32(&c.qfull[b]), TR_SOFTMAX_WARPS);
         }
         if (!x.two) sel ^= 1;
     }
@@ -552,18 +567,19 @@ struct TrRows {
                 // warps do it for both: PV1(n) is issued after P0(n).
                 const TrSlot at = v_slot<KV, D>(done, n, pc.n);
                 if (!wait(&c.full[at.at], at.parity)) return;
-                const int lo = max(0, ctx - t0), hi = p.w.L - t0;
+                const int lo = max(0, ctx - t0), hi = p.w.L - t0, r0 = (SHARED ? x * COLS : 0) + m / 8;
 #pragma unroll 1
                 for (int h = 0; h < D / 64; ++h) {
                     uint4 *blk = reinterpret_cast<uint4 *>(smem + X::OFF_RING + at.at * X::TILE + h * X::BLOCK) +
                                  (SHARED ? x * COLS * 8 : 0);
+                    // this thread's chunks m, m + 128, ..: row m / 8 + 16 i, from the first node's on
 #pragma unroll 1
-                    for (int i = 0; i < COLS / 16; ++i) {   // this thread's chunks m, m + 128, ..: row m / 8 + 16 i
-                        const int r = (SHARED ? x * COLS : 0) + m / 8 + 16 * i;
+                    for (int i = max(0, (lo - r0 + 15) >> 4); i < COLS / 16; ++i) {
+                        const int r = r0 + 16 * i;
                         uint4 &v = blk[m + TR_HALF * i];
                         if (r >= hi) {
                             v = make_uint4(0, 0, 0, 0);
-                        } else if (r >= lo && not_finite<MK>(v)) {
+                        } else if (not_finite<MK>(v)) {
                             v = make_uint4(finite_part<MK>(v.x), finite_part<MK>(v.y), finite_part<MK>(v.z),
                                            finite_part<MK>(v.w));
                             const int bad = t0 + r - ctx;
@@ -701,6 +717,12 @@ __device__ void tr_softmax(uint8_t *smem, TrCtrl &c, const TreeArgs &a, Walk<Tre
         const int mm = pc.two ? x * TR_HALF + m : m;   // row of the row tile
         const bool mine = mm < pc.rows;
         const bool idle = !__any_sync(0xffffffffu, mine);
+        if (p.local == 0) {   // its queries: a quarter of a half each, an eighth of one half
+            const uint16_t *first = a.query + a.first_row(p.w, p.r) * D;
+            const int some = pc.two ? 32 : 16, from = some * (pc.two ? quarter : 4 * x + quarter), b = pc.two ? x : 0;
+            load_queries<D>(a, first, b * TR_HALF, from, min(from + some, pc.rows - b * TR_HALF), smem_u32(smem) + b * X::TILE);
+            if (lane == 0) mbar_arrive_many(smem_u32(&c.qfull[b]), pc.two ? 2 : 1);
+        }
         const int node = pc.node0 + (mm * a.ginv >> 16);
         const int32_t *parents = a.parents + p.w.q0;
         uint32_t *poison = c.poison[p.local & 1];
@@ -807,7 +829,7 @@ __global__ void __launch_bounds__(Tree<KV, D>::THREADS, 1)
             mbar_init(smem_u32(&c.stempty[s]), X::CONV_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_u32(&c.qfull[b]), 1);
+            mbar_init(smem_u32(&c.qfull[b]), TR_SOFTMAX_WARPS);
             mbar_init(smem_u32(&c.qempty[b]), 1);
             for (int own = 0; own < 2; ++own) {
                 mbar_init(smem_u32(&c.sfull[own][b]), 1);
@@ -973,6 +995,7 @@ int launch_tree(TreeArgs a, const void *k_cache, const void *v_cache, cudaStream
     CUtensorMap tmk, tmv;
     if (!block_map(&tmk, k_cache, rows, D, a.bs, KV) || !block_map(&tmv, v_cache, rows, D, a.bs, KV)) return PA_ERR_CUDA;
     a.tile_toks = X::ROWS / a.G;
+    a.tinv = (1 << 20) / a.tile_toks + 1;
     const int ctas = std::min(num_sms(), AXIS_MAX_CTAS);
     if (const int e = launch_early(tree_kernel<KV, D>, dim3((unsigned)ctas), X::THREADS, X::SMEM, st, tmk, tmv, a))
         return e;

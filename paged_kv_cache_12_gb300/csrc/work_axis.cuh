@@ -184,15 +184,15 @@ struct Walk {
         if (u0 >= u1) return false;
         for (;;) {
             ++j;
-            while (j >= w.rts / team) {   // on to the next sequence
-                base += a.start(w, w.rts / team, team);
+            while (j >= w.rts >> (team - 1)) {   // on to the next sequence
+                base += a.start(w, w.rts >> (team - 1), team);
                 if (base >= u1 || ++seq >= a.num_seqs) return false;
                 w = a.seq_work(seq);
                 j = 0;
             }
             s = base + a.start(w, j, team);
             if (s >= u1) return false;
-            r = j * team + (int)blockIdx.x % team;
+            r = j * team + ((int)blockIdx.x & (team - 1));
             ntiles = a.row_tiles(w, r);
             t0 = (int)max(0LL, min((long long)ntiles, u0 - s - P::COST));
             t1 = (int)max(0LL, min((long long)ntiles, u1 - s - P::COST));
