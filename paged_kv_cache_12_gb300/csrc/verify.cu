@@ -637,10 +637,9 @@ __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
 // those tokens go.  `rows`: nodes of the first such wave (later ones, which few
 // sequences reach, take one a CTA).
 //
-// One GB300: 64 sequences of 32 nodes and 131,072 tokens in bf16 55 us (mean of eight
-// draws; one level after another 139), of which the first wave 26: sums 12 to 16 (67 MB), the
-// passing slice 5, meetings 4, collection and walk 2; 4 sequences of 16 nodes and 32,003
-// tokens in fp32 11.9 us.
+// One GB300: 64 sequences of 32 nodes and 131,072 tokens in bf16 41 us (mean of eight
+// draws; one level after another 139), two or three waves, of whose first the 67 MB of sums
+// take about half; 4 sequences of 16 nodes and 32,003 tokens in fp32 10.5 us.
 template <typename T, int VCTAS, int W>
 __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(32 * W, VRESIDENT * VWARPS / W)
     verify_tree_kernel(const TreeVerifyArgs a, int rows) {
