@@ -321,8 +321,8 @@ __device__ __forceinline__ Sum2 piece_sum(const Weights<T> &w, int lo, int hi) {
 // until one was as short as a warp's chunk: three reads one after another, and 64
 // sequences of 131072 tokens in bf16 took 54.8 us where this takes 45.8.)
 constexpr int VPIECE = 128;   // elements of a thread's piece, at most
-template <typename T, int W>
-__device__ __forceinline__ void find_in_slice(Draw<W> &sh, int *next, const Weights<T> &w, int lo, int hi, Sum2 run) {
+template <typename T, int W, class Publish>
+__device__ __forceinline__ void find_in_slice(Draw<W> &sh, Publish publish, const Weights<T> &w, int lo, int hi, Sum2 run) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int piece = ((hi - lo + 32 * W - 1) / (32 * W) + 7) / 8 * 8;
     const int plo = min(hi, lo + (int)threadIdx.x * piece), phi = min(hi, plo + piece);
@@ -340,21 +340,20 @@ __device__ __forceinline__ void find_in_slice(Draw<W> &sh, int *next, const Weig
     const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);   // (a part that was chosen has some weight)
     after.add(-mine.hi, -mine.lo);   // before this lane's piece
     const Sum2 from{__shfl_sync(0xffffffffu, after.hi, l), __shfl_sync(0xffffffffu, after.lo, l)};
-    const int v = find_in_range(w, __shfl_sync(0xffffffffu, plo, l), __shfl_sync(0xffffffffu, phi, l), from, sh.height);
-    if (lane == 0) *next = v;
+    publish(find_in_range(w, __shfl_sync(0xffffffffu, plo, l), __shfl_sync(0xffffffffu, phi, l), from, sh.height));
 }
 
 // Draws a token by the weights w: the smallest whose running sum passes u times
 // the total.  `ctas` CTAs of the cluster from rank `leader` on do it (`has`: for a row;
-// the same CTAs may have none), all CTAs of the cluster take part in its meetings; the
-// token is in *next (in the leader's shared memory, -1 before) after the cluster's next
-// meeting.  Returns the slice in which it lies, -1 where there is none, or `empty` where
+// the same CTAs may have none), all CTAs of the cluster take part in its meetings.  One
+// warp calls publish with the token after the first of them (none does where there is no
+// token).  Returns the slice in which it lies, -1 where there is none, or `empty` where
 // the weights sum to zero.  OWN: the weights are a row's own, nobody needs that answer, and
 // a slice may be long (where few CTAs have a row).
-template <typename T, bool OWN, int W, class Range>
-__device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader, int ctas, Draw<W> &sh, int *next,
+template <typename T, bool OWN, int W, class Range, class Publish>
+__device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader, int ctas, Draw<W> &sh,
                                           const Weights<T> &w, int vocab, bool has, const float *u, int empty,
-                                          Range range) {
+                                          Range range, Publish publish) {
     const int rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slices = ctas * W;   // at most VSLICES
     const int len = ((vocab + slices - 1) / slices + VCHUNK - 1) / VCHUNK * VCHUNK;   // of a slice
@@ -410,17 +409,15 @@ __device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader
     }
     const int slice = *cluster.map_shared_rank(&sh.slice, leader);
     if (is_short) {   // short slices: the warp that summed it finds the element
-        if (slice == own) {
-            const int v = find_in_range(w, lo, hi, *cluster.map_shared_rank(&sh.before, leader),
-                                        *cluster.map_shared_rank(&sh.height, leader));
-            if (lane == 0) *cluster.map_shared_rank(next, leader) = v;
-        }
+        if (slice == own)
+            publish(find_in_range(w, lo, hi, *cluster.map_shared_rank(&sh.before, leader),
+                                  *cluster.map_shared_rank(&sh.height, leader)));
     } else if (rank == leader && slice >= 0) {   // the slice again, in parts (OWN: while it is long)
         int first = slice * len, n = len;
         Sum2 before = sh.before;
         for (;;) {
             if (OWN && n <= 32 * W * VPIECE) {
-                find_in_slice(sh, next, w, first, min(vocab, first + n), before);
+                find_in_slice(sh, publish, w, first, min(vocab, first + n), before);
                 break;
             }
             const int part = ((n + W - 1) / W + VCHUNK - 1) / VCHUNK * VCHUNK;
@@ -432,10 +429,7 @@ __device__ __forceinline__ int draw_token(cg::cluster_group &cluster, int leader
             const Sum2 run = before;
             const int at = passing_part(sh, run, before);
             if (!OWN || at < 0) {
-                if (warp == at) {
-                    const int v = find_in_range(w, plo, phi, before, sh.height);
-                    if (lane == 0) *next = v;
-                }
+                if (warp == at) publish(find_in_range(w, plo, phi, before, sh.height));
                 break;
             }
             n = min(part, n - at * part);
@@ -503,9 +497,10 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(VTHREADS, VRESID
         Weights<T> w(p, q, failed && !a.draft ? a.draft_tokens[d0 + kept] : -1);
         for (int attempt = 0; attempt < 2; ++attempt) {
             const int slice =
-                draw_token<T, false>(cluster, 0, VCTAS, draw, &s_next, w, a.vocab, true, a.sample + seq,
+                draw_token<T, false>(cluster, 0, VCTAS, draw, w, a.vocab, true, a.sample + seq,
                                      attempt == 0 && failed ? -2 : -1,
-                                     [](const Weights<T> &x, int lo, int hi) { return range_sum(x, lo, hi); });
+                                     [](const Weights<T> &x, int lo, int hi) { return range_sum(x, lo, hi); },
+                                     [&](int v) { if (lane == 0) *cluster.map_shared_rank(&s_next, 0) = v; });
             if (slice != -2) break;
             w = Weights<T>(p, nullptr, -1);   // q covers p: draw from p itself
             cluster.sync();   // every CTA has read the decision
@@ -648,7 +643,9 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(32 * W, VRESIDEN
     const int seq = blockIdx.x / VCTAS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ Draw<W> draw;
-    __shared__ int s_next[2];   // by the wave's parity: a CTA may still read one wave's tokens while the next is drawn
+    // the groups' tokens, written into every CTA; by the wave's parity (a CTA may still read
+    // one wave's while the next is drawn)
+    __shared__ int s_next[2][VCTAS];
     __shared__ int s_nodes[VCTAS], s_count;
     __shared__ int s_node, s_level;
     __shared__ int32_t s_parents[PA_TREE_MAX_NODES], s_tokens[PA_TREE_MAX_NODES];   // of the tree's first nodes
@@ -671,24 +668,36 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(32 * W, VRESIDEN
     int level = 0, node = ok ? 0 : -1;
     for (int wave = 0; node >= 0; ++wave) {
         const int most = wave ? VCTAS : rows;
-        if (warp == 0) {   // the present node and the first of its descendants, in the order of their numbers
-            int mine = lane == 0 ? node : -1, count = 1;   // lane i: the i-th of them
-            for (int base = node + 1; count < most && base < n; base += 32) {
-                const int p = base + lane < n ? parent(base + lane) : -1;
-                bool taken = false;
-                for (int i = 0; i < count && count < most; ++i) {   // (a parent comes before its children)
-                    const int node_i = __shfl_sync(0xffffffffu, mine, i);   // (by every lane)
-                    unsigned kids = __ballot_sync(0xffffffffu, !taken && p >= 0 && p == node_i);
-                    if (kids >> lane & 1u) taken = true;
-                    for (; kids && count < most; kids &= kids - 1, ++count)
-                        if (lane == count) mine = base + __ffs((int)kids) - 1;
+        if (warp == 0) {
+            // The present node and the first of its descendants, in the order of their
+            // numbers, among the 1024 nodes behind it: lane k holds those of the k-th 32.
+            unsigned words = 0;
+            int count = 1;
+            for (int k = 0; k < 32 && count < most && node + 1 + 32 * k < n; ++k) {
+                const int j = node + 1 + 32 * k + lane;
+                const int up = j < n ? parent(j) - (node + 1) : -2;   // the parent, so counted; -1: the present node
+                const unsigned word = __shfl_sync(0xffffffffu, words, up >> 5 & 31);
+                bool in = up == -1 || (up >= 0 && up < 32 * k && (word >> (up & 31) & 1u));
+                unsigned set = __ballot_sync(0xffffffffu, in);
+                for (;;) {   // and those whose parent is one of these 32
+                    const int own = up - 32 * k;
+                    in = in || (own >= 0 && own < 32 && (set >> (own & 31) & 1u));
+                    const unsigned more = __ballot_sync(0xffffffffu, in);
+                    if (more == set) break;
+                    set = more;
                 }
+                const int place = count + __popc(set & ((1u << lane) - 1u));
+                if (in && place < most) s_nodes[place] = j;
+                count = min(most, count + __popc(set));
+                if (lane == k) words = set;
             }
-            if (lane < count) s_nodes[lane] = mine;
-            if (lane == 0) s_count = count;
+            if (lane == 0) {
+                s_nodes[0] = node;
+                s_count = count;
+            }
         }
-        int *next = &s_next[wave & 1];
-        if (threadIdx.x == 0) *next = -1;
+        int *next = s_next[wave & 1];
+        if (threadIdx.x < VCTAS) next[threadIdx.x] = -1;
         __syncthreads();
         int groups = 1;
         while (groups < s_count) groups *= 2;
@@ -696,12 +705,14 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(32 * W, VRESIDEN
         const bool has = group < s_count;   // a group without a node has no row either
         const int who = has ? s_nodes[group] : node;
         const T *p = static_cast<const T *>(a.target) + (long long)(n0 + who) * a.target_stride;
-        draw_token<T, true>(cluster, leader, ctas, draw, next, Weights<T>(p, nullptr, -1), a.vocab, has,
-                            a.uniform + n0 + who, -1, [](const Weights<T> &x, int lo, int hi) { return row_sum(x.p, lo, hi); });
+        draw_token<T, true>(cluster, leader, ctas, draw, Weights<T>(p, nullptr, -1), a.vocab, has,
+                            a.uniform + n0 + who, -1,
+                            [](const Weights<T> &x, int lo, int hi) { return row_sum(x.p, lo, hi); },
+                            [&](int v) { if (lane < VCTAS) *cluster.map_shared_rank(&next[group], lane) = v; });
         cluster.sync();   // the tokens are there
         if (warp == 0) {
             const int count = s_count;
-            const int token = lane < count ? *cluster.map_shared_rank(next, lane * ctas) : -1;
+            const int token = lane < count ? next[lane] : -1;
             const int number = lane < count ? s_nodes[lane] : -1;
             int at = 0, cur = node, lv = level, go = -1;
             for (;;) {   // node cur, the at-th of the wave
@@ -742,7 +753,7 @@ __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(32 * W, VRESIDEN
         for (int j = (ok ? level + 1 : 0) + (int)threadIdx.x; j <= a.max_depth; j += 32 * W) tokens[j] = path[j] = -1;
         if (threadIdx.x == 0) a.accepted[seq] = ok ? level : -1;
     }
-    cluster.sync();   // rank 0's shared memory outlives its readers
+    // (nothing reaches into another CTA's shared memory after the last meeting)
 }
 
 // The largest cluster with which all sequences' CTAs are resident at once (100
