@@ -330,17 +330,31 @@ __device__ __forceinline__ void find_in_slice(Draw<W> &sh, Publish publish, cons
     const Sum2 upto = warp_scan(mine);
     if (lane == 31) sh.totals[warp] = upto;
     __syncthreads();
-    Sum2 before;
-    const int at = passing_part(sh, run, before);
+    // Of the sums x of one part a lane, x_upto being their running sum: the first at whose
+    // end that sum passes, from `run` on, else the last of any weight; run becomes the sum
+    // before it.
+    auto first_passing = [&](const Sum2 &x, Sum2 x_upto) {
+        x_upto.add(run);
+        const unsigned any = __ballot_sync(0xffffffffu, x.any());
+        const unsigned over = __ballot_sync(0xffffffffu, x.any() && sh.height.passed_by(x_upto));
+        const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);
+        x_upto.add(-x.hi, -x.lo);
+        run = Sum2{__shfl_sync(0xffffffffu, x_upto.hi, l & 31), __shfl_sync(0xffffffffu, x_upto.lo, l & 31)};
+        return l;   // -1: no weight at all
+    };
+    // eight parts one after another, sixteen a lane each (64 x 32 nodes of 131,072 tokens in
+    // bf16 41.4 us, with a lane each 42.3; 4 x 16 of 32,003 in fp32 9.7 and 9.2)
+    int at;
+    if constexpr (W <= 8) {
+        const Sum2 start = run;
+        at = passing_part(sh, start, run);
+    } else {
+        const Sum2 part = lane < W ? sh.totals[lane] : Sum2();
+        at = first_passing(part, warp_scan(part));
+    }
     if (warp != at) return;
-    Sum2 after = before;
-    after.add(upto);
-    const unsigned any = __ballot_sync(0xffffffffu, mine.any());
-    const unsigned over = __ballot_sync(0xffffffffu, mine.any() && sh.height.passed_by(after));
-    const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);   // (a part that was chosen has some weight)
-    after.add(-mine.hi, -mine.lo);   // before this lane's piece
-    const Sum2 from{__shfl_sync(0xffffffffu, after.hi, l), __shfl_sync(0xffffffffu, after.lo, l)};
-    publish(find_in_range(w, __shfl_sync(0xffffffffu, plo, l), __shfl_sync(0xffffffffu, phi, l), from, sh.height));
+    const int l = first_passing(mine, upto);
+    publish(find_in_range(w, __shfl_sync(0xffffffffu, plo, l), __shfl_sync(0xffffffffu, phi, l), run, sh.height));
 }
 
 // Draws a token by the weights w: the smallest whose running sum passes u times
