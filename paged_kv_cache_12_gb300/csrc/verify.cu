@@ -648,7 +648,7 @@ __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
 //
 // One GB300: 64 sequences of 32 nodes and 131,072 tokens in bf16 41 us (mean of eight
 // draws; one level after another 139), two or three waves, of whose first the 67 MB of sums
-// take about half; 4 sequences of 16 nodes and 32,003 tokens in fp32 10.5 us.
+// take about half; 4 sequences of 16 nodes and 32,003 tokens in fp32 9.2 us.
 template <typename T, int VCTAS, int W>
 __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(32 * W, VRESIDENT * VWARPS / W)
     verify_tree_kernel(const TreeVerifyArgs a, int rows) {
@@ -818,11 +818,11 @@ bool wide_clusters() {
 // The same rule for the cluster, up to sixteen CTAs where a tree has more than eight
 // nodes on average, and of twice the warps where such clusters leave half of the SMs
 // idle: rows in L2, mean of eight draws, with eight CTAs / sixteen / of sixteen warps:
-// 4 x 16 nodes of 32,003 tokens in fp32 - / 11.0 / 10.5 us, 2 x 64 of 131,072 in fp32
-// - / 19.8 / 17.9, but 8 x 12 of 32,003 in fp32 - / 12.4 / 12.9.
+// 4 x 16 nodes of 32,003 tokens in fp32 13.2 / 9.9 / 9.2 us, 2 x 64 of 131,072 in fp32
+// 22.4 / 18.8 / 16.5, 8 x 12 of 32,003 in fp32 13.1 / 11.3 / 11.4.
 // The first wave takes as many nodes a sequence (a power of two, at most a CTA each) as
 // keep its reads within VWAVE_BYTES, and no more than a tree has on average (64 x 32
-// nodes of 131,072 tokens in bf16: 32, 64 and 128 MB 48, 46 and 50 us).
+// nodes of 131,072 tokens in bf16: 32, 64 and 128 MB 43, 41 and 46 us).
 constexpr long long VWAVE_BYTES = 64LL << 20;
 template <typename T>
 int launch_verify_tree(const TreeVerifyArgs &a, cudaStream_t st) {
