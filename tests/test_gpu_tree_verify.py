@@ -108,6 +108,32 @@ def test_trees_of_many_nodes():
     assert acc.max() > 8
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("counts,vocab", [([8], 600011), ([8, 7, 8], 280000), ([17, 16], 1100003)])
+def test_slices_longer_than_a_search(kind, counts, vocab):
+    # a CTA a node and so many tokens that the passing slice is cut before it is searched
+    for seed in (5, 6):
+        compare(tree_case(kind, counts, vocab, seed, width=vocab + 3), 6)
+
+
+@pytest.mark.parametrize("order", ["depth first", "a node's children 700 behind it", "backward"])
+def test_numberings_of_trees(order):
+    # waves take descendants by their numbers: paths through trees whose numbers say little
+    n = 900
+    if order == "depth first":        # chains of 30 from the root
+        parents = [-1] + [0 if j % 30 == 1 else j - 1 for j in range(1, n)]
+    elif order == "backward":         # parents that come after their children are nobody's
+        parents = [-1] + [j + 1 if j % 3 == 0 else j // 3 for j in range(1, n)]
+    else:
+        parents = [-1] + [0 if j <= 700 else j - 700 for j in range(1, n)]
+    g = torch.Generator().manual_seed(4)
+    target = torch.softmax(torch.randn(8 * n, 2, generator=g), 1).to(DEV)
+    tokens = np.random.default_rng(4).integers(0, 2, 8 * n).tolist()
+    u = np.random.default_rng(5).random(8 * n).astype(np.float32)
+    acc, _, _ = compare((target, tokens, parents * 8, [i * n for i in range(9)], u), 40)
+    assert acc.max() > 1
+
+
 def test_siblings_of_one_token_and_foreign_nodes():
     # the first of two children with the same token stands; a node without a parent is nobody's child
     p = torch.zeros(5, 8, device=DEV)
