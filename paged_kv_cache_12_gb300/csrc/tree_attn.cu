@@ -277,7 +277,9 @@ __device__ void tr_load(TrCtrl &c, const TreeArgs &a, Walk<TreeArgs> &p, uint32_
         for (int t = p.t0; t < p.t1; ++t) {
             const int some = min(boxes, blocks - t * boxes);   // the context ends in the last of them
             const bool out = (uint32_t)id >= num_blocks;
-            if (out) c.bad[p.local % TR_MARKS] = p.local + 1;
+            // by the lane that arrives: its arrival publishes the mark to those that read it
+            if (__any_sync(0xffffffffu, out) && lane == 0)
+                *reinterpret_cast<volatile int *>(&c.bad[p.local % TR_MARKS]) = p.local + 1;
             const int row = ((out ? 0 : id) * a.Hkv + g) * a.bs;
             if (t + 1 < p.t1) id = read(t + 1);
             if (!wait(&empty[first + at], parity)) break;
