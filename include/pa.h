@@ -639,8 +639,10 @@ PA_API size_t pa_attention_tree_workspace_size(int num_seqs, int num_query_token
  * that is not a non-decreasing cover of the rows makes every row NaN.  Positions
  * that a node does not see (drafts that are not its ancestors, slots behind the
  * context) may hold anything, infinities and NaN included: they do not reach its
- * output; one that sees a key or value that is not finite gets a row that is not
- * finite.  Deterministic.  pa_workspace_status reads the error word. */
+ * output.  One that sees a value that is not finite, or a key that makes a score
+ * NaN or plus infinity, gets a row that is not finite; a score of minus infinity
+ * is a probability of 0 (a row without any other score is NaN).  Deterministic.
+ * pa_workspace_status reads the error word. */
 PA_API int pa_attention_tree(void *out, const void *query, const void *k_cache, const void *v_cache,
                              const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
                              const int32_t *parents, int num_seqs, int num_query_tokens, int num_heads,
