@@ -538,6 +538,7 @@ enum {
  *   draft_start   int32 [num_seqs + 1], device, a non-decreasing cover of the
  *                 drafts; n at most max_drafts
  *   sample_uniform  float [num_seqs], in [0, 1)
+ * num_drafts, max_drafts and vocab_size up to 2^30.
  * NaN and negative weights count as zero.  If the weights of a failed draft
  * sum to zero (q covers p), the token is drawn from p_a; if that sums to zero
  * as well, or a sum is not finite, it is -1.  A sequence with a draft token
@@ -671,10 +672,10 @@ PA_API int pa_attention_tree(void *out, const void *query, const void *k_cache, 
  *                 node's entry can name its parent)
  *   tree_start    int32 [num_seqs + 1], device, a non-decreasing cover of the nodes
  *   uniform       float [num_nodes], in [0, 1)
- * At most max_depth drafts are accepted.  NaN and negative weights count as
- * zero; where a row sums to zero or its sum is not finite (one of 2^126 or more may
- * count so) the token is -1 and the path ends.  A sequence without nodes or with a
- * bad tree_start gets a = -1 and
+ * At most max_depth drafts are accepted (num_nodes, max_depth and vocab_size up to
+ * 2^30).  NaN and negative weights count as zero; where a row sums to zero or its
+ * sum is not finite (one of 2^126 or more may count so) the token is -1 and the
+ * path ends.  A sequence without nodes or with a bad tree_start gets a = -1 and
  * tokens and path -1.  Sums are carried in twice the precision of a float.
  * Needs no workspace. */
 PA_API int pa_verify_tree(int32_t *accepted, int32_t *tokens, int32_t *path, const void *target_probs,

@@ -860,7 +860,9 @@ extern "C" int pa_verify_drafts(int32_t *accepted, int32_t *tokens, const void *
         return PA_ERR_INVALID_ARG;
     if (probs_dtype != PA_PROBS_F32 && probs_dtype != PA_PROBS_F16 && probs_dtype != PA_PROBS_BF16)
         return PA_ERR_INVALID_ARG;
-    if (num_seqs > (1 << 24) || vocab_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
+    // rows, drafts and a sequence's tokens are counted in 32 bits
+    if (num_seqs > (1 << 24) || vocab_size > (1 << 30) || num_drafts > (1 << 30) || max_drafts > (1 << 30))
+        return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!accepted || !tokens || !target_probs || !draft_start || !sample_uniform ||
         (num_drafts > 0 && (!draft_tokens || !uniform)))
@@ -886,7 +888,9 @@ extern "C" int pa_verify_tree(int32_t *accepted, int32_t *tokens, int32_t *path,
         return PA_ERR_INVALID_ARG;
     if (probs_dtype != PA_PROBS_F32 && probs_dtype != PA_PROBS_F16 && probs_dtype != PA_PROBS_BF16)
         return PA_ERR_INVALID_ARG;
-    if (num_seqs > (1 << 24) || vocab_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
+    // nodes and a path's tokens are counted in 32 bits
+    if (num_seqs > (1 << 24) || vocab_size > (1 << 30) || num_nodes > (1 << 30) || max_depth > (1 << 30))
+        return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!accepted || !tokens || !path || !tree_start ||
         (num_nodes > 0 && (!target_probs || !node_tokens || !parents || !uniform)))

@@ -159,3 +159,11 @@ def test_plain_tree_verification_distribution():
         share = np.array([(after[:, 1] == v).mean() for v in range(3)])
         assert (np.abs(share - p[node]) <= 5 * np.sqrt(p[node] * (1 - p[node]) / len(after))).all(), share
     assert (out[out[:, 0] == 2, 1] == -1).all()
+
+
+def test_counts_that_do_not_fit_are_refused():
+    # a row of max_depth + 1 tokens, and steps of a warp or more past the end, are counted in 32 bits
+    most, V, D = (1 << 31) - 1, pa.lib().pa_verify_tree, pa.lib().pa_verify_drafts
+    for n, depth in ((7, most), (most, 2), (7, (1 << 30) + 1), ((1 << 30) + 1, 2)):
+        assert V(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, n, depth, 50, 50, 0, NUL) == pa.PA_ERR_UNSUPPORTED
+        assert D(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, n, depth, 50, 50, 50, 0, NUL) == pa.PA_ERR_UNSUPPORTED
