@@ -692,7 +692,8 @@ PA_API int pa_verify_tree(int32_t *accepted, int32_t *tokens, int32_t *path, con
  *                  after another: [num_layers][num_blocks][num_kv_heads][block_size][head_dim]
  *   block_tables, context_lens, query_start  as in pa_attention_tree
  *   path, accepted  as pa_verify_tree wrote them
- *   head_dim       a multiple of 8, for FP8 of 16; block_size >= 1
+ *   head_dim       a multiple of 8, for FP8 of 16, at most 2^29; block_size >= 1;
+ *                  max_depth at most 2^30
  * A sequence stays as it is when accepted[i] is negative or above max_depth, its
  * path does not begin with node 0, does not rise or leaves the tree, L, T or
  * query_start is invalid, or a block id on the way is out of range.  Sequences

@@ -134,6 +134,8 @@ extern "C" int pa_kv_move_path(void *k_cache, void *v_cache, const int32_t *bloc
         head_dim <= 0 || head_dim % (fp8 ? 16 : 8) != 0 || block_size <= 0 || num_blocks <= 0 ||
         max_blocks_per_seq <= 0 || (!fp8 && kv_dtype != PA_KV_F16 && kv_dtype != PA_KV_BF16))
         return PA_ERR_INVALID_ARG;
+    // a path's entries and a row's bytes are counted in 32 bits
+    if (max_depth > (1 << 30) || head_dim > (1 << 29)) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || max_depth == 0) return PA_OK;   // only node 0 can stand: it is in its place
     if (!k_cache || !v_cache || !block_tables || !context_lens || !query_start || !path || !accepted ||
         !aligned16(k_cache) || !aligned16(v_cache))

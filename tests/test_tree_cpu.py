@@ -167,3 +167,11 @@ def test_counts_that_do_not_fit_are_refused():
     for n, depth in ((7, most), (most, 2), (7, (1 << 30) + 1), ((1 << 30) + 1, 2)):
         assert V(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, n, depth, 50, 50, 0, NUL) == pa.PA_ERR_UNSUPPORTED
         assert D(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, n, depth, 50, 50, 50, 0, NUL) == pa.PA_ERR_UNSUPPORTED
+
+
+def test_sizes_of_a_move_that_do_not_fit_are_refused():
+    # a sequence's max_depth + 1 path entries and a row's bytes are counted in 32 bits
+    M, most = pa.lib().pa_kv_move_path, (1 << 31) - 1
+    for md, d in ((most, 64), ((1 << 30) + 1, 64), (3, 1 << 30), (3, most - 7)):
+        assert M(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 2, md, 1, 2, d, 16, 9, 4, pa.PA_KV_F16, NUL) == \
+            pa.PA_ERR_UNSUPPORTED, (md, d)
