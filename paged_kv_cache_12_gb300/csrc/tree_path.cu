@@ -50,9 +50,10 @@ __global__ void __launch_bounds__(MOVE_THREADS) move_path_kernel(const MoveArgs 
     const int first = threadIdx.x, here = first <= a.max_depth ? path[first] : 0;   // (read beside what it depends on)
     const int before = first > 0 && first <= a.max_depth ? path[first - 1] : -1;
     const int n = a.accepted[seq];
-    const int q0 = a.query_start[seq], T = a.query_start[seq + 1] - q0, L = a.context_lens[seq];
+    const int q0 = a.query_start[seq], q1 = a.query_start[seq + 1], L = a.context_lens[seq];
+    const int T = q0 >= 0 && q1 > q0 ? q1 - q0 : 0;   // (offsets of other signs may lie further apart than an int holds)
     bool ok = n >= 0 && n <= a.max_depth && T > 0 && T <= PA_TREE_MAX_NODES && n < T && T <= L &&
-              L <= (long long)a.mbps * a.block_size && q0 >= 0;
+              L <= (long long)a.mbps * a.block_size;
     if (ok) {
         for (int j = first; j <= n; j += MOVE_THREADS) {
             const int p = j == first ? here : path[j];

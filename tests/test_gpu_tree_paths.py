@@ -1,5 +1,5 @@
 """Calls of the step over a tree that the other tests do not make: block ids out of
-range in every place of a tile, infinite keys."""
+range in every place of a tile, infinite keys, row offsets whose difference wraps."""
 import math
 
 import numpy as np
@@ -16,6 +16,7 @@ if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("no CUDA device", allow_module_level=True)
 
 import test_gpu_tree as TT
+import test_gpu_tree_verify as TV
 
 DEV = torch.device("cuda:0")
 
@@ -88,3 +89,18 @@ def test_a_row_whose_only_score_is_minus_infinity_is_nan():
     s["q"][0, :, 3] = torch.tensor([0.5, -0.5], dtype=torch.float16, device=DEV)
     s["k"][int(s["tables"][0, 0]), 0, 0, 3] = math.inf
     assert torch.isnan(TT.run(s)).all()
+
+
+# ------------------------------------------------------------------ move of a path
+
+def test_a_path_stays_where_row_offsets_lie_further_apart_than_an_int():
+    # 2^31 - 1 and -2^31 + 5 differ by 6 where a difference wraps
+    counts, past, kept = [6, 6], [20, 20], [3, 3]
+    s = TV.move_case(pa.PA_KV_F16, counts, past, kept, 2, 2, 64, 8, seed=1)
+    k, v, tables, lens, _, path, _, _ = s
+    before = k.clone(), v.clone()
+    for start in ([(1 << 31) - 1, -(1 << 31) + 5, 12], [0, (1 << 31) - 1, -(1 << 31) + 5], [6, 0, -6]):
+        pa.pa_kv_move_path(k, v, tables, TT.i32(lens), TT.i32(start), path, TT.i32(kept))
+        torch.cuda.synchronize()
+        for c, w in zip((k, v), before):
+            assert torch.equal(c.view(torch.uint8), w.view(torch.uint8)), start
