@@ -135,6 +135,30 @@ def test_paths_of_many_waves(kind, counts, vocab):
     assert acc.max() >= 10
 
 
+@pytest.mark.parametrize("behind", [1023, 1024, 1500])
+def test_children_far_behind_their_parents(behind):
+    # a wave takes descendants among the 1024 nodes behind the present one; the path goes on to those further behind
+    n = 2 * behind + 9
+    parents = [-1] + [0 if j <= behind else j - behind for j in range(1, n)]
+    g = torch.Generator().manual_seed(behind)
+    target = torch.softmax(torch.randn(4 * n, 3, generator=g), 1).to(DEV)
+    tokens = np.random.default_rng(behind).integers(0, 3, 4 * n).tolist()
+    for j in range(4 * n):   # few children of the root have a token of the vocabulary: those behind them decide
+        if j % n <= behind and j % n != 1 + j // n:
+            tokens[j] = -1
+    u = np.random.default_rng(6).random(4 * n).astype(np.float32)
+    for i in range(4):       # the root's one child, its child `behind` further on, if it is drafted
+        tokens[i * n + 1 + i] = int(target[i * n].argmax())
+        u[i * n] = float((target[i * n, :tokens[i * n + 1 + i]].double().sum() + 0.5 * target[i * n].max().double())
+                         / target[i * n].double().sum())
+        tokens[i * n + 1 + i + behind] = int(target[i * n + 1 + i].argmax())
+        at = i * n + 1 + i
+        u[at] = float((target[at, :tokens[at + behind]].double().sum() + 0.5 * target[at].max().double())
+                      / target[at].double().sum())
+    acc, _, path = TV.compare((target, tokens, parents * 4, [i * n for i in range(5)], u), 5)
+    assert (acc >= 2).all() and path[:, 2].tolist() == [1 + i + behind for i in range(4)]
+
+
 def test_a_draft_stands_as_often_as_pa_verify_drafts_lets_it():
     # chains of one draft of probability one, n of them with the same rows: by either call
     # the draft stands with probability p(draft) and the first token is distributed as p, the
