@@ -31,12 +31,19 @@
 // have one type; the sums take them unrounded.
 //
 // What bounds it (one GB300).  16 nodes x 64 heads over 100 x 8192 tokens, bf16: HBM,
-// 510 us, 6.68 TB/s (a copy's rate).  25 nodes x 32 heads over 64 contexts of 512 ..
-// 16384 tokens, E4M3: 187 us, 3.3 TB/s; a KV tile takes 2450 clocks, for about 2200 of
-// which shared memory's pipe is busy (codes written, read and stored as 16-bit tiles
-// 1024, the products' operands 768, barriers and the rest 400).  64 nodes x 64 heads over
-// 4 x 32768 tokens, fp16: 225 us, 1220 TFLOP/s; the chain of a half, S with its queries
-// from shared memory 856 clocks, softmax 1900, PV 550 and the hand-overs between them.
+// 500 to 517 us, 6.6 TB/s or more (a copy's rate).  25 nodes x 32 heads over 64 contexts
+// of 512 .. 16384 tokens, E4M3: 185 us, 3.3 TB/s; the shared memory's pipe: on 32 x 8192
+// tokens it is busy for 2070 of a KV tile's 2360 clocks, 1049 of loads and stores (256 read
+// codes and 512 store 16-bit tiles; 142 are bank conflicts), 768 of the products' operands,
+// 256 of the codes' copies (by their bytes; the others counted).  64 nodes x 64 heads over
+// 4 x 32768 tokens, fp16: 216 to 229 us, 1200 to 1270 TFLOP/s; the chain of a half, S with
+// its queries from shared memory 856 clocks, softmax 1900, PV 550 and the hand-overs between
+// them; the same over E4M3, whose KV tiles come and are turned once per 128 rows, 264 us.
+// head_dim 64: 16 nodes x 64 heads over 100 x 8192 tokens, bf16, 286 us, 6.0 TB/s; the wide
+// trees 172 us (the softmax's chain is the same for half the products).
+// The kernel spills: 208 bytes of stores and 296 of loads (16-bit, head_dim 128; 180 and 256
+// with 64; E4M3 128 and 164), in the run 28 loads and 7 stores of a warp a KV tile of the
+// wide trees, 11 and 2 over E4M3.
 // One sequence of 600 tokens and 8 nodes: 12.5 us, latency (of 100 tokens 10.8).
 
 #include <algorithm>
@@ -77,7 +84,11 @@ struct TreeArgs {
     float4 *o;              // [2 AXIS_MAX_CTAS][rows * D / 4] its unnormalised output (see partial_at)
 
     // ---- the work axis: row tile r of a sequence is tile r % per_head of kv head r / per_head
-    static constexpr int COST = 8;   // 64 x 512 .. 16384 tokens, FP8: 194 us with 4, 187 with 8, 188 with 12, 197 with 16
+    // With 4 / 8 / 12 / 16, us: 25 nodes x 32 heads over 64 x 512 .. 16384 tokens, E4M3 192 / 185 /
+    // 190 / 200, bf16 216 / 201 / 193 / 199, 16 nodes at head_dim 64 116 / 118 / 123 / 130; 16 nodes
+    // over 64 x 100 .. 1000, bf16 46 / 46 / 48 / 48; 64 nodes x 64 heads over 24 x 512 .. 8192, bf16
+    // 206 / 204 / 186 / 193.  One number for all: 8 is within 9% of the best everywhere.
+    static constexpr int COST = 8;
     struct Seq {
         int L, T, q0;
         int per_head;   // row tiles of a kv head

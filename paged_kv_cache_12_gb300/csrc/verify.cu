@@ -643,12 +643,15 @@ __device__ __forceinline__ Sum2 row_sum(const T *p, int lo, int hi) {
 // cost a row's read and the meetings for each; so the cluster's CTAs draw the
 // tokens of several nodes at a time, the present one's and those of descendants
 // that it may lead to, in groups of as many CTAs each, and then walk as far as
-// those tokens go.  `rows`: nodes of the first such wave (later ones, which few
-// sequences reach, take one a CTA).
+// those tokens go.  `rows`: nodes of the first such wave; later ones take one a CTA,
+// however long the rows.  That suits drafts that usually stand, where most sequences reach
+// a third or fourth wave: 64 x 32 nodes of 131,072 tokens in bf16 with 1.7 drafts standing
+// on average 42 us, with 5.3 of them 87; with `rows` nodes in every wave 39 and 97 (in fp32
+// 63 and 135 against 57 and 163).
 //
 // One GB300: 64 sequences of 32 nodes and 131,072 tokens in bf16 41 us (mean of eight
-// draws; one level after another 139), two or three waves, of whose first the 67 MB of sums
-// take about half; 4 sequences of 16 nodes and 32,003 tokens in fp32 9.2 us.
+// draws, on the device; one level after another 139), two or three waves, of whose first the
+// 67 MB of sums take about half; 4 sequences of 16 nodes and 32,003 tokens in fp32 9.2 us.
 template <typename T, int VCTAS, int W>
 __global__ void __cluster_dims__(VCTAS, 1, 1) __launch_bounds__(32 * W, VRESIDENT * VWARPS / W)
     verify_tree_kernel(const TreeVerifyArgs a, int rows) {
@@ -821,8 +824,10 @@ bool wide_clusters() {
 // 4 x 16 nodes of 32,003 tokens in fp32 13.2 / 9.9 / 9.2 us, 2 x 64 of 131,072 in fp32
 // 22.4 / 18.8 / 16.5, 8 x 12 of 32,003 in fp32 13.1 / 11.3 / 11.4.
 // The first wave takes as many nodes a sequence (a power of two, at most a CTA each) as
-// keep its reads within VWAVE_BYTES, and no more than a tree has on average (64 x 32
-// nodes of 131,072 tokens in bf16: 32, 64 and 128 MB 43, 41 and 46 us).
+// keep its reads within VWAVE_BYTES, and no more than a tree has on average (with 32, 64 and
+// 128 MB, means of six draws: 64 x 32 nodes of 131,072 tokens in bf16 44, 42 and 46 us, in
+// fp32 61, 63 and 63; 38 x 32 in bf16 35, 30 and 32; 100 x 16 of 32,003 in fp32 32, 30 and
+// 30; 128 x 24 of 65,536 in bf16 39, 40 and 40).
 constexpr long long VWAVE_BYTES = 64LL << 20;
 template <typename T>
 int launch_verify_tree(const TreeVerifyArgs &a, cudaStream_t st) {
